@@ -115,6 +115,54 @@ class AttnTuneResult(ctypes.Structure):
     ]
 
 
+class AttnRopeParams(ctypes.Structure):
+    """Mirror of ``attn_rope_params`` (checked against attn_struct_size(0))."""
+
+    _fields_ = (
+        [(n, ctypes.c_void_p) for n in ("q", "k", "v", "q_out", "k_out")]
+        + [(n, ctypes.c_int) for n in ("B", "N", "Hq", "Hk", "d", "rot", "interleaved", "norm")]
+        + [("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+           ("q_weight_type", ctypes.c_int), ("k_weight_type", ctypes.c_int),
+           ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("pos_type", ctypes.c_int),
+           ("pos_stride", ctypes.c_int64 * 2), ("pos_offset", ctypes.c_int64)]
+        + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride", "k_out_stride")]
+        + [("k_cache", ctypes.c_void_p), ("v_cache", ctypes.c_void_p),
+           ("k_cache_stride", ctypes.c_int64 * 3), ("v_cache_stride", ctypes.c_int64 * 3),
+           ("n_pages", ctypes.c_int), ("page_size", ctypes.c_int), ("block_table", ctypes.c_void_p),
+           ("table_width", ctypes.c_int), ("table_stride", ctypes.c_int64),
+           ("starts", ctypes.c_void_p), ("counts", ctypes.c_void_p), ("stream", ctypes.c_void_p)])
+
+
+class AttnRopeBwdParams(ctypes.Structure):
+    """Mirror of ``attn_rope_bwd_params`` (checked against attn_struct_size(1))."""
+
+    _fields_ = (
+        [(n, ctypes.c_void_p) for n in ("q", "k", "dq_out", "dk_out", "dq", "dk")]
+        + [(n, ctypes.c_int) for n in ("B", "N", "Hq", "Hk", "d", "rot", "interleaved", "norm")]
+        + [("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+           ("q_weight_type", ctypes.c_int), ("k_weight_type", ctypes.c_int),
+           ("dq_weight", ctypes.c_void_p), ("dk_weight", ctypes.c_void_p),
+           ("inv_freq", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("pos_type", ctypes.c_int),
+           ("pos_stride", ctypes.c_int64 * 2), ("pos_offset", ctypes.c_int64)]
+        + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "k_stride", "dq_out_stride", "dk_out_stride",
+                                             "dq_stride", "dk_stride")]
+        + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64), ("stream", ctypes.c_void_p)])
+
+
+class AttnPagedParams(ctypes.Structure):
+    """Mirror of ``attn_paged_params`` (checked against attn_struct_size(2))."""
+
+    _fields_ = (
+        [(n, ctypes.c_void_p) for n in ("q", "k_cache", "v_cache", "o", "lse", "block_table", "kv_lens",
+                                        "q_lens", "prefix_table")]
+        + [(n, ctypes.c_int) for n in ("B", "Hq", "Hk", "Nq", "d", "n_pages", "page_size", "table_width")]
+        + [("table_stride", ctypes.c_int64), ("prefix_len", ctypes.c_int), ("prefix_pages", ctypes.c_int),
+           ("scale", ctypes.c_float), ("mask_kind", ctypes.c_int)]
+        + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "o_stride", "k_cache_stride", "v_cache_stride")]
+        + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64), ("stream", ctypes.c_void_p),
+           ("num_ctas", ctypes.c_int), ("timeout_ns", ctypes.c_uint64), ("inject", ctypes.c_int)])
+
+
 class AttnError(RuntimeError):
     def __init__(self, code: int, message: str):
         super().__init__(message)
@@ -167,6 +215,25 @@ def load(path: str = LIB_PATH):
         lib.attn_workspace_bytes.restype = ctypes.c_int64
         lib.attn_fwd_noalloc.argtypes = [ctypes.POINTER(AttnParamsEx)]
         lib.attn_fwd_noalloc.restype = i
+        for name, cls in (("attn_qk_norm_rope", AttnRopeParams), ("attn_kv_append", AttnRopeParams),
+                          ("attn_qk_norm_rope_bwd", AttnRopeBwdParams), ("attn_paged", AttnPagedParams)):
+            getattr(lib, name).argtypes = [ctypes.POINTER(cls)]
+            getattr(lib, name).restype = i
+        for name, cls in (("attn_rope_params_init", AttnRopeParams),
+                          ("attn_rope_bwd_params_init", AttnRopeBwdParams),
+                          ("attn_paged_params_init", AttnPagedParams)):
+            getattr(lib, name).argtypes = [ctypes.POINTER(cls)]
+            getattr(lib, name).restype = None
+        for name, cls in (("attn_qk_norm_rope_bwd_workspace_bytes", AttnRopeBwdParams),
+                          ("attn_paged_workspace_bytes", AttnPagedParams)):
+            getattr(lib, name).argtypes = [ctypes.POINTER(cls)]
+            getattr(lib, name).restype = ctypes.c_int64
+        lib.attn_struct_size.argtypes = [i]
+        lib.attn_struct_size.restype = i
+        for which, cls in enumerate((AttnRopeParams, AttnRopeBwdParams, AttnPagedParams)):
+            if lib.attn_struct_size(which) != ctypes.sizeof(cls):
+                raise ImportError(f"{cls.__name__} layout mismatch: library {lib.attn_struct_size(which)} "
+                                  f"bytes, binding {ctypes.sizeof(cls)} bytes")
         size = lib.attn_params_size()
         if size != ctypes.sizeof(AttnParamsEx):
             raise ImportError(f"attn_params_ex layout mismatch: library {size} bytes, "

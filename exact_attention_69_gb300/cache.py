@@ -1,0 +1,431 @@
+"""Python entry points around the attention of a language model, over libattn.so.
+
+    rope_freqs(rot)                 frequencies of the rotary positions
+    qk_norm_rope(q, k, ...)         per-head root-mean-square norm and rotary positions in
+                                    one pass; differentiable (qk_norm_rope_fwd, _bwd: its halves)
+    kv_append(k, v, k_cache, ...)   new keys and values into their pages, normed and rotated
+                                    on the way, the queries of the same tokens beside them
+    attn_paged(q, k_cache, ...)     attention over the pages, with a prefix that the whole
+                                    batch shares
+
+Layouts are the framework's: q, k, v [B, H, N, d] bf16 with any strides whose last
+dimension is contiguous (views of a fused projection are read in place); a cache is
+[n_pages, Hk, page_size, d] bf16 (a [n_pages, page_size, Hk, d] one as its transposed
+view); tables, lengths, starts and counts are int32 on the device, so a captured graph
+follows them. Scratch comes from PyTorch's allocator on the call's stream.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+
+import torch
+
+from . import _lib
+
+_WEIGHT_TYPES = {torch.bfloat16: 0, torch.float32: 1}
+_POS_TYPES = {torch.int32: 1, torch.int64: 2}
+
+
+def rope_freqs(rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """Radians per position of each rotated pair, base^(-2i / rot), i < rot / 2: the
+    float64 tensor that `inv_freq` takes. Scaled variants are tensors of the same shape."""
+    if rot <= 0 or rot % 16:
+        raise ValueError("rot must be a positive multiple of 16")
+    device = torch.device("cuda", torch.cuda.current_device()) if device is None else device
+    return float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
+
+
+def _heads(name, t, shape=None):
+    """Checks a [B, H, N, d] bf16 CUDA tensor; returns its element strides (b, h, n)."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() != 4:
+        raise ValueError(f"{name} must have four dimensions")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
+    st = t.stride()
+    if st[3] != 1:
+        raise ValueError(f"the last (head) dimension of {name} must be contiguous")
+    return _nonzero(st, t.shape)
+
+
+def _nonzero(st, shape):
+    # all-zero strides mean "contiguous" to the library: a tensor expanded in every
+    # dimension, or of one row, says d for one of them
+    a, b, c = st[0], st[1], st[2]
+    if not (a or b or c):
+        if shape[0] * shape[1] * shape[2] > 1:
+            raise ValueError("a tensor expanded in every dimension is not supported")
+        return (0, 0, shape[3])
+    return (a, b, c)
+
+
+def _int32(name, t, device, shape):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if t.dim() != len(shape) or any(want is not None and have != want for have, want in zip(t.shape, shape)):
+        raise ValueError(f"{name} must have the shape {tuple('any' if s is None else s for s in shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+    return t.data_ptr()
+
+
+def _same_device(device, **ts):
+    for name, t in ts.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+
+
+def _weight(name, w, d, device):
+    if w is None:
+        return None, 0
+    if w.dtype not in _WEIGHT_TYPES:
+        raise TypeError(f"{name} must be bfloat16 or float32")
+    if w.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if w.shape != (d,) or (d > 1 and w.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous [{d}] tensor")
+    return w.data_ptr(), _WEIGHT_TYPES[w.dtype]
+
+
+def _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, position_offset, interleaved, eps):
+    """The fields that the forward's and the backward's parameter blocks share."""
+    if eps is None:
+        if q_weight is not None or k_weight is not None:
+            raise ValueError("weights need a norm: give eps")
+    else:
+        p.norm, p.eps = 1, float(eps)
+    p.q_weight, p.q_weight_type = _weight("q_weight", q_weight, d, device)
+    p.k_weight, p.k_weight_type = _weight("k_weight", k_weight, d, device)
+    if inv_freq is not None:
+        if inv_freq.dtype != torch.float64:
+            raise TypeError("inv_freq must be float64 (rope_freqs)")
+        if inv_freq.device != device:
+            raise ValueError(f"inv_freq must be on {device}")
+        if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
+            raise ValueError("inv_freq must be a contiguous [rot / 2] tensor")
+        p.rot, p.inv_freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+        if p.rot == 0:
+            raise ValueError("inv_freq must not be empty")
+    p.interleaved = int(bool(interleaved))
+    if positions is not None:
+        if positions.dtype not in _POS_TYPES:
+            raise TypeError("positions must be int32 or int64")
+        if positions.device != device:
+            raise ValueError(f"positions must be on {device}")
+        if tuple(positions.shape) not in ((N,), (B, N)):
+            raise ValueError(f"positions must be [{N}] or [{B}, {N}]")
+        p.positions, p.pos_type = positions.data_ptr(), _POS_TYPES[positions.dtype]
+        st = positions.stride()
+        p.pos_stride[:] = (0, st[0]) if len(st) == 1 else st
+    p.pos_offset = int(position_offset)
+
+
+@contextlib.contextmanager
+def _on(device, stream, tensors):
+    """Makes the tensors' device and the call's stream current, so that outputs and
+    scratch come from that stream's memory; yields the stream's handle. Inputs on another
+    stream than the current one are held for it until its work so far is done."""
+    with torch.cuda.device(device):
+        current = torch.cuda.current_stream(device)
+        if stream is None or stream == current:
+            yield current.cuda_stream
+            return
+        if stream.device != device:
+            raise ValueError(f"the stream must be on {device}")
+        with torch.cuda.stream(stream):
+            yield stream.cuda_stream
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None = None,
+                     k_weight: torch.Tensor | None = None, *, inv_freq: torch.Tensor | None = None,
+                     positions: torch.Tensor | None = None, position_offset: int = 0,
+                     interleaved: bool = False, eps: float | None = 1e-6,
+                     q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None, stream=None):
+    """Norm and rotation of every head of q [B, Hq, N, d] and k [B, Hk, N, d] in one pass.
+
+    Each head is divided by the root of its channels' mean square plus `eps` and
+    multiplied by its weight ([d], bf16 or fp32; None = ones); eps None: no norm. Then
+    the first 2 * len(inv_freq) channels are rotated (rope_freqs; None: no rotation) by
+    the token's position: `positions` [N] or [B, N] int32 or int64, else position_offset
+    + n. Pairs are (i, i + rot / 2), or (2i, 2i + 1) with `interleaved`. k may be None.
+    Returns (q_out, k_out); q_out may be q, k_out k.
+    """
+    if q.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    B, Hq, N, d = q.shape
+    p = _lib.AttnRopeParams()
+    p.B, p.N, p.Hq, p.d = B, N, Hq, d
+    p.q_stride[:] = _heads("q", q)
+    p.q = q.data_ptr()
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("expected [B, H, N, d] tensors")
+        p.Hk = k.shape[1]
+        p.k_stride[:] = _heads("k", k, (B, p.Hk, N, d))
+        p.k = k.data_ptr()
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    _same_device(q.device, k=k, q_out=q_out, k_out=k_out)
+    _set_rope(p, B, N, d, q.device, q_weight, k_weight, inv_freq, positions, position_offset, interleaved, eps)
+    with _on(q.device, stream, (q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out)) as handle:
+        if q_out is None:
+            q_out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
+        p.q_out_stride[:] = _heads("q_out", q_out, (B, Hq, N, d))
+        p.q_out = q_out.data_ptr()
+        if k is not None:
+            if k_out is None:
+                k_out = torch.empty((B, p.Hk, N, d), dtype=torch.bfloat16, device=q.device)
+            p.k_out_stride[:] = _heads("k_out", k_out, (B, p.Hk, N, d))
+            p.k_out = k_out.data_ptr()
+        p.stream = handle
+        _lib.check(_lib.load().attn_qk_norm_rope(ctypes.byref(p)), "qk_norm_rope")
+    return q_out, k_out
+
+
+def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tensor,
+                     dk_out: torch.Tensor | None, q_weight: torch.Tensor | None = None,
+                     k_weight: torch.Tensor | None = None, *, inv_freq: torch.Tensor | None = None,
+                     positions: torch.Tensor | None = None, position_offset: int = 0,
+                     interleaved: bool = False, eps: float | None = 1e-6, weight_grads: bool = True,
+                     stream=None):
+    """Gradients through qk_norm_rope_fwd: (dq, dk, dq_weight, dk_weight) for the
+    gradients dq_out, dk_out at its outputs; the other arguments as the forward had them.
+    Weight gradients have the weights' types (None without a weight, or with
+    weight_grads False); their sums are fp32 in a fixed order."""
+    if q.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out go together")
+    B, Hq, N, d = q.shape
+    p = _lib.AttnRopeBwdParams()
+    p.B, p.N, p.Hq, p.d = B, N, Hq, d
+    p.q_stride[:] = _heads("q", q)
+    p.dq_out_stride[:] = _heads("dq_out", dq_out, q.shape)
+    p.q, p.dq_out = q.data_ptr(), dq_out.data_ptr()
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("expected [B, H, N, d] tensors")
+        p.Hk = k.shape[1]
+        p.k_stride[:] = _heads("k", k, (B, p.Hk, N, d))
+        p.dk_out_stride[:] = _heads("dk_out", dk_out, k.shape)
+        p.k, p.dk_out = k.data_ptr(), dk_out.data_ptr()
+    elif k_weight is not None:
+        raise ValueError("k_weight needs k")
+    _same_device(q.device, k=k, dq_out=dq_out, dk_out=dk_out)
+    _set_rope(p, B, N, d, q.device, q_weight, k_weight, inv_freq, positions, position_offset, interleaved, eps)
+    dk = dwq = dwk = ws = None
+    with _on(q.device, stream, (q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions)) as handle:
+        dq = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
+        p.dq = dq.data_ptr()
+        if k is not None:
+            dk = torch.empty((B, p.Hk, N, d), dtype=torch.bfloat16, device=q.device)
+            p.dk = dk.data_ptr()
+        if weight_grads and q_weight is not None:
+            dwq = torch.empty_like(q_weight)
+            p.dq_weight = dwq.data_ptr()
+        if weight_grads and k_weight is not None:
+            dwk = torch.empty_like(k_weight)
+            p.dk_weight = dwk.data_ptr()
+        lib = _lib.load()
+        n = lib.attn_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(p))
+        if n < 0:
+            _lib.check(int(-n), "qk_norm_rope_bwd")
+        if n > 0:
+            ws = torch.empty(n, dtype=torch.uint8, device=q.device)
+            p.workspace, p.workspace_bytes = ws.data_ptr(), n
+        p.stream = handle
+        _lib.check(lib.attn_qk_norm_rope_bwd(ctypes.byref(p)), "qk_norm_rope_bwd")
+    return dq, dk, dwq, dwk
+
+
+class _QkNormRope(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, inv_freq, positions, opts):
+        qo, ko = qk_norm_rope_fwd(q, k, q_weight, k_weight, inv_freq=inv_freq, positions=positions, **opts)
+        ctx.save_for_backward(q, k, q_weight, k_weight, inv_freq, positions)
+        ctx.opts = opts
+        ctx.set_materialize_grads(False)
+        return qo, ko
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dq_out, dk_out):
+        q, k, q_weight, k_weight, inv_freq, positions = ctx.saved_tensors
+        how = dict(inv_freq=inv_freq, positions=positions, **ctx.opts)
+        weights = ctx.needs_input_grad[2] or ctx.needs_input_grad[3]
+        dq = dk = dwq = dwk = None
+
+        def ready(g):  # any strides will do, but for the last dimension's and their multiples of 16 bytes
+            ok = g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and all(
+                n == 1 or (s > 0 and s % 8 == 0) for s, n in zip(g.stride()[:3], g.shape))
+            return g if ok else g.contiguous()
+
+        # an output that the loss does not reach has no gradient, and its side is left out
+        if dq_out is not None and dk_out is not None:
+            dq, dk, dwq, dwk = qk_norm_rope_bwd(q, k, ready(dq_out), ready(dk_out), q_weight, k_weight,
+                                                weight_grads=weights, **how)
+        elif dq_out is not None:
+            dq, _, dwq, _ = qk_norm_rope_bwd(q, None, ready(dq_out), None, q_weight, None,
+                                             weight_grads=weights, **how)
+        elif dk_out is not None:
+            dk, _, dwk, _ = qk_norm_rope_bwd(k, None, ready(dk_out), None, k_weight, None,
+                                             weight_grads=weights, **how)
+        return dq, dk, dwq, dwk, None, None, None
+
+
+def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None = None,
+                 k_weight: torch.Tensor | None = None, *, inv_freq: torch.Tensor | None = None,
+                 positions: torch.Tensor | None = None, position_offset: int = 0,
+                 interleaved: bool = False, eps: float | None = 1e-6):
+    """qk_norm_rope_fwd as a differentiable torch op: gradients for q, k and the weights
+    (once: the gradient itself is not differentiable). Runs on the current stream."""
+    opts = dict(position_offset=int(position_offset), interleaved=bool(interleaved), eps=eps)
+    return _QkNormRope.apply(q, k, q_weight, k_weight, inv_freq, positions, opts)
+
+
+def _cache(p, k_cache, v_cache, Hk, d, device):
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must both be [n_pages, Hk, page_size, d]")
+    pages, _, page, _ = k_cache.shape
+    p.k_cache_stride[:] = _heads("k_cache", k_cache, (pages, Hk, page, d))
+    p.v_cache_stride[:] = _heads("v_cache", v_cache, (pages, Hk, page, d))
+    _same_device(device, k_cache=k_cache, v_cache=v_cache)
+    p.k_cache, p.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
+    p.n_pages, p.page_size = pages, page
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+              block_table: torch.Tensor, starts: torch.Tensor, *, counts: torch.Tensor | None = None,
+              position_offset: int = 0, positions: torch.Tensor | None = None,
+              inv_freq: torch.Tensor | None = None, interleaved: bool = False, eps: float | None = None,
+              k_weight: torch.Tensor | None = None, q: torch.Tensor | None = None,
+              q_weight: torch.Tensor | None = None, q_out: torch.Tensor | None = None, stream=None):
+    """Appends N new tokens of every sequence to a paged cache, in place.
+
+    k, v [B, Hk, N, d]; k_cache, v_cache [n_pages, Hk, page_size, d] (page_size a power
+    of two from 16); block_table [B, width] pages of each sequence; starts [B] tokens
+    that each holds already. Token n goes to slot starts[b] + n. Keys are normed (eps
+    given; k_weight) and rotated (inv_freq) on the way as qk_norm_rope_fwd does, at
+    `positions`, else at position_offset + starts[b] + n (position_offset: the length of
+    a shared prefix). With `q` [B, Hq, N, d] the same tokens' queries are normed and
+    rotated in the same launch and returned (in q_out if given); else returns None.
+
+    counts [B]: real tokens of each sequence; those behind leave the cache as it was, as
+    do negative starts, slots behind the table's end and entries that are not a page of
+    the cache. The pages that a call writes must not be shared between sequences.
+    """
+    if k.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    B, Hk, N, d = k.shape
+    device = k.device
+    p = _lib.AttnRopeParams()
+    p.B, p.N, p.Hk, p.d = B, N, Hk, d
+    p.k_stride[:] = _heads("k", k)
+    p.v_stride[:] = _heads("v", v, k.shape)
+    p.k, p.v = k.data_ptr(), v.data_ptr()
+    _same_device(device, v=v, q=q, q_out=q_out)
+    _cache(p, k_cache, v_cache, Hk, d, device)
+    p.block_table = _int32("block_table", block_table, device, (B, None))
+    p.table_width, p.table_stride = block_table.shape[1], block_table.stride(0)
+    p.starts = _int32("starts", starts, device, (B,))
+    if counts is not None:
+        p.counts = _int32("counts", counts, device, (B,))
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("expected [B, H, N, d] tensors")
+        p.Hq = q.shape[1]
+        p.q_stride[:] = _heads("q", q, (B, p.Hq, N, d))
+        p.q = q.data_ptr()
+    elif q_weight is not None or q_out is not None:
+        raise ValueError("q_weight and q_out need q")
+    _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, position_offset, interleaved, eps)
+    with _on(device, stream, (k, v, k_cache, v_cache, block_table, starts, counts, positions, inv_freq, k_weight, q,
+                              q_weight, q_out)) as handle:
+        if q is not None:
+            if q_out is None:
+                q_out = torch.empty((B, p.Hq, N, d), dtype=torch.bfloat16, device=device)
+            p.q_out_stride[:] = _heads("q_out", q_out, (B, p.Hq, N, d))
+            p.q_out = q_out.data_ptr()
+        p.stream = handle
+        _lib.check(_lib.load().attn_kv_append(ctypes.byref(p)), "kv_append")
+    return q_out
+
+
+_PAGED_MASKS = {"none": _lib.ATTN_MASK_NONE, "causal_br": _lib.ATTN_MASK_CAUSAL_BR}
+
+
+def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+               kv_lens: torch.Tensor, *, q_lens: torch.Tensor | None = None,
+               prefix_table: torch.Tensor | None = None, prefix_len: int = 0, scale: float | None = None,
+               mask: str = "causal_br", out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               return_lse: bool = True, num_ctas: int = 0, timeout_ns: int = 0, inject: int = 0, stream=None):
+    """Attention of a batch of sequences over a paged cache, with a shared prefix.
+
+    q [B, Hq, Nq, d]; k_cache, v_cache [n_pages, Hk, page_size, d], Hq a multiple of Hk
+    (query head h reads key head h // (Hq // Hk)). The keys of sequence b are the first
+    prefix_len tokens of the pages in prefix_table (one table for the whole batch, read
+    once for all of its queries), then kv_lens[b] tokens of the pages in block_table[b].
+    Its queries are the last q_lens[b] of these tokens (None: Nq); rows behind q_lens[b]
+    are padding. mask 'causal_br': row i sees keys up to i + T - q_lens[b], T = prefix_len
+    + kv_lens[b]; 'none': every real row sees all T. A row that sees no key gives 0 and
+    an LSE of -inf. Lengths and tables are read when the kernels run.
+
+    Returns (o, lse) or o. Raises for what the host can check; a bad table entry reads
+    as zeros, a length beyond the table's end is cut.
+    """
+    if q.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    if mask not in _PAGED_MASKS:
+        raise ValueError(f"mask must be 'none' or 'causal_br', not {mask!r}")
+    B, Hq, Nq, d = q.shape
+    device = q.device
+    p = _lib.AttnPagedParams()
+    p.q_stride[:] = _heads("q", q)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must both be [n_pages, Hk, page_size, d]")
+    p.B, p.Hq, p.Hk, p.Nq, p.d = B, Hq, k_cache.shape[1], Nq, d
+    p.q = q.data_ptr()
+    _cache(p, k_cache, v_cache, p.Hk, d, device)
+    p.block_table = _int32("block_table", block_table, device, (B, None))
+    p.table_width, p.table_stride = block_table.shape[1], block_table.stride(0)
+    p.kv_lens = _int32("kv_lens", kv_lens, device, (B,))
+    if q_lens is not None:
+        p.q_lens = _int32("q_lens", q_lens, device, (B,))
+    p.prefix_len = int(prefix_len)
+    if prefix_table is not None:
+        p.prefix_table = _int32("prefix_table", prefix_table, device, (None,))
+        p.prefix_pages = prefix_table.shape[0]
+    p.scale = float(1.0 / math.sqrt(d) if scale is None else scale)
+    p.mask_kind = _PAGED_MASKS[mask]
+    p.num_ctas, p.timeout_ns, p.inject = int(num_ctas), int(timeout_ns), int(inject)
+    _same_device(device, out=out, lse=lse)
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, Hq, Nq)):
+        raise ValueError("lse must be a contiguous float32 [B, Hq, Nq] tensor")
+    with _on(device, stream, (q, k_cache, v_cache, block_table, kv_lens, q_lens, prefix_table, out, lse)) as handle:
+        if out is None:
+            out = torch.empty((B, Hq, Nq, d), dtype=torch.bfloat16, device=device)
+        p.o_stride[:] = _heads("out", out, (B, Hq, Nq, d))
+        p.o = out.data_ptr()
+        if lse is None and return_lse:
+            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
+        if lse is not None:
+            p.lse = lse.data_ptr()
+        lib = _lib.load()
+        n = lib.attn_paged_workspace_bytes(ctypes.byref(p))
+        if n < 0:
+            _lib.check(int(-n), "attn_paged")
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        p.workspace, p.workspace_bytes = ws.data_ptr(), n
+        p.stream = handle
+        _lib.check(lib.attn_paged(ctypes.byref(p)), "attn_paged")
+    return (out, lse) if return_lse else out

@@ -1,4 +1,6 @@
-// attn_host.cu -- the C ABI of libattn.so (declared in include/attn.h).
+// attn_host.cu -- the C ABI of libattn.so (declared in include/attn.h): the
+// attention forward and backward. (cache_host.cu: norm, rotation and the paged
+// cache.)
 //
 // Host work per call: validate the arguments (before any CUDA call), encode
 // the three TMA tensor maps, pick the kernel specialisation, launch once on
@@ -17,7 +19,9 @@
 #include <mutex>
 
 #include "attn.h"
+#include "attn_host.h"
 #include "attn_kernel.h"
+#include "paged_kernel.h"
 
 namespace {
 
@@ -431,6 +435,20 @@ int acquire_workspace(const attn_params_ex* p, const Plan& pl, DeviceState* ds, 
   return ATTN_OK;
 }
 
+// The paged attention kernels' status word lives in their module; it is read
+// only on devices where they were launched.
+bool g_paged_used[kMaxDevices] = {};
+
+int paged_take(int dev, uint32_t word[4]) {
+  word[0] = word[1] = word[2] = word[3] = 0;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_paged_used[dev]) return ATTN_OK;
+  }
+  const cudaError_t e = attn::paged_take_status(word);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "reading the paged kernels' status");
+}
+
 // Reads and clears the no-alloc entry point's status word on device `dev`
 // (zeros if that entry point was not used there), and forgets its per-device
 // state (under g_mu); defined with it below.
@@ -438,6 +456,60 @@ int noalloc_take_status(int dev, uint32_t word[4]);
 void noalloc_forget();
 
 }  // namespace
+
+// What the entry points of the other translation units share with this one.
+namespace attn {
+namespace host {
+
+int fail_with(int code, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(t_err, sizeof(t_err), fmt, ap);
+  va_end(ap);
+  return code;
+}
+
+int cuda_error(cudaError_t e, const char* what) { return cuda_fail(e, what); }
+
+void clear_error() { t_err[0] = 0; }
+
+cudaStream_t stream_of(void* given) { return given ? static_cast<cudaStream_t>(given) : t_stream; }
+
+int tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn) {
+  const int rc = get_encoder();
+  *fn = g_encode;
+  return rc;
+}
+
+int this_device(int* dev, int* sms) {
+  static int known[kMaxDevices] = {};  // SM count + 1 of devices that were checked
+  cudaError_t e = cudaGetDevice(dev);
+  if (e != cudaSuccess) return cuda_fail(e, "cudaGetDevice");
+  if (*dev < 0 || *dev >= kMaxDevices) return fail(ATTN_ERR_CUDA, "device ordinal %d out of range", *dev);
+  // a driver call (the tensor-map encoder) follows: make the primary context current
+  if ((e = cudaSetDevice(*dev)) != cudaSuccess) return cuda_fail(e, "cudaSetDevice");
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (known[*dev] == 0) {
+    int major = 0, minor = 0, n = 0;
+    if ((e = cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, *dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, *dev)) != cudaSuccess ||
+        (e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, *dev)) != cudaSuccess)
+      return cuda_fail(e, "cudaDeviceGetAttribute");
+    if (major != 10 || minor != 3)
+      return fail(ATTN_ERR_UNSUPPORTED, "device %d is sm_%d%d; this library is built for sm_103a", *dev, major, minor);
+    known[*dev] = n + 1;
+  }
+  *sms = known[*dev] - 1;
+  return ATTN_OK;
+}
+
+void paged_used(int dev) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  g_paged_used[dev] = true;
+}
+
+}  // namespace host
+}  // namespace attn
 
 extern "C" {
 
@@ -536,6 +608,8 @@ int attn_get_device_status(uint32_t* detail) {
   uint32_t word2[4] = {0, 0, 0, 0};
   int rc = noalloc_take_status(dev, word2);
   if (rc != ATTN_OK) return rc;
+  if (word[0] == 0) std::memcpy(word, word2, sizeof(word));
+  if ((rc = paged_take(dev, word2)) != ATTN_OK) return rc;
   if (word[0] == 0) std::memcpy(word, word2, sizeof(word));
   if (detail) std::memcpy(detail, word, sizeof(word));
   if (word[0] == 0) return ATTN_OK;

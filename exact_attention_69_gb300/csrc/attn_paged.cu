@@ -1,0 +1,993 @@
+// attn_paged.cu -- attention over a paged key/value cache: a prefix that every
+// sequence of the batch shares, then each sequence's own pages.
+//
+// Tasks. A task is up to 256 query rows that read the same keys, of one key
+// head: for the prefix, rows of every sequence together (its keys are read
+// once per 256 rows, not once per sequence); for a sequence's own pages, its
+// rows (queries x the heads that share the key head). The tasks' K/V tiles of
+// 128 keys form one sequence of units, one more unit per task for its start,
+// and CTA c takes units [c U / G, (c + 1) U / G): every SM streams the same
+// number of bytes whatever the lengths are. The lengths are read on the
+// device, so a captured graph follows them. A task cut between CTAs leaves
+// parts (row maximum, row sum, unnormalised O in fp32) in the workspace, and a
+// second kernel joins the parts of each row, prefix and own, in a fixed order.
+//
+// A CTA (one per SM):
+//   warp 0      loader: page numbers, TMA of the pages of each K and V tile
+//   warp 1      MMA issuer: S = Q K^T and O += P V (tcgen05, TMEM)
+//   warps 2-3   gather the task's query rows into swizzled shared memory
+//   warps 4-7 / 8-11  softmax of stream 0 / 1: one thread per row
+// A task of more than 128 rows has two query tiles, one per stream, and each
+// K/V tile serves both. A task of up to 128 rows has one query tile and its
+// K/V tiles go to the streams in turn, each with its own running maximum, sum
+// and O in TMEM; the two are joined in the CTA at the task's end. Either way
+// the tensor core works on one stream while the other's softmax runs.
+//
+// Keys at and behind the task's end inside its last tile are masked, and their
+// V rows are set to zero in shared memory first: a page's unused slots may
+// hold anything, and 0 * NaN would reach the sum.
+//
+// P is rounded to bf16 for the second product (the tensor core's input type;
+// the row sum takes the unrounded values), which moves O by at most 2^-9 of
+// sum p |v|, the size of the final rounding to bf16.
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "attn_sm103.cuh"
+#include "paged_kernel.h"
+
+namespace attn {
+namespace dev {
+
+__device__ uint32_t g_paged_status[4];
+
+template <int D>
+struct PCfg {
+  using C = Cfg<D>;  // tile layout (swizzle, chunks) and MMA descriptors
+  static constexpr int kStages = D == 128 ? 2 : (D == 64 ? 5 : 8);  // of K and of V
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = 2 * C::kTileBytes;
+  static constexpr int kOffV = kOffK + kStages * C::kTileBytes;
+  static constexpr int kOffBar = kOffV + kStages * C::kTileBytes;
+  static constexpr int kBarBytes = 512;
+  static constexpr int kOffX = kOffBar + kBarBytes;  // exchange: [2 buffers][2 streams][m, l][128]
+  static constexpr int kXBytes = 2 * 2 * 2 * 128 * 4;
+  static constexpr int kOffScan = kOffX + kXBytes;   // 16 + 4 int32
+  static constexpr int kSmemBytes = kOffScan + 128 + 1024;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+};
+
+struct PBars {
+  uint32_t base;
+  int st;
+  __device__ uint32_t q_full() const { return base; }
+  __device__ uint32_t q_empty() const { return base + 8; }
+  __device__ uint32_t s_full(int h) const { return base + 16 + 8 * h; }
+  __device__ uint32_t p_full(int h, int part) const { return base + 32 + 8 * (2 * h + part); }
+  __device__ uint32_t o_full(int h) const { return base + 64 + 8 * h; }
+  __device__ uint32_t o_empty(int h) const { return base + 80 + 8 * h; }
+  __device__ uint32_t x_full(int h) const { return base + 96 + 8 * h; }
+  __device__ uint32_t done() const { return base + 112; }
+  // every product of a one-tile task is complete (o_full: of stream h of a two-tile task).
+  // One barrier of its own, that both warpgroups wait for at every such task: none skips a phase.
+  __device__ uint32_t t_full() const { return base + 120; }
+  __device__ uint32_t k_full(int s) const { return base + 128 + 8 * s; }
+  __device__ uint32_t k_empty(int s) const { return base + 128 + 8 * (st + s); }
+  __device__ uint32_t v_full(int s) const { return base + 128 + 8 * (2 * st + s); }
+  __device__ uint32_t v_empty(int s) const { return base + 128 + 8 * (3 * st + s); }
+  __device__ int count() const { return 16 + 4 * st; }
+};
+
+// ------------------------------------------------------------------ work split
+
+__device__ __forceinline__ int clampi(int x, int lo, int hi) { return min(max(x, lo), hi); }
+
+struct SeqLens {
+  int len, ql;
+};
+
+__device__ __forceinline__ SeqLens seq_lens(const PagedParams& p, int b) {
+  SeqLens s;
+  s.len = clampi(p.kv_lens[b], 0, p.max_len);
+  s.ql = p.q_lens != nullptr ? clampi(p.q_lens[b], 0, p.Nq) : p.Nq;
+  return s;
+}
+
+// Keys that query n of a sequence sees, counted from the prefix's first.
+__device__ __forceinline__ int keys_seen(const PagedParams& p, SeqLens s, int n) {
+  if (n >= s.ql) return 0;
+  const int total = p.prefix_len + s.len;
+  return p.causal ? clampi(total - s.ql + n + 1, 0, total) : total;
+}
+
+// K/V tiles of a sequence's own keys that task t (rows [256 t, 256 t + 256)) needs.
+__device__ __forceinline__ int own_tiles(const PagedParams& p, SeqLens s, int t) {
+  const int first = t * kPagedTaskRows / p.G;
+  if (first >= s.ql) return 0;
+  const int last = min((min((t + 1) * kPagedTaskRows, p.Nq * p.G) - 1) / p.G, s.ql - 1);
+  return (clampi(keys_seen(p, s, last) - p.prefix_len, 0, s.len) + kBN - 1) / kBN;
+}
+
+__device__ __forceinline__ int own_tasks(const PagedParams& p) {
+  return (p.Nq * p.G + kPagedTaskRows - 1) / kPagedTaskRows;
+}
+
+// Units of one sequence's tasks for one key head.
+__device__ __forceinline__ int own_units(const PagedParams& p, SeqLens s) {
+  const int n = own_tasks(p);
+  int u = 0;
+  for (int t = 0; t < n; ++t) {
+    const int tiles = own_tiles(p, s, t);
+    u += tiles + (tiles > 0 ? kPagedTaskCost : 0);
+  }
+  return u;
+}
+
+__device__ __forceinline__ int prefix_tiles(const PagedParams& p) { return (p.prefix_len + kBN - 1) / kBN; }
+__device__ __forceinline__ int prefix_tasks(const PagedParams& p) {  // per key head
+  return p.prefix_len > 0 ? (p.B * p.Nq * p.G + kPagedTaskRows - 1) / kPagedTaskRows : 0;
+}
+__device__ __forceinline__ int prefix_units(const PagedParams& p) {
+  return p.Hk * prefix_tasks(p) * (prefix_tiles(p) + kPagedTaskCost);
+}
+
+// The split of U units over the CTAs that get some: CTA c starts at c U / n.
+struct Split {
+  int units, ctas;
+  __device__ __forceinline__ Split(int u, int grid) : units(u), ctas(max(1, min(grid, u / kPagedMinUnits))) {}
+  __device__ __forceinline__ int lo(int c) const {
+    return c >= ctas ? units : static_cast<int>(static_cast<int64_t>(c) * units / ctas);
+  }
+  __device__ __forceinline__ int owner(int u) const {  // the CTA whose range holds unit u
+    return static_cast<int>((static_cast<int64_t>(u + 1) * ctas - 1) / units);
+  }
+};
+
+// One CTA's share of one task.
+struct PSeg {
+  bool prefix;
+  int b, hk;       // b: own tasks only
+  int row0, rows;  // first row of the task and the rows that its key head has in all
+  int keys;        // keys of the task's key space
+  int k0, k1;      // tiles [k0, k1)
+  bool twin;       // one query tile, tiles in turn
+  bool whole;      // every tile of the task
+  bool first;      // holds the task's first tile
+};
+
+struct PSegIter {
+  int u, hi;       // units left: [u, hi)
+  int up;          // units of the prefix tasks
+  int b, sb;       // current sequence and its first unit
+  SeqLens cur, nxt;
+  int ub;          // its units per key head
+
+  // u0: the CTA's first unit; b0, s0: the sequence that holds it (or the next) and its first unit.
+  __device__ __forceinline__ PSegIter(const PagedParams& p, int u0, int u1, int b0, int s0)
+      : u(u0), hi(u1), up(prefix_units(p)), b(b0), sb(s0), ub(0) {
+    cur.len = cur.ql = 0;
+    nxt = cur;
+    if (u < hi && b < p.B) {
+      cur = seq_lens(p, b);
+      ub = own_units(p, cur);
+      if (b + 1 < p.B) nxt = seq_lens(p, b + 1);
+    }
+  }
+  __device__ __forceinline__ bool next(const PagedParams& p, PSeg& s) {
+    while (u < hi) {
+      int a, tiles;
+      if (u < up) {
+        tiles = prefix_tiles(p);
+        const int per = tiles + kPagedTaskCost, t = u / per, n = prefix_tasks(p);
+        a = t * per;
+        s.prefix = true;
+        s.hk = t / n;
+        s.b = 0;
+        s.row0 = (t - s.hk * n) * kPagedTaskRows;
+        s.rows = p.B * p.Nq * p.G;
+        s.keys = p.prefix_len;
+      } else {
+        while (u >= sb + p.Hk * ub) {
+          sb += p.Hk * ub;
+          ++b;
+          cur = nxt;
+          ub = own_units(p, cur);
+          if (b + 1 < p.B) nxt = seq_lens(p, b + 1);
+        }
+        s.prefix = false;
+        s.b = b;
+        s.hk = (u - sb) / ub;
+        a = sb + s.hk * ub;
+        int t = 0;
+        tiles = own_tiles(p, cur, 0);
+        for (;;) {
+          const int per = tiles + (tiles > 0 ? kPagedTaskCost : 0);
+          if (u < a + per) break;
+          a += per;
+          tiles = own_tiles(p, cur, ++t);
+        }
+        s.row0 = t * kPagedTaskRows;
+        s.rows = p.Nq * p.G;
+        s.keys = cur.len;
+      }
+      const int first = a + kPagedTaskCost, end = first + tiles;
+      s.k0 = max(u, first) - first;
+      s.k1 = min(hi, end) - first;
+      s.twin = s.rows - s.row0 <= kBM;
+      s.whole = s.k0 == 0 && s.k1 == tiles;
+      s.first = s.k0 == 0;
+      u = min(hi, end);
+      if (s.k1 > s.k0) return true;
+    }
+    return false;
+  }
+};
+
+// Position of row r of a segment's task.
+struct RowPos {
+  int b, n, g;
+};
+__device__ __forceinline__ RowPos row_pos(const PagedParams& p, const PSeg& s, int r) {
+  RowPos x;
+  const int rs = p.Nq * p.G;
+  x.b = s.prefix ? r / rs : s.b;
+  const int i = s.prefix ? r - x.b * rs : r;
+  x.n = i / p.G;
+  x.g = i - x.n * p.G;
+  return x;
+}
+
+// ------------------------------------------------------------------ roles
+
+// A lane's own TMA (each lane that calls it issues one copy).
+__device__ __forceinline__ void tma_lane(uint32_t dst, const CUtensorMap* m, uint32_t bar, int c0, int c1, int c2,
+                                         int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
+      : "memory");
+}
+
+template <int D>
+__device__ void paged_loader(const PagedParams& p, uint32_t sbase, const PBars& bars, PSegIter it, const Ctl& ctl) {
+  using P = PCfg<D>;
+  using C = Cfg<D>;
+  const int lane = threadIdx.x & 31;
+  const int page = 1 << p.page_shift, box = min(page, kBN);
+  const int per_tile = kBN / box;             // pages (or parts of one) of a tile: 1 to 8
+  const uint32_t box_bytes = static_cast<uint32_t>(box) * D * 2;
+  const uint64_t pol_once = l2_policy_evict_first(), pol_reuse = l2_policy_evict_last();
+  RingPos<P::kStages> r;
+  uint32_t armed_k = 0, par_k = 0, armed_v = 0, par_v = 0;
+  bool injected = false;
+  int nth = 0;
+  PSeg s;
+  while (it.next(p, s)) {
+    const int32_t* tab = s.prefix ? p.prefix_table : p.table + s.b * p.table_sb;
+    const uint64_t pol = s.prefix ? pol_reuse : pol_once;
+    // this lane's page of tile k; lanes without keys to load get none
+    auto page_of = [&](int k, bool& mine) -> int {
+      const int key = k * kBN + lane * box;
+      mine = lane < per_tile && key < s.keys;
+      return mine ? tab[key >> p.page_shift] : 0;
+    };
+    bool mine, mine_next = false;
+    int id = page_of(s.k0, mine), id_next = 0;
+    for (int k = s.k0; k < s.k1; ++k, ++nth) {
+      if (k + 1 < s.k1) id_next = page_of(k + 1, mine_next);
+      const int slot = (k * kBN + lane * box) & (page - 1);
+      const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine))) * box_bytes;
+      if (!ctl_wait(bars.k_empty(r.s), r.ph ^ 1u, ctl, k, kRoleLoader)) goto drain;
+      if (p.inject && !injected && nth == 1) {
+        injected = true;  // withhold this K tile: the MMA issuer's wait must run out
+      } else {
+        mbar_expect_tx(bars.k_full(r.s), bytes);
+        __syncwarp();
+        if (mine)
+          for (int c = 0; c < C::kChunks; ++c)
+            tma_lane(sbase + P::kOffK + r.s * C::kTileBytes + c * C::kChunkBytes + lane * box * C::kSwizzle, &p.tm_k,
+                     bars.k_full(r.s), c * C::kBoxCols, slot, s.hk, id, pol);
+        armed_k |= 1u << r.s;
+        par_k = (par_k & ~(1u << r.s)) | (r.ph << r.s);
+      }
+      __syncwarp();
+      if (!ctl_wait(bars.v_empty(r.s), r.ph ^ 1u, ctl, k, kRoleLoader)) goto drain;
+      mbar_expect_tx(bars.v_full(r.s), bytes);
+      __syncwarp();
+      if (mine)
+        for (int c = 0; c < C::kChunks; ++c)
+          tma_lane(sbase + P::kOffV + r.s * C::kTileBytes + c * C::kChunkBytes + lane * box * C::kSwizzle, &p.tm_v,
+                   bars.v_full(r.s), c * C::kBoxCols, slot, s.hk, id, pol);
+      armed_v |= 1u << r.s;
+      par_v = (par_v & ~(1u << r.s)) | (r.ph << r.s);
+      __syncwarp();
+      r.advance();
+      id = id_next;
+      mine = mine_next;
+    }
+  }
+drain:
+  __syncwarp();
+  // The last copy armed on each barrier must have landed before the CTA exits.
+  for (int st = 0; st < P::kStages; ++st) {
+    if ((armed_k >> st) & 1u) ctl_wait(bars.k_full(st), (par_k >> st) & 1u, ctl, -1, kRoleLoader, false);
+    if ((armed_v >> st) & 1u) ctl_wait(bars.v_full(st), (par_v >> st) & 1u, ctl, -1, kRoleLoader, false);
+  }
+}
+
+// Warps 2 and 3: the task's query rows, each warp every other group of rows,
+// into the swizzled K-major layout that the MMA descriptor expects.
+template <int D>
+__device__ void paged_gather_q(const PagedParams& p, uint8_t* smem, const PBars& bars, PSegIter it, const Ctl& ctl) {
+  using P = PCfg<D>;
+  using C = Cfg<D>;
+  constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row; rows per instruction
+  constexpr int kU = 4;
+  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 2;
+  const int c = lane % kLanes;                        // 16-byte chunk of the row
+  uint32_t ph = 0;
+  PSeg s;
+  while (it.next(p, s)) {
+    if (!ctl_wait(bars.q_empty(), ph ^ 1u, ctl, -1, kRoleLoader)) return;
+    ph ^= 1u;
+    const int n = min(s.rows - s.row0, kPagedTaskRows);
+    for (int i0 = w * kRows * kU; i0 < n; i0 += 2 * kRows * kU) {
+      uint4 v[kU];
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int i = i0 + u * kRows + lane / kLanes;
+        if (i < n) {
+          const RowPos x = row_pos(p, s, s.row0 + i);
+          v[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + x.b * p.q_sb +
+                                                 static_cast<int64_t>(s.hk * p.G + x.g) * p.q_sh + x.n * p.q_sn +
+                                                 c * 8);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kU; ++u) {
+        const int i = i0 + u * kRows + lane / kLanes;
+        if (i < n) {
+          const int row = i % kBM;
+          const int swz = C::kSwizzle == 128 ? ((c & 7) ^ (row & 7)) : (c ^ ((row >> 1) & 3));
+          const int off = P::kOffQ + (i / kBM) * C::kTileBytes + (C::kSwizzle == 128 ? (c >> 3) * C::kChunkBytes : 0) +
+                          row * C::kSwizzle + swz * 16;
+          *reinterpret_cast<uint4*>(smem + off) = v[u];
+        }
+      }
+    }
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars.q_full());
+  }
+}
+
+template <int D>
+__device__ void paged_mma(const PagedParams& p, uint32_t sbase, const PBars& bars, uint32_t tmem, PSegIter it,
+                          const Ctl& ctl) {
+  using P = PCfg<D>;
+  using C = Cfg<D>;
+  const uint64_t q0 = smem_desc(sbase + P::kOffQ, 16, 8 * C::kSwizzle, C::kLayout);
+  const uint64_t q1 = smem_desc(sbase + P::kOffQ + C::kTileBytes, 16, 8 * C::kSwizzle, C::kLayout);
+  const uint64_t k_base = smem_desc(sbase + P::kOffK, 16, 8 * C::kSwizzle, C::kLayout);
+  const uint64_t v_base = smem_desc(sbase + P::kOffV, C::kChunkBytes, 8 * C::kSwizzle, C::kLayout);
+  constexpr uint64_t kStep = static_cast<uint64_t>(C::kTileBytes >> 4);
+  uint32_t q_ph = 0, p_par = 0, o_par = 0;  // bit h of p_par, o_par: parity of stream h's next phase
+  RingPos<P::kStages> kr, vr;
+  PSeg s;
+  while (it.next(p, s)) {
+    if (!ctl_wait(bars.q_full(), q_ph, ctl, -1, kRoleMma)) goto drain;
+    q_ph ^= 1u;
+    tc_fence_after();
+    uint32_t o_ready = 0;
+    const bool twin = s.twin;
+    // S of tile k: both streams' (two query tiles), or its own stream's
+    auto scores = [&](int h) {
+      issue_s<D>(tmem + (h ? C::tm_s(1) : C::tm_s(0)), (h && !twin) ? q1 : q0, k_base + kr.s * kStep);
+      mma_commit(bars.s_full(h));
+    };
+    auto take_k = [&](int k) -> bool {
+      if (!ctl_wait(bars.k_full(kr.s), kr.ph, ctl, k, kRoleMma)) return false;
+      tc_fence_after();
+      return true;
+    };
+    auto give_k = [&]() {
+      mma_commit(bars.k_empty(kr.s));
+      kr.advance();
+    };
+    auto product = [&](int k, int h) -> bool {
+      if (!((o_ready >> h) & 1u) && !ctl_wait(bars.o_empty(h), ((o_par >> h) & 1u) ^ 1u, ctl, k, kRoleMma)) return false;
+      const uint32_t par = (p_par >> h) & 1u;
+      for (int part = 0; part < 2; ++part) {
+        if (!ctl_wait(bars.p_full(h, part), par, ctl, k, kRoleMma)) return false;
+        tc_fence_after();
+        issue_pv<D>(tmem + (h ? C::tm_o(1) : C::tm_o(0)), tmem + (h ? C::tm_p(1) : C::tm_p(0)), v_base + vr.s * kStep,
+                    part, (((o_ready >> h) & 1u) != 0u || part > 0) ? 1u : 0u);
+      }
+      p_par ^= 1u << h;
+      o_ready |= 1u << h;
+      return true;
+    };
+    const int ahead = twin ? 2 : 1;  // tiles whose S goes before the first P V
+    for (int k = s.k0; k < min(s.k0 + ahead, s.k1); ++k) {
+      if (!take_k(k)) goto drain;
+      if (twin) {
+        scores((k - s.k0) & 1);
+      } else {
+        scores(0);
+        scores(1);
+      }
+      give_k();
+    }
+    if (s.k0 + ahead >= s.k1) mma_commit(bars.q_empty());
+    for (int k = s.k0; k < s.k1; ++k) {
+      const int kn = k + ahead;
+      if (!ctl_wait(bars.v_full(vr.s), vr.ph, ctl, k, kRoleMma)) goto drain;
+      tc_fence_after();
+      if (twin) {
+        const int h = (k - s.k0) & 1;
+        if (!product(k, h)) goto drain;
+        if (kn < s.k1) {
+          if (!take_k(kn)) goto drain;
+          scores(h);
+          give_k();
+        }
+      } else {
+        for (int h = 0; h < 2; ++h) {
+          if (!product(k, h)) goto drain;
+          if (kn < s.k1) {
+            if (h == 0 && !take_k(kn)) goto drain;
+            scores(h);
+          }
+        }
+        if (kn < s.k1) give_k();
+      }
+      mma_commit(bars.v_empty(vr.s));
+      vr.advance();
+      if (kn < s.k1 && kn + 1 == s.k1) mma_commit(bars.q_empty());  // the task's last S is issued
+    }
+    for (int h = 0; h < 2; ++h) {
+      if (!((o_ready >> h) & 1u)) {  // a stream without a tile keeps its phases in step
+        if (!ctl_wait(bars.o_empty(h), ((o_par >> h) & 1u) ^ 1u, ctl, -1, kRoleMma)) goto drain;
+      }
+      if (!twin) mma_commit(bars.o_full(h));
+      o_par ^= 1u << h;
+    }
+    if (twin) mma_commit(bars.t_full());
+  }
+drain:
+  mma_commit(bars.done());
+  ctl_wait(bars.done(), 0, ctl, -1, kRoleMma, false);
+}
+
+// A part's slot: quarters of 32 rows, each [D/4][32 rows] float4, then m[32], l[32].
+template <int D>
+__device__ __forceinline__ float* paged_slot(const PagedParams& p, int cta, bool first, int tile, int quarter) {
+  return p.slots + (static_cast<int64_t>((2 * cta + (first ? 1 : 0)) * 2 + tile) * 4 + quarter) * 32 * (D + 2);
+}
+
+// Row of (b, key head, query, head of the group) in the row buffers and in the join.
+__device__ __forceinline__ int64_t row_index(const PagedParams& p, int b, int hk, int n, int g) {
+  return ((static_cast<int64_t>(b) * p.Hk + hk) * p.Nq + n) * p.G + g;
+}
+
+// Where one row of a finished (part of a) task goes.
+template <int D>
+struct RowSink {
+  float* part = nullptr;          // cut task: float4 i at part + 128 * i
+  float* buf = nullptr;           // uncut task with another part to join: row-major fp32
+  __nv_bfloat16* out = nullptr;   // the final result
+  float inv = 0.f;                // 1 / row sum (final result); 0: the row saw no key
+  __device__ __forceinline__ void put32(int ch, const float (&x)[32]) const {
+    if (part != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4*>(part + 128 * (ch * 8 + i)) =
+            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else if (buf != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        *reinterpret_cast<float4*>(buf + ch * 32 + 4 * i) =
+            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    } else if (out != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          w[j] = inv == 0.f ? 0u : pack_bf16(x[8 * i + 2 * j] * inv, x[8 * i + 2 * j + 1] * inv);
+        *reinterpret_cast<uint4*>(out + ch * 32 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+  }
+};
+
+template <int D>
+__device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars& bars, uint32_t tmem, PSegIter it,
+                              const Ctl& ctl) {
+  using P = PCfg<D>;
+  using C = Cfg<D>;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int h = (warp - 4) >> 2, quarter = warp & 3, row = quarter * 32 + lane;
+  const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+  const uint32_t t_s = lane_base + (h ? C::tm_s(1) : C::tm_s(0)), t_o = lane_base + (h ? C::tm_o(1) : C::tm_o(0)),
+                 t_p = lane_base + (h ? C::tm_p(1) : C::tm_p(0));
+  float* xch = reinterpret_cast<float*>(smem + P::kOffX);
+  const float c = p.c;
+  uint32_t s_par = 0, o_par = 0, t_par = 0;
+  uint32_t n_tiles = 0;  // tiles that the CTA has taken: the V ring's position
+  PSeg s;
+  while (it.next(p, s)) {
+    const int r = s.row0 + (s.twin ? 0 : h * kBM) + row;
+    int seen = 0;  // keys of this task that the row sees
+    RowPos x{0, 0, 0};
+    const bool real = r < s.rows;
+    if (real) {
+      x = row_pos(p, s, r);
+      const int all = keys_seen(p, seq_lens(p, x.b), x.n);
+      seen = s.prefix ? min(all, p.prefix_len) : max(all - p.prefix_len, 0);
+    }
+    const bool any = __any_sync(0xffffffffu, seen > 0);
+    float m_ref = -CUDART_INF_F, l = 0.f;
+    bool first = true;
+    for (int k = s.k0 + (s.twin ? h : 0); k < s.k1; k += s.twin ? 2 : 1) {
+      const int base = k * kBN;
+      if (!warp_wait(bars.s_full(h), s_par, ctl, k)) return;
+      s_par ^= 1u;
+      tc_fence_after();
+      if (base + kBN > s.keys) {
+        // The task's last tile: V rows behind its end become zero. (After
+        // s_full: this tile's S went out behind the products of the tiles that
+        // held its V stage before, so v_full is in this tile's phase or past
+        // it, and the parity below cannot match an older one.)
+        const uint32_t at = n_tiles + static_cast<uint32_t>(k - s.k0);
+        const int st = static_cast<int>(at % P::kStages);
+        if (!warp_wait(bars.v_full(st), (at / P::kStages) & 1u, ctl, k)) return;
+        const int z0 = max(s.keys - base, quarter * 32), z1 = quarter * 32 + 32;
+        for (int ch = 0; ch < C::kChunks; ++ch) {
+          uint8_t* v = smem + P::kOffV + st * C::kTileBytes + ch * C::kChunkBytes;
+          for (int i = z0 * C::kSwizzle + lane * 16; i < z1 * C::kSwizzle; i += 512)
+            *reinterpret_cast<uint4*>(v + i) = make_uint4(0, 0, 0, 0);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      if (any) {
+        uint32_t sr[128];
+        tmem_ld128(t_s, sr);
+        const int lim = seen - base;
+        if (__any_sync(0xffffffffu, lim < kBN)) {
+          const uint32_t neg_inf = __float_as_uint(-CUDART_INF_F);
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            if (i >= lim) sr[i] = neg_inf;
+        }
+        const float mx = row_max128(sr);
+        const float m_tile = (mx == -CUDART_INF_F) ? -CUDART_INF_F : mx * c;
+        const bool grow = m_tile > m_ref + kRescaleLog2;
+        float alpha = 1.f;
+        if (grow) {
+          alpha = ex2(m_ref - m_tile);
+          l *= alpha;
+          m_ref = m_tile;
+        }
+        if (__any_sync(0xffffffffu, grow && !first)) rescale_o<D>(t_o, alpha);
+        const float neg_m = (m_ref == -CUDART_INF_F) ? 0.f : -m_ref;
+        const float2 c2 = make_float2(c, c), nm2 = make_float2(neg_m, neg_m);
+        float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int part = 0; part < 2; ++part) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int e = 64 * part + 2 * i;
+            const float2 y =
+                __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, nm2);
+            const float2 pe = make_float2(ex2(y.x), ex2(y.y));
+            sum4[i & 3] = __fadd2_rn(sum4[i & 3], pe);
+            pk[i] = pack_bf16(pe.x, pe.y);
+          }
+          if (part == 1) {
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.p_full(h, 0));
+          }
+          tmem_st32(t_p + 32 * part, pk);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.p_full(h, 1));
+        const float2 sa = __fadd2_rn(sum4[0], sum4[1]), sb = __fadd2_rn(sum4[2], sum4[3]);
+        l += (sa.x + sa.y) + (sb.x + sb.y);
+      } else {
+        // no row of this warp sees a key of the task: its P and O are never read
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(bars.p_full(h, 0));
+          mbar_arrive(bars.p_full(h, 1));
+        }
+      }
+      first = false;
+    }
+    n_tiles += static_cast<uint32_t>(s.k1 - s.k0);
+
+    // the end of the segment: O of this row, to its part, its buffer or the result
+    float m = m_ref, w0 = 1.f, w1 = 0.f;
+    if (s.twin) {
+      // Join the streams: each warpgroup takes half of the columns. The maxima
+      // and sums go through shared memory, two buffers in turn. Each side
+      // arrives after t_full, which the other side's warps are all needed for,
+      // so neither runs a whole phase ahead of a warp that has yet to look.
+      if (!warp_wait(bars.t_full(), t_par, ctl, -1)) return;
+      float* mine = xch + ((t_par * 2 + h) * 2) * kBM;
+      const float* other = xch + ((t_par * 2 + (h ^ 1)) * 2) * kBM;
+      mine[row] = m_ref;
+      mine[kBM + row] = l;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.x_full(h));
+      if (!warp_wait(bars.x_full(h ^ 1), t_par, ctl, -1)) return;
+      t_par ^= 1u;
+      const float mo = other[row], lo = other[kBM + row];
+      m = fmaxf(m_ref, mo);
+      const float wm = m_ref == -CUDART_INF_F ? 0.f : ex2(m_ref - m), wo = mo == -CUDART_INF_F ? 0.f : ex2(mo - m);
+      w0 = h ? wo : wm;
+      w1 = h ? wm : wo;
+      const float l0 = h ? lo : l, l1 = h ? l : lo;
+      l = fmaf(l1, w1, l0 * w0);
+    } else {
+      if (!warp_wait(bars.o_full(h), o_par, ctl, -1)) return;
+      o_par ^= 1u;
+    }
+    tc_fence_after();
+    RowSink<D> sink;
+    const bool none = m == -CUDART_INF_F;
+    const bool lead = !s.twin || h == 0;  // writes the row's m and l
+    if (real) {
+      if (!s.whole) {
+        float* base = paged_slot<D>(p, blockIdx.x, s.first, s.twin ? 0 : h, quarter);
+        if (!none) sink.part = base + 4 * lane;
+        if (lead) {
+          base[32 * D + lane] = m;
+          base[32 * D + 32 + lane] = l;
+        }
+      } else if (p.prefix_len > 0) {
+        const int64_t rows = static_cast<int64_t>(p.B) * p.Nq * p.Hq;
+        const int64_t i = (s.prefix ? 0 : rows) + row_index(p, x.b, s.hk, x.n, x.g);
+        if (!none) sink.buf = p.rows_o + i * D;
+        if (lead) p.rows_ml[i] = make_float2(m, l);
+      } else {
+        const int64_t head = s.hk * p.G + x.g;
+        sink.out = static_cast<__nv_bfloat16*>(p.o) + x.b * p.o_sb + head * p.o_sh + x.n * p.o_sn;
+        sink.inv = none ? 0.f : 1.f / l;
+        if (lead && p.lse != nullptr)
+          p.lse[(static_cast<int64_t>(x.b) * p.Hq + head) * p.Nq + x.n] =
+              none ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994530942f;
+      }
+    }
+    const int n_ch = D / 32;
+    const int ch0 = s.twin ? (h * n_ch + 1) / 2 : 0, ch1 = s.twin ? (h ? n_ch : (n_ch + 1) / 2) : n_ch;
+    const bool rows_here = __any_sync(0xffffffffu, real);
+    for (int ch = ch0; ch < ch1; ++ch) {
+      if (!rows_here) break;
+      __syncwarp();
+      uint32_t a[32];
+      float y[32];
+      if (s.twin) {
+        uint32_t b[32];
+        tmem_ld32(lane_base + C::tm_o(0) + ch * 32, a);
+        tmem_ld32(lane_base + C::tm_o(1) + ch * 32, b);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          // a stream without a key for this row is left out by a select: its O may never have been written
+          const float u = w0 > 0.f ? __uint_as_float(a[i]) * w0 : 0.f;
+          y[i] = w1 > 0.f ? fmaf(__uint_as_float(b[i]), w1, u) : u;
+        }
+      } else {
+        tmem_ld32(t_o + ch * 32, a);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(a[i]);
+      }
+      sink.put32(ch, y);
+    }
+    tc_fence_before();
+    __syncwarp();
+    // both warpgroups' arrivals free a stream's O: two of a warp when only its own reads it
+    if (s.twin) {
+      if (lane < 2) mbar_arrive(bars.o_empty(lane));
+    } else if (lane < 2) {
+      mbar_arrive(bars.o_empty(h));
+    }
+    if (*ctl.abort) return;
+  }
+}
+
+// ------------------------------------------------------------------ kernel
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constant__ PagedParams p) {
+  using P = PCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  const uint32_t sbase = (raw + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (sbase - raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  PBars bars{sbase + P::kOffBar, P::kStages};
+  static_assert(8 * (16 + 4 * P::kStages) + 8 <= P::kBarBytes, "barrier area");
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kOffBar + 8 * bars.count());
+  volatile uint32_t* abort_flag = tmem_slot + 1;
+  int32_t* scan = reinterpret_cast<int32_t*>(smem + P::kOffScan);  // [0, 12) warps' sums, [16..19] results
+
+  if (threadIdx.x == 0) {
+    mbar_init(bars.q_full(), 2);
+    mbar_init(bars.q_empty(), 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(bars.s_full(h), 1);
+      mbar_init(bars.p_full(h, 0), 4);
+      mbar_init(bars.p_full(h, 1), 4);
+      mbar_init(bars.o_full(h), 1);
+      mbar_init(bars.o_empty(h), 8);
+      mbar_init(bars.x_full(h), 4);
+    }
+    mbar_init(bars.done(), 1);
+    mbar_init(bars.t_full(), 1);
+    for (int s = 0; s < P::kStages; ++s) {
+      mbar_init(bars.k_full(s), 1);
+      mbar_init(bars.k_empty(s), 1);
+      mbar_init(bars.v_full(s), 1);
+      mbar_init(bars.v_empty(s), 1);
+    }
+    *abort_flag = 0u;
+    fence_barrier_init();
+    prefetch_tmap(&p.tm_k);
+    prefetch_tmap(&p.tm_v);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), Cfg<D>::kTmemCols);
+    tmem_relinquish();
+  }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dep_wait();  // the lengths are the previous kernel's to write
+
+  // First the total, then a running sum over the sequences: the CTA's first
+  // unit and the sequence that holds it. CTA 0 leaves the running sums for the
+  // kernel that joins the parts.
+  const int up = prefix_units(p);
+  auto block_sum = [&](int v, int& below) -> int {  // sum over the block; below: over the threads before this one
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    __syncthreads();
+    if (lane == 31) scan[warp] = inc;
+    __syncthreads();
+    int total = 0;
+    below = inc - v;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) below += scan[w];
+      total += scan[w];
+    }
+    return total;
+  };
+  int mine = 0, below;
+  for (int b = threadIdx.x; b < p.B; b += kThreads) mine += p.Hk * own_units(p, seq_lens(p, b));
+  const int units = up + block_sum(mine, below);
+  const Split split(units, gridDim.x);
+  const int u0 = split.lo(blockIdx.x), u1 = split.lo(blockIdx.x + 1);
+  if (threadIdx.x == 0) {
+    scan[16] = u0 < up ? 0 : p.B;  // first sequence to look at
+    scan[17] = u0 < up ? up : units;
+  }
+  int run = up;
+  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    const int v = b < p.B ? p.Hk * own_units(p, seq_lens(p, b)) : 0;
+    const int total = block_sum(v, below);
+    const int at = run + below;
+    if (b < p.B) {
+      if (blockIdx.x == 0) p.starts[b] = at;
+      if (u0 >= up && u0 >= at && u0 < at + v) {
+        scan[16] = b;
+        scan[17] = at;
+      }
+    }
+    run += total;
+  }
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.starts[p.B] = units;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Ctl ctl{abort_flag, g_paged_status, p.timeout_ns};
+  const PSegIter it(p, u0, u1, scan[16], scan[17]);
+
+  if (warp < 4) {
+    set_max_regs_dec<kRegsControl>();
+    if (warp == 0) {
+      paged_loader<D>(p, sbase, bars, it, ctl);
+    } else if (warp == 1) {
+      paged_mma<D>(p, sbase, bars, tmem, it, ctl);
+    } else {
+      paged_gather_q<D>(p, smem, bars, it, ctl);
+    }
+    __syncwarp();
+  } else {
+    set_max_regs_inc<kRegsSoftmax>();
+    paged_softmax<D>(p, smem, bars, tmem, it, ctl);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, Cfg<D>::kTmemCols);
+  }
+}
+
+// ------------------------------------------------------------------ joining the parts
+//
+// A warp per row. The parts of a row, in order: those of its prefix task, then
+// those of its own task; each is a slot of a CTA (cut task) or a row of the row
+// buffers (uncut). Lane i holds part i's maximum, sum and address; then the warp
+// goes over the parts, lane j adding float4 j of each.
+constexpr int kJoinWarps = 8;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  grid_dep_wait();
+  const int lane = threadIdx.x & 31;
+  const int64_t rows = static_cast<int64_t>(p.B) * p.Nq * p.Hq;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int rs = p.Nq * p.G;
+  const int64_t bh = row / rs;
+  const int r = static_cast<int>(row - bh * rs), b = static_cast<int>(bh / p.Hk), hk = static_cast<int>(bh - static_cast<int64_t>(b) * p.Hk);
+  const int n = r / p.G, g = r - n * p.G;
+  const int units = p.starts[p.B];
+  const Split split(units, grid);
+
+  // the row's two tasks: first unit with a tile, tiles, row inside the task
+  struct Span {
+    int c0, parts, in_task;  // parts 0: none; 1: uncut
+  };
+  auto span = [&](int a, int tiles, int in_task) {
+    Span s{0, 0, in_task};
+    if (tiles > 0) {
+      s.c0 = split.owner(a + kPagedTaskCost);
+      s.parts = split.owner(a + kPagedTaskCost + tiles - 1) - s.c0 + 1;
+    }
+    return s;
+  };
+  Span pre{0, 0, 0}, own{0, 0, 0};
+  const SeqLens sl = seq_lens(p, b);
+  if (p.prefix_len > 0) {
+    const int rp = b * rs + r, t = rp / kPagedTaskRows, tiles = prefix_tiles(p);
+    pre = span((hk * prefix_tasks(p) + t) * (tiles + kPagedTaskCost), tiles, rp - t * kPagedTaskRows);
+  }
+  {
+    const int t = r / kPagedTaskRows;
+    int a = p.starts[b] + hk * own_units(p, sl);
+    for (int i = 0; i < t; ++i) {
+      const int tiles = own_tiles(p, sl, i);
+      a += tiles + (tiles > 0 ? kPagedTaskCost : 0);
+    }
+    own = span(a, own_tiles(p, sl, t), r - t * kPagedTaskRows);
+  }
+  if (p.prefix_len == 0 && own.parts == 1) return;  // written by the attention kernel
+
+  const int parts = pre.parts + own.parts;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float M = -CUDART_INF_F, L = 0.f;
+  for (int base = 0; base < parts; base += 32) {
+    const int i = base + lane;
+    float m = -CUDART_INF_F, l = 0.f;
+    const float* src = nullptr;  // float4 j of the row at src + j * step
+    int step = 0;
+    if (i < parts) {
+      const bool is_pre = i < pre.parts;
+      const Span s = is_pre ? pre : own;
+      const int k = is_pre ? i : i - pre.parts;
+      if (s.parts == 1) {
+        const int64_t at = (is_pre ? 0 : rows) + row;
+        const float2 ml = p.rows_ml[at];
+        m = ml.x;
+        l = ml.y;
+        src = p.rows_o + at * D;
+        step = 4;
+      } else {
+        const int quarter = (s.in_task % kBM) / 32, in_q = s.in_task % 32;
+        const float* slot = paged_slot<D>(p, s.c0 + k, k == 0, s.in_task / kBM, quarter);
+        m = slot[32 * D + in_q];
+        l = slot[32 * D + 32 + in_q];
+        src = slot + 4 * in_q;
+        step = 128;
+      }
+    }
+    float mx = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    const float M1 = fmaxf(M, mx);
+    if (M1 == -CUDART_INF_F) continue;
+    const float old = M == -CUDART_INF_F ? 0.f : ex2(M - M1);
+    const float w = m == -CUDART_INF_F ? 0.f : ex2(m - M1);
+    acc.x *= old;
+    acc.y *= old;
+    acc.z *= old;
+    acc.w *= old;
+    float lw = l * w;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+    L = fmaf(L, old, lw);
+    M = M1;
+    const int count = min(32, parts - base);
+    for (int j = 0; j < count; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const float* sj = reinterpret_cast<const float*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j));
+      const int st = __shfl_sync(0xffffffffu, step, j);
+      if (wj > 0.f && lane < D / 4) {
+        const float4 v = *reinterpret_cast<const float4*>(sj + lane * st);
+        acc.x = fmaf(v.x, wj, acc.x);
+        acc.y = fmaf(v.y, wj, acc.y);
+        acc.z = fmaf(v.z, wj, acc.z);
+        acc.w = fmaf(v.w, wj, acc.w);
+      }
+    }
+  }
+  const int64_t head = hk * p.G + g;
+  const float inv = 1.f / L;
+  if (lane < D / 4) {
+    uint2 w = make_uint2(0u, 0u);
+    if (M != -CUDART_INF_F) w = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + b * p.o_sb + head * p.o_sh + n * p.o_sn + lane * 4) = w;
+  }
+  if (lane == 0 && p.lse != nullptr)
+    p.lse[(static_cast<int64_t>(b) * p.Hq + head) * p.Nq + n] =
+        M == -CUDART_INF_F ? -CUDART_INF_F : (M + log2f(L)) * 0.69314718055994530942f;
+}
+
+template <int D>
+cudaError_t launch_paged_dim(const PagedParams& p, int grid, cudaStream_t s) {
+  constexpr int smem = PCfg<D>::kSmemBytes > kMinSmemBytes ? PCfg<D>::kSmemBytes : kMinSmemBytes;
+  cudaError_t e = cudaFuncSetAttribute(paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, paged_kernel<D>, p)) != cudaSuccess) return e;
+  const int64_t rows = static_cast<int64_t>(p.B) * p.Nq * p.Hq;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(kJoinWarps * 32);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p, grid);
+}
+
+}  // namespace dev
+
+cudaError_t launch_paged(const PagedParams& p, int d, int grid, cudaStream_t s) {
+  switch (d) {
+    case 32: return dev::launch_paged_dim<32>(p, grid, s);
+    case 64: return dev::launch_paged_dim<64>(p, grid, s);
+    case 128: return dev::launch_paged_dim<128>(p, grid, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t paged_take_status(uint32_t word[4]) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, dev::g_paged_status, 4 * sizeof(uint32_t), 0, cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess || word[0] == 0) return e;
+  const uint32_t zero[4] = {0, 0, 0, 0};
+  return cudaMemcpyToSymbol(dev::g_paged_status, zero, sizeof(zero), 0, cudaMemcpyHostToDevice);
+}
+
+}  // namespace attn

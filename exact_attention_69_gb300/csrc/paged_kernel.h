@@ -1,0 +1,50 @@
+// paged_kernel.h -- parameters of the paged attention kernels (attn_paged.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace attn {
+
+// Rows of a task are numbered r = n * G + g inside one sequence (G query heads
+// share a key head) and b * Nq * G + n * G + g over the batch for the prefix.
+constexpr int kPagedTaskRows = 256;  // two 128-row query tiles
+// Cost of starting a task in units of one K/V tile: query gather, epilogue.
+constexpr int kPagedTaskCost = 1;
+constexpr int kPagedMinUnits = 2;    // least work that opens another CTA
+
+struct PagedParams {
+  CUtensorMap tm_k;             // 4-D (d, slot, head, page) bf16 maps, box (swizzle span, min(page, 128), 1, 1)
+  CUtensorMap tm_v;
+  const void* q;                // bf16, element strides of b, h, n
+  int64_t q_sb, q_sh, q_sn;
+  void* o;
+  int64_t o_sb, o_sh, o_sn;
+  float* lse;                   // fp32 [B, Hq, Nq] or nullptr
+  const int32_t* table;         // [B, table_width] pages of each sequence
+  int64_t table_sb;
+  const int32_t* kv_lens;       // [B]
+  const int32_t* q_lens;        // [B] or nullptr (Nq each)
+  const int32_t* prefix_table;  // pages of the shared prefix
+  int B, Hq, Hk, Nq, G;
+  int prefix_len;
+  int page_shift;
+  int max_len;                  // table_width * page size: longest own length that the table holds
+  int causal;                   // bottom-right causal over prefix and own keys together
+  float c;                      // scale * log2(e)
+  // workspace
+  int32_t* starts;              // [B + 1]: first unit of each sequence's tasks; the total
+  float* slots;                 // per CTA 2 x 2 query tiles x 128 rows x (d + 2): parts of cut tasks
+  float* rows_o;                // [2][B * Nq * Hq][d]: uncut prefix and own results
+  float2* rows_ml;              // [2][B * Nq * Hq]: their running maximum (log2 units) and sum
+  uint64_t timeout_ns;
+  int inject;
+};
+
+// grid: CTAs of the attention kernel; the second kernel joins the parts.
+cudaError_t launch_paged(const PagedParams& p, int d, int grid, cudaStream_t s);
+// Reads and clears the current device's status word of the paged kernels.
+cudaError_t paged_take_status(uint32_t word[4]);
+
+}  // namespace attn

@@ -1,0 +1,451 @@
+// rope.cu -- root-mean-square norm of every head with the rotary position
+// embedding in the same pass, its gradient, and the append to a paged cache.
+//
+//   y = R(pos) (x * r * w),  r = 1 / sqrt(mean(x^2) + eps)
+// with R turning each pair of the first `rot` channels by pos * inv_freq.
+//
+// What bounds it: each row is read once and written once and a row has ~10
+// operations an element, so device memory. A row of d channels is d/8 threads
+// of 16 bytes each, so a warp reads 512 contiguous bytes of rows; the row sum
+// and the exchange with the pair's other half (raw bf16, four words) are warp
+// shuffles and nothing is staged. A thread keeps one token and one channel
+// chunk and goes over the heads: its cosines and sines are computed once and
+// stay in registers. Loads of four heads are in flight at a time.
+//
+// Angles: a frequency becomes a 64-bit fraction of a turn, and position times
+// frequency is a 64-bit integer product whose overflow drops whole turns. The
+// fraction is exact to 2^-64 * position, where a 32-bit product of position
+// and frequency is off by 2^-24 of the angle (0.06 radians at position 10^6).
+#include <cuda_bf16.h>
+#include <math_constants.h>
+
+#include "rope_kernel.h"
+
+namespace attn {
+namespace {
+
+constexpr int kUnroll = 4;
+
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// radians per position -> turns per position as a 64-bit fraction (whole turns
+// dropped): f = m 2^e, f / 2pi = m (2^66 / 2pi) 2^(e - 66), times 2^64. Integer
+// arithmetic: the double-precision units of this GPU are few.
+__device__ __forceinline__ uint64_t turns_of(double f) {
+  const uint64_t bits = static_cast<uint64_t>(__double_as_longlong(f));
+  const int ex = static_cast<int>((bits >> 52) & 0x7ff);
+  if (ex == 0 || ex == 0x7ff) return 0;  // zero, subnormal; infinity and NaN have no angle
+  const uint64_t m = (bits & 0xFFFFFFFFFFFFFull) | (1ull << 52);
+  const uint64_t kInvTwoPi66 = 11743562013128004906ull;  // round(2^66 / (2 pi))
+  const uint64_t hi = __umul64hi(m, kInvTwoPi66), lo = m * kInvTwoPi66;
+  const int sh = 2 - (ex - 1075);  // right shift of the 128-bit product
+  uint64_t t;
+  if (sh <= 0) {
+    t = -sh < 64 ? lo << -sh : 0;
+  } else if (sh < 64) {
+    t = (lo >> sh) | (hi << (64 - sh));
+  } else {
+    t = sh < 128 ? hi >> (sh - 64) : 0;
+  }
+  return (bits >> 63) ? 0ull - t : t;
+}
+
+// cos and sin of position * frequency.
+__device__ __forceinline__ void angle(int64_t pos, uint64_t turns, float& c, float& s) {
+  const uint64_t ph = static_cast<uint64_t>(pos) * turns;
+  const float half_turns = static_cast<float>(static_cast<int32_t>(ph >> 32)) * 4.656612873077392578125e-10f;  // 2^-31
+  sincospif(half_turns, &s, &c);
+}
+
+__device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
+  return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+}
+
+__device__ __forceinline__ void load_weights(const void* w, int type, int at, float (&out)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    out[i] = w == nullptr ? 1.f
+             : type == 1  ? static_cast<const float*>(w)[at + i]
+                          : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[at + i]);
+}
+
+// Sum over the d/8 threads of a row.
+template <int D>
+__device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+  for (int o = D / 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+
+__device__ __forceinline__ int64_t position(const void* pos, int type, int64_t sb, int64_t sn, int b, int n) {
+  const int64_t at = b * sb + n * sn;
+  return type == 1 ? static_cast<const int32_t*>(pos)[at] : static_cast<const int64_t*>(pos)[at];
+}
+
+// A thread's place in its row and its angles. Half-split pairs (IL false):
+// channel i turns with channel i + rot/2, held by the thread rot/16 chunks
+// away; side by side (IL true): both channels of a pair are the thread's own.
+template <int D, bool IL>
+struct Turn {
+  static constexpr int kN = IL ? 4 : 8;
+  int c;         // chunk of 8 channels
+  bool on;       // the chunk is rotated
+  bool low;      // half-split: the first half of the pairs
+  int partner;   // half-split: lane of the other half
+  int pchunk;    // half-split: its chunk
+  float cs[kN], sn[kN];
+
+  __device__ __forceinline__ Turn(int rot) {
+    c = threadIdx.x % (D / 8);
+    const int lane = threadIdx.x & 31, hc = rot / 16;
+    on = c * 8 < rot;
+    low = c < hc;
+    pchunk = (!IL && on) ? (low ? c + hc : c - hc) : c;
+    partner = lane + (pchunk - c);
+  }
+  __device__ __forceinline__ void set(int64_t pos, const uint64_t* turns) {
+    const int f0 = IL ? c * 4 : (low ? c : pchunk) * 8;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      cs[i] = 1.f;
+      sn[i] = 0.f;
+      if (on) angle(pos, turns[f0 + i], cs[i], sn[i]);
+      if (!IL && low) sn[i] = -sn[i];
+    }
+  }
+  // y = R x (sign 1) or R^T x (sign -1); other: the partner's values (half-split).
+  __device__ __forceinline__ void apply(float (&x)[8], const float (&other)[8], float sign) const {
+    if (!on) return;
+    if constexpr (IL) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = x[2 * i], b = x[2 * i + 1], s = sign * sn[i];
+        x[2 * i] = a * cs[i] - b * s;
+        x[2 * i + 1] = b * cs[i] + a * s;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[i] = x[i] * cs[i] + other[i] * (sign * sn[i]);
+    }
+  }
+  // The partner's raw chunk (all 32 lanes call it).
+  __device__ __forceinline__ uint4 exchange(const uint4& u) const {
+    if constexpr (IL) {
+      return u;
+    } else {
+      return make_uint4(__shfl_sync(0xffffffffu, u.x, partner), __shfl_sync(0xffffffffu, u.y, partner),
+                        __shfl_sync(0xffffffffu, u.z, partner), __shfl_sync(0xffffffffu, u.w, partner));
+    }
+  }
+};
+
+__device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
+  return __ldcs(reinterpret_cast<const uint4*>(p));
+}
+__device__ __forceinline__ void store16(__nv_bfloat16* p, const uint4& u) { *reinterpret_cast<uint4*>(p) = u; }
+
+// Heads [h0, h1) of one token: norm, turn, store. in/out: the token's first
+// head at this thread's channels. Every lane of the warp goes through the
+// same heads; `live` and `write` say whose loads and stores are real.
+template <int D, bool IL, bool NORM>
+__device__ __forceinline__ void rope_heads(const __nv_bfloat16* in, int64_t in_sh, __nv_bfloat16* out,
+                                           int64_t out_sh, int h0, int h1, bool live, bool write,
+                                           const void* w, int w_type, float eps, const Turn<D, IL>& t) {
+  float wo[8], wp[8];
+  if constexpr (NORM) {
+    load_weights(w, w_type, t.c * 8, wo);
+    load_weights(w, w_type, t.pchunk * 8, wp);
+  }
+  for (int h = h0; h < h1; h += kUnroll) {
+    uint4 raw[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      raw[u] = make_uint4(0, 0, 0, 0);
+      if (live && h + u < h1) raw[u] = load16(in + (h + u) * in_sh);
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (h + u >= h1) break;  // the same for the whole block
+      float x[8], o[8];
+      unpack(raw[u], x);
+      unpack(t.exchange(raw[u]), o);
+      if constexpr (NORM) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+        const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          x[i] *= r * wo[i];
+          o[i] *= r * wp[i];
+        }
+      }
+      t.apply(x, o, 1.f);
+      if (write) store16(out + (h + u) * out_sh, pack(x));
+    }
+  }
+}
+
+template <int D, bool IL, bool NORM>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ uint64_t turns[D / 2];
+  grid_dep_launch();
+  grid_dep_wait();
+  for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turns[i] = turns_of(p.inv_freq[i]);
+  __syncthreads();
+  const int64_t tok = static_cast<int64_t>(blockIdx.x) * rope_tokens_per_block(D) + threadIdx.x / (D / 8);
+  const bool live = tok < static_cast<int64_t>(p.B) * p.N;
+  const int b = live ? static_cast<int>(tok / p.N) : 0, n = live ? static_cast<int>(tok - static_cast<int64_t>(b) * p.N) : 0;
+  Turn<D, IL> t(p.rot);
+  const int start = p.starts != nullptr ? p.starts[b] : 0;
+  t.set(p.pos != nullptr ? position(p.pos, p.pos_type, p.pos_sb, p.pos_sn, b, n) : p.pos_offset + start + n, turns);
+  // virtual heads: queries, then keys, then values
+  const int v0 = blockIdx.y * p.heads_per_block, v1 = v0 + p.heads_per_block;
+  const auto at = [&](const RopeTensor& x) {
+    return static_cast<__nv_bfloat16*>(x.p) + b * x.sb + n * x.sn + t.c * 8;
+  };
+  if (v0 < p.Hq)
+    rope_heads<D, IL, NORM>(at(p.q), p.q.sh, at(p.qo), p.qo.sh, v0, min(v1, p.Hq), live, live, p.wq, p.wq_type,
+                            p.eps, t);
+  const int k0 = max(v0 - p.Hq, 0), k1 = min(v1 - p.Hq, p.Hk);
+  if (!p.cache) {
+    if (k0 < k1)
+      rope_heads<D, IL, NORM>(at(p.k), p.k.sh, at(p.ko), p.ko.sh, k0, k1, live, live, p.wk, p.wk_type, p.eps, t);
+    return;
+  }
+  // The token's slot. A token behind its sequence's count, behind the table's
+  // end or on a page that the cache does not have leaves the cache as it was.
+  const int64_t slot = static_cast<int64_t>(start) + n;
+  bool write = live && start >= 0 && (p.counts == nullptr || n < p.counts[b]) && (slot >> p.page_shift) < p.table_width;
+  int page = 0;
+  if (write) {
+    page = p.table[b * p.table_sb + (slot >> p.page_shift)];
+    write = page >= 0 && page < p.n_pages;
+  }
+  const int in_page = static_cast<int>(slot & ((1 << p.page_shift) - 1));
+  const int c8 = t.c * 8;
+  if (k0 < k1)
+    rope_heads<D, IL, NORM>(at(p.k), p.k.sh,
+                            static_cast<__nv_bfloat16*>(p.kc) + page * p.kc_sp + in_page * p.kc_st + c8, p.kc_sh, k0,
+                            k1, write, write, p.wk, p.wk_type, p.eps, t);
+  const int w0 = max(v0 - p.Hq - p.Hk, 0), w1 = min(v1 - p.Hq - p.Hk, p.Hk);
+  if (!write) return;
+  const __nv_bfloat16* vi = at(p.v);
+  __nv_bfloat16* vo = static_cast<__nv_bfloat16*>(p.vc) + page * p.vc_sp + in_page * p.vc_st + c8;
+  for (int h = w0; h < w1; h += kUnroll) {
+    uint4 raw[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (h + u < w1) raw[u] = load16(vi + (h + u) * p.v.sh);
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (h + u < w1) store16(vo + (h + u) * p.vc_sh, raw[u]);
+  }
+}
+
+// ---------------------------------------------------------------- backward
+//
+//   g = R^T dy,  h = g * w,  dx = r h - x r^3 mean(h x),  dw = sum g x r
+// A thread keeps one channel chunk over all of its rows, so dw is eight
+// registers; the block adds its threads' sums in a fixed order and leaves one
+// row of partial sums, which a second kernel adds: no atomics, the same bits
+// every time.
+template <int D, bool IL, bool NORM>
+__device__ __forceinline__ void rope_bwd_heads(const __nv_bfloat16* x_in, int64_t x_sh, const __nv_bfloat16* dy_in,
+                                               int64_t dy_sh, __nv_bfloat16* dx_out, int64_t dx_sh, int H, bool live,
+                                               const float (&w)[8], float eps, const Turn<D, IL>& t,
+                                               float (&dw)[8]) {
+  constexpr int kU = 2;
+  for (int h = 0; h < H; h += kU) {
+    uint4 rx[kU], rg[kU];
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
+      if (live && h + u < H) {
+        if constexpr (NORM) rx[u] = load16(x_in + (h + u) * x_sh);
+        rg[u] = load16(dy_in + (h + u) * dy_sh);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      if (h + u >= H) break;
+      float g[8], o[8];
+      unpack(rg[u], g);
+      unpack(t.exchange(rg[u]), o);
+      t.apply(g, o, -1.f);
+      if constexpr (NORM) {
+        float x[8];
+        unpack(rx[u], x);
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          ss = fmaf(x[i], x[i], ss);
+          dot = fmaf(g[i] * w[i], x[i], dot);
+        }
+        const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
+        const float k = row_sum<D>(dot) * (1.f / D) * r * r * r;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (live) dw[i] = fmaf(g[i] * r, x[i], dw[i]);
+          g[i] = r * g[i] * w[i] - x[i] * k;
+        }
+      }
+      if (live) store16(dx_out + (h + u) * dx_sh, pack(g));
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void block_sum(const float (&dw)[8], float* smem, float* out) {
+  // [token slot][channel]; then one thread per channel adds the slots in order
+  constexpr int kRows = rope_tokens_per_block(D);
+  __syncthreads();
+  const int c = threadIdx.x % (D / 8), row = threadIdx.x / (D / 8);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) smem[row * D + c * 8 + i] = dw[i];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float s = 0.f;
+    for (int r = 0; r < kRows; ++r) s += smem[r * D + threadIdx.x];
+    out[threadIdx.x] = s;
+  }
+}
+
+template <int D, bool IL, bool NORM>
+__global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const __grid_constant__ RopeBwdParams p) {
+  __shared__ uint64_t turns[D / 2];
+  __shared__ float sums[rope_tokens_per_block(D) * D];
+  grid_dep_launch();
+  grid_dep_wait();
+  for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turns[i] = turns_of(p.inv_freq[i]);
+  __syncthreads();
+  Turn<D, IL> t(p.rot);
+  float wq[8], wk[8], dwq[8], dwk[8];
+  load_weights(p.wq, p.wq_type, t.c * 8, wq);
+  load_weights(p.wk, p.wk_type, t.c * 8, wk);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
+  const int64_t total = static_cast<int64_t>(p.B) * p.N;
+  constexpr int kTok = rope_tokens_per_block(D);
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok; t0 < total; t0 += static_cast<int64_t>(gridDim.x) * kTok) {
+    const int64_t tok = t0 + threadIdx.x / (D / 8);
+    const bool live = tok < total;
+    const int b = live ? static_cast<int>(tok / p.N) : 0,
+              n = live ? static_cast<int>(tok - static_cast<int64_t>(b) * p.N) : 0;
+    t.set(p.pos != nullptr ? position(p.pos, p.pos_type, p.pos_sb, p.pos_sn, b, n) : p.pos_offset + n, turns);
+    const auto at = [&](const RopeTensor& x) {
+      return static_cast<__nv_bfloat16*>(x.p) + b * x.sb + n * x.sn + t.c * 8;
+    };
+    rope_bwd_heads<D, IL, NORM>(at(p.q), p.q.sh, at(p.dyq), p.dyq.sh, at(p.dq), p.dq.sh, p.Hq, live, wq, p.eps, t,
+                                dwq);
+    rope_bwd_heads<D, IL, NORM>(at(p.k), p.k.sh, at(p.dyk), p.dyk.sh, at(p.dk), p.dk.sh, p.Hk, live, wk, p.eps, t,
+                                dwk);
+  }
+  if constexpr (NORM) {
+    if (p.dwq != nullptr) block_sum<D>(dwq, sums, p.part + static_cast<int64_t>(blockIdx.x) * 2 * D);
+    if (p.dwk != nullptr) block_sum<D>(dwk, sums, p.part + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * D);
+  }
+}
+
+// dw[side][channel] = sum of the blocks' partial sums; a block per side and 32
+// channels, a warp per stripe of rows, stripes joined in order.
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int blocks, int d, void* dwq, int wq_type,
+                                                       void* dwk, int wk_type) {
+  __shared__ float s[32][33];
+  grid_dep_launch();
+  grid_dep_wait();
+  const int side = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  void* out = side ? dwk : dwq;
+  if (out == nullptr) return;
+  const int c = blockIdx.x * 32 + lane;
+  float a = 0.f;
+  for (int r = warp; r < blocks; r += 32) a += part[(static_cast<int64_t>(r) * 2 + side) * d + c];
+  s[warp][lane] = a;
+  __syncthreads();
+  if (warp == 0) {
+    float z = 0.f;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) z += s[w][lane];
+    if ((side ? wk_type : wq_type) == 1)
+      static_cast<float*>(out)[c] = z;
+    else
+      static_cast<__nv_bfloat16*>(out)[c] = __float2bfloat16(z);
+  }
+}
+
+template <typename... Args, typename... Given>
+cudaError_t launch(void (*kern)(Args...), dim3 grid, int threads, cudaStream_t s, const Given&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D>
+cudaError_t launch_rope_dim(const RopeParams& p, dim3 grid, cudaStream_t s) {
+  if (p.interleaved)
+    return p.norm ? launch(rope_kernel<D, true, true>, grid, kRopeThreads, s, p)
+                  : launch(rope_kernel<D, true, false>, grid, kRopeThreads, s, p);
+  return p.norm ? launch(rope_kernel<D, false, true>, grid, kRopeThreads, s, p)
+                : launch(rope_kernel<D, false, false>, grid, kRopeThreads, s, p);
+}
+
+template <int D>
+cudaError_t launch_rope_bwd_dim(const RopeBwdParams& p, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.blocks));
+  if (p.interleaved)
+    return p.norm ? launch(rope_bwd_kernel<D, true, true>, grid, kRopeThreads, s, p)
+                  : launch(rope_bwd_kernel<D, true, false>, grid, kRopeThreads, s, p);
+  return p.norm ? launch(rope_bwd_kernel<D, false, true>, grid, kRopeThreads, s, p)
+                : launch(rope_bwd_kernel<D, false, false>, grid, kRopeThreads, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeParams& p, int d, dim3 grid, cudaStream_t s) {
+  switch (d) {
+    case 32: return launch_rope_dim<32>(p, grid, s);
+    case 64: return launch_rope_dim<64>(p, grid, s);
+    case 128: return launch_rope_dim<128>(p, grid, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_rope_bwd(const RopeBwdParams& p, int d, cudaStream_t s) {
+  cudaError_t e;
+  switch (d) {
+    case 32: e = launch_rope_bwd_dim<32>(p, s); break;
+    case 64: e = launch_rope_bwd_dim<64>(p, s); break;
+    case 128: e = launch_rope_bwd_dim<128>(p, s); break;
+    default: return cudaErrorInvalidValue;
+  }
+  if (e != cudaSuccess || !p.norm || (p.dwq == nullptr && p.dwk == nullptr)) return e;
+  return launch(rope_dw_kernel, dim3(static_cast<unsigned>(d / 32), 2), 1024, s,
+                static_cast<const float*>(p.part), p.blocks, d, p.dwq, p.wq_type, p.dwk, p.wk_type);
+}
+
+}  // namespace attn

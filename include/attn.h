@@ -310,6 +310,183 @@ int attn_bwd(const attn_bwd_params* p);
  */
 int attn_fwd_noalloc(const attn_params_ex* p);
 
+/* ------------------------------------------------------------------------
+ * Around the attention of a language model: per-head norm with rotary
+ * positions (and its gradient), the append to a paged key/value cache, and
+ * attention over such a cache with a prefix that the whole batch shares.
+ *
+ * These calls own no device memory: scratch is the caller's (a size function
+ * beside each call that needs some), needs no initialisation and is free again
+ * when the call's kernels are done. Calls that overlap on the device, captured
+ * graphs among them, each need their own. The first call may be a captured one.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { ATTN_TYPE_BF16 = 0, ATTN_TYPE_FP32 = 1 } attn_weight_type;
+typedef enum { ATTN_POS_NONE = 0, ATTN_POS_INT32 = 1, ATTN_POS_INT64 = 2 } attn_pos_type;
+
+/*
+ * attn_qk_norm_rope: y = R(pos) (x * r * w), r = 1 / sqrt(mean(x^2) + eps), for
+ * every head of q and k in one pass; the mean is over the head's d channels
+ * and w has d entries, the same for all heads of q (of k).
+ *   norm 0: no norm (r * w = 1; the weights must be NULL).
+ *   rot: channels of each head that are rotated, the first `rot` of d; 0 =
+ *     none, else a multiple of 16 up to d. Pair i turns by
+ *     position * inv_freq[i] (radians): (x_i, x_{i + rot/2}), or
+ *     (x_{2i}, x_{2i+1}) with `interleaved`. The product is formed modulo a
+ *     turn in 64-bit fixed point, so far positions lose nothing. A frequency
+ *     that is zero, subnormal or not finite does not rotate.
+ *   positions: int32 or int64 [B, N] with element strides pos_stride (0
+ *     allowed: shared by the batch), or NULL: token n is at pos_offset + n.
+ * q, q_out [B, Hq, N, d]; k, k_out [B, Hk, N, d] bf16; element strides of
+ * (b, h, n), all zero = contiguous; inputs may have zero strides; the last
+ * dimension contiguous, pointers 16-byte aligned, strides multiples of 8. A
+ * stride of a dimension of size 1 is ignored. An output may be its own input.
+ * d in {32, 64, 128}. Hk 0: queries only (k, k_out NULL).
+ */
+typedef struct attn_rope_params {
+  const void* q;
+  const void* k;
+  const void* v;              /* attn_kv_append only */
+  void* q_out;
+  void* k_out;                /* attn_qk_norm_rope only */
+  int B, N, Hq, Hk, d;
+  int rot, interleaved, norm;
+  float eps;                  /* >= 0 and finite */
+  const void* q_weight;       /* [d] or NULL (ones) */
+  const void* k_weight;
+  int q_weight_type, k_weight_type; /* attn_weight_type */
+  const double* inv_freq;     /* device, [rot / 2]; NULL iff rot is 0 */
+  const void* positions;      /* device, or NULL */
+  int pos_type;               /* attn_pos_type; NONE iff positions is NULL */
+  int64_t pos_stride[2];
+  int64_t pos_offset;
+  int64_t q_stride[3], k_stride[3], v_stride[3], q_out_stride[3], k_out_stride[3];
+  /* attn_kv_append only (else zero) */
+  void* k_cache;              /* bf16 [n_pages, Hk, page_size, d] */
+  void* v_cache;
+  int64_t k_cache_stride[3];  /* elements between pages, heads, slots; zero = contiguous */
+  int64_t v_cache_stride[3];
+  int n_pages, page_size;     /* page_size: a power of two >= 16 */
+  const int32_t* block_table; /* device, [B, table_width] pages of each sequence */
+  int table_width;
+  int64_t table_stride;       /* elements between sequences */
+  const int32_t* starts;      /* device, [B]: tokens that each sequence holds already */
+  const int32_t* counts;      /* device, [B]: real tokens of the N new ones, or NULL (all) */
+  void* stream;               /* cudaStream_t; NULL = the calling thread's stream */
+} attn_rope_params;
+
+/* Zero every field. */
+void attn_rope_params_init(attn_rope_params* p);
+
+int attn_qk_norm_rope(const attn_rope_params* p);
+
+/*
+ * attn_kv_append: token n of sequence b goes to slot starts[b] + n of the
+ * sequence, page block_table[b][slot / page_size], place slot % page_size:
+ * keys normed and rotated as by attn_qk_norm_rope, values as they are. With
+ * Hq > 0 the queries of the same tokens are normed and rotated into q_out in
+ * the same launch (every token, also behind counts[b]). Without `positions`
+ * token n is at pos_offset + starts[b] + n. Nothing else of the cache is
+ * written: not for tokens n >= counts[b], for a negative start, for slots
+ * behind the table's end, nor for entries that are not a page of the cache.
+ * Two tokens of one call on the same place of a page leave one or the other,
+ * in parts of 16 bytes.
+ */
+int attn_kv_append(const attn_rope_params* p);
+
+/*
+ * attn_qk_norm_rope_bwd: gradients through attn_qk_norm_rope. With g = R^T dy
+ * and h = g * w: dx = r h - x r^3 mean(h x), dw = sum over tokens and heads of
+ * g x r (without norm dx = g). Sums are fp32 in a fixed order: the same inputs
+ * give the same bits. dq, dk as q, k; dq_weight, dk_weight of the weights'
+ * types, or NULL. Workspace: attn_qk_norm_rope_bwd_workspace_bytes (0 without
+ * weight gradients), 16-byte aligned.
+ */
+typedef struct attn_rope_bwd_params {
+  const void* q;
+  const void* k;
+  const void* dq_out;         /* gradients at the outputs */
+  const void* dk_out;
+  void* dq;
+  void* dk;
+  int B, N, Hq, Hk, d;
+  int rot, interleaved, norm;
+  float eps;
+  const void* q_weight;
+  const void* k_weight;
+  int q_weight_type, k_weight_type;
+  void* dq_weight;
+  void* dk_weight;
+  const double* inv_freq;
+  const void* positions;
+  int pos_type;
+  int64_t pos_stride[2];
+  int64_t pos_offset;
+  int64_t q_stride[3], k_stride[3], dq_out_stride[3], dk_out_stride[3], dq_stride[3], dk_stride[3];
+  void* workspace;
+  uint64_t workspace_bytes;
+  void* stream;
+} attn_rope_bwd_params;
+
+void attn_rope_bwd_params_init(attn_rope_bwd_params* p);
+int attn_qk_norm_rope_bwd(const attn_rope_bwd_params* p);
+/* Bytes of workspace, or a negative attn_status. */
+int64_t attn_qk_norm_rope_bwd_workspace_bytes(const attn_rope_bwd_params* p);
+
+/*
+ * attn_paged: attention of B sequences over a paged cache. The keys of
+ * sequence b are the prefix_len tokens of the pages in prefix_table, the same
+ * for all sequences, then kv_lens[b] tokens of the pages in block_table[b].
+ * Its Nq query rows are the last q_lens[b] of those tokens (rows behind
+ * q_lens[b] are padding); with T = prefix_len + kv_lens[b]
+ *   ATTN_MASK_CAUSAL_BR  row i sees keys j <= i + T - q_lens[b]
+ *   ATTN_MASK_NONE       every row i < q_lens[b] sees all T keys
+ *   O[b,h,i,:] = sum_j softmax_j(scale q . k_j) v_j,  LSE the natural-log sum.
+ * A row that sees no key gives O = 0, LSE = -inf. Query head h reads key head
+ * h / (Hq / Hk). The prefix's keys are read once for up to 256 query rows
+ * (Nq * Hq / Hk of each sequence), not once per sequence.
+ * Lengths and tables are read on the device when the kernels run. kv_lens is
+ * clamped to what the table holds, q_lens to Nq; a table entry that is not a
+ * page of the cache reads as zeros. Slots of a page behind a sequence's end
+ * may hold anything. Values of keys that only some rows see must be finite.
+ * Two kernels are enqueued: attention, and the join of tasks that were cut.
+ */
+typedef struct attn_paged_params {
+  const void* q;              /* bf16 [B, Hq, Nq, d] */
+  const void* k_cache;        /* bf16 [n_pages, Hk, page_size, d] */
+  const void* v_cache;
+  void* o;                    /* bf16 [B, Hq, Nq, d] */
+  float* lse;                 /* fp32 [B, Hq, Nq] contiguous, or NULL */
+  const int32_t* block_table; /* device, [B, table_width] */
+  const int32_t* kv_lens;     /* device, [B] */
+  const int32_t* q_lens;      /* device, [B], or NULL (Nq each) */
+  const int32_t* prefix_table;/* device, [prefix_pages], or NULL */
+  int B, Hq, Hk, Nq, d;       /* Hq a multiple of Hk; d in {32, 64, 128} */
+  int n_pages, page_size;     /* page_size: a power of two >= 16 */
+  int table_width;
+  int64_t table_stride;
+  int prefix_len, prefix_pages;
+  float scale;                /* > 0 and finite */
+  int mask_kind;              /* ATTN_MASK_NONE or ATTN_MASK_CAUSAL_BR */
+  int64_t q_stride[3], o_stride[3];             /* elements, (b, h, n); zero = contiguous */
+  int64_t k_cache_stride[3], v_cache_stride[3]; /* pages, heads, slots; zero = contiguous */
+  void* workspace;            /* attn_paged_workspace_bytes, 16-byte aligned */
+  uint64_t workspace_bytes;
+  void* stream;
+  int num_ctas;               /* 0 = one per SM (smaller values are for tests) */
+  uint64_t timeout_ns;        /* bound on every device-side wait; 0 = 2 seconds */
+  int inject;                 /* test hook, as attn_params_ex.inject */
+} attn_paged_params;
+
+void attn_paged_params_init(attn_paged_params* p);
+int attn_paged(const attn_paged_params* p);
+/* Bytes of workspace on the current device, or a negative attn_status. Depends
+ * on B, Hq, Nq, d, num_ctas and whether there is a prefix, not on lengths. */
+int64_t attn_paged_workspace_bytes(const attn_paged_params* p);
+
+/* sizeof of attn_rope_params (0), attn_rope_bwd_params (1), attn_paged_params (2). */
+int attn_struct_size(int which);
+
 #ifdef __cplusplus
 }
 #endif
