@@ -15,7 +15,9 @@
 // A CTA (one per SM):
 //   warp 0      loader: page numbers, TMA of the pages of each K and V tile
 //   warp 1      MMA issuer: S = Q K^T and O += P V (tcgen05, TMEM)
-//   warps 2-3   gather the task's query rows into swizzled shared memory
+//   warp 2      gathers the task's query rows into swizzled shared memory
+//   warp 3      works out the CTA's tasks and hands them to the others through
+//               a small ring: the divisions are done once, not by every role
 //   warps 4-7 / 8-11  softmax of stream 0 / 1: one thread per row
 // A task of more than 128 rows has two query tiles, one per stream, and each
 // K/V tile serves both. A task of up to 128 rows has one query tile and its
@@ -41,25 +43,50 @@ namespace dev {
 
 __device__ uint32_t g_paged_status[4];
 
+// One CTA's share of one task, as warp 3 hands it to the other roles.
+struct PSeg {
+  int rows;        // rows that the task's key head has in all; 0: the CTA is done
+  int row0;        // first row of the task
+  int keys;        // keys of the task's key space
+  int k0, k1;      // tiles [k0, k1)
+  int hk, b;       // key head; sequence (own tasks)
+  int len, ql;     // the sequence's lengths (own tasks)
+  int flags;
+  int pad[2];
+  static constexpr int kPrefix = 1, kTwin = 2, kWhole = 4, kFirst = 8;
+  __device__ bool prefix() const { return flags & kPrefix; }
+  __device__ bool twin() const { return flags & kTwin; }    // one query tile, tiles in turn
+  __device__ bool whole() const { return flags & kWhole; }  // every tile of the task
+  __device__ bool first() const { return flags & kFirst; }  // holds the task's first tile
+};
+static_assert(sizeof(PSeg) == 48, "three 16-byte words");
+
 template <int D>
 struct PCfg {
   using C = Cfg<D>;  // tile layout (swizzle, chunks) and MMA descriptors
-  static constexpr int kStages = D == 128 ? 2 : (D == 64 ? 5 : 8);  // of K and of V
+  // K and V tiles share one ring in the order in which the MMA warp takes
+  // them; with 128 channels its five stages are what shared memory holds
+  // beside two query tiles (two stages each of K and V kept one tile of four
+  // in flight too few: 3600 cycles a tile against 2850).
+  static constexpr int kStages = D == 128 ? 5 : (D == 64 ? 10 : 16);
+  static constexpr int kSegs = 4;  // ring of task descriptors
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = 2 * C::kTileBytes;
-  static constexpr int kOffV = kOffK + kStages * C::kTileBytes;
-  static constexpr int kOffBar = kOffV + kStages * C::kTileBytes;
-  static constexpr int kBarBytes = 512;
-  static constexpr int kOffX = kOffBar + kBarBytes;  // exchange: [2 buffers][2 streams][m, l][128]
-  static constexpr int kXBytes = 2 * 2 * 2 * 128 * 4;
-  static constexpr int kOffScan = kOffX + kXBytes;   // 16 + 4 int32
-  static constexpr int kSmemBytes = kOffScan + 128 + 1024;
+  static constexpr int kOffKV = 2 * C::kTileBytes;
+  static constexpr int kOffX = kOffKV + kStages * C::kTileBytes;  // exchange: [2 streams][m, l][128]
+  static constexpr int kXBytes = 2 * 2 * 128 * 4;
+  static constexpr int kOffSeg = kOffX + kXBytes;
+  static constexpr int kOffScan = kOffSeg + kSegs * static_cast<int>(sizeof(PSeg));
+  static constexpr int kScanBytes = 96;
+  static constexpr int kOffBar = kOffScan + kScanBytes;
+  static constexpr int kBars = 16 + 2 * kSegs + 2 * kStages;
+  static constexpr int kSmemBytes = kOffBar + 8 * kBars + 16;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
 
+template <int D>
 struct PBars {
   uint32_t base;
-  int st;
+  static constexpr int kSt = PCfg<D>::kStages, kSg = PCfg<D>::kSegs;
   __device__ uint32_t q_full() const { return base; }
   __device__ uint32_t q_empty() const { return base + 8; }
   __device__ uint32_t s_full(int h) const { return base + 16 + 8 * h; }
@@ -71,11 +98,10 @@ struct PBars {
   // every product of a one-tile task is complete (o_full: of stream h of a two-tile task).
   // One barrier of its own, that both warpgroups wait for at every such task: none skips a phase.
   __device__ uint32_t t_full() const { return base + 120; }
-  __device__ uint32_t k_full(int s) const { return base + 128 + 8 * s; }
-  __device__ uint32_t k_empty(int s) const { return base + 128 + 8 * (st + s); }
-  __device__ uint32_t v_full(int s) const { return base + 128 + 8 * (2 * st + s); }
-  __device__ uint32_t v_empty(int s) const { return base + 128 + 8 * (3 * st + s); }
-  __device__ int count() const { return 16 + 4 * st; }
+  __device__ uint32_t seg_full(int s) const { return base + 128 + 8 * s; }
+  __device__ uint32_t seg_empty(int s) const { return base + 128 + 8 * (kSg + s); }
+  __device__ uint32_t full(int s) const { return base + 128 + 8 * (2 * kSg + s); }
+  __device__ uint32_t empty(int s) const { return base + 128 + 8 * (2 * kSg + kSt + s); }
 };
 
 // ------------------------------------------------------------------ work split
@@ -139,20 +165,10 @@ struct Split {
     return c >= ctas ? units : static_cast<int>(static_cast<int64_t>(c) * units / ctas);
   }
   __device__ __forceinline__ int owner(int u) const {  // the CTA whose range holds unit u
-    return static_cast<int>((static_cast<int64_t>(u + 1) * ctas - 1) / units);
+    const uint64_t x = static_cast<uint64_t>(u + 1) * static_cast<uint32_t>(ctas) - 1;
+    return (x >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(units))
+                          : static_cast<int>(x / static_cast<uint32_t>(units));
   }
-};
-
-// One CTA's share of one task.
-struct PSeg {
-  bool prefix;
-  int b, hk;       // b: own tasks only
-  int row0, rows;  // first row of the task and the rows that its key head has in all
-  int keys;        // keys of the task's key space
-  int k0, k1;      // tiles [k0, k1)
-  bool twin;       // one query tile, tiles in turn
-  bool whole;      // every tile of the task
-  bool first;      // holds the task's first tile
 };
 
 struct PSegIter {
@@ -180,9 +196,9 @@ struct PSegIter {
         tiles = prefix_tiles(p);
         const int per = tiles + kPagedTaskCost, t = u / per, n = prefix_tasks(p);
         a = t * per;
-        s.prefix = true;
+        s.flags = PSeg::kPrefix;
         s.hk = t / n;
-        s.b = 0;
+        s.b = s.len = s.ql = 0;
         s.row0 = (t - s.hk * n) * kPagedTaskRows;
         s.rows = p.B * p.Nq * p.G;
         s.keys = p.prefix_len;
@@ -194,8 +210,10 @@ struct PSegIter {
           ub = own_units(p, cur);
           if (b + 1 < p.B) nxt = seq_lens(p, b + 1);
         }
-        s.prefix = false;
+        s.flags = 0;
         s.b = b;
+        s.len = cur.len;
+        s.ql = cur.ql;
         s.hk = (u - sb) / ub;
         a = sb + s.hk * ub;
         int t = 0;
@@ -213,12 +231,12 @@ struct PSegIter {
       const int first = a + kPagedTaskCost, end = first + tiles;
       s.k0 = max(u, first) - first;
       s.k1 = min(hi, end) - first;
-      s.twin = s.rows - s.row0 <= kBM;
-      s.whole = s.k0 == 0 && s.k1 == tiles;
-      s.first = s.k0 == 0;
+      if (s.rows - s.row0 <= kBM) s.flags |= PSeg::kTwin;
+      if (s.k0 == 0) s.flags |= s.k1 == tiles ? PSeg::kWhole | PSeg::kFirst : PSeg::kFirst;
       u = min(hi, end);
       if (s.k1 > s.k0) return true;
     }
+    s.rows = 0;
     return false;
   }
 };
@@ -230,11 +248,22 @@ struct RowPos {
 __device__ __forceinline__ RowPos row_pos(const PagedParams& p, const PSeg& s, int r) {
   RowPos x;
   const int rs = p.Nq * p.G;
-  x.b = s.prefix ? r / rs : s.b;
-  const int i = s.prefix ? r - x.b * rs : r;
+  x.b = s.prefix() ? r / rs : s.b;
+  const int i = s.prefix() ? r - x.b * rs : r;
   x.n = i / p.G;
   x.g = i - x.n * p.G;
   return x;
+}
+
+// Stores 16 consecutive 32-bit TMEM columns of this thread's lane (completion: tmem_wait_st).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16};\n"
+      :
+      : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
 // ------------------------------------------------------------------ roles
@@ -249,8 +278,60 @@ __device__ __forceinline__ void tma_lane(uint32_t dst, const CUtensorMap* m, uin
       : "memory");
 }
 
+// Warp 3: the CTA's segments, one after the other, into the descriptor ring.
 template <int D>
-__device__ void paged_loader(const PagedParams& p, uint32_t sbase, const PBars& bars, PSegIter it, const Ctl& ctl) {
+__device__ void paged_scheduler(const PagedParams& p, uint8_t* smem, const PBars<D>& bars, int u0, int u1, int b0,
+                                int s0, const Ctl& ctl) {
+  using P = PCfg<D>;
+  PSegIter it(p, u0, u1, b0, s0);
+  RingPos<P::kSegs> r;
+  for (bool more = true; more;) {
+    PSeg s;
+    more = it.next(p, s);
+    if (!ctl_wait(bars.seg_empty(r.s), r.ph ^ 1u, ctl, -1, kRoleLoader)) return;
+    if ((threadIdx.x & 31) == 0) {
+      *reinterpret_cast<PSeg*>(smem + P::kOffSeg + r.s * sizeof(PSeg)) = s;
+      mbar_arrive(bars.seg_full(r.s));
+    }
+    __syncwarp();
+    r.advance();
+  }
+}
+
+// A role's view of the ring. take: the next descriptor (rows 0: no more).
+template <int D>
+struct SegReader {
+  RingPos<PCfg<D>::kSegs> r;
+  __device__ __forceinline__ bool take(PSeg& s, const uint8_t* smem, const PBars<D>& bars, const Ctl& ctl,
+                                       uint32_t role) {
+    if (!ctl_wait(bars.seg_full(r.s), r.ph, ctl, -1, role)) return false;
+    const int4* src = reinterpret_cast<const int4*>(smem + PCfg<D>::kOffSeg + r.s * sizeof(PSeg));
+    const int4 a = src[0], b = src[1], c = src[2];
+    s.rows = a.x;
+    s.row0 = a.y;
+    s.keys = a.z;
+    s.k0 = a.w;
+    s.k1 = b.x;
+    s.hk = b.y;
+    s.b = b.z;
+    s.len = b.w;
+    s.ql = c.x;
+    s.flags = c.y;
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bars.seg_empty(r.s));
+    r.advance();
+    return s.rows > 0;
+  }
+};
+
+// The ring's order of a segment's n tiles: the K tiles of the first `ahead`
+// (one, or two where the streams take tiles in turn), then V(i), K(i + ahead).
+// The last position is the last tile's V.
+__device__ __forceinline__ int tiles_ahead(const PSeg& s) { return s.twin() ? 2 : 1; }
+
+template <int D>
+__device__ void paged_loader(const PagedParams& p, uint8_t* smem, uint32_t sbase, const PBars<D>& bars,
+                             const Ctl& ctl) {
   using P = PCfg<D>;
   using C = Cfg<D>;
   const int lane = threadIdx.x & 31;
@@ -259,192 +340,202 @@ __device__ void paged_loader(const PagedParams& p, uint32_t sbase, const PBars& 
   const uint32_t box_bytes = static_cast<uint32_t>(box) * D * 2;
   const uint64_t pol_once = l2_policy_evict_first(), pol_reuse = l2_policy_evict_last();
   RingPos<P::kStages> r;
-  uint32_t armed_k = 0, par_k = 0, armed_v = 0, par_v = 0;
-  bool injected = false;
-  int nth = 0;
+  uint32_t armed = 0, par = 0;
+  int nth = 0;                                // K tiles issued (test hook)
+  SegReader<D> segs;
   PSeg s;
-  while (it.next(p, s)) {
-    const int32_t* tab = s.prefix ? p.prefix_table : p.table + s.b * p.table_sb;
-    const uint64_t pol = s.prefix ? pol_reuse : pol_once;
-    // this lane's page of tile k; lanes without keys to load get none
-    auto page_of = [&](int k, bool& mine) -> int {
+  while (segs.take(s, smem, bars, ctl, kRoleLoader)) {
+    const int32_t* tab = s.prefix() ? p.prefix_table : p.table + s.b * p.table_sb;
+    const uint64_t pol = s.prefix() ? pol_reuse : pol_once;
+    const int ahead = tiles_ahead(s);
+    // this lane's page of tile k, -1: none (a tile's pages behind the last key are not loaded)
+    auto page_of = [&](int k) -> int {
       const int key = k * kBN + lane * box;
-      mine = lane < per_tile && key < s.keys;
-      return mine ? tab[key >> p.page_shift] : 0;
+      return (k < s.k1 && lane < per_tile && key < s.keys) ? tab[key >> p.page_shift] : 0;
     };
-    bool mine, mine_next = false;
-    int id = page_of(s.k0, mine), id_next = 0;
-    for (int k = s.k0; k < s.k1; ++k, ++nth) {
-      if (k + 1 < s.k1) id_next = page_of(k + 1, mine_next);
-      const int slot = (k * kBN + lane * box) & (page - 1);
+    auto load = [&](const CUtensorMap* map, int k, int id, bool withhold) -> bool {
+      if (!ctl_wait(bars.empty(r.s), r.ph ^ 1u, ctl, k, kRoleLoader)) return false;
+      const bool mine = lane < per_tile && k * kBN + lane * box < s.keys;
       const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine))) * box_bytes;
-      if (!ctl_wait(bars.k_empty(r.s), r.ph ^ 1u, ctl, k, kRoleLoader)) goto drain;
-      if (p.inject && !injected && nth == 1) {
-        injected = true;  // withhold this K tile: the MMA issuer's wait must run out
-      } else {
-        mbar_expect_tx(bars.k_full(r.s), bytes);
+      if (!withhold) {
+        mbar_expect_tx(bars.full(r.s), bytes);
         __syncwarp();
-        if (mine)
+        if (mine) {
+          const uint32_t dst = sbase + P::kOffKV + r.s * C::kTileBytes + lane * box * C::kSwizzle;
+          const int slot = (k * kBN + lane * box) & (page - 1);
           for (int c = 0; c < C::kChunks; ++c)
-            tma_lane(sbase + P::kOffK + r.s * C::kTileBytes + c * C::kChunkBytes + lane * box * C::kSwizzle, &p.tm_k,
-                     bars.k_full(r.s), c * C::kBoxCols, slot, s.hk, id, pol);
-        armed_k |= 1u << r.s;
-        par_k = (par_k & ~(1u << r.s)) | (r.ph << r.s);
+            tma_lane(dst + c * C::kChunkBytes, map, bars.full(r.s), c * C::kBoxCols, slot, s.hk, id, pol);
+        }
+        __syncwarp();
+        armed |= 1u << r.s;
+        par = (par & ~(1u << r.s)) | (r.ph << r.s);
       }
-      __syncwarp();
-      if (!ctl_wait(bars.v_empty(r.s), r.ph ^ 1u, ctl, k, kRoleLoader)) goto drain;
-      mbar_expect_tx(bars.v_full(r.s), bytes);
-      __syncwarp();
-      if (mine)
-        for (int c = 0; c < C::kChunks; ++c)
-          tma_lane(sbase + P::kOffV + r.s * C::kTileBytes + c * C::kChunkBytes + lane * box * C::kSwizzle, &p.tm_v,
-                   bars.v_full(r.s), c * C::kBoxCols, slot, s.hk, id, pol);
-      armed_v |= 1u << r.s;
-      par_v = (par_v & ~(1u << r.s)) | (r.ph << r.s);
-      __syncwarp();
       r.advance();
-      id = id_next;
-      mine = mine_next;
+      return true;
+    };
+    // page numbers are fetched one step before they are used
+    int id_k = page_of(s.k0), id_n = page_of(s.k0 + 1), id_v = id_k;
+    for (int i = 0; i < ahead && s.k0 + i < s.k1; ++i) {
+      const bool withhold = p.inject && nth == 1;  // test hook: the MMA issuer's wait must run out
+      ++nth;
+      if (!load(&p.tm_k, s.k0 + i, i ? id_n : id_k, withhold)) goto drain;
+    }
+    for (int k = s.k0; k < s.k1; ++k) {
+      // id_v: pages of tile k; id_n: of tile k + 1
+      const int id_2 = page_of(k + 2);
+      if (!load(&p.tm_v, k, id_v, false)) goto drain;
+      const int kn = k + ahead;
+      if (kn < s.k1) {
+        const bool withhold = p.inject && nth == 1;
+        ++nth;
+        if (!load(&p.tm_k, kn, ahead == 2 ? id_2 : id_n, withhold)) goto drain;
+      }
+      id_v = id_n;
+      id_n = id_2;
     }
   }
 drain:
   __syncwarp();
   // The last copy armed on each barrier must have landed before the CTA exits.
-  for (int st = 0; st < P::kStages; ++st) {
-    if ((armed_k >> st) & 1u) ctl_wait(bars.k_full(st), (par_k >> st) & 1u, ctl, -1, kRoleLoader, false);
-    if ((armed_v >> st) & 1u) ctl_wait(bars.v_full(st), (par_v >> st) & 1u, ctl, -1, kRoleLoader, false);
-  }
+  for (int st = 0; st < P::kStages; ++st)
+    if ((armed >> st) & 1u) ctl_wait(bars.full(st), (par >> st) & 1u, ctl, -1, kRoleLoader, false);
 }
 
-// Warps 2 and 3: the task's query rows, each warp every other group of rows,
-// into the swizzled K-major layout that the MMA descriptor expects.
+// Warp 2: the task's query rows into the swizzled K-major layout that the MMA
+// descriptor expects, 16 bytes a copy, every copy of a task in flight at once.
+// Each lane works out the address of one row of 32; a row's d/8 lanes get it
+// by shuffles.
 template <int D>
-__device__ void paged_gather_q(const PagedParams& p, uint8_t* smem, const PBars& bars, PSegIter it, const Ctl& ctl) {
+__device__ void paged_gather_q(const PagedParams& p, uint8_t* smem, uint32_t sbase, const PBars<D>& bars,
+                               const Ctl& ctl) {
   using P = PCfg<D>;
   using C = Cfg<D>;
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row; rows per instruction
-  constexpr int kU = 4;
-  const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - 2;
-  const int c = lane % kLanes;                        // 16-byte chunk of the row
+  const int lane = threadIdx.x & 31;
+  const int c = lane % kLanes, sub = lane / kLanes;   // 16-byte chunk of the row; which row of the instruction's
   uint32_t ph = 0;
+  SegReader<D> segs;
   PSeg s;
-  while (it.next(p, s)) {
-    if (!ctl_wait(bars.q_empty(), ph ^ 1u, ctl, -1, kRoleLoader)) return;
-    ph ^= 1u;
+  while (segs.take(s, smem, bars, ctl, kRoleLoader)) {
     const int n = min(s.rows - s.row0, kPagedTaskRows);
-    for (int i0 = w * kRows * kU; i0 < n; i0 += 2 * kRows * kU) {
-      uint4 v[kU];
-#pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int i = i0 + u * kRows + lane / kLanes;
-        if (i < n) {
-          const RowPos x = row_pos(p, s, s.row0 + i);
-          v[u] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + x.b * p.q_sb +
-                                                 static_cast<int64_t>(s.hk * p.G + x.g) * p.q_sh + x.n * p.q_sn +
-                                                 c * 8);
-        }
+    bool waited = false;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const __nv_bfloat16* src = nullptr;
+      if (i0 + lane < n) {
+        const RowPos x = row_pos(p, s, s.row0 + i0 + lane);
+        src = static_cast<const __nv_bfloat16*>(p.q) + x.b * p.q_sb + static_cast<int64_t>(s.hk * p.G + x.g) * p.q_sh +
+              x.n * p.q_sn;
+      }
+      if (!waited) {
+        if (!ctl_wait(bars.q_empty(), ph ^ 1u, ctl, -1, kRoleLoader)) return;
+        ph ^= 1u;
+        waited = true;
       }
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int i = i0 + u * kRows + lane / kLanes;
-        if (i < n) {
-          const int row = i % kBM;
-          const int swz = C::kSwizzle == 128 ? ((c & 7) ^ (row & 7)) : (c ^ ((row >> 1) & 3));
-          const int off = P::kOffQ + (i / kBM) * C::kTileBytes + (C::kSwizzle == 128 ? (c >> 3) * C::kChunkBytes : 0) +
-                          row * C::kSwizzle + swz * 16;
-          *reinterpret_cast<uint4*>(smem + off) = v[u];
-        }
+      for (int j = 0; j < 32 / kRows; ++j) {
+        const int i = j * kRows + sub;  // row of the 32
+        const __nv_bfloat16* from = reinterpret_cast<const __nv_bfloat16*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
+        const int row = (i0 + i) % kBM;
+        const int swz = C::kSwizzle == 128 ? ((c & 7) ^ (row & 7)) : (c ^ ((row >> 1) & 3));
+        const uint32_t dst = sbase + P::kOffQ + ((i0 + i) / kBM) * C::kTileBytes +
+                             (C::kSwizzle == 128 ? (c >> 3) * C::kChunkBytes : 0) + row * C::kSwizzle + swz * 16;
+        if (from != nullptr)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from + c * 8) : "memory");
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
     if (lane == 0) mbar_arrive(bars.q_full());
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 template <int D>
-__device__ void paged_mma(const PagedParams& p, uint32_t sbase, const PBars& bars, uint32_t tmem, PSegIter it,
+__device__ void paged_mma(const PagedParams& p, uint8_t* smem, uint32_t sbase, const PBars<D>& bars, uint32_t tmem,
                           const Ctl& ctl) {
   using P = PCfg<D>;
   using C = Cfg<D>;
   const uint64_t q0 = smem_desc(sbase + P::kOffQ, 16, 8 * C::kSwizzle, C::kLayout);
-  const uint64_t q1 = smem_desc(sbase + P::kOffQ + C::kTileBytes, 16, 8 * C::kSwizzle, C::kLayout);
-  const uint64_t k_base = smem_desc(sbase + P::kOffK, 16, 8 * C::kSwizzle, C::kLayout);
-  const uint64_t v_base = smem_desc(sbase + P::kOffV, C::kChunkBytes, 8 * C::kSwizzle, C::kLayout);
+  const uint64_t k_base = smem_desc(sbase + P::kOffKV, 16, 8 * C::kSwizzle, C::kLayout);
+  const uint64_t v_base = smem_desc(sbase + P::kOffKV, C::kChunkBytes, 8 * C::kSwizzle, C::kLayout);
   constexpr uint64_t kStep = static_cast<uint64_t>(C::kTileBytes >> 4);
   uint32_t q_ph = 0, p_par = 0, o_par = 0;  // bit h of p_par, o_par: parity of stream h's next phase
-  RingPos<P::kStages> kr, vr;
+  RingPos<P::kStages> r;
+  SegReader<D> segs;
   PSeg s;
-  while (it.next(p, s)) {
+  while (segs.take(s, smem, bars, ctl, kRoleMma)) {
     if (!ctl_wait(bars.q_full(), q_ph, ctl, -1, kRoleMma)) goto drain;
     q_ph ^= 1u;
     tc_fence_after();
     uint32_t o_ready = 0;
-    const bool twin = s.twin;
-    // S of tile k: both streams' (two query tiles), or its own stream's
+    const bool twin = s.twin();
+    const uint64_t q1 = twin ? q0 : q0 + kStep;
     auto scores = [&](int h) {
-      issue_s<D>(tmem + (h ? C::tm_s(1) : C::tm_s(0)), (h && !twin) ? q1 : q0, k_base + kr.s * kStep);
+      issue_s<D>(tmem + static_cast<uint32_t>(h) * C::tm_s(1), h ? q1 : q0, k_base + r.s * kStep);
       mma_commit(bars.s_full(h));
     };
-    auto take_k = [&](int k) -> bool {
-      if (!ctl_wait(bars.k_full(kr.s), kr.ph, ctl, k, kRoleMma)) return false;
+    auto take = [&](int k) -> bool {
+      if (!ctl_wait(bars.full(r.s), r.ph, ctl, k, kRoleMma)) return false;
       tc_fence_after();
       return true;
     };
-    auto give_k = [&]() {
-      mma_commit(bars.k_empty(kr.s));
-      kr.advance();
+    auto give = [&]() {
+      mma_commit(bars.empty(r.s));
+      r.advance();
     };
-    auto product = [&](int k, int h) -> bool {
+    auto product = [&](int k, int h, uint64_t v) -> bool {
       if (!((o_ready >> h) & 1u) && !ctl_wait(bars.o_empty(h), ((o_par >> h) & 1u) ^ 1u, ctl, k, kRoleMma)) return false;
       const uint32_t par = (p_par >> h) & 1u;
       for (int part = 0; part < 2; ++part) {
         if (!ctl_wait(bars.p_full(h, part), par, ctl, k, kRoleMma)) return false;
         tc_fence_after();
-        issue_pv<D>(tmem + (h ? C::tm_o(1) : C::tm_o(0)), tmem + (h ? C::tm_p(1) : C::tm_p(0)), v_base + vr.s * kStep,
+        issue_pv<D>(tmem + C::tm_o(0) + static_cast<uint32_t>(h) * D, tmem + static_cast<uint32_t>(h) * C::tm_p(1), v,
                     part, (((o_ready >> h) & 1u) != 0u || part > 0) ? 1u : 0u);
       }
       p_par ^= 1u << h;
       o_ready |= 1u << h;
       return true;
     };
-    const int ahead = twin ? 2 : 1;  // tiles whose S goes before the first P V
-    for (int k = s.k0; k < min(s.k0 + ahead, s.k1); ++k) {
-      if (!take_k(k)) goto drain;
-      if (twin) {
-        scores((k - s.k0) & 1);
-      } else {
-        scores(0);
-        scores(1);
-      }
-      give_k();
+    const int ahead = tiles_ahead(s);
+    for (int i = 0; i < ahead && s.k0 + i < s.k1; ++i) {
+      if (!take(s.k0 + i)) goto drain;
+      scores(i);
+      if (!twin) scores(1);
+      give();
     }
     if (s.k0 + ahead >= s.k1) mma_commit(bars.q_empty());
     for (int k = s.k0; k < s.k1; ++k) {
       const int kn = k + ahead;
-      if (!ctl_wait(bars.v_full(vr.s), vr.ph, ctl, k, kRoleMma)) goto drain;
-      tc_fence_after();
+      const bool more = kn < s.k1;
+      if (!take(k)) goto drain;
+      const uint64_t v = v_base + r.s * kStep;
+      const uint32_t v_empty = bars.empty(r.s);
+      r.advance();
       if (twin) {
         const int h = (k - s.k0) & 1;
-        if (!product(k, h)) goto drain;
-        if (kn < s.k1) {
-          if (!take_k(kn)) goto drain;
+        if (!product(k, h, v)) goto drain;
+        mma_commit(v_empty);
+        if (more) {
+          if (!take(kn)) goto drain;
           scores(h);
-          give_k();
+          give();
         }
       } else {
-        for (int h = 0; h < 2; ++h) {
-          if (!product(k, h)) goto drain;
-          if (kn < s.k1) {
-            if (h == 0 && !take_k(kn)) goto drain;
-            scores(h);
-          }
+        if (!product(k, 0, v)) goto drain;
+        if (more) {
+          if (!take(kn)) goto drain;
+          scores(0);
         }
-        if (kn < s.k1) give_k();
+        if (!product(k, 1, v)) goto drain;
+        mma_commit(v_empty);
+        if (more) {
+          scores(1);
+          give();
+        }
       }
-      mma_commit(bars.v_empty(vr.s));
-      vr.advance();
-      if (kn < s.k1 && kn + 1 == s.k1) mma_commit(bars.q_empty());  // the task's last S is issued
+      if (more && kn + 1 == s.k1) mma_commit(bars.q_empty());  // the task's last S is issued
     }
     for (int h = 0; h < 2; ++h) {
       if (!((o_ready >> h) & 1u)) {  // a stream without a tile keeps its phases in step
@@ -503,7 +594,7 @@ struct RowSink {
 };
 
 template <int D>
-__device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars& bars, uint32_t tmem, PSegIter it,
+__device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D>& bars, uint32_t tmem,
                               const Ctl& ctl) {
   using P = PCfg<D>;
   using C = Cfg<D>;
@@ -515,53 +606,82 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars& 
   float* xch = reinterpret_cast<float*>(smem + P::kOffX);
   const float c = p.c;
   uint32_t s_par = 0, o_par = 0, t_par = 0;
-  uint32_t n_tiles = 0;  // tiles that the CTA has taken: the V ring's position
+  uint32_t ring = 0;  // K and V tiles that the CTA took before this segment: the ring's position
+  SegReader<D> segs;
   PSeg s;
-  while (it.next(p, s)) {
-    const int r = s.row0 + (s.twin ? 0 : h * kBM) + row;
-    int seen = 0;  // keys of this task that the row sees
-    RowPos x{0, 0, 0};
+  while (segs.take(s, smem, bars, ctl, kRoleSoftmax)) {
+    const bool twin = s.twin();
+    const int r = s.row0 + (twin ? 0 : h * kBM) + row;
     const bool real = r < s.rows;
+    // Keys of this task that the row sees. Lanes without a row see them all:
+    // what they compute is never read, and they ask for no masking.
+    int seen = s.keys;
+    RowPos x{0, 0, 0};
     if (real) {
       x = row_pos(p, s, r);
-      const int all = keys_seen(p, seq_lens(p, x.b), x.n);
-      seen = s.prefix ? min(all, p.prefix_len) : max(all - p.prefix_len, 0);
+      SeqLens sl;
+      if (s.prefix()) {
+        sl = seq_lens(p, x.b);
+      } else {
+        sl.len = s.len;
+        sl.ql = s.ql;
+      }
+      const int all = keys_seen(p, sl, x.n);
+      seen = s.prefix() ? min(all, p.prefix_len) : max(all - p.prefix_len, 0);
     }
-    const bool any = __any_sync(0xffffffffu, seen > 0);
+    const bool any = __any_sync(0xffffffffu, real && seen > 0);
+    ring += 2u * static_cast<uint32_t>(s.k1 - s.k0);
     float m_ref = -CUDART_INF_F, l = 0.f;
     bool first = true;
-    for (int k = s.k0 + (s.twin ? h : 0); k < s.k1; k += s.twin ? 2 : 1) {
+    for (int k = s.k0 + (twin ? h : 0); k < s.k1; k += twin ? 2 : 1) {
       const int base = k * kBN;
       if (!warp_wait(bars.s_full(h), s_par, ctl, k)) return;
       s_par ^= 1u;
       tc_fence_after();
       if (base + kBN > s.keys) {
-        // The task's last tile: V rows behind its end become zero. (After
-        // s_full: this tile's S went out behind the products of the tiles that
-        // held its V stage before, so v_full is in this tile's phase or past
-        // it, and the parity below cannot match an older one.)
-        const uint32_t at = n_tiles + static_cast<uint32_t>(k - s.k0);
+        // The task's last tile: V rows behind its end become zero. Its V is the
+        // segment's last in the ring. (After s_full: this tile's S went out
+        // behind whatever held the stage before, so `full` is in this tile's
+        // phase or past it, and the parity below cannot match an older one.)
+        const uint32_t at = ring - 1u;
         const int st = static_cast<int>(at % P::kStages);
-        if (!warp_wait(bars.v_full(st), (at / P::kStages) & 1u, ctl, k)) return;
+        if (!warp_wait(bars.full(st), (at / P::kStages) & 1u, ctl, k)) return;
         const int z0 = max(s.keys - base, quarter * 32), z1 = quarter * 32 + 32;
         for (int ch = 0; ch < C::kChunks; ++ch) {
-          uint8_t* v = smem + P::kOffV + st * C::kTileBytes + ch * C::kChunkBytes;
+          uint8_t* v = smem + P::kOffKV + st * C::kTileBytes + ch * C::kChunkBytes;
           for (int i = z0 * C::kSwizzle + lane * 16; i < z1 * C::kSwizzle; i += 512)
             *reinterpret_cast<uint4*>(v + i) = make_uint4(0, 0, 0, 0);
         }
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
       }
       if (any) {
-        uint32_t sr[128];
-        tmem_ld128(t_s, sr);
+        // Two passes over S in pieces of 32 keys, read from TMEM twice: the
+        // loops stay rolled and the code small, which counts where a launch
+        // has only a few tiles an SM (one pass over 128 registers took ~5000
+        // cycles for the first tile, most of them instruction fetches).
         const int lim = seen - base;
-        if (__any_sync(0xffffffffu, lim < kBN)) {
-          const uint32_t neg_inf = __float_as_uint(-CUDART_INF_F);
+        const bool cut = __any_sync(0xffffffffu, lim < kBN);
+        float mx = -CUDART_INF_F;
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          uint32_t sr[32];
+          tmem_ld32(t_s + 32 * j, sr);
+          if (cut) {
+            const int lj = lim - 32 * j;
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= lim) sr[i] = neg_inf;
+            for (int i = 0; i < 32; ++i)
+              if (i >= lj) sr[i] = __float_as_uint(-CUDART_INF_F);
+          }
+          float m4[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 4]));
+#pragma unroll
+          for (int i = 8; i < 32; i += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], __uint_as_float(sr[i + q]), __uint_as_float(sr[i + q + 4]));
+          mx = fmax3(mx, fmax3(m4[0], m4[1], m4[2]), m4[3]);
         }
-        const float mx = row_max128(sr);
         const float m_tile = (mx == -CUDART_INF_F) ? -CUDART_INF_F : mx * c;
         const bool grow = m_tile > m_ref + kRescaleLog2;
         float alpha = 1.f;
@@ -573,33 +693,36 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars& 
         if (__any_sync(0xffffffffu, grow && !first)) rescale_o<D>(t_o, alpha);
         const float neg_m = (m_ref == -CUDART_INF_F) ? 0.f : -m_ref;
         const float2 c2 = make_float2(c, c), nm2 = make_float2(neg_m, neg_m);
-        float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // P of keys [32 j, 32 j + 32) goes over columns [16 j, 16 j + 16) of S,
+        // which pass 2 has read by then
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          uint32_t sr[32], pk[16];
+          tmem_ld32(t_s + 32 * j, sr);
+          if (cut) {
+            const int lj = lim - 32 * j;
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          uint32_t pk[32];
+            for (int i = 0; i < 32; ++i)
+              if (i >= lj) sr[i] = __float_as_uint(-CUDART_INF_F);
+          }
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int e = 64 * part + 2 * i;
+          for (int i = 0; i < 16; ++i) {
             const float2 y =
-                __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, nm2);
+                __ffma2_rn(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nm2);
             const float2 pe = make_float2(ex2(y.x), ex2(y.y));
-            sum4[i & 3] = __fadd2_rn(sum4[i & 3], pe);
+            sum2[i & 1] = __fadd2_rn(sum2[i & 1], pe);
             pk[i] = pack_bf16(pe.x, pe.y);
           }
-          if (part == 1) {
+          tmem_st16(t_p + 16 * j, pk);
+          if (j & 1) {  // 64 keys of P are announced at a time
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.p_full(h, 0));
+            if (lane == 0) mbar_arrive(bars.p_full(h, j >> 1));
           }
-          tmem_st32(t_p + 32 * part, pk);
         }
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bars.p_full(h, 1));
-        const float2 sa = __fadd2_rn(sum4[0], sum4[1]), sb = __fadd2_rn(sum4[2], sum4[3]);
-        l += (sa.x + sa.y) + (sb.x + sb.y);
+        l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
       } else {
         // no row of this warp sees a key of the task: its P and O are never read
         tc_fence_before();
@@ -611,18 +734,18 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars& 
       }
       first = false;
     }
-    n_tiles += static_cast<uint32_t>(s.k1 - s.k0);
 
     // the end of the segment: O of this row, to its part, its buffer or the result
     float m = m_ref, w0 = 1.f, w1 = 0.f;
-    if (s.twin) {
-      // Join the streams: each warpgroup takes half of the columns. The maxima
-      // and sums go through shared memory, two buffers in turn. Each side
-      // arrives after t_full, which the other side's warps are all needed for,
-      // so neither runs a whole phase ahead of a warp that has yet to look.
+    if (twin) {
+      // Join the streams: each warpgroup takes half of the columns; the maxima
+      // and sums go through shared memory. Both write after t_full, whose
+      // products waited for o_empty, that is for every warp's reads of the task
+      // before; and neither side can run a whole phase ahead of a warp that has
+      // yet to look, since t_full needs them all.
       if (!warp_wait(bars.t_full(), t_par, ctl, -1)) return;
-      float* mine = xch + ((t_par * 2 + h) * 2) * kBM;
-      const float* other = xch + ((t_par * 2 + (h ^ 1)) * 2) * kBM;
+      float* mine = xch + h * 2 * kBM;
+      const float* other = xch + (h ^ 1) * 2 * kBM;
       mine[row] = m_ref;
       mine[kBM + row] = l;
       __syncwarp();
@@ -643,10 +766,10 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars& 
     tc_fence_after();
     RowSink<D> sink;
     const bool none = m == -CUDART_INF_F;
-    const bool lead = !s.twin || h == 0;  // writes the row's m and l
+    const bool lead = !twin || h == 0;  // writes the row's m and l
     if (real) {
-      if (!s.whole) {
-        float* base = paged_slot<D>(p, blockIdx.x, s.first, s.twin ? 0 : h, quarter);
+      if (!s.whole()) {
+        float* base = paged_slot<D>(p, blockIdx.x, s.first(), twin ? 0 : h, quarter);
         if (!none) sink.part = base + 4 * lane;
         if (lead) {
           base[32 * D + lane] = m;
@@ -654,7 +777,7 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars& 
         }
       } else if (p.prefix_len > 0) {
         const int64_t rows = static_cast<int64_t>(p.B) * p.Nq * p.Hq;
-        const int64_t i = (s.prefix ? 0 : rows) + row_index(p, x.b, s.hk, x.n, x.g);
+        const int64_t i = (s.prefix() ? 0 : rows) + row_index(p, x.b, s.hk, x.n, x.g);
         if (!none) sink.buf = p.rows_o + i * D;
         if (lead) p.rows_ml[i] = make_float2(m, l);
       } else {
@@ -667,14 +790,14 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars& 
       }
     }
     const int n_ch = D / 32;
-    const int ch0 = s.twin ? (h * n_ch + 1) / 2 : 0, ch1 = s.twin ? (h ? n_ch : (n_ch + 1) / 2) : n_ch;
+    const int ch0 = twin ? (h * n_ch + 1) / 2 : 0, ch1 = twin ? (h ? n_ch : (n_ch + 1) / 2) : n_ch;
     const bool rows_here = __any_sync(0xffffffffu, real);
     for (int ch = ch0; ch < ch1; ++ch) {
       if (!rows_here) break;
       __syncwarp();
       uint32_t a[32];
       float y[32];
-      if (s.twin) {
+      if (twin) {
         uint32_t b[32];
         tmem_ld32(lane_base + C::tm_o(0) + ch * 32, a);
         tmem_ld32(lane_base + C::tm_o(1) + ch * 32, b);
@@ -694,7 +817,7 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars& 
     tc_fence_before();
     __syncwarp();
     // both warpgroups' arrivals free a stream's O: two of a warp when only its own reads it
-    if (s.twin) {
+    if (twin) {
       if (lane < 2) mbar_arrive(bars.o_empty(lane));
     } else if (lane < 2) {
       mbar_arrive(bars.o_empty(h));
@@ -708,19 +831,23 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars& 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constant__ PagedParams p) {
   using P = PCfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  const uint32_t raw = smem_u32(smem_raw);
-  const uint32_t sbase = (raw + 1023u) & ~1023u;
-  uint8_t* smem = smem_raw + (sbase - raw);
+  // The swizzled tiles need 1024-byte alignment. Without static shared memory
+  // the dynamic part starts at such an address; the five stages of d = 128
+  // leave no room to align by hand, so a CTA that finds it otherwise reports it.
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const uint32_t sbase = smem_u32(smem);
+  if ((sbase & 1023u) != 0u) {
+    if (threadIdx.x == 0) atomicCAS(g_paged_status, 0u, 255u);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  PBars bars{sbase + P::kOffBar, P::kStages};
-  static_assert(8 * (16 + 4 * P::kStages) + 8 <= P::kBarBytes, "barrier area");
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kOffBar + 8 * bars.count());
+  const PBars<D> bars{sbase + P::kOffBar};
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kOffBar + 8 * P::kBars);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  int32_t* scan = reinterpret_cast<int32_t*>(smem + P::kOffScan);  // [0, 12) warps' sums, [16..19] results
+  int32_t* scan = reinterpret_cast<int32_t*>(smem + P::kOffScan);  // [0, 12) warps' sums, [16..17] results
 
   if (threadIdx.x == 0) {
-    mbar_init(bars.q_full(), 2);
+    mbar_init(bars.q_full(), 1);
     mbar_init(bars.q_empty(), 1);
     for (int h = 0; h < 2; ++h) {
       mbar_init(bars.s_full(h), 1);
@@ -732,11 +859,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     }
     mbar_init(bars.done(), 1);
     mbar_init(bars.t_full(), 1);
+    for (int s = 0; s < P::kSegs; ++s) {
+      mbar_init(bars.seg_full(s), 1);
+      mbar_init(bars.seg_empty(s), kWarps - 1);  // every warp but the scheduler
+    }
     for (int s = 0; s < P::kStages; ++s) {
-      mbar_init(bars.k_full(s), 1);
-      mbar_init(bars.k_empty(s), 1);
-      mbar_init(bars.v_full(s), 1);
-      mbar_init(bars.v_empty(s), 1);
+      mbar_init(bars.full(s), 1);
+      mbar_init(bars.empty(s), 1);
     }
     *abort_flag = 0u;
     fence_barrier_init();
@@ -772,20 +901,28 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     }
     return total;
   };
-  int mine = 0, below;
-  for (int b = threadIdx.x; b < p.B; b += kThreads) mine += p.Hk * own_units(p, seq_lens(p, b));
-  const int units = up + block_sum(mine, below);
+  // (up to 384 sequences: one look at each, kept in a register)
+  const int v0 = threadIdx.x < p.B ? p.Hk * own_units(p, seq_lens(p, threadIdx.x)) : 0;
+  int below;
+  int own = block_sum(v0, below);
+  for (int b0 = kThreads; b0 < p.B; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int unused;
+    own += block_sum(b < p.B ? p.Hk * own_units(p, seq_lens(p, b)) : 0, unused);
+  }
+  const int units = up + own;
   const Split split(units, gridDim.x);
   const int u0 = split.lo(blockIdx.x), u1 = split.lo(blockIdx.x + 1);
-  if (threadIdx.x == 0) {
-    scan[16] = u0 < up ? 0 : p.B;  // first sequence to look at
-    scan[17] = u0 < up ? up : units;
+  if (threadIdx.x == 0 && u0 < up) {
+    scan[16] = 0;  // first sequence to look at, and its first unit
+    scan[17] = up;
   }
   int run = up;
   for (int b0 = 0; b0 < p.B; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    const int v = b < p.B ? p.Hk * own_units(p, seq_lens(p, b)) : 0;
-    const int total = block_sum(v, below);
+    int v = v0, total = 0;
+    if (b0 > 0) v = b < p.B ? p.Hk * own_units(p, seq_lens(p, b)) : 0;
+    if (p.B > kThreads) total = block_sum(v, below);
     const int at = run + below;
     if (b < p.B) {
       if (blockIdx.x == 0) p.starts[b] = at;
@@ -802,21 +939,23 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Ctl ctl{abort_flag, g_paged_status, p.timeout_ns};
-  const PSegIter it(p, u0, u1, scan[16], scan[17]);
 
   if (warp < 4) {
     set_max_regs_dec<kRegsControl>();
     if (warp == 0) {
-      paged_loader<D>(p, sbase, bars, it, ctl);
+      paged_loader<D>(p, smem, sbase, bars, ctl);
     } else if (warp == 1) {
-      paged_mma<D>(p, sbase, bars, tmem, it, ctl);
+      paged_mma<D>(p, smem, sbase, bars, tmem, ctl);
+    } else if (warp == 2) {
+      paged_gather_q<D>(p, smem, sbase, bars, ctl);
     } else {
-      paged_gather_q<D>(p, smem, bars, it, ctl);
+      // a CTA without units (u0 == u1) has no sequence to start from and reads none
+      paged_scheduler<D>(p, smem, bars, u0, u1, u0 < u1 ? scan[16] : 0, u0 < u1 ? scan[17] : 0, ctl);
     }
     __syncwarp();
   } else {
     set_max_regs_inc<kRegsSoftmax>();
-    paged_softmax<D>(p, smem, bars, tmem, it, ctl);
+    paged_softmax<D>(p, smem, bars, tmem, ctl);
   }
   tc_fence_before();
   __syncthreads();
@@ -881,59 +1020,75 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
   const int parts = pre.parts + own.parts;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -CUDART_INF_F, L = 0.f;
+  constexpr int kBatch = 8;  // parts whose loads are in flight together
   for (int base = 0; base < parts; base += 32) {
-    const int i = base + lane;
-    float m = -CUDART_INF_F, l = 0.f;
-    const float* src = nullptr;  // float4 j of the row at src + j * step
-    int step = 0;
+    const int i = base + lane, count = min(32, parts - base);
+    const float* src = p.rows_o;  // float4 j of the row at src + j * step
+    const float* pm = nullptr;
+    int step = 4;
+    bool pair = false;            // m and l side by side
     if (i < parts) {
       const bool is_pre = i < pre.parts;
       const Span s = is_pre ? pre : own;
       const int k = is_pre ? i : i - pre.parts;
       if (s.parts == 1) {
         const int64_t at = (is_pre ? 0 : rows) + row;
-        const float2 ml = p.rows_ml[at];
-        m = ml.x;
-        l = ml.y;
+        pm = reinterpret_cast<const float*>(p.rows_ml + at);
+        pair = true;
         src = p.rows_o + at * D;
-        step = 4;
       } else {
         const int quarter = (s.in_task % kBM) / 32, in_q = s.in_task % 32;
         const float* slot = paged_slot<D>(p, s.c0 + k, k == 0, s.in_task / kBM, quarter);
-        m = slot[32 * D + in_q];
-        l = slot[32 * D + 32 + in_q];
+        pm = slot + 32 * D + in_q;
         src = slot + 4 * in_q;
         step = 128;
       }
     }
+    float m = -CUDART_INF_F, l = 0.f;
+    if (pm != nullptr) {
+      m = pm[0];
+      l = pm[pair ? 1 : 32];
+    }
+    // the first batch's data is asked for beside the maxima, before they are known
+    float4 v[kBatch];
+    auto fetch = [&](int j0) {
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int j = min(j0 + u, count - 1);
+        const float* sj = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j));
+        const int st = __shfl_sync(0xffffffffu, step, j);
+        if (j0 + u < count && lane < D / 4) v[u] = *reinterpret_cast<const float4*>(sj + lane * st);
+      }
+    };
+    fetch(0);
     float mx = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float M1 = fmaxf(M, mx);
-    if (M1 == -CUDART_INF_F) continue;
     const float old = M == -CUDART_INF_F ? 0.f : ex2(M - M1);
     const float w = m == -CUDART_INF_F ? 0.f : ex2(m - M1);
     acc.x *= old;
     acc.y *= old;
     acc.z *= old;
     acc.w *= old;
-    float lw = l * w;
+    float lw = w > 0.f ? l * w : 0.f;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
     L = fmaf(L, old, lw);
     M = M1;
-    const int count = min(32, parts - base);
-    for (int j = 0; j < count; ++j) {
-      const float wj = __shfl_sync(0xffffffffu, w, j);
-      const float* sj = reinterpret_cast<const float*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j));
-      const int st = __shfl_sync(0xffffffffu, step, j);
-      if (wj > 0.f && lane < D / 4) {
-        const float4 v = *reinterpret_cast<const float4*>(sj + lane * st);
-        acc.x = fmaf(v.x, wj, acc.x);
-        acc.y = fmaf(v.y, wj, acc.y);
-        acc.z = fmaf(v.z, wj, acc.z);
-        acc.w = fmaf(v.w, wj, acc.w);
+    for (int j0 = 0; j0 < count; j0 += kBatch) {
+      if (j0 > 0) fetch(j0);
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const float wj = __shfl_sync(0xffffffffu, w, min(j0 + u, 31));
+        // a part that saw no key for this row never wrote its O: left out, not weighted by zero
+        if (j0 + u < count && wj > 0.f) {
+          acc.x = fmaf(v[u].x, wj, acc.x);
+          acc.y = fmaf(v[u].y, wj, acc.y);
+          acc.z = fmaf(v[u].z, wj, acc.z);
+          acc.w = fmaf(v[u].w, wj, acc.w);
+        }
       }
     }
   }
@@ -951,7 +1106,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
 
 template <int D>
 cudaError_t launch_paged_dim(const PagedParams& p, int grid, cudaStream_t s) {
-  constexpr int smem = PCfg<D>::kSmemBytes > kMinSmemBytes ? PCfg<D>::kSmemBytes : kMinSmemBytes;
+  constexpr int smem = PCfg<D>::kSmemBytes > kMinSmemBytes ? PCfg<D>::kSmemBytes : kMinSmemBytes;  // one CTA an SM
   cudaError_t e = cudaFuncSetAttribute(paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
