@@ -128,33 +128,20 @@ __device__ __forceinline__ int keys_seen(const PagedParams& p, SeqLens s, int n)
 
 // K/V tiles of a sequence's own keys that task t (rows [256 t, 256 t + 256)) needs.
 __device__ __forceinline__ int own_tiles(const PagedParams& p, SeqLens s, int t) {
-  const int first = t * kPagedTaskRows / p.G;
+  const int first = p.by_g.div(t * kPagedTaskRows);
   if (first >= s.ql) return 0;
-  const int last = min((min((t + 1) * kPagedTaskRows, p.Nq * p.G) - 1) / p.G, s.ql - 1);
+  const int last = min(p.by_g.div(min((t + 1) * kPagedTaskRows, p.Nq * p.G) - 1), s.ql - 1);
   return (clampi(keys_seen(p, s, last) - p.prefix_len, 0, s.len) + kBN - 1) / kBN;
-}
-
-__device__ __forceinline__ int own_tasks(const PagedParams& p) {
-  return (p.Nq * p.G + kPagedTaskRows - 1) / kPagedTaskRows;
 }
 
 // Units of one sequence's tasks for one key head.
 __device__ __forceinline__ int own_units(const PagedParams& p, SeqLens s) {
-  const int n = own_tasks(p);
   int u = 0;
-  for (int t = 0; t < n; ++t) {
+  for (int t = 0; t < p.own_tasks; ++t) {
     const int tiles = own_tiles(p, s, t);
     u += tiles + (tiles > 0 ? kPagedTaskCost : 0);
   }
   return u;
-}
-
-__device__ __forceinline__ int prefix_tiles(const PagedParams& p) { return (p.prefix_len + kBN - 1) / kBN; }
-__device__ __forceinline__ int prefix_tasks(const PagedParams& p) {  // per key head
-  return p.prefix_len > 0 ? (p.B * p.Nq * p.G + kPagedTaskRows - 1) / kPagedTaskRows : 0;
-}
-__device__ __forceinline__ int prefix_units(const PagedParams& p) {
-  return p.Hk * prefix_tasks(p) * (prefix_tiles(p) + kPagedTaskCost);
 }
 
 // The split of U units over the CTAs that get some: CTA c starts at c U / n.
@@ -180,7 +167,7 @@ struct PSegIter {
 
   // u0: the CTA's first unit; b0, s0: the sequence that holds it (or the next) and its first unit.
   __device__ __forceinline__ PSegIter(const PagedParams& p, int u0, int u1, int b0, int s0)
-      : u(u0), hi(u1), up(prefix_units(p)), b(b0), sb(s0), ub(0) {
+      : u(u0), hi(u1), up(p.prefix_units), b(b0), sb(s0), ub(0) {
     cur.len = cur.ql = 0;
     nxt = cur;
     if (u < hi && b < p.B) {
@@ -193,13 +180,13 @@ struct PSegIter {
     while (u < hi) {
       int a, tiles;
       if (u < up) {
-        tiles = prefix_tiles(p);
-        const int per = tiles + kPagedTaskCost, t = u / per, n = prefix_tasks(p);
-        a = t * per;
+        tiles = p.prefix_tiles;
+        const int t = p.by_prefix_units.div(u);
+        a = t * (tiles + kPagedTaskCost);
         s.flags = PSeg::kPrefix;
-        s.hk = t / n;
+        s.hk = p.by_prefix_tasks.div(t);
         s.b = s.len = s.ql = 0;
-        s.row0 = (t - s.hk * n) * kPagedTaskRows;
+        s.row0 = (t - s.hk * p.prefix_tasks) * kPagedTaskRows;
         s.rows = p.B * p.Nq * p.G;
         s.keys = p.prefix_len;
       } else {
@@ -247,10 +234,9 @@ struct RowPos {
 };
 __device__ __forceinline__ RowPos row_pos(const PagedParams& p, const PSeg& s, int r) {
   RowPos x;
-  const int rs = p.Nq * p.G;
-  x.b = s.prefix() ? r / rs : s.b;
-  const int i = s.prefix() ? r - x.b * rs : r;
-  x.n = i / p.G;
+  x.b = s.prefix() ? p.by_rows.div(r) : s.b;
+  const int i = s.prefix() ? r - x.b * p.Nq * p.G : r;
+  x.n = p.by_g.div(i);
   x.g = i - x.n * p.G;
   return x;
 }
@@ -302,9 +288,14 @@ __device__ void paged_scheduler(const PagedParams& p, uint8_t* smem, const PBars
 template <int D>
 struct SegReader {
   RingPos<PCfg<D>::kSegs> r;
-  __device__ __forceinline__ bool take(PSeg& s, const uint8_t* smem, const PBars<D>& bars, const Ctl& ctl,
-                                       uint32_t role) {
-    if (!ctl_wait(bars.seg_full(r.s), r.ph, ctl, -1, role)) return false;
+  // ROLE softmax waits inline: a call in these warps' loop costs them their registers (2700 bytes of spills).
+  template <uint32_t ROLE>
+  __device__ __forceinline__ bool take(PSeg& s, const uint8_t* smem, const PBars<D>& bars, const Ctl& ctl) {
+    if (ROLE == kRoleSoftmax) {
+      if (!warp_wait(bars.seg_full(r.s), r.ph, ctl, -1)) return false;
+    } else {
+      if (!ctl_wait(bars.seg_full(r.s), r.ph, ctl, -1, ROLE)) return false;
+    }
     const int4* src = reinterpret_cast<const int4*>(smem + PCfg<D>::kOffSeg + r.s * sizeof(PSeg));
     const int4 a = src[0], b = src[1], c = src[2];
     s.rows = a.x;
@@ -344,7 +335,7 @@ __device__ void paged_loader(const PagedParams& p, uint8_t* smem, uint32_t sbase
   int nth = 0;                                // K tiles issued (test hook)
   SegReader<D> segs;
   PSeg s;
-  while (segs.take(s, smem, bars, ctl, kRoleLoader)) {
+  while (segs.template take<kRoleLoader>(s, smem, bars, ctl)) {
     const int32_t* tab = s.prefix() ? p.prefix_table : p.table + s.b * p.table_sb;
     const uint64_t pol = s.prefix() ? pol_reuse : pol_once;
     const int ahead = tiles_ahead(s);
@@ -416,7 +407,7 @@ __device__ void paged_gather_q(const PagedParams& p, uint8_t* smem, uint32_t sba
   uint32_t ph = 0;
   SegReader<D> segs;
   PSeg s;
-  while (segs.take(s, smem, bars, ctl, kRoleLoader)) {
+  while (segs.template take<kRoleLoader>(s, smem, bars, ctl)) {
     const int n = min(s.rows - s.row0, kPagedTaskRows);
     bool waited = false;
     for (int i0 = 0; i0 < n; i0 += 32) {
@@ -431,17 +422,21 @@ __device__ void paged_gather_q(const PagedParams& p, uint8_t* smem, uint32_t sba
         ph ^= 1u;
         waited = true;
       }
+      // (the shuffles first: between the copies each would wait for the one before)
+      constexpr int kCopies = 32 / kRows;
+      unsigned long long from[kCopies];
 #pragma unroll
-      for (int j = 0; j < 32 / kRows; ++j) {
+      for (int j = 0; j < kCopies; ++j)
+        from[j] = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j * kRows + sub);
+#pragma unroll
+      for (int j = 0; j < kCopies; ++j) {
         const int i = j * kRows + sub;  // row of the 32
-        const __nv_bfloat16* from = reinterpret_cast<const __nv_bfloat16*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i));
         const int row = (i0 + i) % kBM;
         const int swz = C::kSwizzle == 128 ? ((c & 7) ^ (row & 7)) : (c ^ ((row >> 1) & 3));
         const uint32_t dst = sbase + P::kOffQ + ((i0 + i) / kBM) * C::kTileBytes +
                              (C::kSwizzle == 128 ? (c >> 3) * C::kChunkBytes : 0) + row * C::kSwizzle + swz * 16;
-        if (from != nullptr)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from + c * 8) : "memory");
+        if (from[j] != 0)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from[j] + c * 16) : "memory");
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
@@ -465,7 +460,7 @@ __device__ void paged_mma(const PagedParams& p, uint8_t* smem, uint32_t sbase, c
   RingPos<P::kStages> r;
   SegReader<D> segs;
   PSeg s;
-  while (segs.take(s, smem, bars, ctl, kRoleMma)) {
+  while (segs.template take<kRoleMma>(s, smem, bars, ctl)) {
     if (!ctl_wait(bars.q_full(), q_ph, ctl, -1, kRoleMma)) goto drain;
     q_ph ^= 1u;
     tc_fence_after();
@@ -609,36 +604,49 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
   uint32_t ring = 0;  // K and V tiles that the CTA took before this segment: the ring's position
   SegReader<D> segs;
   PSeg s;
-  while (segs.take(s, smem, bars, ctl, kRoleSoftmax)) {
-    const bool twin = s.twin();
-    const int r = s.row0 + (twin ? 0 : h * kBM) + row;
-    const bool real = r < s.rows;
+  // Round 0 runs the tile code once on whatever TMEM holds, while the first
+  // queries and keys are on their way: nothing is announced, P goes to columns
+  // that no product uses yet, and the real first tile finds its instructions
+  // fetched (they took ~3000 cycles of it).
+  const uint32_t t_warm = lane_base + (D == 32 ? 320u : 256u) + 128u * static_cast<uint32_t>(h);
+  s.rows = s.row0 = s.keys = s.k0 = s.flags = 0;
+  s.k1 = 1;
+  for (uint32_t warm = opaque(1u);; warm = 0u) {
     // Keys of this task that the row sees. Lanes without a row see them all:
     // what they compute is never read, and they ask for no masking.
-    int seen = s.keys;
-    RowPos x{0, 0, 0};
-    if (real) {
-      x = row_pos(p, s, r);
-      SeqLens sl;
-      if (s.prefix()) {
-        sl = seq_lens(p, x.b);
-      } else {
-        sl.len = s.len;
-        sl.ql = s.ql;
+    int seen = kBN / 2;
+    bool any = true;
+    if (warm == 0u) {
+      if (!segs.template take<kRoleSoftmax>(s, smem, bars, ctl)) return;
+      seen = s.keys;
+      const int r = s.row0 + (s.twin() ? 0 : h * kBM) + row;
+      const bool real = r < s.rows;
+      if (real) {
+        const RowPos x = row_pos(p, s, r);
+        SeqLens sl;
+        if (s.prefix()) {
+          sl = seq_lens(p, x.b);
+        } else {
+          sl.len = s.len;
+          sl.ql = s.ql;
+        }
+        const int all = keys_seen(p, sl, x.n);
+        seen = s.prefix() ? min(all, p.prefix_len) : max(all - p.prefix_len, 0);
       }
-      const int all = keys_seen(p, sl, x.n);
-      seen = s.prefix() ? min(all, p.prefix_len) : max(all - p.prefix_len, 0);
+      any = __any_sync(0xffffffffu, real && seen > 0);
+      ring += 2u * static_cast<uint32_t>(s.k1 - s.k0);
     }
-    const bool any = __any_sync(0xffffffffu, real && seen > 0);
-    ring += 2u * static_cast<uint32_t>(s.k1 - s.k0);
+    const bool twin = s.twin();
     float m_ref = -CUDART_INF_F, l = 0.f;
     bool first = true;
     for (int k = s.k0 + (twin ? h : 0); k < s.k1; k += twin ? 2 : 1) {
       const int base = k * kBN;
-      if (!warp_wait(bars.s_full(h), s_par, ctl, k)) return;
-      s_par ^= 1u;
-      tc_fence_after();
-      if (base + kBN > s.keys) {
+      if (warm == 0u) {
+        if (!warp_wait(bars.s_full(h), s_par, ctl, k)) return;
+        s_par ^= 1u;
+        tc_fence_after();
+      }
+      if (warm == 0u && base + kBN > s.keys) {
         // The task's last tile: V rows behind its end become zero. Its V is the
         // segment's last in the ring. (After s_full: this tile's S went out
         // behind whatever held the stage before, so `full` is in this tile's
@@ -656,32 +664,18 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
         __syncwarp();
       }
       if (any) {
-        // Two passes over S in pieces of 32 keys, read from TMEM twice: the
-        // loops stay rolled and the code small, which counts where a launch
-        // has only a few tiles an SM (one pass over 128 registers took ~5000
-        // cycles for the first tile, most of them instruction fetches).
+        // one tile of scores: mask, running maximum and sum, P as bf16 over S in two
+        // halves, each announced on its own barrier
         const int lim = seen - base;
-        const bool cut = __any_sync(0xffffffffu, lim < kBN);
-        float mx = -CUDART_INF_F;
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          uint32_t sr[32];
-          tmem_ld32(t_s + 32 * j, sr);
-          if (cut) {
-            const int lj = lim - 32 * j;
+        uint32_t sr[128];
+        tmem_ld128(t_s, sr);
+        if (__any_sync(0xffffffffu, lim < kBN)) {
+          const uint32_t neg_inf = __float_as_uint(-CUDART_INF_F);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i >= lj) sr[i] = __float_as_uint(-CUDART_INF_F);
-          }
-          float m4[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 4]));
-#pragma unroll
-          for (int i = 8; i < 32; i += 8)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], __uint_as_float(sr[i + q]), __uint_as_float(sr[i + q + 4]));
-          mx = fmax3(mx, fmax3(m4[0], m4[1], m4[2]), m4[3]);
+          for (int i = 0; i < 128; ++i)
+            if (i >= lim) sr[i] = neg_inf;
         }
+        const float mx = row_max128(sr);
         const float m_tile = (mx == -CUDART_INF_F) ? -CUDART_INF_F : mx * c;
         const bool grow = m_tile > m_ref + kRescaleLog2;
         float alpha = 1.f;
@@ -693,36 +687,32 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
         if (__any_sync(0xffffffffu, grow && !first)) rescale_o<D>(t_o, alpha);
         const float neg_m = (m_ref == -CUDART_INF_F) ? 0.f : -m_ref;
         const float2 c2 = make_float2(c, c), nm2 = make_float2(neg_m, neg_m);
-        float2 sum2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        // P of keys [32 j, 32 j + 32) goes over columns [16 j, 16 j + 16) of S,
-        // which pass 2 has read by then
-#pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          uint32_t sr[32], pk[16];
-          tmem_ld32(t_s + 32 * j, sr);
-          if (cut) {
-            const int lj = lim - 32 * j;
+        float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i >= lj) sr[i] = __float_as_uint(-CUDART_INF_F);
-          }
+        for (int part = 0; part < 2; ++part) {
+          uint32_t pk[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 y =
-                __ffma2_rn(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nm2);
+          for (int i = 0; i < 32; ++i) {
+            const int e = 64 * part + 2 * i;
+            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, nm2);
             const float2 pe = make_float2(ex2(y.x), ex2(y.y));
-            sum2[i & 1] = __fadd2_rn(sum2[i & 1], pe);
+            sum4[i & 3] = __fadd2_rn(sum4[i & 3], pe);
             pk[i] = pack_bf16(pe.x, pe.y);
           }
-          tmem_st16(t_p + 16 * j, pk);
-          if (j & 1) {  // 64 keys of P are announced at a time
+          if (part == 1) {
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bars.p_full(h, j >> 1));
+            if (lane == 0 && warm == 0u) mbar_arrive(bars.p_full(h, 0));
           }
+          tmem_st32((warm ? t_warm : t_p) + 32 * part, pk);
         }
-        l += (sum2[0].x + sum2[0].y) + (sum2[1].x + sum2[1].y);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0 && warm == 0u) mbar_arrive(bars.p_full(h, 1));
+        const float2 sa = __fadd2_rn(sum4[0], sum4[1]), sb = __fadd2_rn(sum4[2], sum4[3]);
+        l += (sa.x + sa.y) + (sb.x + sb.y);
       } else {
         // no row of this warp sees a key of the task: its P and O are never read
         tc_fence_before();
@@ -735,6 +725,7 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
       first = false;
     }
 
+    if (warm) continue;
     // the end of the segment: O of this row, to its part, its buffer or the result
     float m = m_ref, w0 = 1.f, w1 = 0.f;
     if (twin) {
@@ -765,6 +756,9 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
     }
     tc_fence_after();
     RowSink<D> sink;
+    const int r = s.row0 + (twin ? 0 : h * kBM) + row;
+    const bool real = r < s.rows;
+    const RowPos x = row_pos(p, s, real ? r : s.row0);
     const bool none = m == -CUDART_INF_F;
     const bool lead = !twin || h == 0;  // writes the row's m and l
     if (real) {
@@ -882,7 +876,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   // First the total, then a running sum over the sequences: the CTA's first
   // unit and the sequence that holds it. CTA 0 leaves the running sums for the
   // kernel that joins the parts.
-  const int up = prefix_units(p);
+  const int up = p.prefix_units;
   auto block_sum = [&](int v, int& below) -> int {  // sum over the block; below: over the threads before this one
     int inc = v;
 #pragma unroll
@@ -974,17 +968,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 constexpr int kJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   grid_dep_wait();
   const int lane = threadIdx.x & 31;
-  const int64_t rows = static_cast<int64_t>(p.B) * p.Nq * p.Hq;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
+  const int rows = p.B * p.Nq * p.Hq;  // below 2^30
+  const int row = static_cast<int>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   if (row >= rows) return;
   const int rs = p.Nq * p.G;
-  const int64_t bh = row / rs;
-  const int r = static_cast<int>(row - bh * rs), b = static_cast<int>(bh / p.Hk), hk = static_cast<int>(bh - static_cast<int64_t>(b) * p.Hk);
-  const int n = r / p.G, g = r - n * p.G;
+  const int bh = p.by_rows.div(row), r = row - bh * rs, b = bh / p.Hk, hk = bh - b * p.Hk;
+  const int n = p.by_g.div(r), g = r - n * p.G;
   const int units = p.starts[p.B];
   const Split split(units, grid);
 
@@ -1003,8 +996,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
   Span pre{0, 0, 0}, own{0, 0, 0};
   const SeqLens sl = seq_lens(p, b);
   if (p.prefix_len > 0) {
-    const int rp = b * rs + r, t = rp / kPagedTaskRows, tiles = prefix_tiles(p);
-    pre = span((hk * prefix_tasks(p) + t) * (tiles + kPagedTaskCost), tiles, rp - t * kPagedTaskRows);
+    const int rp = b * rs + r, t = rp / kPagedTaskRows, tiles = p.prefix_tiles;
+    pre = span((hk * p.prefix_tasks + t) * (tiles + kPagedTaskCost), tiles, rp - t * kPagedTaskRows);
   }
   {
     const int t = r / kPagedTaskRows;
@@ -1032,7 +1025,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_join_kernel(const __gri
       const Span s = is_pre ? pre : own;
       const int k = is_pre ? i : i - pre.parts;
       if (s.parts == 1) {
-        const int64_t at = (is_pre ? 0 : rows) + row;
+        const int64_t at = static_cast<int64_t>(is_pre ? 0 : rows) + row;
         pm = reinterpret_cast<const float*>(p.rows_ml + at);
         pair = true;
         src = p.rows_o + at * D;

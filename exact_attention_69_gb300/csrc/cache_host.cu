@@ -388,7 +388,7 @@ int attn_paged(const attn_paged_params* p) {
     return fail_with(ATTN_ERR_INVALID_ARG, "mask kind %d is not ATTN_MASK_NONE or ATTN_MASK_CAUSAL_BR", p->mask_kind);
   if (p->inject != 0 && p->inject != 1) return fail_with(ATTN_ERR_INVALID_ARG, "inject must be 0 or 1");
   attn::PagedParams k;
-  std::memset(&k, 0, sizeof(k));
+  std::memset(static_cast<void*>(&k), 0, sizeof(k));
   attn::RopeTensor q, o, kc, vc;
   if (p->n_pages < 1) return fail_with(ATTN_ERR_INVALID_ARG, "n_pages must be >= 1");
   if ((rc = log2_page(p->page_size, &k.page_shift)) != ATTN_OK ||
@@ -452,6 +452,14 @@ int attn_paged(const attn_paged_params* p) {
   k.Nq = p->Nq;
   k.G = static_cast<int>(G);
   k.prefix_len = p->prefix_len;
+  k.prefix_tiles = (p->prefix_len + attn::kBN - 1) / attn::kBN;
+  k.prefix_tasks = p->prefix_len > 0 ? static_cast<int>(tasks_pre) : 0;
+  k.prefix_units = p->Hk * k.prefix_tasks * (k.prefix_tiles + attn::kPagedTaskCost);
+  k.own_tasks = static_cast<int>(tasks_own);
+  k.by_g = attn::FastDiv(static_cast<uint32_t>(G));
+  k.by_rows = attn::FastDiv(static_cast<uint32_t>(p->Nq * G));
+  k.by_prefix_units = attn::FastDiv(static_cast<uint32_t>(k.prefix_tiles + attn::kPagedTaskCost));
+  k.by_prefix_tasks = attn::FastDiv(static_cast<uint32_t>(k.prefix_tasks > 0 ? k.prefix_tasks : 1));
   k.max_len = static_cast<int>(max_len);
   k.causal = p->mask_kind == ATTN_MASK_CAUSAL_BR;
   k.c = p->scale * 1.4426950408889634f;

@@ -14,6 +14,24 @@ constexpr int kPagedTaskRows = 256;  // two 128-row query tiles
 constexpr int kPagedTaskCost = 1;
 constexpr int kPagedMinUnits = 2;    // least work that opens another CTA
 
+// Division of n < 2^31 by a divisor that the host knows: n * mul >> (32 + shift)
+// with mul = ceil(2^(32 + shift) / d), shift = ceil(log2 d) - 1 (the error term
+// n * (mul * d - 2^(32 + shift)) stays below 2^(32 + shift)); d = 1 is kept apart.
+struct FastDiv {
+  uint32_t d, mul, shift;
+#ifdef __CUDACC__
+  __host__ __device__ FastDiv() : d(1), mul(0), shift(0) {}
+  __host__ explicit FastDiv(uint32_t div) : d(div), mul(0), shift(0) {
+    if (div <= 1) return;
+    while ((uint64_t{2} << shift) < div) ++shift;
+    mul = static_cast<uint32_t>(((uint64_t{1} << (32 + shift)) + div - 1) / div);
+  }
+  __device__ __forceinline__ int div(int n) const {
+    return d == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul) >> shift);
+  }
+#endif
+};
+
 struct PagedParams {
   CUtensorMap tm_k;             // 4-D (d, slot, head, page) bf16 maps, box (swizzle span, min(page, 128), 1, 1)
   CUtensorMap tm_v;
@@ -31,6 +49,11 @@ struct PagedParams {
   int prefix_len;
   int page_shift;
   int max_len;                  // table_width * page size: longest own length that the table holds
+  FastDiv by_g, by_rows;        // by G; by Nq * G, the rows of a sequence
+  FastDiv by_prefix_units;      // by the units of a prefix task
+  FastDiv by_prefix_tasks;      // by the prefix tasks of a key head
+  int prefix_tiles, prefix_tasks, prefix_units;  // tiles of a task; tasks of a key head; units of all
+  int own_tasks;                // tasks of a sequence for one key head
   int causal;                   // bottom-right causal over prefix and own keys together
   float c;                      // scale * log2(e)
   // workspace
