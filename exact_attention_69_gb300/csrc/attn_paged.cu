@@ -47,7 +47,7 @@ __device__ uint32_t g_paged_status[4];
 struct PSeg {
   int rows;        // rows that the task's key head has in all; 0: the CTA is done
   int row0;        // first row of the task
-  int keys;        // keys of the task's key space
+  int pt;          // leading tiles that are the prefix's; the others are the sequence's own
   int k0, k1;      // tiles [k0, k1)
   int hk, b;       // key head; sequence (own tasks)
   int len, ql;     // the sequence's lengths (own tasks)
@@ -75,10 +75,8 @@ struct PCfg {
   static constexpr int kOffX = kOffKV + kStages * C::kTileBytes;  // exchange: [2 streams][m, l][128]
   static constexpr int kXBytes = 2 * 2 * 128 * 4;
   static constexpr int kOffSeg = kOffX + kXBytes;
-  static constexpr int kOffScan = kOffSeg + kSegs * static_cast<int>(sizeof(PSeg));
-  static constexpr int kScanBytes = 96;
-  static constexpr int kOffBar = kOffScan + kScanBytes;
-  static constexpr int kBars = 16 + 2 * kSegs + 2 * kStages;
+  static constexpr int kOffBar = kOffSeg + kSegs * static_cast<int>(sizeof(PSeg));
+  static constexpr int kBars = 17 + 2 * kSegs + 2 * kStages;
   static constexpr int kSmemBytes = kOffBar + 8 * kBars + 16;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
@@ -98,10 +96,11 @@ struct PBars {
   // every product of a one-tile task is complete (o_full: of stream h of a two-tile task).
   // One barrier of its own, that both warpgroups wait for at every such task: none skips a phase.
   __device__ uint32_t t_full() const { return base + 120; }
-  __device__ uint32_t seg_full(int s) const { return base + 128 + 8 * s; }
-  __device__ uint32_t seg_empty(int s) const { return base + 128 + 8 * (kSg + s); }
-  __device__ uint32_t full(int s) const { return base + 128 + 8 * (2 * kSg + s); }
-  __device__ uint32_t empty(int s) const { return base + 128 + 8 * (2 * kSg + kSt + s); }
+  __device__ uint32_t q_asked() const { return base + 128; }  // the first task's queries are on their way
+  __device__ uint32_t seg_full(int s) const { return base + 136 + 8 * s; }
+  __device__ uint32_t seg_empty(int s) const { return base + 136 + 8 * (kSg + s); }
+  __device__ uint32_t full(int s) const { return base + 136 + 8 * (2 * kSg + s); }
+  __device__ uint32_t empty(int s) const { return base + 136 + 8 * (2 * kSg + kSt + s); }
 };
 
 // ------------------------------------------------------------------ work split
@@ -126,19 +125,25 @@ __device__ __forceinline__ int keys_seen(const PagedParams& p, SeqLens s, int n)
   return p.causal ? clampi(total - s.ql + n + 1, 0, total) : total;
 }
 
-// K/V tiles of a sequence's own keys that task t (rows [256 t, 256 t + 256)) needs.
-__device__ __forceinline__ int own_tiles(const PagedParams& p, SeqLens s, int t) {
+// K/V tiles that task t (rows [256 t, 256 t + 256)) of a sequence needs: the
+// prefix's unless batched tasks go over them, and its own.
+struct Tiles {
+  int prefix, all;
+};
+__device__ __forceinline__ Tiles own_tiles(const PagedParams& p, SeqLens s, int t) {
   const int first = p.by_g.div(t * kPagedTaskRows);
-  if (first >= s.ql) return 0;
+  if (first >= s.ql) return Tiles{0, 0};
   const int last = min(p.by_g.div(min((t + 1) * kPagedTaskRows, p.Nq * p.G) - 1), s.ql - 1);
-  return (clampi(keys_seen(p, s, last) - p.prefix_len, 0, s.len) + kBN - 1) / kBN;
+  const int seen = keys_seen(p, s, last);
+  const int pre = p.prefix_tasks > 0 ? 0 : (min(seen, p.prefix_len) + kBN - 1) / kBN;
+  return Tiles{pre, pre + (max(seen - p.prefix_len, 0) + kBN - 1) / kBN};
 }
 
 // Units of one sequence's tasks for one key head.
 __device__ __forceinline__ int own_units(const PagedParams& p, SeqLens s) {
   int u = 0;
   for (int t = 0; t < p.own_tasks; ++t) {
-    const int tiles = own_tiles(p, s, t);
+    const int tiles = own_tiles(p, s, t).all;
     u += tiles + (tiles > 0 ? kPagedTaskCost : 0);
   }
   return u;
@@ -164,6 +169,7 @@ struct PSegIter {
   int b, sb;       // current sequence and its first unit
   SeqLens cur, nxt;
   int ub;          // its units per key head
+  int task, parts_end;  // of the segment: index in the task table; its last unit
 
   // u0: the CTA's first unit; b0, s0: the sequence that holds it (or the next) and its first unit.
   __device__ __forceinline__ PSegIter(const PagedParams& p, int u0, int u1, int b0, int s0)
@@ -188,7 +194,8 @@ struct PSegIter {
         s.b = s.len = s.ql = 0;
         s.row0 = (t - s.hk * p.prefix_tasks) * kPagedTaskRows;
         s.rows = p.B * p.Nq * p.G;
-        s.keys = p.prefix_len;
+        s.pt = tiles;
+        task = p.B * p.Hk * p.own_tasks + t;
       } else {
         while (u >= sb + p.Hk * ub) {
           sb += p.Hk * ub;
@@ -204,22 +211,25 @@ struct PSegIter {
         s.hk = (u - sb) / ub;
         a = sb + s.hk * ub;
         int t = 0;
-        tiles = own_tiles(p, cur, 0);
+        Tiles n = own_tiles(p, cur, 0);
         for (;;) {
-          const int per = tiles + (tiles > 0 ? kPagedTaskCost : 0);
+          const int per = n.all + (n.all > 0 ? kPagedTaskCost : 0);
           if (u < a + per) break;
           a += per;
-          tiles = own_tiles(p, cur, ++t);
+          n = own_tiles(p, cur, ++t);
         }
+        tiles = n.all;
+        s.pt = n.prefix;
+        task = (b * p.Hk + s.hk) * p.own_tasks + t;
         s.row0 = t * kPagedTaskRows;
         s.rows = p.Nq * p.G;
-        s.keys = cur.len;
       }
       const int first = a + kPagedTaskCost, end = first + tiles;
       s.k0 = max(u, first) - first;
       s.k1 = min(hi, end) - first;
       if (s.rows - s.row0 <= kBM) s.flags |= PSeg::kTwin;
       if (s.k0 == 0) s.flags |= s.k1 == tiles ? PSeg::kWhole | PSeg::kFirst : PSeg::kFirst;
+      parts_end = end - 1;
       u = min(hi, end);
       if (s.k1 > s.k0) return true;
     }
@@ -264,20 +274,53 @@ __device__ __forceinline__ void tma_lane(uint32_t dst, const CUtensorMap* m, uin
       : "memory");
 }
 
-// Warp 3: the CTA's segments, one after the other, into the descriptor ring.
+// Warp 3: reads the lengths, finds the CTA's share of the units (first the
+// total, then a running sum over the sequences up to the CTA's first unit) and
+// puts its segments into the descriptor ring, one after the other. Whoever
+// holds a task's first tile notes who else has parts of it, for the join.
 template <int D>
-__device__ void paged_scheduler(const PagedParams& p, uint8_t* smem, const PBars<D>& bars, int u0, int u1, int b0,
-                                int s0, const Ctl& ctl) {
+__device__ void paged_scheduler(const PagedParams& p, uint8_t* smem, const PBars<D>& bars, const Ctl& ctl) {
   using P = PCfg<D>;
+  const int lane = threadIdx.x & 31;
+  grid_dep_wait();  // lengths and tables are the previous kernel's to write
+  const int mine = lane < p.B ? p.Hk * own_units(p, seq_lens(p, lane)) : 0;  // of the first 32 sequences
+  int sum = mine;
+#pragma unroll 4
+  for (int b = lane + 32; b < p.B; b += 32) sum += p.Hk * own_units(p, seq_lens(p, b));
+  const Split split(p.prefix_units + __reduce_add_sync(0xffffffffu, sum), gridDim.x);
+  const int u0 = split.lo(blockIdx.x), u1 = split.lo(blockIdx.x + 1);
+  int b0 = 0, s0 = p.prefix_units;  // the sequence that holds u0 (or the first behind it), its first unit
+  if (u0 < u1 && u0 >= p.prefix_units) {
+    for (;; b0 += 32) {
+      const int b = b0 + lane;
+      const int v = b0 == 0 ? mine : (b < p.B ? p.Hk * own_units(p, seq_lens(p, b)) : 0);
+      int inc = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, s0 + inc > u0);
+      if (past != 0u) {
+        const int at = __ffs(past) - 1;
+        s0 += __shfl_sync(0xffffffffu, inc - v, at);
+        b0 += at;
+        break;
+      }
+      s0 += __shfl_sync(0xffffffffu, inc, 31);
+    }
+  }
   PSegIter it(p, u0, u1, b0, s0);
   RingPos<P::kSegs> r;
   for (bool more = true; more;) {
     PSeg s;
     more = it.next(p, s);
     if (!ctl_wait(bars.seg_empty(r.s), r.ph ^ 1u, ctl, -1, kRoleLoader)) return;
-    if ((threadIdx.x & 31) == 0) {
+    if (lane == 0) {
       *reinterpret_cast<PSeg*>(smem + P::kOffSeg + r.s * sizeof(PSeg)) = s;
       mbar_arrive(bars.seg_full(r.s));
+      if (more && s.first())
+        p.tasks[it.task] = make_int2(blockIdx.x, split.owner(it.parts_end) - static_cast<int>(blockIdx.x) + 1);
     }
     __syncwarp();
     r.advance();
@@ -300,7 +343,7 @@ struct SegReader {
     const int4 a = src[0], b = src[1], c = src[2];
     s.rows = a.x;
     s.row0 = a.y;
-    s.keys = a.z;
+    s.pt = a.z;
     s.k0 = a.w;
     s.k1 = b.x;
     s.hk = b.y;
@@ -335,25 +378,28 @@ __device__ void paged_loader(const PagedParams& p, uint8_t* smem, uint32_t sbase
   int nth = 0;                                // K tiles issued (test hook)
   SegReader<D> segs;
   PSeg s;
+  grid_dep_wait();
   while (segs.template take<kRoleLoader>(s, smem, bars, ctl)) {
-    const int32_t* tab = s.prefix() ? p.prefix_table : p.table + s.b * p.table_sb;
-    const uint64_t pol = s.prefix() ? pol_reuse : pol_once;
+    const int32_t* own = p.table + s.b * p.table_sb;
     const int ahead = tiles_ahead(s);
-    // this lane's page of tile k, -1: none (a tile's pages behind the last key are not loaded)
+    // this lane's first key of tile k among the prefix's or the own keys, and whether
+    // it has a page to load (pages behind the last key are not loaded)
+    auto key_of = [&](int k) -> int { return (k < s.pt ? k : k - s.pt) * kBN + lane * box; };
+    auto has = [&](int k) -> bool { return lane < per_tile && key_of(k) < (k < s.pt ? p.prefix_len : s.len); };
     auto page_of = [&](int k) -> int {
-      const int key = k * kBN + lane * box;
-      return (k < s.k1 && lane < per_tile && key < s.keys) ? tab[key >> p.page_shift] : 0;
+      return k < s.k1 && has(k) ? (k < s.pt ? p.prefix_table : own)[key_of(k) >> p.page_shift] : 0;
     };
     auto load = [&](const CUtensorMap* map, int k, int id, bool withhold) -> bool {
       if (!ctl_wait(bars.empty(r.s), r.ph ^ 1u, ctl, k, kRoleLoader)) return false;
-      const bool mine = lane < per_tile && k * kBN + lane * box < s.keys;
+      const bool mine = has(k);
       const uint32_t bytes = static_cast<uint32_t>(__popc(__ballot_sync(0xffffffffu, mine))) * box_bytes;
       if (!withhold) {
         mbar_expect_tx(bars.full(r.s), bytes);
         __syncwarp();
         if (mine) {
           const uint32_t dst = sbase + P::kOffKV + r.s * C::kTileBytes + lane * box * C::kSwizzle;
-          const int slot = (k * kBN + lane * box) & (page - 1);
+          const int slot = key_of(k) & (page - 1);
+          const uint64_t pol = k < s.pt ? pol_reuse : pol_once;
           for (int c = 0; c < C::kChunks; ++c)
             tma_lane(dst + c * C::kChunkBytes, map, bars.full(r.s), c * C::kBoxCols, slot, s.hk, id, pol);
         }
@@ -366,6 +412,9 @@ __device__ void paged_loader(const PagedParams& p, uint8_t* smem, uint32_t sbase
     };
     // page numbers are fetched one step before they are used
     int id_k = page_of(s.k0), id_n = page_of(s.k0 + 1), id_v = id_k;
+    if (nth == 0) {  // the CTA's first queries go ahead of its first five tiles: behind them they waited 6000 cycles
+      if (!ctl_wait(bars.q_asked(), 0, ctl, -1, kRoleLoader)) goto drain;
+    }
     for (int i = 0; i < ahead && s.k0 + i < s.k1; ++i) {
       const bool withhold = p.inject && nth == 1;  // test hook: the MMA issuer's wait must run out
       ++nth;
@@ -393,11 +442,13 @@ drain:
 }
 
 // Warp 2: the task's query rows into the swizzled K-major layout that the MMA
-// descriptor expects, 16 bytes a copy, every copy of a task in flight at once.
-// Each lane works out the address of one row of 32; a row's d/8 lanes get it
-// by shuffles.
+// descriptor expects. Where a query tile is a box of a tensor map it is one TMA
+// per column chunk: prefix tasks of one query a sequence (rows b, head), and
+// tasks inside one sequence of many rows (rows n, head), if G divides 128.
+// Otherwise 16 bytes a copy, every copy of a task in flight at once: each lane
+// works out the address of one row of 32, a row's d/8 lanes get it by shuffles.
 template <int D>
-__device__ void paged_gather_q(const PagedParams& p, uint8_t* smem, uint32_t sbase, const PBars<D>& bars,
+__device__ void paged_gather_q(const PagedParams& p, uint32_t sbase, uint8_t* smem, const PBars<D>& bars,
                                const Ctl& ctl) {
   using P = PCfg<D>;
   using C = Cfg<D>;
@@ -405,46 +456,63 @@ __device__ void paged_gather_q(const PagedParams& p, uint8_t* smem, uint32_t sba
   const int lane = threadIdx.x & 31;
   const int c = lane % kLanes, sub = lane / kLanes;   // 16-byte chunk of the row; which row of the instruction's
   uint32_t ph = 0;
+  bool asked = false;
+  bool box = false;  // the last task's queries came as boxes
   SegReader<D> segs;
   PSeg s;
+  grid_dep_wait();
   while (segs.template take<kRoleLoader>(s, smem, bars, ctl)) {
     const int n = min(s.rows - s.row0, kPagedTaskRows);
-    bool waited = false;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const __nv_bfloat16* src = nullptr;
-      if (i0 + lane < n) {
-        const RowPos x = row_pos(p, s, s.row0 + i0 + lane);
-        src = static_cast<const __nv_bfloat16*>(p.q) + x.b * p.q_sb + static_cast<int64_t>(s.hk * p.G + x.g) * p.q_sh +
-              x.n * p.q_sn;
-      }
-      if (!waited) {
-        if (!ctl_wait(bars.q_empty(), ph ^ 1u, ctl, -1, kRoleLoader)) return;
-        ph ^= 1u;
-        waited = true;
-      }
-      // (the shuffles first: between the copies each would wait for the one before)
-      constexpr int kCopies = 32 / kRows;
-      unsigned long long from[kCopies];
+    if (!ctl_wait(bars.q_empty(), ph ^ 1u, ctl, -1, kRoleLoader)) break;
+    box = p.q_map == (s.prefix() ? 1 : 2);
+    if (box) {
+      const int tiles = n > kBM ? 2 : 1, first = p.by_g.div(s.row0), per = p.by_g.div(kBM);
+      mbar_expect_tx(bars.q_full(), static_cast<uint32_t>(tiles) * C::kTileBytes);
+      for (int i = 0; i < tiles; ++i)
+        for (int ch = 0; ch < C::kChunks; ++ch)
+          tma_load_4d(sbase + P::kOffQ + i * C::kTileBytes + ch * C::kChunkBytes, &p.tm_q, bars.q_full(),
+                      ch * C::kBoxCols, s.hk * p.G, s.prefix() ? 0 : first + i * per, s.prefix() ? first + i * per : s.b);
+    } else {
+      for (int i0 = 0; i0 < n; i0 += 32) {
+        const __nv_bfloat16* src = nullptr;
+        if (i0 + lane < n) {
+          const RowPos x = row_pos(p, s, s.row0 + i0 + lane);
+          src = static_cast<const __nv_bfloat16*>(p.q) + x.b * p.q_sb + static_cast<int64_t>(s.hk * p.G + x.g) * p.q_sh +
+                x.n * p.q_sn;
+        }
+        // (the shuffles first: between the copies each would wait for the one before)
+        constexpr int kCopies = 32 / kRows;
+        unsigned long long from[kCopies];
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j)
-        from[j] = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j * kRows + sub);
+        for (int j = 0; j < kCopies; ++j)
+          from[j] = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j * kRows + sub);
 #pragma unroll
-      for (int j = 0; j < kCopies; ++j) {
-        const int i = j * kRows + sub;  // row of the 32
-        const int row = (i0 + i) % kBM;
-        const int swz = C::kSwizzle == 128 ? ((c & 7) ^ (row & 7)) : (c ^ ((row >> 1) & 3));
-        const uint32_t dst = sbase + P::kOffQ + ((i0 + i) / kBM) * C::kTileBytes +
-                             (C::kSwizzle == 128 ? (c >> 3) * C::kChunkBytes : 0) + row * C::kSwizzle + swz * 16;
-        if (from[j] != 0)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from[j] + c * 16) : "memory");
+        for (int j = 0; j < kCopies; ++j) {
+          const int i = j * kRows + sub;  // row of the 32
+          const int row = (i0 + i) % kBM;
+          const int swz = C::kSwizzle == 128 ? ((c & 7) ^ (row & 7)) : (c ^ ((row >> 1) & 3));
+          const uint32_t dst = sbase + P::kOffQ + ((i0 + i) / kBM) * C::kTileBytes +
+                               (C::kSwizzle == 128 ? (c >> 3) * C::kChunkBytes : 0) + row * C::kSwizzle + swz * 16;
+          if (from[j] != 0)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from[j] + c * 16) : "memory");
+        }
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bars.q_full());
+    if (!asked) {
+      asked = true;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.q_asked());
+    }
+    if (!box) {
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars.q_full());
+    }
+    ph ^= 1u;
   }
-  asm volatile("cp.async.wait_all;" ::: "memory");
+  // boxes on their way must have landed before the CTA exits (those of earlier tasks were used)
+  if (box) ctl_wait(bars.q_full(), ph ^ 1u, ctl, -1, kRoleLoader, false);
 }
 
 template <int D>
@@ -460,6 +528,7 @@ __device__ void paged_mma(const PagedParams& p, uint8_t* smem, uint32_t sbase, c
   RingPos<P::kStages> r;
   SegReader<D> segs;
   PSeg s;
+  grid_dep_wait();  // (the bound on the waits below is not for the kernel before)
   while (segs.template take<kRoleMma>(s, smem, bars, ctl)) {
     if (!ctl_wait(bars.q_full(), q_ph, ctl, -1, kRoleMma)) goto drain;
     q_ph ^= 1u;
@@ -609,18 +678,19 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
   // that no product uses yet, and the real first tile finds its instructions
   // fetched (they took ~3000 cycles of it).
   const uint32_t t_warm = lane_base + (D == 32 ? 320u : 256u) + 128u * static_cast<uint32_t>(h);
-  s.rows = s.row0 = s.keys = s.k0 = s.flags = 0;
+  s.rows = s.row0 = s.pt = s.k0 = s.len = s.flags = 0;
   s.k1 = 1;
   for (uint32_t warm = opaque(1u);; warm = 0u) {
-    // Keys of this task that the row sees. Lanes without a row see them all:
-    // what they compute is never read, and they ask for no masking.
+    // Keys that the row sees, the prefix's first. Lanes without a row see them
+    // all: what they compute is never read, and they ask for no masking.
     int seen = kBN / 2;
     bool any = true;
     if (warm == 0u) {
+      grid_dep_wait();  // (returns at once after the first time)
       if (!segs.template take<kRoleSoftmax>(s, smem, bars, ctl)) return;
-      seen = s.keys;
       const int r = s.row0 + (s.twin() ? 0 : h * kBM) + row;
       const bool real = r < s.rows;
+      seen = 1 << 30;
       if (real) {
         const RowPos x = row_pos(p, s, r);
         SeqLens sl;
@@ -630,43 +700,43 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
           sl.len = s.len;
           sl.ql = s.ql;
         }
-        const int all = keys_seen(p, sl, x.n);
-        seen = s.prefix() ? min(all, p.prefix_len) : max(all - p.prefix_len, 0);
+        seen = keys_seen(p, sl, x.n);
       }
       any = __any_sync(0xffffffffu, real && seen > 0);
-      ring += 2u * static_cast<uint32_t>(s.k1 - s.k0);
     }
     const bool twin = s.twin();
     float m_ref = -CUDART_INF_F, l = 0.f;
     bool first = true;
     for (int k = s.k0 + (twin ? h : 0); k < s.k1; k += twin ? 2 : 1) {
-      const int base = k * kBN;
+      // the tile's first key among the prefix's or the own keys, and how many of those there are
+      const int base = (k < s.pt ? k : k - s.pt) * kBN, end = k < s.pt ? p.prefix_len : s.len;
       if (warm == 0u) {
         if (!warp_wait(bars.s_full(h), s_par, ctl, k)) return;
         s_par ^= 1u;
         tc_fence_after();
-      }
-      if (warm == 0u && base + kBN > s.keys) {
-        // The task's last tile: V rows behind its end become zero. Its V is the
-        // segment's last in the ring. (After s_full: this tile's S went out
-        // behind whatever held the stage before, so `full` is in this tile's
-        // phase or past it, and the parity below cannot match an older one.)
-        const uint32_t at = ring - 1u;
-        const int st = static_cast<int>(at % P::kStages);
-        if (!warp_wait(bars.full(st), (at / P::kStages) & 1u, ctl, k)) return;
-        const int z0 = max(s.keys - base, quarter * 32), z1 = quarter * 32 + 32;
-        for (int ch = 0; ch < C::kChunks; ++ch) {
-          uint8_t* v = smem + P::kOffKV + st * C::kTileBytes + ch * C::kChunkBytes;
-          for (int i = z0 * C::kSwizzle + lane * 16; i < z1 * C::kSwizzle; i += 512)
-            *reinterpret_cast<uint4*>(v + i) = make_uint4(0, 0, 0, 0);
+        if (base + kBN > end) {
+          // The last tile of the prefix or of the own keys: V rows behind their
+          // end become zero. (After s_full: this tile's S went out behind
+          // whatever held the V's stage before, so `full` is in this tile's
+          // phase or past it, and the parity below cannot match an older one.)
+          const int i = k - s.k0, n = s.k1 - s.k0, ahead = min(tiles_ahead(s), n);
+          const uint32_t at = ring + static_cast<uint32_t>(ahead + i + min(i, n - ahead));
+          const int st = static_cast<int>(at % P::kStages);
+          if (!warp_wait(bars.full(st), (at / P::kStages) & 1u, ctl, k)) return;
+          const int z0 = max(end - base, quarter * 32), z1 = quarter * 32 + 32;
+          for (int ch = 0; ch < C::kChunks; ++ch) {
+            uint8_t* v = smem + P::kOffKV + st * C::kTileBytes + ch * C::kChunkBytes;
+            for (int i2 = z0 * C::kSwizzle + lane * 16; i2 < z1 * C::kSwizzle; i2 += 512)
+              *reinterpret_cast<uint4*>(v + i2) = make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
         }
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        __syncwarp();
       }
       if (any) {
         // one tile of scores: mask, running maximum and sum, P as bf16 over S in two
         // halves, each announced on its own barrier
-        const int lim = seen - base;
+        const int lim = (k < s.pt ? min(seen, end) : min(seen - p.prefix_len, end)) - base;
         uint32_t sr[128];
         tmem_ld128(t_s, sr);
         if (__any_sync(0xffffffffu, lim < kBN)) {
@@ -726,6 +796,8 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
     }
 
     if (warm) continue;
+    ring += 2u * static_cast<uint32_t>(s.k1 - s.k0);
+
     // the end of the segment: O of this row, to its part, its buffer or the result
     float m = m_ref, w0 = 1.f, w1 = 0.f;
     if (twin) {
@@ -769,7 +841,7 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
           base[32 * D + lane] = m;
           base[32 * D + 32 + lane] = l;
         }
-      } else if (p.prefix_len > 0) {
+      } else if (p.prefix_tasks > 0) {
         const int64_t rows = static_cast<int64_t>(p.B) * p.Nq * p.Hq;
         const int64_t i = (s.prefix() ? 0 : rows) + row_index(p, x.b, s.hk, x.n, x.g);
         if (!none) sink.buf = p.rows_o + i * D;
@@ -834,11 +906,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     if (threadIdx.x == 0) atomicCAS(g_paged_status, 0u, 255u);
     return;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const PBars<D> bars{sbase + P::kOffBar};
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + P::kOffBar + 8 * P::kBars);
   volatile uint32_t* abort_flag = tmem_slot + 1;
-  int32_t* scan = reinterpret_cast<int32_t*>(smem + P::kOffScan);  // [0, 12) warps' sums, [16..17] results
 
   if (threadIdx.x == 0) {
     mbar_init(bars.q_full(), 1);
@@ -853,6 +924,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     }
     mbar_init(bars.done(), 1);
     mbar_init(bars.t_full(), 1);
+    mbar_init(bars.q_asked(), 1);
     for (int s = 0; s < P::kSegs; ++s) {
       mbar_init(bars.seg_full(s), 1);
       mbar_init(bars.seg_empty(s), kWarps - 1);  // every warp but the scheduler
@@ -865,74 +937,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     fence_barrier_init();
     prefetch_tmap(&p.tm_k);
     prefetch_tmap(&p.tm_v);
+    if (p.q_map != 0) prefetch_tmap(&p.tm_q);
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(tmem_slot), Cfg<D>::kTmemCols);
     tmem_relinquish();
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  grid_dep_wait();  // the lengths are the previous kernel's to write
-
-  // First the total, then a running sum over the sequences: the CTA's first
-  // unit and the sequence that holds it. CTA 0 leaves the running sums for the
-  // kernel that joins the parts.
-  const int up = p.prefix_units;
-  auto block_sum = [&](int v, int& below) -> int {  // sum over the block; below: over the threads before this one
-    int inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int t = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += t;
-    }
-    __syncthreads();
-    if (lane == 31) scan[warp] = inc;
-    __syncthreads();
-    int total = 0;
-    below = inc - v;
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) below += scan[w];
-      total += scan[w];
-    }
-    return total;
-  };
-  // (up to 384 sequences: one look at each, kept in a register)
-  const int v0 = threadIdx.x < p.B ? p.Hk * own_units(p, seq_lens(p, threadIdx.x)) : 0;
-  int below;
-  int own = block_sum(v0, below);
-  for (int b0 = kThreads; b0 < p.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    int unused;
-    own += block_sum(b < p.B ? p.Hk * own_units(p, seq_lens(p, b)) : 0, unused);
-  }
-  const int units = up + own;
-  const Split split(units, gridDim.x);
-  const int u0 = split.lo(blockIdx.x), u1 = split.lo(blockIdx.x + 1);
-  if (threadIdx.x == 0 && u0 < up) {
-    scan[16] = 0;  // first sequence to look at, and its first unit
-    scan[17] = up;
-  }
-  int run = up;
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-    const int b = b0 + threadIdx.x;
-    int v = v0, total = 0;
-    if (b0 > 0) v = b < p.B ? p.Hk * own_units(p, seq_lens(p, b)) : 0;
-    if (p.B > kThreads) total = block_sum(v, below);
-    const int at = run + below;
-    if (b < p.B) {
-      if (blockIdx.x == 0) p.starts[b] = at;
-      if (u0 >= up && u0 >= at && u0 < at + v) {
-        scan[16] = b;
-        scan[17] = at;
-      }
-    }
-    run += total;
-  }
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.starts[p.B] = units;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Ctl ctl{abort_flag, g_paged_status, p.timeout_ns};
+  // So far and in the softmax warps' round 0 only shared memory and TMEM are
+  // touched; every role waits for the previous kernel on the stream before its
+  // first global access.
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp < 4) {
     set_max_regs_dec<kRegsControl>();
@@ -941,10 +960,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
     } else if (warp == 1) {
       paged_mma<D>(p, smem, sbase, bars, tmem, ctl);
     } else if (warp == 2) {
-      paged_gather_q<D>(p, smem, sbase, bars, ctl);
+      paged_gather_q<D>(p, sbase, smem, bars, ctl);
     } else {
-      // a CTA without units (u0 == u1) has no sequence to start from and reads none
-      paged_scheduler<D>(p, smem, bars, u0, u1, u0 < u1 ? scan[16] : 0, u0 < u1 ? scan[17] : 0, ctl);
+      paged_scheduler<D>(p, smem, bars, ctl);
     }
     __syncwarp();
   } else {
@@ -968,7 +986,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 constexpr int kJoinWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32, 2) paged_join_kernel(const __grid_constant__ PagedParams p, int grid) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 2) paged_join_kernel(const __grid_constant__ PagedParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   grid_dep_wait();
   const int lane = threadIdx.x & 31;
@@ -976,39 +994,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 2) paged_join_kernel(const __
   const int row = static_cast<int>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
   if (row >= rows) return;
   const int rs = p.Nq * p.G;
-  const int bh = p.by_rows.div(row), r = row - bh * rs, b = bh / p.Hk, hk = bh - b * p.Hk;
+  const int bh = p.by_rows.div(row), r = row - bh * rs, b = p.by_heads.div(bh), hk = bh - b * p.Hk;
   const int n = p.by_g.div(r), g = r - n * p.G;
-  const int units = p.starts[p.B];
-  const Split split(units, grid);
 
-  // the row's two tasks: first unit with a tile, tiles, row inside the task
+  // the row's two tasks: where their parts are, and the row inside the task
   struct Span {
-    int c0, parts, in_task;  // parts 0: none; 1: uncut
-  };
-  auto span = [&](int a, int tiles, int in_task) {
-    Span s{0, 0, in_task};
-    if (tiles > 0) {
-      s.c0 = split.owner(a + kPagedTaskCost);
-      s.parts = split.owner(a + kPagedTaskCost + tiles - 1) - s.c0 + 1;
-    }
-    return s;
+    int c0, parts, in_task;  // parts 0: no key to see; 1: uncut
   };
   Span pre{0, 0, 0}, own{0, 0, 0};
-  const SeqLens sl = seq_lens(p, b);
-  if (p.prefix_len > 0) {
-    const int rp = b * rs + r, t = rp / kPagedTaskRows, tiles = p.prefix_tiles;
-    pre = span((hk * p.prefix_tasks + t) * (tiles + kPagedTaskCost), tiles, rp - t * kPagedTaskRows);
+  const int t = r / kPagedTaskRows, rp = b * rs + r, tp = rp / kPagedTaskRows;
+  const int2 at_own = p.tasks[bh * p.own_tasks + t];  // (written only if the task has a tile)
+  if (p.prefix_tasks > 0) {
+    const int2 e = p.tasks[p.B * p.Hk * p.own_tasks + hk * p.prefix_tasks + tp];
+    pre = Span{e.x, e.y, rp - tp * kPagedTaskRows};
   }
-  {
-    const int t = r / kPagedTaskRows;
-    int a = p.starts[b] + hk * own_units(p, sl);
-    for (int i = 0; i < t; ++i) {
-      const int tiles = own_tiles(p, sl, i);
-      a += tiles + (tiles > 0 ? kPagedTaskCost : 0);
-    }
-    own = span(a, own_tiles(p, sl, t), r - t * kPagedTaskRows);
-  }
-  if (p.prefix_len == 0 && own.parts == 1) return;  // written by the attention kernel
+  if (own_tiles(p, seq_lens(p, b), t).all > 0) own = Span{at_own.x, at_own.y, r - t * kPagedTaskRows};
+  if (p.prefix_tasks == 0 && own.parts == 1) return;  // written by the attention kernel
 
   const int parts = pre.parts + own.parts;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -1117,7 +1118,7 @@ cudaError_t launch_paged_dim(const PagedParams& p, int grid, cudaStream_t s) {
   cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p, grid);
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p);
 }
 
 }  // namespace dev

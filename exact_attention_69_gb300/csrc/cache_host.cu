@@ -173,8 +173,9 @@ int64_t up256(int64_t x) { return (x + 255) & ~int64_t{255}; }
 
 struct PagedPlan {
   int grid = 0;
-  int64_t starts = 0, slots = 0, rows_o = 0, rows_ml = 0;  // bytes of the workspace's parts
-  int64_t bytes() const { return starts + slots + rows_o + rows_ml; }
+  bool batched = false;  // the prefix's tiles once for rows of several sequences
+  int64_t tasks = 0, slots = 0, rows_o = 0, rows_ml = 0;  // bytes of the workspace's parts
+  int64_t bytes() const { return tasks + slots + rows_o + rows_ml; }
 };
 
 int check_paged_sizes(const attn_paged_params* p) {
@@ -196,9 +197,19 @@ int check_paged_sizes(const attn_paged_params* p) {
 void plan_paged(const attn_paged_params* p, int sms, PagedPlan* pl) {
   pl->grid = p->num_ctas > 0 && p->num_ctas < sms ? p->num_ctas : sms;
   const int64_t rows = static_cast<int64_t>(p->B) * p->Nq * p->Hq;
-  pl->starts = up256((static_cast<int64_t>(p->B) + 1) * 4);
+  // Batched: 256 rows of the batch read the prefix's tiles together, and each
+  // row's prefix part and own part go through the workspace to the join, which
+  // for 256 rows moves as many bytes as kJoinTiles K/V tiles (d fp32 written and
+  // read, twice). Otherwise each sequence's tasks go over the prefix and its own
+  // keys in one go. Few rows a sequence (decoding): batched, unless the prefix
+  // is a tile or two for one sequence; hundreds (prompt chunks): not.
+  constexpr int kJoinTiles = 8;
+  const int64_t rs = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk), tr = attn::kPagedTaskRows;
+  const int64_t own = (rs + tr - 1) / tr, pre = (p->B * rs + tr - 1) / tr, tiles = (static_cast<int64_t>(p->prefix_len) + 127) / 128;
+  pl->batched = p->prefix_len > 0 && p->B * own * tiles > pre * (tiles + attn::kPagedTaskCost) + kJoinTiles * p->B * rs / tr;
+  pl->tasks = up256((p->B * p->Hk * own + (pl->batched ? p->Hk * pre : 0)) * static_cast<int64_t>(sizeof(int2)));
   pl->slots = up256(static_cast<int64_t>(pl->grid) * 4 * 128 * (p->d + 2) * 4);
-  if (p->prefix_len > 0) {
+  if (pl->batched) {
     pl->rows_o = up256(2 * rows * p->d * 4);
     pl->rows_ml = up256(2 * rows * 8);
   }
@@ -221,6 +232,25 @@ int encode_pages(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)
     return fail_with(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", name, static_cast<int>(r));
+  return ATTN_OK;
+}
+
+int encode_queries(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const attn_paged_params* p,
+                   const attn::RopeTensor& q, int G, bool sequences) {
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p->d), static_cast<cuuint64_t>(p->Hq),
+                              static_cast<cuuint64_t>(p->Nq), static_cast<cuuint64_t>(p->B)};
+  auto bytes = [&](int64_t s) { return static_cast<cuuint64_t>(s > 0 ? s : p->d) * 2; };
+  const cuuint64_t strides[3] = {bytes(q.sh), bytes(q.sn), bytes(q.sb)};
+  const cuuint32_t per = static_cast<cuuint32_t>(128 / G);
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(p->d >= 64 ? 64 : 32), static_cast<cuuint32_t>(G),
+                             sequences ? 1u : per, sequences ? per : 1u};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, q.p, dims, strides, box, ones,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            p->d >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail_with(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled(q) failed with CUresult %d", static_cast<int>(r));
   return ATTN_OK;
 }
 
@@ -414,7 +444,7 @@ int attn_paged(const attn_paged_params* p) {
                 tasks_pre = (static_cast<int64_t>(p->B) * p->Nq * G + attn::kPagedTaskRows - 1) / attn::kPagedTaskRows;
   const double most = static_cast<double>(p->Hk) *
                       (static_cast<double>(tasks_pre) * (p->prefix_len / 128 + 2) +
-                       static_cast<double>(p->B) * tasks_own * (static_cast<double>(max_len) / 128 + 2));
+                       static_cast<double>(p->B) * tasks_own * (static_cast<double>(max_len + p->prefix_len) / 128 + 3));
   if (most >= static_cast<double>(kMaxCount)) return fail_with(ATTN_ERR_INVALID_ARG, "problem too large");
   if (p->workspace && !aligned(p->workspace, 16)) return fail_with(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
 
@@ -432,6 +462,13 @@ int attn_paged(const attn_paged_params* p) {
   if ((rc = encode_pages(encode, &k.tm_k, p->k_cache, p->d, p->page_size, p->Hk, p->n_pages, ks, "k_cache")) != ATTN_OK ||
       (rc = encode_pages(encode, &k.tm_v, p->v_cache, p->d, p->page_size, p->Hk, p->n_pages, vs, "v_cache")) != ATTN_OK)
     return rc;
+  // Query tiles as boxes of a tensor map: 128 / G queries of a sequence (tasks of
+  // many rows), or one query of 128 / G sequences (prefix tasks while decoding).
+  const bool one = pl.batched && p->Nq == 1, many = p->Nq * G > 64;
+  if ((one || many) && 128 % G == 0 && (p->B == 1 || q.sb > 0) && (p->Hq == 1 || q.sh > 0) && (p->Nq == 1 || q.sn > 0)) {
+    if ((rc = encode_queries(encode, &k.tm_q, p, q, static_cast<int>(G), one)) != ATTN_OK) return rc;
+    k.q_map = one ? 1 : 2;
+  }
   k.q = q.p;
   k.q_sb = q.sb;
   k.q_sh = q.sh;
@@ -453,9 +490,10 @@ int attn_paged(const attn_paged_params* p) {
   k.G = static_cast<int>(G);
   k.prefix_len = p->prefix_len;
   k.prefix_tiles = (p->prefix_len + attn::kBN - 1) / attn::kBN;
-  k.prefix_tasks = p->prefix_len > 0 ? static_cast<int>(tasks_pre) : 0;
+  k.prefix_tasks = pl.batched ? static_cast<int>(tasks_pre) : 0;
   k.prefix_units = p->Hk * k.prefix_tasks * (k.prefix_tiles + attn::kPagedTaskCost);
   k.own_tasks = static_cast<int>(tasks_own);
+  k.by_heads = attn::FastDiv(static_cast<uint32_t>(p->Hk));
   k.by_g = attn::FastDiv(static_cast<uint32_t>(G));
   k.by_rows = attn::FastDiv(static_cast<uint32_t>(p->Nq * G));
   k.by_prefix_units = attn::FastDiv(static_cast<uint32_t>(k.prefix_tiles + attn::kPagedTaskCost));
@@ -464,10 +502,10 @@ int attn_paged(const attn_paged_params* p) {
   k.causal = p->mask_kind == ATTN_MASK_CAUSAL_BR;
   k.c = p->scale * 1.4426950408889634f;
   char* ws = static_cast<char*>(p->workspace);
-  k.starts = reinterpret_cast<int32_t*>(ws);
-  k.slots = reinterpret_cast<float*>(ws + pl.starts);
-  k.rows_o = reinterpret_cast<float*>(ws + pl.starts + pl.slots);
-  k.rows_ml = reinterpret_cast<float2*>(ws + pl.starts + pl.slots + pl.rows_o);
+  k.tasks = reinterpret_cast<int2*>(ws);
+  k.slots = reinterpret_cast<float*>(ws + pl.tasks);
+  k.rows_o = reinterpret_cast<float*>(ws + pl.tasks + pl.slots);
+  k.rows_ml = reinterpret_cast<float2*>(ws + pl.tasks + pl.slots + pl.rows_o);
   k.timeout_ns = p->timeout_ns ? p->timeout_ns : attn::host::kTimeoutNs;
   k.inject = p->inject;
   attn::host::paged_used(dev);

@@ -35,6 +35,7 @@ struct FastDiv {
 struct PagedParams {
   CUtensorMap tm_k;             // 4-D (d, slot, head, page) bf16 maps, box (swizzle span, min(page, 128), 1, 1)
   CUtensorMap tm_v;
+  CUtensorMap tm_q;             // 4-D (d, head, query, sequence); see q_map
   const void* q;                // bf16, element strides of b, h, n
   int64_t q_sb, q_sh, q_sn;
   void* o;
@@ -50,14 +51,19 @@ struct PagedParams {
   int page_shift;
   int max_len;                  // table_width * page size: longest own length that the table holds
   FastDiv by_g, by_rows;        // by G; by Nq * G, the rows of a sequence
+  FastDiv by_heads;             // by Hk
   FastDiv by_prefix_units;      // by the units of a prefix task
   FastDiv by_prefix_tasks;      // by the prefix tasks of a key head
-  int prefix_tiles, prefix_tasks, prefix_units;  // tiles of a task; tasks of a key head; units of all
+  int prefix_tiles;             // K/V tiles of the prefix
+  int prefix_tasks, prefix_units;  // batched prefix: tasks of a key head; units of all. 0: each
+                                // sequence's tasks go over the prefix's tiles themselves
   int own_tasks;                // tasks of a sequence for one key head
+  int q_map;                    // what a box of tm_q holds: 0 nothing (gather), 1 rows of several
+                                // sequences (prefix tasks of one query each), 2 rows of one
   int causal;                   // bottom-right causal over prefix and own keys together
   float c;                      // scale * log2(e)
   // workspace
-  int32_t* starts;              // [B + 1]: first unit of each sequence's tasks; the total
+  int2* tasks;                  // [B * Hk * own_tasks | Hk * prefix_tasks]: first CTA and parts of each
   float* slots;                 // per CTA 2 x 2 query tiles x 128 rows x (d + 2): parts of cut tasks
   float* rows_o;                // [2][B * Nq * Hq][d]: uncut prefix and own results
   float2* rows_ml;              // [2][B * Nq * Hq]: their running maximum (log2 units) and sum

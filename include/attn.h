@@ -481,7 +481,7 @@ typedef struct attn_paged_params {
 void attn_paged_params_init(attn_paged_params* p);
 int attn_paged(const attn_paged_params* p);
 /* Bytes of workspace on the current device, or a negative attn_status. Depends
- * on B, Hq, Nq, d, num_ctas and whether there is a prefix, not on lengths. */
+ * on the block's sizes and prefix_len, not on what kv_lens and q_lens hold. */
 int64_t attn_paged_workspace_bytes(const attn_paged_params* p);
 
 /* sizeof of attn_rope_params (0), attn_rope_bwd_params (1), attn_paged_params (2). */
