@@ -149,17 +149,20 @@ __device__ __forceinline__ int own_units(const PagedParams& p, SeqLens s) {
   return u;
 }
 
-// The split of U units over the CTAs that get some: CTA c starts at c U / n.
+// The split of U units over the CTAs that get some: U / n each, one more for
+// the first U mod n.
 struct Split {
-  int units, ctas;
-  __device__ __forceinline__ Split(int u, int grid) : units(u), ctas(max(1, min(grid, u / kPagedMinUnits))) {}
-  __device__ __forceinline__ int lo(int c) const {
-    return c >= ctas ? units : static_cast<int>(static_cast<int64_t>(c) * units / ctas);
+  int ctas, per, extra;
+  __device__ __forceinline__ Split(int u, int grid) : ctas(max(1, min(grid, u / kPagedMinUnits))) {
+    per = static_cast<int>(static_cast<uint32_t>(u) / static_cast<uint32_t>(ctas));
+    extra = u - per * ctas;
   }
+  __device__ __forceinline__ int lo(int c) const { return min(c, ctas) * per + min(c, extra); }
   __device__ __forceinline__ int owner(int u) const {  // the CTA whose range holds unit u
-    const uint64_t x = static_cast<uint64_t>(u + 1) * static_cast<uint32_t>(ctas) - 1;
-    return (x >> 32) == 0 ? static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(units))
-                          : static_cast<int>(x / static_cast<uint32_t>(units));
+    const int wide = extra * (per + 1);
+    const bool in = u < wide;
+    return (in ? 0 : extra) + static_cast<int>(static_cast<uint32_t>(in ? u : u - wide) /
+                                               static_cast<uint32_t>(in ? per + 1 : max(per, 1)));
   }
 };
 
@@ -172,13 +175,12 @@ struct PSegIter {
   int task, parts_end;  // of the segment: index in the task table; its last unit
 
   // u0: the CTA's first unit; b0, s0: the sequence that holds it (or the next) and its first unit.
-  __device__ __forceinline__ PSegIter(const PagedParams& p, int u0, int u1, int b0, int s0)
-      : u(u0), hi(u1), up(p.prefix_units), b(b0), sb(s0), ub(0) {
+  __device__ __forceinline__ PSegIter(const PagedParams& p, int u0, int u1, int b0, int s0, int ub0)
+      : u(u0), hi(u1), up(p.prefix_units), b(b0), sb(s0), ub(ub0) {
     cur.len = cur.ql = 0;
     nxt = cur;
     if (u < hi && b < p.B) {
       cur = seq_lens(p, b);
-      ub = own_units(p, cur);
       if (b + 1 < p.B) nxt = seq_lens(p, b + 1);
     }
   }
@@ -283,34 +285,44 @@ __device__ void paged_scheduler(const PagedParams& p, uint8_t* smem, const PBars
   using P = PCfg<D>;
   const int lane = threadIdx.x & 31;
   grid_dep_wait();  // lengths and tables are the previous kernel's to write
-  const int mine = lane < p.B ? p.Hk * own_units(p, seq_lens(p, lane)) : 0;  // of the first 32 sequences
-  int sum = mine;
-#pragma unroll 4
-  for (int b = lane + 32; b < p.B; b += 32) sum += p.Hk * own_units(p, seq_lens(p, b));
-  const Split split(p.prefix_units + __reduce_add_sync(0xffffffffu, sum), gridDim.x);
-  const int u0 = split.lo(blockIdx.x), u1 = split.lo(blockIdx.x + 1);
+  // (One loop for the total and the running sum, the divisions few: what bounds
+  // the start of a launch is fetching this code.)
+  int v = 0, sum = 0, u0 = 0, u1 = 0;
   int b0 = 0, s0 = p.prefix_units;  // the sequence that holds u0 (or the first behind it), its first unit
-  if (u0 < u1 && u0 >= p.prefix_units) {
-    for (;; b0 += 32) {
-      const int b = b0 + lane;
-      const int v = b0 == 0 ? mine : (b < p.B ? p.Hk * own_units(p, seq_lens(p, b)) : 0);
-      int inc = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      const uint32_t past = __ballot_sync(0xffffffffu, s0 + inc > u0);
-      if (past != 0u) {
-        const int at = __ffs(past) - 1;
-        s0 += __shfl_sync(0xffffffffu, inc - v, at);
-        b0 += at;
-        break;
-      }
-      s0 += __shfl_sync(0xffffffffu, inc, 31);
+  int ub = 0;                       // and its units per key head
+  Split split(0, 1);
+  for (int pass = 0, at = 0;; at += 32) {
+    if (at >= p.B) {
+      if (pass == 1) break;
+      pass = 1;
+      at = 0;
+      split = Split(p.prefix_units + p.Hk * __reduce_add_sync(0xffffffffu, sum), gridDim.x);
+      u0 = split.lo(blockIdx.x);
+      u1 = split.lo(blockIdx.x + 1);
+      if (u0 >= u1) break;
     }
+    if (pass == 0 || p.B > 32) v = at + lane < p.B ? own_units(p, seq_lens(p, at + lane)) : 0;
+    if (pass == 0) {
+      sum += v;
+      continue;
+    }
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const uint32_t past = __ballot_sync(0xffffffffu, s0 + p.Hk * inc > u0);
+    const int i = u0 < p.prefix_units ? 0 : __ffs(past) - 1;
+    if (i >= 0) {
+      s0 += p.Hk * __shfl_sync(0xffffffffu, inc - v, i);
+      ub = __shfl_sync(0xffffffffu, v, i);
+      b0 = at + i;
+      break;
+    }
+    s0 += p.Hk * __shfl_sync(0xffffffffu, inc, 31);
   }
-  PSegIter it(p, u0, u1, b0, s0);
+  PSegIter it(p, u0, u1, b0, s0, ub);
   RingPos<P::kSegs> r;
   for (bool more = true; more;) {
     PSeg s;
@@ -480,21 +492,17 @@ __device__ void paged_gather_q(const PagedParams& p, uint32_t sbase, uint8_t* sm
           src = static_cast<const __nv_bfloat16*>(p.q) + x.b * p.q_sb + static_cast<int64_t>(s.hk * p.G + x.g) * p.q_sh +
                 x.n * p.q_sn;
         }
-        // (the shuffles first: between the copies each would wait for the one before)
-        constexpr int kCopies = 32 / kRows;
-        unsigned long long from[kCopies];
-#pragma unroll
-        for (int j = 0; j < kCopies; ++j)
-          from[j] = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j * kRows + sub);
-#pragma unroll
-        for (int j = 0; j < kCopies; ++j) {
-          const int i = j * kRows + sub;  // row of the 32
+        const int m = min(32, n - i0);
+#pragma unroll 4
+        for (int j = 0; j < m; j += kRows) {
+          const int i = j + sub;  // row of the 32
+          const unsigned long long from = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i & 31);
           const int row = (i0 + i) % kBM;
           const int swz = C::kSwizzle == 128 ? ((c & 7) ^ (row & 7)) : (c ^ ((row >> 1) & 3));
           const uint32_t dst = sbase + P::kOffQ + ((i0 + i) / kBM) * C::kTileBytes +
                                (C::kSwizzle == 128 ? (c >> 3) * C::kChunkBytes : 0) + row * C::kSwizzle + swz * 16;
-          if (from[j] != 0)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from[j] + c * 16) : "memory");
+          if (i < m)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from + c * 16) : "memory");
         }
       }
     }
@@ -680,7 +688,8 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
   const uint32_t t_warm = lane_base + (D == 32 ? 320u : 256u) + 128u * static_cast<uint32_t>(h);
   s.rows = s.row0 = s.pt = s.k0 = s.len = s.flags = 0;
   s.k1 = 1;
-  for (uint32_t warm = opaque(1u);; warm = 0u) {
+  // (one warpgroup's four warps warm the four schedulers' caches)
+  for (uint32_t warm = opaque(h == 0 ? 1u : 0u);; warm = 0u) {
     // Keys that the row sees, the prefix's first. Lanes without a row see them
     // all: what they compute is never read, and they ask for no masking.
     int seen = kBN / 2;
