@@ -264,6 +264,26 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// 32 columns at each of two addresses of this thread's lane, one wait for both.
+__device__ __forceinline__ void tmem_ld32x2(uint32_t ta, uint32_t (&a)[32], uint32_t tb, uint32_t (&b)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, "
+      "%46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+        "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(a[16]),
+        "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]),
+        "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31]), "=r"(b[0]),
+        "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]),
+        "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15]), "=r"(b[16]), "=r"(b[17]),
+        "=r"(b[18]), "=r"(b[19]), "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]), "=r"(b[24]), "=r"(b[25]),
+        "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31])
+      : "r"(ta), "r"(tb)
+      : "memory");
+}
+
 // ------------------------------------------------------------------ roles
 
 // A lane's own TMA (each lane that calls it issues one copy).
@@ -629,42 +649,6 @@ __device__ __forceinline__ float* paged_slot(const PagedParams& p, int cta, bool
   return p.slots + (static_cast<int64_t>((2 * cta + (first ? 1 : 0)) * 2 + tile) * 4 + quarter) * 32 * (D + 2);
 }
 
-// Row of (b, key head, query, head of the group) in the row buffers and in the join.
-__device__ __forceinline__ int64_t row_index(const PagedParams& p, int b, int hk, int n, int g) {
-  return ((static_cast<int64_t>(b) * p.Hk + hk) * p.Nq + n) * p.G + g;
-}
-
-// Where one row of a finished (part of a) task goes.
-template <int D>
-struct RowSink {
-  float* part = nullptr;          // cut task: float4 i at part + 128 * i
-  float* buf = nullptr;           // uncut task with another part to join: row-major fp32
-  __nv_bfloat16* out = nullptr;   // the final result
-  float inv = 0.f;                // 1 / row sum (final result); 0: the row saw no key
-  __device__ __forceinline__ void put32(int ch, const float (&x)[32]) const {
-    if (part != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<float4*>(part + 128 * (ch * 8 + i)) =
-            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    } else if (buf != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        *reinterpret_cast<float4*>(buf + ch * 32 + 4 * i) =
-            make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
-    } else if (out != nullptr) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          w[j] = inv == 0.f ? 0u : pack_bf16(x[8 * i + 2 * j] * inv, x[8 * i + 2 * j + 1] * inv);
-        *reinterpret_cast<uint4*>(out + ch * 32 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    }
-  }
-};
-
 template <int D>
 __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D>& bars, uint32_t tmem,
                               const Ctl& ctl) {
@@ -689,6 +673,8 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
   s.rows = s.row0 = s.pt = s.k0 = s.len = s.flags = 0;
   s.k1 = 1;
   // (one warpgroup's four warps warm the four schedulers' caches)
+  int r = 0, bq = 0;   // the row inside its sequence's (queries x group) rows; the sequence
+  bool real = false;   // the lane has a row
   for (uint32_t warm = opaque(h == 0 ? 1u : 0u);; warm = 0u) {
     // Keys that the row sees, the prefix's first. Lanes without a row see them
     // all: what they compute is never read, and they ask for no masking.
@@ -697,20 +683,20 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
     if (warm == 0u) {
       grid_dep_wait();  // (returns at once after the first time)
       if (!segs.template take<kRoleSoftmax>(s, smem, bars, ctl)) return;
-      const int r = s.row0 + (s.twin() ? 0 : h * kBM) + row;
-      const bool real = r < s.rows;
-      seen = 1 << 30;
-      if (real) {
-        const RowPos x = row_pos(p, s, r);
-        SeqLens sl;
-        if (s.prefix()) {
-          sl = seq_lens(p, x.b);
-        } else {
-          sl.len = s.len;
-          sl.ql = s.ql;
-        }
-        seen = keys_seen(p, sl, x.n);
+      const int rs = p.Nq * p.G;
+      r = s.row0 + (s.twin() ? 0 : h * kBM) + row;
+      real = r < s.rows;
+      bq = s.b;
+      SeqLens sl;
+      sl.len = s.len;
+      sl.ql = s.ql;
+      if (s.prefix()) {
+        bq = p.by_rows.div(real ? r : s.row0);
+        r -= bq * rs;
+        if (p.row_limits) sl = seq_lens(p, bq);
       }
+      seen = 1 << 30;
+      if (real && p.row_limits) seen = keys_seen(p, sl, p.by_g.div(r));
       any = __any_sync(0xffffffffu, real && seen > 0);
     }
     const bool twin = s.twin();
@@ -836,58 +822,80 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
       o_par ^= 1u;
     }
     tc_fence_after();
-    RowSink<D> sink;
-    const int r = s.row0 + (twin ? 0 : h * kBM) + row;
-    const bool real = r < s.rows;
-    const RowPos x = row_pos(p, s, real ? r : s.row0);
     const bool none = m == -CUDART_INF_F;
     const bool lead = !twin || h == 0;  // writes the row's m and l
-    if (real) {
-      if (!s.whole()) {
-        float* base = paged_slot<D>(p, blockIdx.x, s.first(), twin ? 0 : h, quarter);
-        if (!none) sink.part = base + 4 * lane;
-        if (lead) {
-          base[32 * D + lane] = m;
-          base[32 * D + 32 + lane] = l;
-        }
-      } else if (p.prefix_tasks > 0) {
-        const int64_t rows = static_cast<int64_t>(p.B) * p.Nq * p.Hq;
-        const int64_t i = (s.prefix() ? 0 : rows) + row_index(p, x.b, s.hk, x.n, x.g);
-        if (!none) sink.buf = p.rows_o + i * D;
-        if (lead) p.rows_ml[i] = make_float2(m, l);
-      } else {
-        const int64_t head = s.hk * p.G + x.g;
-        sink.out = static_cast<__nv_bfloat16*>(p.o) + x.b * p.o_sb + head * p.o_sh + x.n * p.o_sn;
-        sink.inv = none ? 0.f : 1.f / l;
-        if (lead && p.lse != nullptr)
-          p.lse[(static_cast<int64_t>(x.b) * p.Hq + head) * p.Nq + x.n] =
-              none ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994530942f;
-      }
-    }
     const int n_ch = D / 32;
     const int ch0 = twin ? (h * n_ch + 1) / 2 : 0, ch1 = twin ? (h ? n_ch : (n_ch + 1) / 2) : n_ch;
-    const bool rows_here = __any_sync(0xffffffffu, real);
-    for (int ch = ch0; ch < ch1; ++ch) {
-      if (!rows_here) break;
-      __syncwarp();
-      uint32_t a[32];
-      float y[32];
-      if (twin) {
-        uint32_t b[32];
-        tmem_ld32(lane_base + C::tm_o(0) + ch * 32, a);
-        tmem_ld32(lane_base + C::tm_o(1) + ch * 32, b);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          // a stream without a key for this row is left out by a select: its O may never have been written
-          const float u = w0 > 0.f ? __uint_as_float(a[i]) * w0 : 0.f;
-          y[i] = w1 > 0.f ? fmaf(__uint_as_float(b[i]), w1, u) : u;
-        }
+    const bool direct = s.whole() && p.prefix_tasks == 0;
+    if (__any_sync(0xffffffffu, real)) {
+      // Where the row goes: its part of a cut task (float4 i at dst + 128 i), the
+      // buffer of uncut results (row-major), or the result.
+      float* dst = nullptr;
+      int step = 4;
+      __nv_bfloat16* out = nullptr;
+      float inv = 0.f;
+      if (direct) {
+        const int n = p.by_g.div(r);
+        const int head = s.hk * p.G + r - n * p.G;
+        if (real) out = static_cast<__nv_bfloat16*>(p.o) + bq * p.o_sb + head * p.o_sh + n * p.o_sn;
+        inv = none ? 0.f : 1.f / l;
+        if (real && lead && p.lse != nullptr)
+          p.lse[(static_cast<int64_t>(bq) * p.Hq + head) * p.Nq + n] =
+              none ? -CUDART_INF_F : (m + log2f(l)) * 0.69314718055994530942f;
       } else {
-        tmem_ld32(t_o + ch * 32, a);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(a[i]);
+        float *pm, *pl;
+        if (s.whole()) {
+          const int i = (bq * p.Hk + s.hk) * (p.Nq * p.G) + r + (s.prefix() ? 0 : p.B * p.Nq * p.Hq);
+          dst = p.rows_o + static_cast<int64_t>(i) * D;
+          pm = reinterpret_cast<float*>(p.rows_ml + i);
+          pl = pm + 1;
+        } else {
+          dst = paged_slot<D>(p, blockIdx.x, s.first(), twin ? 0 : h, quarter) + 4 * lane;
+          step = 128;
+          pm = dst - 3 * lane + 32 * D;
+          pl = pm + 32;
+        }
+        if (real && lead) {
+          *pm = m;
+          *pl = l;
+        }
+        if (!real || none) dst = nullptr;  // (a row that saw no key: its O is never read)
       }
-      sink.put32(ch, y);
+#pragma unroll 1
+      for (int ch = ch0; ch < ch1; ++ch) {
+        __syncwarp();
+        uint32_t a[32];
+        float y[32];
+        if (twin) {
+          uint32_t b[32];
+          tmem_ld32x2(lane_base + C::tm_o(0) + ch * 32, a, lane_base + C::tm_o(1) + ch * 32, b);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            // a stream without a key for this row is left out by a select: its O may never have been written
+            const float u = w0 > 0.f ? __uint_as_float(a[i]) * w0 : 0.f;
+            y[i] = w1 > 0.f ? fmaf(__uint_as_float(b[i]), w1, u) : u;
+          }
+        } else {
+          tmem_ld32(t_o + ch * 32, a);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(a[i]);
+        }
+        if (dst != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(dst + (ch * 8 + i) * step) =
+                make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        } else if (out != nullptr) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              w[j] = none ? 0u : pack_bf16(y[8 * i + 2 * j] * inv, y[8 * i + 2 * j + 1] * inv);
+            *reinterpret_cast<uint4*>(out + ch * 32 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
     }
     tc_fence_before();
     __syncwarp();
@@ -988,123 +996,143 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 
 // ------------------------------------------------------------------ joining the parts
 //
-// A warp per row. The parts of a row, in order: those of its prefix task, then
-// those of its own task; each is a slot of a CTA (cut task) or a row of the row
-// buffers (uncut). Lane i holds part i's maximum, sum and address; then the warp
-// goes over the parts, lane j adding float4 j of each.
-constexpr int kJoinWarps = 8;
+// The parts of a row, in order: those of its prefix task, then those of its own
+// task; each is a slot of a CTA (cut task) or a row of the row buffers (uncut).
+// A warp joins four rows, eight lanes a row: lane j of a row holds part j's
+// maximum, sum and address, and adds float4 j, j + 8, ... of every part. The
+// slots keep 32 rows' float4 side by side, so four neighbouring rows read whole
+// 64-byte pieces (one row a warp took 11 us for 20 parts of 2048 rows, 32 lines
+// a load).
+constexpr int kJoinWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kJoinWarps * 32, 2) paged_join_kernel(const __grid_constant__ PagedParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __grid_constant__ PagedParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   grid_dep_wait();
-  const int lane = threadIdx.x & 31;
+  constexpr int kJ = D / 32;    // float4 of a lane
+  constexpr int kBatch = 4;     // parts whose loads are in flight together
+  const int lane = threadIdx.x & 31, sub = lane >> 2, which = lane & 3;  // which of the four rows
   const int rows = p.B * p.Nq * p.Hq;  // below 2^30
-  const int row = static_cast<int>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5);
-  if (row >= rows) return;
-  const int rs = p.Nq * p.G;
-  const int bh = p.by_rows.div(row), r = row - bh * rs, b = p.by_heads.div(bh), hk = bh - b * p.Hk;
-  const int n = p.by_g.div(r), g = r - n * p.G;
+  // rows in the order (key head, sequence, query, head of the group): neighbours in the prefix's slots too
+  const int at = (static_cast<int>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5)) * 4 + which;
+  const bool live = at < rows;
+  const int rs = p.Nq * p.G, batch_rows = p.B * rs;
+  const int hk = live ? p.by_batch_rows.div(at) : 0, rp = live ? at - hk * batch_rows : 0;
+  const int b = p.by_rows.div(rp), r = rp - b * rs, bh = b * p.Hk + hk;
+  const int t = r / kPagedTaskRows, tp = rp / kPagedTaskRows;
+  const int row = bh * rs + r;  // in the row buffers
 
   // the row's two tasks: where their parts are, and the row inside the task
   struct Span {
     int c0, parts, in_task;  // parts 0: no key to see; 1: uncut
   };
   Span pre{0, 0, 0}, own{0, 0, 0};
-  const int t = r / kPagedTaskRows, rp = b * rs + r, tp = rp / kPagedTaskRows;
   const int2 at_own = p.tasks[bh * p.own_tasks + t];  // (written only if the task has a tile)
   if (p.prefix_tasks > 0) {
     const int2 e = p.tasks[p.B * p.Hk * p.own_tasks + hk * p.prefix_tasks + tp];
     pre = Span{e.x, e.y, rp - tp * kPagedTaskRows};
   }
   if (own_tiles(p, seq_lens(p, b), t).all > 0) own = Span{at_own.x, at_own.y, r - t * kPagedTaskRows};
-  if (p.prefix_tasks == 0 && own.parts == 1) return;  // written by the attention kernel
+  // an uncut row without a batched prefix was written by the attention kernel
+  const bool mine = live && !(p.prefix_tasks == 0 && own.parts == 1);
+  const int parts = mine ? pre.parts + own.parts : 0;
+  const int most = __reduce_max_sync(0xffffffffu, parts);
 
-  const int parts = pre.parts + own.parts;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[kJ];
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -CUDART_INF_F, L = 0.f;
-  constexpr int kBatch = 8;  // parts whose loads are in flight together
-  for (int base = 0; base < parts; base += 32) {
-    const int i = base + lane, count = min(32, parts - base);
-    const float* src = p.rows_o;  // float4 j of the row at src + j * step
-    const float* pm = nullptr;
+  for (int base = 0; base < most; base += 8) {
+    const int i = base + sub, count = parts - base;  // of this row, from here on
+    const float* src = p.slots;  // float4 j of the row at src + j * step
+    float m = -CUDART_INF_F, l = 0.f;
     int step = 4;
-    bool pair = false;            // m and l side by side
     if (i < parts) {
       const bool is_pre = i < pre.parts;
       const Span s = is_pre ? pre : own;
       const int k = is_pre ? i : i - pre.parts;
       if (s.parts == 1) {
-        const int64_t at = static_cast<int64_t>(is_pre ? 0 : rows) + row;
-        pm = reinterpret_cast<const float*>(p.rows_ml + at);
-        pair = true;
-        src = p.rows_o + at * D;
+        const int64_t x = static_cast<int64_t>(is_pre ? 0 : rows) + row;
+        const float2 ml = p.rows_ml[x];
+        m = ml.x;
+        l = ml.y;
+        src = p.rows_o + x * D;
       } else {
         const int quarter = (s.in_task % kBM) / 32, in_q = s.in_task % 32;
         const float* slot = paged_slot<D>(p, s.c0 + k, k == 0, s.in_task / kBM, quarter);
-        pm = slot + 32 * D + in_q;
+        m = slot[32 * D + in_q];
+        l = slot[32 * D + 32 + in_q];
         src = slot + 4 * in_q;
         step = 128;
       }
     }
-    float m = -CUDART_INF_F, l = 0.f;
-    if (pm != nullptr) {
-      m = pm[0];
-      l = pm[pair ? 1 : 32];
-    }
     // the first batch's data is asked for beside the maxima, before they are known
-    float4 v[kBatch];
+    float4 v[kBatch][kJ];
     auto fetch = [&](int j0) {
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const int j = min(j0 + u, count - 1);
-        const float* sj = reinterpret_cast<const float*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), j));
-        const int st = __shfl_sync(0xffffffffu, step, j);
-        if (j0 + u < count && lane < D / 4) v[u] = *reinterpret_cast<const float4*>(sj + lane * st);
+        const int holder = ((j0 + u) << 2) | which;
+        const float* su = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), holder));
+        const int st = __shfl_sync(0xffffffffu, step, holder);
+        if (j0 + u < count) {
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) v[u][j] = *reinterpret_cast<const float4*>(su + (sub + 8 * j) * st);
+        }
       }
     };
     fetch(0);
     float mx = m;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     const float M1 = fmaxf(M, mx);
     const float old = M == -CUDART_INF_F ? 0.f : ex2(M - M1);
     const float w = m == -CUDART_INF_F ? 0.f : ex2(m - M1);
-    acc.x *= old;
-    acc.y *= old;
-    acc.z *= old;
-    acc.w *= old;
     float lw = w > 0.f ? l * w : 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
+    for (int o = 4; o < 32; o <<= 1) lw += __shfl_xor_sync(0xffffffffu, lw, o);
     L = fmaf(L, old, lw);
     M = M1;
-    for (int j0 = 0; j0 < count; j0 += kBatch) {
-      if (j0 > 0) fetch(j0);
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      acc[j].x *= old;
+      acc[j].y *= old;
+      acc[j].z *= old;
+      acc[j].w *= old;
+    }
+#pragma unroll
+    for (int j0 = 0; j0 < 8; j0 += kBatch) {
+      if (j0 > 0 && base + j0 < most) fetch(j0);
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
-        const float wj = __shfl_sync(0xffffffffu, w, min(j0 + u, 31));
+        const float wu = __shfl_sync(0xffffffffu, w, ((j0 + u) << 2) | which);
         // a part that saw no key for this row never wrote its O: left out, not weighted by zero
-        if (j0 + u < count && wj > 0.f) {
-          acc.x = fmaf(v[u].x, wj, acc.x);
-          acc.y = fmaf(v[u].y, wj, acc.y);
-          acc.z = fmaf(v[u].z, wj, acc.z);
-          acc.w = fmaf(v[u].w, wj, acc.w);
+        if (j0 + u < count && wu > 0.f) {
+#pragma unroll
+          for (int j = 0; j < kJ; ++j) {
+            acc[j].x = fmaf(v[u][j].x, wu, acc[j].x);
+            acc[j].y = fmaf(v[u][j].y, wu, acc[j].y);
+            acc[j].z = fmaf(v[u][j].z, wu, acc[j].z);
+            acc[j].w = fmaf(v[u][j].w, wu, acc[j].w);
+          }
         }
       }
     }
   }
-  const int64_t head = hk * p.G + g;
-  const float inv = 1.f / L;
-  if (lane < D / 4) {
+  if (!mine) return;
+  const int n = p.by_g.div(r), head = hk * p.G + r - n * p.G;
+  const bool none = M == -CUDART_INF_F;
+  const float inv = none ? 0.f : 1.f / L;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + b * p.o_sb + head * p.o_sh + n * p.o_sn + sub * 4;
+#pragma unroll
+  for (int j = 0; j < kJ; ++j) {
     uint2 w = make_uint2(0u, 0u);
-    if (M != -CUDART_INF_F) w = make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + b * p.o_sb + head * p.o_sh + n * p.o_sn + lane * 4) = w;
+    if (!none) w = make_uint2(pack_bf16(acc[j].x * inv, acc[j].y * inv), pack_bf16(acc[j].z * inv, acc[j].w * inv));
+    *reinterpret_cast<uint2*>(out + 32 * j) = w;
   }
-  if (lane == 0 && p.lse != nullptr)
+  if (sub == 0 && p.lse != nullptr)
     p.lse[(static_cast<int64_t>(b) * p.Hq + head) * p.Nq + n] =
-        M == -CUDART_INF_F ? -CUDART_INF_F : (M + log2f(L)) * 0.69314718055994530942f;
+        none ? -CUDART_INF_F : (M + log2f(L)) * 0.69314718055994530942f;
 }
 
 template <int D>
@@ -1124,7 +1152,7 @@ cudaError_t launch_paged_dim(const PagedParams& p, int grid, cudaStream_t s) {
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, paged_kernel<D>, p)) != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.B) * p.Nq * p.Hq;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + 4 * kJoinWarps - 1) / (4 * kJoinWarps)));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
   return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p);

@@ -493,13 +493,14 @@ int attn_paged(const attn_paged_params* p) {
   k.prefix_tasks = pl.batched ? static_cast<int>(tasks_pre) : 0;
   k.prefix_units = p->Hk * k.prefix_tasks * (k.prefix_tiles + attn::kPagedTaskCost);
   k.own_tasks = static_cast<int>(tasks_own);
-  k.by_heads = attn::FastDiv(static_cast<uint32_t>(p->Hk));
+  k.by_batch_rows = attn::FastDiv(static_cast<uint32_t>(p->B * p->Nq * G));
   k.by_g = attn::FastDiv(static_cast<uint32_t>(G));
   k.by_rows = attn::FastDiv(static_cast<uint32_t>(p->Nq * G));
   k.by_prefix_units = attn::FastDiv(static_cast<uint32_t>(k.prefix_tiles + attn::kPagedTaskCost));
   k.by_prefix_tasks = attn::FastDiv(static_cast<uint32_t>(k.prefix_tasks > 0 ? k.prefix_tasks : 1));
   k.max_len = static_cast<int>(max_len);
   k.causal = p->mask_kind == ATTN_MASK_CAUSAL_BR;
+  k.row_limits = p->q_lens != nullptr || (k.causal && p->Nq > 1);
   k.c = p->scale * 1.4426950408889634f;
   char* ws = static_cast<char*>(p->workspace);
   k.tasks = reinterpret_cast<int2*>(ws);

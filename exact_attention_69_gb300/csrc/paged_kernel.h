@@ -51,7 +51,7 @@ struct PagedParams {
   int page_shift;
   int max_len;                  // table_width * page size: longest own length that the table holds
   FastDiv by_g, by_rows;        // by G; by Nq * G, the rows of a sequence
-  FastDiv by_heads;             // by Hk
+  FastDiv by_batch_rows;        // by B * Nq * G, the rows of a key head
   FastDiv by_prefix_units;      // by the units of a prefix task
   FastDiv by_prefix_tasks;      // by the prefix tasks of a key head
   int prefix_tiles;             // K/V tiles of the prefix
@@ -60,6 +60,7 @@ struct PagedParams {
   int own_tasks;                // tasks of a sequence for one key head
   int q_map;                    // what a box of tm_q holds: 0 nothing (gather), 1 rows of several
                                 // sequences (prefix tasks of one query each), 2 rows of one
+  int row_limits;               // rows of a sequence may see different numbers of keys
   int causal;                   // bottom-right causal over prefix and own keys together
   float c;                      // scale * log2(e)
   // workspace
