@@ -16,7 +16,6 @@ follows them. Scratch comes from PyTorch's allocator on the call's stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -39,28 +38,19 @@ def rope_freqs(rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
 
 def _heads(name, t, shape=None):
     """Checks a [B, H, N, d] bf16 CUDA tensor; returns its element strides (b, h, n)."""
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dim() != 4:
-        raise ValueError(f"{name} must have four dimensions")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have the shape {tuple(shape)}, not {tuple(t.shape)}")
-    st = t.stride()
-    if st[3] != 1:
+    a, b, c, last = t.stride()
+    if last != 1:
         raise ValueError(f"the last (head) dimension of {name} must be contiguous")
-    return _nonzero(st, t.shape)
-
-
-def _nonzero(st, shape):
-    # all-zero strides mean "contiguous" to the library: a tensor expanded in every
-    # dimension, or of one row, says d for one of them
-    a, b, c = st[0], st[1], st[2]
-    if not (a or b or c):
-        if shape[0] * shape[1] * shape[2] > 1:
-            raise ValueError("a tensor expanded in every dimension is not supported")
-        return (0, 0, shape[3])
+    if not (a or b or c):  # all-zero strides mean "contiguous" to the library
+        if t.shape[:3].numel() > 1:
+            raise ValueError(f"{name} is expanded in every dimension")
+        return (0, 0, t.shape[3])
     return (a, b, c)
 
 
@@ -127,23 +117,23 @@ def _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, posit
     p.pos_offset = int(position_offset)
 
 
-@contextlib.contextmanager
-def _on(device, stream, tensors):
-    """Makes the tensors' device and the call's stream current, so that outputs and
-    scratch come from that stream's memory; yields the stream's handle. Inputs on another
+def _on(device, stream, tensors, run):
+    """run(handle) with the tensors' device and the call's stream current, so that
+    outputs and scratch come from that stream's memory. Inputs of a call on another
     stream than the current one are held for it until its work so far is done."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return run(torch._C._cuda_getCurrentRawStream(device.index))
     with torch.cuda.device(device):
-        current = torch.cuda.current_stream(device)
-        if stream is None or stream == current:
-            yield current.cuda_stream
-            return
+        if stream is None or stream == torch.cuda.current_stream(device):
+            return run(torch.cuda.current_stream(device).cuda_stream)
         if stream.device != device:
             raise ValueError(f"the stream must be on {device}")
         with torch.cuda.stream(stream):
-            yield stream.cuda_stream
+            out = run(stream.cuda_stream)
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)
+        return out
 
 
 def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None = None,
@@ -177,19 +167,26 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Te
         raise ValueError("k_weight and k_out need k")
     _same_device(q.device, k=k, q_out=q_out, k_out=k_out)
     _set_rope(p, B, N, d, q.device, q_weight, k_weight, inv_freq, positions, position_offset, interleaved, eps)
-    with _on(q.device, stream, (q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out)) as handle:
-        if q_out is None:
-            q_out = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
-        p.q_out_stride[:] = _heads("q_out", q_out, (B, Hq, N, d))
-        p.q_out = q_out.data_ptr()
+    if q_out is not None:
+        p.q_out_stride[:] = _heads("q_out", q_out, q.shape)
+    if k_out is not None:
+        p.k_out_stride[:] = _heads("k_out", k_out, k.shape)
+
+    def run(handle):  # (outputs that are made here are contiguous: strides of zero)
+        qo = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
+        p.q_out = qo.data_ptr()
+        ko = k_out
         if k is not None:
-            if k_out is None:
-                k_out = torch.empty((B, p.Hk, N, d), dtype=torch.bfloat16, device=q.device)
-            p.k_out_stride[:] = _heads("k_out", k_out, (B, p.Hk, N, d))
-            p.k_out = k_out.data_ptr()
+            if ko is None:
+                ko = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
+            p.k_out = ko.data_ptr()
         p.stream = handle
-        _lib.check(_lib.load().attn_qk_norm_rope(ctypes.byref(p)), "qk_norm_rope")
-    return q_out, k_out
+        code = _lib.load().attn_qk_norm_rope(ctypes.byref(p))
+        if code:
+            _lib.check(code, "qk_norm_rope")
+        return qo, ko
+
+    return _on(q.device, stream, (q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out), run)
 
 
 def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tensor,
@@ -223,12 +220,13 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tens
         raise ValueError("k_weight needs k")
     _same_device(q.device, k=k, dq_out=dq_out, dk_out=dk_out)
     _set_rope(p, B, N, d, q.device, q_weight, k_weight, inv_freq, positions, position_offset, interleaved, eps)
-    dk = dwq = dwk = ws = None
-    with _on(q.device, stream, (q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions)) as handle:
-        dq = torch.empty((B, Hq, N, d), dtype=torch.bfloat16, device=q.device)
+
+    def run(handle):
+        dk = dwq = dwk = None
+        dq = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
         p.dq = dq.data_ptr()
         if k is not None:
-            dk = torch.empty((B, p.Hk, N, d), dtype=torch.bfloat16, device=q.device)
+            dk = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
             p.dk = dk.data_ptr()
         if weight_grads and q_weight is not None:
             dwq = torch.empty_like(q_weight)
@@ -237,15 +235,19 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tens
             dwk = torch.empty_like(k_weight)
             p.dk_weight = dwk.data_ptr()
         lib = _lib.load()
-        n = lib.attn_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(p))
-        if n < 0:
-            _lib.check(int(-n), "qk_norm_rope_bwd")
-        if n > 0:
+        if dwq is not None or dwk is not None:
+            n = lib.attn_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(p))
+            if n < 0:
+                _lib.check(int(-n), "qk_norm_rope_bwd")
             ws = torch.empty(n, dtype=torch.uint8, device=q.device)
             p.workspace, p.workspace_bytes = ws.data_ptr(), n
         p.stream = handle
-        _lib.check(lib.attn_qk_norm_rope_bwd(ctypes.byref(p)), "qk_norm_rope_bwd")
-    return dq, dk, dwq, dwk
+        code = lib.attn_qk_norm_rope_bwd(ctypes.byref(p))
+        if code:
+            _lib.check(code, "qk_norm_rope_bwd")
+        return dq, dk, dwq, dwk
+
+    return _on(q.device, stream, (q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions), run)
 
 
 class _QkNormRope(torch.autograd.Function):
@@ -349,16 +351,23 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     elif q_weight is not None or q_out is not None:
         raise ValueError("q_weight and q_out need q")
     _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, position_offset, interleaved, eps)
-    with _on(device, stream, (k, v, k_cache, v_cache, block_table, starts, counts, positions, inv_freq, k_weight, q,
-                              q_weight, q_out)) as handle:
+    if q_out is not None:
+        p.q_out_stride[:] = _heads("q_out", q_out, q.shape)
+
+    def run(handle):
+        qo = q_out
         if q is not None:
-            if q_out is None:
-                q_out = torch.empty((B, p.Hq, N, d), dtype=torch.bfloat16, device=device)
-            p.q_out_stride[:] = _heads("q_out", q_out, (B, p.Hq, N, d))
-            p.q_out = q_out.data_ptr()
+            if qo is None:
+                qo = torch.empty(q.shape, dtype=torch.bfloat16, device=device)
+            p.q_out = qo.data_ptr()
         p.stream = handle
-        _lib.check(_lib.load().attn_kv_append(ctypes.byref(p)), "kv_append")
-    return q_out
+        code = _lib.load().attn_kv_append(ctypes.byref(p))
+        if code:
+            _lib.check(code, "kv_append")
+        return qo
+
+    return _on(device, stream, (k, v, k_cache, v_cache, block_table, starts, counts, positions, inv_freq, k_weight, q,
+                                q_weight, q_out), run)
 
 
 _PAGED_MASKS = {"none": _lib.ATTN_MASK_NONE, "causal_br": _lib.ATTN_MASK_CAUSAL_BR}
@@ -411,15 +420,17 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     _same_device(device, out=out, lse=lse)
     if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, Hq, Nq)):
         raise ValueError("lse must be a contiguous float32 [B, Hq, Nq] tensor")
-    with _on(device, stream, (q, k_cache, v_cache, block_table, kv_lens, q_lens, prefix_table, out, lse)) as handle:
-        if out is None:
-            out = torch.empty((B, Hq, Nq, d), dtype=torch.bfloat16, device=device)
-        p.o_stride[:] = _heads("out", out, (B, Hq, Nq, d))
-        p.o = out.data_ptr()
-        if lse is None and return_lse:
-            lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
-        if lse is not None:
-            p.lse = lse.data_ptr()
+    if out is not None:
+        p.o_stride[:] = _heads("out", out, q.shape)
+
+    def run(handle):
+        o = torch.empty(q.shape, dtype=torch.bfloat16, device=device) if out is None else out
+        p.o = o.data_ptr()
+        z = lse
+        if z is None and return_lse:
+            z = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
+        if z is not None:
+            p.lse = z.data_ptr()
         lib = _lib.load()
         n = lib.attn_paged_workspace_bytes(ctypes.byref(p))
         if n < 0:
@@ -427,5 +438,9 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
         ws = torch.empty(n, dtype=torch.uint8, device=device)
         p.workspace, p.workspace_bytes = ws.data_ptr(), n
         p.stream = handle
-        _lib.check(lib.attn_paged(ctypes.byref(p)), "attn_paged")
-    return (out, lse) if return_lse else out
+        code = lib.attn_paged(ctypes.byref(p))
+        if code:
+            _lib.check(code, "attn_paged")
+        return (o, z) if return_lse else o
+
+    return _on(device, stream, (q, k_cache, v_cache, block_table, kv_lens, q_lens, prefix_table, out, lse), run)

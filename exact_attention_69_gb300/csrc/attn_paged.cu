@@ -311,6 +311,10 @@ __device__ void paged_scheduler(const PagedParams& p, uint8_t* smem, const PBars
   int b0 = 0, s0 = p.prefix_units;  // the sequence that holds u0 (or the first behind it), its first unit
   int ub = 0;                       // and its units per key head
   Split split(0, 1);
+  SeqLens first[4];                 // of the first 128 sequences, all asked for at once
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (32 * j + lane < p.B) first[j] = seq_lens(p, 32 * j + lane);
   for (int pass = 0, at = 0;; at += 32) {
     if (at >= p.B) {
       if (pass == 1) break;
@@ -321,7 +325,11 @@ __device__ void paged_scheduler(const PagedParams& p, uint8_t* smem, const PBars
       u1 = split.lo(blockIdx.x + 1);
       if (u0 >= u1) break;
     }
-    if (pass == 0 || p.B > 32) v = at + lane < p.B ? own_units(p, seq_lens(p, at + lane)) : 0;
+    if (pass == 0 || p.B > 32) {
+      SeqLens sl = first[0];
+      if (at > 0) sl = at == 32 ? first[1] : at == 64 ? first[2] : at == 96 ? first[3] : seq_lens(p, min(at + lane, p.B - 1));
+      v = at + lane < p.B ? own_units(p, sl) : 0;
+    }
     if (pass == 0) {
       sum += v;
       continue;
@@ -665,69 +673,35 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
   uint32_t ring = 0;  // K and V tiles that the CTA took before this segment: the ring's position
   SegReader<D> segs;
   PSeg s;
-  // Round 0 runs the tile code once on whatever TMEM holds, while the first
-  // queries and keys are on their way: nothing is announced, P goes to columns
-  // that no product uses yet, and the real first tile finds its instructions
-  // fetched (they took ~3000 cycles of it).
-  const uint32_t t_warm = lane_base + (D == 32 ? 320u : 256u) + 128u * static_cast<uint32_t>(h);
-  s.rows = s.row0 = s.pt = s.k0 = s.len = s.flags = 0;
-  s.k1 = 1;
-  // (one warpgroup's four warps warm the four schedulers' caches)
-  int r = 0, bq = 0;   // the row inside its sequence's (queries x group) rows; the sequence
-  bool real = false;   // the lane has a row
-  for (uint32_t warm = opaque(h == 0 ? 1u : 0u);; warm = 0u) {
+  grid_dep_wait();
+  while (segs.template take<kRoleSoftmax>(s, smem, bars, ctl)) {
+    // the row inside its sequence's (queries x group) rows; the sequence; the lane has a row
+    const int rs = p.Nq * p.G;
+    int r = s.row0 + (s.twin() ? 0 : h * kBM) + row, bq = s.b;
+    const bool real = r < s.rows;
+    SeqLens sl;
+    sl.len = s.len;
+    sl.ql = s.ql;
+    if (s.prefix()) {
+      bq = p.by_rows.div(real ? r : s.row0);
+      r -= bq * rs;
+      if (p.row_limits) sl = seq_lens(p, bq);
+    }
     // Keys that the row sees, the prefix's first. Lanes without a row see them
     // all: what they compute is never read, and they ask for no masking.
-    int seen = kBN / 2;
-    bool any = true;
-    if (warm == 0u) {
-      grid_dep_wait();  // (returns at once after the first time)
-      if (!segs.template take<kRoleSoftmax>(s, smem, bars, ctl)) return;
-      const int rs = p.Nq * p.G;
-      r = s.row0 + (s.twin() ? 0 : h * kBM) + row;
-      real = r < s.rows;
-      bq = s.b;
-      SeqLens sl;
-      sl.len = s.len;
-      sl.ql = s.ql;
-      if (s.prefix()) {
-        bq = p.by_rows.div(real ? r : s.row0);
-        r -= bq * rs;
-        if (p.row_limits) sl = seq_lens(p, bq);
-      }
-      seen = 1 << 30;
-      if (real && p.row_limits) seen = keys_seen(p, sl, p.by_g.div(r));
-      any = __any_sync(0xffffffffu, real && seen > 0);
-    }
+    int seen = 1 << 30;
+    if (real && p.row_limits) seen = keys_seen(p, sl, p.by_g.div(r));
+    const bool any = __any_sync(0xffffffffu, real && seen > 0);
     const bool twin = s.twin();
     float m_ref = -CUDART_INF_F, l = 0.f;
     bool first = true;
     for (int k = s.k0 + (twin ? h : 0); k < s.k1; k += twin ? 2 : 1) {
       // the tile's first key among the prefix's or the own keys, and how many of those there are
       const int base = (k < s.pt ? k : k - s.pt) * kBN, end = k < s.pt ? p.prefix_len : s.len;
-      if (warm == 0u) {
-        if (!warp_wait(bars.s_full(h), s_par, ctl, k)) return;
-        s_par ^= 1u;
-        tc_fence_after();
-        if (base + kBN > end) {
-          // The last tile of the prefix or of the own keys: V rows behind their
-          // end become zero. (After s_full: this tile's S went out behind
-          // whatever held the V's stage before, so `full` is in this tile's
-          // phase or past it, and the parity below cannot match an older one.)
-          const int i = k - s.k0, n = s.k1 - s.k0, ahead = min(tiles_ahead(s), n);
-          const uint32_t at = ring + static_cast<uint32_t>(ahead + i + min(i, n - ahead));
-          const int st = static_cast<int>(at % P::kStages);
-          if (!warp_wait(bars.full(st), (at / P::kStages) & 1u, ctl, k)) return;
-          const int z0 = max(end - base, quarter * 32), z1 = quarter * 32 + 32;
-          for (int ch = 0; ch < C::kChunks; ++ch) {
-            uint8_t* v = smem + P::kOffKV + st * C::kTileBytes + ch * C::kChunkBytes;
-            for (int i2 = z0 * C::kSwizzle + lane * 16; i2 < z1 * C::kSwizzle; i2 += 512)
-              *reinterpret_cast<uint4*>(v + i2) = make_uint4(0, 0, 0, 0);
-          }
-          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-          __syncwarp();
-        }
-      }
+      if (!warp_wait(bars.s_full(h), s_par, ctl, k)) return;
+      s_par ^= 1u;
+      tc_fence_after();
+      const bool tail = base + kBN > end;
       if (any) {
         // one tile of scores: mask, running maximum and sum, P as bf16 over S in two
         // halves, each announced on its own barrier
@@ -768,29 +742,45 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
-            if (lane == 0 && warm == 0u) mbar_arrive(bars.p_full(h, 0));
+            if (lane == 0 && !tail) mbar_arrive(bars.p_full(h, 0));
           }
-          tmem_st32((warm ? t_warm : t_p) + 32 * part, pk);
+          tmem_st32(t_p + 32 * part, pk);
         }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0 && warm == 0u) mbar_arrive(bars.p_full(h, 1));
+        if (lane == 0 && !tail) mbar_arrive(bars.p_full(h, 1));
         const float2 sa = __fadd2_rn(sum4[0], sum4[1]), sb = __fadd2_rn(sum4[2], sum4[3]);
         l += (sa.x + sa.y) + (sb.x + sb.y);
-      } else {
+      } else if (!tail) {
         // no row of this warp sees a key of the task: its P and O are never read
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(bars.p_full(h, 0));
-          mbar_arrive(bars.p_full(h, 1));
+        if (lane < 2) mbar_arrive(bars.p_full(h, lane));
+      }
+      if (tail) {
+        // The last tile of the prefix or of the own keys: V rows behind their end
+        // become zero before P is announced. (After s_full: this tile's S went
+        // out behind whatever held the V's stage before, so `full` is in this
+        // tile's phase or past it, and the parity below cannot match an older one.)
+        const int i = k - s.k0, n = s.k1 - s.k0, ahead = min(tiles_ahead(s), n);
+        const uint32_t at = ring + static_cast<uint32_t>(ahead + i + min(i, n - ahead));
+        const int st = static_cast<int>(at % P::kStages);
+        if (!warp_wait(bars.full(st), (at / P::kStages) & 1u, ctl, k)) return;
+        const int z0 = max(end - base, quarter * 32), z1 = quarter * 32 + 32;
+        for (int ch = 0; ch < C::kChunks; ++ch) {
+          uint8_t* v = smem + P::kOffKV + st * C::kTileBytes + ch * C::kChunkBytes;
+          for (int i2 = z0 * C::kSwizzle + lane * 16; i2 < z1 * C::kSwizzle; i2 += 512)
+            *reinterpret_cast<uint4*>(v + i2) = make_uint4(0, 0, 0, 0);
         }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane < 2) mbar_arrive(bars.p_full(h, lane));
       }
       first = false;
     }
 
-    if (warm) continue;
     ring += 2u * static_cast<uint32_t>(s.k1 - s.k0);
 
     // the end of the segment: O of this row, to its part, its buffer or the result
@@ -869,11 +859,12 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
         if (twin) {
           uint32_t b[32];
           tmem_ld32x2(lane_base + C::tm_o(0) + ch * 32, a, lane_base + C::tm_o(1) + ch * 32, b);
+          if (s.k1 - s.k0 > 1) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            // a stream without a key for this row is left out by a select: its O may never have been written
-            const float u = w0 > 0.f ? __uint_as_float(a[i]) * w0 : 0.f;
-            y[i] = w1 > 0.f ? fmaf(__uint_as_float(b[i]), w1, u) : u;
+            for (int i = 0; i < 32; ++i) y[i] = fmaf(__uint_as_float(b[i]), w1, __uint_as_float(a[i]) * w0);
+          } else {  // stream 1 had no tile: its O was not written
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(a[i]);
           }
         } else {
           tmem_ld32(t_o + ch * 32, a);
@@ -965,9 +956,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Ctl ctl{abort_flag, g_paged_status, p.timeout_ns};
-  // So far and in the softmax warps' round 0 only shared memory and TMEM are
-  // touched; every role waits for the previous kernel on the stream before its
-  // first global access.
+  // So far only shared memory and TMEM are touched; every role waits for the
+  // previous kernel on the stream before its first global access.
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp < 4) {

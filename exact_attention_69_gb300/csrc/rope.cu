@@ -4,13 +4,16 @@
 //   y = R(pos) (x * r * w),  r = 1 / sqrt(mean(x^2) + eps)
 // with R turning each pair of the first `rot` channels by pos * inv_freq.
 //
-// What bounds it: each row is read once and written once and a row has ~10
-// operations an element, so device memory. A row of d channels is d/8 threads
-// of 16 bytes each, so a warp reads 512 contiguous bytes of rows; the row sum
-// and the exchange with the pair's other half (raw bf16, four words) are warp
-// shuffles and nothing is staged. A thread keeps one token and one channel
-// chunk and goes over the heads: its cosines and sines are computed once and
-// stay in registers. Loads of four heads are in flight at a time.
+// What bounds it: each row is read once and written once, so device memory; but
+// an SM moves only 23 bytes a clock, so it has some 20 instructions for each 16
+// bytes read before the arithmetic shows. A row of d channels is d/8 threads of
+// 16 bytes each, so a warp reads 512 contiguous bytes of rows; the row sum and the
+// exchange with the pair's other half (raw bf16, four words) are warp shuffles. A
+// thread keeps one token and one channel chunk and goes over the heads, and
+// weights, cosines and sines are folded into two factors a channel that stay in
+// registers: y = r (x A + x' B), packed two channels an instruction. The block's
+// angles are computed once, into shared memory (a thread for each was half of the
+// time with 16 heads). Loads of four heads are in flight at a time.
 //
 // Angles: a frequency becomes a 64-bit fraction of a turn, and position times
 // frequency is a 64-bit integer product whose overflow drops whole turns. The
@@ -60,31 +63,35 @@ __device__ __forceinline__ void angle(int64_t pos, uint64_t turns, float& c, flo
   sincospif(half_turns, &s, &c);
 }
 
-__device__ __forceinline__ void unpack(const uint4& u, float (&x)[8]) {
+__device__ __forceinline__ void unpack(const uint4& u, float2 (&x)[4]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < 4; ++i) x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
 }
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+__device__ __forceinline__ uint32_t pack2(float2 x) {
   uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(x.y), "f"(x.x));
   return r;
 }
 
-__device__ __forceinline__ uint4 pack(const float (&x)[8]) {
-  return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+__device__ __forceinline__ uint4 pack(const float2 (&x)[4]) {
+  return make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
 }
 
-__device__ __forceinline__ void load_weights(const void* w, int type, int at, float (&out)[8]) {
+__device__ __forceinline__ void load_weights(const void* w, int type, int at, float2 (&out)[4]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    out[i] = w == nullptr ? 1.f
-             : type == 1  ? static_cast<const float*>(w)[at + i]
-                          : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[at + i]);
+  for (int i = 0; i < 4; ++i) {
+    const int j = at + 2 * i;
+    if (w == nullptr) {
+      out[i] = make_float2(1.f, 1.f);
+    } else if (type == 1) {
+      out[i] = make_float2(static_cast<const float*>(w)[j], static_cast<const float*>(w)[j + 1]);
+    } else {
+      const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(w) + j;
+      out[i] = make_float2(__bfloat162float(x[0]), __bfloat162float(x[1]));
+    }
+  }
 }
 
 // Sum over the d/8 threads of a row.
@@ -100,20 +107,53 @@ __device__ __forceinline__ int64_t position(const void* pos, int type, int64_t s
   return type == 1 ? static_cast<const int32_t*>(pos)[at] : static_cast<const int64_t*>(pos)[at];
 }
 
-// A thread's place in its row and its angles. Half-split pairs (IL false):
-// channel i turns with channel i + rot/2, held by the thread rot/16 chunks
-// away; side by side (IL true): both channels of a pair are the thread's own.
+// cos and sin of the block's tokens, [token slot][frequency].
+template <int D>
+struct Angles {
+  static constexpr int kTokens = rope_tokens_per_block(D);
+  uint64_t turns[D / 2];
+  int64_t pos[kTokens];
+  float2 cs[kTokens * (D / 2)];
+};
+
+// Fills the table for tokens t0 ... of B * N (all threads; P: either parameter block).
+template <int D, typename P>
+__device__ __forceinline__ void fill_angles(Angles<D>& a, const P& p, int64_t t0, int64_t total, const int32_t* starts,
+                                            bool first) {
+  constexpr int kT = Angles<D>::kTokens;
+  const int n_f = p.rot / 2;
+  if (n_f == 0) return;
+  __syncthreads();
+  if (first)
+    for (int i = threadIdx.x; i < n_f; i += kRopeThreads) a.turns[i] = turns_of(p.inv_freq[i]);
+  if (threadIdx.x < kT && t0 + threadIdx.x < total) {
+    const int64_t tok = t0 + threadIdx.x;
+    const int b = static_cast<int>(tok / p.N), n = static_cast<int>(tok - static_cast<int64_t>(b) * p.N);
+    a.pos[threadIdx.x] = p.pos != nullptr ? position(p.pos, p.pos_type, p.pos_sb, p.pos_sn, b, n)
+                                          : p.pos_offset + n + (starts != nullptr ? starts[b] : 0);
+  }
+  __syncthreads();
+  const int live = static_cast<int>(min(static_cast<int64_t>(kT), total - t0)) * n_f;
+  for (int i = threadIdx.x; i < live; i += kRopeThreads) {
+    const int tok = i / n_f, f = i - tok * n_f;
+    float2 x;
+    angle(a.pos[tok], a.turns[f], x.x, x.y);
+    a.cs[tok * (D / 2) + f] = x;
+  }
+  __syncthreads();
+}
+
+// A thread's place in its row. Half-split pairs (IL false): channel i turns with
+// channel i + rot/2, held by the thread rot/16 chunks away; side by side (IL
+// true): both channels of a pair are the thread's own.
 template <int D, bool IL>
-struct Turn {
-  static constexpr int kN = IL ? 4 : 8;
+struct Place {
   int c;         // chunk of 8 channels
   bool on;       // the chunk is rotated
   bool low;      // half-split: the first half of the pairs
   int partner;   // half-split: lane of the other half
   int pchunk;    // half-split: its chunk
-  float cs[kN], sn[kN];
-
-  __device__ __forceinline__ Turn(int rot) {
+  __device__ __forceinline__ explicit Place(int rot) {
     c = threadIdx.x % (D / 8);
     const int lane = threadIdx.x & 31, hc = rot / 16;
     on = c * 8 < rot;
@@ -121,41 +161,51 @@ struct Turn {
     pchunk = (!IL && on) ? (low ? c + hc : c - hc) : c;
     partner = lane + (pchunk - c);
   }
-  __device__ __forceinline__ void set(int64_t pos, const uint64_t* turns) {
-    const int f0 = IL ? c * 4 : (low ? c : pchunk) * 8;
+  // The rotation as factors of the own and the paired channel, y = x A + x' B.
+  __device__ __forceinline__ void factors(const float2* cs, float2 (&A)[4], float2 (&B)[4]) const {
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      cs[i] = 1.f;
-      sn[i] = 0.f;
-      if (on) angle(pos, turns[f0 + i], cs[i], sn[i]);
-      if (!IL && low) sn[i] = -sn[i];
+    for (int i = 0; i < 4; ++i) {
+      A[i] = make_float2(1.f, 1.f);
+      B[i] = make_float2(0.f, 0.f);
     }
-  }
-  // y = R x (sign 1) or R^T x (sign -1); other: the partner's values (half-split).
-  __device__ __forceinline__ void apply(float (&x)[8], const float (&other)[8], float sign) const {
     if (!on) return;
     if constexpr (IL) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float a = x[2 * i], b = x[2 * i + 1], s = sign * sn[i];
-        x[2 * i] = a * cs[i] - b * s;
-        x[2 * i + 1] = b * cs[i] + a * s;
+        const float2 x = cs[c * 4 + i];
+        A[i] = make_float2(x.x, x.x);
+        B[i] = make_float2(-x.y, x.y);
       }
     } else {
+      const float2* f = cs + (low ? c : pchunk) * 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) x[i] = x[i] * cs[i] + other[i] * (sign * sn[i]);
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = f[2 * i], y = f[2 * i + 1];
+        A[i] = make_float2(x.x, y.x);
+        B[i] = low ? make_float2(-x.y, -y.y) : make_float2(x.y, y.y);
+      }
     }
   }
-  // The partner's raw chunk (all 32 lanes call it).
-  __device__ __forceinline__ uint4 exchange(const uint4& u) const {
+  // The paired channels of the thread's chunk; zeros where it is not rotated (an
+  // infinity there must not meet the factor 0). All 32 lanes call it.
+  __device__ __forceinline__ void paired(const uint4& u, const float2 (&x)[4], float2 (&o)[4]) const {
     if constexpr (IL) {
-      return u;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = make_float2(x[i].y, x[i].x);
     } else {
-      return make_uint4(__shfl_sync(0xffffffffu, u.x, partner), __shfl_sync(0xffffffffu, u.y, partner),
-                        __shfl_sync(0xffffffffu, u.z, partner), __shfl_sync(0xffffffffu, u.w, partner));
+      uint4 w = make_uint4(__shfl_sync(0xffffffffu, u.x, partner), __shfl_sync(0xffffffffu, u.y, partner),
+                           __shfl_sync(0xffffffffu, u.z, partner), __shfl_sync(0xffffffffu, u.w, partner));
+      unpack(w, o);
+    }
+    if (!on) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = make_float2(0.f, 0.f);
     }
   }
 };
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
 
 __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
   return __ldcs(reinterpret_cast<const uint4*>(p));
@@ -164,15 +214,24 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const uint4& u) { *rei
 
 // Heads [h0, h1) of one token: norm, turn, store. in/out: the token's first
 // head at this thread's channels. Every lane of the warp goes through the
-// same heads; `live` and `write` say whose loads and stores are real.
+// same heads; `live` says whether its loads and stores are real.
 template <int D, bool IL, bool NORM>
 __device__ __forceinline__ void rope_heads(const __nv_bfloat16* in, int64_t in_sh, __nv_bfloat16* out,
-                                           int64_t out_sh, int h0, int h1, bool live, bool write,
-                                           const void* w, int w_type, float eps, const Turn<D, IL>& t) {
-  float wo[8], wp[8];
+                                           int64_t out_sh, int h0, int h1, bool live, const void* w, int w_type,
+                                           float eps, const Place<D, IL>& pl, const float2* cs) {
+  float2 A[4], B[4];
+  pl.factors(cs, A, B);
   if constexpr (NORM) {
-    load_weights(w, w_type, t.c * 8, wo);
-    load_weights(w, w_type, t.pchunk * 8, wp);
+    if (w != nullptr) {
+      float2 wo[4], wp[4];
+      load_weights(w, w_type, pl.c * 8, wo);
+      load_weights(w, w_type, pl.pchunk * 8, wp);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        A[i] = mul2(A[i], wo[i]);
+        B[i] = mul2(B[i], IL ? make_float2(wo[i].y, wo[i].x) : wp[i]);
+      }
+    }
   }
   for (int h = h0; h < h1; h += kUnroll) {
     uint4 raw[kUnroll];
@@ -184,55 +243,56 @@ __device__ __forceinline__ void rope_heads(const __nv_bfloat16* in, int64_t in_s
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (h + u >= h1) break;  // the same for the whole block
-      float x[8], o[8];
+      float2 x[4], o[4];
       unpack(raw[u], x);
-      unpack(t.exchange(raw[u]), o);
+      pl.paired(raw[u], x, o);
+      float2 r2 = make_float2(1.f, 1.f);
       if constexpr (NORM) {
-        float ss = 0.f;
+        float2 s = mul2(x[0], x[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-        const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          x[i] *= r * wo[i];
-          o[i] *= r * wp[i];
-        }
+        for (int i = 1; i < 4; ++i) s = fma2(x[i], x[i], s);
+        const float r = rsqrtf(row_sum<D>(s.x + s.y) * (1.f / D) + eps);
+        r2 = make_float2(r, r);
       }
-      t.apply(x, o, 1.f);
-      if (write) store16(out + (h + u) * out_sh, pack(x));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        x[i] = fma2(x[i], A[i], mul2(o[i], B[i]));
+        if constexpr (NORM) x[i] = mul2(x[i], r2);
+      }
+      if (live) store16(out + (h + u) * out_sh, pack(x));
     }
   }
 }
 
 template <int D, bool IL, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams p) {
-  __shared__ uint64_t turns[D / 2];
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
+  __shared__ Angles<D> ang;
   grid_dep_launch();
   grid_dep_wait();
-  for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turns[i] = turns_of(p.inv_freq[i]);
-  __syncthreads();
-  const int64_t tok = static_cast<int64_t>(blockIdx.x) * rope_tokens_per_block(D) + threadIdx.x / (D / 8);
-  const bool live = tok < static_cast<int64_t>(p.B) * p.N;
+  const int64_t t0 = static_cast<int64_t>(blockIdx.x) * rope_tokens_per_block(D), total = static_cast<int64_t>(p.B) * p.N;
+  fill_angles(ang, p, t0, total, p.starts, true);
+  const int slot_in_block = threadIdx.x / (D / 8);
+  const int64_t tok = t0 + slot_in_block;
+  const bool live = tok < total;
   const int b = live ? static_cast<int>(tok / p.N) : 0, n = live ? static_cast<int>(tok - static_cast<int64_t>(b) * p.N) : 0;
-  Turn<D, IL> t(p.rot);
-  const int start = p.starts != nullptr ? p.starts[b] : 0;
-  t.set(p.pos != nullptr ? position(p.pos, p.pos_type, p.pos_sb, p.pos_sn, b, n) : p.pos_offset + start + n, turns);
+  const Place<D, IL> pl(p.rot);
+  const float2* cs = ang.cs + (live ? slot_in_block : 0) * (D / 2);
   // virtual heads: queries, then keys, then values
   const int v0 = blockIdx.y * p.heads_per_block, v1 = v0 + p.heads_per_block;
   const auto at = [&](const RopeTensor& x) {
-    return static_cast<__nv_bfloat16*>(x.p) + b * x.sb + n * x.sn + t.c * 8;
+    return static_cast<__nv_bfloat16*>(x.p) + b * x.sb + n * x.sn + pl.c * 8;
   };
   if (v0 < p.Hq)
-    rope_heads<D, IL, NORM>(at(p.q), p.q.sh, at(p.qo), p.qo.sh, v0, min(v1, p.Hq), live, live, p.wq, p.wq_type,
-                            p.eps, t);
+    rope_heads<D, IL, NORM>(at(p.q), p.q.sh, at(p.qo), p.qo.sh, v0, min(v1, p.Hq), live, p.wq, p.wq_type, p.eps, pl, cs);
   const int k0 = max(v0 - p.Hq, 0), k1 = min(v1 - p.Hq, p.Hk);
   if (!p.cache) {
     if (k0 < k1)
-      rope_heads<D, IL, NORM>(at(p.k), p.k.sh, at(p.ko), p.ko.sh, k0, k1, live, live, p.wk, p.wk_type, p.eps, t);
+      rope_heads<D, IL, NORM>(at(p.k), p.k.sh, at(p.ko), p.ko.sh, k0, k1, live, p.wk, p.wk_type, p.eps, pl, cs);
     return;
   }
   // The token's slot. A token behind its sequence's count, behind the table's
   // end or on a page that the cache does not have leaves the cache as it was.
+  const int start = p.starts[b];
   const int64_t slot = static_cast<int64_t>(start) + n;
   bool write = live && start >= 0 && (p.counts == nullptr || n < p.counts[b]) && (slot >> p.page_shift) < p.table_width;
   int page = 0;
@@ -240,12 +300,13 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     page = p.table[b * p.table_sb + (slot >> p.page_shift)];
     write = page >= 0 && page < p.n_pages;
   }
+  if (!write) page = 0;
   const int in_page = static_cast<int>(slot & ((1 << p.page_shift) - 1));
-  const int c8 = t.c * 8;
+  const int c8 = pl.c * 8;
   if (k0 < k1)
     rope_heads<D, IL, NORM>(at(p.k), p.k.sh,
                             static_cast<__nv_bfloat16*>(p.kc) + page * p.kc_sp + in_page * p.kc_st + c8, p.kc_sh, k0,
-                            k1, write, write, p.wk, p.wk_type, p.eps, t);
+                            k1, write, p.wk, p.wk_type, p.eps, pl, cs);
   const int w0 = max(v0 - p.Hq - p.Hk, 0), w1 = min(v1 - p.Hq - p.Hk, p.Hk);
   if (!write) return;
   const __nv_bfloat16* vi = at(p.v);
@@ -271,8 +332,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 template <int D, bool IL, bool NORM>
 __device__ __forceinline__ void rope_bwd_heads(const __nv_bfloat16* x_in, int64_t x_sh, const __nv_bfloat16* dy_in,
                                                int64_t dy_sh, __nv_bfloat16* dx_out, int64_t dx_sh, int H, bool live,
-                                               const float (&w)[8], float eps, const Turn<D, IL>& t,
-                                               float (&dw)[8]) {
+                                               const float2 (&w)[4], float eps, const Place<D, IL>& pl,
+                                               const float2 (&A)[4], const float2 (&B)[4], float2 (&dw)[4]) {
   constexpr int kU = 2;
   for (int h = 0; h < H; h += kU) {
     uint4 rx[kU], rg[kU];
@@ -287,25 +348,27 @@ __device__ __forceinline__ void rope_bwd_heads(const __nv_bfloat16* x_in, int64_
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (h + u >= H) break;
-      float g[8], o[8];
+      float2 g[4], o[4];
       unpack(rg[u], g);
-      unpack(t.exchange(rg[u]), o);
-      t.apply(g, o, -1.f);
+      pl.paired(rg[u], g, o);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) g[i] = fma2(g[i], A[i], mul2(o[i], make_float2(-B[i].x, -B[i].y)));
       if constexpr (NORM) {
-        float x[8];
+        float2 x[4], s = make_float2(0.f, 0.f), dot = make_float2(0.f, 0.f);
         unpack(rx[u], x);
-        float ss = 0.f, dot = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(x[i], x[i], ss);
-          dot = fmaf(g[i] * w[i], x[i], dot);
+        for (int i = 0; i < 4; ++i) {
+          s = fma2(x[i], x[i], s);
+          dot = fma2(mul2(g[i], w[i]), x[i], dot);
         }
-        const float r = rsqrtf(row_sum<D>(ss) * (1.f / D) + eps);
-        const float k = row_sum<D>(dot) * (1.f / D) * r * r * r;
+        const float r = rsqrtf(row_sum<D>(s.x + s.y) * (1.f / D) + eps);
+        const float k = row_sum<D>(dot.x + dot.y) * (-1.f / D) * r * r * r;
+        const float2 r2 = make_float2(r, r), k2 = make_float2(k, k);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (live) dw[i] = fmaf(g[i] * r, x[i], dw[i]);
-          g[i] = r * g[i] * w[i] - x[i] * k;
+        for (int i = 0; i < 4; ++i) {
+          g[i] = mul2(g[i], r2);
+          if (live) dw[i] = fma2(g[i], x[i], dw[i]);
+          g[i] = fma2(g[i], w[i], mul2(x[i], k2));
         }
       }
       if (live) store16(dx_out + (h + u) * dx_sh, pack(g));
@@ -314,13 +377,13 @@ __device__ __forceinline__ void rope_bwd_heads(const __nv_bfloat16* x_in, int64_
 }
 
 template <int D>
-__device__ __forceinline__ void block_sum(const float (&dw)[8], float* smem, float* out) {
+__device__ __forceinline__ void block_sum(const float2 (&dw)[4], float* smem, float* out) {
   // [token slot][channel]; then one thread per channel adds the slots in order
   constexpr int kRows = rope_tokens_per_block(D);
   __syncthreads();
   const int c = threadIdx.x % (D / 8), row = threadIdx.x / (D / 8);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) smem[row * D + c * 8 + i] = dw[i];
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<float2*>(smem + row * D + c * 8 + 2 * i) = dw[i];
   __syncthreads();
   if (threadIdx.x < D) {
     float s = 0.f;
@@ -330,33 +393,34 @@ __device__ __forceinline__ void block_sum(const float (&dw)[8], float* smem, flo
 }
 
 template <int D, bool IL, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads) rope_bwd_kernel(const __grid_constant__ RopeBwdParams p) {
-  __shared__ uint64_t turns[D / 2];
-  __shared__ float sums[rope_tokens_per_block(D) * D];
+__global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_constant__ RopeBwdParams p) {
+  __shared__ Angles<D> ang;
+  __shared__ __align__(16) float sums[rope_tokens_per_block(D) * D];
   grid_dep_launch();
   grid_dep_wait();
-  for (int i = threadIdx.x; i < p.rot / 2; i += kRopeThreads) turns[i] = turns_of(p.inv_freq[i]);
-  __syncthreads();
-  Turn<D, IL> t(p.rot);
-  float wq[8], wk[8], dwq[8], dwk[8];
-  load_weights(p.wq, p.wq_type, t.c * 8, wq);
-  load_weights(p.wk, p.wk_type, t.c * 8, wk);
+  const Place<D, IL> pl(p.rot);
+  float2 wq[4], wk[4], dwq[4], dwk[4];
+  load_weights(p.wq, p.wq_type, pl.c * 8, wq);
+  load_weights(p.wk, p.wk_type, pl.c * 8, wk);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) dwq[i] = dwk[i] = 0.f;
+  for (int i = 0; i < 4; ++i) dwq[i] = dwk[i] = make_float2(0.f, 0.f);
   const int64_t total = static_cast<int64_t>(p.B) * p.N;
   constexpr int kTok = rope_tokens_per_block(D);
   for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok; t0 < total; t0 += static_cast<int64_t>(gridDim.x) * kTok) {
-    const int64_t tok = t0 + threadIdx.x / (D / 8);
+    fill_angles(ang, p, t0, total, nullptr, t0 == static_cast<int64_t>(blockIdx.x) * kTok);
+    const int slot = threadIdx.x / (D / 8);
+    const int64_t tok = t0 + slot;
     const bool live = tok < total;
     const int b = live ? static_cast<int>(tok / p.N) : 0,
               n = live ? static_cast<int>(tok - static_cast<int64_t>(b) * p.N) : 0;
-    t.set(p.pos != nullptr ? position(p.pos, p.pos_type, p.pos_sb, p.pos_sn, b, n) : p.pos_offset + n, turns);
+    float2 A[4], B[4];
+    pl.factors(ang.cs + (live ? slot : 0) * (D / 2), A, B);
     const auto at = [&](const RopeTensor& x) {
-      return static_cast<__nv_bfloat16*>(x.p) + b * x.sb + n * x.sn + t.c * 8;
+      return static_cast<__nv_bfloat16*>(x.p) + b * x.sb + n * x.sn + pl.c * 8;
     };
-    rope_bwd_heads<D, IL, NORM>(at(p.q), p.q.sh, at(p.dyq), p.dyq.sh, at(p.dq), p.dq.sh, p.Hq, live, wq, p.eps, t,
+    rope_bwd_heads<D, IL, NORM>(at(p.q), p.q.sh, at(p.dyq), p.dyq.sh, at(p.dq), p.dq.sh, p.Hq, live, wq, p.eps, pl, A, B,
                                 dwq);
-    rope_bwd_heads<D, IL, NORM>(at(p.k), p.k.sh, at(p.dyk), p.dyk.sh, at(p.dk), p.dk.sh, p.Hk, live, wk, p.eps, t,
+    rope_bwd_heads<D, IL, NORM>(at(p.k), p.k.sh, at(p.dyk), p.dyk.sh, at(p.dk), p.dk.sh, p.Hk, live, wk, p.eps, pl, A, B,
                                 dwk);
   }
   if constexpr (NORM) {
@@ -377,6 +441,7 @@ __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int bl
   if (out == nullptr) return;
   const int c = blockIdx.x * 32 + lane;
   float a = 0.f;
+#pragma unroll 4
   for (int r = warp; r < blocks; r += 32) a += part[(static_cast<int64_t>(r) * 2 + side) * d + c];
   s[warp][lane] = a;
   __syncthreads();
