@@ -136,7 +136,7 @@ int fill_rope(const attn_rope_params* p, attn::RopeParams* r) {
 // Blocks of 256 threads go over tokens (x) and over the heads in turn (y).
 // Few tokens: the heads are dealt to more blocks until the GPU has about
 // kBlocksPerSm blocks an SM; the angles are then computed once per block row.
-constexpr int kBlocksPerSm = 16;
+constexpr int kBlocksPerSm = 6;
 
 int launch_rope(attn::RopeParams* r, int d, int heads, cudaStream_t s) {
   int dev = 0, sms = 0;

@@ -214,11 +214,23 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const uint4& u) { *rei
 
 // Heads [h0, h1) of one token: norm, turn, store. in/out: the token's first
 // head at this thread's channels. Every lane of the warp goes through the
-// same heads; `live` says whether its loads and stores are real.
-template <int D, bool IL, bool NORM>
+// same heads; `live` says whether its loads and stores are real. The next
+// heads' loads go out before these are worked on, and the first ones' before
+// `angles` (the block's table, where it is not there yet).
+template <int D, bool IL, bool NORM, typename Fill>
 __device__ __forceinline__ void rope_heads(const __nv_bfloat16* in, int64_t in_sh, __nv_bfloat16* out,
                                            int64_t out_sh, int h0, int h1, bool live, const void* w, int w_type,
-                                           float eps, const Place<D, IL>& pl, const float2* cs) {
+                                           float eps, const Place<D, IL>& pl, const float2* cs, const Fill& angles) {
+  uint4 next[kUnroll];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      next[u] = make_uint4(0, 0, 0, 0);
+      if (live && h + u < h1) next[u] = load16(in + (h + u) * in_sh);
+    }
+  };
+  fetch(h0);
+  angles();
   float2 A[4], B[4];
   pl.factors(cs, A, B);
   if constexpr (NORM) {
@@ -236,10 +248,8 @@ __device__ __forceinline__ void rope_heads(const __nv_bfloat16* in, int64_t in_s
   for (int h = h0; h < h1; h += kUnroll) {
     uint4 raw[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (live && h + u < h1) raw[u] = load16(in + (h + u) * in_sh);
-    }
+    for (int u = 0; u < kUnroll; ++u) raw[u] = next[u];
+    if (h + kUnroll < h1) fetch(h + kUnroll);
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
       if (h + u >= h1) break;  // the same for the whole block
@@ -265,12 +275,11 @@ __device__ __forceinline__ void rope_heads(const __nv_bfloat16* in, int64_t in_s
 }
 
 template <int D, bool IL, bool NORM>
-__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_constant__ RopeParams p) {
   __shared__ Angles<D> ang;
   grid_dep_launch();
   grid_dep_wait();
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * rope_tokens_per_block(D), total = static_cast<int64_t>(p.B) * p.N;
-  fill_angles(ang, p, t0, total, p.starts, true);
   const int slot_in_block = threadIdx.x / (D / 8);
   const int64_t tok = t0 + slot_in_block;
   const bool live = tok < total;
@@ -282,12 +291,17 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   const auto at = [&](const RopeTensor& x) {
     return static_cast<__nv_bfloat16*>(x.p) + b * x.sb + n * x.sn + pl.c * 8;
   };
+  const auto fill = [&]() { fill_angles(ang, p, t0, total, p.starts, true); };
   if (v0 < p.Hq)
-    rope_heads<D, IL, NORM>(at(p.q), p.q.sh, at(p.qo), p.qo.sh, v0, min(v1, p.Hq), live, p.wq, p.wq_type, p.eps, pl, cs);
+    rope_heads<D, IL, NORM>(at(p.q), p.q.sh, at(p.qo), p.qo.sh, v0, min(v1, p.Hq), live, p.wq, p.wq_type, p.eps, pl, cs,
+                            fill);
   const int k0 = max(v0 - p.Hq, 0), k1 = min(v1 - p.Hq, p.Hk);
+  const auto fill_k = [&]() {
+    if (v0 >= p.Hq) fill();
+  };
   if (!p.cache) {
     if (k0 < k1)
-      rope_heads<D, IL, NORM>(at(p.k), p.k.sh, at(p.ko), p.ko.sh, k0, k1, live, p.wk, p.wk_type, p.eps, pl, cs);
+      rope_heads<D, IL, NORM>(at(p.k), p.k.sh, at(p.ko), p.ko.sh, k0, k1, live, p.wk, p.wk_type, p.eps, pl, cs, fill_k);
     return;
   }
   // The token's slot. A token behind its sequence's count, behind the table's
@@ -306,7 +320,7 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   if (k0 < k1)
     rope_heads<D, IL, NORM>(at(p.k), p.k.sh,
                             static_cast<__nv_bfloat16*>(p.kc) + page * p.kc_sp + in_page * p.kc_st + c8, p.kc_sh, k0,
-                            k1, write, p.wk, p.wk_type, p.eps, pl, cs);
+                            k1, write, p.wk, p.wk_type, p.eps, pl, cs, fill_k);
   const int w0 = max(v0 - p.Hq - p.Hk, 0), w1 = min(v1 - p.Hq - p.Hk, p.Hk);
   if (!write) return;
   const __nv_bfloat16* vi = at(p.v);
@@ -334,7 +348,7 @@ __device__ __forceinline__ void rope_bwd_heads(const __nv_bfloat16* x_in, int64_
                                                int64_t dy_sh, __nv_bfloat16* dx_out, int64_t dx_sh, int H, bool live,
                                                const float2 (&w)[4], float eps, const Place<D, IL>& pl,
                                                const float2 (&A)[4], const float2 (&B)[4], float2 (&dw)[4]) {
-  constexpr int kU = 2;
+  constexpr int kU = 4;
   for (int h = 0; h < H; h += kU) {
     uint4 rx[kU], rg[kU];
 #pragma unroll
@@ -399,33 +413,38 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_
   grid_dep_launch();
   grid_dep_wait();
   const Place<D, IL> pl(p.rot);
-  float2 wq[4], wk[4], dwq[4], dwk[4];
-  load_weights(p.wq, p.wq_type, pl.c * 8, wq);
-  load_weights(p.wk, p.wk_type, pl.c * 8, wk);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) dwq[i] = dwk[i] = make_float2(0.f, 0.f);
   const int64_t total = static_cast<int64_t>(p.B) * p.N;
   constexpr int kTok = rope_tokens_per_block(D);
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kTok; t0 < total; t0 += static_cast<int64_t>(gridDim.x) * kTok) {
-    fill_angles(ang, p, t0, total, nullptr, t0 == static_cast<int64_t>(blockIdx.x) * kTok);
-    const int slot = threadIdx.x / (D / 8);
-    const int64_t tok = t0 + slot;
-    const bool live = tok < total;
-    const int b = live ? static_cast<int>(tok / p.N) : 0,
-              n = live ? static_cast<int>(tok - static_cast<int64_t>(b) * p.N) : 0;
-    float2 A[4], B[4];
-    pl.factors(ang.cs + (live ? slot : 0) * (D / 2), A, B);
-    const auto at = [&](const RopeTensor& x) {
-      return static_cast<__nv_bfloat16*>(x.p) + b * x.sb + n * x.sn + pl.c * 8;
-    };
-    rope_bwd_heads<D, IL, NORM>(at(p.q), p.q.sh, at(p.dyq), p.dyq.sh, at(p.dq), p.dq.sh, p.Hq, live, wq, p.eps, pl, A, B,
-                                dwq);
-    rope_bwd_heads<D, IL, NORM>(at(p.k), p.k.sh, at(p.dyk), p.dyk.sh, at(p.dk), p.dk.sh, p.Hk, live, wk, p.eps, pl, A, B,
-                                dwk);
-  }
-  if constexpr (NORM) {
-    if (p.dwq != nullptr) block_sum<D>(dwq, sums, p.part + static_cast<int64_t>(blockIdx.x) * 2 * D);
-    if (p.dwk != nullptr) block_sum<D>(dwk, sums, p.part + (static_cast<int64_t>(blockIdx.x) * 2 + 1) * D);
+  const int64_t first = static_cast<int64_t>(blockIdx.x) * kTok;
+  // the queries' rows, then the keys': one set of weights and sums in registers at a time
+#pragma unroll 1
+  for (int side = 0; side < 2; ++side) {
+    const int H = side ? p.Hk : p.Hq;
+    if (H == 0) continue;
+    const RopeTensor &x = side ? p.k : p.q, &dy = side ? p.dyk : p.dyq, &dx = side ? p.dk : p.dq;
+    float2 w[4], dw[4];
+    load_weights(side ? p.wk : p.wq, side ? p.wk_type : p.wq_type, pl.c * 8, w);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) dw[i] = make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int64_t t0 = first; t0 < total; t0 += static_cast<int64_t>(gridDim.x) * kTok) {
+      fill_angles(ang, p, t0, total, nullptr, t0 == first && (side == 0 || p.Hq == 0));
+      const int slot = threadIdx.x / (D / 8);
+      const int64_t tok = t0 + slot;
+      const bool live = tok < total;
+      const int b = live ? static_cast<int>(tok / p.N) : 0,
+                n = live ? static_cast<int>(tok - static_cast<int64_t>(b) * p.N) : 0;
+      float2 A[4], B[4];
+      pl.factors(ang.cs + (live ? slot : 0) * (D / 2), A, B);
+      const auto at = [&](const RopeTensor& y) {
+        return static_cast<__nv_bfloat16*>(y.p) + b * y.sb + n * y.sn + pl.c * 8;
+      };
+      rope_bwd_heads<D, IL, NORM>(at(x), x.sh, at(dy), dy.sh, at(dx), dx.sh, H, live, w, p.eps, pl, A, B, dw);
+    }
+    if constexpr (NORM) {
+      if ((side ? p.dwk : p.dwq) != nullptr)
+        block_sum<D>(dw, sums, p.part + (static_cast<int64_t>(blockIdx.x) * 2 + side) * D);
+    }
   }
 }
 
