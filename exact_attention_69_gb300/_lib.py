@@ -176,6 +176,8 @@ _lib = None
 def load(path: str = LIB_PATH):
     """Load libattn.so once and declare the C signatures."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

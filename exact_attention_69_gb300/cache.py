@@ -36,6 +36,27 @@ def rope_freqs(rot: int, base: float = 10000.0, device=None) -> torch.Tensor:
     return float(base) ** (-torch.arange(0, rot, 2, dtype=torch.float64, device=device) / rot)
 
 
+# Plans: a call's checks and the parts of its parameter block that follow from the
+# shapes, strides, types and devices of its tensors and from its options, made once for
+# each combination of them and copied for every call; pointers are filled in each time.
+_plans: dict = {}
+
+
+def _remember(key, plan):
+    if len(_plans) >= 4096:
+        _plans.clear()
+    _plans[key] = plan
+    return plan
+
+
+def _sig(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _heads(name, t, shape=None):
     """Checks a [B, H, N, d] bf16 CUDA tensor; returns its element strides (b, h, n)."""
     if t.dtype is not torch.bfloat16:
@@ -63,7 +84,6 @@ def _int32(name, t, device, shape):
         raise ValueError(f"{name} must have the shape {tuple('any' if s is None else s for s in shape)}")
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
-    return t.data_ptr()
 
 
 def _same_device(device, **ts):
@@ -74,25 +94,25 @@ def _same_device(device, **ts):
 
 def _weight(name, w, d, device):
     if w is None:
-        return None, 0
+        return 0
     if w.dtype not in _WEIGHT_TYPES:
         raise TypeError(f"{name} must be bfloat16 or float32")
     if w.device != device:
         raise ValueError(f"{name} must be on {device}")
     if w.shape != (d,) or (d > 1 and w.stride(0) != 1):
         raise ValueError(f"{name} must be a contiguous [{d}] tensor")
-    return w.data_ptr(), _WEIGHT_TYPES[w.dtype]
+    return _WEIGHT_TYPES[w.dtype]
 
 
-def _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, position_offset, interleaved, eps):
-    """The fields that the forward's and the backward's parameter blocks share."""
+def _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, interleaved, eps):
+    """The fields that the forward's and the backward's plans share."""
     if eps is None:
         if q_weight is not None or k_weight is not None:
             raise ValueError("weights need a norm: give eps")
     else:
         p.norm, p.eps = 1, float(eps)
-    p.q_weight, p.q_weight_type = _weight("q_weight", q_weight, d, device)
-    p.k_weight, p.k_weight_type = _weight("k_weight", k_weight, d, device)
+    p.q_weight_type = _weight("q_weight", q_weight, d, device)
+    p.k_weight_type = _weight("k_weight", k_weight, d, device)
     if inv_freq is not None:
         if inv_freq.dtype != torch.float64:
             raise TypeError("inv_freq must be float64 (rope_freqs)")
@@ -100,7 +120,7 @@ def _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, posit
             raise ValueError(f"inv_freq must be on {device}")
         if inv_freq.dim() != 1 or not inv_freq.is_contiguous():
             raise ValueError("inv_freq must be a contiguous [rot / 2] tensor")
-        p.rot, p.inv_freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+        p.rot = 2 * inv_freq.shape[0]
         if p.rot == 0:
             raise ValueError("inv_freq must not be empty")
     p.interleaved = int(bool(interleaved))
@@ -111,10 +131,9 @@ def _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, posit
             raise ValueError(f"positions must be on {device}")
         if tuple(positions.shape) not in ((N,), (B, N)):
             raise ValueError(f"positions must be [{N}] or [{B}, {N}]")
-        p.positions, p.pos_type = positions.data_ptr(), _POS_TYPES[positions.dtype]
+        p.pos_type = _POS_TYPES[positions.dtype]
         st = positions.stride()
         p.pos_stride[:] = (0, st[0]) if len(st) == 1 else st
-    p.pos_offset = int(position_offset)
 
 
 def _on(device, stream, tensors, run):
@@ -136,6 +155,29 @@ def _on(device, stream, tensors, run):
         return out
 
 
+def _plan_fwd(q, k, q_weight, k_weight, inv_freq, positions, interleaved, eps, q_out, k_out):
+    if q.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    B, Hq, N, d = q.shape
+    p = _lib.AttnRopeParams()
+    p.B, p.N, p.Hq, p.d = B, N, Hq, d
+    p.q_stride[:] = _heads("q", q)
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("expected [B, H, N, d] tensors")
+        p.Hk = k.shape[1]
+        p.k_stride[:] = _heads("k", k, (B, p.Hk, N, d))
+    elif k_weight is not None or k_out is not None:
+        raise ValueError("k_weight and k_out need k")
+    _same_device(q.device, k=k, q_out=q_out, k_out=k_out)
+    _set_rope(p, B, N, d, q.device, q_weight, k_weight, inv_freq, positions, interleaved, eps)
+    if q_out is not None:
+        p.q_out_stride[:] = _heads("q_out", q_out, q.shape)
+    if k_out is not None:
+        p.k_out_stride[:] = _heads("k_out", k_out, k.shape)
+    return bytes(p)
+
+
 def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor | None = None,
                      k_weight: torch.Tensor | None = None, *, inv_freq: torch.Tensor | None = None,
                      positions: torch.Tensor | None = None, position_offset: int = 0,
@@ -150,27 +192,14 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Te
     + n. Pairs are (i, i + rot / 2), or (2i, 2i + 1) with `interleaved`. k may be None.
     Returns (q_out, k_out); q_out may be q, k_out k.
     """
-    if q.dim() != 4:
-        raise ValueError("expected [B, H, N, d] tensors")
-    B, Hq, N, d = q.shape
-    p = _lib.AttnRopeParams()
-    p.B, p.N, p.Hq, p.d = B, N, Hq, d
-    p.q_stride[:] = _heads("q", q)
-    p.q = q.data_ptr()
-    if k is not None:
-        if k.dim() != 4:
-            raise ValueError("expected [B, H, N, d] tensors")
-        p.Hk = k.shape[1]
-        p.k_stride[:] = _heads("k", k, (B, p.Hk, N, d))
-        p.k = k.data_ptr()
-    elif k_weight is not None or k_out is not None:
-        raise ValueError("k_weight and k_out need k")
-    _same_device(q.device, k=k, q_out=q_out, k_out=k_out)
-    _set_rope(p, B, N, d, q.device, q_weight, k_weight, inv_freq, positions, position_offset, interleaved, eps)
-    if q_out is not None:
-        p.q_out_stride[:] = _heads("q_out", q_out, q.shape)
-    if k_out is not None:
-        p.k_out_stride[:] = _heads("k_out", k_out, k.shape)
+    key = ("fwd", _sig(q), _sig(k), _sig(q_weight), _sig(k_weight), _sig(inv_freq), _sig(positions), _sig(q_out),
+           _sig(k_out), interleaved, eps)
+    plan = _plans.get(key)
+    if plan is None:
+        plan = _remember(key, _plan_fwd(q, k, q_weight, k_weight, inv_freq, positions, interleaved, eps, q_out, k_out))
+    p = _lib.AttnRopeParams.from_buffer_copy(plan)
+    p.q, p.k, p.q_weight, p.k_weight = q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight)
+    p.inv_freq, p.positions, p.pos_offset = _ptr(inv_freq), _ptr(positions), int(position_offset)
 
     def run(handle):  # (outputs that are made here are contiguous: strides of zero)
         qo = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
@@ -189,6 +218,39 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Te
     return _on(q.device, stream, (q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out), run)
 
 
+def _plan_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions, interleaved, eps, weight_grads):
+    """(the parameter block, bytes of workspace)"""
+    if q.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    if (k is None) != (dk_out is None):
+        raise ValueError("k and dk_out go together")
+    B, Hq, N, d = q.shape
+    p = _lib.AttnRopeBwdParams()
+    p.B, p.N, p.Hq, p.d = B, N, Hq, d
+    p.q_stride[:] = _heads("q", q)
+    p.dq_out_stride[:] = _heads("dq_out", dq_out, q.shape)
+    if k is not None:
+        if k.dim() != 4:
+            raise ValueError("expected [B, H, N, d] tensors")
+        p.Hk = k.shape[1]
+        p.k_stride[:] = _heads("k", k, (B, p.Hk, N, d))
+        p.dk_out_stride[:] = _heads("dk_out", dk_out, k.shape)
+    elif k_weight is not None:
+        raise ValueError("k_weight needs k")
+    _same_device(q.device, k=k, dq_out=dq_out, dk_out=dk_out)
+    _set_rope(p, B, N, d, q.device, q_weight, k_weight, inv_freq, positions, interleaved, eps)
+    plan, n = bytes(p), 0
+    if weight_grads and (q_weight is not None or k_weight is not None):
+        p.inv_freq, p.positions = _ptr(inv_freq), _ptr(positions)
+        p.q_weight, p.k_weight = _ptr(q_weight), _ptr(k_weight)
+        p.dq_weight, p.dk_weight = _ptr(q_weight), _ptr(k_weight)  # (only whether they are wanted)
+        with torch.cuda.device(q.device):
+            n = _lib.load().attn_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(p))
+        if n < 0:
+            _lib.check(int(-n), "qk_norm_rope_bwd")
+    return plan, int(n)
+
+
 def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tensor,
                      dk_out: torch.Tensor | None, q_weight: torch.Tensor | None = None,
                      k_weight: torch.Tensor | None = None, *, inv_freq: torch.Tensor | None = None,
@@ -199,27 +261,16 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tens
     gradients dq_out, dk_out at its outputs; the other arguments as the forward had them.
     Weight gradients have the weights' types (None without a weight, or with
     weight_grads False); their sums are fp32 in a fixed order."""
-    if q.dim() != 4:
-        raise ValueError("expected [B, H, N, d] tensors")
-    if (k is None) != (dk_out is None):
-        raise ValueError("k and dk_out go together")
-    B, Hq, N, d = q.shape
-    p = _lib.AttnRopeBwdParams()
-    p.B, p.N, p.Hq, p.d = B, N, Hq, d
-    p.q_stride[:] = _heads("q", q)
-    p.dq_out_stride[:] = _heads("dq_out", dq_out, q.shape)
-    p.q, p.dq_out = q.data_ptr(), dq_out.data_ptr()
-    if k is not None:
-        if k.dim() != 4:
-            raise ValueError("expected [B, H, N, d] tensors")
-        p.Hk = k.shape[1]
-        p.k_stride[:] = _heads("k", k, (B, p.Hk, N, d))
-        p.dk_out_stride[:] = _heads("dk_out", dk_out, k.shape)
-        p.k, p.dk_out = k.data_ptr(), dk_out.data_ptr()
-    elif k_weight is not None:
-        raise ValueError("k_weight needs k")
-    _same_device(q.device, k=k, dq_out=dq_out, dk_out=dk_out)
-    _set_rope(p, B, N, d, q.device, q_weight, k_weight, inv_freq, positions, position_offset, interleaved, eps)
+    key = ("bwd", _sig(q), _sig(k), _sig(dq_out), _sig(dk_out), _sig(q_weight), _sig(k_weight), _sig(inv_freq),
+           _sig(positions), interleaved, eps, weight_grads)
+    plan = _plans.get(key)
+    if plan is None:
+        plan = _remember(key, _plan_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions, interleaved, eps,
+                                        weight_grads))
+    p = _lib.AttnRopeBwdParams.from_buffer_copy(plan[0])
+    p.q, p.k, p.dq_out, p.dk_out = q.data_ptr(), _ptr(k), dq_out.data_ptr(), _ptr(dk_out)
+    p.q_weight, p.k_weight = _ptr(q_weight), _ptr(k_weight)
+    p.inv_freq, p.positions, p.pos_offset = _ptr(inv_freq), _ptr(positions), int(position_offset)
 
     def run(handle):
         dk = dwq = dwk = None
@@ -234,15 +285,11 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tens
         if weight_grads and k_weight is not None:
             dwk = torch.empty_like(k_weight)
             p.dk_weight = dwk.data_ptr()
-        lib = _lib.load()
-        if dwq is not None or dwk is not None:
-            n = lib.attn_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(p))
-            if n < 0:
-                _lib.check(int(-n), "qk_norm_rope_bwd")
-            ws = torch.empty(n, dtype=torch.uint8, device=q.device)
-            p.workspace, p.workspace_bytes = ws.data_ptr(), n
+        if plan[1]:
+            ws = torch.empty(plan[1], dtype=torch.uint8, device=q.device)
+            p.workspace, p.workspace_bytes = ws.data_ptr(), plan[1]
         p.stream = handle
-        code = lib.attn_qk_norm_rope_bwd(ctypes.byref(p))
+        code = _lib.load().attn_qk_norm_rope_bwd(ctypes.byref(p))
         if code:
             _lib.check(code, "qk_norm_rope_bwd")
         return dq, dk, dwq, dwk
@@ -267,10 +314,11 @@ class _QkNormRope(torch.autograd.Function):
         weights = ctx.needs_input_grad[2] or ctx.needs_input_grad[3]
         dq = dk = dwq = dwk = None
 
-        def ready(g):  # any strides will do, but for the last dimension's and their multiples of 16 bytes
-            ok = g.stride(-1) == 1 and g.data_ptr() % 16 == 0 and all(
-                n == 1 or (s > 0 and s % 8 == 0) for s, n in zip(g.stride()[:3], g.shape))
-            return g if ok else g.contiguous()
+        def ready(g):  # most strides will do as they are: see attn_rope_bwd_params
+            if g.data_ptr() % 16 == 0 and (g.is_contiguous() or (g.stride(3) == 1 and all(
+                    n == 1 or (s > 0 and s % 8 == 0) for s, n in zip(g.stride(), g.shape[:3])))):
+                return g
+            return g.contiguous()
 
         # an output that the loss does not reach has no gradient, and its side is left out
         if dq_out is not None and dk_out is not None:
@@ -302,8 +350,37 @@ def _cache(p, k_cache, v_cache, Hk, d, device):
     p.k_cache_stride[:] = _heads("k_cache", k_cache, (pages, Hk, page, d))
     p.v_cache_stride[:] = _heads("v_cache", v_cache, (pages, Hk, page, d))
     _same_device(device, k_cache=k_cache, v_cache=v_cache)
-    p.k_cache, p.v_cache = k_cache.data_ptr(), v_cache.data_ptr()
     p.n_pages, p.page_size = pages, page
+
+
+def _plan_append(k, v, k_cache, v_cache, block_table, starts, counts, positions, inv_freq, interleaved, eps, k_weight,
+                 q, q_weight, q_out):
+    if k.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    B, Hk, N, d = k.shape
+    device = k.device
+    p = _lib.AttnRopeParams()
+    p.B, p.N, p.Hk, p.d = B, N, Hk, d
+    p.k_stride[:] = _heads("k", k)
+    p.v_stride[:] = _heads("v", v, k.shape)
+    _same_device(device, v=v, q=q, q_out=q_out)
+    _cache(p, k_cache, v_cache, Hk, d, device)
+    _int32("block_table", block_table, device, (B, None))
+    p.table_width, p.table_stride = block_table.shape[1], block_table.stride(0)
+    _int32("starts", starts, device, (B,))
+    if counts is not None:
+        _int32("counts", counts, device, (B,))
+    if q is not None:
+        if q.dim() != 4:
+            raise ValueError("expected [B, H, N, d] tensors")
+        p.Hq = q.shape[1]
+        p.q_stride[:] = _heads("q", q, (B, p.Hq, N, d))
+    elif q_weight is not None or q_out is not None:
+        raise ValueError("q_weight and q_out need q")
+    _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, interleaved, eps)
+    if q_out is not None:
+        p.q_out_stride[:] = _heads("q_out", q_out, q.shape)
+    return bytes(p)
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -326,33 +403,18 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     do negative starts, slots behind the table's end and entries that are not a page of
     the cache. The pages that a call writes must not be shared between sequences.
     """
-    if k.dim() != 4:
-        raise ValueError("expected [B, H, N, d] tensors")
-    B, Hk, N, d = k.shape
+    key = ("append", _sig(k), _sig(v), _sig(k_cache), _sig(v_cache), _sig(block_table), _sig(starts), _sig(counts),
+           _sig(positions), _sig(inv_freq), interleaved, eps, _sig(k_weight), _sig(q), _sig(q_weight), _sig(q_out))
+    plan = _plans.get(key)
+    if plan is None:
+        plan = _remember(key, _plan_append(k, v, k_cache, v_cache, block_table, starts, counts, positions, inv_freq,
+                                           interleaved, eps, k_weight, q, q_weight, q_out))
     device = k.device
-    p = _lib.AttnRopeParams()
-    p.B, p.N, p.Hk, p.d = B, N, Hk, d
-    p.k_stride[:] = _heads("k", k)
-    p.v_stride[:] = _heads("v", v, k.shape)
-    p.k, p.v = k.data_ptr(), v.data_ptr()
-    _same_device(device, v=v, q=q, q_out=q_out)
-    _cache(p, k_cache, v_cache, Hk, d, device)
-    p.block_table = _int32("block_table", block_table, device, (B, None))
-    p.table_width, p.table_stride = block_table.shape[1], block_table.stride(0)
-    p.starts = _int32("starts", starts, device, (B,))
-    if counts is not None:
-        p.counts = _int32("counts", counts, device, (B,))
-    if q is not None:
-        if q.dim() != 4:
-            raise ValueError("expected [B, H, N, d] tensors")
-        p.Hq = q.shape[1]
-        p.q_stride[:] = _heads("q", q, (B, p.Hq, N, d))
-        p.q = q.data_ptr()
-    elif q_weight is not None or q_out is not None:
-        raise ValueError("q_weight and q_out need q")
-    _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, position_offset, interleaved, eps)
-    if q_out is not None:
-        p.q_out_stride[:] = _heads("q_out", q_out, q.shape)
+    p = _lib.AttnRopeParams.from_buffer_copy(plan)
+    p.q, p.k, p.v, p.k_cache, p.v_cache = _ptr(q), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+    p.block_table, p.starts, p.counts = block_table.data_ptr(), starts.data_ptr(), _ptr(counts)
+    p.q_weight, p.k_weight = _ptr(q_weight), _ptr(k_weight)
+    p.inv_freq, p.positions, p.pos_offset = _ptr(inv_freq), _ptr(positions), int(position_offset)
 
     def run(handle):
         qo = q_out
@@ -371,6 +433,45 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
 
 
 _PAGED_MASKS = {"none": _lib.ATTN_MASK_NONE, "causal_br": _lib.ATTN_MASK_CAUSAL_BR}
+
+
+def _plan_paged(q, k_cache, v_cache, block_table, kv_lens, q_lens, prefix_table, prefix_len, scale, mask, out, lse,
+                num_ctas):
+    """(the parameter block, bytes of workspace)"""
+    if mask not in _PAGED_MASKS:
+        raise ValueError(f"mask must be 'none' or 'causal_br', not {mask!r}")
+    if q.dim() != 4:
+        raise ValueError("expected [B, H, N, d] tensors")
+    B, Hq, Nq, d = q.shape
+    device = q.device
+    p = _lib.AttnPagedParams()
+    p.q_stride[:] = _heads("q", q)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must both be [n_pages, Hk, page_size, d]")
+    p.B, p.Hq, p.Hk, p.Nq, p.d = B, Hq, k_cache.shape[1], Nq, d
+    _cache(p, k_cache, v_cache, p.Hk, d, device)
+    _int32("block_table", block_table, device, (B, None))
+    p.table_width, p.table_stride = block_table.shape[1], block_table.stride(0)
+    _int32("kv_lens", kv_lens, device, (B,))
+    if q_lens is not None:
+        _int32("q_lens", q_lens, device, (B,))
+    p.prefix_len = int(prefix_len)
+    if prefix_table is not None:
+        _int32("prefix_table", prefix_table, device, (None,))
+        p.prefix_pages = prefix_table.shape[0]
+    p.scale = float(1.0 / math.sqrt(d) if scale is None else scale)
+    p.mask_kind = _PAGED_MASKS[mask]
+    p.num_ctas = int(num_ctas)
+    _same_device(device, out=out, lse=lse)
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, Hq, Nq)):
+        raise ValueError("lse must be a contiguous float32 [B, Hq, Nq] tensor")
+    if out is not None:
+        p.o_stride[:] = _heads("out", out, q.shape)
+    with torch.cuda.device(device):
+        n = _lib.load().attn_paged_workspace_bytes(ctypes.byref(p))
+    if n < 0:
+        _lib.check(int(-n), "attn_paged")
+    return bytes(p), int(n)
 
 
 def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -392,53 +493,30 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     Returns (o, lse) or o. Raises for what the host can check; a bad table entry reads
     as zeros, a length beyond the table's end is cut.
     """
-    if q.dim() != 4:
-        raise ValueError("expected [B, H, N, d] tensors")
-    if mask not in _PAGED_MASKS:
-        raise ValueError(f"mask must be 'none' or 'causal_br', not {mask!r}")
-    B, Hq, Nq, d = q.shape
+    key = ("paged", _sig(q), _sig(k_cache), _sig(v_cache), _sig(block_table), _sig(kv_lens), _sig(q_lens),
+           _sig(prefix_table), prefix_len, scale, mask, _sig(out), _sig(lse), num_ctas)
+    plan = _plans.get(key)
+    if plan is None:
+        plan = _remember(key, _plan_paged(q, k_cache, v_cache, block_table, kv_lens, q_lens, prefix_table, prefix_len,
+                                          scale, mask, out, lse, num_ctas))
     device = q.device
-    p = _lib.AttnPagedParams()
-    p.q_stride[:] = _heads("q", q)
-    if k_cache.dim() != 4:
-        raise ValueError("k_cache and v_cache must both be [n_pages, Hk, page_size, d]")
-    p.B, p.Hq, p.Hk, p.Nq, p.d = B, Hq, k_cache.shape[1], Nq, d
-    p.q = q.data_ptr()
-    _cache(p, k_cache, v_cache, p.Hk, d, device)
-    p.block_table = _int32("block_table", block_table, device, (B, None))
-    p.table_width, p.table_stride = block_table.shape[1], block_table.stride(0)
-    p.kv_lens = _int32("kv_lens", kv_lens, device, (B,))
-    if q_lens is not None:
-        p.q_lens = _int32("q_lens", q_lens, device, (B,))
-    p.prefix_len = int(prefix_len)
-    if prefix_table is not None:
-        p.prefix_table = _int32("prefix_table", prefix_table, device, (None,))
-        p.prefix_pages = prefix_table.shape[0]
-    p.scale = float(1.0 / math.sqrt(d) if scale is None else scale)
-    p.mask_kind = _PAGED_MASKS[mask]
-    p.num_ctas, p.timeout_ns, p.inject = int(num_ctas), int(timeout_ns), int(inject)
-    _same_device(device, out=out, lse=lse)
-    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, Hq, Nq)):
-        raise ValueError("lse must be a contiguous float32 [B, Hq, Nq] tensor")
-    if out is not None:
-        p.o_stride[:] = _heads("out", out, q.shape)
+    p = _lib.AttnPagedParams.from_buffer_copy(plan[0])
+    p.q, p.k_cache, p.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+    p.block_table, p.kv_lens, p.q_lens = block_table.data_ptr(), kv_lens.data_ptr(), _ptr(q_lens)
+    p.prefix_table, p.timeout_ns, p.inject = _ptr(prefix_table), int(timeout_ns), int(inject)
 
     def run(handle):
         o = torch.empty(q.shape, dtype=torch.bfloat16, device=device) if out is None else out
         p.o = o.data_ptr()
         z = lse
         if z is None and return_lse:
-            z = torch.empty((B, Hq, Nq), dtype=torch.float32, device=device)
+            z = torch.empty(q.shape[:3], dtype=torch.float32, device=device)
         if z is not None:
             p.lse = z.data_ptr()
-        lib = _lib.load()
-        n = lib.attn_paged_workspace_bytes(ctypes.byref(p))
-        if n < 0:
-            _lib.check(int(-n), "attn_paged")
-        ws = torch.empty(n, dtype=torch.uint8, device=device)
-        p.workspace, p.workspace_bytes = ws.data_ptr(), n
+        ws = torch.empty(plan[1], dtype=torch.uint8, device=device)
+        p.workspace, p.workspace_bytes = ws.data_ptr(), plan[1]
         p.stream = handle
-        code = lib.attn_paged(ctypes.byref(p))
+        code = _lib.load().attn_paged(ctypes.byref(p))
         if code:
             _lib.check(code, "attn_paged")
         return (o, z) if return_lse else o
