@@ -264,6 +264,18 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       : "memory");
 }
 
+// Loads 16 consecutive 32-bit TMEM columns of this thread's lane, then waits for them.
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 // 32 columns at each of two addresses of this thread's lane, one wait for both.
 __device__ __forceinline__ void tmem_ld32x2(uint32_t ta, uint32_t (&a)[32], uint32_t tb, uint32_t (&b)[32]) {
   asm volatile(
@@ -703,55 +715,81 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
       tc_fence_after();
       const bool tail = base + kBN > end;
       if (any) {
-        // one tile of scores: mask, running maximum and sum, P as bf16 over S in two
-        // halves, each announced on its own barrier
+        // One tile of scores, 32 keys at a time in a rolled loop: mask, running
+        // maximum and sum, P as bf16 over S (P of keys [32 j, 32 j + 32) goes over
+        // columns [16 j, 16 j + 16), read by then). The code is a quarter of the
+        // unrolled tile's, and fetching it is what a tile took when a CTA turned to
+        // it once a task: 7000 cycles against 1300 in a long run of tiles.
+        // A later piece whose maximum passes the reference by more than 2^8 brings
+        // O, the sum and the pieces of P before it to its own (rare).
         const int lim = (k < s.pt ? min(seen, end) : min(seen - p.prefix_len, end)) - base;
-        uint32_t sr[128];
-        tmem_ld128(t_s, sr);
-        if (__any_sync(0xffffffffu, lim < kBN)) {
-          const uint32_t neg_inf = __float_as_uint(-CUDART_INF_F);
+        float2 sum2 = make_float2(0.f, 0.f);
+#pragma unroll 1
+        for (int j = 0; j < 4; ++j) {
+          uint32_t sr[32], pk[16];
+          tmem_ld32(t_s + 32 * j, sr);
+          const int lj = lim - 32 * j;
+          if (__any_sync(0xffffffffu, lj < 32)) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (i >= lim) sr[i] = neg_inf;
-        }
-        const float mx = row_max128(sr);
-        const float m_tile = (mx == -CUDART_INF_F) ? -CUDART_INF_F : mx * c;
-        const bool grow = m_tile > m_ref + kRescaleLog2;
-        float alpha = 1.f;
-        if (grow) {
-          alpha = ex2(m_ref - m_tile);
-          l *= alpha;
-          m_ref = m_tile;
-        }
-        if (__any_sync(0xffffffffu, grow && !first)) rescale_o<D>(t_o, alpha);
-        const float neg_m = (m_ref == -CUDART_INF_F) ? 0.f : -m_ref;
-        const float2 c2 = make_float2(c, c), nm2 = make_float2(neg_m, neg_m);
-        float2 sum4[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            for (int i = 0; i < 32; ++i)
+              if (i >= lj) sr[i] = __float_as_uint(-CUDART_INF_F);
+          }
+          float m4[4];
 #pragma unroll
-        for (int part = 0; part < 2; ++part) {
-          uint32_t pk[32];
+          for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 4]));
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int e = 64 * part + 2 * i;
-            const float2 y = __ffma2_rn(make_float2(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1])), c2, nm2);
+          for (int i = 8; i < 32; i += 8)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], __uint_as_float(sr[i + q]), __uint_as_float(sr[i + q + 4]));
+          const float mx = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
+          const float m_piece = (mx == -CUDART_INF_F) ? -CUDART_INF_F : mx * c;
+          const bool grow = m_piece > m_ref + kRescaleLog2;
+          if (__any_sync(0xffffffffu, grow)) {
+            float alpha = 1.f;
+            if (grow) {
+              alpha = ex2(m_ref - m_piece);  // 0 while m_ref is still -inf
+              l *= alpha;
+              m_ref = m_piece;
+            }
+            sum2 = __fmul2_rn(sum2, make_float2(alpha, alpha));
+            if (!first) rescale_o<D>(t_o, alpha);
+            if (j > 0) {
+              tmem_wait_st();
+              for (int q = 0; q < j; ++q) {
+                uint32_t pp[16];
+                tmem_ld16(t_p + 16 * q, pp);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  pp[i] = pack_bf16(__uint_as_float(pp[i] << 16) * alpha, __uint_as_float(pp[i] & 0xffff0000u) * alpha);
+                tmem_st16(t_p + 16 * q, pp);
+              }
+            }
+          }
+          const float neg_m = (m_ref == -CUDART_INF_F) ? 0.f : -m_ref;
+          const float2 c2 = make_float2(c, c), nm2 = make_float2(neg_m, neg_m);
+          float2 part = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float2 y =
+                __ffma2_rn(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nm2);
             const float2 pe = make_float2(ex2(y.x), ex2(y.y));
-            sum4[i & 3] = __fadd2_rn(sum4[i & 3], pe);
+            if (i & 1) {
+              part = __fadd2_rn(part, pe);
+            } else {
+              sum2 = __fadd2_rn(sum2, pe);
+            }
             pk[i] = pack_bf16(pe.x, pe.y);
           }
-          if (part == 1) {
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0 && !tail) mbar_arrive(bars.p_full(h, 0));
-          }
-          tmem_st32(t_p + 32 * part, pk);
+          sum2 = __fadd2_rn(sum2, part);
+          tmem_st16(t_p + 16 * j, pk);
         }
+        l += sum2.x + sum2.y;
         tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0 && !tail) mbar_arrive(bars.p_full(h, 1));
-        const float2 sa = __fadd2_rn(sum4[0], sum4[1]), sb = __fadd2_rn(sum4[2], sum4[3]);
-        l += (sa.x + sa.y) + (sb.x + sb.y);
+        if (!tail) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane < 2) mbar_arrive(bars.p_full(h, lane));
+        }
       } else if (!tail) {
         // no row of this warp sees a key of the task: its P and O are never read
         tc_fence_before();
