@@ -139,12 +139,17 @@ __device__ __forceinline__ Tiles own_tiles(const PagedParams& p, SeqLens s, int 
   return Tiles{pre, pre + (max(seen - p.prefix_len, 0) + kBN - 1) / kBN};
 }
 
+// Units of a tile of a task that has `rows` rows left, and of the task.
+__device__ __forceinline__ int tile_units(int rows) { return rows > kBM ? kPagedPairTile : kPagedTile; }
+__device__ __forceinline__ int task_units(int tiles, int rows) {
+  return tiles > 0 ? kPagedTaskCost + tiles * tile_units(rows) : 0;
+}
+
 // Units of one sequence's tasks for one key head.
 __device__ __forceinline__ int own_units(const PagedParams& p, SeqLens s) {
   int u = 0;
   for (int t = 0; t < p.own_tasks; ++t) {
-    const int tiles = own_tiles(p, s, t).all;
-    u += tiles + (tiles > 0 ? kPagedTaskCost : 0);
+    u += task_units(own_tiles(p, s, t).all, p.Nq * p.G - t * kPagedTaskRows);
   }
   return u;
 }
@@ -172,7 +177,7 @@ struct PSegIter {
   int b, sb;       // current sequence and its first unit
   SeqLens cur, nxt;
   int ub;          // its units per key head
-  int task, parts_end;  // of the segment: index in the task table; its last unit
+  int task, parts_end;  // of the segment: index in the task table; its last tile's first unit
 
   // u0: the CTA's first unit; b0, s0: the sequence that holds it (or the next) and its first unit.
   __device__ __forceinline__ PSegIter(const PagedParams& p, int u0, int u1, int b0, int s0, int ub0)
@@ -189,15 +194,16 @@ struct PSegIter {
       int a, tiles;
       if (u < up) {
         tiles = p.prefix_tiles;
-        const int t = p.by_prefix_units.div(u);
-        a = t * (tiles + kPagedTaskCost);
+        s.hk = p.by_prefix_head.div(u);
+        a = s.hk * static_cast<int>(p.by_prefix_head.d);
+        const int t = min(p.by_prefix_task.div(u - a), p.prefix_tasks - 1);
+        a += t * static_cast<int>(p.by_prefix_task.d);
         s.flags = PSeg::kPrefix;
-        s.hk = p.by_prefix_tasks.div(t);
         s.b = s.len = s.ql = 0;
-        s.row0 = (t - s.hk * p.prefix_tasks) * kPagedTaskRows;
+        s.row0 = t * kPagedTaskRows;
         s.rows = p.B * p.Nq * p.G;
         s.pt = tiles;
-        task = p.B * p.Hk * p.own_tasks + t;
+        task = p.B * p.Hk * p.own_tasks + s.hk * p.prefix_tasks + t;
       } else {
         while (u >= sb + p.Hk * ub) {
           sb += p.Hk * ub;
@@ -215,7 +221,7 @@ struct PSegIter {
         int t = 0;
         Tiles n = own_tiles(p, cur, 0);
         for (;;) {
-          const int per = n.all + (n.all > 0 ? kPagedTaskCost : 0);
+          const int per = task_units(n.all, p.Nq * p.G - t * kPagedTaskRows);
           if (u < a + per) break;
           a += per;
           n = own_tiles(p, cur, ++t);
@@ -226,12 +232,13 @@ struct PSegIter {
         s.row0 = t * kPagedTaskRows;
         s.rows = p.Nq * p.G;
       }
-      const int first = a + kPagedTaskCost, end = first + tiles;
-      s.k0 = max(u, first) - first;
-      s.k1 = min(hi, end) - first;
+      // a tile is the share's that holds its first unit
+      const int w = tile_units(s.rows - s.row0), first = a + kPagedTaskCost, end = first + tiles * w;
+      s.k0 = (max(u, first) - first + w - 1) / w;
+      s.k1 = (max(min(hi, end), first) - first + w - 1) / w;
       if (s.rows - s.row0 <= kBM) s.flags |= PSeg::kTwin;
       if (s.k0 == 0) s.flags |= s.k1 == tiles ? PSeg::kWhole | PSeg::kFirst : PSeg::kFirst;
-      parts_end = end - 1;
+      parts_end = end - w;
       u = min(hi, end);
       if (s.k1 > s.k0) return true;
     }

@@ -206,7 +206,7 @@ void plan_paged(const attn_paged_params* p, int sms, PagedPlan* pl) {
   constexpr int kJoinTiles = 8;
   const int64_t rs = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk), tr = attn::kPagedTaskRows;
   const int64_t own = (rs + tr - 1) / tr, pre = (p->B * rs + tr - 1) / tr, tiles = (static_cast<int64_t>(p->prefix_len) + 127) / 128;
-  pl->batched = p->prefix_len > 0 && p->B * own * tiles > pre * (tiles + attn::kPagedTaskCost) + kJoinTiles * p->B * rs / tr;
+  pl->batched = p->prefix_len > 0 && p->B * own * tiles > pre * (tiles + 1) + kJoinTiles * p->B * rs / tr;
   pl->tasks = up256((p->B * p->Hk * own + (pl->batched ? p->Hk * pre : 0)) * static_cast<int64_t>(sizeof(int2)));
   pl->slots = up256(static_cast<int64_t>(pl->grid) * 4 * 128 * (p->d + 2) * 4);
   if (pl->batched) {
@@ -442,7 +442,7 @@ int attn_paged(const attn_paged_params* p) {
   // most units that the lengths can give, each task at its longest
   const int64_t G = p->Hq / p->Hk, tasks_own = (p->Nq * G + attn::kPagedTaskRows - 1) / attn::kPagedTaskRows,
                 tasks_pre = (static_cast<int64_t>(p->B) * p->Nq * G + attn::kPagedTaskRows - 1) / attn::kPagedTaskRows;
-  const double most = static_cast<double>(p->Hk) *
+  const double most = static_cast<double>(p->Hk) * attn::kPagedPairTile *
                       (static_cast<double>(tasks_pre) * (p->prefix_len / 128 + 2) +
                        static_cast<double>(p->B) * tasks_own * (static_cast<double>(max_len + p->prefix_len) / 128 + 3));
   if (most >= static_cast<double>(kMaxCount)) return fail_with(ATTN_ERR_INVALID_ARG, "problem too large");
@@ -491,13 +491,18 @@ int attn_paged(const attn_paged_params* p) {
   k.prefix_len = p->prefix_len;
   k.prefix_tiles = (p->prefix_len + attn::kBN - 1) / attn::kBN;
   k.prefix_tasks = pl.batched ? static_cast<int>(tasks_pre) : 0;
-  k.prefix_units = p->Hk * k.prefix_tasks * (k.prefix_tiles + attn::kPagedTaskCost);
+  const int full = attn::kPagedTaskCost + k.prefix_tiles * attn::kPagedPairTile;
+  int head = k.prefix_tasks * full;  // (the last task may have one query tile)
+  if (p->B * p->Nq * G - (tasks_pre - 1) * attn::kPagedTaskRows <= attn::kBM)
+    head -= k.prefix_tiles * (attn::kPagedPairTile - attn::kPagedTile);
+  if (!pl.batched) head = 0;
+  k.prefix_units = p->Hk * head;
   k.own_tasks = static_cast<int>(tasks_own);
   k.by_batch_rows = attn::FastDiv(static_cast<uint32_t>(p->B * p->Nq * G));
   k.by_g = attn::FastDiv(static_cast<uint32_t>(G));
   k.by_rows = attn::FastDiv(static_cast<uint32_t>(p->Nq * G));
-  k.by_prefix_units = attn::FastDiv(static_cast<uint32_t>(k.prefix_tiles + attn::kPagedTaskCost));
-  k.by_prefix_tasks = attn::FastDiv(static_cast<uint32_t>(k.prefix_tasks > 0 ? k.prefix_tasks : 1));
+  k.by_prefix_task = attn::FastDiv(static_cast<uint32_t>(full));
+  k.by_prefix_head = attn::FastDiv(static_cast<uint32_t>(head > 0 ? head : 1));
   k.max_len = static_cast<int>(max_len);
   k.causal = p->mask_kind == ATTN_MASK_CAUSAL_BR;
   k.row_limits = p->q_lens != nullptr || (k.causal && p->Nq > 1);

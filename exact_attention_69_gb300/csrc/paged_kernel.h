@@ -10,9 +10,11 @@ namespace attn {
 // Rows of a task are numbered r = n * G + g inside one sequence (G query heads
 // share a key head) and b * Nq * G + n * G + g over the batch for the prefix.
 constexpr int kPagedTaskRows = 256;  // two 128-row query tiles
-// Cost of starting a task in units of one K/V tile: query gather, epilogue.
-constexpr int kPagedTaskCost = 1;
-constexpr int kPagedMinUnits = 2;    // least work that opens another CTA
+// Work is dealt out in units of a quarter of a K/V tile of one query tile. A tile
+// for two query tiles, where the softmax and not memory sets the pace, takes a
+// little longer; a task's start and end as long as a tile.
+constexpr int kPagedTile = 4, kPagedPairTile = 5, kPagedTaskCost = 4;
+constexpr int kPagedMinUnits = 8;    // least work that opens another CTA; no less than a tile
 
 // Division of n < 2^31 by a divisor that the host knows: n * mul >> (32 + shift)
 // with mul = ceil(2^(32 + shift) / d), shift = ceil(log2 d) - 1 (the error term
@@ -52,8 +54,8 @@ struct PagedParams {
   int max_len;                  // table_width * page size: longest own length that the table holds
   FastDiv by_g, by_rows;        // by G; by Nq * G, the rows of a sequence
   FastDiv by_batch_rows;        // by B * Nq * G, the rows of a key head
-  FastDiv by_prefix_units;      // by the units of a prefix task
-  FastDiv by_prefix_tasks;      // by the prefix tasks of a key head
+  FastDiv by_prefix_task;       // by the units of a prefix task of two query tiles
+  FastDiv by_prefix_head;       // by the units of the prefix tasks of a key head
   int prefix_tiles;             // K/V tiles of the prefix
   int prefix_tasks, prefix_units;  // batched prefix: tasks of a key head; units of all. 0: each
                                 // sequence's tasks go over the prefix's tiles themselves
