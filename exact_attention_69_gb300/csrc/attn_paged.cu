@@ -260,26 +260,14 @@ __device__ __forceinline__ RowPos row_pos(const PagedParams& p, const PSeg& s, i
   return x;
 }
 
-// Stores 16 consecutive 32-bit TMEM columns of this thread's lane (completion: tmem_wait_st).
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+// Loads 64 consecutive 32-bit TMEM columns of this thread's lane, then waits for them.
+__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16};\n"
-      :
-      : "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
-
-// Loads 16 consecutive 32-bit TMEM columns of this thread's lane, then waits for them.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
-      "[%16];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
       "tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]), "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]), "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]), "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]), "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr), "r"(taddr + 32u)
       : "memory");
 }
 
@@ -722,30 +710,31 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
       tc_fence_after();
       const bool tail = base + kBN > end;
       if (any) {
-        // One tile of scores, 32 keys at a time in a rolled loop: mask, running
-        // maximum and sum, P as bf16 over S (P of keys [32 j, 32 j + 32) goes over
-        // columns [16 j, 16 j + 16), read by then). The code is a quarter of the
+        // One tile of scores, 64 keys at a time in a rolled loop: mask, running
+        // maximum and sum, P as bf16 over S (P of keys [64 j, 64 j + 64) goes over
+        // columns [32 j, 32 j + 32), read by then). The code is half of the
         // unrolled tile's, and fetching it is what a tile took when a CTA turned to
-        // it once a task: 7000 cycles against 1300 in a long run of tiles.
+        // it once a task: 7000 cycles against 1300 in a long run of tiles. (32 keys
+        // at a time: 138 us for a long prefix and 96 sequences, 64: 125.)
         // A later piece whose maximum passes the reference by more than 2^8 brings
         // O, the sum and the pieces of P before it to its own (rare).
         const int lim = (k < s.pt ? min(seen, end) : min(seen - p.prefix_len, end)) - base;
         float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll 1
-        for (int j = 0; j < 4; ++j) {
-          uint32_t sr[32], pk[16];
-          tmem_ld32(t_s + 32 * j, sr);
-          const int lj = lim - 32 * j;
-          if (__any_sync(0xffffffffu, lj < 32)) {
+        for (int j = 0; j < 2; ++j) {
+          uint32_t sr[64], pk[32];
+          tmem_ld64(t_s + 64 * j, sr);
+          const int lj = lim - 64 * j;
+          if (__any_sync(0xffffffffu, lj < 64)) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
+            for (int i = 0; i < 64; ++i)
               if (i >= lj) sr[i] = __float_as_uint(-CUDART_INF_F);
           }
           float m4[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) m4[i] = fmaxf(__uint_as_float(sr[i]), __uint_as_float(sr[i + 4]));
 #pragma unroll
-          for (int i = 8; i < 32; i += 8)
+          for (int i = 8; i < 64; i += 8)
 #pragma unroll
             for (int q = 0; q < 4; ++q) m4[q] = fmax3(m4[q], __uint_as_float(sr[i + q]), __uint_as_float(sr[i + q + 4]));
           const float mx = fmax3(fmaxf(m4[0], m4[1]), m4[2], m4[3]);
@@ -763,12 +752,12 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
             if (j > 0) {
               tmem_wait_st();
               for (int q = 0; q < j; ++q) {
-                uint32_t pp[16];
-                tmem_ld16(t_p + 16 * q, pp);
+                uint32_t pp[32];
+                tmem_ld32(t_p + 32 * q, pp);
 #pragma unroll
-                for (int i = 0; i < 16; ++i)
+                for (int i = 0; i < 32; ++i)
                   pp[i] = pack_bf16(__uint_as_float(pp[i] << 16) * alpha, __uint_as_float(pp[i] & 0xffff0000u) * alpha);
-                tmem_st16(t_p + 16 * q, pp);
+                tmem_st32(t_p + 32 * q, pp);
               }
             }
           }
@@ -776,7 +765,7 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
           const float2 c2 = make_float2(c, c), nm2 = make_float2(neg_m, neg_m);
           float2 part = make_float2(0.f, 0.f);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 32; ++i) {
             const float2 y =
                 __ffma2_rn(make_float2(__uint_as_float(sr[2 * i]), __uint_as_float(sr[2 * i + 1])), c2, nm2);
             const float2 pe = make_float2(ex2(y.x), ex2(y.y));
@@ -788,7 +777,7 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
             pk[i] = pack_bf16(pe.x, pe.y);
           }
           sum2 = __fadd2_rn(sum2, part);
-          tmem_st16(t_p + 16 * j, pk);
+          tmem_st32(t_p + 32 * j, pk);
         }
         l += sum2.x + sum2.y;
         tmem_wait_st();
