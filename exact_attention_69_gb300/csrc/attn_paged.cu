@@ -177,6 +177,7 @@ struct PSegIter {
   int b, sb;       // current sequence and its first unit
   SeqLens cur, nxt;
   int ub;          // its units per key head
+  int at_head = -1, at_a = -1, at_t = 0;  // first unit of the own head and task looked at last, and its number
   int task, parts_end;  // of the segment: index in the task table; its last tile's first unit
 
   // u0: the CTA's first unit; b0, s0: the sequence that holds it (or the next) and its first unit.
@@ -217,15 +218,21 @@ struct PSegIter {
         s.len = cur.len;
         s.ql = cur.ql;
         s.hk = (u - sb) / ub;
-        a = sb + s.hk * ub;
-        int t = 0;
-        Tiles n = own_tiles(p, cur, 0);
-        for (;;) {
-          const int per = task_units(n.all, p.Nq * p.G - t * kPagedTaskRows);
-          if (u < a + per) break;
-          a += per;
-          n = own_tiles(p, cur, ++t);
+        // the task that holds u, from where the last look ended if that was in this head
+        const int a0 = sb + s.hk * ub;
+        if (at_a < a0 || at_head != a0) {
+          at_head = at_a = a0;
+          at_t = 0;
         }
+        Tiles n = own_tiles(p, cur, at_t);
+        for (;;) {
+          const int per = task_units(n.all, p.Nq * p.G - at_t * kPagedTaskRows);
+          if (u < at_a + per) break;
+          at_a += per;
+          n = own_tiles(p, cur, ++at_t);
+        }
+        const int t = at_t;
+        a = at_a;
         tiles = n.all;
         s.pt = n.prefix;
         task = (b * p.Hk + s.hk) * p.own_tasks + t;

@@ -152,9 +152,9 @@ int launch_rope(attn::RopeParams* r, int d, int heads, cudaStream_t s) {
   return e == cudaSuccess ? ATTN_OK : attn::host::cuda_error(e, "norm and rotation launch");
 }
 
-// Blocks of the backward: a few an SM, each over many tokens, so that few rows
+// Blocks of the backward: what an SM holds, each over many tokens, so that few rows
 // of partial sums are left to add.
-constexpr int kBwdBlocksPerSm = 4;
+constexpr int kBwdBlocksPerSm = 2;
 
 int bwd_blocks(const attn_rope_bwd_params* p, int sms) {
   const int per = attn::rope_tokens_per_block(p->d);

@@ -343,22 +343,35 @@ __global__ void __launch_bounds__(kRopeThreads, 3) rope_kernel(const __grid_cons
 // registers; the block adds its threads' sums in a fixed order and leaves one
 // row of partial sums, which a second kernel adds: no atomics, the same bits
 // every time.
-template <int D, bool IL, bool NORM>
+template <int D, bool IL, bool NORM, typename Fill>
 __device__ __forceinline__ void rope_bwd_heads(const __nv_bfloat16* x_in, int64_t x_sh, const __nv_bfloat16* dy_in,
                                                int64_t dy_sh, __nv_bfloat16* dx_out, int64_t dx_sh, int H, bool live,
                                                const float2 (&w)[4], float eps, const Place<D, IL>& pl,
-                                               const float2 (&A)[4], const float2 (&B)[4], float2 (&dw)[4]) {
-  constexpr int kU = 4;
+                                               const float2* cs, const Fill& angles, float2 (&dw)[4]) {
+  constexpr int kU = 2;
+  uint4 nx[kU], ng[kU];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int u = 0; u < kU; ++u) {
+      nx[u] = ng[u] = make_uint4(0, 0, 0, 0);
+      if (live && h + u < H) {
+        if constexpr (NORM) nx[u] = load16(x_in + (h + u) * x_sh);
+        ng[u] = load16(dy_in + (h + u) * dy_sh);
+      }
+    }
+  };
+  fetch(0);
+  angles();
+  float2 A[4], B[4];
+  pl.factors(cs, A, B);
   for (int h = 0; h < H; h += kU) {
     uint4 rx[kU], rg[kU];
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
-      rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
-      if (live && h + u < H) {
-        if constexpr (NORM) rx[u] = load16(x_in + (h + u) * x_sh);
-        rg[u] = load16(dy_in + (h + u) * dy_sh);
-      }
+      rx[u] = nx[u];
+      rg[u] = ng[u];
     }
+    if (h + kU < H) fetch(h + kU);
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       if (h + u >= H) break;
@@ -428,18 +441,18 @@ __global__ void __launch_bounds__(kRopeThreads, 2) rope_bwd_kernel(const __grid_
     for (int i = 0; i < 4; ++i) dw[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
     for (int64_t t0 = first; t0 < total; t0 += static_cast<int64_t>(gridDim.x) * kTok) {
-      fill_angles(ang, p, t0, total, nullptr, t0 == first && (side == 0 || p.Hq == 0));
       const int slot = threadIdx.x / (D / 8);
       const int64_t tok = t0 + slot;
       const bool live = tok < total;
       const int b = live ? static_cast<int>(tok / p.N) : 0,
                 n = live ? static_cast<int>(tok - static_cast<int64_t>(b) * p.N) : 0;
-      float2 A[4], B[4];
-      pl.factors(ang.cs + (live ? slot : 0) * (D / 2), A, B);
       const auto at = [&](const RopeTensor& y) {
         return static_cast<__nv_bfloat16*>(y.p) + b * y.sb + n * y.sn + pl.c * 8;
       };
-      rope_bwd_heads<D, IL, NORM>(at(x), x.sh, at(dy), dy.sh, at(dx), dx.sh, H, live, w, p.eps, pl, A, B, dw);
+      rope_bwd_heads<D, IL, NORM>(at(x), x.sh, at(dy), dy.sh, at(dx), dx.sh, H, live, w, p.eps, pl,
+                                  ang.cs + (live ? slot : 0) * (D / 2),
+                                  [&]() { fill_angles(ang, p, t0, total, nullptr, t0 == first && (side == 0 || p.Hq == 0)); },
+                                  dw);
     }
     if constexpr (NORM) {
       if ((side ? p.dwk : p.dwq) != nullptr)

@@ -1,6 +1,10 @@
 """GPU: attention over a paged cache with a shared prefix against its definition in
 64 bits (bounds in cache_oracle), and a serving step of the cache operators together."""
 import math
+import os
+import random
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -198,6 +202,101 @@ def test_many_sequences(E):
     """More sequences than threads of a block, most of them short or empty."""
     lens = [(7 * i) % 23 if i % 3 else 0 for i in range(900)]
     Problem(2, 1, 32, 1, 50, lens, 16, seed=900).check(E)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_problems(E, seed):
+    """Sizes drawn at random: groups of heads, lengths, pages, cuts, padding."""
+    r = random.Random(seed)
+    Hk, G, d = r.choice([1, 2, 3]), r.choice([1, 2, 4, 5, 8, 16]), r.choice([32, 64, 128])
+    Nq = r.choice([1, 1, 2, r.randint(3, 20), r.randint(60, 140)])
+    B = r.randint(1, 9 if Nq < 21 else 3)
+    page = r.choice([16, 32, 64, 128, 512])
+    q_lens = [r.randint(0, Nq) for _ in range(B)] if r.random() < 0.4 else None
+    lens = [max(r.choice([0, 1, r.randint(2, 600)]), q_lens[b] if q_lens else Nq) if r.random() < 0.8 else r.randint(0, 40)
+            for b in range(B)]
+    P = r.choice([0, 0, r.randint(1, 130), r.randint(200, 1500)])
+    Problem(Hk * G, Hk, d, Nq, P, lens, page, q_lens, seed=2000 + 10 * seed).check(
+        E, r.choice(["none", "causal_br"]), num_ctas=r.choice([0, 0, r.randint(1, 60)]))
+
+
+def test_offsets_beyond_32_bits(E):
+    """Caches of more than 2^31 elements: their last pages are written and read."""
+    Hk, page, d, n_pages = 8, 64, 128, 33000
+    kc, vc = (torch.empty(n_pages, Hk, page, d, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert kc.numel() > 2 ** 31
+    table = torch.tensor([[n_pages - 1, 3], [n_pages - 2, n_pages - 3]], dtype=torch.int32)
+    small = {int(p): i for i, p in enumerate(sorted(set(table.flatten().tolist())))}
+    k, v = rnd(31, 2, Hk, 100, d), rnd(32, 2, Hk, 100, d)
+    E.kv_append(k.cuda(), v.cuda(), kc, vc, table.cuda(), torch.zeros(2, dtype=torch.int32, device="cuda"))
+    q = rnd(33, 2, Hk, 1, d)
+    o, lse = E.attn_paged(q.cuda(), kc, vc, table.cuda(), torch.tensor([100, 77], dtype=torch.int32, device="cuda"))
+    ks, vs = (torch.stack([c[p].cpu() for p in small]).nan_to_num(0.0) for c in (kc, vc))
+    for b in range(2):
+        for j in range(100):
+            pg = small[int(table[b, j // page])]
+            assert torch.equal(ks[pg, :, j % page], k[b, :, j]) and torch.equal(vs[pg, :, j % page], v[b, :, j])
+    remap = torch.tensor([[small[int(p)] for p in row] for row in table], dtype=torch.int32)
+    ro, bo, rl, bl = O.paged(q, ks, vs, remap, [100, 77], None, None, 0, 1 / math.sqrt(d), "causal_br")
+    O.check("o", o, ro, bo)
+    O.check("lse", lse, rl, bl)
+
+
+def test_keys_and_values_in_one_tensor(E):
+    """Caches that are views of one [page, 2, head, slot, d] tensor."""
+    p = Problem(4, 2, 64, 1, 90, [130, 40], 32, seed=1300)
+    kv = torch.stack([p.k, p.v], dim=1).cuda()
+    q, _, _, table, lens, _, prefix = p.cuda()
+    o, lse = E.attn_paged(q, kv[:, 0], kv[:, 1], table, lens, prefix_table=prefix, prefix_len=90)
+    ro, bo, rl, bl = p.want()
+    O.check("o", o, ro, bo)
+    O.check("lse", lse, rl, bl)
+
+
+def test_first_calls_captured():
+    """In a new process the first call of each operator may be a captured one."""
+    code = """
+import torch, exact_attention_69_gb300 as E
+t = lambda *s: torch.ones(*s, dtype=torch.bfloat16, device="cuda")
+k, kc, vc, q = t(2, 2, 3, 64), t(4, 2, 16, 64), t(4, 2, 16, 64), t(2, 4, 3, 64)
+table = torch.tensor([[0, 1], [2, 3]], dtype=torch.int32, device="cuda")
+starts = torch.tensor([0, 5], dtype=torch.int32, device="cuda")
+f, w = E.rope_freqs(64), torch.ones(64, device="cuda")
+lens = starts + 3
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    qr = E.kv_append(k, k, kc, vc, table, starts, inv_freq=f, eps=1e-6, q=q)
+    o, lse = E.attn_paged(qr, kc, vc, table, lens)
+    a, b = E.qk_norm_rope_fwd(q, k, w, w, inv_freq=f)
+    grads = E.qk_norm_rope_bwd(q, k, a, b, w, w, inv_freq=f)
+g.replay()
+torch.cuda.synchronize()
+assert E.device_status()[0] == 0 and bool(torch.isfinite(o).all()) and bool((o == 1).all())
+print("captured")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=root, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_refusals(E):
+    """What the host can see is refused before anything runs."""
+    p = Problem(4, 2, 64, 2, 20, [30, 9], 16, seed=1400)
+    q, k, v, table, lens, _, prefix = p.cuda()
+    call = lambda **kw: E.attn_paged(**{**dict(q=q, k_cache=k, v_cache=v, block_table=table, kv_lens=lens,  # noqa: E731
+                                               prefix_table=prefix, prefix_len=20), **kw})
+    for bad in (dict(q=q.float()), dict(kv_lens=lens.long()), dict(kv_lens=lens[:1]), dict(block_table=table[:1]),
+                dict(v_cache=v[:, :1]), dict(k_cache=k[:, :, :, :32]), dict(mask="causal"), dict(kv_lens=lens.cpu()),
+                dict(out=q[:1]), dict(lse=torch.empty(2, 4, 2, device="cuda", dtype=torch.float64)),
+                dict(q=q.transpose(2, 3)), dict(q_lens=lens.float())):
+        with pytest.raises((TypeError, ValueError)):
+            call(**bad)
+    for bad in (dict(prefix_len=-1), dict(prefix_len=33), dict(prefix_table=None), dict(scale=0.0), dict(scale=float("nan")),
+                dict(q=q[:, :3].contiguous()), dict(q=q.new_empty(0, 4, 2, 64), block_table=table[:0], kv_lens=lens[:0])):
+        with pytest.raises(E.AttnError):
+            call(**bad)
+    call()
 
 
 def test_timeout_is_reported(E):

@@ -214,6 +214,58 @@ def test_append_leaves_the_rest(E):
     O.check("v_cache", vcc, want_v, torch.zeros_like(want_v))
 
 
+def test_queries_alone_and_no_rotation(E):
+    """k None through autograd; norm without rotation; rotation without norm (its own
+    gradient is the inverse rotation)."""
+    q, g = rnd(81, 2, 3, 11, 64), rnd(82, 2, 3, 11, 64)
+    pos, freqs = torch.arange(11)[None].expand(2, 11), E.rope_freqs(64, device="cpu")
+    for f, eps in ((None, 1e-6), (freqs, None), (freqs, 1e-6)):
+        x = q.cuda().requires_grad_()
+        y, none = E.qk_norm_rope(x, None, inv_freq=None if f is None else f.cuda(), eps=eps)
+        assert none is None
+        (dx,) = torch.autograd.grad(y, x, g.cuda())
+        O.check("y", y, *O.norm_rope(q, None, pos, f, False, eps))
+        O.check("dx", dx, *O.norm_rope_back(q, None, g, pos, f, False, eps)[:2])
+
+
+def test_two_streams_at_once(E):
+    """Two gradients at once have their own scratch."""
+    q, g, w = rnd(83, 2, 8, 600, 128).cuda(), rnd(84, 2, 8, 600, 128).cuda(), weight(85, 128, torch.float32).cuda()
+    f = E.rope_freqs(128)
+    want = E.qk_norm_rope_bwd(q, None, g, None, w, inv_freq=f)
+    other = E.qk_norm_rope_bwd(g, None, q, None, w, inv_freq=f)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(5):
+        a = E.qk_norm_rope_bwd(q, None, g, None, w, inv_freq=f, stream=s1)
+        b = E.qk_norm_rope_bwd(g, None, q, None, w, inv_freq=f, stream=s2)
+        torch.cuda.synchronize()
+        assert torch.equal(a[0], want[0]) and torch.equal(a[2], want[2])
+        assert torch.equal(b[0], other[0]) and torch.equal(b[2], other[2])
+
+
+def test_refusals(E):
+    q, k = rnd(86, 1, 4, 5, 64).cuda(), rnd(87, 1, 2, 5, 64).cuda()
+    w, f = weight(88, 64, torch.float32).cuda(), E.rope_freqs(64)
+    for args, kw in (((q.float(), k), {}), ((q[0], k), {}), ((q, k[:, :, :4]), {}), ((q, k, w[:32]), {}),
+                     ((q, k, w.double()), {}), ((q, k, w), dict(eps=None)), ((q, k), dict(inv_freq=f.float())),
+                     ((q, k), dict(inv_freq=f.cpu())), ((q, k), dict(inv_freq=f, positions=torch.zeros(4, device="cuda").long())),
+                     ((q, k), dict(inv_freq=f, positions=torch.zeros(5, device="cuda"))), ((q, k), dict(k_out=q)),
+                     ((q.transpose(2, 3), k), {}), ((q, None, None, w), {})):
+        with pytest.raises((TypeError, ValueError)):
+            E.qk_norm_rope_fwd(*args, **kw)
+    for kw in (dict(inv_freq=E.rope_freqs(128)), dict(inv_freq=f[:4].contiguous()), dict(eps=float("nan"))):
+        with pytest.raises(E.AttnError):
+            E.qk_norm_rope_fwd(q, k, **kw)
+    with pytest.raises(E.AttnError):  # a view that starts off a 16-byte boundary
+        E.qk_norm_rope_fwd(torch.zeros(1, 1, 5, 72, dtype=torch.bfloat16, device="cuda")[..., 4:68], None)
+    x = q.clone().requires_grad_()
+    y, _ = E.qk_norm_rope(x, k, inv_freq=f)
+    (dx,) = torch.autograd.grad(y, x, torch.ones_like(y, requires_grad=True), create_graph=True)
+    with pytest.raises(RuntimeError):
+        dx.sum().backward()
+
+
 def test_side_stream_and_graph(E):
     """On a given stream, and captured: the replay follows new starts."""
     B, Hk, N, d, page = 2, 2, 3, 64, 16
