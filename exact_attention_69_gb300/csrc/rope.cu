@@ -195,7 +195,9 @@ struct Place {
     } else {
       uint4 w = make_uint4(__shfl_sync(0xffffffffu, u.x, partner), __shfl_sync(0xffffffffu, u.y, partner),
                            __shfl_sync(0xffffffffu, u.z, partner), __shfl_sync(0xffffffffu, u.w, partner));
+      if (!on) w = make_uint4(0u, 0u, 0u, 0u);
       unpack(w, o);
+      return;
     }
     if (!on) {
 #pragma unroll
