@@ -110,7 +110,7 @@ def _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, inter
         if q_weight is not None or k_weight is not None:
             raise ValueError("weights need a norm: give eps")
     else:
-        p.norm, p.eps = 1, float(eps)
+        p.norm, p.eps = 1, eps
     p.q_weight_type = _weight("q_weight", q_weight, d, device)
     p.k_weight_type = _weight("k_weight", k_weight, d, device)
     if inv_freq is not None:
@@ -123,7 +123,7 @@ def _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, inter
         p.rot = 2 * inv_freq.shape[0]
         if p.rot == 0:
             raise ValueError("inv_freq must not be empty")
-    p.interleaved = int(bool(interleaved))
+    p.interleaved = int(interleaved)
     if positions is not None:
         if positions.dtype not in _POS_TYPES:
             raise TypeError("positions must be int32 or int64")
@@ -192,6 +192,7 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Te
     + n. Pairs are (i, i + rot / 2), or (2i, 2i + 1) with `interleaved`. k may be None.
     Returns (q_out, k_out); q_out may be q, k_out k.
     """
+    interleaved, eps = bool(interleaved), None if eps is None else float(eps)
     key = ("fwd", _sig(q), _sig(k), _sig(q_weight), _sig(k_weight), _sig(inv_freq), _sig(positions), _sig(q_out),
            _sig(k_out), interleaved, eps)
     plan = _plans.get(key)
@@ -261,8 +262,9 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tens
     gradients dq_out, dk_out at its outputs; the other arguments as the forward had them.
     Weight gradients have the weights' types (None without a weight, or with
     weight_grads False); their sums are fp32 in a fixed order."""
+    interleaved, eps = bool(interleaved), None if eps is None else float(eps)
     key = ("bwd", _sig(q), _sig(k), _sig(dq_out), _sig(dk_out), _sig(q_weight), _sig(k_weight), _sig(inv_freq),
-           _sig(positions), interleaved, eps, weight_grads)
+           _sig(positions), interleaved, eps, bool(weight_grads))
     plan = _plans.get(key)
     if plan is None:
         plan = _remember(key, _plan_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions, interleaved, eps,
@@ -338,7 +340,9 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor
                  positions: torch.Tensor | None = None, position_offset: int = 0,
                  interleaved: bool = False, eps: float | None = 1e-6):
     """qk_norm_rope_fwd as a differentiable torch op: gradients for q, k and the weights
-    (once: the gradient itself is not differentiable). Runs on the current stream."""
+    (once: the gradient itself is not differentiable). Runs on the current stream. As for
+    any PyTorch op, a backward pass is captured into a graph only while no eager graph
+    of the same leaves is alive."""
     opts = dict(position_offset=int(position_offset), interleaved=bool(interleaved), eps=eps)
     return _QkNormRope.apply(q, k, q_weight, k_weight, inv_freq, positions, opts)
 
@@ -403,6 +407,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     do negative starts, slots behind the table's end and entries that are not a page of
     the cache. The pages that a call writes must not be shared between sequences.
     """
+    interleaved, eps = bool(interleaved), None if eps is None else float(eps)
     key = ("append", _sig(k), _sig(v), _sig(k_cache), _sig(v_cache), _sig(block_table), _sig(starts), _sig(counts),
            _sig(positions), _sig(inv_freq), interleaved, eps, _sig(k_weight), _sig(q), _sig(q_weight), _sig(q_out))
     plan = _plans.get(key)
@@ -455,13 +460,13 @@ def _plan_paged(q, k_cache, v_cache, block_table, kv_lens, q_lens, prefix_table,
     _int32("kv_lens", kv_lens, device, (B,))
     if q_lens is not None:
         _int32("q_lens", q_lens, device, (B,))
-    p.prefix_len = int(prefix_len)
+    p.prefix_len = prefix_len
     if prefix_table is not None:
         _int32("prefix_table", prefix_table, device, (None,))
         p.prefix_pages = prefix_table.shape[0]
     p.scale = float(1.0 / math.sqrt(d) if scale is None else scale)
     p.mask_kind = _PAGED_MASKS[mask]
-    p.num_ctas = int(num_ctas)
+    p.num_ctas = num_ctas
     _same_device(device, out=out, lse=lse)
     if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, Hq, Nq)):
         raise ValueError("lse must be a contiguous float32 [B, Hq, Nq] tensor")
@@ -490,9 +495,11 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     + kv_lens[b]; 'none': every real row sees all T. A row that sees no key gives 0 and
     an LSE of -inf. Lengths and tables are read when the kernels run.
 
-    Returns (o, lse) or o. Raises for what the host can check; a bad table entry reads
+    Returns (o, lse) or o; no gradient goes through it. Raises for what the host can check; a bad table entry reads
     as zeros, a length beyond the table's end is cut.
     """
+    prefix_len, num_ctas = int(prefix_len), int(num_ctas)  # (what a key holds is a value, never a tensor)
+    scale = None if scale is None else float(scale)
     key = ("paged", _sig(q), _sig(k_cache), _sig(v_cache), _sig(block_table), _sig(kv_lens), _sig(q_lens),
            _sig(prefix_table), prefix_len, scale, mask, _sig(out), _sig(lse), num_ctas)
     plan = _plans.get(key)

@@ -5,10 +5,10 @@
 // head: for the prefix, rows of every sequence together (its keys are read
 // once per 256 rows, not once per sequence); for a sequence's own pages, its
 // rows (queries x the heads that share the key head). The tasks' K/V tiles of
-// 128 keys form one sequence of units, one more unit per task for its start,
-// and CTA c takes units [c U / G, (c + 1) U / G): every SM streams the same
-// number of bytes whatever the lengths are. The lengths are read on the
-// device, so a captured graph follows them. A task cut between CTAs leaves
+// 128 keys form one sequence of units (so many for a task's start, then so many
+// a tile), and CTA c takes units [c U / G, (c + 1) U / G): every SM has the same
+// work whatever the lengths are. The lengths are read on the device, so a
+// captured graph follows them. A task cut between CTAs leaves
 // parts (row maximum, row sum, unnormalised O in fp32) in the workspace, and a
 // second kernel joins the parts of each row, prefix and own, in a fixed order.
 //
@@ -30,7 +30,7 @@
 // hold anything, and 0 * NaN would reach the sum.
 //
 // P is rounded to bf16 for the second product (the tensor core's input type;
-// the row sum takes the unrounded values), which moves O by at most 2^-9 of
+// the row sum takes the unrounded values), which moves O by at most 2^-8 of
 // sum p |v|, the size of the final rounding to bf16.
 #include <cuda_bf16.h>
 #include <math_constants.h>
@@ -497,8 +497,8 @@ drain:
 
 // Warp 2: the task's query rows into the swizzled K-major layout that the MMA
 // descriptor expects. Where a query tile is a box of a tensor map it is one TMA
-// per column chunk: prefix tasks of one query a sequence (rows b, head), and
-// tasks inside one sequence of many rows (rows n, head), if G divides 128.
+// per column chunk: prefix tasks (rows b, n, head) if a sequence's rows divide
+// 128, else tasks inside one sequence (rows n, head) if G does.
 // Otherwise 16 bytes a copy, every copy of a task in flight at once: each lane
 // works out the address of one row of 32, a row's d/8 lanes get it by shuffles.
 template <int D>
@@ -520,7 +520,9 @@ __device__ void paged_gather_q(const PagedParams& p, uint32_t sbase, uint8_t* sm
     if (!ctl_wait(bars.q_empty(), ph ^ 1u, ctl, -1, kRoleLoader)) break;
     box = p.q_map == (s.prefix() ? 1 : 2);
     if (box) {
-      const int tiles = n > kBM ? 2 : 1, first = p.by_g.div(s.row0), per = p.by_g.div(kBM);
+      // first query, or first sequence, and how many of them a box holds
+      const FastDiv& rows = s.prefix() ? p.by_rows : p.by_g;
+      const int tiles = n > kBM ? 2 : 1, first = rows.div(s.row0), per = rows.div(kBM);
       mbar_expect_tx(bars.q_full(), static_cast<uint32_t>(tiles) * C::kTileBytes);
       for (int i = 0; i < tiles; ++i)
         for (int ch = 0; ch < C::kChunks; ++ch)
@@ -1058,12 +1060,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
     int c0, parts, in_task;  // parts 0: no key to see; 1: uncut
   };
   Span pre{0, 0, 0}, own{0, 0, 0};
+  // (after a wait that ran out some entries were never written: whatever they hold must name slots that exist)
+  const auto span = [&](int2 e, int in_task) {
+    const int c0 = clampi(e.x, 0, p.grid - 1);
+    return Span{c0, clampi(e.y, 0, p.grid - c0), in_task};
+  };
   const int2 at_own = p.tasks[bh * p.own_tasks + t];  // (written only if the task has a tile)
   if (p.prefix_tasks > 0) {
     const int2 e = p.tasks[p.B * p.Hk * p.own_tasks + hk * p.prefix_tasks + tp];
-    pre = Span{e.x, e.y, rp - tp * kPagedTaskRows};
+    pre = span(e, rp - tp * kPagedTaskRows);
   }
-  if (own_tiles(p, seq_lens(p, b), t).all > 0) own = Span{at_own.x, at_own.y, r - t * kPagedTaskRows};
+  if (own_tiles(p, seq_lens(p, b), t).all > 0) own = span(at_own, r - t * kPagedTaskRows);
   // an uncut row without a batched prefix was written by the attention kernel
   const bool mine = live && !(p.prefix_tasks == 0 && own.parts == 1);
   const int parts = mine ? pre.parts + own.parts : 0;
@@ -1167,12 +1174,12 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
 }
 
 template <int D>
-cudaError_t launch_paged_dim(const PagedParams& p, int grid, cudaStream_t s) {
+cudaError_t launch_paged_dim(const PagedParams& p, cudaStream_t s) {
   constexpr int smem = PCfg<D>::kSmemBytes > kMinSmemBytes ? PCfg<D>::kSmemBytes : kMinSmemBytes;  // one CTA an SM
   cudaError_t e = cudaFuncSetAttribute(paged_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.gridDim = dim3(static_cast<unsigned>(p.grid));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
@@ -1191,11 +1198,11 @@ cudaError_t launch_paged_dim(const PagedParams& p, int grid, cudaStream_t s) {
 
 }  // namespace dev
 
-cudaError_t launch_paged(const PagedParams& p, int d, int grid, cudaStream_t s) {
+cudaError_t launch_paged(const PagedParams& p, int d, cudaStream_t s) {
   switch (d) {
-    case 32: return dev::launch_paged_dim<32>(p, grid, s);
-    case 64: return dev::launch_paged_dim<64>(p, grid, s);
-    case 128: return dev::launch_paged_dim<128>(p, grid, s);
+    case 32: return dev::launch_paged_dim<32>(p, s);
+    case 64: return dev::launch_paged_dim<64>(p, s);
+    case 128: return dev::launch_paged_dim<128>(p, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -12,9 +12,14 @@ namespace attn {
 constexpr int kPagedTaskRows = 256;  // two 128-row query tiles
 // Work is dealt out in units of a quarter of a K/V tile of one query tile. A tile
 // for two query tiles, where the softmax and not memory sets the pace, takes a
-// little longer; a task's start and end as long as a tile.
+// little longer (with 4 / 5 / 6 units 96 sequences behind 32768 tokens took 144.6 /
+// 137.9 / 143.9 us); a task's start and end as long as a tile (2 / 4 / 6 units: 32
+// sequences behind 4096 tokens 33.6 / 30.0 / 29.7 us, 16 of up to 4096 own keys at
+// d = 32 14.5 / 12.7 / 13.4 us).
 constexpr int kPagedTile = 4, kPagedPairTile = 5, kPagedTaskCost = 4;
-constexpr int kPagedMinUnits = 8;    // least work that opens another CTA; no less than a tile
+// Least work that opens another CTA; no less than a tile. (5 / 8 / 16 / 24: 4 sequences
+// behind 512 tokens 11.0 / 10.4 / 12.7 / 17.0 us; larger calls have a CTA an SM anyway.)
+constexpr int kPagedMinUnits = 8;
 
 // Division of n < 2^31 by a divisor that the host knows: n * mul >> (32 + shift)
 // with mul = ceil(2^(32 + shift) / d), shift = ceil(log2 d) - 1 (the error term
@@ -61,7 +66,7 @@ struct PagedParams {
                                 // sequence's tasks go over the prefix's tiles themselves
   int own_tasks;                // tasks of a sequence for one key head
   int q_map;                    // what a box of tm_q holds: 0 nothing (gather), 1 rows of several
-                                // sequences (prefix tasks of one query each), 2 rows of one
+                                // sequences (prefix tasks), 2 rows of one
   int row_limits;               // rows of a sequence may see different numbers of keys
   int causal;                   // bottom-right causal over prefix and own keys together
   float c;                      // scale * log2(e)
@@ -70,12 +75,13 @@ struct PagedParams {
   float* slots;                 // per CTA 2 x 2 query tiles x 128 rows x (d + 2): parts of cut tasks
   float* rows_o;                // [2][B * Nq * Hq][d]: uncut prefix and own results
   float2* rows_ml;              // [2][B * Nq * Hq]: their running maximum (log2 units) and sum
+  int grid;                     // CTAs of the attention kernel
   uint64_t timeout_ns;
   int inject;
 };
 
-// grid: CTAs of the attention kernel; the second kernel joins the parts.
-cudaError_t launch_paged(const PagedParams& p, int d, int grid, cudaStream_t s);
+// The attention kernel, then the one that joins the parts.
+cudaError_t launch_paged(const PagedParams& p, int d, cudaStream_t s);
 // Reads and clears the current device's status word of the paged kernels.
 cudaError_t paged_take_status(uint32_t word[4]);
 

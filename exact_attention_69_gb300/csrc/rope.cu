@@ -15,6 +15,16 @@
 // angles are computed once, into shared memory (a thread for each was half of the
 // time with 16 heads). Loads of four heads are in flight at a time.
 //
+// Measured (rows read and written, with weights and positions):
+//   B8 H32+8 N4096 d128 out of a fused projection: 114 us, 5.9 TB/s; gradient 196 us, 5.1 TB/s
+//   B4 H16+4 N2048 d128: 23.4 us, 3.6 TB/s; gradient 32.4 us, 3.9 TB/s
+//   B1 H8+8 N16384 d128: 29.6 us, 4.5 TB/s; gradient 51.1 us, 3.9 TB/s
+// Below the largest size the last, partly filled round of blocks shows (1024
+// blocks of 16 tokens on 456 places). Persistent blocks over smaller tiles even
+// that out and are slower all the same (43.7 us where one block a tile takes
+// 29.6): each tile waits for its angles at a barrier. Head subsets inside a
+// block, one tile a block, took 39 to 51 us.
+//
 // Angles: a frequency becomes a 64-bit fraction of a turn, and position times
 // frequency is a 64-bit integer product whose overflow drops whole turns. The
 // fraction is exact to 2^-64 * position, where a 32-bit product of position

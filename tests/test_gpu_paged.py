@@ -310,6 +310,39 @@ def test_timeout_is_reported(E):
     p.check(E)
 
 
+def test_timeout_before_the_task_table_is_written(E, monkeypatch):
+    """One CTA stops at its second tile, with tasks that it never noted for the join: a
+    workspace full of large numbers must not send the join anywhere else, with and
+    without a batched prefix, and the next call is right."""
+    empty = torch.empty
+
+    def full(*a, **kw):
+        t = empty(*a, **kw)
+        return t.fill_(0x7F) if t.dtype == torch.uint8 else t
+
+    for P in (0, 2000):
+        p = Problem(4, 1, 64, 1, P, [700] * 24, 16, seed=1010)
+        with monkeypatch.context() as m:
+            m.setattr(torch, "empty", full)
+            p.run(E, num_ctas=1, timeout_ns=20_000_000, inject=1)
+        torch.cuda.synchronize()
+        assert E.device_status()[0] == 5
+        p.check(E)
+
+
+def test_options_by_value(E):
+    """Options given as tensors are read at each call, not when their combination was first seen."""
+    p = Problem(4, 2, 64, 1, 60, [40, 7], 16, seed=1020)
+    n = torch.tensor(30)
+    q, k, v, table, lens, _, prefix = p.cuda()
+    E.attn_paged(q, k, v, table, lens, prefix_table=prefix, prefix_len=n)
+    n.fill_(60)
+    o, lse = E.attn_paged(q, k, v, table, lens, prefix_table=prefix, prefix_len=n)
+    ro, bo, rl, bl = p.want()
+    O.check("o", o, ro, bo)
+    O.check("lse", lse, rl, bl)
+
+
 def test_serving_steps(E):
     """Prompt chunk and decoding steps over one cache: norm, rotation, append and attention
     as a server runs them, against the same steps in 64 bits."""
