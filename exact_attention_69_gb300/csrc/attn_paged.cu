@@ -76,7 +76,7 @@ struct PCfg {
   static constexpr int kXBytes = 2 * 2 * 128 * 4;
   static constexpr int kOffSeg = kOffX + kXBytes;
   static constexpr int kOffBar = kOffSeg + kSegs * static_cast<int>(sizeof(PSeg));
-  static constexpr int kBars = 17 + 2 * kSegs + 2 * kStages;
+  static constexpr int kBars = 19 + 2 * kSegs + 2 * kStages;
   static constexpr int kSmemBytes = kOffBar + 8 * kBars + 16;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
 };
@@ -85,22 +85,22 @@ template <int D>
 struct PBars {
   uint32_t base;
   static constexpr int kSt = PCfg<D>::kStages, kSg = PCfg<D>::kSegs;
-  __device__ uint32_t q_full() const { return base; }
-  __device__ uint32_t q_empty() const { return base + 8; }
-  __device__ uint32_t s_full(int h) const { return base + 16 + 8 * h; }
-  __device__ uint32_t p_full(int h, int part) const { return base + 32 + 8 * (2 * h + part); }
-  __device__ uint32_t o_full(int h) const { return base + 64 + 8 * h; }
-  __device__ uint32_t o_empty(int h) const { return base + 80 + 8 * h; }
-  __device__ uint32_t x_full(int h) const { return base + 96 + 8 * h; }
-  __device__ uint32_t done() const { return base + 112; }
+  __device__ uint32_t q_full(int s) const { return base + 8 * s; }
+  __device__ uint32_t q_empty(int s) const { return base + 16 + 8 * s; }
+  __device__ uint32_t s_full(int h) const { return base + 32 + 8 * h; }
+  __device__ uint32_t p_full(int h, int part) const { return base + 48 + 8 * (2 * h + part); }
+  __device__ uint32_t o_full(int h) const { return base + 80 + 8 * h; }
+  __device__ uint32_t o_empty(int h) const { return base + 96 + 8 * h; }
+  __device__ uint32_t x_full(int h) const { return base + 112 + 8 * h; }
+  __device__ uint32_t done() const { return base + 128; }
   // every product of a one-tile task is complete (o_full: of stream h of a two-tile task).
   // One barrier of its own, that both warpgroups wait for at every such task: none skips a phase.
-  __device__ uint32_t t_full() const { return base + 120; }
-  __device__ uint32_t q_asked() const { return base + 128; }  // the first task's queries are on their way
-  __device__ uint32_t seg_full(int s) const { return base + 136 + 8 * s; }
-  __device__ uint32_t seg_empty(int s) const { return base + 136 + 8 * (kSg + s); }
-  __device__ uint32_t full(int s) const { return base + 136 + 8 * (2 * kSg + s); }
-  __device__ uint32_t empty(int s) const { return base + 136 + 8 * (2 * kSg + kSt + s); }
+  __device__ uint32_t t_full() const { return base + 136; }
+  __device__ uint32_t q_asked() const { return base + 144; }  // the first task's queries are on their way
+  __device__ uint32_t seg_full(int s) const { return base + 152 + 8 * s; }
+  __device__ uint32_t seg_empty(int s) const { return base + 152 + 8 * (kSg + s); }
+  __device__ uint32_t full(int s) const { return base + 152 + 8 * (2 * kSg + s); }
+  __device__ uint32_t empty(int s) const { return base + 152 + 8 * (2 * kSg + kSt + s); }
 };
 
 // ------------------------------------------------------------------ work split
@@ -501,6 +501,8 @@ drain:
 // 128, else tasks inside one sequence (rows n, head) if G does.
 // Otherwise 16 bytes a copy, every copy of a task in flight at once: each lane
 // works out the address of one row of 32, a row's d/8 lanes get it by shuffles.
+// The two query tiles are a ring: a one-tile task's queries arrive while the
+// task before, in the other slot, is still at work.
 template <int D>
 __device__ void paged_gather_q(const PagedParams& p, uint32_t sbase, uint8_t* smem, const PBars<D>& bars,
                                const Ctl& ctl) {
@@ -509,46 +511,54 @@ __device__ void paged_gather_q(const PagedParams& p, uint32_t sbase, uint8_t* sm
   constexpr int kLanes = D / 8, kRows = 32 / kLanes;  // lanes of a row; rows per instruction
   const int lane = threadIdx.x & 31;
   const int c = lane % kLanes, sub = lane / kLanes;   // 16-byte chunk of the row; which row of the instruction's
-  uint32_t ph = 0;
+  RingPos<2> r;
   bool asked = false;
-  bool box = false;  // the last task's queries came as boxes
+  uint32_t armed = 0, par = 0;  // slots whose last queries came as boxes, and their phases
   SegReader<D> segs;
   PSeg s;
   grid_dep_wait();
   while (segs.template take<kRoleLoader>(s, smem, bars, ctl)) {
-    const int n = min(s.rows - s.row0, kPagedTaskRows);
-    if (!ctl_wait(bars.q_empty(), ph ^ 1u, ctl, -1, kRoleLoader)) break;
-    box = p.q_map == (s.prefix() ? 1 : 2);
-    if (box) {
-      // first query, or first sequence, and how many of them a box holds
-      const FastDiv& rows = s.prefix() ? p.by_rows : p.by_g;
-      const int tiles = n > kBM ? 2 : 1, first = rows.div(s.row0), per = rows.div(kBM);
-      mbar_expect_tx(bars.q_full(), static_cast<uint32_t>(tiles) * C::kTileBytes);
-      for (int i = 0; i < tiles; ++i)
+    const int n = min(s.rows - s.row0, kPagedTaskRows), tiles = n > kBM ? 2 : 1;
+    const bool box = p.q_map == (s.prefix() ? 1 : 2);
+    // first query, or first sequence, of the task and how many of them a box holds
+    const FastDiv& rows = s.prefix() ? p.by_rows : p.by_g;
+    const int first = rows.div(s.row0), per = rows.div(kBM);
+    const int slot0 = r.s;
+    for (int i = 0; i < tiles; ++i) {
+      if (!ctl_wait(bars.q_empty(r.s), r.ph ^ 1u, ctl, -1, kRoleLoader)) goto drain;
+      const uint32_t tile = sbase + P::kOffQ + r.s * C::kTileBytes;
+      if (box) {
+        mbar_expect_tx(bars.q_full(r.s), C::kTileBytes);
         for (int ch = 0; ch < C::kChunks; ++ch)
-          tma_load_4d(sbase + P::kOffQ + i * C::kTileBytes + ch * C::kChunkBytes, &p.tm_q, bars.q_full(),
-                      ch * C::kBoxCols, s.hk * p.G, s.prefix() ? 0 : first + i * per, s.prefix() ? first + i * per : s.b);
-    } else {
-      for (int i0 = 0; i0 < n; i0 += 32) {
-        const __nv_bfloat16* src = nullptr;
-        if (i0 + lane < n) {
-          const RowPos x = row_pos(p, s, s.row0 + i0 + lane);
-          src = static_cast<const __nv_bfloat16*>(p.q) + x.b * p.q_sb + static_cast<int64_t>(s.hk * p.G + x.g) * p.q_sh +
-                x.n * p.q_sn;
-        }
-        const int m = min(32, n - i0);
+          tma_load_4d(tile + ch * C::kChunkBytes, &p.tm_q, bars.q_full(r.s), ch * C::kBoxCols, s.hk * p.G,
+                      s.prefix() ? 0 : first + i * per, s.prefix() ? first + i * per : s.b);
+        armed |= 1u << r.s;
+        par = (par & ~(1u << r.s)) | (r.ph << r.s);
+      } else {
+        armed &= ~(1u << r.s);
+        const int here = min(n - i * kBM, kBM);  // rows of this query tile
+        for (int i0 = 0; i0 < here; i0 += 32) {
+          const __nv_bfloat16* src = nullptr;
+          if (i0 + lane < here) {
+            const RowPos x = row_pos(p, s, s.row0 + i * kBM + i0 + lane);
+            src = static_cast<const __nv_bfloat16*>(p.q) + x.b * p.q_sb + static_cast<int64_t>(s.hk * p.G + x.g) * p.q_sh +
+                  x.n * p.q_sn;
+          }
+          const int m = min(32, here - i0);
 #pragma unroll 4
-        for (int j = 0; j < m; j += kRows) {
-          const int i = j + sub;  // row of the 32
-          const unsigned long long from = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), i & 31);
-          const int row = (i0 + i) % kBM;
-          const int swz = C::kSwizzle == 128 ? ((c & 7) ^ (row & 7)) : (c ^ ((row >> 1) & 3));
-          const uint32_t dst = sbase + P::kOffQ + ((i0 + i) / kBM) * C::kTileBytes +
-                               (C::kSwizzle == 128 ? (c >> 3) * C::kChunkBytes : 0) + row * C::kSwizzle + swz * 16;
-          if (i < m)
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from + c * 16) : "memory");
+          for (int j = 0; j < m; j += kRows) {
+            const int k = j + sub;  // row of the 32
+            const unsigned long long from = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), k & 31);
+            const int row = i0 + k;
+            const int swz = C::kSwizzle == 128 ? ((c & 7) ^ (row & 7)) : (c ^ ((row >> 1) & 3));
+            const uint32_t dst =
+                tile + (C::kSwizzle == 128 ? (c >> 3) * C::kChunkBytes : 0) + row * C::kSwizzle + swz * 16;
+            if (k < m)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(from + c * 16) : "memory");
+          }
         }
       }
+      r.advance();
     }
     if (!asked) {
       asked = true;
@@ -559,12 +569,14 @@ __device__ void paged_gather_q(const PagedParams& p, uint32_t sbase, uint8_t* sm
       asm volatile("cp.async.wait_all;" ::: "memory");
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
-      if (lane == 0) mbar_arrive(bars.q_full());
+      if (lane < tiles) mbar_arrive(bars.q_full(slot0 ^ lane));
     }
-    ph ^= 1u;
   }
-  // boxes on their way must have landed before the CTA exits (those of earlier tasks were used)
-  if (box) ctl_wait(bars.q_full(), ph ^ 1u, ctl, -1, kRoleLoader, false);
+drain:
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  // boxes on their way must have landed before the CTA exits
+  for (int i = 0; i < 2; ++i)
+    if ((armed >> i) & 1u) ctl_wait(bars.q_full(i), (par >> i) & 1u, ctl, -1, kRoleLoader, false);
 }
 
 template <int D>
@@ -572,22 +584,30 @@ __device__ void paged_mma(const PagedParams& p, uint8_t* smem, uint32_t sbase, c
                           const Ctl& ctl) {
   using P = PCfg<D>;
   using C = Cfg<D>;
-  const uint64_t q0 = smem_desc(sbase + P::kOffQ, 16, 8 * C::kSwizzle, C::kLayout);
+  const uint64_t q_base = smem_desc(sbase + P::kOffQ, 16, 8 * C::kSwizzle, C::kLayout);
   const uint64_t k_base = smem_desc(sbase + P::kOffKV, 16, 8 * C::kSwizzle, C::kLayout);
   const uint64_t v_base = smem_desc(sbase + P::kOffKV, C::kChunkBytes, 8 * C::kSwizzle, C::kLayout);
   constexpr uint64_t kStep = static_cast<uint64_t>(C::kTileBytes >> 4);
-  uint32_t q_ph = 0, p_par = 0, o_par = 0;  // bit h of p_par, o_par: parity of stream h's next phase
+  uint32_t p_par = 0, o_par = 0;  // bit h of p_par, o_par: parity of stream h's next phase
   RingPos<P::kStages> r;
+  RingPos<2> q;
   SegReader<D> segs;
   PSeg s;
   grid_dep_wait();  // (the bound on the waits below is not for the kernel before)
   while (segs.template take<kRoleMma>(s, smem, bars, ctl)) {
-    if (!ctl_wait(bars.q_full(), q_ph, ctl, -1, kRoleMma)) goto drain;
-    q_ph ^= 1u;
+    const bool twin = s.twin();
+    const int slot0 = q.s;  // the task's query tiles: this slot, and the other
+    for (int i = 0; i < (twin ? 1 : 2); ++i) {
+      if (!ctl_wait(bars.q_full(q.s), q.ph, ctl, -1, kRoleMma)) goto drain;
+      q.advance();
+    }
     tc_fence_after();
     uint32_t o_ready = 0;
-    const bool twin = s.twin();
-    const uint64_t q1 = twin ? q0 : q0 + kStep;
+    const uint64_t q0 = q_base + slot0 * kStep, q1 = twin ? q0 : q_base + (slot0 ^ 1) * kStep;
+    auto q_done = [&]() {
+      mma_commit(bars.q_empty(slot0));
+      if (!twin) mma_commit(bars.q_empty(slot0 ^ 1));
+    };
     auto scores = [&](int h) {
       issue_s<D>(tmem + static_cast<uint32_t>(h) * C::tm_s(1), h ? q1 : q0, k_base + r.s * kStep);
       mma_commit(bars.s_full(h));
@@ -621,7 +641,7 @@ __device__ void paged_mma(const PagedParams& p, uint8_t* smem, uint32_t sbase, c
       if (!twin) scores(1);
       give();
     }
-    if (s.k0 + ahead >= s.k1) mma_commit(bars.q_empty());
+    if (s.k0 + ahead >= s.k1) q_done();
     for (int k = s.k0; k < s.k1; ++k) {
       const int kn = k + ahead;
       const bool more = kn < s.k1;
@@ -651,7 +671,7 @@ __device__ void paged_mma(const PagedParams& p, uint8_t* smem, uint32_t sbase, c
           give();
         }
       }
-      if (more && kn + 1 == s.k1) mma_commit(bars.q_empty());  // the task's last S is issued
+      if (more && kn + 1 == s.k1) q_done();  // the task's last S is issued
     }
     for (int h = 0; h < 2; ++h) {
       if (!((o_ready >> h) & 1u)) {  // a stream without a tile keeps its phases in step
@@ -963,9 +983,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
   volatile uint32_t* abort_flag = tmem_slot + 1;
 
   if (threadIdx.x == 0) {
-    mbar_init(bars.q_full(), 1);
-    mbar_init(bars.q_empty(), 1);
     for (int h = 0; h < 2; ++h) {
+      mbar_init(bars.q_full(h), 1);
+      mbar_init(bars.q_empty(h), 1);
       mbar_init(bars.s_full(h), 1);
       mbar_init(bars.p_full(h, 0), 4);
       mbar_init(bars.p_full(h, 1), 4);
