@@ -141,8 +141,9 @@ __device__ __forceinline__ Tiles own_tiles(const PagedParams& p, SeqLens s, int 
 
 // Units of a tile of a task that has `rows` rows left, and of the task.
 __device__ __forceinline__ int tile_units(int rows) { return rows > kBM ? kPagedPairTile : kPagedTile; }
+__device__ __forceinline__ int task_cost(int rows) { return rows > kBM ? kPagedPairTaskCost : kPagedTaskCost; }
 __device__ __forceinline__ int task_units(int tiles, int rows) {
-  return tiles > 0 ? kPagedTaskCost + tiles * tile_units(rows) : 0;
+  return tiles > 0 ? task_cost(rows) + tiles * tile_units(rows) : 0;
 }
 
 // Units of one sequence's tasks for one key head.
@@ -240,7 +241,7 @@ struct PSegIter {
         s.rows = p.Nq * p.G;
       }
       // a tile is the share's that holds its first unit
-      const int w = tile_units(s.rows - s.row0), first = a + kPagedTaskCost, end = first + tiles * w;
+      const int w = tile_units(s.rows - s.row0), first = a + task_cost(s.rows - s.row0), end = first + tiles * w;
       s.k0 = (max(u, first) - first + w - 1) / w;
       s.k1 = (max(min(hi, end), first) - first + w - 1) / w;
       if (s.rows - s.row0 <= kBM) s.flags |= PSeg::kTwin;
@@ -693,6 +694,17 @@ __device__ __forceinline__ float* paged_slot(const PagedParams& p, int cta, bool
   return p.slots + (static_cast<int64_t>((2 * cta + (first ? 1 : 0)) * 2 + tile) * 4 + quarter) * 32 * (D + 2);
 }
 
+// The buffer of uncut results: the prefix's rows by (key head, sequence, row of
+// the sequence), then, from a multiple of 32 on, the own ones by (sequence, key
+// head, row); both in groups of 32 rows laid out as the quarters of a slot.
+__device__ __forceinline__ int buffer_row(const PagedParams& p, bool prefix, int pair, int r) {
+  return pair * (p.Nq * p.G) + r + (prefix ? 0 : paged_rows32(p.B * p.Nq * p.Hq));
+}
+template <int D>
+__device__ __forceinline__ float* buffer_o(const PagedParams& p, int i) {
+  return p.rows_o + static_cast<int64_t>(i >> 5) * 32 * D + 4 * (i & 31);
+}
+
 template <int D>
 __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D>& bars, uint32_t tmem,
                               const Ctl& ctl) {
@@ -881,10 +893,12 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
     const int ch0 = twin ? (h * n_ch + 1) / 2 : 0, ch1 = twin ? (h ? n_ch : (n_ch + 1) / 2) : n_ch;
     const bool direct = s.whole() && p.prefix_tasks == 0;
     if (__any_sync(0xffffffffu, real)) {
-      // Where the row goes: its part of a cut task (float4 i at dst + 128 i), the
-      // buffer of uncut results (row-major), or the result.
+      // Where the row goes: its part of a cut task or its place in the buffer of
+      // uncut results (float4 i at dst + 128 i in both: 32 rows side by side, so
+      // that a warp's store is whole lines), or the result. (Trading 16-byte pieces
+      // between lanes, to store the result in whole 64-byte pieces of rows, gained
+      // nothing for 256 rows and took 15 % longer for 4: more code to fetch.)
       float* dst = nullptr;
-      int step = 4;
       __nv_bfloat16* out = nullptr;
       float inv = 0.f;
       if (direct) {
@@ -898,13 +912,12 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
       } else {
         float *pm, *pl;
         if (s.whole()) {
-          const int i = (bq * p.Hk + s.hk) * (p.Nq * p.G) + r + (s.prefix() ? 0 : p.B * p.Nq * p.Hq);
-          dst = p.rows_o + static_cast<int64_t>(i) * D;
+          const int i = buffer_row(p, s.prefix(), s.prefix() ? s.hk * p.B + bq : bq * p.Hk + s.hk, r);
+          dst = buffer_o<D>(p, i);
           pm = reinterpret_cast<float*>(p.rows_ml + i);
           pl = pm + 1;
         } else {
           dst = paged_slot<D>(p, blockIdx.x, s.first(), twin ? 0 : h, quarter) + 4 * lane;
-          step = 128;
           pm = dst - 3 * lane + 32 * D;
           pl = pm + 32;
         }
@@ -934,20 +947,22 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
 #pragma unroll
           for (int i = 0; i < 32; ++i) y[i] = __uint_as_float(a[i]);
         }
-        if (dst != nullptr) {
+        if (direct) {
+          if (out != nullptr) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                w[j] = none ? 0u : pack_bf16(y[8 * i + 2 * j] * inv, y[8 * i + 2 * j + 1] * inv);
+              *reinterpret_cast<uint4*>(out + ch * 32 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+        } else if (dst != nullptr) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
-            *reinterpret_cast<float4*>(dst + (ch * 8 + i) * step) =
+            *reinterpret_cast<float4*>(dst + (ch * 8 + i) * 128) =
                 make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-        } else if (out != nullptr) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              w[j] = none ? 0u : pack_bf16(y[8 * i + 2 * j] * inv, y[8 * i + 2 * j + 1] * inv);
-            *reinterpret_cast<uint4*>(out + ch * 32 + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
         }
       }
     }
@@ -1055,25 +1070,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 // maximum, sum and address, and adds float4 j, j + 8, ... of every part. The
 // slots keep 32 rows' float4 side by side, so four neighbouring rows read whole
 // 64-byte pieces (one row a warp took 11 us for 20 parts of 2048 rows, 32 lines
-// a load).
+// a load). Few rows may have many parts each: then the block's warps share four
+// rows, each taking eight parts of every 32, and the first adds up what they found.
 constexpr int kJoinWarps = 4;
 
-template <int D>
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __grid_constant__ PagedParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   grid_dep_wait();
   constexpr int kJ = D / 32;    // float4 of a lane
   constexpr int kBatch = 4;     // parts whose loads are in flight together
-  const int lane = threadIdx.x & 31, sub = lane >> 2, which = lane & 3;  // which of the four rows
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> 2, which = lane & 3;  // which of the four rows
   const int rows = p.B * p.Nq * p.Hq;  // below 2^30
   // rows in the order (key head, sequence, query, head of the group): neighbours in the prefix's slots too
-  const int at = (static_cast<int>(blockIdx.x) * kJoinWarps + (threadIdx.x >> 5)) * 4 + which;
+  const int at = (SPLIT ? static_cast<int>(blockIdx.x) : static_cast<int>(blockIdx.x) * kJoinWarps + warp) * 4 + which;
   const bool live = at < rows;
   const int rs = p.Nq * p.G, batch_rows = p.B * rs;
   const int hk = live ? p.by_batch_rows.div(at) : 0, rp = live ? at - hk * batch_rows : 0;
   const int b = p.by_rows.div(rp), r = rp - b * rs, bh = b * p.Hk + hk;
   const int t = r / kPagedTaskRows, tp = rp / kPagedTaskRows;
-  const int row = bh * rs + r;  // in the row buffers
 
   // the row's two tasks: where their parts are, and the row inside the task
   struct Span {
@@ -1095,33 +1110,32 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
   const bool mine = live && !(p.prefix_tasks == 0 && own.parts == 1);
   const int parts = mine ? pre.parts + own.parts : 0;
   const int most = __reduce_max_sync(0xffffffffu, parts);
+  if (SPLIT && warp > 0 && most <= 8) return;  // (the same for all of the block's warps)
 
   float4 acc[kJ];
 #pragma unroll
   for (int j = 0; j < kJ; ++j) acc[j] = make_float4(0.f, 0.f, 0.f, 0.f);
   float M = -CUDART_INF_F, L = 0.f;
-  for (int base = 0; base < most; base += 8) {
+  for (int base = SPLIT ? 8 * warp : 0; base < most; base += SPLIT ? 8 * kJoinWarps : 8) {
     const int i = base + sub, count = parts - base;  // of this row, from here on
-    const float* src = p.slots;  // float4 j of the row at src + j * step
+    const float* src = p.slots;  // float4 j of the row at src + 128 j
     float m = -CUDART_INF_F, l = 0.f;
-    int step = 4;
     if (i < parts) {
       const bool is_pre = i < pre.parts;
       const Span s = is_pre ? pre : own;
       const int k = is_pre ? i : i - pre.parts;
       if (s.parts == 1) {
-        const int64_t x = static_cast<int64_t>(is_pre ? 0 : rows) + row;
+        const int x = buffer_row(p, is_pre, is_pre ? hk * p.B + b : bh, r);
         const float2 ml = p.rows_ml[x];
         m = ml.x;
         l = ml.y;
-        src = p.rows_o + x * D;
+        src = buffer_o<D>(p, x);
       } else {
         const int quarter = (s.in_task % kBM) / 32, in_q = s.in_task % 32;
         const float* slot = paged_slot<D>(p, s.c0 + k, k == 0, s.in_task / kBM, quarter);
         m = slot[32 * D + in_q];
         l = slot[32 * D + 32 + in_q];
         src = slot + 4 * in_q;
-        step = 128;
       }
     }
     // the first batch's data is asked for beside the maxima, before they are known
@@ -1132,10 +1146,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
         const int holder = ((j0 + u) << 2) | which;
         const float* su = reinterpret_cast<const float*>(
             __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), holder));
-        const int st = __shfl_sync(0xffffffffu, step, holder);
         if (j0 + u < count) {
 #pragma unroll
-          for (int j = 0; j < kJ; ++j) v[u][j] = *reinterpret_cast<const float4*>(su + (sub + 8 * j) * st);
+          for (int j = 0; j < kJ; ++j) v[u][j] = *reinterpret_cast<const float4*>(su + (sub + 8 * j) * 128);
         }
       }
     };
@@ -1177,6 +1190,33 @@ __global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __
       }
     }
   }
+  if constexpr (SPLIT) if (most > 8) {
+    __shared__ float4 sh_acc[kJoinWarps - 1][kJ][32];
+    __shared__ float2 sh_ml[kJoinWarps - 1][32];
+    if (warp > 0) {
+      sh_ml[warp - 1][lane] = make_float2(M, L);
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) sh_acc[warp - 1][j][lane] = acc[j];
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 0; w < kJoinWarps - 1; ++w) {
+      const float2 ml = sh_ml[w][lane];
+      const float M1 = fmaxf(M, ml.x);
+      const float a = M == -CUDART_INF_F ? 0.f : ex2(M - M1), z = ml.x == -CUDART_INF_F ? 0.f : ex2(ml.x - M1);
+      M = M1;
+      L = fmaf(L, a, ml.y * z);
+#pragma unroll
+      for (int j = 0; j < kJ; ++j) {
+        const float4 v = sh_acc[w][j][lane];
+        acc[j].x = fmaf(acc[j].x, a, v.x * z);
+        acc[j].y = fmaf(acc[j].y, a, v.y * z);
+        acc[j].z = fmaf(acc[j].z, a, v.z * z);
+        acc[j].w = fmaf(acc[j].w, a, v.w * z);
+      }
+    }
+  }
   if (!mine) return;
   const int n = p.by_g.div(r), head = hk * p.G + r - n * p.G;
   const bool none = M == -CUDART_INF_F;
@@ -1210,10 +1250,12 @@ cudaError_t launch_paged_dim(const PagedParams& p, cudaStream_t s) {
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, paged_kernel<D>, p)) != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.B) * p.Nq * p.Hq;
-  cfg.gridDim = dim3(static_cast<unsigned>((rows + 4 * kJoinWarps - 1) / (4 * kJoinWarps)));
+  const int64_t per_block = p.join_split ? 4 : 4 * kJoinWarps;
+  cfg.gridDim = dim3(static_cast<unsigned>((rows + per_block - 1) / per_block));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, p);
+  const auto join = p.join_split ? paged_join_kernel<D, true> : paged_join_kernel<D, false>;
+  return cudaLaunchKernelEx(&cfg, join, p);
 }
 
 }  // namespace dev

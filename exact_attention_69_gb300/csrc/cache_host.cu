@@ -174,6 +174,14 @@ int64_t bwd_workspace(const attn_rope_bwd_params* p, int blocks) {
 
 int64_t up256(int64_t x) { return (x + 255) & ~int64_t{255}; }
 
+// The join's blocks take four rows each, parts dealt to their warps, if rows are few
+// (up to kJoinSplitRows an SM) and may have more than kJoinParts parts; else sixteen.
+// Shared blocks and not, d = 128: 64 x 8 rows x 2 key heads behind 8192 tokens 23.6
+// and 30.3 us, 8 x 32 x 8 behind 2048 19.2 and 22.1, 32 x 4 x 8 behind 4096 28.8 and
+// 29.9; 64 an SM instead of 16: 32 x 16 x 8 behind 512 23.8 and 21.5. Own keys only, a
+// task and more a CTA, so a part or two a row: 57 x 4 x 8 22.4 and 20.7.
+constexpr int kJoinSplitRows = 16, kJoinParts = 8;
+
 struct PagedPlan {
   int grid = 0;
   bool batched = false;  // the prefix's tiles once for rows of several sequences
@@ -201,22 +209,28 @@ void plan_paged(const attn_paged_params* p, int sms, PagedPlan* pl) {
   pl->grid = p->num_ctas > 0 && p->num_ctas < sms ? p->num_ctas : sms;
   const int64_t rows = static_cast<int64_t>(p->B) * p->Nq * p->Hq;
   // Batched: 256 rows of the batch read the prefix's tiles together, and each
-  // row's prefix part and own part go through the workspace to the join, which
-  // for 256 rows moves as many bytes as kJoinTiles K/V tiles (d fp32 written and
-  // read, twice). Otherwise each sequence's tasks go over the prefix and its own
-  // keys in one go. Few rows a sequence (decoding): batched, unless the prefix
-  // is a tile or two for one sequence; hundreds (prompt chunks): not. Measured
-  // batched and not: 32 sequences of one token behind 4096 shared ones 30 and
-  // 107 us, 96 behind 32768 127 and 1219 us; 3 x 512 tokens behind 2048 54 and 40 us.
-  constexpr int kJoinTiles = 8;
+  // row's prefix part and own part go through the workspace to the join.
+  // Otherwise each sequence's tasks go over the prefix and its own keys in one
+  // go. What batching saves is tiles, what it costs are the prefix tasks' start
+  // and end and a longer join, so it has to save some tiles a CTA: one if a key
+  // head's rows fit one query tile, five if not. Measured at d = 128 with 256 own
+  // keys, batched and not (sequences x rows x key heads, prefix):
+  //   one tile:  16 x 8 x 2, 512: 0.8 saved, 13.8 and 13.3 us; 2048: 3.1, 15.3 and 17.1
+  //              4 x 4 x 8, 512: 0.6, 13.6 and 13.5;  16 x 4 x 8, 512: 3.1, 16.3 and 17.8
+  //   pairs:     64 x 8 x 2, 512: 3.2, 20.5 and 18.5; 8 x 32 x 8, 2048: 5.8, 18.6 and 19.9
+  //              32 x 16 x 8, 512: 6.2, 25.5 and 26.0; 2048: 25, 28.8 and 39.9
+  //   96 x 4 x 8 behind 32768: 123 and 1141;  3 x 512 x 16 behind 2048 (saves none): 54 and 40
+  constexpr int kGainOne = 1, kGainPair = 5;
   const int64_t rs = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk), tr = attn::kPagedTaskRows;
   const int64_t own = (rs + tr - 1) / tr, pre = (p->B * rs + tr - 1) / tr, tiles = (static_cast<int64_t>(p->prefix_len) + 127) / 128;
-  pl->batched = p->prefix_len > 0 && p->B * own * tiles > pre * (tiles + 1) + kJoinTiles * p->B * rs / tr;
+  const int64_t gain = p->Hk * (p->B * own * tiles - pre * (tiles + 1));
+  pl->batched = gain > pl->grid * (p->B * rs <= attn::kBM ? kGainOne : kGainPair);
   pl->tasks = up256((p->B * p->Hk * own + (pl->batched ? p->Hk * pre : 0)) * static_cast<int64_t>(sizeof(int2)));
   pl->slots = up256(static_cast<int64_t>(pl->grid) * 4 * 128 * (p->d + 2) * 4);
   if (pl->batched) {
-    pl->rows_o = up256(2 * rows * p->d * 4);
-    pl->rows_ml = up256(2 * rows * 8);
+    const int64_t rows32 = attn::paged_rows32(static_cast<int>(rows));
+    pl->rows_o = up256(2 * rows32 * p->d * 4);
+    pl->rows_ml = up256(2 * rows32 * 8);
   }
 }
 
@@ -448,8 +462,8 @@ int attn_paged(const attn_paged_params* p) {
   const int64_t G = p->Hq / p->Hk, tasks_own = (p->Nq * G + attn::kPagedTaskRows - 1) / attn::kPagedTaskRows,
                 tasks_pre = (static_cast<int64_t>(p->B) * p->Nq * G + attn::kPagedTaskRows - 1) / attn::kPagedTaskRows;
   const double most = static_cast<double>(p->Hk) * attn::kPagedPairTile *
-                      (static_cast<double>(tasks_pre) * (p->prefix_len / 128 + 2) +
-                       static_cast<double>(p->B) * tasks_own * (static_cast<double>(max_len + p->prefix_len) / 128 + 3));
+                      (static_cast<double>(tasks_pre) * (p->prefix_len / 128 + 5) +
+                       static_cast<double>(p->B) * tasks_own * (static_cast<double>(max_len + p->prefix_len) / 128 + 6));
   if (most >= static_cast<double>(kMaxCount)) return fail_with(ATTN_ERR_INVALID_ARG, "problem too large");
   if (p->workspace && !aligned(p->workspace, 16)) return fail_with(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
 
@@ -498,10 +512,10 @@ int attn_paged(const attn_paged_params* p) {
   k.prefix_len = p->prefix_len;
   k.prefix_tiles = (p->prefix_len + attn::kBN - 1) / attn::kBN;
   k.prefix_tasks = pl.batched ? static_cast<int>(tasks_pre) : 0;
-  const int full = attn::kPagedTaskCost + k.prefix_tiles * attn::kPagedPairTile;
+  const int full = attn::kPagedPairTaskCost + k.prefix_tiles * attn::kPagedPairTile;
   int head = k.prefix_tasks * full;  // (the last task may have one query tile)
   if (p->B * p->Nq * G - (tasks_pre - 1) * attn::kPagedTaskRows <= attn::kBM)
-    head -= k.prefix_tiles * (attn::kPagedPairTile - attn::kPagedTile);
+    head -= attn::kPagedPairTaskCost - attn::kPagedTaskCost + k.prefix_tiles * (attn::kPagedPairTile - attn::kPagedTile);
   if (!pl.batched) head = 0;
   k.prefix_units = p->Hk * head;
   k.own_tasks = static_cast<int>(tasks_own);
@@ -522,6 +536,8 @@ int attn_paged(const attn_paged_params* p) {
   k.timeout_ns = p->timeout_ns ? p->timeout_ns : attn::host::kTimeoutNs;
   k.inject = p->inject;
   k.grid = pl.grid;
+  const int64_t fewest = p->Hk * (pl.batched && tasks_pre < p->B * tasks_own ? tasks_pre : p->B * tasks_own);
+  k.join_split = static_cast<int64_t>(p->B) * p->Nq * p->Hq <= kJoinSplitRows * int64_t{sms} && fewest * kJoinParts < pl.grid;
   attn::host::paged_used(dev);
   const cudaError_t e = attn::launch_paged(k, p->d, attn::host::stream_of(p->stream));
   return e == cudaSuccess ? ATTN_OK : attn::host::cuda_error(e, "paged attention launch");

@@ -15,8 +15,10 @@ constexpr int kPagedTaskRows = 256;  // two 128-row query tiles
 // little longer (with 4 / 5 / 6 units 96 sequences behind 32768 tokens took 144.6 /
 // 137.9 / 143.9 us); a task's start and end as long as a tile (2 / 4 / 6 units: 32
 // sequences behind 4096 tokens 33.6 / 30.0 / 29.7 us, 16 of up to 4096 own keys at
-// d = 32 14.5 / 12.7 / 13.4 us).
-constexpr int kPagedTile = 4, kPagedPairTile = 5, kPagedTaskCost = 4;
+// d = 32 14.5 / 12.7 / 13.4 us), that of two query tiles longer (4 / 8 / 16 units: 64
+// sequences of 4 rows x 8 key heads behind 512 tokens 35.3 / 30.9 / 30.7 us, 3 x 512
+// tokens x 16 heads behind 2048 43.6 / 43.0 / 42.3 us).
+constexpr int kPagedTile = 4, kPagedPairTile = 5, kPagedTaskCost = 4, kPagedPairTaskCost = 16;
 // Least work that opens another CTA; no less than a tile. (5 / 8 / 16 / 24: 4 sequences
 // behind 512 tokens 11.0 / 10.4 / 12.7 / 17.0 us; larger calls have a CTA an SM anyway.)
 constexpr int kPagedMinUnits = 8;
@@ -38,6 +40,9 @@ struct FastDiv {
   }
 #endif
 };
+
+// Rows of a buffer half, whole groups of 32.
+__host__ __device__ constexpr int paged_rows32(int rows) { return (rows + 31) & ~31; }
 
 struct PagedParams {
   CUtensorMap tm_k;             // 4-D (d, slot, head, page) bf16 maps, box (swizzle span, min(page, 128), 1, 1)
@@ -73,8 +78,9 @@ struct PagedParams {
   // workspace
   int2* tasks;                  // [B * Hk * own_tasks | Hk * prefix_tasks]: first CTA and parts of each
   float* slots;                 // per CTA 2 x 2 query tiles x 128 rows x (d + 2): parts of cut tasks
-  float* rows_o;                // [2][B * Nq * Hq][d]: uncut prefix and own results
-  float2* rows_ml;              // [2][B * Nq * Hq]: their running maximum (log2 units) and sum
+  float* rows_o;                // [2][paged_rows32(B * Nq * Hq)][d]: uncut prefix and own results
+  float2* rows_ml;              // [2][paged_rows32(B * Nq * Hq)]: their running maximum (log2 units) and sum
+  int join_split;               // the join's blocks take four rows, not four rows a warp
   int grid;                     // CTAs of the attention kernel
   uint64_t timeout_ns;
   int inject;

@@ -124,6 +124,31 @@ def test_cuts(E, case, ctas, mask):
     Problem(Hq, Hk, d, Nq, P, lens, page, q_lens, seed=200).check(E, mask, num_ctas=ctas)
 
 
+@pytest.mark.parametrize("mask", ["none", "causal_br"])
+@pytest.mark.parametrize("case", [c for c in CASES if c[4] > 0], ids=str)
+def test_prefix_tasks(E, case, mask):
+    """Few CTAs, where going over the prefix once for the batch pays earliest."""
+    Hq, Hk, d, Nq, P, lens, page, q_lens = case
+    Problem(Hq, Hk, d, Nq, P, lens, page, q_lens, seed=400).check(E, mask, num_ctas=2)
+
+
+@pytest.mark.parametrize("case", [
+    # prefix rows in boxes of several sequences, gathered, in one and in two query tiles
+    (8, 2, 64, 1, 600, [(7 * i) % 90 for i in range(100)], 16, None),
+    (4, 2, 32, 4, 700, [(11 * i) % 70 for i in range(90)], 32, [1 + i % 4 for i in range(90)]),
+    (6, 2, 128, 5, 500, [(13 * i) % 60 for i in range(120)], 16, None),
+    (4, 4, 64, 8, 1500, [(5 * i) % 40 for i in range(16)], 64, None),
+    # rows of many parts each: more than eight, and more than one warp's share
+    (4, 1, 128, 1, 6000, [3000, 2500], 64, None),
+    (4, 2, 64, 4, 7000, [50, 4000, 0], 16, None),
+    (2, 1, 32, 2, 17000, [100], 128, None),
+    (1, 1, 64, 1, 0, [20000], 256, None),
+], ids=str)
+def test_shared_prefixes_and_many_parts(E, case):
+    Hq, Hk, d, Nq, P, lens, page, q_lens = case
+    Problem(Hq, Hk, d, Nq, P, lens, page, q_lens, seed=450).check(E)
+
+
 def test_rising_maxima(E):
     """Scores that grow along the keys (the running maximum is raised tile after tile) and
     parts whose maxima are far apart."""
