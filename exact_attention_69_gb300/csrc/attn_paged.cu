@@ -124,12 +124,13 @@ struct SeqLens {
   int len, ql;
 };
 
-__device__ __forceinline__ SeqLens seq_lens(const PagedParams& p, int b) {
-  SeqLens s;
-  s.len = clampi(p.kv_lens[b], 0, p.max_len);
-  s.ql = p.q_lens != nullptr ? clampi(p.q_lens[b], 0, p.Nq) : p.Nq;
-  return s;
+__device__ __forceinline__ SeqLens raw_lens(const PagedParams& p, int b) {
+  return SeqLens{p.kv_lens[b], p.q_lens != nullptr ? p.q_lens[b] : p.Nq};
 }
+__device__ __forceinline__ SeqLens clamp_lens(const PagedParams& p, SeqLens s) {
+  return SeqLens{clampi(s.len, 0, p.max_len), clampi(s.ql, 0, p.Nq)};
+}
+__device__ __forceinline__ SeqLens seq_lens(const PagedParams& p, int b) { return clamp_lens(p, raw_lens(p, b)); }
 
 // Keys that query n of a sequence sees, counted from the prefix's first.
 __device__ __forceinline__ int keys_seen(const PagedParams& p, SeqLens s, int n) {
@@ -189,20 +190,15 @@ struct PSegIter {
   int u, hi;       // units left: [u, hi)
   int up;          // units of the prefix tasks
   int b, sb;       // current sequence and its first unit
-  SeqLens cur, nxt;
+  SeqLens cur, nxt;  // its lengths, and the next one's as they are in memory (nobody waits for them yet)
   int ub;          // its units per key head
   int at_head = -1, at_a = -1, at_t = 0;  // first unit of the own head and task looked at last, and its number
   int task, parts_end;  // of the segment: index in the task table; its last tile's first unit
 
   // u0: the CTA's first unit; b0, s0: the sequence that holds it (or the next) and its first unit.
-  __device__ __forceinline__ PSegIter(const PagedParams& p, int u0, int u1, int b0, int s0, int ub0)
-      : u(u0), hi(u1), up(p.prefix_units), b(b0), sb(s0), ub(ub0) {
-    cur.len = cur.ql = 0;
-    nxt = cur;
-    if (u < hi && b < p.B) {
-      cur = seq_lens(p, b);
-      if (b + 1 < p.B) nxt = seq_lens(p, b + 1);
-    }
+  __device__ __forceinline__ PSegIter(const PagedParams& p, int u0, int u1, int b0, int s0, int ub0, SeqLens lens0)
+      : u(u0), hi(u1), up(p.prefix_units), b(b0), sb(s0), cur(lens0), nxt{0, 0}, ub(ub0) {
+    if (b + 1 < p.B) nxt = raw_lens(p, b + 1);
   }
   __device__ __forceinline__ bool next(const PagedParams& p, PSeg& s) {
     while (u < hi) {
@@ -223,9 +219,9 @@ struct PSegIter {
         while (u >= sb + p.Hk * ub) {
           sb += p.Hk * ub;
           ++b;
-          cur = nxt;
+          cur = clamp_lens(p, nxt);
           ub = own_units(p, cur);
-          if (b + 1 < p.B) nxt = seq_lens(p, b + 1);
+          if (b + 1 < p.B) nxt = raw_lens(p, b + 1);
         }
         s.flags = 0;
         s.b = b;
@@ -338,11 +334,13 @@ __device__ void paged_scheduler(const PagedParams& p, uint8_t* smem, const PBars
   int v = 0, sum = 0, u0 = 0, u1 = 0;
   int b0 = 0, s0 = p.prefix_units;  // the sequence that holds u0 (or the first behind it), its first unit
   int ub = 0;                       // and its units per key head
+  SeqLens lens{0, 0};               // and its lengths
   Split split(0, 1);
   SeqLens first[4];                 // of the first 128 sequences, all asked for at once
 #pragma unroll
   for (int j = 0; j < 4; ++j)
     if (32 * j + lane < p.B) first[j] = seq_lens(p, 32 * j + lane);
+  SeqLens sl{0, 0};                 // of this lane's sequence of the 32 looked at
   for (int pass = 0, at = 0;; at += 32) {
     if (at >= p.B) {
       if (pass == 1) break;
@@ -354,7 +352,7 @@ __device__ void paged_scheduler(const PagedParams& p, uint8_t* smem, const PBars
       if (u0 >= u1) break;
     }
     if (pass == 0 || p.B > 32) {
-      SeqLens sl = first[0];
+      sl = first[0];
       if (at > 0) sl = at == 32 ? first[1] : at == 64 ? first[2] : at == 96 ? first[3] : seq_lens(p, min(at + lane, p.B - 1));
       v = at + lane < p.B ? own_units(p, sl) : 0;
     }
@@ -373,12 +371,13 @@ __device__ void paged_scheduler(const PagedParams& p, uint8_t* smem, const PBars
     if (i >= 0) {
       s0 += p.Hk * __shfl_sync(0xffffffffu, inc - v, i);
       ub = __shfl_sync(0xffffffffu, v, i);
+      lens = SeqLens{__shfl_sync(0xffffffffu, sl.len, i), __shfl_sync(0xffffffffu, sl.ql, i)};
       b0 = at + i;
       break;
     }
     s0 += p.Hk * __shfl_sync(0xffffffffu, inc, 31);
   }
-  PSegIter it(p, u0, u1, b0, s0, ub);
+  PSegIter it(p, u0, u1, b0, s0, ub, lens);
   RingPos<P::kSegs> r;
   for (bool more = true; more;) {
     PSeg s;
