@@ -31,8 +31,8 @@
 //
 // What bounds it, and what it takes (GPU time of both kernels, captured calls):
 //   - Long keys of few rows: memory. 64 sequences x 2048 own keys, 8 key heads, d = 128,
-//     pages of 64: 89.5 us, 6.0 TB/s. 96 sequences behind 32768 tokens, G = 4: 123 us
-//     for 556 MB, 4.5 TB/s (softmax of the prefix's two query tiles, and the cuts).
+//     pages of 64: 89.5 us, 6.0 TB/s. 96 sequences behind 32768 tokens, G = 4: 121 us
+//     for 556 MB, 4.6 TB/s (softmax of the prefix's two query tiles, and the cuts).
 //   - Prompt chunks: the tile of two query tiles, 2900 cycles, the pace of this library's
 //     forward kernel with 128 channels; 3 x 512 tokens x 16 heads behind 2048: 39 us.
 //   - Short keys: latency. A task of one or two tiles takes 3.7 to 4.2 us, one step after
@@ -40,7 +40,7 @@
 //     the next), O, the exchange, the store. The next task's tiles and queries wait in
 //     shared memory meanwhile. A launch takes 5 us to its first tile (lengths, shares,
 //     page numbers, tiles, one after the other) and the join some 4 more: 4 sequences
-//     behind 512 tokens 10.4 us, 32 behind 4096 29 us.
+//     behind 512 tokens 10.4 us, 32 behind 4096 27 us.
 //
 // P is rounded to bf16 for the second product (the tensor core's input type;
 // the row sum takes the unrounded values), which moves O by at most 2^-8 of
@@ -1084,14 +1084,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_kernel(const __grid_constan
 // 64-byte pieces (one row a warp took 11 us for 20 parts of 2048 rows, 32 lines
 // a load). Few rows may have many parts each: then the block's warps share four
 // rows, each taking eight parts of every 32, and the first adds up what they found.
+// kBatch parts' loads are in flight together: eight want twice the registers.
 constexpr int kJoinWarps = 4;
 
-template <int D, bool SPLIT>
-__global__ void __launch_bounds__(kJoinWarps * 32, 4) paged_join_kernel(const __grid_constant__ PagedParams p) {
+template <int D, bool SPLIT, int kBatch>
+__global__ void __launch_bounds__(kJoinWarps * 32, kBatch > 4 ? 2 : 4) paged_join_kernel(const __grid_constant__ PagedParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   grid_dep_wait();
   constexpr int kJ = D / 32;    // float4 of a lane
-  constexpr int kBatch = 4;     // parts whose loads are in flight together
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane >> 2, which = lane & 3;  // which of the four rows
   const int rows = p.B * p.Nq * p.Hq;  // below 2^30
   // rows in the order (key head, sequence, query, head of the group): neighbours in the prefix's slots too
@@ -1262,11 +1262,13 @@ cudaError_t launch_paged_dim(const PagedParams& p, cudaStream_t s) {
   cfg.numAttrs = 1;
   if ((e = cudaLaunchKernelEx(&cfg, paged_kernel<D>, p)) != cudaSuccess) return e;
   const int64_t rows = static_cast<int64_t>(p.B) * p.Nq * p.Hq;
-  const int64_t per_block = p.join_split ? 4 : 4 * kJoinWarps;
+  const int64_t per_block = p.join == PagedParams::kJoinSplit ? 4 : 4 * kJoinWarps;
   cfg.gridDim = dim3(static_cast<unsigned>((rows + per_block - 1) / per_block));
   cfg.blockDim = dim3(kJoinWarps * 32);
   cfg.dynamicSmemBytes = 0;
-  const auto join = p.join_split ? paged_join_kernel<D, true> : paged_join_kernel<D, false>;
+  const auto join = p.join == PagedParams::kJoinSplit ? paged_join_kernel<D, true, 8>
+                    : p.join == PagedParams::kJoinFew ? paged_join_kernel<D, false, 8>
+                                                      : paged_join_kernel<D, false, 4>;
   return cudaLaunchKernelEx(&cfg, join, p);
 }
 

@@ -180,7 +180,12 @@ int64_t up256(int64_t x) { return (x + 255) & ~int64_t{255}; }
 // and 30.3 us, 8 x 32 x 8 behind 2048 19.2 and 22.1, 32 x 4 x 8 behind 4096 28.8 and
 // 29.9; 64 an SM instead of 16: 32 x 16 x 8 behind 512 23.8 and 21.5. Own keys only, a
 // task and more a CTA, so a part or two a row: 57 x 4 x 8 22.4 and 20.7.
-constexpr int kJoinSplitRows = 16, kJoinParts = 8;
+// Sixteen rows a block: eight parts' loads in flight up to kJoinFewRows rows an SM
+// (32 x 16 x 8 behind 2048 24.4 us, four 26.8; 96 x 4 x 8 behind 32768 121.0 and
+// 123.5), four above (32 x 32 x 8 behind 2048 29.9 us, eight 31.4; 3 x 512 x 16
+// behind 2048 38.5 and 41.9). Shared blocks have eight (four: 20.0 and not 18.1 us
+// for 64 x 8 x 2 behind 2048).
+constexpr int kJoinSplitRows = 16, kJoinParts = 8, kJoinFewRows = 32;
 
 struct PagedPlan {
   int grid = 0;
@@ -537,7 +542,10 @@ int attn_paged(const attn_paged_params* p) {
   k.inject = p->inject;
   k.grid = pl.grid;
   const int64_t fewest = p->Hk * (pl.batched && tasks_pre < p->B * tasks_own ? tasks_pre : p->B * tasks_own);
-  k.join_split = static_cast<int64_t>(p->B) * p->Nq * p->Hq <= kJoinSplitRows * int64_t{sms} && fewest * kJoinParts < pl.grid;
+  const int64_t rows = static_cast<int64_t>(p->B) * p->Nq * p->Hq;
+  k.join = rows <= kJoinSplitRows * int64_t{sms} && fewest * kJoinParts < pl.grid ? attn::PagedParams::kJoinSplit
+           : rows <= kJoinFewRows * int64_t{sms}                                  ? attn::PagedParams::kJoinFew
+                                                                                  : attn::PagedParams::kJoinMany;
   attn::host::paged_used(dev);
   const cudaError_t e = attn::launch_paged(k, p->d, attn::host::stream_of(p->stream));
   return e == cudaSuccess ? ATTN_OK : attn::host::cuda_error(e, "paged attention launch");

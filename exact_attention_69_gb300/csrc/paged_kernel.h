@@ -80,7 +80,8 @@ struct PagedParams {
   float* slots;                 // per CTA 2 x 2 query tiles x 128 rows x (d + 2): parts of cut tasks
   float* rows_o;                // [2][paged_rows32(B * Nq * Hq)][d]: uncut prefix and own results
   float2* rows_ml;              // [2][paged_rows32(B * Nq * Hq)]: their running maximum (log2 units) and sum
-  int join_split;               // the join's blocks take four rows, not four rows a warp
+  enum { kJoinMany, kJoinFew, kJoinSplit };
+  int join;                     // the join's form: see the rule's comment in cache_host.cu
   int grid;                     // CTAs of the attention kernel
   uint64_t timeout_ns;
   int inject;
