@@ -801,9 +801,11 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
               m_ref = m_piece;
             }
             sum2 = __fmul2_rn(sum2, make_float2(alpha, alpha));
+            // The piece before may have scaled O too, and stored P: both are read again here,
+            // and stores to TMEM are not in order with the loads behind them.
+            if (j > 0) tmem_wait_st();
             if (!first) rescale_o<D>(t_o, alpha);
             if (j > 0) {
-              tmem_wait_st();
               for (int q = 0; q < j; ++q) {
                 uint32_t pp[32];
                 tmem_ld32(t_p + 32 * q, pp);
