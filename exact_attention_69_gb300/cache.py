@@ -492,8 +492,10 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     once for all of its queries), then kv_lens[b] tokens of the pages in block_table[b].
     Its queries are the last q_lens[b] of these tokens (None: Nq); rows behind q_lens[b]
     are padding. mask 'causal_br': row i sees keys up to i + T - q_lens[b], T = prefix_len
-    + kv_lens[b]; 'none': every real row sees all T. A row that sees no key gives 0 and
-    an LSE of -inf. Lengths and tables are read when the kernels run.
+    + kv_lens[b]; 'none': every real row sees all T. A row that sees no key (or only
+    scores of -inf) gives 0 and an LSE of -inf, one with a score that is NaN or +inf NaN
+    for both. Values (v_cache) of keys that only some rows of a sequence see must be
+    finite. Lengths and tables are read when the kernels run.
 
     Returns (o, lse) or o; no gradient goes through it. Raises for what the host can check; a bad table entry reads
     as zeros, a length beyond the table's end is cut.

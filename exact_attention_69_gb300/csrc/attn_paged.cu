@@ -871,6 +871,10 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
     }
 
     ring += 2u * static_cast<uint32_t>(s.k1 - s.k0);
+    // A score that is NaN makes the sum NaN but not the maximum (fmaxf drops it), which may
+    // still be -inf, "saw no key", or so low that the join gives the part no weight. +inf
+    // brings the NaN through every join: exp2 of inf - inf.
+    if (l != l) m_ref = CUDART_INF_F;
 
     // the end of the segment: O of this row, to its part, its buffer or the result
     float m = m_ref, w0 = 1.f, w1 = 0.f;

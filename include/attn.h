@@ -442,8 +442,9 @@ int64_t attn_qk_norm_rope_bwd_workspace_bytes(const attn_rope_bwd_params* p);
  *   ATTN_MASK_CAUSAL_BR  row i sees keys j <= i + T - q_lens[b]
  *   ATTN_MASK_NONE       every row i < q_lens[b] sees all T keys
  *   O[b,h,i,:] = sum_j softmax_j(scale q . k_j) v_j,  LSE the natural-log sum.
- * A row that sees no key gives O = 0, LSE = -inf. Query head h reads key head
- * h / (Hq / Hk). The prefix's keys are read once for up to 256 query rows
+ * A row that sees no key, or none whose score is above -inf, gives O = 0,
+ * LSE = -inf; one with a score that is NaN or +inf gives NaN for both. Query
+ * head h reads key head h / (Hq / Hk). The prefix's keys are read once for up to 256 query rows
  * (Nq * Hq / Hk of each sequence), not once per sequence.
  * Lengths and tables are read on the device when the kernels run. kv_lens is
  * clamped to what the table holds, q_lens to Nq; a table entry that is not a

@@ -1,10 +1,11 @@
 """GPU: paged attention where its arithmetic is at an edge: maxima that jump inside a
-tile. Against the definition in 64 bits (bounds in cache_oracle)."""
+tile, NaN and infinities in keys and queries that are seen. Against the definition in 64 bits (bounds in cache_oracle)."""
 import math
 
 import pytest
 import torch
 
+from tests import cache_oracle as O
 from tests.test_gpu_paged import E, Problem  # noqa: F401  (E: fixture)
 
 pytestmark = pytest.mark.gpu
@@ -45,3 +46,83 @@ def test_maxima_jump_in_both_halves_of_a_tile(E, Hq, Hk, Nq, P, lens, d, rows): 
                                 "every second": lambda r: r % 2 == 0}[rows])
     for ctas in (1, 3):
         p.check(E, num_ctas=ctas)
+
+
+def check_nan(name, got, ref, bound):
+    """As O.check, and NaN where the definition has NaN."""
+    got = got.double().cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(ref)), f"{name}: NaN in the wrong places"
+    rest = ~torch.isnan(ref)
+    O.check(name, got[rest], ref[rest], bound[rest])
+
+
+# whole in one CTA, cut over many, prefix apart from the own keys, pairs of query tiles
+NAN_CASES = [(4, 2, 64, 1, 0, [700, 0, 40], 16, 1), (4, 2, 128, 1, 0, [900, 33], 32, 0),
+             (8, 2, 64, 1, 600, [(7 * i) % 90 + 1 for i in range(60)], 16, 0),
+             (4, 2, 32, 2, 1500, [1, 300, 2], 16, 2), (2, 1, 64, 100, 260, [100, 500], 64, 3)]
+
+
+@pytest.mark.parametrize("case", NAN_CASES, ids=str)
+@pytest.mark.parametrize("where", ["query", "half of a query", "first prefix or own key", "last own key"])
+def test_nan_scores_give_nan(E, case, where):  # noqa: F811
+    """A score that is NaN and seen makes its row NaN, O and LSE, whatever the cuts are: all
+    of a row's scores, or one key's (alone in its part, or far below the other scores)."""
+    Hq, Hk, d, Nq, P, lens, page, ctas = case
+    p = Problem(Hq, Hk, d, Nq, P, lens, page, seed=3100)
+    nan = float("nan")
+    if where == "query":
+        p.q[0, 1, Nq - 1] = nan
+    elif where == "half of a query":
+        p.q[-1, :, 0, d // 2:] = nan
+    elif where == "first prefix or own key":
+        if P:
+            p.k[int(p.prefix[0]), 0, 0, 3] = nan
+        else:
+            p.k[int(p.table[0, 0]), 0, 0, 3] = nan
+    else:
+        at = lens[-1] - 1
+        p.k[int(p.table[-1, at // page]), -1, at % page, 0] = nan
+    q, k, v, table, ln, q_lens, prefix = p.cuda()
+    o, lse = E.attn_paged(q, k, v, table, ln, q_lens=q_lens, prefix_table=prefix, prefix_len=P, num_ctas=ctas)
+    assert E.device_status()[0] == 0
+    # (slots that no sequence holds are NaN too: the definition never looks at them)
+    ro, bo, rl, bl = O.paged(p.q, p.k, p.v, p.table, p.lens, p.q_lens, p.prefix, P, 1 / math.sqrt(d), "causal_br")
+    assert bool(torch.isnan(rl).any())
+    check_nan("o", o, ro, bo)
+    check_nan("lse", lse, rl, bl)
+
+
+@pytest.mark.parametrize("ctas", [1, 0])
+def test_nan_key_in_a_part_without_weight(E, ctas):  # noqa: F811
+    """A NaN key among keys whose weights underflow (scores 300 log2 units lower)."""
+    p = Problem(4, 1, 64, 1, 0, [2000], 32, seed=3200)
+    stairs(p, 4, 1, 64, 12.0, lambda r: True)
+    p.k[int(p.table[0, 0]), 0, 5] = float("nan")
+    q, k, v, table, ln, _, _ = p.cuda()
+    o, lse = E.attn_paged(q, k, v, table, ln, num_ctas=ctas)
+    assert bool(torch.isnan(o).all()) and bool(torch.isnan(lse).all())
+
+
+def test_infinite_scores(E):  # noqa: F811
+    """+inf: NaN for O and LSE. -inf: a key without weight; a row with no other has seen
+    nothing."""
+    p = Problem(2, 1, 64, 1, 0, [300, 300, 20], 16, seed=3300)
+    p.q = p.q.abs() + 0.1
+    inf = float("inf")
+    p.k[int(p.table[0, 2]), 0, 3] = inf
+    p.k[int(p.table[1, 0]), 0, :9] = -inf
+    for j in range(20):
+        p.k[int(p.table[2, j // 16]), 0, j % 16] = -inf
+    # sequence 1 without those keys, in pages of its own
+    k1, v1 = (torch.zeros(1, 1, 304, 64, dtype=torch.bfloat16) for _ in range(2))
+    for j in range(9, 300):
+        at = int(p.table[1, j // 16]), 0, j % 16
+        k1[0, 0, j - 9], v1[0, 0, j - 9] = p.k[at], p.v[at]
+    ro, bo, rl, bl = O.paged(p.q[1:2], k1, v1, torch.zeros(1, 1, dtype=torch.int32), [291], None, None, 0, 1 / 8, "causal_br")
+    for ctas in (1, 0):
+        q, k, v, table, ln, _, _ = p.cuda()
+        o, lse = E.attn_paged(q, k, v, table, ln, num_ctas=ctas)
+        assert bool(torch.isnan(o[0]).all()) and bool(torch.isnan(lse[0]).all())
+        assert float(o[2].abs().max()) == 0.0 and bool((lse[2] == -inf).all())
+        O.check("o", o[1:2], ro, bo)
+        O.check("lse", lse[1:2], rl, bl)
