@@ -770,7 +770,8 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
         // it once a task: 7000 cycles against 1300 in a long run of tiles. (32 keys
         // at a time: 138 us for a long prefix and 96 sequences, 64: 125.)
         // A later piece whose maximum passes the reference by more than 2^8 brings
-        // O, the sum and the pieces of P before it to its own (rare).
+        // O, the sum and the pieces of P before it to its own, rounded up to a whole power
+        // of two (rare).
         const int lim = (k < s.pt ? min(seen, end) : min(seen - p.prefix_len, end)) - base;
         float2 sum2 = make_float2(0.f, 0.f);
 #pragma unroll 1
@@ -796,9 +797,11 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
           if (__any_sync(0xffffffffu, grow)) {
             float alpha = 1.f;
             if (grow) {
-              alpha = ex2(m_ref - m_piece);  // 0 while m_ref is still -inf
+              // (a whole number: alpha is a power of two, and what it scales is not rounded again)
+              const float m_new = ceilf(m_piece);
+              alpha = ex2(m_ref - m_new);  // 0 while m_ref is still -inf
+              m_ref = m_new;
               l *= alpha;
-              m_ref = m_piece;
             }
             sum2 = __fmul2_rn(sum2, make_float2(alpha, alpha));
             // The piece before may have scaled O too, and stored P: both are read again here,

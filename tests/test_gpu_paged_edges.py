@@ -1,5 +1,5 @@
 """GPU: paged attention where its arithmetic is at an edge: maxima that jump inside a
-tile, NaN and infinities in keys and queries that are seen. Against the definition in 64 bits (bounds in cache_oracle)."""
+tile, weights rounded, NaN and infinities in keys and queries that are seen. Against the definition in 64 bits (bounds in cache_oracle)."""
 import math
 
 import pytest
@@ -126,3 +126,36 @@ def test_infinite_scores(E):  # noqa: F811
         assert float(o[2].abs().max()) == 0.0 and bool((lse[2] == -inf).all())
         O.check("o", o[1:2], ro, bo)
         O.check("lse", lse[1:2], rl, bl)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("before", [0, 128, 200])
+def test_weights_are_rounded_once(E, d, before):  # noqa: F811
+    """Weights that lie just below half a bf16 step, 63 alike, then keys 2^9 times as heavy
+    whose ratio lies there too and whose values are 0: rounding the 63 once for their own
+    maximum and again for the new one would move O by two half steps. Scores are in log2
+    units: scale = ln 2. `before`: lighter keys ahead of them."""
+    p = Problem(4, 1, d, 1, 0, [before + 128], 16, seed=3400)
+    p.q = torch.zeros_like(p.q)
+    p.q[..., :2] = 1.0
+    low = torch.tensor(1.4 / 256).to(torch.bfloat16)
+    g = torch.arange(d) % 32
+    first = before // 64 * 64  # where a half of a tile starts
+    for j in range(before + 128):
+        at = int(p.table[0, j // 16]), 0, j % 16
+        p.k[at] = 0
+        p.v[at] = 1 + g / 128.0
+        if j < first:
+            p.k[at][0] = -30.0
+        elif j < first + 64:
+            p.k[at][0], p.k[at][1] = (0.0, 0.0) if j == first else (-1.0, low)
+        else:
+            p.k[at][0], p.k[at][1] = 9.0, -low
+            p.v[at] = 0
+    q, k, v, table, ln, _, _ = p.cuda()
+    k0, v0 = (c.nan_to_num(0.0) for c in (p.k, p.v))
+    ro, bo, rl, bl = O.paged(p.q, k0, v0, p.table, p.lens, None, None, 0, math.log(2), "causal_br")
+    for ctas in (1, 0):
+        o, lse = E.attn_paged(q, k, v, table, ln, scale=math.log(2), num_ctas=ctas)
+        O.check("o", o, ro, bo)
+        O.check("lse", lse, rl, bl)
