@@ -320,7 +320,7 @@ class _QkNormRope(torch.autograd.Function):
             if g.data_ptr() % 16 == 0 and (g.is_contiguous() or (g.stride(3) == 1 and all(
                     n == 1 or (s > 0 and s % 8 == 0) for s, n in zip(g.stride(), g.shape[:3])))):
                 return g
-            return g.contiguous()
+            return g.clone(memory_format=torch.contiguous_format)  # (contiguous() would keep a misaligned one)
 
         # an output that the loss does not reach has no gradient, and its side is left out
         if dq_out is not None and dk_out is not None:
