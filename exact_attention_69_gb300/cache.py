@@ -57,8 +57,17 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+def _fits(name, x, bits=32):
+    """x, if a signed field of the library's parameter blocks holds it (ctypes drops what does not fit)."""
+    if not -(1 << (bits - 1)) <= x < 1 << (bits - 1):
+        raise ValueError(f"{name} ({x}) is not a {bits}-bit number")
+    return x
+
+
 def _heads(name, t, shape=None):
     """Checks a [B, H, N, d] bf16 CUDA tensor; returns its element strides (b, h, n)."""
+    for n in t.shape:
+        _fits(f"a size of {name}", n)
     if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16")
     if not t.is_cuda:
@@ -84,6 +93,8 @@ def _int32(name, t, device, shape):
         raise ValueError(f"{name} must have the shape {tuple('any' if s is None else s for s in shape)}")
     if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"the last dimension of {name} must be contiguous")
+    for n in t.shape:
+        _fits(f"a size of {name}", n)
 
 
 def _same_device(device, **ts):
@@ -200,7 +211,8 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Te
         plan = _remember(key, _plan_fwd(q, k, q_weight, k_weight, inv_freq, positions, interleaved, eps, q_out, k_out))
     p = _lib.AttnRopeParams.from_buffer_copy(plan)
     p.q, p.k, p.q_weight, p.k_weight = q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight)
-    p.inv_freq, p.positions, p.pos_offset = _ptr(inv_freq), _ptr(positions), int(position_offset)
+    p.inv_freq, p.positions = _ptr(inv_freq), _ptr(positions)
+    p.pos_offset = _fits("position_offset", int(position_offset), 64)
 
     def run(handle):  # (outputs that are made here are contiguous: strides of zero)
         qo = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if q_out is None else q_out
@@ -272,7 +284,8 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tens
     p = _lib.AttnRopeBwdParams.from_buffer_copy(plan[0])
     p.q, p.k, p.dq_out, p.dk_out = q.data_ptr(), _ptr(k), dq_out.data_ptr(), _ptr(dk_out)
     p.q_weight, p.k_weight = _ptr(q_weight), _ptr(k_weight)
-    p.inv_freq, p.positions, p.pos_offset = _ptr(inv_freq), _ptr(positions), int(position_offset)
+    p.inv_freq, p.positions = _ptr(inv_freq), _ptr(positions)
+    p.pos_offset = _fits("position_offset", int(position_offset), 64)
 
     def run(handle):
         dk = dwq = dwk = None
@@ -419,7 +432,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     p.q, p.k, p.v, p.k_cache, p.v_cache = _ptr(q), k.data_ptr(), v.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
     p.block_table, p.starts, p.counts = block_table.data_ptr(), starts.data_ptr(), _ptr(counts)
     p.q_weight, p.k_weight = _ptr(q_weight), _ptr(k_weight)
-    p.inv_freq, p.positions, p.pos_offset = _ptr(inv_freq), _ptr(positions), int(position_offset)
+    p.inv_freq, p.positions = _ptr(inv_freq), _ptr(positions)
+    p.pos_offset = _fits("position_offset", int(position_offset), 64)
 
     def run(handle):
         qo = q_out
@@ -445,6 +459,8 @@ def _plan_paged(q, k_cache, v_cache, block_table, kv_lens, q_lens, prefix_table,
     """(the parameter block, bytes of workspace)"""
     if mask not in _PAGED_MASKS:
         raise ValueError(f"mask must be 'none' or 'causal_br', not {mask!r}")
+    _fits("prefix_len", prefix_len)
+    _fits("num_ctas", num_ctas)
     if q.dim() != 4:
         raise ValueError("expected [B, H, N, d] tensors")
     B, Hq, Nq, d = q.shape
@@ -501,6 +517,9 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     as zeros, a length beyond the table's end is cut.
     """
     prefix_len, num_ctas = int(prefix_len), int(num_ctas)  # (what a key holds is a value, never a tensor)
+    timeout_ns, inject = _fits("timeout_ns", int(timeout_ns), 64), _fits("inject", int(inject))
+    if timeout_ns < 0:
+        raise ValueError("timeout_ns must be >= 0")
     scale = None if scale is None else float(scale)
     key = ("paged", _sig(q), _sig(k_cache), _sig(v_cache), _sig(block_table), _sig(kv_lens), _sig(q_lens),
            _sig(prefix_table), prefix_len, scale, mask, _sig(out), _sig(lse), num_ctas)
@@ -512,7 +531,7 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     p = _lib.AttnPagedParams.from_buffer_copy(plan[0])
     p.q, p.k_cache, p.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
     p.block_table, p.kv_lens, p.q_lens = block_table.data_ptr(), kv_lens.data_ptr(), _ptr(q_lens)
-    p.prefix_table, p.timeout_ns, p.inject = _ptr(prefix_table), int(timeout_ns), int(inject)
+    p.prefix_table, p.timeout_ns, p.inject = _ptr(prefix_table), timeout_ns, inject
 
     def run(handle):
         o = torch.empty(q.shape, dtype=torch.bfloat16, device=device) if out is None else out

@@ -333,8 +333,9 @@ typedef enum { ATTN_POS_NONE = 0, ATTN_POS_INT32 = 1, ATTN_POS_INT64 = 2 } attn_
  *     none, else a multiple of 16 up to d. Pair i turns by
  *     position * inv_freq[i] (radians): (x_i, x_{i + rot/2}), or
  *     (x_{2i}, x_{2i+1}) with `interleaved`. The product is formed modulo a
- *     turn in 64-bit fixed point, so far positions lose nothing. A frequency
- *     that is zero, subnormal or not finite does not rotate.
+ *     turn in 64-bit fixed point, exact to position * 2^-64 of a turn: no
+ *     position below 2^40 loses anything of the fp32 result. A frequency that
+ *     is zero, subnormal or not finite does not rotate.
  *   positions: int32 or int64 [B, N] with element strides pos_stride (0
  *     allowed: shared by the batch), or NULL: token n is at pos_offset + n.
  * q, q_out [B, Hq, N, d]; k, k_out [B, Hk, N, d] bf16; element strides of

@@ -157,3 +157,21 @@ def test_python_refuses_cpu_tensors_and_types():
         E.attn_paged(q, q, q, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32), mask="causal")
     with pytest.raises(ValueError):
         E.rope_freqs(24)
+
+
+def test_python_refuses_numbers_that_do_not_fit():
+    """A number that the library's fields cannot hold is refused, not cut to its low bits."""
+    import exact_attention_69_gb300 as E
+    q = torch.zeros(1, 2, 3, 32, dtype=torch.bfloat16)
+    table, lens = torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    for name, bad in (("prefix_len", 2 ** 32 + 5), ("prefix_len", 2 ** 31), ("prefix_len", -2 ** 32), ("num_ctas", 2 ** 32 + 1),
+                      ("inject", 2 ** 32), ("timeout_ns", 2 ** 64 + 1), ("timeout_ns", -1)):
+        with pytest.raises(ValueError, match=name):
+            E.attn_paged(q, q, q, table, lens, **{name: bad})
+    from exact_attention_69_gb300 import cache
+    with pytest.raises(ValueError, match="a size of q"):
+        cache._heads("q", torch.zeros(1, 1, 1, 32, dtype=torch.bfloat16).expand(2 ** 32 + 1, 1, 1, 32))
+    with pytest.raises(ValueError, match="a size of table"):
+        cache._int32("table", lens.expand(2 ** 31)[:, None], torch.device("cpu"), (None, 1))
+    for ok, bits in ((2 ** 31 - 1, 32), (-2 ** 31, 32), (2 ** 63 - 1, 64)):
+        assert cache._fits("x", ok, bits) == ok

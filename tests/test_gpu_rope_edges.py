@@ -22,3 +22,26 @@ def test_gradient_off_a_16_byte_boundary(E, off):  # noqa: F811
     got = torch.autograd.grad(E.qk_norm_rope(x, y, inv_freq=freqs), (x, y), (dq, dk))
     for have, a, g in zip(got, (q, k), (gq, gk)):
         O.check("dx", have, *O.norm_rope_back(a, None, g, pos, freqs.cpu(), False, 1e-6)[:2])
+
+
+def test_offsets_that_do_not_fit(E):  # noqa: F811
+    """position_offset is a signed 64-bit number: its ends are taken, beyond them it is refused."""
+    q = rnd(110, 1, 2, 1, 64)
+    f = E.rope_freqs(64)
+    c, table, one = torch.zeros(1, 2, 16, 64, dtype=torch.bfloat16, device="cuda"), *(
+        torch.zeros(s, dtype=torch.int32, device="cuda") for s in ((1, 1), (1,)))
+    for bad in (2 ** 63, -2 ** 63 - 1, 2 ** 64 + 5):
+        with pytest.raises(ValueError, match="position_offset"):
+            E.qk_norm_rope_fwd(q.cuda(), None, inv_freq=f, position_offset=bad)
+        with pytest.raises(ValueError, match="position_offset"):
+            E.qk_norm_rope_bwd(q.cuda(), None, q.cuda(), None, inv_freq=f, position_offset=bad)
+        with pytest.raises(ValueError, match="position_offset"):
+            E.kv_append(q.cuda(), q.cuda(), c, c.clone(), table, one, inv_freq=f, position_offset=bad)
+    # (the 64-bit fixed point is exact to position * 2^-64 of a turn: at 2^40 to 2^-21.3 radians)
+    few = torch.tensor([1.0, 0.5, -0.75, 2.0 ** -9, 3 * 2.0 ** -30, 1.25, 2.0 ** -40, 0.375], dtype=torch.float64)
+    for far in (2 ** 40 + 3, -2 ** 40 - 1):
+        y, _ = E.qk_norm_rope_fwd(q.cuda(), None, inv_freq=few.cuda(), position_offset=far)
+        O.check("y", y, *O.norm_rope(q, None, torch.tensor([[far]]), few, False, 1e-6))
+    for end in (2 ** 63 - 1, -2 ** 63):
+        y, _ = E.qk_norm_rope_fwd(q.cuda(), None, inv_freq=few.cuda(), position_offset=end)
+        assert bool(torch.isfinite(y).all())
