@@ -2,6 +2,7 @@
 // the cache append and paged attention (declared in include/attn.h). Every
 // argument is checked here before any CUDA call; what the device reads
 // (lengths, tables, counts) is checked or clamped in the kernels.
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 
@@ -19,9 +20,14 @@ constexpr int64_t kMaxCount = int64_t{1} << 30;  // tokens, rows and units are c
 
 bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// What a call does with a tensor: an input's strides may be anything, a cache's
+// places are boxes of a tensor map, a written tensor must not overlap itself.
+enum Use { kRead, kMapped, kWritten };
+
 // Element strides of (b, h, n), or of (page, head, slot): given or contiguous.
-// A dimension of size 1 has no stride. Outputs must not overlap themselves.
-int strides(const int64_t in[3], const int64_t size[3], int64_t d, bool output, const char* name, int64_t out[3]) {
+// A dimension of size 1 has no stride. A written tensor's dimensions, in the
+// order of their strides, must each step over all that the ones before reach.
+int strides(const int64_t in[3], const int64_t size[3], int64_t d, Use use, const char* name, int64_t out[3]) {
   if (in[0] == 0 && in[1] == 0 && in[2] == 0) {
     out[2] = d;
     out[1] = size[2] * d;
@@ -34,20 +40,30 @@ int strides(const int64_t in[3], const int64_t size[3], int64_t d, bool output, 
     if (out[i] % 8 != 0)
       return fail_with(ATTN_ERR_MISALIGNED, "%s stride %d (%lld elements) is not a multiple of 8", name, i,
                        static_cast<long long>(out[i]));
-    if (output && size[i] > 1 && out[i] < d)
+    if (use != kRead && size[i] > 1 && out[i] < d)
       return fail_with(ATTN_ERR_INVALID_ARG, "%s stride %d (%lld elements) is smaller than d", name, i,
                        static_cast<long long>(out[i]));
+  }
+  if (use != kWritten) return ATTN_OK;
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return out[a] < out[b]; });
+  int64_t reach = d;
+  for (int i : order) {
+    if (size[i] == 1) continue;
+    if (out[i] < reach) return fail_with(ATTN_ERR_INVALID_ARG, "%s overlaps itself", name);
+    if (out[i] > (INT64_MAX - reach) / (size[i] - 1)) return fail_with(ATTN_ERR_INVALID_ARG, "%s stride %d is too large", name, i);
+    reach += out[i] * (size[i] - 1);
   }
   return ATTN_OK;
 }
 
-int tensor(const void* p, const int64_t st[3], int B, int H, int N, int d, bool output, const char* name,
+int tensor(const void* p, const int64_t st[3], int B, int H, int N, int d, Use use, const char* name,
            attn::RopeTensor* out) {
   if (p == nullptr) return fail_with(ATTN_ERR_INVALID_ARG, "%s must be non-null", name);
   if (!aligned(p, 16)) return fail_with(ATTN_ERR_MISALIGNED, "%s must be 16-byte aligned", name);
   const int64_t size[3] = {B, H, N};
   int64_t s[3];
-  const int rc = strides(st, size, d, output, name, s);
+  const int rc = strides(st, size, d, use, name, s);
   out->p = const_cast<void*>(p);
   out->sb = s[0];
   out->sh = s[1];
@@ -101,14 +117,14 @@ int fill_rope(const attn_rope_params* p, attn::RopeParams* r) {
   if (rc != ATTN_OK) return rc;
   std::memset(r, 0, sizeof(*r));
   if (p->Hq > 0) {
-    if ((rc = tensor(p->q, p->q_stride, p->B, p->Hq, p->N, p->d, false, "q", &r->q)) != ATTN_OK ||
-        (rc = tensor(p->q_out, p->q_out_stride, p->B, p->Hq, p->N, p->d, true, "q_out", &r->qo)) != ATTN_OK)
+    if ((rc = tensor(p->q, p->q_stride, p->B, p->Hq, p->N, p->d, kRead, "q", &r->q)) != ATTN_OK ||
+        (rc = tensor(p->q_out, p->q_out_stride, p->B, p->Hq, p->N, p->d, kWritten, "q_out", &r->qo)) != ATTN_OK)
       return rc;
   } else if (p->q || p->q_out || p->q_weight) {
     return fail_with(ATTN_ERR_INVALID_ARG, "q, q_out and q_weight need Hq > 0");
   }
   if (p->Hk > 0) {
-    if ((rc = tensor(p->k, p->k_stride, p->B, p->Hk, p->N, p->d, false, "k", &r->k)) != ATTN_OK) return rc;
+    if ((rc = tensor(p->k, p->k_stride, p->B, p->Hk, p->N, p->d, kRead, "k", &r->k)) != ATTN_OK) return rc;
   } else if (p->k || p->k_out || p->k_weight) {
     return fail_with(ATTN_ERR_INVALID_ARG, "k, k_out and k_weight need Hk > 0");
   }
@@ -312,7 +328,7 @@ int attn_qk_norm_rope(const attn_rope_params* p) {
   if (p->v || p->k_cache || p->v_cache || p->block_table || p->starts || p->counts)
     return fail_with(ATTN_ERR_INVALID_ARG, "v and the cache fields are attn_kv_append's");
   if (p->Hk > 0 &&
-      (rc = tensor(p->k_out, p->k_out_stride, p->B, p->Hk, p->N, p->d, true, "k_out", &r.ko)) != ATTN_OK)
+      (rc = tensor(p->k_out, p->k_out_stride, p->B, p->Hk, p->N, p->d, kWritten, "k_out", &r.ko)) != ATTN_OK)
     return rc;
   return launch_rope(&r, p->d, p->Hq + p->Hk, attn::host::stream_of(p->stream));
 }
@@ -325,17 +341,17 @@ int attn_kv_append(const attn_rope_params* p) {
   if (rc != ATTN_OK) return rc;
   if (p->Hk < 1) return fail_with(ATTN_ERR_INVALID_ARG, "Hk must be >= 1");
   if (p->k_out) return fail_with(ATTN_ERR_INVALID_ARG, "k_out is attn_qk_norm_rope's: the keys go to their pages");
-  if ((rc = tensor(p->v, p->v_stride, p->B, p->Hk, p->N, p->d, false, "v", &r.v)) != ATTN_OK) return rc;
+  if ((rc = tensor(p->v, p->v_stride, p->B, p->Hk, p->N, p->d, kRead, "v", &r.v)) != ATTN_OK) return rc;
   if (p->n_pages < 1) return fail_with(ATTN_ERR_INVALID_ARG, "n_pages must be >= 1");
   if ((rc = log2_page(p->page_size, &r.page_shift)) != ATTN_OK) return rc;
   attn::RopeTensor c;
-  if ((rc = tensor(p->k_cache, p->k_cache_stride, p->n_pages, p->Hk, p->page_size, p->d, true, "k_cache", &c)) != ATTN_OK)
+  if ((rc = tensor(p->k_cache, p->k_cache_stride, p->n_pages, p->Hk, p->page_size, p->d, kWritten, "k_cache", &c)) != ATTN_OK)
     return rc;
   r.kc = c.p;
   r.kc_sp = c.sb;
   r.kc_sh = c.sh;
   r.kc_st = c.sn;
-  if ((rc = tensor(p->v_cache, p->v_cache_stride, p->n_pages, p->Hk, p->page_size, p->d, true, "v_cache", &c)) != ATTN_OK)
+  if ((rc = tensor(p->v_cache, p->v_cache_stride, p->n_pages, p->Hk, p->page_size, p->d, kWritten, "v_cache", &c)) != ATTN_OK)
     return rc;
   r.vc = c.p;
   r.vc_sp = c.sb;
@@ -372,17 +388,17 @@ int attn_qk_norm_rope_bwd(const attn_rope_bwd_params* p) {
   attn::RopeBwdParams r;
   std::memset(&r, 0, sizeof(r));
   if (p->Hq > 0) {
-    if ((rc = tensor(p->q, p->q_stride, p->B, p->Hq, p->N, p->d, false, "q", &r.q)) != ATTN_OK ||
-        (rc = tensor(p->dq_out, p->dq_out_stride, p->B, p->Hq, p->N, p->d, false, "dq_out", &r.dyq)) != ATTN_OK ||
-        (rc = tensor(p->dq, p->dq_stride, p->B, p->Hq, p->N, p->d, true, "dq", &r.dq)) != ATTN_OK)
+    if ((rc = tensor(p->q, p->q_stride, p->B, p->Hq, p->N, p->d, kRead, "q", &r.q)) != ATTN_OK ||
+        (rc = tensor(p->dq_out, p->dq_out_stride, p->B, p->Hq, p->N, p->d, kRead, "dq_out", &r.dyq)) != ATTN_OK ||
+        (rc = tensor(p->dq, p->dq_stride, p->B, p->Hq, p->N, p->d, kWritten, "dq", &r.dq)) != ATTN_OK)
       return rc;
   } else if (p->dq_weight != nullptr) {
     return fail_with(ATTN_ERR_INVALID_ARG, "dq_weight needs Hq > 0");
   }
   if (p->Hk > 0) {
-    if ((rc = tensor(p->k, p->k_stride, p->B, p->Hk, p->N, p->d, false, "k", &r.k)) != ATTN_OK ||
-        (rc = tensor(p->dk_out, p->dk_out_stride, p->B, p->Hk, p->N, p->d, false, "dk_out", &r.dyk)) != ATTN_OK ||
-        (rc = tensor(p->dk, p->dk_stride, p->B, p->Hk, p->N, p->d, true, "dk", &r.dk)) != ATTN_OK)
+    if ((rc = tensor(p->k, p->k_stride, p->B, p->Hk, p->N, p->d, kRead, "k", &r.k)) != ATTN_OK ||
+        (rc = tensor(p->dk_out, p->dk_out_stride, p->B, p->Hk, p->N, p->d, kRead, "dk_out", &r.dyk)) != ATTN_OK ||
+        (rc = tensor(p->dk, p->dk_stride, p->B, p->Hk, p->N, p->d, kWritten, "dk", &r.dk)) != ATTN_OK)
       return rc;
   } else if (p->dk_weight != nullptr) {
     return fail_with(ATTN_ERR_INVALID_ARG, "dk_weight needs Hk > 0");
@@ -446,10 +462,10 @@ int attn_paged(const attn_paged_params* p) {
   attn::RopeTensor q, o, kc, vc;
   if (p->n_pages < 1) return fail_with(ATTN_ERR_INVALID_ARG, "n_pages must be >= 1");
   if ((rc = log2_page(p->page_size, &k.page_shift)) != ATTN_OK ||
-      (rc = tensor(p->q, p->q_stride, p->B, p->Hq, p->Nq, p->d, false, "q", &q)) != ATTN_OK ||
-      (rc = tensor(p->o, p->o_stride, p->B, p->Hq, p->Nq, p->d, true, "o", &o)) != ATTN_OK ||
-      (rc = tensor(p->k_cache, p->k_cache_stride, p->n_pages, p->Hk, p->page_size, p->d, true, "k_cache", &kc)) != ATTN_OK ||
-      (rc = tensor(p->v_cache, p->v_cache_stride, p->n_pages, p->Hk, p->page_size, p->d, true, "v_cache", &vc)) != ATTN_OK)
+      (rc = tensor(p->q, p->q_stride, p->B, p->Hq, p->Nq, p->d, kRead, "q", &q)) != ATTN_OK ||
+      (rc = tensor(p->o, p->o_stride, p->B, p->Hq, p->Nq, p->d, kWritten, "o", &o)) != ATTN_OK ||
+      (rc = tensor(p->k_cache, p->k_cache_stride, p->n_pages, p->Hk, p->page_size, p->d, kMapped, "k_cache", &kc)) != ATTN_OK ||
+      (rc = tensor(p->v_cache, p->v_cache_stride, p->n_pages, p->Hk, p->page_size, p->d, kMapped, "v_cache", &vc)) != ATTN_OK)
     return rc;
   if (!p->block_table || !p->kv_lens) return fail_with(ATTN_ERR_INVALID_ARG, "block_table and kv_lens must be non-null");
   if (!aligned(p->block_table, 4) || !aligned(p->kv_lens, 4) || !aligned(p->q_lens, 4) || !aligned(p->prefix_table, 4) ||

@@ -341,7 +341,9 @@ typedef enum { ATTN_POS_NONE = 0, ATTN_POS_INT32 = 1, ATTN_POS_INT64 = 2 } attn_
  * q, q_out [B, Hq, N, d]; k, k_out [B, Hk, N, d] bf16; element strides of
  * (b, h, n), all zero = contiguous; inputs may have zero strides; the last
  * dimension contiguous, pointers 16-byte aligned, strides multiples of 8. A
- * stride of a dimension of size 1 is ignored. An output may be its own input.
+ * stride of a dimension of size 1 is ignored. An output may be its own input; it
+ * must not overlap itself (each stride no smaller than what the dimensions of
+ * smaller strides reach).
  * d in {32, 64, 128}. Hk 0: queries only (k, k_out NULL).
  */
 typedef struct attn_rope_params {

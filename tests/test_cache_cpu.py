@@ -175,3 +175,32 @@ def test_python_refuses_numbers_that_do_not_fit():
         cache._int32("table", lens.expand(2 ** 31)[:, None], torch.device("cpu"), (None, 1))
     for ok, bits in ((2 ** 31 - 1, 32), (-2 ** 31, 32), (2 ** 63 - 1, 64)):
         assert cache._fits("x", ok, bits) == ok
+
+
+# strides (b, h, n) under which places of a written tensor lie on one another; B 2, N 8, d 64, 9 pages of 16
+OVERLAPS = [
+    ("attn_qk_norm_rope", rope, dict(q_out_stride=(64, 64, 64))), ("attn_qk_norm_rope", rope, dict(q_out_stride=(2048, 256, 64))),
+    ("attn_qk_norm_rope", rope, dict(k_out_stride=(512, 512, 64))), ("attn_qk_norm_rope", rope, dict(k_out_stride=(64, 128, 128))),
+    ("attn_qk_norm_rope", rope, dict(q_out_stride=(1 << 62, 512, 1 << 61))),
+    ("attn_kv_append", append, dict(q_out_stride=(1024, 512, 64))), ("attn_kv_append", append, dict(k_cache_stride=(1024, 1024, 64))),
+    ("attn_kv_append", append, dict(v_cache_stride=(64, 1024, 64))),
+    ("attn_qk_norm_rope_bwd", rope_bwd, dict(dq_stride=(2040, 512, 64))), ("attn_qk_norm_rope_bwd", rope_bwd, dict(dk_stride=(64, 64, 128))),
+    ("attn_paged", paged, dict(o_stride=(64, 64, 0))),
+]
+
+
+@pytest.mark.parametrize("call,make,changes", OVERLAPS, ids=lambda x: str(x) if isinstance(x, dict) else None)
+def test_written_tensors_that_overlap_themselves(lib, call, make, changes):
+    refuses(lib, call, make(), changes, INV)
+
+
+def test_written_strides_that_do_not_overlap(lib):
+    """Heads last, padded rows, any order of the dimensions: the host's checks reach the last
+    one that follows (no workspace), or the missing GPU."""
+    for st in ((2048, 64, 256), (4096, 512, 64), (64, 128, 512), (2048, 512, 64), (1 << 30, 72, 576)):
+        p = rope_bwd()
+        p.dq_stride[:] = st
+        p.q_weight = p.dq_weight = A
+        code = lib.attn_qk_norm_rope_bwd(ctypes.byref(p))
+        said = lib.attn_last_error()
+        assert b"overlap" not in said and (code != INV or b"workspace" in said), said
