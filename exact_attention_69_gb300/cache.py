@@ -147,6 +147,12 @@ def _set_rope(p, B, N, d, device, q_weight, k_weight, inv_freq, positions, inter
         p.pos_stride[:] = (0, st[0]) if len(st) == 1 else st
 
 
+def _wrote(ts):
+    """Tells autograd which of the caller's tensors a call has written: a graph that saved one
+    refuses its backward pass, as after any in-place op."""
+    torch.autograd.graph.increment_version(ts)
+
+
 def _on(device, stream, tensors, run):
     """run(handle) with the tensors' device and the call's stream current, so that
     outputs and scratch come from that stream's memory. Inputs of a call on another
@@ -201,7 +207,8 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Te
     the first 2 * len(inv_freq) channels are rotated (rope_freqs; None: no rotation) by
     the token's position: `positions` [N] or [B, N] int32 or int64, else position_offset
     + n. Pairs are (i, i + rot / 2), or (2i, 2i + 1) with `interleaved`. k may be None.
-    Returns (q_out, k_out); q_out may be q, k_out k.
+    Returns (q_out, k_out); q_out may be q, k_out k. No gradient goes through it:
+    qk_norm_rope is the differentiable one.
     """
     interleaved, eps = bool(interleaved), None if eps is None else float(eps)
     key = ("fwd", _sig(q), _sig(k), _sig(q_weight), _sig(k_weight), _sig(inv_freq), _sig(positions), _sig(q_out),
@@ -226,6 +233,8 @@ def qk_norm_rope_fwd(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Te
         code = _lib.load().attn_qk_norm_rope(ctypes.byref(p))
         if code:
             _lib.check(code, "qk_norm_rope")
+        if q_out is not None or k_out is not None:
+            _wrote([t for t in (q_out, k_out) if t is not None])
         return qo, ko
 
     return _on(q.device, stream, (q, k, q_weight, k_weight, inv_freq, positions, q_out, k_out), run)
@@ -419,6 +428,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
     counts [B]: real tokens of each sequence; those behind leave the cache as it was, as
     do negative starts, slots behind the table's end and entries that are not a page of
     the cache. The pages that a call writes must not be shared between sequences.
+    No gradient goes through it.
     """
     interleaved, eps = bool(interleaved), None if eps is None else float(eps)
     key = ("append", _sig(k), _sig(v), _sig(k_cache), _sig(v_cache), _sig(block_table), _sig(starts), _sig(counts),
@@ -445,6 +455,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: 
         code = _lib.load().attn_kv_append(ctypes.byref(p))
         if code:
             _lib.check(code, "kv_append")
+        _wrote((k_cache, v_cache) if q_out is None else (k_cache, v_cache, q_out))
         return qo
 
     return _on(device, stream, (k, v, k_cache, v_cache, block_table, starts, counts, positions, inv_freq, k_weight, q,
@@ -513,8 +524,8 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
     for both. Values (v_cache) of keys that only some rows of a sequence see must be
     finite. Lengths and tables are read when the kernels run.
 
-    Returns (o, lse) or o; no gradient goes through it. Raises for what the host can check; a bad table entry reads
-    as zeros, a length beyond the table's end is cut.
+    Returns (o, lse) or o; no gradient goes through it. Raises for what the host can
+    check; a bad table entry reads as zeros, a length beyond the table's end is cut.
     """
     prefix_len, num_ctas = int(prefix_len), int(num_ctas)  # (what a key holds is a value, never a tensor)
     timeout_ns, inject = _fits("timeout_ns", int(timeout_ns), 64), _fits("inject", int(inject))
@@ -547,6 +558,8 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
         code = _lib.load().attn_paged(ctypes.byref(p))
         if code:
             _lib.check(code, "attn_paged")
+        if out is not None or lse is not None:
+            _wrote([t for t in (out, lse) if t is not None])
         return (o, z) if return_lse else o
 
     return _on(device, stream, (q, k_cache, v_cache, block_table, kv_lens, q_lens, prefix_table, out, lse), run)

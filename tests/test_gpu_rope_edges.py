@@ -45,3 +45,44 @@ def test_offsets_that_do_not_fit(E):  # noqa: F811
     for end in (2 ** 63 - 1, -2 ** 63):
         y, _ = E.qk_norm_rope_fwd(q.cuda(), None, inv_freq=few.cuda(), position_offset=end)
         assert bool(torch.isfinite(y).all())
+
+
+def test_written_tensors_are_known_to_autograd(E):  # noqa: F811
+    """A graph that saved a tensor which a later call writes refuses its backward pass."""
+    q, k = rnd(120, 1, 2, 20, 64).cuda(), rnd(121, 1, 2, 20, 64).cuda()
+    f = E.rope_freqs(64)
+    table, one = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    lens = one + 20
+    cache = lambda: torch.zeros(2, 2, 16, 64, dtype=torch.bfloat16, device="cuda")  # noqa: E731
+
+    def saved(t):  # a graph that keeps t
+        w = torch.ones((), device="cuda", dtype=t.dtype, requires_grad=True)
+        return (w * t).sum()
+
+    def refused(loss):
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            loss.backward()
+
+    x = q.clone().requires_grad_()
+    y, _ = E.qk_norm_rope(x, None, inv_freq=f)
+    with torch.no_grad():
+        E.qk_norm_rope_fwd(x, k, inv_freq=f, q_out=x)
+    refused(y.float().sum())
+    k2 = k.clone()
+    loss = saved(k2)
+    E.qk_norm_rope_fwd(q, k2, inv_freq=f, k_out=k2)
+    refused(loss)
+    kc, vc, qo = cache(), cache(), torch.empty_like(q)
+    losses = [saved(t) for t in (kc, vc, qo)]
+    E.kv_append(k, k, kc, vc, table, one, q=q, q_out=qo)
+    for loss in losses:
+        refused(loss)
+    o, z = torch.empty_like(q), torch.empty(1, 2, 20, device="cuda")
+    losses = [saved(t) for t in (o, z)]
+    kept = saved(kc)  # read, not written
+    E.attn_paged(q, kc, vc, table, lens, out=o, lse=z)
+    for loss in losses:
+        refused(loss)
+    kept.backward()
+    with torch.inference_mode():
+        E.kv_append(k, k, cache(), cache(), table, one, q=q, q_out=torch.empty_like(q))
