@@ -262,10 +262,10 @@ def _plan_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions, int
     _same_device(q.device, k=k, dq_out=dq_out, dk_out=dk_out)
     _set_rope(p, B, N, d, q.device, q_weight, k_weight, inv_freq, positions, interleaved, eps)
     plan, n = bytes(p), 0
-    if weight_grads and (q_weight is not None or k_weight is not None):
+    if any(weight_grads):
         p.inv_freq, p.positions = _ptr(inv_freq), _ptr(positions)
         p.q_weight, p.k_weight = _ptr(q_weight), _ptr(k_weight)
-        p.dq_weight, p.dk_weight = _ptr(q_weight), _ptr(k_weight)  # (only whether they are wanted)
+        p.dq_weight, p.dk_weight = (_ptr(w) if want else None for w, want in zip((q_weight, k_weight), weight_grads))
         with torch.cuda.device(q.device):
             n = _lib.load().attn_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(p))
         if n < 0:
@@ -277,15 +277,17 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tens
                      dk_out: torch.Tensor | None, q_weight: torch.Tensor | None = None,
                      k_weight: torch.Tensor | None = None, *, inv_freq: torch.Tensor | None = None,
                      positions: torch.Tensor | None = None, position_offset: int = 0,
-                     interleaved: bool = False, eps: float | None = 1e-6, weight_grads: bool = True,
-                     stream=None):
+                     interleaved: bool = False, eps: float | None = 1e-6,
+                     weight_grads: bool | tuple[bool, bool] = True, stream=None):
     """Gradients through qk_norm_rope_fwd: (dq, dk, dq_weight, dk_weight) for the
     gradients dq_out, dk_out at its outputs; the other arguments as the forward had them.
-    Weight gradients have the weights' types (None without a weight, or with
-    weight_grads False); their sums are fp32 in a fixed order."""
+    Weight gradients have the weights' types (None without a weight, or where weight_grads,
+    one for both or a pair, is False); their sums are fp32 in a fixed order."""
     interleaved, eps = bool(interleaved), None if eps is None else float(eps)
+    want_q, want_k = weight_grads if isinstance(weight_grads, tuple) else (weight_grads, weight_grads)
+    weight_grads = (bool(want_q) and q_weight is not None, bool(want_k) and k_weight is not None)
     key = ("bwd", _sig(q), _sig(k), _sig(dq_out), _sig(dk_out), _sig(q_weight), _sig(k_weight), _sig(inv_freq),
-           _sig(positions), interleaved, eps, bool(weight_grads))
+           _sig(positions), interleaved, eps, weight_grads)
     plan = _plans.get(key)
     if plan is None:
         plan = _remember(key, _plan_bwd(q, k, dq_out, dk_out, q_weight, k_weight, inv_freq, positions, interleaved, eps,
@@ -303,10 +305,10 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tens
         if k is not None:
             dk = torch.empty(k.shape, dtype=torch.bfloat16, device=q.device)
             p.dk = dk.data_ptr()
-        if weight_grads and q_weight is not None:
+        if weight_grads[0]:
             dwq = torch.empty_like(q_weight)
             p.dq_weight = dwq.data_ptr()
-        if weight_grads and k_weight is not None:
+        if weight_grads[1]:
             dwk = torch.empty_like(k_weight)
             p.dk_weight = dwk.data_ptr()
         if plan[1]:
@@ -335,7 +337,7 @@ class _QkNormRope(torch.autograd.Function):
     def backward(ctx, dq_out, dk_out):
         q, k, q_weight, k_weight, inv_freq, positions = ctx.saved_tensors
         how = dict(inv_freq=inv_freq, positions=positions, **ctx.opts)
-        weights = ctx.needs_input_grad[2] or ctx.needs_input_grad[3]
+        need_q, need_k, need_wq, need_wk = ctx.needs_input_grad[:4]
         dq = dk = dwq = dwk = None
 
         def ready(g):  # most strides will do as they are: see attn_rope_bwd_params
@@ -344,16 +346,22 @@ class _QkNormRope(torch.autograd.Function):
                 return g
             return g.clone(memory_format=torch.contiguous_format)  # (contiguous() would keep a misaligned one)
 
-        # an output that the loss does not reach has no gradient, and its side is left out
-        if dq_out is not None and dk_out is not None:
+        # a side is left out if the loss does not reach its output, or nothing of it needs a gradient
+        on_q = dq_out is not None and (need_q or need_wq)
+        on_k = dk_out is not None and (need_k or need_wk)
+        if on_q and on_k:
             dq, dk, dwq, dwk = qk_norm_rope_bwd(q, k, ready(dq_out), ready(dk_out), q_weight, k_weight,
-                                                weight_grads=weights, **how)
-        elif dq_out is not None:
+                                                weight_grads=(need_wq, need_wk), **how)
+        elif on_q:
             dq, _, dwq, _ = qk_norm_rope_bwd(q, None, ready(dq_out), None, q_weight, None,
-                                             weight_grads=weights, **how)
-        elif dk_out is not None:
+                                             weight_grads=(need_wq, False), **how)
+        elif on_k:
             dk, _, dwk, _ = qk_norm_rope_bwd(k, None, ready(dk_out), None, k_weight, None,
-                                             weight_grads=weights, **how)
+                                             weight_grads=(need_wk, False), **how)
+        if not need_q:
+            dq = None
+        if not need_k:
+            dk = None
         return dq, dk, dwq, dwk, None, None, None
 
 

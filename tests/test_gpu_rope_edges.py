@@ -86,3 +86,32 @@ def test_written_tensors_are_known_to_autograd(E):  # noqa: F811
     kept.backward()
     with torch.inference_mode():
         E.kv_append(k, k, cache(), cache(), table, one, q=q, q_out=torch.empty_like(q))
+
+
+@pytest.mark.parametrize("needs", [(1, 0, 0, 0), (0, 1, 0, 0), (0, 0, 1, 0), (1, 1, 0, 1), (1, 0, 0, 1),
+                                   (0, 0, 1, 1), (1, 1, 1, 1)], ids=str)
+def test_only_the_gradients_that_are_asked_for(E, needs, monkeypatch):  # noqa: F811
+    """Sides and weights that need no gradient are left out of the call; what is asked for
+    does not depend on the rest."""
+    from exact_attention_69_gb300 import cache
+    q, k, gq, gk = (rnd(130 + i, 2, h, 19, 64) for i, h in enumerate((4, 2, 4, 2)))
+    wq, wk = weight(134, 64, torch.float32), weight(135, 64, torch.bfloat16)
+    pos, freqs = torch.arange(19)[None].expand(2, 19), E.rope_freqs(64)
+    calls, real = [], cache.qk_norm_rope_bwd
+
+    def spy(*a, **kw):
+        out = real(*a, **kw)
+        calls.append((a, out))
+        return out
+
+    monkeypatch.setattr(cache, "qk_norm_rope_bwd", spy)
+    ts = [t.cuda().requires_grad_(bool(n)) for t, n in zip((q, k, wq, wk), needs)]
+    got = torch.autograd.grad(E.qk_norm_rope(*ts, inv_freq=freqs), [t for t in ts if t.requires_grad], (gq.cuda(), gk.cuda()))
+    (args, out), = calls
+    sides = (needs[0] or needs[2]) + (needs[1] or needs[3])
+    assert (args[1] is not None) == (sides == 2)
+    assert sum(t is not None for t in out[2:]) == needs[2] + needs[3]
+    bq, bk = (O.norm_rope_back(x, w, g, pos, freqs.cpu(), False, 1e-6) for x, w, g in ((q, wq, gq), (k, wk, gk)))
+    want = [bq[:2], bk[:2], bq[2:], bk[2:]]
+    for have, (ref, bound) in zip(got, [w for w, n in zip(want, needs) if n]):
+        O.check("gradient", have, ref, bound)
