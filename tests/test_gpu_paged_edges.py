@@ -159,3 +159,24 @@ def test_weights_are_rounded_once(E, d, before):  # noqa: F811
         o, lse = E.attn_paged(q, k, v, table, ln, scale=math.log(2), num_ctas=ctas)
         O.check("o", o, ro, bo)
         O.check("lse", lse, rl, bl)
+
+
+@pytest.mark.parametrize("what", ["heads", "queries", "sequences", "scale"])
+@pytest.mark.parametrize("case", [(8, 2, 64, 1, 600, [(7 * i) % 90 + 1 for i in range(60)], 16),
+                                  (4, 2, 128, 3, 0, [70, 300], 32), (2, 1, 32, 140, 50, [200], 64)], ids=str)
+def test_expanded_queries_and_a_scale(E, case, what):  # noqa: F811
+    """Queries with a stride of zero over heads, tokens or sequences (gathered row by row), and
+    a scale other than 1 / sqrt(d)."""
+    Hq, Hk, d, Nq, P, lens, page = case
+    p = Problem(Hq, Hk, d, Nq, P, lens, page, seed=3500)
+    q, k, v, table, ln, _, prefix = p.cuda()
+    scale = 0.31 if what == "scale" else 1 / math.sqrt(d)
+    if what != "scale":
+        dim = {"sequences": 0, "heads": 1, "queries": 2}[what]
+        q = q.narrow(dim, 0, 1).expand(p.q.shape)
+    k0, v0 = (c.nan_to_num(0.0) for c in (p.k, p.v))
+    ro, bo, rl, bl = O.paged(q.cpu(), k0, v0, p.table, p.lens, None, p.prefix, P, scale, "causal_br")
+    for ctas in (0, 2):
+        o, lse = E.attn_paged(q, k, v, table, ln, prefix_table=prefix, prefix_len=P, scale=scale, num_ctas=ctas)
+        O.check("o", o, ro, bo)
+        O.check("lse", lse, rl, bl)

@@ -115,3 +115,117 @@ def test_only_the_gradients_that_are_asked_for(E, needs, monkeypatch):  # noqa: 
     want = [bq[:2], bk[:2], bq[2:], bk[2:]]
     for have, (ref, bound) in zip(got, [w for w, n in zip(want, needs) if n]):
         O.check("gradient", have, ref, bound)
+
+
+@pytest.mark.parametrize("form", ["int32 [N]", "int64 [B, N]", "int32 [N, B] transposed", "int64 [N] every third"])
+@pytest.mark.parametrize("interleaved", [False, True], ids=["half", "pairs"])
+def test_gradient_with_positions(E, form, interleaved):  # noqa: F811
+    """The gradient turns back by the positions that the forward was given, not by an offset."""
+    B, N = 3, 21
+    q, k, gq, gk = (rnd(140 + i, B, h, N, 64) for i, h in enumerate((4, 2, 4, 2)))
+    w = weight(144, 64, torch.bfloat16)
+    g = torch.Generator().manual_seed(145)
+    if form == "int32 [N]":
+        pos = torch.randint(-500, 10 ** 6, (N,), generator=g).to(torch.int32)
+        given = pos.cuda()
+    elif form == "int64 [B, N]":
+        pos = torch.randint(-500, 10 ** 6, (B, N), generator=g)
+        given = pos.cuda()
+    elif form == "int32 [N, B] transposed":
+        pos = torch.randint(0, 10 ** 6, (N, B), generator=g).to(torch.int32)
+        given, pos = pos.cuda().t(), pos.t()
+    else:
+        pos = torch.randint(0, 10 ** 6, (3 * N,), generator=g)
+        given, pos = pos.cuda()[::3], pos[::3]
+    full = pos.expand(B, N) if pos.dim() == 1 else pos
+    freqs = E.rope_freqs(32)
+    x, y, ww = q.cuda().requires_grad_(), k.cuda().requires_grad_(), w.cuda().requires_grad_()
+    out = E.qk_norm_rope(x, y, ww, None, inv_freq=freqs, positions=given, position_offset=99, interleaved=interleaved)
+    O.check("q", out[0], *O.norm_rope(q, w, full, freqs.cpu(), interleaved, 1e-6))
+    dq, dk, dw = torch.autograd.grad(out, (x, y, ww), (gq.cuda(), gk.cuda()))
+    rq, bq, rw, bw = O.norm_rope_back(q, w, gq, full, freqs.cpu(), interleaved, 1e-6)
+    O.check("dq", dq, rq, bq)
+    O.check("dw", dw, rw, bw)
+    O.check("dk", dk, *O.norm_rope_back(k, None, gk, full, freqs.cpu(), interleaved, 1e-6)[:2])
+
+
+@pytest.mark.parametrize("eps", [None, 1e-6], ids=["plain", "norm"])
+@pytest.mark.parametrize("interleaved", [False, True], ids=["half", "pairs"])
+@pytest.mark.parametrize("d,rot", [(32, 16), (64, 32), (64, 48), (128, 64), (128, 16)])
+def test_append_partly_rotated(E, d, rot, interleaved, eps):  # noqa: F811
+    """Fewer rotated channels than a head has, into the cache and beside it."""
+    B, Hq, Hk, N, page = 2, 3, 1, 19, 16
+    starts = [5, 30]
+    table = torch.tensor([[4, 0, 9], [2, 7, 1], ], dtype=torch.int32)
+    table = torch.cat([table, torch.tensor([[3], [5]], dtype=torch.int32)], 1)
+    q, k, v = rnd(150, B, Hq, N, d), rnd(151, B, Hk, N, d), rnd(152, B, Hk, N, d)
+    kc, vc = rnd(153, 10, Hk, page, d), rnd(154, 10, Hk, page, d)
+    wk = weight(155, d, torch.bfloat16) if eps is not None else None
+    freqs = E.rope_freqs(rot)
+    kcc, vcc = kc.cuda(), vc.cuda()
+    qo = E.kv_append(k.cuda(), v.cuda(), kcc, vcc, table.cuda(), torch.tensor(starts, dtype=torch.int32).cuda(),
+                     position_offset=77, inv_freq=freqs, interleaved=interleaved, eps=eps,
+                     k_weight=None if wk is None else wk.cuda(), q=q.cuda())
+    pos = 77 + torch.tensor(starts)[:, None] + torch.arange(N)
+    want_k, kb, want_v = O.append(k, v, kc, vc, table, starts, None, pos, freqs.cpu(), interleaved, eps, wk)
+    O.check("k_cache", kcc, want_k, kb)
+    O.check("v_cache", vcc, want_v, torch.zeros_like(want_v))
+    O.check("q", qo, *O.norm_rope(q, None, pos, freqs.cpu(), interleaved, eps))
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64], ids=["int32", "int64"])
+@pytest.mark.parametrize("shared", [False, True], ids=["own", "shared"])
+def test_append_with_positions_and_outputs(E, dtype, shared):  # noqa: F811
+    """Positions that are not the slots, [B, N] and [N]; queries into a heads-last tensor, and
+    over themselves inside a fused projection."""
+    B, Hq, Hk, N, d, page = 3, 4, 2, 11, 64, 16
+    starts = [0, 20, 9]
+    table = torch.tensor([[0, 1], [6, 3], [4, 5]], dtype=torch.int32)
+    x = rnd(160, B, N, Hq + 2 * Hk, d)
+    q, k, v = (x[:, :, a:b].transpose(1, 2) for a, b in ((0, Hq), (Hq, Hq + Hk), (Hq + Hk, Hq + 2 * Hk)))
+    kc, vc = rnd(161, 7, Hk, page, d), rnd(162, 7, Hk, page, d)
+    g = torch.Generator().manual_seed(163)
+    pos = torch.randint(0, 2 ** 31 - 1, (N,) if shared else (B, N), generator=g).to(dtype)
+    full = pos.expand(B, N)
+    freqs = E.rope_freqs(d)
+    want_k, kb, want_v = O.append(k, v, kc, vc, table, starts, None, full, freqs.cpu(), False, 1e-6, None)
+    want_q = O.norm_rope(q, None, full, freqs.cpu(), False, 1e-6)
+    for place in ("heads last", "itself"):
+        xc, kcc, vcc = x.cuda(), kc.cuda(), vc.cuda()
+        qc = xc[:, :, :Hq].transpose(1, 2)
+        out = qc if place == "itself" else torch.full((B, N, Hq, d), 9.0, dtype=torch.bfloat16, device="cuda").transpose(1, 2)
+        got = E.kv_append(xc[:, :, Hq:Hq + Hk].transpose(1, 2), xc[:, :, Hq + Hk:].transpose(1, 2), kcc, vcc, table.cuda(),
+                          torch.tensor(starts, dtype=torch.int32).cuda(), position_offset=5, positions=pos.cuda(),
+                          inv_freq=freqs, eps=1e-6, q=qc, q_out=out)
+        assert got.data_ptr() == out.data_ptr()
+        O.check("k_cache", kcc, want_k, kb)
+        O.check("v_cache", vcc, want_v, torch.zeros_like(want_v))
+        O.check("q", out, *want_q)
+        assert torch.equal(xc[:, :, Hq:].cpu(), x[:, :, Hq:]), "keys and values beside the queries stay"
+
+
+@pytest.mark.parametrize("interleaved", [False, True], ids=["half", "pairs"])
+def test_infinity_stays_in_its_channel(E, interleaved):  # noqa: F811
+    """An infinity in a channel that is not rotated reaches no other one, forward and back;
+    in a rotated one it reaches its pair and nothing else."""
+    q, g = rnd(170, 1, 3, 5, 64), rnd(171, 1, 3, 5, 64)
+    pos, freqs = 1 + torch.arange(5)[None], E.rope_freqs(32)
+    inf = float("inf")
+    for at, reached in ((40, {40}), (63, {63}), (32, {32}), (3, {3, 2} if interleaved else {3, 19})):
+        x, dy = q.clone(), g.clone()
+        x[0, 1, 2, at] = dy[0, 1, 2, at] = inf
+        xc = x.cuda().requires_grad_()
+        y, _ = E.qk_norm_rope(xc, None, inv_freq=freqs, position_offset=1, interleaved=interleaved, eps=None)
+        (dx,) = torch.autograd.grad(y, xc, dy.cuda())
+        rest = torch.ones(64, dtype=torch.bool)
+        rest[list(reached)] = False
+        x0, dy0 = x.clone(), dy.clone()
+        x0[0, 1, 2, at] = dy0[0, 1, 2, at] = 0.0
+        for name, have, (ref, bound) in (("y", y, O.norm_rope(x0, None, pos, freqs.cpu(), interleaved, None)),
+                                         ("dx", dx, O.norm_rope_back(x0, None, dy0, pos, freqs.cpu(), interleaved, None)[:2])):
+            have = have.detach().cpu()
+            assert not bool(torch.isfinite(have[0, 1, 2][~rest]).any())
+            O.check(name, have[..., rest], ref[..., rest], bound[..., rest])
+            have[0, 1, 2] = 0
+            ref[0, 1, 2], bound[0, 1, 2] = 0, 0
+            O.check(name + " of other rows", have, ref, bound)
