@@ -180,3 +180,29 @@ def test_expanded_queries_and_a_scale(E, case, what):  # noqa: F811
         o, lse = E.attn_paged(q, k, v, table, ln, prefix_table=prefix, prefix_len=P, scale=scale, num_ctas=ctas)
         O.check("o", o, ro, bo)
         O.check("lse", lse, rl, bl)
+
+
+@pytest.mark.parametrize("mask", ["causal_br", "none"])
+@pytest.mark.parametrize("ctas", [0, 1, 7])
+def test_many_tasks_of_a_sequence(E, ctas, mask):  # noqa: F811
+    """Chunks of many tasks (up to 12 of 256 rows a key head), the last ones of some sequences
+    without a row, early ones of a causal chunk with few keys."""
+    Problem(4, 2, 64, 1500, 130, [1600, 0, 700, 1500], 64, [1500, 0, 257, 1], seed=3600).check(E, mask, num_ctas=ctas)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("at", [0, 5, 135, 300])
+def test_a_key_with_all_of_the_weight(E, d, at):  # noqa: F811
+    """A key 57 log2 units above the others, in the first half of a tile: its weight is 1
+    without a rounding, and O is its value, bit for bit."""
+    p = Problem(4, 1, d, 1, 0, [500], 16, seed=3700)
+    g = torch.Generator().manual_seed(3701)
+    p.q = (1 + torch.rand(p.q.shape, generator=g)).to(torch.bfloat16)
+    scale = 40.3 / (float(p.q[0, :, 0].float().sum(-1).min()) * math.log2(math.e))
+    for j in range(500):
+        p.k[int(p.table[0, j // 16]), 0, j % 16] = 1.0 if j == at else -0.415
+    q, k, v, table, ln, _, _ = p.cuda()
+    want = p.v[int(p.table[0, at // 16]), 0, at % 16]
+    for ctas in (1, 0):
+        o, _ = E.attn_paged(q, k, v, table, ln, scale=scale, num_ctas=ctas)
+        assert torch.equal(o[0, :, 0].cpu(), want.expand(4, d))
