@@ -523,8 +523,9 @@ def attn_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, bl
 
     q [B, Hq, Nq, d]; k_cache, v_cache [n_pages, Hk, page_size, d], Hq a multiple of Hk
     (query head h reads key head h // (Hq // Hk)). The keys of sequence b are the first
-    prefix_len tokens of the pages in prefix_table (one table for the whole batch, read
-    once for all of its queries), then kv_lens[b] tokens of the pages in block_table[b].
+    prefix_len tokens of the pages in prefix_table (one table for the whole batch; its
+    keys are read once per 256 query rows of a key head, of all sequences together, where
+    that pays, else by each sequence), then kv_lens[b] tokens of the pages in block_table[b].
     Its queries are the last q_lens[b] of these tokens (None: Nq); rows behind q_lens[b]
     are padding. mask 'causal_br': row i sees keys up to i + T - q_lens[b], T = prefix_len
     + kv_lens[b]; 'none': every real row sees all T. A row that sees no key (or only

@@ -2,9 +2,10 @@
 // sequence of the batch shares, then each sequence's own pages.
 //
 // Tasks. A task is up to 256 query rows that read the same keys, of one key
-// head: for the prefix, rows of every sequence together (its keys are read
-// once per 256 rows, not once per sequence); for a sequence's own pages, its
-// rows (queries x the heads that share the key head). The tasks' K/V tiles of
+// head: rows of one sequence (queries x the heads that share the key head) over the
+// prefix's keys and then its own; or, where that saves enough tiles (plan_paged's
+// rule), rows of every sequence together over the prefix, whose keys are then read
+// once per 256 rows of the batch, and each sequence's over its own. The tasks' K/V tiles of
 // 128 keys form one sequence of units (so many for a task's start, then so many
 // a tile), and CTA c takes units [c U / G, (c + 1) U / G): every SM has the same
 // work whatever the lengths are. The lengths are read on the device, so a
@@ -31,10 +32,10 @@
 //
 // What bounds it, and what it takes (GPU time of both kernels, captured calls):
 //   - Long keys of few rows: memory. 64 sequences x 2048 own keys, 8 key heads, d = 128,
-//     pages of 64: 89.5 us, 6.0 TB/s. 96 sequences behind 32768 tokens, G = 4: 121 us
+//     pages of 64: 86.3 us, 6.2 TB/s. 96 sequences behind 32768 tokens, G = 4: 121 us
 //     for 556 MB, 4.6 TB/s (softmax of the prefix's two query tiles, and the cuts).
 //   - Prompt chunks: the tile of two query tiles, 2900 cycles, the pace of this library's
-//     forward kernel with 128 channels; 3 x 512 tokens x 16 heads behind 2048: 39 us.
+//     forward kernel with 128 channels; 3 x 512 tokens x 16 heads behind 2048: 38 us.
 //   - Short keys: latency. A task of one or two tiles takes 3.7 to 4.2 us, one step after
 //     the other: S, softmax (fetching its code: 1700 cycles for the first 64 keys, 530 for
 //     the next), O, the exchange, the store. The next task's tiles and queries wait in
@@ -44,7 +45,11 @@
 //
 // P is rounded to bf16 for the second product (the tensor core's input type;
 // the row sum takes the unrounded values), which moves O by at most 2^-8 of
-// sum p |v|, the size of the final rounding to bf16.
+// sum p |v|, the size of the final rounding to bf16. (Each weight is rounded once; the
+// heaviest of the first 64 keys, and one that raises the maximum by 2^8 in the first
+// half of a tile, is 1 and not rounded. Against 64 bits O is off by 0.0018 of its norm
+// while decoding and in chunks, 0.0022 with one key head of 32 channels; the rounding of
+// the output alone is 0.0016.)
 #include <cuda_bf16.h>
 #include <math_constants.h>
 
@@ -767,8 +772,9 @@ __device__ void paged_softmax(const PagedParams& p, uint8_t* smem, const PBars<D
         // maximum and sum, P as bf16 over S (P of keys [64 j, 64 j + 64) goes over
         // columns [32 j, 32 j + 32), read by then). The code is half of the
         // unrolled tile's, and fetching it is what a tile took when a CTA turned to
-        // it once a task: 7000 cycles against 1300 in a long run of tiles. (32 keys
-        // at a time: 138 us for a long prefix and 96 sequences, 64: 125.)
+        // it once a task: 7000 cycles against 1300 in a long run of tiles. (When the
+        // loop came in, 32 keys at a time took 138 us for a long prefix and 96
+        // sequences, 64 took 125.)
         // A later piece whose maximum passes the reference by more than 2^8 brings
         // O, the sum and the pieces of P before it to its own (rare).
         const int lim = (k < s.pt ? min(seen, end) : min(seen - p.prefix_len, end)) - base;

@@ -152,8 +152,9 @@ int fill_rope(const attn_rope_params* p, attn::RopeParams* r) {
 // Blocks of 256 threads go over tokens (x) and over the heads in turn (y).
 // Few tokens: the heads are dealt to more blocks until the GPU has about
 // kBlocksPerSm blocks an SM; the angles are then computed once per block row.
-// Measured with 4 / 6 / 12 an SM: B5 N1000 H16+4 d64 appended 9.6 / 9.0 / 13.8 us,
-// B4 H16+4 N2048 d128 23.4 / 23.4 / 30.3 us, B2 H20+4 N3000 d64 13.8 / 15.0 / 17.4 us.
+// Measured with 4 / 6 / 12 an SM: B5 N1000 H16+4 d64 appended 9.6 / 9.1 / 13.6 us,
+// B4 H16+4 N2048 d128 22.1 / 22.1 / 28.9 us, B2 H20+4 N3000 d64 12.9 / 13.8 / 16.3 us,
+// B1 H8+8 N16384 d128 28.9 / 28.9 / 32.1 us.
 constexpr int kBlocksPerSm = 6;
 
 int launch_rope(attn::RopeParams* r, int d, int heads, cudaStream_t s) {
@@ -171,8 +172,9 @@ int launch_rope(attn::RopeParams* r, int d, int heads, cudaStream_t s) {
 }
 
 // Blocks of the backward: what an SM holds, each over many tokens, so that few rows
-// of partial sums are left to add (B8 H32+8 N4096 d128 with 2 / 4 / 8 blocks an SM:
-// 197.5 / 200.1 / 201.5 us).
+// of partial sums are left to add (with 1 / 2 / 4 / 8 blocks an SM, d = 128: B8 H32+8
+// N4096 294 / 190 / 193 / 196 us, B4 H16+4 N2048 50.8 / 31.6 / 33.1 / 33.1, B1 H8+8
+// N16384 78.4 / 51.7 / 50.6 / 54.7).
 constexpr int kBwdBlocksPerSm = 2;
 
 int bwd_blocks(const attn_rope_bwd_params* p, int sms) {
@@ -192,15 +194,15 @@ int64_t up256(int64_t x) { return (x + 255) & ~int64_t{255}; }
 
 // The join's blocks take four rows each, parts dealt to their warps, if rows are few
 // (up to kJoinSplitRows an SM) and may have more than kJoinParts parts; else sixteen.
-// Shared blocks and not, d = 128: 64 x 8 rows x 2 key heads behind 8192 tokens 23.6
-// and 30.3 us, 8 x 32 x 8 behind 2048 19.2 and 22.1, 32 x 4 x 8 behind 4096 28.8 and
-// 29.9; 64 an SM instead of 16: 32 x 16 x 8 behind 512 23.8 and 21.5. Own keys only, a
-// task and more a CTA, so a part or two a row: 57 x 4 x 8 22.4 and 20.7.
+// Shared blocks and not, d = 128, 256 own keys each: 64 x 8 rows x 2 key heads behind
+// 8192 tokens 21.0 and 26.0 us, 32 x 4 x 8 behind 4096 20.4 and 21.0, 8 x 32 x 8 behind
+// 2048 19.6 and 19.0; 64 an SM instead of 16: 32 x 16 x 8 behind 512 26.2 and 19.1. Own
+// keys only (1024), a task and more a CTA, so a part or two a row: 57 x 4 x 8 44.6 and 42.2.
 // Sixteen rows a block: eight parts' loads in flight up to kJoinFewRows rows an SM
-// (32 x 16 x 8 behind 2048 24.4 us, four 26.8; 96 x 4 x 8 behind 32768 121.0 and
-// 123.5), four above (32 x 32 x 8 behind 2048 29.9 us, eight 31.4; 3 x 512 x 16
-// behind 2048 38.5 and 41.9). Shared blocks have eight (four: 20.0 and not 18.1 us
-// for 64 x 8 x 2 behind 2048).
+// (32 x 16 x 8 behind 2048 24.8 us, four 26.4; 96 x 4 x 8 behind 32768 119.8 and
+// 121.7), four above (32 x 32 x 8 behind 2048 29.6 us, eight 30.9; 3 x 512 x 16
+// behind 2048 38.2 and 41.7). Shared blocks have eight (four: 64 x 8 x 2 behind 2048
+// 19.8 us and not 17.9, behind 8192 23.7 and not 21.2).
 constexpr int kJoinSplitRows = 16, kJoinParts = 8, kJoinFewRows = 32;
 
 struct PagedPlan {
@@ -236,11 +238,11 @@ void plan_paged(const attn_paged_params* p, int sms, PagedPlan* pl) {
   // and end and a longer join, so it has to save some tiles a CTA: one if a key
   // head's rows fit one query tile, five if not. Measured at d = 128 with 256 own
   // keys, batched and not (sequences x rows x key heads, prefix):
-  //   one tile:  16 x 8 x 2, 512: 0.8 saved, 13.8 and 13.3 us; 2048: 3.1, 15.3 and 17.1
-  //              4 x 4 x 8, 512: 0.6, 13.6 and 13.5;  16 x 4 x 8, 512: 3.1, 16.3 and 17.8
-  //   pairs:     64 x 8 x 2, 512: 3.2, 20.5 and 18.5; 8 x 32 x 8, 2048: 5.8, 18.6 and 19.9
-  //              32 x 16 x 8, 512: 6.2, 25.5 and 26.0; 2048: 25, 28.8 and 39.9
-  //   96 x 4 x 8 behind 32768: 123 and 1141;  3 x 512 x 16 behind 2048 (saves none): 54 and 40
+  //   one tile:  16 x 8 x 2, 512: 0.8 saved, 12.0 and 11.7 us; 2048: 3.1, 12.8 and 14.7
+  //              4 x 4 x 8, 512: 0.6, 12.1 and 12.0;  16 x 4 x 8, 512: 3.1, 15.1 and 16.5
+  //   pairs:     64 x 8 x 2, 512: 3.2, 16.9 and 17.2; 8 x 32 x 8, 2048: 5.8, 19.4 and 18.2
+  //              32 x 16 x 8, 512: 6.2, 19.7 and 23.8; 2048: 25, 24.4 and 37.9
+  //   96 x 4 x 8 behind 32768: 120 and 1126;  3 x 512 x 16 behind 2048 (saves none): 54 and 38
   constexpr int kGainOne = 1, kGainPair = 5;
   const int64_t rs = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk), tr = attn::kPagedTaskRows;
   const int64_t own = (rs + tr - 1) / tr, pre = (p->B * rs + tr - 1) / tr, tiles = (static_cast<int64_t>(p->prefix_len) + 127) / 128;
@@ -504,8 +506,8 @@ int attn_paged(const attn_paged_params* p) {
     return rc;
   // Query tiles as boxes of a tensor map: 128 / G queries of a sequence, or all
   // queries of several sequences (batched prefix tasks). Boxes against rows
-  // gathered one by one: prompt chunks of 3 x 512 tokens behind 2048 40.0 and
-  // 46.7 us, 32 sequences decoding behind 4096 shared tokens 30.0 and 31.7 us.
+  // gathered one by one: prompt chunks of 3 x 512 tokens behind 2048 38.2 and
+  // 43.8 us, 32 sequences decoding behind 4096 shared tokens 26.7 and 28.4 us.
   const bool several = pl.batched && 128 % (p->Nq * G) == 0;
   if (128 % G == 0 && (p->B == 1 || q.sb > 0) && (p->Hq == 1 || q.sh > 0) && (p->Nq == 1 || q.sn > 0)) {
     if ((rc = encode_queries(encode, &k.tm_q, p, q, static_cast<int>(G), several)) != ATTN_OK) return rc;

@@ -12,15 +12,17 @@ namespace attn {
 constexpr int kPagedTaskRows = 256;  // two 128-row query tiles
 // Work is dealt out in units of a quarter of a K/V tile of one query tile. A tile
 // for two query tiles, where the softmax and not memory sets the pace, takes a
-// little longer (with 4 / 5 / 6 units 96 sequences behind 32768 tokens took 144.6 /
-// 137.9 / 143.9 us); a task's start and end as long as a tile (2 / 4 / 6 units: 32
-// sequences behind 4096 tokens 33.6 / 30.0 / 29.7 us, 16 of up to 4096 own keys at
-// d = 32 14.5 / 12.7 / 13.4 us), that of two query tiles longer (4 / 8 / 16 units: 64
-// sequences of 4 rows x 8 key heads behind 512 tokens 35.3 / 30.9 / 30.7 us, 3 x 512
-// tokens x 16 heads behind 2048 43.6 / 43.0 / 42.3 us).
+// little longer (with 4 / 5 / 6 units 96 sequences behind 32768 tokens take 135.8 /
+// 119.8 / 119.3 us, 3 x 512 tokens x 16 heads behind 2048 38.9 / 38.2 / 38.1 us); a
+// task's start and end as long as a tile (2 / 4 / 6 units: 32 sequences behind 4096
+// tokens 30.1 / 26.7 / 27.4 us, 16 of up to 4096 own keys at d = 32 12.9 / 10.8 / 11.3
+// us), that of two query tiles longer (4 / 8 / 16 units: 64 sequences of 4 rows x 8 key
+// heads and 256 own keys behind 512 tokens 33.9 / 29.9 / 29.0 us, the 3 x 512 tokens
+// 39.8 / 39.0 / 38.2 us).
 constexpr int kPagedTile = 4, kPagedPairTile = 5, kPagedTaskCost = 4, kPagedPairTaskCost = 16;
 // Least work that opens another CTA; no less than a tile. (5 / 8 / 16 / 24: 4 sequences
-// behind 512 tokens 11.0 / 10.4 / 12.7 / 17.0 us; larger calls have a CTA an SM anyway.)
+// behind 512 tokens 10.6 / 10.1 / 12.6 / 14.3 us, 7 x 5 tokens behind 1021 12.2 / 11.9 /
+// 15.8 / 16.6 us; larger calls have a CTA an SM anyway.)
 constexpr int kPagedMinUnits = 8;
 
 // Division of n < 2^31 by a divisor that the host knows: n * mul >> (32 + shift)

@@ -344,7 +344,8 @@ typedef enum { ATTN_POS_NONE = 0, ATTN_POS_INT32 = 1, ATTN_POS_INT64 = 2 } attn_
  * stride of a dimension of size 1 is ignored. An output may be its own input; it
  * must not overlap itself (each stride no smaller than what the dimensions of
  * smaller strides reach).
- * d in {32, 64, 128}. Hk 0: queries only (k, k_out NULL).
+ * d in {32, 64, 128}. Hk 0: queries only (k, k_out NULL). Squares are summed in
+ * fp32: a head whose sum of squares passes 3.4e38 gives zeros.
  */
 typedef struct attn_rope_params {
   const void* q;
@@ -447,8 +448,9 @@ int64_t attn_qk_norm_rope_bwd_workspace_bytes(const attn_rope_bwd_params* p);
  *   O[b,h,i,:] = sum_j softmax_j(scale q . k_j) v_j,  LSE the natural-log sum.
  * A row that sees no key, or none whose score is above -inf, gives O = 0,
  * LSE = -inf; one with a score that is NaN or +inf gives NaN for both. Query
- * head h reads key head h / (Hq / Hk). The prefix's keys are read once for up to 256 query rows
- * (Nq * Hq / Hk of each sequence), not once per sequence.
+ * head h reads key head h / (Hq / Hk). Keys are read once for up to 256 query
+ * rows of a key head (a sequence has Nq * Hq / Hk): rows of one sequence, or,
+ * for the prefix where that saves enough, rows of all sequences together.
  * Lengths and tables are read on the device when the kernels run. kv_lens is
  * clamped to what the table holds, q_lens to Nq; a table entry that is not a
  * page of the cache reads as zeros. Slots of a page behind a sequence's end
