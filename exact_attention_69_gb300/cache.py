@@ -373,7 +373,8 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor | None, q_weight: torch.Tensor
     (once: the gradient itself is not differentiable). Runs on the current stream. As for
     any PyTorch op, a backward pass is captured into a graph only while no eager graph
     of the same leaves is alive."""
-    opts = dict(position_offset=int(position_offset), interleaved=bool(interleaved), eps=eps)
+    opts = dict(position_offset=int(position_offset), interleaved=bool(interleaved),
+                eps=None if eps is None else float(eps))
     return _QkNormRope.apply(q, k, q_weight, k_weight, inv_freq, positions, opts)
 
 

@@ -1,5 +1,7 @@
 """GPU: paged attention where its arithmetic is at an edge: maxima that jump inside a
-tile, weights rounded, NaN and infinities in keys and queries that are seen. Against the definition in 64 bits (bounds in cache_oracle)."""
+tile, weights rounded, NaN and infinities in keys and queries that are seen, and forms
+that its callers meet less often. Against the definition in 64 bits (bounds in
+cache_oracle)."""
 import math
 
 import pytest

@@ -229,3 +229,18 @@ def test_infinity_stays_in_its_channel(E, interleaved):  # noqa: F811
             have[0, 1, 2] = 0
             ref[0, 1, 2], bound[0, 1, 2] = 0, 0
             O.check(name + " of other rows", have, ref, bound)
+
+
+def test_gradient_options_by_value(E):  # noqa: F811
+    """eps and the offset given as tensors are read once, in the forward call."""
+    q, g = rnd(180, 1, 2, 9, 32), rnd(181, 1, 2, 9, 32)
+    eps, off = torch.tensor(0.5), torch.tensor(3)
+    x = q.cuda().requires_grad_()
+    f = E.rope_freqs(32)
+    y, _ = E.qk_norm_rope(x, None, inv_freq=f, eps=eps, position_offset=off)
+    eps.fill_(100.0)
+    off.fill_(70)
+    (dx,) = torch.autograd.grad(y, x, g.cuda())
+    pos = 3 + torch.arange(9)[None]
+    O.check("y", y, *O.norm_rope(q, None, pos, f.cpu(), False, 0.5))
+    O.check("dx", dx, *O.norm_rope_back(q, None, g, pos, f.cpu(), False, 0.5)[:2])
