@@ -284,7 +284,7 @@ def qk_norm_rope_bwd(q: torch.Tensor, k: torch.Tensor | None, dq_out: torch.Tens
     Weight gradients have the weights' types (None without a weight, or where weight_grads,
     one for both or a pair, is False); their sums are fp32 in a fixed order."""
     interleaved, eps = bool(interleaved), None if eps is None else float(eps)
-    want_q, want_k = weight_grads if isinstance(weight_grads, tuple) else (weight_grads, weight_grads)
+    want_q, want_k = weight_grads if isinstance(weight_grads, (tuple, list)) else (weight_grads, weight_grads)
     weight_grads = (bool(want_q) and q_weight is not None, bool(want_k) and k_weight is not None)
     key = ("bwd", _sig(q), _sig(k), _sig(dq_out), _sig(dk_out), _sig(q_weight), _sig(k_weight), _sig(inv_freq),
            _sig(positions), interleaved, eps, weight_grads)

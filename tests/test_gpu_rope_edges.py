@@ -244,3 +244,17 @@ def test_gradient_options_by_value(E):  # noqa: F811
     pos = 3 + torch.arange(9)[None]
     O.check("y", y, *O.norm_rope(q, None, pos, f.cpu(), False, 0.5))
     O.check("dx", dx, *O.norm_rope_back(q, None, g, pos, f.cpu(), False, 0.5)[:2])
+
+
+def test_weight_gradients_by_pairs(E):  # noqa: F811
+    """weight_grads: one for both, or a tuple or list of two."""
+    q, k, gq, gk = (rnd(190 + i, 1, h, 9, 32).cuda() for i, h in enumerate((2, 1, 2, 1)))
+    w = weight(194, 32, torch.float32).cuda()
+    f = E.rope_freqs(32)
+    both = E.qk_norm_rope_bwd(q, k, gq, gk, w, w, inv_freq=f)
+    for how in (True, False, (True, False), [False, True], [False, False], (1, 1)):
+        want = how if isinstance(how, (tuple, list)) else (how, how)
+        got = E.qk_norm_rope_bwd(q, k, gq, gk, w, w, inv_freq=f, weight_grads=how)
+        assert torch.equal(got[0], both[0]) and torch.equal(got[1], both[1])
+        for g, b, n in zip(got[2:], both[2:], want):
+            assert torch.equal(g, b) if n else g is None
