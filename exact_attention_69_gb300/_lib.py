@@ -163,6 +163,25 @@ class AttnPagedParams(ctypes.Structure):
            ("num_ctas", ctypes.c_int), ("timeout_ns", ctypes.c_uint64), ("inject", ctypes.c_int)])
 
 
+class AttnLongParams(ctypes.Structure):
+    """Mirror of ``attn_long_params`` (checked against attn_struct_size(3))."""
+
+    _fields_ = (
+        [(n, ctypes.c_void_p) for n in ("q", "k_cache", "v_cache", "bounds", "block_table", "dst_table", "kv_lens",
+                                        "q_lens", "o", "lse", "scores", "blocks", "weights", "weights_out", "kept",
+                                        "new_lens")]
+        + [(n, ctypes.c_int) for n in ("B", "Hq", "Hk", "Nq", "d", "n_pages", "page_size", "table_width")]
+        + [("table_stride", ctypes.c_int64), ("dst_width", ctypes.c_int), ("dst_stride", ctypes.c_int64)]
+        + [(n, ctypes.c_int) for n in ("n", "first", "last", "n_new")]
+        + [("scale", ctypes.c_float), ("decay", ctypes.c_float), ("mask_kind", ctypes.c_int)]
+        + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "o_stride", "k_cache_stride", "v_cache_stride")]
+        + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64), ("stream", ctypes.c_void_p)])
+
+
+LONG_CALLS = ("attn_kv_bounds", "attn_block_scores", "attn_block_select", "attn_blocks", "attn_kv_weights",
+              "attn_kv_evict")
+
+
 class AttnError(RuntimeError):
     def __init__(self, code: int, message: str):
         super().__init__(message)
@@ -218,21 +237,24 @@ def load(path: str = LIB_PATH):
         lib.attn_fwd_noalloc.argtypes = [ctypes.POINTER(AttnParamsEx)]
         lib.attn_fwd_noalloc.restype = i
         for name, cls in (("attn_qk_norm_rope", AttnRopeParams), ("attn_kv_append", AttnRopeParams),
-                          ("attn_qk_norm_rope_bwd", AttnRopeBwdParams), ("attn_paged", AttnPagedParams)):
+                          ("attn_qk_norm_rope_bwd", AttnRopeBwdParams), ("attn_paged", AttnPagedParams),
+                          *((name, AttnLongParams) for name in LONG_CALLS)):
             getattr(lib, name).argtypes = [ctypes.POINTER(cls)]
             getattr(lib, name).restype = i
         for name, cls in (("attn_rope_params_init", AttnRopeParams),
                           ("attn_rope_bwd_params_init", AttnRopeBwdParams),
-                          ("attn_paged_params_init", AttnPagedParams)):
+                          ("attn_paged_params_init", AttnPagedParams),
+                          ("attn_long_params_init", AttnLongParams)):
             getattr(lib, name).argtypes = [ctypes.POINTER(cls)]
             getattr(lib, name).restype = None
         for name, cls in (("attn_qk_norm_rope_bwd_workspace_bytes", AttnRopeBwdParams),
-                          ("attn_paged_workspace_bytes", AttnPagedParams)):
+                          ("attn_paged_workspace_bytes", AttnPagedParams),
+                          ("attn_blocks_workspace_bytes", AttnLongParams)):
             getattr(lib, name).argtypes = [ctypes.POINTER(cls)]
             getattr(lib, name).restype = ctypes.c_int64
         lib.attn_struct_size.argtypes = [i]
         lib.attn_struct_size.restype = i
-        for which, cls in enumerate((AttnRopeParams, AttnRopeBwdParams, AttnPagedParams)):
+        for which, cls in enumerate((AttnRopeParams, AttnRopeBwdParams, AttnPagedParams, AttnLongParams)):
             if lib.attn_struct_size(which) != ctypes.sizeof(cls):
                 raise ImportError(f"{cls.__name__} layout mismatch: library {lib.attn_struct_size(which)} "
                                   f"bytes, binding {ctypes.sizeof(cls)} bytes")

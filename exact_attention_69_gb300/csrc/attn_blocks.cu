@@ -1,0 +1,389 @@
+// attn_blocks.cu -- attention of each query over the pages that it selected.
+//
+// Rows r = n * G + g of one sequence and key head (G query heads share it) go in tiles
+// of 8 or 16. A tile reads every page that one of its queries selected once: a bit per
+// page and query in shared memory, then the list of pages that have a bit, with the
+// queries' bits beside them; a score counts only where the row's query has the bit.
+// Products are computed transposed, S^T = K Q^T and O^T = V^T P^T, so that 16 keys (or 16
+// channels) fill the matrix instruction's long side and 8 rows its short one: for a few
+// rows half the work of the other order. K and V go from global memory to registers
+// that are the instruction's operands; nothing is staged. Each warp takes every
+// (warps)-th group of 16 keys with a running maximum and sum of its own; the warps' parts
+// are joined in shared memory, those of CTAs that share a tile by a second kernel, in
+// a fixed order.
+//
+// The running maximum is a whole number (log2 units) and moves only when a score
+// passes it by more than 8: weights stay below 2^8 and rescaling is exact.
+#include <math_constants.h>
+
+#include "long_dev.cuh"
+#include "long_kernel.h"
+
+namespace attn {
+namespace {
+
+using namespace ldev;
+
+constexpr int kWindow = 1024;  // pages that the bits cover at a time
+constexpr int kThreads = 32 * kBlocksWarps;
+constexpr float kSlack = 8.f;
+
+struct Entry {
+  int block, id;
+};
+
+template <int D, int NT>
+struct Shared {
+  static constexpr int kRows = 8 * NT;
+  struct Lists {
+    uint32_t bits[kRows][kWindow / 32];
+    Entry entry[kWindow];
+    uint16_t who[kWindow];
+    int32_t table[kWindow];
+    uint32_t sums[kBlocksWarps];
+  };
+  struct Join {
+    float o[kBlocksWarps][kRows][D];
+    float2 ml[kBlocksWarps][kRows];
+  };
+  union {
+    Lists l;
+    Join j;
+  };
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) blocks_kernel(const __grid_constant__ LongParams p) {
+  constexpr int kRows = 8 * NT, kC = D / 32, kM = D / 16;
+  constexpr int kVec = D == 32 ? 4 : 8;           // neighbouring channels that a lane takes of V
+  constexpr int kVC = D == 128 ? 2 : 1;           // such runs
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared<D, NT>& sh = *reinterpret_cast<Shared<D, NT>*>(smem);
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = lane >> 2, j = lane & 3;
+  const int rows = p.Nq * p.G, tiles = (rows + kRows - 1) / kRows;
+  const int split = blockIdx.x % p.splits, tile = blockIdx.x / p.splits % tiles;
+  const int hk = blockIdx.y, b = blockIdx.z;
+  const int r0 = tile * kRows, rn = min(rows - r0, kRows);
+  const int tok0 = r0 / p.G, toks = (r0 + rn - 1) / p.G - tok0 + 1;
+  const LongLens lens = long_lens(p, b);
+  const int32_t* lists = p.blocks + ((static_cast<int64_t>(b) * p.Hk + hk) * p.Nq + tok0) * p.n;
+  const int page_mask = (1 << p.page_shift) - 1;
+
+  // this lane's rows (columns 2 j, 2 j + 1 of each group), what they see, and Q
+  int seen[2 * NT];
+  uint32_t bit[2 * NT];
+  uint32_t qf[NT][kC][4];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = 8 * t + 2 * j + x;
+      const int n = (r0 + r) / p.G;
+      seen[2 * t + x] = r < rn ? long_seen(p, lens, n) : 0;
+      bit[2 * t + x] = r < rn ? 1u << (n - tok0) : 0u;
+    }
+    const int r = min(8 * t + i, rn - 1), n = (r0 + r) / p.G, g = r0 + r - n * p.G;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb +
+                             (static_cast<int64_t>(hk) * p.G + g) * p.q_sh + n * p.q_sn + j * 8;
+#pragma unroll
+    for (int c = 0; c < kC; ++c) *reinterpret_cast<uint4*>(qf[t][c]) = ld16(q + c * 32);
+  }
+
+  float o[NT][kM][4];
+  float m[2 * NT], l[2 * NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int c = 0; c < kM; ++c)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[t][c][e] = 0.f;
+#pragma unroll
+  for (int x = 0; x < 2 * NT; ++x) {
+    m[x] = -INFINITY;
+    l[x] = 0.f;
+  }
+
+  const int pages = min(long_pages(p, long_seen(p, lens, min(tok0 + toks, lens.ql) - 1)), p.table_width);
+  const __nv_bfloat16* kbase = static_cast<const __nv_bfloat16*>(p.kc) + hk * p.kc_sh + j * 8;
+  const __nv_bfloat16* vbase = static_cast<const __nv_bfloat16*>(p.vc) + hk * p.vc_sh + i * kVec;
+  const int shift = p.page_shift - 4;             // groups of 16 keys a page
+  const int workers = kBlocksWarps * p.splits, me = split * kBlocksWarps + warp;
+
+  for (int w0 = 0; w0 < (lens.ql > tok0 ? pages : 0); w0 += kWindow) {
+    __syncthreads();
+    for (int x = threadIdx.x; x < kRows * (kWindow / 32); x += kThreads) (&sh.l.bits[0][0])[x] = 0u;
+    for (int x = threadIdx.x; x < min(kWindow, pages - w0); x += kThreads)
+      sh.l.table[x] = p.table[b * p.table_sb + w0 + x];
+    __syncthreads();
+    for (int x = threadIdx.x; x < toks * p.n; x += kThreads) {
+      const int t = x / p.n, blk = lists[x] - w0;
+      const int most = min(long_pages(p, long_seen(p, lens, tok0 + t)) - w0, kWindow);
+      if (blk >= 0 && blk < most) atomicOr(&sh.l.bits[t][blk >> 5], 1u << (blk & 31));
+    }
+    __syncthreads();
+    // the pages that have a bit, in order: thread x has 8 of them
+    constexpr int kPer = kWindow / kThreads;
+    static_assert(kPer == 8, "a byte of the bits a thread");
+    uint32_t mine = 0;
+    const int word = threadIdx.x / 4, sft = (threadIdx.x % 4) * 8;
+    for (int t = 0; t < toks; ++t) mine |= sh.l.bits[t][word];
+    mine = (mine >> sft) & 255u;
+    uint32_t at = __popc(mine);
+#pragma unroll
+    for (int s = 1; s < 32; s *= 2) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, at, s);
+      if (lane >= s) at += y;
+    }
+    if (lane == 31) sh.l.sums[warp] = at;
+    __syncthreads();
+    int count = 0;
+    at -= __popc(mine);
+#pragma unroll
+    for (int s = 0; s < kBlocksWarps; ++s) {
+      if (s < warp) at += sh.l.sums[s];
+      count += sh.l.sums[s];
+    }
+    while (mine != 0u) {
+      const int k = __ffs(mine) - 1, blk = word * 32 + sft + k;
+      mine &= mine - 1;
+      uint32_t who = 0;
+      for (int t = 0; t < toks; ++t) who |= ((sh.l.bits[t][word] >> (sft + k)) & 1u) << t;
+      sh.l.entry[at] = Entry{w0 + blk, sh.l.table[blk]};
+      sh.l.who[at] = static_cast<uint16_t>(who);
+      ++at;
+    }
+    __syncthreads();
+
+    // groups of 16 keys, each warp every workers-th
+    const int units = count << shift;
+    uint4 kf[2][kC];
+    uint32_t vf[4][kVC][kVec / 2];
+    const auto load_k = [&](int u) {
+      const Entry e = sh.l.entry[u >> shift];
+      const int slot = ((u & ((1 << shift) - 1)) << 4) + i;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool live = e.id >= 0 && e.id < p.n_pages && (e.block << p.page_shift) + slot + 8 * h < lens.len;
+        const __nv_bfloat16* k = kbase + e.id * p.kc_sp + ((slot + 8 * h) & page_mask) * p.kc_st;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) kf[h][c] = live ? ld16(k + c * 32) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    // keys 2 j, 2 j + 1, 2 j + 8, 2 j + 9 of the group; zeros behind the sequence's end,
+    // where a page may hold anything
+    const auto load_v = [&](int u) {
+      const Entry e = sh.l.entry[u >> shift];
+      const int slot = ((u & ((1 << shift) - 1)) << 4) + 2 * j;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        const int s = slot + (h & 1) + 8 * (h >> 1);
+        const bool live = e.id >= 0 && e.id < p.n_pages && (e.block << p.page_shift) + s < lens.len;
+        const __nv_bfloat16* v = vbase + e.id * p.vc_sp + s * p.vc_st;
+#pragma unroll
+        for (int c = 0; c < kVC; ++c) {
+          if constexpr (kVec == 8)
+            *reinterpret_cast<uint4*>(vf[h][c]) = live ? ld16(v + c * 64) : make_uint4(0, 0, 0, 0);
+          else
+            *reinterpret_cast<uint2*>(vf[h][c]) = live ? ld8(v) : make_uint2(0, 0);
+        }
+      }
+    };
+    int u = me;
+    if (u < units) {
+      load_k(u);
+      load_v(u);
+    }
+    for (; u < units; u += workers) {
+      float s[NT][4];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < kC; ++c) {
+          mma(s[t], kf[0][c].x, kf[1][c].x, kf[0][c].y, kf[1][c].y, qf[t][c][0], qf[t][c][1]);
+          mma(s[t], kf[0][c].z, kf[1][c].z, kf[0][c].w, kf[1][c].w, qf[t][c][2], qf[t][c][3]);
+        }
+      }
+      const Entry e = sh.l.entry[u >> shift];
+      const uint32_t who = sh.l.who[u >> shift];
+      const int key = (e.block << p.page_shift) + ((u & ((1 << shift) - 1)) << 4) + i;
+      if (u + workers < units) load_k(u + workers);
+      // s[t][0], s[t][1]: key i, rows 2 j and 2 j + 1; s[t][2], s[t][3]: key i + 8
+      bool grow = false;
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = 2 * t + (x & 1);
+          const bool sees = (who & bit[r]) != 0u && key + (x >> 1) * 8 < seen[r];
+          s[t][x] = sees ? s[t][x] * p.c_hi : -INFINITY;
+          grow |= s[t][x] > m[r] + kSlack;  // (m -inf: any score above -inf)
+        }
+      if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int r = 2 * t + x;
+            float top = fmaxf(s[t][x], s[t][x + 2]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            top = fmaxf(m[r], ceilf(top));
+            const float f = m[r] == top ? 1.f : ex2(m[r] - top);  // (m -inf: 0)
+            m[r] = top;
+            l[r] *= f;
+#pragma unroll
+            for (int c = 0; c < kM; ++c) {
+              o[t][c][x] *= f;
+              o[t][c][x + 2] *= f;
+            }
+          }
+      }
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int r = 2 * t + (x & 1);
+          const float base = m[r] == -INFINITY ? 0.f : m[r];
+          s[t][x] = ex2(s[t][x] - base);  // a score of +inf: inf - inf, NaN
+          l[r] += s[t][x];
+        }
+        pf[t][0] = transpose8(pack_bf16(s[t][0], s[t][1]));
+        pf[t][1] = transpose8(pack_bf16(s[t][2], s[t][3]));
+      }
+#pragma unroll
+      for (int c = 0; c < kVC; ++c)
+#pragma unroll
+        for (int w = 0; w < kVec / 2; ++w) {
+          const uint32_t a0 = __byte_perm(vf[0][c][w], vf[1][c][w], 0x5410), a1 = __byte_perm(vf[0][c][w], vf[1][c][w], 0x7632);
+          const uint32_t a2 = __byte_perm(vf[2][c][w], vf[3][c][w], 0x5410), a3 = __byte_perm(vf[2][c][w], vf[3][c][w], 0x7632);
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma(o[t][c * (kVec / 2) + w], a0, a1, a2, a3, pf[t][0], pf[t][1]);
+        }
+      if (u + workers < units) load_v(u + workers);
+    }
+  }
+
+  // the warps' parts: rows 2 j, 2 j + 1; channels i * kVec + 2 w, + 1 of run c
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = 8 * t + 2 * j + x;
+      float z = l[2 * t + x];
+      z += __shfl_xor_sync(0xffffffffu, z, 4);
+      z += __shfl_xor_sync(0xffffffffu, z, 8);
+      z += __shfl_xor_sync(0xffffffffu, z, 16);
+      if (i == 0) sh.j.ml[warp][r] = make_float2(m[2 * t + x], z);
+#pragma unroll
+      for (int c = 0; c < kVC; ++c)
+#pragma unroll
+        for (int w = 0; w < kVec / 2; ++w)
+          *reinterpret_cast<float2*>(&sh.j.o[warp][r][c * 64 + i * kVec + 2 * w]) =
+              make_float2(o[t][c * (kVec / 2) + w][x], o[t][c * (kVec / 2) + w][x + 2]);
+    }
+  __syncthreads();
+  for (int x = threadIdx.x; x < rn * (D / 4); x += kThreads) {
+    const int r = x / (D / 4), c = (x % (D / 4)) * 4;
+    float top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kBlocksWarps; ++w) top = fmaxf(top, sh.j.ml[w][r].x);
+    const float base = top == -INFINITY ? 0.f : top;
+    float sum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kBlocksWarps; ++w) {
+      const float2 ml = sh.j.ml[w][r];
+      const float f = ex2(ml.x - base);
+      const float4 v = *reinterpret_cast<const float4*>(&sh.j.o[w][r][c]);
+      sum += f * ml.y;
+      acc.x += f * v.x;
+      acc.y += f * v.y;
+      acc.z += f * v.z;
+      acc.w += f * v.w;
+    }
+    if (p.splits > 1) {
+      const int64_t at = ((((static_cast<int64_t>(b) * p.Hk + hk) * tiles + tile) * p.splits + split) * kRows + r);
+      *reinterpret_cast<float4*>(p.part_o + at * D + c) = acc;
+      if (c == 0) p.part_ml[at] = make_float2(top, sum);
+      continue;
+    }
+    const int n = (r0 + r) / p.G, h = hk * p.G + r0 + r - n * p.G;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + b * p.o_sb + h * p.o_sh + n * p.o_sn + c) =
+        make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+    if (c == 0 && p.lse != nullptr)
+      p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Nq + n] = CUDART_LN2_F * (top + log2f(sum));
+  }
+}
+
+// Joins the parts of each row; D / 4 threads a row.
+template <int D>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ LongParams p, int tile_rows) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / (D / 4)) + threadIdx.x / (D / 4);
+  const int rows = p.Nq * p.G, tiles = (rows + tile_rows - 1) / tile_rows;
+  if (row >= static_cast<int64_t>(p.B) * p.Hk * rows) return;
+  const int c = (threadIdx.x % (D / 4)) * 4;
+  const int64_t head = row / rows;
+  const int r = static_cast<int>(row - head * rows), tile = r / tile_rows;
+  const int64_t at = (head * tiles + tile) * p.splits * tile_rows + r - tile * tile_rows;
+  float top = -INFINITY;
+  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_ml[at + static_cast<int64_t>(s) * tile_rows].x);
+  const float base = top == -INFINITY ? 0.f : top;
+  float sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s) {
+    const int64_t x = at + static_cast<int64_t>(s) * tile_rows;
+    const float2 ml = p.part_ml[x];
+    const float f = ex2(ml.x - base);
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + x * D + c);
+    sum += f * ml.y;
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+  }
+  const int b = static_cast<int>(head / p.Hk), hk = static_cast<int>(head - static_cast<int64_t>(b) * p.Hk);
+  const int n = r / p.G, h = hk * p.G + r - n * p.G;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + b * p.o_sb + h * p.o_sh + n * p.o_sn + c) =
+      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+  if (c == 0 && p.lse != nullptr)
+    p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Nq + n] = CUDART_LN2_F * (top + log2f(sum));
+}
+
+template <int D, int NT>
+cudaError_t blocks_dim(const LongParams& p, cudaStream_t s) {
+  constexpr int kRows = 8 * NT;
+  const int64_t rows = static_cast<int64_t>(p.Nq) * p.G, tiles = (rows + kRows - 1) / kRows;
+  const dim3 grid(static_cast<unsigned>(tiles * p.splits), p.Hk, p.B);
+  constexpr size_t kSmem = sizeof(Shared<D, NT>);
+  static_assert(kSmem <= 48 * 1024, "no opt-in needed");
+  cudaError_t e = launch(blocks_kernel<D, NT>, grid, kThreads, kSmem, s, p);
+  if (e != cudaSuccess || p.splits == 1) return e;
+  constexpr int kPer = 256 / (D / 4);
+  const int64_t all = rows * p.B * p.Hk;
+  return launch(join_kernel<D>, dim3(static_cast<unsigned>((all + kPer - 1) / kPer)), 256, 0, s, p, kRows);
+}
+
+}  // namespace
+
+cudaError_t launch_blocks(const LongParams& p, int d, cudaStream_t s) {
+  const bool one = blocks_tile_rows(static_cast<int64_t>(p.Nq) * p.G) == 8;
+  switch (d) {
+    case 32: return one ? blocks_dim<32, 1>(p, s) : blocks_dim<32, 2>(p, s);
+    case 64: return one ? blocks_dim<64, 1>(p, s) : blocks_dim<64, 2>(p, s);
+    case 128: return one ? blocks_dim<128, 1>(p, s) : blocks_dim<128, 2>(p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace attn

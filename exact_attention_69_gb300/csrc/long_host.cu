@@ -1,0 +1,301 @@
+// long_host.cu -- C entry points of the long-cache operators (declared in
+// include/attn.h): page bounds and scores, page selection, attention over selected
+// pages, received weights, eviction. Every argument is checked here before any CUDA
+// call; what the device reads (lengths, tables, lists) is checked in the kernels.
+#include <cmath>
+#include <cstring>
+
+#include "attn.h"
+#include "attn_host.h"
+#include "cache_checks.h"
+#include "long_kernel.h"
+
+namespace {
+
+using namespace attn::host;
+using attn::LongParams;
+using attn::RopeTensor;
+
+constexpr int kGridYZ = 65535;  // key heads and sequences are grid dimensions
+
+int check_sizes(const attn_long_params* p, bool queries, bool heads) {
+  if (p == nullptr) return fail_with(ATTN_ERR_INVALID_ARG, "null parameter block");
+  if (p->B < 1 || p->Hk < 1 || p->B > kGridYZ || p->Hk > kGridYZ)
+    return fail_with(ATTN_ERR_INVALID_ARG, "B and Hk must be 1 to %d (got %d, %d)", kGridYZ, p->B, p->Hk);
+  if (heads && p->d != 32 && p->d != 64 && p->d != 128)
+    return fail_with(ATTN_ERR_UNSUPPORTED, "head dimension %d is not one of 32, 64, 128", p->d);
+  if (queries && p->Nq < 1) return fail_with(ATTN_ERR_INVALID_ARG, "Nq must be >= 1 (got %d)", p->Nq);
+  if (queries && heads && (p->Hq < 1 || p->Hq % p->Hk != 0))
+    return fail_with(ATTN_ERR_INVALID_ARG, "Hq (%d) must be a multiple of Hk (%d)", p->Hq, p->Hk);
+  if (queries) {  // (in steps, so that no product passes 64 bits)
+    int64_t rows = static_cast<int64_t>(p->B) * p->Nq;
+    if (rows < kMaxCount) rows *= heads ? p->Hq : p->Hk;
+    if (rows >= kMaxCount) return fail_with(ATTN_ERR_INVALID_ARG, "too many query rows");
+  }
+  return ATTN_OK;
+}
+
+// Sizes, lengths and the table: what every call has.
+int fill(const attn_long_params* p, LongParams* r, bool queries, bool heads, bool table) {
+  int rc = check_sizes(p, queries, heads);
+  if (rc != ATTN_OK) return rc;
+  std::memset(r, 0, sizeof(*r));
+  if ((rc = log2_page(p->page_size, &r->page_shift)) != ATTN_OK) return rc;
+  if (table && p->n_pages < 1) return fail_with(ATTN_ERR_INVALID_ARG, "n_pages must be >= 1");
+  if (p->kv_lens == nullptr || (table && p->block_table == nullptr))
+    return fail_with(ATTN_ERR_INVALID_ARG, "block_table and kv_lens must be non-null");
+  if (!aligned(p->block_table, 4) || !aligned(p->dst_table, 4) || !aligned(p->kv_lens, 4) || !aligned(p->q_lens, 4) ||
+      !aligned(p->lse, 4) || !aligned(p->scores, 4) || !aligned(p->blocks, 4) || !aligned(p->weights, 4) ||
+      !aligned(p->weights_out, 4) || !aligned(p->kept, 4) || !aligned(p->new_lens, 4))
+    return fail_with(ATTN_ERR_MISALIGNED, "tables, lengths, lists, scores, weights and lse must be 4-byte aligned");
+  if (p->table_width < 1 || (table && (p->table_stride < 0 || (p->B > 1 && p->table_stride < p->table_width))))
+    return fail_with(ATTN_ERR_INVALID_ARG, "table_width must be >= 1 and table_stride no smaller");
+  const int64_t max_len = static_cast<int64_t>(p->table_width) * p->page_size;
+  if (max_len >= kMaxCount) return fail_with(ATTN_ERR_INVALID_ARG, "table too wide");
+  if (queries) {
+    if (p->mask_kind != ATTN_MASK_NONE && p->mask_kind != ATTN_MASK_CAUSAL_BR)
+      return fail_with(ATTN_ERR_INVALID_ARG, "mask kind %d is not ATTN_MASK_NONE or ATTN_MASK_CAUSAL_BR", p->mask_kind);
+    r->causal = p->mask_kind == ATTN_MASK_CAUSAL_BR;
+  }
+  r->table = p->block_table;
+  r->table_sb = p->table_stride;
+  r->table_width = p->table_width;
+  r->kv_lens = p->kv_lens;
+  r->q_lens = p->q_lens;
+  r->lse = p->lse;
+  r->scores = p->scores;
+  r->blocks = p->blocks;
+  r->weights = p->weights;
+  r->weights_out = p->weights_out;
+  r->kept = p->kept;
+  r->new_lens = p->new_lens;
+  r->bounds = p->bounds;
+  r->B = p->B;
+  r->Hq = p->Hq;
+  r->Hk = p->Hk;
+  r->Nq = p->Nq;
+  r->G = heads && queries ? p->Hq / p->Hk : 1;
+  r->n_pages = p->n_pages;
+  r->max_len = static_cast<int>(max_len);
+  r->n = p->n;
+  r->first = p->first;
+  r->last = p->last;
+  r->n_new = p->n_new;
+  r->decay = p->decay;
+  return ATTN_OK;
+}
+
+int fill_queries(const attn_long_params* p, LongParams* r) {
+  RopeTensor q;
+  const int rc = tensor(p->q, p->q_stride, p->B, p->Hq, p->Nq, p->d, kRead, "q", &q);
+  r->q = q.p;
+  r->q_sb = q.sb;
+  r->q_sh = q.sh;
+  r->q_sn = q.sn;
+  return rc;
+}
+
+int fill_cache(const attn_long_params* p, LongParams* r, bool keys, bool values, Use use) {
+  RopeTensor c;
+  int rc;
+  if (keys) {
+    if ((rc = tensor(p->k_cache, p->k_cache_stride, p->n_pages, p->Hk, p->page_size, p->d, use, "k_cache", &c)) != ATTN_OK)
+      return rc;
+    r->kc = c.p;
+    r->kc_sp = c.sb;
+    r->kc_sh = c.sh;
+    r->kc_st = c.sn;
+  }
+  if (values) {
+    if ((rc = tensor(p->v_cache, p->v_cache_stride, p->n_pages, p->Hk, p->page_size, p->d, use, "v_cache", &c)) != ATTN_OK)
+      return rc;
+    r->vc = c.p;
+    r->vc_sp = c.sb;
+    r->vc_sh = c.sh;
+    r->vc_st = c.sn;
+  }
+  return ATTN_OK;
+}
+
+int need(const void* p, const char* name) {
+  return p != nullptr ? ATTN_OK : fail_with(ATTN_ERR_INVALID_ARG, "%s must be non-null", name);
+}
+
+int check_scale(const attn_long_params* p, LongParams* r) {
+  if (!std::isfinite(p->scale) || !(p->scale > 0.f)) return fail_with(ATTN_ERR_INVALID_ARG, "scale must be finite and > 0");
+  r->scale = p->scale;
+  r->c_hi = p->scale * 1.4426950408889634f;
+  return ATTN_OK;
+}
+
+int check_taken(const attn_long_params* p, const char* what) {
+  if (p->n < 1) return fail_with(ATTN_ERR_INVALID_ARG, "n (%s) must be >= 1", what);
+  if (p->first < 0 || p->last < 0 || static_cast<int64_t>(p->first) + p->last > p->n)
+    return fail_with(ATTN_ERR_INVALID_ARG, "first and last must be >= 0 and no more than n together");
+  return ATTN_OK;
+}
+
+// attn_blocks: CTAs that share a tile. Enough for kBlocksCtas a SM, each warp with
+// kBlocksUnits groups of 16 keys or more.
+constexpr int kBlocksCtas = 3, kBlocksUnits = 2, kBlocksMaxSplits = 32;
+
+struct BlocksPlan {
+  int splits;
+  int64_t tiles, rows_o, rows_ml;
+  int64_t bytes() const { return rows_o + rows_ml; }
+};
+
+BlocksPlan plan_blocks(const attn_long_params* p, int sms) {
+  BlocksPlan pl;
+  const int64_t rows = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk);
+  const int tr = attn::blocks_tile_rows(rows);
+  pl.tiles = (rows + tr - 1) / tr;
+  const int64_t all = pl.tiles * p->B * p->Hk;
+  int64_t units = static_cast<int64_t>(p->n < p->table_width ? p->n : p->table_width) * (p->page_size / 16);
+  int64_t s = (static_cast<int64_t>(sms) * kBlocksCtas + all - 1) / all;
+  const int64_t most = (units + attn::kBlocksWarps * kBlocksUnits - 1) / (attn::kBlocksWarps * kBlocksUnits);
+  if (s > most) s = most;
+  if (s > kBlocksMaxSplits) s = kBlocksMaxSplits;
+  if (s < 1) s = 1;
+  pl.splits = static_cast<int>(s);
+  pl.rows_o = s > 1 ? all * s * tr * p->d * 4 : 0;
+  pl.rows_ml = s > 1 ? all * s * tr * 8 : 0;
+  return pl;
+}
+
+int this_gpu() {
+  int dev = 0, sms = 0;
+  return this_device(&dev, &sms);
+}
+
+int done(cudaError_t e, const char* what) { return e == cudaSuccess ? ATTN_OK : cuda_error(e, what); }
+
+}  // namespace
+
+extern "C" {
+
+void attn_long_params_init(attn_long_params* p) {
+  if (p) std::memset(p, 0, sizeof(*p));
+}
+
+int attn_kv_bounds(const attn_long_params* p) {
+  clear_error();
+  LongParams r;
+  int rc = fill(p, &r, false, true, true);
+  if (rc != ATTN_OK || (rc = fill_cache(p, &r, true, false, kMapped)) != ATTN_OK || (rc = need(p->bounds, "bounds")) != ATTN_OK)
+    return rc;
+  if (!aligned(p->bounds, 16)) return fail_with(ATTN_ERR_MISALIGNED, "bounds must be 16-byte aligned");
+  if (p->n_new < -1) return fail_with(ATTN_ERR_INVALID_ARG, "n_new must be >= 0, or -1 for all tokens");
+  if ((rc = this_gpu()) != ATTN_OK) return rc;
+  return done(attn::launch_bounds(r, p->d, stream_of(p->stream)), "page bounds launch");
+}
+
+int attn_block_scores(const attn_long_params* p) {
+  clear_error();
+  LongParams r;
+  int rc = fill(p, &r, true, true, true);
+  if (rc != ATTN_OK || (rc = fill_queries(p, &r)) != ATTN_OK || (rc = check_scale(p, &r)) != ATTN_OK ||
+      (rc = need(p->bounds, "bounds")) != ATTN_OK || (rc = need(p->scores, "scores")) != ATTN_OK)
+    return rc;
+  if (!aligned(p->bounds, 16)) return fail_with(ATTN_ERR_MISALIGNED, "bounds must be 16-byte aligned");
+  if ((rc = this_gpu()) != ATTN_OK) return rc;
+  return done(attn::launch_scores(r, p->d, stream_of(p->stream)), "page scores launch");
+}
+
+int attn_block_select(const attn_long_params* p) {
+  clear_error();
+  LongParams r;
+  int rc = fill(p, &r, true, false, false);
+  if (rc != ATTN_OK || (rc = check_taken(p, "pages of a list")) != ATTN_OK || (rc = need(p->scores, "scores")) != ATTN_OK ||
+      (rc = need(p->blocks, "blocks")) != ATTN_OK || (rc = this_gpu()) != ATTN_OK)
+    return rc;
+  return done(attn::launch_select(r, stream_of(p->stream)), "page selection launch");
+}
+
+int64_t attn_blocks_workspace_bytes(const attn_long_params* p) {
+  clear_error();
+  int rc = check_sizes(p, true, true), dev = 0, sms = 0;
+  if (rc != ATTN_OK) return -rc;
+  if (p->n < 1 || p->table_width < 1 || p->page_size < 16)
+    return -fail_with(ATTN_ERR_INVALID_ARG, "n and table_width must be >= 1 and page_size >= 16");
+  if ((rc = this_device(&dev, &sms)) != ATTN_OK) return -rc;
+  return plan_blocks(p, sms).bytes();
+}
+
+int attn_blocks(const attn_long_params* p) {
+  clear_error();
+  LongParams r;
+  RopeTensor o;
+  int rc = fill(p, &r, true, true, true);
+  if (rc != ATTN_OK || (rc = fill_queries(p, &r)) != ATTN_OK || (rc = fill_cache(p, &r, true, true, kRead)) != ATTN_OK ||
+      (rc = check_scale(p, &r)) != ATTN_OK || (rc = need(p->blocks, "blocks")) != ATTN_OK ||
+      (rc = tensor(p->o, p->o_stride, p->B, p->Hq, p->Nq, p->d, kWritten, "o", &o)) != ATTN_OK)
+    return rc;
+  if (p->n < 1 || static_cast<int64_t>(p->n) * p->Nq >= kMaxCount)
+    return fail_with(ATTN_ERR_INVALID_ARG, "n must be >= 1, and n * Nq below 2^30");
+  if (p->workspace && !aligned(p->workspace, 16)) return fail_with(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
+  int dev = 0, sms = 0;
+  if ((rc = this_device(&dev, &sms)) != ATTN_OK) return rc;
+  const BlocksPlan pl = plan_blocks(p, sms);
+  if (pl.bytes() > 0 && (p->workspace == nullptr || p->workspace_bytes < static_cast<uint64_t>(pl.bytes())))
+    return fail_with(ATTN_ERR_INVALID_ARG, "workspace of %llu bytes, this call needs %lld",
+                     static_cast<unsigned long long>(p->workspace ? p->workspace_bytes : 0),
+                     static_cast<long long>(pl.bytes()));
+  r.o = o.p;
+  r.o_sb = o.sb;
+  r.o_sh = o.sh;
+  r.o_sn = o.sn;
+  r.splits = pl.splits;
+  r.part_o = static_cast<float*>(p->workspace);
+  r.part_ml = reinterpret_cast<float2*>(static_cast<char*>(p->workspace) + pl.rows_o);
+  return done(attn::launch_blocks(r, p->d, stream_of(p->stream)), "attention over selected pages launch");
+}
+
+int attn_kv_weights(const attn_long_params* p) {
+  clear_error();
+  LongParams r;
+  int rc = fill(p, &r, true, true, true);
+  if (rc != ATTN_OK || (rc = fill_queries(p, &r)) != ATTN_OK || (rc = fill_cache(p, &r, true, false, kRead)) != ATTN_OK ||
+      (rc = check_scale(p, &r)) != ATTN_OK || (rc = need(p->lse, "lse")) != ATTN_OK ||
+      (rc = need(p->weights_out, "weights_out")) != ATTN_OK)
+    return rc;
+  if (!std::isfinite(p->decay) || p->decay < 0.f) return fail_with(ATTN_ERR_INVALID_ARG, "decay must be finite and >= 0");
+  if (p->decay != 0.f && (rc = need(p->weights, "weights")) != ATTN_OK) return rc;
+  // scale * log2(e) as an fp32 value below it and what that leaves: both positive, so
+  // that a score of -inf stays -inf in the sum of its two products
+  const double c = static_cast<double>(p->scale) * 1.4426950408889634074;
+  r.c_hi = static_cast<float>(c);
+  if (static_cast<double>(r.c_hi) >= c) r.c_hi = std::nextafter(r.c_hi, 0.f);
+  r.c_lo = static_cast<float>(c - static_cast<double>(r.c_hi));
+  if (!std::isfinite(r.c_hi) || !(r.c_lo > 0.f)) return fail_with(ATTN_ERR_INVALID_ARG, "scale is out of range");
+  if ((rc = this_gpu()) != ATTN_OK) return rc;
+  return done(attn::launch_weights(r, p->d, stream_of(p->stream)), "received weights launch");
+}
+
+int attn_kv_evict(const attn_long_params* p) {
+  clear_error();
+  LongParams r;
+  int rc = fill(p, &r, false, true, true);
+  if (rc != ATTN_OK || (rc = fill_cache(p, &r, true, true, kWritten)) != ATTN_OK ||
+      (rc = check_taken(p, "tokens to keep")) != ATTN_OK || (rc = need(p->weights, "weights")) != ATTN_OK ||
+      (rc = need(p->kept, "kept")) != ATTN_OK || (rc = need(p->new_lens, "new_lens")) != ATTN_OK)
+    return rc;
+  if (p->new_lens == p->kv_lens) return fail_with(ATTN_ERR_INVALID_ARG, "new_lens must not be kv_lens");
+  if (static_cast<int64_t>(p->B) * p->Hk >= kMaxCount || static_cast<int64_t>(p->n) >= kMaxCount)
+    return fail_with(ATTN_ERR_INVALID_ARG, "too many rows, or n too large");
+  if (p->dst_table != nullptr) {
+    const int64_t most = r.n < r.max_len ? r.n : r.max_len;
+    if (p->dst_width < 1 || p->dst_stride < 0 || (p->B > 1 && p->dst_stride < p->dst_width))
+      return fail_with(ATTN_ERR_INVALID_ARG, "dst_width must be >= 1 and dst_stride no smaller");
+    if (static_cast<int64_t>(p->dst_width) * p->page_size < most && p->dst_width < p->table_width)
+      return fail_with(ATTN_ERR_INVALID_ARG, "dst_table holds fewer tokens than may be kept");
+    r.dst = p->dst_table;
+    r.dst_sb = p->dst_stride;
+    r.dst_width = p->dst_width;
+  }
+  r.weights_out = p->weights;
+  if ((rc = this_gpu()) != ATTN_OK) return rc;
+  return done(attn::launch_evict(r, p->d, stream_of(p->stream)), "eviction launch");
+}
+
+}  // extern "C"

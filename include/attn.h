@@ -490,7 +490,127 @@ int attn_paged(const attn_paged_params* p);
  * on the block's sizes and prefix_len, not on what kv_lens and q_lens hold. */
 int64_t attn_paged_workspace_bytes(const attn_paged_params* p);
 
-/* sizeof of attn_rope_params (0), attn_rope_bwd_params (1), attn_paged_params (2). */
+/* ------------------------------------------------------------------------
+ * A long paged cache kept affordable: attention over the pages that a cheap score
+ * selects for each query, and a cache cut to the tokens that received the most
+ * attention. Conventions are attn_paged's (without a prefix: a shared prefix is pages
+ * that several rows of the table name): sequence b has kv_lens[b] tokens in the pages
+ * of block_table[b], its queries are the last q_lens[b] of them, and with
+ * ATTN_MASK_CAUSAL_BR query i sees slots j <= i + kv_lens[b] - q_lens[b], with
+ * ATTN_MASK_NONE all of them. Lengths, tables and lists are read on the device when the
+ * kernels run; lengths are clamped, a table entry that is not a page of the cache reads
+ * as zeros and is never written. Pages that a call writes must not be shared between
+ * sequences. Slots behind a sequence's end may hold anything.
+ *
+ * One parameter block serves the six calls; each names the fields that it reads, and
+ * takes the sizes (B, Hk, d, n_pages, page_size, table_width) with the table always.
+ * ------------------------------------------------------------------------ */
+
+typedef struct attn_long_params {
+  const void* q;              /* bf16 [B, Hq, Nq, d] */
+  void* k_cache;              /* bf16 [n_pages, Hk, page_size, d] */
+  void* v_cache;
+  void* bounds;               /* bf16 [n_pages, Hk, 2, d] contiguous: lower, upper */
+  const int32_t* block_table; /* device, [B, table_width] */
+  const int32_t* dst_table;   /* device, [B, dst_width]; attn_kv_evict only, or NULL */
+  const int32_t* kv_lens;     /* device, [B] */
+  const int32_t* q_lens;      /* device, [B], or NULL (Nq each) */
+  void* o;                    /* bf16 [B, Hq, Nq, d] */
+  float* lse;                 /* fp32 [B, Hq, Nq] contiguous */
+  float* scores;              /* fp32 [B, Hk, Nq, table_width] contiguous */
+  int32_t* blocks;            /* [B, Hk, Nq, n] contiguous: entries of a sequence's table row, -1 = none */
+  float* weights;             /* fp32 [n_pages, Hk, page_size] contiguous */
+  float* weights_out;         /* attn_kv_weights: as weights, which it may be */
+  int32_t* kept;              /* [B, Hk, n] contiguous */
+  int32_t* new_lens;          /* [B]; not kv_lens itself */
+  int B, Hq, Hk, Nq, d;       /* Hq a multiple of Hk; d in {32, 64, 128}; B and Hk up to 65535 */
+  int n_pages, page_size;     /* page_size: a power of two >= 16 */
+  int table_width;
+  int64_t table_stride;       /* elements between sequences */
+  int dst_width;
+  int64_t dst_stride;
+  int n;                      /* pages of a query's list; tokens that a sequence keeps */
+  int first, last;            /* of these, always taken at either end: first + last <= n */
+  int n_new;                  /* attn_kv_bounds: newest tokens of each sequence; -1 = all of them */
+  float scale;                /* > 0 and finite */
+  float decay;                /* attn_kv_weights: >= 0 and finite */
+  int mask_kind;              /* ATTN_MASK_NONE or ATTN_MASK_CAUSAL_BR */
+  int64_t q_stride[3], o_stride[3];             /* elements, (b, h, n); zero = contiguous */
+  int64_t k_cache_stride[3], v_cache_stride[3]; /* pages, heads, slots; zero = contiguous */
+  void* workspace;            /* attn_blocks: attn_blocks_workspace_bytes, 16-byte aligned */
+  uint64_t workspace_bytes;
+  void* stream;
+} attn_long_params;
+
+void attn_long_params_init(attn_long_params* p);
+
+/*
+ * attn_kv_bounds: the least and the greatest value of every channel of a page's keys,
+ * over its slots below the sequence's end: bounds[page][h][0] and [1]. Only pages that
+ * hold one of the newest n_new tokens are looked at, each whole, so a recycled page
+ * needs no clearing. A key that is NaN makes both bounds of its channel NaN.
+ * Reads k_cache, kv_lens; writes bounds.
+ */
+int attn_kv_bounds(const attn_long_params* p);
+
+/*
+ * attn_block_scores: for page x of a sequence and query i the largest of the query
+ * heads' bounds, scale * sum_c (min(q_c, 0) lower_c + max(q_c, 0) upper_c): no key of
+ * the page has a greater product with the query. -inf for pages of which the query
+ * sees nothing. An infinite or NaN bound gives infinity or NaN.
+ * Reads q, bounds, kv_lens, q_lens; writes all of scores. (Only table entries that
+ * hold tokens are looked at.)
+ */
+int attn_block_scores(const attn_long_params* p);
+
+/*
+ * attn_block_select: the `first` first and `last` last pages that a query sees and
+ * those of the greatest score among the others, n in all (fewer if it sees fewer):
+ * ties to the lowest page, NaN above everything; ascending, -1 behind them. Exact.
+ * Reads scores, kv_lens, q_lens; writes blocks. d, Hq and block_table's content do not
+ * matter (Hq 0, d 0, block_table NULL are allowed).
+ */
+int attn_block_select(const attn_long_params* p);
+
+/*
+ * attn_blocks: attention of each query over the slots that it sees of the pages in its
+ * list; one list for the query heads of a key head. A page named twice counts once; an
+ * entry that is negative or holds nothing that the query sees counts not at all; any
+ * order. A row without a slot, or without a score above -inf, gives O = 0, LSE = -inf;
+ * one with a score that is NaN or +inf NaN for both. Values (v_cache) of pages that only
+ * some queries of a sequence read, and of slots that only some see, must be finite.
+ * Reads q, k_cache, v_cache, kv_lens, q_lens, blocks; writes o and lse (or NULL).
+ */
+int attn_blocks(const attn_long_params* p);
+/* Bytes of workspace on the current device, or a negative attn_status. */
+int64_t attn_blocks_workspace_bytes(const attn_long_params* p);
+
+/*
+ * attn_kv_weights: weights_out[slot] = decay * weights[slot] + sum over the queries that
+ * see the slot and the query heads of its key head of exp(scale q . k - lse), lse being
+ * what the attention of the same queries returned (rows of -inf count nothing). With
+ * ATTN_MASK_CAUSAL_BR the queries' own slots, the last q_lens[b], are new in this call
+ * and start from zero; with decay 0 all do, and weights is not read. Sums are fp32 in a
+ * fixed order. Slots that no sequence holds stay as they are.
+ * Reads q, k_cache, kv_lens, q_lens, lse, weights (NULL if decay is 0); writes weights_out.
+ */
+int attn_kv_weights(const attn_long_params* p);
+
+/*
+ * attn_kv_evict: of each sequence and key head the n tokens to keep: the `first` first,
+ * the `last` last and those of the greatest weight among the others, ties to the
+ * earliest, NaN above everything; all if there are no more than n. Their keys, values
+ * and weights move, in order, to the front of the sequence's pages, or to the pages of
+ * dst_table[b] (which must not be pages of block_table; a destination that is not a
+ * page, or lies behind dst_width, is left out). new_lens[b] = min(kv_lens[b], n), kept =
+ * the slots that they came from, -1 behind. Each key head keeps tokens of its own, so a
+ * page's bounds have to be found again (attn_kv_bounds, n_new = -1).
+ * Reads kv_lens; reads and writes k_cache, v_cache, weights; writes kept, new_lens.
+ */
+int attn_kv_evict(const attn_long_params* p);
+
+/* sizeof of attn_rope_params (0), attn_rope_bwd_params (1), attn_paged_params (2),
+ * attn_long_params (3). */
 int attn_struct_size(int which);
 
 #ifdef __cplusplus
