@@ -175,7 +175,7 @@ class AttnLongParams(ctypes.Structure):
         + [(n, ctypes.c_int) for n in ("n", "first", "last", "n_new")]
         + [("scale", ctypes.c_float), ("decay", ctypes.c_float), ("mask_kind", ctypes.c_int)]
         + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "o_stride", "k_cache_stride", "v_cache_stride")]
-        + [("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_uint64), ("stream", ctypes.c_void_p)])
+        + [("stream", ctypes.c_void_p)])
 
 
 LONG_CALLS = ("attn_kv_bounds", "attn_block_scores", "attn_block_select", "attn_blocks", "attn_kv_weights",
@@ -248,8 +248,7 @@ def load(path: str = LIB_PATH):
             getattr(lib, name).argtypes = [ctypes.POINTER(cls)]
             getattr(lib, name).restype = None
         for name, cls in (("attn_qk_norm_rope_bwd_workspace_bytes", AttnRopeBwdParams),
-                          ("attn_paged_workspace_bytes", AttnPagedParams),
-                          ("attn_blocks_workspace_bytes", AttnLongParams)):
+                          ("attn_paged_workspace_bytes", AttnPagedParams)):
             getattr(lib, name).argtypes = [ctypes.POINTER(cls)]
             getattr(lib, name).restype = ctypes.c_int64
         lib.attn_struct_size.argtypes = [i]

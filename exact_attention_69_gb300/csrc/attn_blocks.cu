@@ -9,8 +9,8 @@
 // rows half the work of the other order. K and V go from global memory to registers
 // that are the instruction's operands; nothing is staged. Each warp takes every
 // (warps)-th group of 16 keys with a running maximum and sum of its own; the warps' parts
-// are joined in shared memory, those of CTAs that share a tile by a second kernel, in
-// a fixed order.
+// are joined in shared memory, and those of the CTAs that share a tile, which are a
+// cluster, through each other's shared memory: one launch, no workspace, a fixed order.
 //
 // The running maximum is a whole number (log2 units) and moves only when a score
 // passes it by more than 8: weights stay below 2^8 and rescaling is exact.
@@ -28,6 +28,53 @@ constexpr int kWindow = 1024;  // pages that the bits cover at a time
 constexpr int kThreads = 32 * kBlocksWarps;
 constexpr float kSlack = 8.f;
 
+// Parts of a row: maxima (log2 units) and sums first, then the weighted values in order.
+template <int N>
+struct Part {
+  float2 ml[N];
+  float m, base, sum;
+  float4 acc;
+  __device__ __forceinline__ void top() {
+    m = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < N; ++w) m = fmaxf(m, ml[w].x);
+    base = m == -INFINITY ? 0.f : m;
+    sum = 0.f;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void add(int w, float4 v) {
+    const float f = ex2(ml[w].x - base);
+    sum += f * ml[w].y;
+    acc.x += f * v.x;
+    acc.y += f * v.y;
+    acc.z += f * v.z;
+    acc.w += f * v.w;
+  }
+};
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same shared address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer(uint32_t addr, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float2 peer_f2(uint32_t addr, int rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer(addr, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_f4(uint32_t addr, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer(addr, rank))
+               : "memory");
+  return v;
+}
+
 struct Entry {
   int block, id;
 };
@@ -43,8 +90,9 @@ struct Shared {
     uint32_t sums[kBlocksWarps];
   };
   struct Join {
-    float o[kBlocksWarps][kRows][D];
+    float o[kBlocksWarps][kRows][D];  // (the first also takes the joined part)
     float2 ml[kBlocksWarps][kRows];
+    float2 part[kRows];
   };
   union {
     Lists l;
@@ -288,76 +336,45 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) blocks_kernel(const
               make_float2(o[t][c * (kVec / 2) + w][x], o[t][c * (kVec / 2) + w][x + 2]);
     }
   __syncthreads();
-  for (int x = threadIdx.x; x < rn * (D / 4); x += kThreads) {
-    const int r = x / (D / 4), c = (x % (D / 4)) * 4;
-    float top = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kBlocksWarps; ++w) top = fmaxf(top, sh.j.ml[w][r].x);
-    const float base = top == -INFINITY ? 0.f : top;
-    float sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kBlocksWarps; ++w) {
-      const float2 ml = sh.j.ml[w][r];
-      const float f = ex2(ml.x - base);
-      const float4 v = *reinterpret_cast<const float4*>(&sh.j.o[w][r][c]);
-      sum += f * ml.y;
-      acc.x += f * v.x;
-      acc.y += f * v.y;
-      acc.z += f * v.z;
-      acc.w += f * v.w;
-    }
-    if (p.splits > 1) {
-      const int64_t at = ((((static_cast<int64_t>(b) * p.Hk + hk) * tiles + tile) * p.splits + split) * kRows + r);
-      *reinterpret_cast<float4*>(p.part_o + at * D + c) = acc;
-      if (c == 0) p.part_ml[at] = make_float2(top, sum);
-      continue;
-    }
+  const auto store = [&](int r, int c, float top, float sum, float4 acc) {
     const int n = (r0 + r) / p.G, h = hk * p.G + r0 + r - n * p.G;
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + b * p.o_sb + h * p.o_sh + n * p.o_sn + c) =
         make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
     if (c == 0 && p.lse != nullptr)
       p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Nq + n] = CUDART_LN2_F * (top + log2f(sum));
+  };
+  for (int x = threadIdx.x; x < rn * (D / 4); x += kThreads) {
+    const int r = x / (D / 4), c = (x % (D / 4)) * 4;
+    Part<kBlocksWarps> all;
+#pragma unroll
+    for (int w = 0; w < kBlocksWarps; ++w) all.ml[w] = sh.j.ml[w][r];
+    all.top();
+#pragma unroll
+    for (int w = 0; w < kBlocksWarps; ++w) all.add(w, *reinterpret_cast<const float4*>(&sh.j.o[w][r][c]));
+    if (p.splits == 1) {
+      store(r, c, all.m, all.sum, all.acc);
+    } else {
+      *reinterpret_cast<float4*>(&sh.j.o[0][r][c]) = all.acc;
+      if (c == 0) sh.j.part[r] = make_float2(all.m, all.sum);
+    }
   }
-}
-
-// Joins the parts of each row; D / 4 threads a row.
-template <int D>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ LongParams p, int tile_rows) {
-  grid_dep_wait();
-  grid_dep_launch();
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * (256 / (D / 4)) + threadIdx.x / (D / 4);
-  const int rows = p.Nq * p.G, tiles = (rows + tile_rows - 1) / tile_rows;
-  if (row >= static_cast<int64_t>(p.B) * p.Hk * rows) return;
-  const int c = (threadIdx.x % (D / 4)) * 4;
-  const int64_t head = row / rows;
-  const int r = static_cast<int>(row - head * rows), tile = r / tile_rows;
-  const int64_t at = (head * tiles + tile) * p.splits * tile_rows + r - tile * tile_rows;
-  float top = -INFINITY;
-  for (int s = 0; s < p.splits; ++s) top = fmaxf(top, p.part_ml[at + static_cast<int64_t>(s) * tile_rows].x);
-  const float base = top == -INFINITY ? 0.f : top;
-  float sum = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int s = 0; s < p.splits; ++s) {
-    const int64_t x = at + static_cast<int64_t>(s) * tile_rows;
-    const float2 ml = p.part_ml[x];
-    const float f = ex2(ml.x - base);
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + x * D + c);
-    sum += f * ml.y;
-    acc.x += f * v.x;
-    acc.y += f * v.y;
-    acc.z += f * v.z;
-    acc.w += f * v.w;
+  if (p.splits == 1) return;
+  cluster_sync();
+  for (int x = split * kThreads + threadIdx.x; x < rn * (D / 4); x += p.splits * kThreads) {
+    const int r = x / (D / 4), c = (x % (D / 4)) * 4;
+    const uint32_t ml_at = smem_addr(&sh.j.part[r]), o_at = smem_addr(&sh.j.o[0][r][c]);
+    Part<kBlocksMaxSplits> all;
+#pragma unroll
+    for (int w = 0; w < kBlocksMaxSplits; ++w)
+      all.ml[w] = w < p.splits ? peer_f2(ml_at, w) : make_float2(-INFINITY, 0.f);
+    all.top();
+#pragma unroll
+    for (int w = 0; w < kBlocksMaxSplits; ++w)
+      if (w < p.splits) all.add(w, peer_f4(o_at, w));
+    store(r, c, all.m, all.sum, all.acc);
   }
-  const int b = static_cast<int>(head / p.Hk), hk = static_cast<int>(head - static_cast<int64_t>(b) * p.Hk);
-  const int n = r / p.G, h = hk * p.G + r - n * p.G;
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + b * p.o_sb + h * p.o_sh + n * p.o_sn + c) =
-      make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-  if (c == 0 && p.lse != nullptr)
-    p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Nq + n] = CUDART_LN2_F * (top + log2f(sum));
+  cluster_sync();  // (no CTA leaves while another reads its part)
 }
 
 template <int D, int NT>
@@ -367,11 +384,7 @@ cudaError_t blocks_dim(const LongParams& p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(tiles * p.splits), p.Hk, p.B);
   constexpr size_t kSmem = sizeof(Shared<D, NT>);
   static_assert(kSmem <= 48 * 1024, "no opt-in needed");
-  cudaError_t e = launch(blocks_kernel<D, NT>, grid, kThreads, kSmem, s, p);
-  if (e != cudaSuccess || p.splits == 1) return e;
-  constexpr int kPer = 256 / (D / 4);
-  const int64_t all = rows * p.B * p.Hk;
-  return launch(join_kernel<D>, dim3(static_cast<unsigned>((all + kPer - 1) / kPer)), 256, 0, s, p, kRows);
+  return launch(blocks_kernel<D, NT>, grid, kThreads, kSmem, s, p.splits, p);
 }
 
 }  // namespace

@@ -80,60 +80,72 @@ __host__ __device__ constexpr int padded_heads(int g) {
 }
 
 // A warp keeps the bounds of 16 pages in registers and goes over the block's query
-// rows, which lie in shared memory, 8 at a time. Grid: pages x row chunks, key head,
-// sequence.
-template <int D>
-__global__ void __launch_bounds__(32 * kScoreWarps) scores_kernel(const __grid_constant__ LongParams p, int row_chunks) {
+// rows 8 at a time; these come into shared memory 64 at a time, the next ones while
+// these are used. Columns of a product are rows n * Gp + g (Gp padded heads, GP if that
+// is 1 to 8, else 0), so the largest of a token's heads is found among a lane's two
+// columns and its neighbours'. Grid: pages x runs of `tokens` tokens, key head, sequence.
+template <int D, int GP>
+__global__ void __launch_bounds__(32 * kScoreWarps) scores_kernel(const __grid_constant__ LongParams p, int tokens) {
   constexpr int kC = D / 32;  // 16-byte chunks that a lane takes of a vector of d channels
-  __shared__ __align__(16) unsigned char qs[kScoreRows * row_bytes<D>()];
+  __shared__ __align__(16) unsigned char qs[2][kScoreRows * row_bytes<D>()];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, i = lane >> 2, j = lane & 3;
   const int b = blockIdx.z, hk = blockIdx.y;
-  const int chunk = blockIdx.x % row_chunks, page0 = (blockIdx.x / row_chunks) * kScorePages + warp * 16;
-  const int Gp = padded_heads(p.G);
-  // whole tokens a chunk
-  const int per = Gp >= kScoreRows ? 1 : kScoreRows / Gp;
-  const int tok0 = chunk * per, tok1 = min(tok0 + per, p.Nq);
+  const int runs = (p.Nq + tokens - 1) / tokens;
+  const int run = blockIdx.x % runs, page0 = (blockIdx.x / runs) * kScorePages + warp * 16;
+  const int Gp = GP > 0 ? GP : padded_heads(p.G);
+  const int tok0 = run * tokens, tok1 = min(tok0 + tokens, p.Nq);
+  const int rows = (tok1 - tok0) * Gp;
+  const int ids[2] = {page0 + i < p.table_width ? p.table[b * p.table_sb + page0 + i] : -1,
+                      page0 + i + 8 < p.table_width ? p.table[b * p.table_sb + page0 + i + 8] : -1};
   const LongLens lens = long_lens(p, b);
   const int pages = long_pages(p, lens.len);
 
   uint4 lo[2][kC], hi[2][kC];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int page = page0 + i + 8 * h;
-    const int id = page < pages ? p.table[b * p.table_sb + page] : -1;
+    const bool real = page0 + i + 8 * h < pages && ids[h] >= 0 && ids[h] < p.n_pages;
     const __nv_bfloat16* v =
-        static_cast<const __nv_bfloat16*>(p.bounds) + (static_cast<int64_t>(id) * p.Hk + hk) * 2 * D + j * 8;
+        static_cast<const __nv_bfloat16*>(p.bounds) + (static_cast<int64_t>(ids[h]) * p.Hk + hk) * 2 * D + j * 8;
 #pragma unroll
     for (int c = 0; c < kC; ++c) {
-      lo[h][c] = hi[h][c] = make_uint4(0, 0, 0, 0);
-      if (id >= 0 && id < p.n_pages) {
-        lo[h][c] = ld16(v + c * 32);
-        hi[h][c] = ld16(v + D + c * 32);
-      }
+      lo[h][c] = real ? ld16(v + c * 32) : make_uint4(0, 0, 0, 0);
+      hi[h][c] = real ? ld16(v + D + c * 32) : make_uint4(0, 0, 0, 0);
     }
   }
-  float* out = p.scores + (static_cast<int64_t>(b) * p.Hk + hk) * p.Nq * p.table_width;
-
-  float best[2] = {-INFINITY, -INFINITY};  // of a token that has several groups of columns
-  const int rows = (tok1 - tok0) * Gp;
-  for (int base = 0; base < rows; base += kScoreRows) {  // (more than once only for Gp > kScoreRows)
-    __syncthreads();
+  // rows [base, base + 64) into a buffer; padded heads are zeros
+  const auto fetch = [&](int base, int buf) {
     for (int x = threadIdx.x; x < min(kScoreRows, rows - base) * (D / 8); x += 32 * kScoreWarps) {
       const int r = x / (D / 8), c = x % (D / 8), tok = tok0 + (base + r) / Gp, g = (base + r) % Gp;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (g < p.G)
-        v = ld16(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb + (static_cast<int64_t>(hk) * p.G + g) * p.q_sh +
-                 tok * p.q_sn + c * 8);
-      *reinterpret_cast<uint4*>(qs + r * row_bytes<D>() + c * 16) = v;
+      const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb +
+                               (static_cast<int64_t>(hk) * p.G + min(g, p.G - 1)) * p.q_sh + tok * p.q_sn + c * 8;
+      copy16(smem_addr(qs[buf] + r * row_bytes<D>() + c * 16), q, g < p.G ? 16 : 0);
     }
+    copy_commit();
+  };
+  float* out = p.scores + ((static_cast<int64_t>(b) * p.Hk + hk) * p.Nq + tok0) * p.table_width + page0 + i;
+  const bool in[2] = {page0 + i < p.table_width, page0 + i + 8 < p.table_width};
+  const auto put = [&](int tok, const float (&v)[2]) {  // counted from tok0
+    if (tok >= tok1 - tok0) return;
+    const int most = long_pages(p, long_seen(p, lens, tok0 + tok)) - page0 - i;
+    float* at = out + static_cast<int64_t>(tok) * p.table_width;
+    if (in[0]) at[0] = most > 0 ? v[0] * p.scale : -INFINITY;
+    if (in[1]) at[8] = most > 8 ? v[1] * p.scale : -INFINITY;
+  };
+  const auto top = [](float a, float x) { return a > x || a != a ? a : x; };  // (NaN stays: fmax would drop it)
+
+  float best[2] = {-INFINITY, -INFINITY};  // GP 0: of a token that has several groups of columns
+  fetch(0, 0);
+  for (int base = 0, buf = 0; base < rows; base += kScoreRows, buf ^= 1) {
+    copy_wait();
     __syncthreads();
-    if (page0 >= p.table_width) continue;
-    for (int r0 = 0; r0 < kScoreRows && base + r0 < rows; r0 += 8) {
+    if (base + kScoreRows < rows) fetch(base + kScoreRows, buf ^ 1);
+#pragma unroll 2
+    for (int r0 = 0; r0 < min(kScoreRows, rows - base); r0 += 8) {
       float acc[4] = {0.f, 0.f, 0.f, 0.f};
       if (page0 < pages) {
-        const unsigned char* row = qs + (r0 + i) * row_bytes<D>() + j * 16;
+        const unsigned char* row = qs[buf] + (r0 + i) * row_bytes<D>() + j * 16;
 #pragma unroll
         for (int c = 0; c < kC; ++c) {
           uint4 v = *reinterpret_cast<const uint4*>(row + c * 64), neg, pos;
@@ -150,36 +162,30 @@ __global__ void __launch_bounds__(32 * kScoreWarps) scores_kernel(const __grid_c
           mma(acc, hi[0][c].z, hi[1][c].z, hi[0][c].w, hi[1][c].w, pos.z, pos.w);
         }
       }
-      // columns 2 j and 2 j + 1 are rows r and r + 1; NaN stays NaN (fmax would drop it)
+      // columns 2 j and 2 j + 1 are rows r and r + 1
       const int r = base + r0 + 2 * j;
-      const auto put = [&](int h, int tok, float v) {
-        const int page = page0 + i + 8 * h;
-        if (tok < tok1 && page < p.table_width)
-          out[static_cast<int64_t>(tok) * p.table_width + page] =
-              page < long_pages(p, long_seen(p, lens, tok)) ? v * p.scale : -INFINITY;
-      };
-      const auto top = [](float a, float x) { return a > x || a != a ? a : x; };
+      if constexpr (GP == 1) {
+        const float a[2] = {acc[0], acc[2]}, z[2] = {acc[1], acc[3]};
+        put(r, a);
+        put(r + 1, z);
+        continue;
+      }
+      float v[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        float v0 = acc[2 * h], v1 = acc[2 * h + 1];
-        if (Gp == 1) {
-          put(h, tok0 + r, v0);
-          put(h, tok0 + r + 1, v1);
-          continue;
-        }
-        if (r % Gp >= p.G) v0 = -INFINITY;
-        if (r % Gp + 1 >= p.G) v1 = -INFINITY;
-        float v = top(v0, v1);
-        if (Gp >= 4) v = top(v, __shfl_xor_sync(0xffffffffu, v, 1));
-        if (Gp >= 8) v = top(v, __shfl_xor_sync(0xffffffffu, v, 2));
-        if (Gp <= 8) {
-          if (r % Gp == 0) put(h, tok0 + r / Gp, v);
-          continue;
-        }
-        best[h] = top(best[h], v);
+        const int g = r % Gp;
+        v[h] = top(g < p.G ? acc[2 * h] : -INFINITY, g + 1 < p.G ? acc[2 * h + 1] : -INFINITY);
+        if constexpr (GP != 2) v[h] = top(v[h], __shfl_xor_sync(0xffffffffu, v[h], 1));
+        if constexpr (GP == 8 || GP == 0) v[h] = top(v[h], __shfl_xor_sync(0xffffffffu, v[h], 2));
+      }
+      if constexpr (GP > 0) {
+        if (r % GP == 0) put(r / GP, v);
+      } else {
+        best[0] = top(best[0], v[0]);
+        best[1] = top(best[1], v[1]);
         if ((base + r0 + 8) % Gp == 0) {
-          if (j == 0) put(h, tok0 + (base + r0) / Gp, best[h]);
-          best[h] = -INFINITY;
+          if (j == 0) put((base + r0) / Gp, best);
+          best[0] = best[1] = -INFINITY;
         }
       }
     }
@@ -195,15 +201,30 @@ cudaError_t bounds_dim(const LongParams& p, cudaStream_t s) {
     if (p.n_new == 0) return cudaSuccess;
     if (most < x) x = most;
   }
-  return launch(bounds_kernel<D>, dim3(static_cast<unsigned>(x), p.Hk, p.B), kBoundsThreads, 0, s, p);
+  return launch(bounds_kernel<D>, dim3(static_cast<unsigned>(x), p.Hk, p.B), kBoundsThreads, 0, s, 1, p);
 }
+
+// Tokens of a block: enough rows to be worth the pages' bounds (up to kScoreMost), few
+// enough for kScoreBlocks blocks.
+constexpr int kScoreMost = 1024, kScoreBlocks = 4 * 152;
 
 template <int D>
 cudaError_t scores_dim(const LongParams& p, cudaStream_t s) {
-  const int Gp = padded_heads(p.G), per = Gp >= kScoreRows ? 1 : kScoreRows / Gp;
-  const int chunks = (p.Nq + per - 1) / per;
-  const int64_t x = static_cast<int64_t>((p.table_width + kScorePages - 1) / kScorePages) * chunks;
-  return launch(scores_kernel<D>, dim3(static_cast<unsigned>(x), p.Hk, p.B), 32 * kScoreWarps, 0, s, p, chunks);
+  const int Gp = padded_heads(p.G);
+  const int64_t cols = (p.table_width + kScorePages - 1) / kScorePages;
+  int64_t rows = cols * p.B * p.Hk * p.Nq * Gp / kScoreBlocks;
+  rows = rows < kScoreRows ? kScoreRows : (rows > kScoreMost ? kScoreMost : rows / kScoreRows * kScoreRows);
+  const int tokens = static_cast<int>(rows / Gp < 1 ? 1 : (rows / Gp < p.Nq ? rows / Gp : p.Nq));
+  const int64_t x = cols * ((p.Nq + tokens - 1) / tokens);
+  const dim3 grid(static_cast<unsigned>(x), p.Hk, p.B);
+  const int threads = 32 * kScoreWarps;
+  switch (Gp) {
+    case 1: return launch(scores_kernel<D, 1>, grid, threads, 0, s, 1, p, tokens);
+    case 2: return launch(scores_kernel<D, 2>, grid, threads, 0, s, 1, p, tokens);
+    case 4: return launch(scores_kernel<D, 4>, grid, threads, 0, s, 1, p, tokens);
+    case 8: return launch(scores_kernel<D, 8>, grid, threads, 0, s, 1, p, tokens);
+    default: return launch(scores_kernel<D, 0>, grid, threads, 0, s, 1, p, tokens);
+  }
 }
 
 }  // namespace

@@ -5,10 +5,10 @@
 // taken (the first ones and the last ones), ties to the lowest index, listed in
 // ascending order. Values become unsigned keys of the same order (NaN above
 // everything, -0 equal to +0). A team of threads holds a row's keys in registers, each
-// thread a run of consecutive ones, and finds the k-th greatest key bit by bit from the
-// top: the largest T that at least k keys reach. One scan over the team then places
-// the keys above T and the first of those equal to it. No atomics, so the same row
-// always gives the same answer.
+// warp a run of consecutive ones, and finds bit by bit from the top the largest T that
+// at least k keys reach, or earlier one that exactly k reach. Ballots then place the
+// keys above T and the first of those equal to it. No atomics on the way, so the same
+// row always gives the same answer.
 #include "long_dev.cuh"
 #include "long_kernel.h"
 
@@ -28,78 +28,107 @@ template <int T>
 struct Team {
   static_assert(T == 32 || (T % 32 == 0 && T <= 1024), "team");
   int rank;
-  uint32_t* sums;  // shared, two times T / 32 words
+  uint32_t* words;  // shared, two times T / 32
   int turn = 0;
-  __device__ __forceinline__ Team(uint32_t* s) : rank(threadIdx.x % T), sums(s) {}
+  __device__ __forceinline__ Team(uint32_t* s) : rank(threadIdx.x % T), words(s) {}
+  __device__ __forceinline__ int lane() const { return rank % 32; }
+  __device__ __forceinline__ int warp() const { return rank / 32; }
 
-  // Sum over the team.
+  // A value of every warp, in lane w that of warp w (others 0).
+  __device__ __forceinline__ uint32_t gather(uint32_t x) {
+    uint32_t* s = words + (turn ^= T / 32);  // (one barrier a call: the other half may still be read)
+    if (lane() == 0) s[warp()] = x;
+    __syncthreads();
+    return lane() < T / 32 ? s[lane()] : 0u;
+  }
   __device__ __forceinline__ uint32_t sum(uint32_t x) {
     x = __reduce_add_sync(0xffffffffu, x);
-    if constexpr (T > 32) {
-      uint32_t* s = sums + (turn ^= T / 32);
-      if (rank % 32 == 0) s[rank / 32] = x;
-      __syncthreads();
-      x = __reduce_add_sync(0xffffffffu, rank % 32 < T / 32 ? s[rank % 32] : 0u);
-    }
-    return x;
+    return T == 32 ? x : __reduce_add_sync(0xffffffffu, gather(x));
   }
-  // What the threads before this one have together; `all` gets the team's sum.
-  __device__ __forceinline__ uint32_t before(uint32_t x, uint32_t* all) {
-    uint32_t z = x;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, z, o);
-      if (rank % 32 >= o) z += y;
-    }
+  // Bits in which the threads' values differ.
+  __device__ __forceinline__ uint32_t differ(uint32_t ones, uint32_t zeros) {
+    ones = __reduce_or_sync(0xffffffffu, ones);
+    zeros = __reduce_or_sync(0xffffffffu, zeros);
     if constexpr (T > 32) {
-      uint32_t* s = sums + (turn ^= T / 32);
-      if (rank % 32 == 31) s[rank / 32] = z;
-      __syncthreads();
-      uint32_t w = rank % 32 < T / 32 ? s[rank % 32] : 0u;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
-        if (rank % 32 >= o) w += y;
-      }
-      *all = __shfl_sync(0xffffffffu, w, T / 32 - 1);
-      const uint32_t prev = __shfl_sync(0xffffffffu, w, max(rank / 32 - 1, 0));
-      return z - x + (rank >= 32 ? prev : 0u);
+      ones = __reduce_or_sync(0xffffffffu, gather(ones));
+      zeros = __reduce_or_sync(0xffffffffu, gather(zeros));
     }
-    *all = __shfl_sync(0xffffffffu, z, 31);
-    return z - x;
+    return ones & zeros;
+  }
+  // Of a count that is the same in all lanes of a warp: that of the warps before; `all`
+  // gets the sum.
+  __device__ __forceinline__ uint32_t before(uint32_t x, uint32_t* all) {
+    if constexpr (T == 32) {
+      *all = x;
+      return 0u;
+    }
+    const uint32_t w = gather(x);
+    *all = __reduce_add_sync(0xffffffffu, w);
+    return __reduce_add_sync(0xffffffffu, lane() < warp() ? w : 0u);
   }
 };
 
-// The k greatest of the values at [lo, hi), 1 <= k < hi - lo <= T * E, ascending to out.
+// The k greatest of the values at [lo, hi), 1 <= k < hi - lo, hi <= T * E, ascending to
+// out. Warp w has the values 32 E w ..; value e of lane x is number 32 e + x of them.
 template <int T, int E, typename At>
 __device__ __forceinline__ void pick(Team<T>& team, At at, int lo, int hi, int k, int32_t* out) {
   uint32_t key[E];
-  const int first = lo + team.rank * E;
+  const int first = team.warp() * 32 * E + team.lane();
+  uint32_t ones = 0, zeros = 0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) key[e] = first + e < hi ? key_of(at(first + e)) : 0u;
-  uint32_t t = 0;
-  for (uint32_t bit = 0x80000000u; bit != 0; bit >>= 1) {
+  for (int e = 0; e < E; ++e) {
+    const int x = first + 32 * e;
+    key[e] = 0u;  // (no value has this key)
+    if (x >= lo && x < hi) key[e] = key_of(at(x));
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (key[e] != 0u) {
+      ones |= key[e];
+      zeros |= ~key[e];
+    }
+  const uint32_t open = team.differ(ones, zeros);
+  // bits that all keys have above the highest one in which they differ
+  const uint32_t top = open == 0u ? 0u : 0x80000000u >> __clz(open);
+  uint32_t t = T == 32 ? __reduce_or_sync(0xffffffffu, ones) : 0u;
+  if constexpr (T > 32) t = __reduce_or_sync(0xffffffffu, team.gather(__reduce_or_sync(0xffffffffu, ones)));
+  t &= open == 0u ? 0xffffffffu : ~((top << 1) - 1u);
+  bool ties = true;  // more keys than wanted may be equal to t
+  for (uint32_t bit = top; bit != 0; bit >>= 1) {
     uint32_t c = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e) c += key[e] >= (t | bit);
-    if (team.sum(c) >= static_cast<uint32_t>(k)) t |= bit;
+    c = team.sum(c);
+    if (c >= static_cast<uint32_t>(k)) t |= bit;
+    if (c == static_cast<uint32_t>(k)) {
+      ties = false;
+      break;
+    }
   }
-  // (places behind hi have key 0, which no value has)
   uint32_t above = 0, equal = 0, all;
+  if (!ties) t -= 1;  // (t has a bit set: it is some key's prefix above lower ones)
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     above += key[e] > t;
     equal += key[e] == t;
   }
-  uint32_t a = team.before(above, &all);
-  const uint32_t ties = static_cast<uint32_t>(k) - all;  // of those equal to t, the first
-  uint32_t q = team.before(equal, &all);
+  above = __reduce_add_sync(0xffffffffu, above);
+  uint32_t a = team.before(above, &all), q = 0, want = 0;
+  if (ties) {
+    want = static_cast<uint32_t>(k) - all;  // of those equal to t, the first
+    q = team.before(__reduce_add_sync(0xffffffffu, equal), &all);
+  }
+  const uint32_t mine = (1u << team.lane()) - 1u;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const bool up = key[e] > t, eq = key[e] == t;
-    if (up || (eq && q < ties)) out[a + min(q, ties)] = first + e;
-    a += up;
-    q += eq;
+    const uint32_t up = __ballot_sync(0xffffffffu, key[e] > t);
+    uint32_t eq = 0;
+    if (ties) eq = __ballot_sync(0xffffffffu, key[e] == t);
+    const uint32_t qe = q + __popc(eq & mine);
+    const bool take = key[e] > t || (ties && key[e] == t && qe < want);
+    if (take) out[a + __popc(up & mine) + min(qe, want)] = first + 32 * e;
+    a += __popc(up);
+    q += __popc(eq);
   }
 }
 
@@ -125,15 +154,18 @@ __device__ __forceinline__ void pick_long(Team<T>& team, uint32_t* hist, At at, 
     t |= static_cast<uint32_t>(digit) << shift;
   }
   uint32_t done = 0, tied = 0;
+  const uint32_t mine = (1u << team.lane()) - 1u;
   for (int x0 = lo; x0 < hi; x0 += T) {
     const int x = x0 + team.rank;
     const uint32_t key = x < hi ? key_of(at(x)) : 0u;
     const bool eq = x < hi && key == t;
     uint32_t all;
-    const uint32_t q = tied + team.before(eq, &all);
+    const uint32_t same = __ballot_sync(0xffffffffu, eq);
+    const uint32_t q = tied + team.before(__popc(same), &all) + __popc(same & mine);
     tied += all;
     const bool take = key > t || (eq && q < static_cast<uint32_t>(left));
-    const uint32_t a = done + team.before(take, &all);
+    const uint32_t took = __ballot_sync(0xffffffffu, take);
+    const uint32_t a = done + team.before(__popc(took), &all) + __popc(took & mine);
     done += all;
     if (take) out[a] = x;
   }
@@ -163,7 +195,7 @@ __device__ __forceinline__ void choose(Team<T>& team, uint32_t* hist, At at, int
 
 template <int T, int E, bool LONG>
 __global__ void __launch_bounds__(T < 128 ? 128 : T) select_kernel(const __grid_constant__ LongParams p) {
-  __shared__ uint32_t sums[T > 32 ? 2 * (T / 32) : 1];
+  __shared__ uint32_t words[T > 32 ? 2 * (T / 32) : 1];
   __shared__ uint32_t hist[LONG ? 256 : 1];
   grid_dep_wait();
   grid_dep_launch();
@@ -172,7 +204,7 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) select_kernel(const __grid_
   const int i = static_cast<int>(row % p.Nq), b = static_cast<int>(row / (static_cast<int64_t>(p.Nq) * p.Hk));
   const int n = min(long_pages(p, long_seen(p, long_lens(p, b), i)), p.table_width);
   const float* s = p.scores + row * p.table_width;
-  Team<T> team(sums);
+  Team<T> team(words);
   choose<T, E, LONG>(team, hist, [&](int x) { return s[x]; }, n, p.n, p.first, p.last, p.n, p.blocks + row * p.n);
 }
 
@@ -180,7 +212,7 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) select_kernel(const __grid_
 
 template <int T, int E, bool LONG>
 __global__ void __launch_bounds__(T) keep_kernel(const __grid_constant__ LongParams p) {
-  __shared__ uint32_t sums[2 * (T / 32)];
+  __shared__ uint32_t words[2 * (T / 32)];
   __shared__ uint32_t hist[LONG ? 256 : 1];
   grid_dep_wait();
   grid_dep_launch();
@@ -189,7 +221,7 @@ __global__ void __launch_bounds__(T) keep_kernel(const __grid_constant__ LongPar
   if (hk == 0 && threadIdx.x == 0) p.new_lens[b] = min(n, p.n);
   const int32_t* table = p.table + b * p.table_sb;
   const int mask = (1 << p.page_shift) - 1;
-  Team<T> team(sums);
+  Team<T> team(words);
   const auto at = [&](int x) {
     const int id = table[x >> p.page_shift];
     return id >= 0 && id < p.n_pages ? p.weights[((static_cast<int64_t>(id) * p.Hk + hk) << p.page_shift) + (x & mask)] : 0.f;
@@ -202,59 +234,73 @@ __global__ void __launch_bounds__(T) keep_kernel(const __grid_constant__ LongPar
 // writes (places below its end) was read in it or before (sources of later steps are
 // all at or behind its end). Blocks of one list differ in the bytes of a token that
 // they take, never in tokens. Into other pages the lists are cut freely.
-constexpr int kMoveThreads = 256;
+constexpr int kMoveThreads = 256, kMoveDeep = 4;  // tokens that a thread has in flight
 
 template <int D, bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ LongParams p, int steps) {
-  constexpr int kPieces = 4;                       // 16-byte pieces of a token that a block takes
-  constexpr int kSlices = D / 8 / kPieces;         // blocks of K, and of V, for one list
-  constexpr int kTokens = kMoveThreads / kPieces;  // tokens a step
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ LongParams p) {
+  // 16-byte pieces of a token's key, and of its value, that a block takes
+  constexpr int kPieces = IN_PLACE ? 4 : D / 8, kSlices = D / 8 / kPieces;
+  constexpr int kTokens = kMoveThreads / kPieces;
   grid_dep_wait();
   grid_dep_launch();
-  const int slice = blockIdx.x % (2 * kSlices), hk = blockIdx.y, b = blockIdx.z;
-  const bool values = slice >= kSlices;
-  const int piece = (slice % kSlices) * kPieces + threadIdx.x % kPieces;
+  const int slice = blockIdx.x % kSlices, hk = blockIdx.y, b = blockIdx.z;
+  const int piece = slice * kPieces + threadIdx.x % kPieces, row = threadIdx.x / kPieces;
   const int n = min(min(max(p.kv_lens[b], 0), p.max_len), p.n);
   const int32_t* kept = p.kept + (static_cast<int64_t>(b) * p.Hk + hk) * p.n;
   const int32_t *from = p.table + b * p.table_sb, *to = IN_PLACE ? from : p.dst + b * p.dst_sb;
   const int to_width = IN_PLACE ? p.table_width : p.dst_width;
-  __nv_bfloat16* cache = static_cast<__nv_bfloat16*>(values ? p.vc : p.kc) + hk * (values ? p.vc_sh : p.kc_sh) + piece * 8;
-  const int64_t sp = values ? p.vc_sp : p.kc_sp, st = values ? p.vc_st : p.kc_st;
+  __nv_bfloat16* kc = static_cast<__nv_bfloat16*>(p.kc) + hk * p.kc_sh + piece * 8;
+  __nv_bfloat16* vc = static_cast<__nv_bfloat16*>(p.vc) + hk * p.vc_sh + piece * 8;
   const int mask = (1 << p.page_shift) - 1;
-  const bool weigh = slice == 0 && threadIdx.x % kPieces == 0 && p.weights_out != nullptr;
-  int x = IN_PLACE ? 0 : static_cast<int>(blockIdx.x / (2 * kSlices)) * steps * kTokens;
-  const int end = IN_PLACE ? n : min(n, x + steps * kTokens);
-  for (; x < end; x += kTokens) {
-    const int at = x + static_cast<int>(threadIdx.x) / kPieces;
-    int src = -1, to_id = -1, from_id = -1;
-    if (at < end) {
-      src = kept[at];
-      from_id = from[src >> p.page_shift];
-      if ((at >> p.page_shift) < to_width) to_id = to[at >> p.page_shift];
+  const auto weight = [&](int id, int at) {
+    return p.weights_out + (((static_cast<int64_t>(id) * p.Hk + hk) << p.page_shift) + (at & mask));
+  };
+  int x = IN_PLACE ? 0 : static_cast<int>(blockIdx.x / kSlices) * kTokens * kMoveDeep;
+  const int end = IN_PLACE ? n : min(n, x + kTokens * kMoveDeep);
+  for (; x < end; x += kTokens * kMoveDeep) {
+    int src[kMoveDeep], from_id[kMoveDeep], to_id[kMoveDeep];
+    uint4 k[kMoveDeep], v[kMoveDeep];
+    float w[kMoveDeep];
+#pragma unroll
+    for (int e = 0; e < kMoveDeep; ++e) {
+      const int at = x + e * kTokens + row;
+      src[e] = at < end ? kept[at] : -1;
+      to_id[e] = at < end && (at >> p.page_shift) < to_width ? to[at >> p.page_shift] : -1;
     }
-    const bool go = to_id >= 0 && to_id < p.n_pages && !(IN_PLACE && src == at), real = from_id >= 0 && from_id < p.n_pages;
-    uint4 v = make_uint4(0, 0, 0, 0);
-    float w = 0.f;
-    if (go && real) {
-      v = *reinterpret_cast<const uint4*>(cache + from_id * sp + (src & mask) * st);
-      if (weigh) w = p.weights_out[((static_cast<int64_t>(from_id) * p.Hk + hk) << p.page_shift) + (src & mask)];
+#pragma unroll
+    for (int e = 0; e < kMoveDeep; ++e) from_id[e] = src[e] >= 0 ? from[src[e] >> p.page_shift] : -1;
+#pragma unroll
+    for (int e = 0; e < kMoveDeep; ++e) {
+      k[e] = v[e] = make_uint4(0, 0, 0, 0);
+      w[e] = 0.f;
+      if (from_id[e] >= 0 && from_id[e] < p.n_pages) {
+        const int64_t at = src[e] & mask;
+        k[e] = *reinterpret_cast<const uint4*>(kc + from_id[e] * p.kc_sp + at * p.kc_st);
+        v[e] = *reinterpret_cast<const uint4*>(vc + from_id[e] * p.vc_sp + at * p.vc_st);
+        if (piece == 0) w[e] = *weight(from_id[e], src[e]);
+      }
     }
     if constexpr (IN_PLACE) __syncthreads();
-    if (go) {
-      *reinterpret_cast<uint4*>(cache + to_id * sp + (at & mask) * st) = v;
-      if (weigh) p.weights_out[((static_cast<int64_t>(to_id) * p.Hk + hk) << p.page_shift) + (at & mask)] = w;
+#pragma unroll
+    for (int e = 0; e < kMoveDeep; ++e) {
+      const int at = x + e * kTokens + row;
+      if (to_id[e] < 0 || to_id[e] >= p.n_pages || (IN_PLACE && src[e] == at)) continue;
+      const int64_t place = at & mask;
+      *reinterpret_cast<uint4*>(kc + to_id[e] * p.kc_sp + place * p.kc_st) = k[e];
+      *reinterpret_cast<uint4*>(vc + to_id[e] * p.vc_sp + place * p.vc_st) = v[e];
+      if (piece == 0) *weight(to_id[e], at) = w[e];
     }
   }
 }
 
 template <int D>
 cudaError_t move_dim(const LongParams& p, cudaStream_t s) {
-  constexpr int kSlices = 2 * (D / 8 / 4), kTokens = kMoveThreads / 4, kSteps = 4;
   if (p.dst == nullptr)
-    return launch(move_kernel<D, true>, dim3(kSlices, p.Hk, p.B), kMoveThreads, 0, s, p, 0);
+    return launch(move_kernel<D, true>, dim3(D / 32, p.Hk, p.B), kMoveThreads, 0, s, 1, p);
+  constexpr int kTokens = kMoveThreads / (D / 8) * kMoveDeep;
   const int most = p.n < p.max_len ? p.n : p.max_len;
-  const unsigned cuts = static_cast<unsigned>((most + kTokens * kSteps - 1) / (kTokens * kSteps));
-  return launch(move_kernel<D, false>, dim3(kSlices * cuts, p.Hk, p.B), kMoveThreads, 0, s, p, static_cast<int>(kSteps));
+  return launch(move_kernel<D, false>, dim3(static_cast<unsigned>((most + kTokens - 1) / kTokens), p.Hk, p.B),
+                kMoveThreads, 0, s, 1, p);
 }
 
 }  // namespace
@@ -263,25 +309,25 @@ cudaError_t launch_select(const LongParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.B) * p.Hk * p.Nq;
   const dim3 warps(static_cast<unsigned>((rows + 3) / 4)), blocks(static_cast<unsigned>(rows));
   const int w = p.table_width;
-  if (w <= 128) return launch(select_kernel<32, 4, false>, warps, 128, 0, s, p);
-  if (w <= 512) return launch(select_kernel<32, 16, false>, warps, 128, 0, s, p);
-  if (w <= 1024) return launch(select_kernel<32, 32, false>, warps, 128, 0, s, p);
-  if (w <= 4096) return launch(select_kernel<256, 16, false>, blocks, 256, 0, s, p);
-  if (w <= 16384) return launch(select_kernel<1024, 16, false>, blocks, 1024, 0, s, p);
-  return launch(select_kernel<1024, 1, true>, blocks, 1024, 0, s, p);
+  if (w <= 128) return launch(select_kernel<32, 4, false>, warps, 128, 0, s, 1, p);
+  if (w <= 512) return launch(select_kernel<32, 16, false>, warps, 128, 0, s, 1, p);
+  if (w <= 1024) return launch(select_kernel<32, 32, false>, warps, 128, 0, s, 1, p);
+  if (w <= 4096) return launch(select_kernel<256, 16, false>, blocks, 256, 0, s, 1, p);
+  if (w <= 16384) return launch(select_kernel<1024, 16, false>, blocks, 1024, 0, s, 1, p);
+  return launch(select_kernel<1024, 1, true>, blocks, 1024, 0, s, 1, p);
 }
 
 cudaError_t launch_evict(const LongParams& p, int d, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Hk));
   cudaError_t e;
   if (p.max_len <= 4096)
-    e = launch(keep_kernel<1024, 4, false>, grid, 1024, 0, s, p);
+    e = launch(keep_kernel<1024, 4, false>, grid, 1024, 0, s, 1, p);
   else if (p.max_len <= 16384)
-    e = launch(keep_kernel<1024, 16, false>, grid, 1024, 0, s, p);
+    e = launch(keep_kernel<1024, 16, false>, grid, 1024, 0, s, 1, p);
   else if (p.max_len <= 32768)
-    e = launch(keep_kernel<1024, 32, false>, grid, 1024, 0, s, p);
+    e = launch(keep_kernel<1024, 32, false>, grid, 1024, 0, s, 1, p);
   else
-    e = launch(keep_kernel<1024, 1, true>, grid, 1024, 0, s, p);
+    e = launch(keep_kernel<1024, 1, true>, grid, 1024, 0, s, 1, p);
   if (e != cudaSuccess) return e;
   switch (d) {
     case 32: return move_dim<32>(p, s);

@@ -135,32 +135,20 @@ int check_taken(const attn_long_params* p, const char* what) {
   return ATTN_OK;
 }
 
-// attn_blocks: CTAs that share a tile. Enough for kBlocksCtas a SM, each warp with
-// kBlocksUnits groups of 16 keys or more.
-constexpr int kBlocksCtas = 3, kBlocksUnits = 2, kBlocksMaxSplits = 32;
+// attn_blocks: CTAs that share a tile, a power of two. Enough for kBlocksCtas a SM, each
+// warp with kBlocksUnits groups of 16 keys or more.
+constexpr int kBlocksCtas = 3, kBlocksUnits = 2;
 
-struct BlocksPlan {
-  int splits;
-  int64_t tiles, rows_o, rows_ml;
-  int64_t bytes() const { return rows_o + rows_ml; }
-};
-
-BlocksPlan plan_blocks(const attn_long_params* p, int sms) {
-  BlocksPlan pl;
+int blocks_splits(const attn_long_params* p, int sms) {
   const int64_t rows = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk);
   const int tr = attn::blocks_tile_rows(rows);
-  pl.tiles = (rows + tr - 1) / tr;
-  const int64_t all = pl.tiles * p->B * p->Hk;
-  int64_t units = static_cast<int64_t>(p->n < p->table_width ? p->n : p->table_width) * (p->page_size / 16);
-  int64_t s = (static_cast<int64_t>(sms) * kBlocksCtas + all - 1) / all;
-  const int64_t most = (units + attn::kBlocksWarps * kBlocksUnits - 1) / (attn::kBlocksWarps * kBlocksUnits);
-  if (s > most) s = most;
-  if (s > kBlocksMaxSplits) s = kBlocksMaxSplits;
-  if (s < 1) s = 1;
-  pl.splits = static_cast<int>(s);
-  pl.rows_o = s > 1 ? all * s * tr * p->d * 4 : 0;
-  pl.rows_ml = s > 1 ? all * s * tr * 8 : 0;
-  return pl;
+  const int64_t all = (rows + tr - 1) / tr * p->B * p->Hk;
+  const int64_t units = static_cast<int64_t>(p->n < p->table_width ? p->n : p->table_width) * (p->page_size / 16);
+  int s = 1;
+  while (s < attn::kBlocksMaxSplits && all * s < static_cast<int64_t>(sms) * kBlocksCtas &&
+         2 * s * attn::kBlocksWarps * kBlocksUnits <= units)
+    s *= 2;
+  return s;
 }
 
 int this_gpu() {
@@ -212,16 +200,6 @@ int attn_block_select(const attn_long_params* p) {
   return done(attn::launch_select(r, stream_of(p->stream)), "page selection launch");
 }
 
-int64_t attn_blocks_workspace_bytes(const attn_long_params* p) {
-  clear_error();
-  int rc = check_sizes(p, true, true), dev = 0, sms = 0;
-  if (rc != ATTN_OK) return -rc;
-  if (p->n < 1 || p->table_width < 1 || p->page_size < 16)
-    return -fail_with(ATTN_ERR_INVALID_ARG, "n and table_width must be >= 1 and page_size >= 16");
-  if ((rc = this_device(&dev, &sms)) != ATTN_OK) return -rc;
-  return plan_blocks(p, sms).bytes();
-}
-
 int attn_blocks(const attn_long_params* p) {
   clear_error();
   LongParams r;
@@ -233,21 +211,13 @@ int attn_blocks(const attn_long_params* p) {
     return rc;
   if (p->n < 1 || static_cast<int64_t>(p->n) * p->Nq >= kMaxCount)
     return fail_with(ATTN_ERR_INVALID_ARG, "n must be >= 1, and n * Nq below 2^30");
-  if (p->workspace && !aligned(p->workspace, 16)) return fail_with(ATTN_ERR_MISALIGNED, "workspace must be 16-byte aligned");
   int dev = 0, sms = 0;
   if ((rc = this_device(&dev, &sms)) != ATTN_OK) return rc;
-  const BlocksPlan pl = plan_blocks(p, sms);
-  if (pl.bytes() > 0 && (p->workspace == nullptr || p->workspace_bytes < static_cast<uint64_t>(pl.bytes())))
-    return fail_with(ATTN_ERR_INVALID_ARG, "workspace of %llu bytes, this call needs %lld",
-                     static_cast<unsigned long long>(p->workspace ? p->workspace_bytes : 0),
-                     static_cast<long long>(pl.bytes()));
   r.o = o.p;
   r.o_sb = o.sb;
   r.o_sh = o.sh;
   r.o_sn = o.sn;
-  r.splits = pl.splits;
-  r.part_o = static_cast<float*>(p->workspace);
-  r.part_ml = reinterpret_cast<float2*>(static_cast<char*>(p->workspace) + pl.rows_o);
+  r.splits = blocks_splits(p, sms);
   return done(attn::launch_blocks(r, p->d, stream_of(p->stream)), "attention over selected pages launch");
 }
 

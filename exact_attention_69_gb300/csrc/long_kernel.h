@@ -42,9 +42,7 @@ struct LongParams {
   float scale;                  // of the scores
   float c_hi, c_lo;             // scale * log2(e), the fp32 value and what it leaves
   float decay;
-  int splits;                   // CTAs that share a row tile's pages
-  float* part_o;                // [tiles][splits][rows][d] and
-  float2* part_ml;              // [tiles][splits][rows]: parts of a tile (maximum in log2 units, sum)
+  int splits;                   // CTAs (a cluster) that share a row tile's pages
 };
 
 // Keys that query n of a sequence with `len` cached tokens and `ql` queries sees.
@@ -76,6 +74,7 @@ cudaError_t launch_weights(const LongParams& p, int d, cudaStream_t s);
 
 // attn_blocks: rows of a tile (a group of 8 columns of the products, or two).
 __host__ __device__ constexpr int blocks_tile_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
-constexpr int kBlocksWarps = 4;   // warps of a CTA, each with keys of its own
+constexpr int kBlocksWarps = 4;       // warps of a CTA, each with keys of its own
+constexpr int kBlocksMaxSplits = 8;   // CTAs of a cluster on any GPU
 
 }  // namespace attn

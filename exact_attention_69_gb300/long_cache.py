@@ -243,11 +243,7 @@ def _plan_blocks(q, k_cache, v_cache, block_table, kv_lens, blocks, q_lens, scal
         p.o_stride[:] = _heads("out", out, q.shape)
     if lse is not None:
         _plain("lse", lse, torch.float32, device, q.shape[:3])
-    with torch.cuda.device(device):
-        n = _lib.load().attn_blocks_workspace_bytes(ctypes.byref(p))
-    if n < 0:
-        _lib.check(int(-n), "attn_blocks")
-    return bytes(p), int(n)
+    return bytes(p)
 
 
 def attn_blocks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -273,7 +269,7 @@ def attn_blocks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
         plan = _remember(key, _plan_blocks(q, k_cache, v_cache, block_table, kv_lens, blocks, q_lens, scale, mask, out,
                                            lse))
     device = q.device
-    p = _lib.AttnLongParams.from_buffer_copy(plan[0])
+    p = _lib.AttnLongParams.from_buffer_copy(plan)
     p.q, p.k_cache, p.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
     p.block_table, p.kv_lens, p.q_lens, p.blocks = block_table.data_ptr(), kv_lens.data_ptr(), _ptr(q_lens), blocks.data_ptr()
 
@@ -284,9 +280,6 @@ def attn_blocks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
         if z is None and return_lse:
             z = torch.empty(q.shape[:3], dtype=torch.float32, device=device)
         p.lse = _ptr(z)
-        if plan[1]:
-            ws = torch.empty(plan[1], dtype=torch.uint8, device=device)
-            p.workspace, p.workspace_bytes = ws.data_ptr(), plan[1]
         _call("attn_blocks", p, handle)
         if out is not None or lse is not None:
             _wrote([t for t in (out, lse) if t is not None])

@@ -504,6 +504,7 @@ int64_t attn_paged_workspace_bytes(const attn_paged_params* p);
  *
  * One parameter block serves the six calls; each names the fields that it reads, and
  * takes the sizes (B, Hk, d, n_pages, page_size, table_width) with the table always.
+ * No call needs scratch, or allocates any; the first may be a captured one.
  * ------------------------------------------------------------------------ */
 
 typedef struct attn_long_params {
@@ -537,8 +538,6 @@ typedef struct attn_long_params {
   int mask_kind;              /* ATTN_MASK_NONE or ATTN_MASK_CAUSAL_BR */
   int64_t q_stride[3], o_stride[3];             /* elements, (b, h, n); zero = contiguous */
   int64_t k_cache_stride[3], v_cache_stride[3]; /* pages, heads, slots; zero = contiguous */
-  void* workspace;            /* attn_blocks: attn_blocks_workspace_bytes, 16-byte aligned */
-  uint64_t workspace_bytes;
   void* stream;
 } attn_long_params;
 
@@ -582,8 +581,6 @@ int attn_block_select(const attn_long_params* p);
  * Reads q, k_cache, v_cache, kv_lens, q_lens, blocks; writes o and lse (or NULL).
  */
 int attn_blocks(const attn_long_params* p);
-/* Bytes of workspace on the current device, or a negative attn_status. */
-int64_t attn_blocks_workspace_bytes(const attn_long_params* p);
 
 /*
  * attn_kv_weights: weights_out[slot] = decay * weights[slot] + sum over the queries that

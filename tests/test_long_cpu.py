@@ -24,7 +24,7 @@ def block(name):
     p = _lib.AttnLongParams()
     given = dict(
         attn_kv_bounds=("k_cache", "bounds"), attn_block_scores=("q", "bounds", "scores"),
-        attn_block_select=("scores", "blocks"), attn_blocks=("q", "k_cache", "v_cache", "o", "lse", "blocks", "workspace"),
+        attn_block_select=("scores", "blocks"), attn_blocks=("q", "k_cache", "v_cache", "o", "lse", "blocks"),
         attn_kv_weights=("q", "k_cache", "lse", "weights", "weights_out"),
         attn_kv_evict=("k_cache", "v_cache", "weights", "kept", "new_lens"))[name]
     for n in given + ("block_table",):
@@ -32,7 +32,6 @@ def block(name):
     p.kv_lens = 2 * A
     p.B, p.Hq, p.Hk, p.Nq, p.d, p.scale, p.mask_kind = 2, 8, 2, 3, 64, 0.125, _lib.ATTN_MASK_CAUSAL_BR
     p.n_pages, p.page_size, p.table_width, p.table_stride, p.n, p.decay = 9, 16, 4, 4, 8, 1.0
-    p.workspace_bytes = 1 << 40
     return p
 
 
@@ -54,7 +53,7 @@ BAD = dict(
     attn_block_select=COMMON + QUERIES + TAKEN + [(dict(scores=None), INV), (dict(blocks=None), INV), (dict(blocks=A + 2), MIS)],
     attn_blocks=COMMON + TABLE + HEADS + QUERIES + Q + KEYS + VALUES + [
         (dict(blocks=None), INV), (dict(o=None), INV), (dict(o=A + 8), MIS), (dict(o_stride=(64, 64, 0)), INV), (dict(n=0), INV),
-        (dict(n=1 << 29), INV), (dict(workspace=A + 8), MIS), (dict(lse=A + 2), MIS)],
+        (dict(n=1 << 29), INV), (dict(lse=A + 2), MIS)],
     attn_kv_weights=COMMON + TABLE + HEADS + QUERIES + Q + KEYS + [(dict(lse=None), INV), (dict(weights=None), INV),
                                                                    (dict(weights_out=None), INV), (dict(decay=-1.0), INV), (dict(decay=math.nan), INV),
                                                                    (dict(weights=A + 2), MIS), (dict(scale=1e-44), INV)],
@@ -81,7 +80,6 @@ def test_refuses(lib, name, changes, code):
 def test_null_blocks(lib):
     for name in _lib.LONG_CALLS:
         assert getattr(lib, name)(None) == INV
-    assert lib.attn_blocks_workspace_bytes(None) == -INV
 
 
 def test_python_refuses(lib):
