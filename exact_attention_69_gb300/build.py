@@ -24,7 +24,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 SOURCES = ["attn_host.cu", "attn_fwd_d32.cu", "attn_fwd_d64.cu", "attn_fwd_d128.cu", "attn_bwd.cu",
            "rope.cu", "attn_paged.cu", "cache_host.cu", "block_scores.cu", "block_select.cu", "attn_blocks.cu",
-           "kv_weights.cu", "long_host.cu"]
+           "kv_weights.cu", "long_tiles.cu", "long_host.cu"]
 
 
 def nvcc() -> str:

@@ -21,6 +21,7 @@
 #include "attn.h"
 #include "attn_host.h"
 #include "attn_kernel.h"
+#include "long_kernel.h"
 #include "paged_kernel.h"
 
 namespace {
@@ -449,6 +450,19 @@ int paged_take(int dev, uint32_t word[4]) {
   return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "reading the paged kernels' status");
 }
 
+// The same for the long-cache kernels.
+bool g_long_used[kMaxDevices] = {};
+
+int long_take(int dev, uint32_t word[4]) {
+  word[0] = word[1] = word[2] = word[3] = 0;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!g_long_used[dev]) return ATTN_OK;
+  }
+  const cudaError_t e = attn::long_take_status(word);
+  return e == cudaSuccess ? ATTN_OK : cuda_fail(e, "reading the long-cache kernels' status");
+}
+
 // Reads and clears the no-alloc entry point's status word on device `dev`
 // (zeros if that entry point was not used there), and forgets its per-device
 // state (under g_mu); defined with it below.
@@ -506,6 +520,11 @@ int this_device(int* dev, int* sms) {
 void paged_used(int dev) {
   std::lock_guard<std::mutex> lk(g_mu);
   g_paged_used[dev] = true;
+}
+
+void long_used(int dev) {
+  std::lock_guard<std::mutex> lk(g_mu);
+  g_long_used[dev] = true;
 }
 
 }  // namespace host
@@ -610,6 +629,8 @@ int attn_get_device_status(uint32_t* detail) {
   if (rc != ATTN_OK) return rc;
   if (word[0] == 0) std::memcpy(word, word2, sizeof(word));
   if ((rc = paged_take(dev, word2)) != ATTN_OK) return rc;
+  if (word[0] == 0) std::memcpy(word, word2, sizeof(word));
+  if ((rc = long_take(dev, word2)) != ATTN_OK) return rc;
   if (word[0] == 0) std::memcpy(word, word2, sizeof(word));
   if (detail) std::memcpy(detail, word, sizeof(word));
   if (word[0] == 0) return ATTN_OK;

@@ -21,6 +21,7 @@ int tensor_map_encoder(PFN_cuTensorMapEncodeTiled_v12000* fn);
 // The current device, checked to be an sm_103 GPU, and its SM count. Allocates nothing.
 int this_device(int* dev, int* sms);
 void paged_used(int dev);  // from now on attn_get_device_status reads the paged kernels' word there
+void long_used(int dev);   // the same for the long-cache kernels
 
 }  // namespace host
 }  // namespace attn

@@ -7,6 +7,9 @@
 // query heads that share the key head.
 #include "long_dev.cuh"
 #include "long_kernel.h"
+#ifndef TILE_ROWS
+#define TILE_ROWS 33
+#endif
 
 namespace attn {
 namespace {
@@ -239,6 +242,7 @@ cudaError_t launch_bounds(const LongParams& p, int d, cudaStream_t s) {
 }
 
 cudaError_t launch_scores(const LongParams& p, int d, cudaStream_t s) {
+  if (static_cast<int64_t>(p.Nq) * p.G >= TILE_ROWS) return launch_scores_tiles(p, d, s);
   switch (d) {
     case 32: return scores_dim<32>(p, s);
     case 64: return scores_dim<64>(p, s);

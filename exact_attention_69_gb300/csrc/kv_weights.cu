@@ -8,6 +8,9 @@
 // where the weight is not.
 #include "long_dev.cuh"
 #include "long_kernel.h"
+#ifndef TILE_ROWS
+#define TILE_ROWS 33
+#endif
 
 namespace attn {
 namespace {
@@ -158,6 +161,7 @@ cudaError_t weights_dim(const LongParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_weights(const LongParams& p, int d, cudaStream_t s) {
+  if (static_cast<int64_t>(p.Nq) * p.G >= TILE_ROWS) return launch_weights_tiles(p, d, s);
   switch (d) {
     case 32: return weights_dim<32>(p, s);
     case 64: return weights_dim<64>(p, s);

@@ -153,7 +153,9 @@ int blocks_splits(const attn_long_params* p, int sms) {
 
 int this_gpu() {
   int dev = 0, sms = 0;
-  return this_device(&dev, &sms);
+  const int rc = this_device(&dev, &sms);
+  if (rc == ATTN_OK) long_used(dev);
+  return rc;
 }
 
 int done(cudaError_t e, const char* what) { return e == cudaSuccess ? ATTN_OK : cuda_error(e, what); }

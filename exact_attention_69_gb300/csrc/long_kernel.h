@@ -71,6 +71,11 @@ cudaError_t launch_select(const LongParams& p, cudaStream_t s);
 cudaError_t launch_evict(const LongParams& p, int d, cudaStream_t s);
 cudaError_t launch_blocks(const LongParams& p, int d, cudaStream_t s);
 cudaError_t launch_weights(const LongParams& p, int d, cudaStream_t s);
+// The same for many query rows (long_tiles.cu).
+cudaError_t launch_scores_tiles(const LongParams& p, int d, cudaStream_t s);
+cudaError_t launch_weights_tiles(const LongParams& p, int d, cudaStream_t s);
+// Reads and clears the current device's status word of these two.
+cudaError_t long_take_status(uint32_t word[4]);
 
 // attn_blocks: rows of a tile (a group of 8 columns of the products, or two).
 __host__ __device__ constexpr int blocks_tile_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }

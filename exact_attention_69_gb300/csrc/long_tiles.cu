@@ -1,0 +1,451 @@
+// long_tiles.cu -- page scores and received weights for many query rows, on the tensor
+// core's full tiles (tcgen05, accumulators in TMEM).
+//
+// Both are products of 128 cached things (pages' bounds, or keys) with query rows, of
+// which only a reduction over rows is kept: the largest over a token's heads, or the sum
+// of exponentials over all rows. So the cached side is the long one: it stays in shared
+// memory as the A operand, query rows stream by as B, 64 at a time, and a thread owns one
+// page or key (a TMEM lane) and walks along the rows (columns) with its running maximum or
+// sum in a register: no shuffles, no padding of heads, neighbouring lanes write
+// neighbouring places. A CTA is four warps; several share an SM. While the tensor core
+// works on tile t, the warps reduce tile t - 1 and the rows of tile t + 1 are on their
+// way.
+//
+// Every wait is bounded: when one runs out the CTA notes it in the status word, leaves its
+// loop, waits (bounded) for its products in flight, frees TMEM and returns.
+#include <math_constants.h>
+
+#include "attn_sm103.cuh"
+#include "long_dev.cuh"
+#include "long_kernel.h"
+
+namespace attn {
+namespace dev {
+
+__device__ uint32_t g_long_status[4];
+
+constexpr int kTileThreads = 128, kTileRows = 64;  // threads: one for each of 128 pages or keys
+constexpr uint32_t kTileCols = 2 * kTileRows;      // TMEM columns: two accumulators
+constexpr uint32_t kRoleTiles = 4;
+
+// True once phase `parity` of `bar` is complete; false after about two seconds.
+__device__ __forceinline__ bool tile_wait(uint32_t bar, uint32_t parity, int tile) {
+  if (mbar_test(bar, parity)) return true;
+  for (int i = 0; i < 10000; ++i)
+    if (mbar_test_sleep(bar, parity, kSleepHintNs)) return true;
+  if (atomicCAS(g_long_status, 0u, kStatusTimeout) == 0u) {
+    g_long_status[1] = kRoleTiles;
+    g_long_status[2] = static_cast<uint32_t>(tile);
+    g_long_status[3] = blockIdx.x;
+    __threadfence();
+  }
+  return false;
+}
+
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Byte of 16-byte piece `c` of row r in a K-major operand of `rows` rows: blocks of 64
+// channels one after the other, 128-byte rows swizzled over 8 (32 channels: 64-byte
+// rows, swizzled over pairs of 4).
+template <int K>
+__device__ __forceinline__ uint32_t operand_at(int r, int c, int rows) {
+  if constexpr (K >= 64) return (c >> 3) * rows * 128 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// D (128 x 64) = A (128 x K) B (64 x K)^T, operands at a and b.
+template <int K>
+__device__ __forceinline__ void issue_tile(uint32_t d_tmem, uint32_t a, uint32_t b) {
+  constexpr uint32_t kIdesc = make_idesc(128, kTileRows, false);
+  constexpr int kRow = K >= 64 ? 128 : 64;
+  constexpr uint32_t kLayout = K >= 64 ? 2u : 4u;
+  const uint64_t da = smem_desc(a, 16, 8 * kRow, kLayout), db = smem_desc(b, 16, 8 * kRow, kLayout);
+  if constexpr (K == 32) {
+    mma_ss2<2>(d_tmem, da, db, kIdesc, 0u);
+  } else {
+#pragma unroll
+    for (int c = 0; c < K / 64; ++c)
+      mma_ss4<2, 4, 6>(d_tmem, da + (c * 128 * kRow >> 4), db + (c * kTileRows * kRow >> 4), kIdesc, c != 0);
+  }
+}
+
+// What both kernels set up: barriers and TMEM.
+struct Tiles2 {
+  uint32_t bar[2];
+  uint32_t tmem;
+  __device__ __forceinline__ uint32_t d(int t) const { return tmem + (t & 1) * kTileRows; }
+  __device__ __forceinline__ bool wait(int t) const { return tile_wait(bar[t & 1], (t >> 1) & 1, t); }
+  __device__ __forceinline__ void begin(uint64_t* bars, uint32_t* slot) {
+    bar[0] = smem_u32(bars);
+    bar[1] = bar[0] + 8;
+    if (threadIdx.x == 0) {
+      mbar_init(bar[0], 1);
+      mbar_init(bar[1], 1);
+      fence_barrier_init();
+    }
+    if (threadIdx.x < 32) {
+      tmem_alloc(smem_u32(slot), kTileCols);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    tmem = *slot;
+  }
+  __device__ __forceinline__ void end() const {
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x < 32) tmem_dealloc(tmem, kTileCols);
+  }
+};
+
+// ------------------------------------------------------------------ scores
+
+template <int D>
+struct ScoreSmem {
+  static constexpr int kK = 2 * D;  // lower and upper bounds side by side
+  static constexpr int kA = 128 * kK * 2, kB = kTileRows * kK * 2;
+  static constexpr int kBytes = kA + kB + 1024;
+};
+
+// B holds min(q, 0) in its first D channels and max(q, 0) in the others. G: query heads of a
+// key head (0: any number).
+template <int D, int G>
+__global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_constant__ LongParams p, int tokens) {
+  using S = ScoreSmem<D>;
+  constexpr int kPieces = D / 8, kLoads = kTileRows * kPieces / kTileThreads;
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t bars[2];
+  __shared__ uint32_t slot;
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const uint32_t a_at = smem_u32(smem), b_at = a_at + S::kA;
+  Tiles2 tl;
+  tl.begin(bars, &slot);
+  ldev::grid_dep_launch();
+  ldev::grid_dep_wait();
+
+  const int b = blockIdx.z, hk = blockIdx.y, heads = G > 0 ? G : p.G;
+  const int runs = (p.Nq + tokens - 1) / tokens;
+  const int tok0 = static_cast<int>(blockIdx.x % runs) * tokens, page0 = static_cast<int>(blockIdx.x / runs) * 128;
+  const LongLens lens = long_lens(p, b);
+  const int toks = min(tokens, p.Nq - tok0);
+  const int page = page0 + static_cast<int>(threadIdx.x);
+  float* out = p.scores + ((static_cast<int64_t>(b) * p.Hk + hk) * p.Nq + tok0) * p.table_width + page;
+  // pages of which no query of the run sees anything need no product
+  const int live = min(tok0 + toks, lens.ql);
+  const int pages = live > tok0 ? long_pages(p, long_seen(p, lens, live - 1)) : 0;
+  const bool some = page0 < pages;
+  const int rows = some ? (live - tok0) * heads : 0, tiles = (rows + kTileRows - 1) / kTileRows;
+
+  // query rows of a tile: pieces of 16 bytes, D / 8 threads a row
+  uint4 q[kLoads];
+  const auto load = [&](int t) {
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) {
+      const int x = e * kTileThreads + static_cast<int>(threadIdx.x), r = t * kTileRows + x / kPieces, c = x % kPieces;
+      const int n = r / heads, g = r - n * heads;
+      q[e] = make_uint4(0, 0, 0, 0);
+      if (r < rows)
+        q[e] = ldev::ld16(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb +
+                          (static_cast<int64_t>(hk) * heads + g) * p.q_sh + (tok0 + n) * p.q_sn + c * 8);
+    }
+  };
+  if (tiles > 0) {
+    load(0);
+    for (int x = threadIdx.x; x < 128 * 2 * kPieces; x += kTileThreads) {
+      const int r = x / (2 * kPieces), c = x % (2 * kPieces);
+      const int id = page0 + r < pages ? p.table[b * p.table_sb + page0 + r] : -1;
+      const bool real = id >= 0 && id < p.n_pages;
+      ldev::copy16(a_at + operand_at<S::kK>(r, c, 128),
+                   static_cast<const __nv_bfloat16*>(p.bounds) + ((real ? static_cast<int64_t>(id) : 0) * p.Hk + hk) * 2 * D + c * 8,
+                   real ? 16 : 0);
+    }
+    ldev::copy_commit();
+  }
+
+  float best = -INFINITY;
+  int tok = 0, g = 0;  // the token and head that the next column is
+  const auto reduce = [&](int t) {
+    uint32_t v[2][32];
+    tmem_ld32(tl.d(t) + ((threadIdx.x >> 5) << 21), v[0]);
+    tmem_ld32(tl.d(t) + ((threadIdx.x >> 5) << 21) + 32, v[1]);
+#pragma unroll
+    for (int c = 0; c < kTileRows; ++c) {
+      best = max_nan(best, __uint_as_float(v[c >> 5][c & 31]));
+      bool last;
+      if constexpr (G > 0) {
+        last = (c + 1) % G == 0;  // (G divides the tile)
+      } else {
+        last = ++g == heads;
+      }
+      if (last) {
+        if (tok < live - tok0 && page < p.table_width) {
+          const bool sees = page < long_pages(p, long_seen(p, lens, tok0 + tok));
+          out[static_cast<int64_t>(tok) * p.table_width] = sees ? best * p.scale : -INFINITY;
+        }
+        best = -INFINITY;
+        g = 0;
+        ++tok;
+      }
+    }
+  };
+
+  bool ok = true;
+  int t = 0;
+  for (; t < tiles; ++t) {
+    if (t > 0) ok = tl.wait(t - 1);  // its operand may be replaced
+#pragma unroll
+    for (int e = 0; e < kLoads; ++e) {
+      const int x = e * kTileThreads + static_cast<int>(threadIdx.x), r = x / kPieces, c = x % kPieces;
+      const __nv_bfloat162 zero(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
+      uint4 neg, pos;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 y = reinterpret_cast<const __nv_bfloat162*>(&q[e])[i];
+        reinterpret_cast<__nv_bfloat162*>(&neg)[i] = __hmin2_nan(y, zero);
+        reinterpret_cast<__nv_bfloat162*>(&pos)[i] = __hmax2_nan(y, zero);
+      }
+      *reinterpret_cast<uint4*>(smem + S::kA + operand_at<S::kK>(r, c, kTileRows)) = neg;
+      *reinterpret_cast<uint4*>(smem + S::kA + operand_at<S::kK>(r, c + kPieces, kTileRows)) = pos;
+    }
+    if (t == 0) ldev::copy_wait();
+    fence_async_smem();
+    tc_fence_before();
+    if (__syncthreads_or(!ok)) break;
+    if (threadIdx.x < 32) {
+      tc_fence_after();
+      issue_tile<S::kK>(tl.d(t), a_at, b_at);
+      mma_commit(tl.bar[t & 1]);
+    }
+    tc_fence_after();
+    if (t + 1 < tiles) load(t + 1);
+    if (t > 0) reduce(t - 1);
+  }
+  if (t > 0 && t == tiles) {
+    ok = tl.wait(t - 1);
+    tc_fence_after();
+    if (ok) reduce(t - 1);
+  }
+  // what no query sees
+  for (int n = some ? max(live - tok0, 0) : 0; n < toks; ++n)
+    if (page < p.table_width) out[static_cast<int64_t>(n) * p.table_width] = -INFINITY;
+  tl.end();
+}
+
+// ------------------------------------------------------------------ weights
+
+template <int D>
+struct WeightSmem {
+  static constexpr int kA = 128 * D * 2, kB = kTileRows * D * 2;
+  static constexpr int kBytes = kA + 2 * kB + 1024;
+};
+
+// The numbers of a tile's rows: -lse * log2(e) in two parts, slots that the row sees.
+struct alignas(16) RowNumbers {  // (read 16 bytes at a time)
+  float hi[kTileRows], lo[kTileRows];
+  int sees[kTileRows];
+  int least[2];  // of the first and second half of sees
+};
+
+template <int D>
+__global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_constant__ LongParams p) {
+  using S = WeightSmem<D>;
+  constexpr int kPieces = D / 8;
+  extern __shared__ uint8_t raw[];
+  __shared__ uint64_t bars[2];
+  __shared__ uint32_t slot;
+  __shared__ __align__(16) RowNumbers numbers[3];
+  uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
+  const uint32_t a_at = smem_u32(smem), b_at = a_at + S::kA;
+  Tiles2 tl;
+  tl.begin(bars, &slot);
+  ldev::grid_dep_launch();
+  ldev::grid_dep_wait();
+
+  const int b = blockIdx.z, hk = blockIdx.y;
+  const LongLens lens = long_lens(p, b);
+  const int key0 = static_cast<int>(blockIdx.x) * 128, key = key0 + static_cast<int>(threadIdx.x);
+  const int page_mask = (1 << p.page_shift) - 1;
+  const int rows = key0 < lens.len ? lens.ql * p.G : 0, tiles = (rows + kTileRows - 1) / kTileRows;
+  const float* lse = p.lse + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * p.Nq;
+
+  const auto fetch = [&](int t) {
+    const int base = t * kTileRows;
+#pragma unroll
+    for (int x0 = 0; x0 < kTileRows * kPieces; x0 += kTileThreads) {
+      const int x = x0 + static_cast<int>(threadIdx.x), r = x / kPieces, c = x % kPieces;
+      const int n = (base + r) / p.G, g = base + r - n * p.G;
+      if (base + r < rows)
+        ldev::copy16(b_at + (t & 1) * S::kB + operand_at<D>(r, c, kTileRows),
+                     static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb + (static_cast<int64_t>(hk) * p.G + g) * p.q_sh +
+                         n * p.q_sn + c * 8,
+                     16);
+    }
+    ldev::copy_commit();
+    if (threadIdx.x < kTileRows) {
+      RowNumbers& to = numbers[t % 3];
+      const int r = threadIdx.x;
+      float hi = 0.f, lo = 0.f;
+      int most = 0;
+      if (base + r < rows) {
+        const int n = (base + r) / p.G, g = base + r - n * p.G;
+        const float x = lse[static_cast<int64_t>(g) * p.Nq + n];
+        hi = -x * 1.4426950408889634f;
+        lo = fabsf(x) == INFINITY ? 0.f : fmaf(-x, 1.4426950408889634f, -hi) - x * 1.925963033e-8f;
+        most = x == -INFINITY ? 0 : long_seen(p, lens, n);
+      }
+      to.hi[r] = hi;
+      to.lo[r] = lo;
+      to.sees[r] = most;
+      const int least = __reduce_min_sync(0xffffffffu, most);
+      if ((r & 31) == 0) to.least[r >> 5] = least;
+    }
+  };
+  ldev::F2 sum = ldev::pair(0.f, 0.f);
+  const ldev::F2 c_hi = ldev::pair(p.c_hi, p.c_hi), c_lo = ldev::pair(p.c_lo, p.c_lo);
+  const auto reduce = [&](int t) {
+    const RowNumbers& now = numbers[t % 3];
+    const bool whole = key0 + 128 <= min(now.least[0], now.least[1]);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      uint32_t v[32];
+      tmem_ld32(tl.d(t) + ((threadIdx.x >> 5) << 21) + half * 32, v);
+#pragma unroll
+      for (int c = 0; c < 32; c += 4) {
+        const float4 hi = *reinterpret_cast<const float4*>(now.hi + half * 32 + c);
+        const float4 lo = *reinterpret_cast<const float4*>(now.lo + half * 32 + c);
+        const ldev::F2 y0 = ldev::pair(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+        const ldev::F2 y1 = ldev::pair(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
+        const float2 a0 = ldev::split(ldev::add2(ldev::fma2(y0, c_hi, ldev::pair(hi.x, hi.y)), ldev::fma2(y0, c_lo, ldev::pair(lo.x, lo.y))));
+        const float2 a1 = ldev::split(ldev::add2(ldev::fma2(y1, c_hi, ldev::pair(hi.z, hi.w)), ldev::fma2(y1, c_lo, ldev::pair(lo.z, lo.w))));
+        float w[4] = {ex2(a0.x), ex2(a0.y), ex2(a1.x), ex2(a1.y)};
+        if (!whole) {
+          const int4 most = *reinterpret_cast<const int4*>(now.sees + half * 32 + c);
+          if (key >= most.x) w[0] = 0.f;
+          if (key >= most.y) w[1] = 0.f;
+          if (key >= most.z) w[2] = 0.f;
+          if (key >= most.w) w[3] = 0.f;
+        }
+        sum = ldev::add2(sum, ldev::add2(ldev::pair(w[0], w[1]), ldev::pair(w[2], w[3])));
+      }
+    }
+  };
+
+  if (tiles > 0) {
+    for (int x = threadIdx.x; x < 128 * kPieces; x += kTileThreads) {
+      const int r = x / kPieces, c = x % kPieces, at = key0 + r;
+      const int id = at < lens.len ? p.table[b * p.table_sb + (at >> p.page_shift)] : -1;
+      const bool real = id >= 0 && id < p.n_pages;
+      ldev::copy16(a_at + operand_at<D>(r, c, 128),
+                   static_cast<const __nv_bfloat16*>(p.kc) + (real ? id * p.kc_sp : 0) + hk * p.kc_sh +
+                       (at & page_mask) * p.kc_st + c * 8,
+                   real ? 16 : 0);
+    }
+    fetch(0);
+  }
+  bool ok = true;
+  int t = 0;
+  for (; t < tiles; ++t) {
+    ldev::copy_wait();
+    fence_async_smem();
+    tc_fence_before();
+    if (__syncthreads_or(!ok)) break;
+    if (threadIdx.x < 32) {
+      tc_fence_after();
+      issue_tile<D>(tl.d(t), a_at, b_at + (t & 1) * S::kB);
+      mma_commit(tl.bar[t & 1]);
+    }
+    if (t > 0) ok = tl.wait(t - 1);
+    tc_fence_after();
+    if (t + 1 < tiles) fetch(t + 1);
+    if (t > 0 && ok) reduce(t - 1);
+  }
+  if (t > 0 && t == tiles) {
+    ok = tl.wait(t - 1) && ok;
+    tc_fence_after();
+    if (ok) reduce(t - 1);
+  }
+  if (key < lens.len && ok) {
+    const int id = p.table[b * p.table_sb + (key >> p.page_shift)];
+    if (id >= 0 && id < p.n_pages) {
+      const int64_t at = ((static_cast<int64_t>(id) * p.Hk + hk) << p.page_shift) + (key & page_mask);
+      const float2 z = ldev::split(sum);
+      const bool old = p.decay != 0.f && !(p.causal && key >= lens.len - lens.ql);
+      p.weights_out[at] = old ? fmaf(p.decay, p.weights[at], z.x + z.y) : z.x + z.y;
+    }
+  }
+  tl.end();
+}
+
+// ------------------------------------------------------------------ launches
+
+template <typename... Args, typename... Given>
+cudaError_t launch_tiles(void (*kern)(Args...), dim3 grid, int bytes, cudaStream_t s, const Given&... args) {
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
+  return ldev::launch(kern, grid, kTileThreads, static_cast<size_t>(bytes), s, 1, args...);
+}
+
+// Tokens of a CTA: rows that are worth loading the pages' bounds for, few enough to give
+// every SM work.
+constexpr int kScoreMost = 2048, kScoreLeast = 256, kScoreCtas = 4 * 152;
+
+template <int D>
+cudaError_t scores_tiles_dim(const LongParams& p, cudaStream_t s) {
+  const int64_t cols = (p.table_width + 127) / 128;
+  int64_t rows = cols * p.B * p.Hk * p.Nq * p.G / kScoreCtas;
+  rows = rows < kScoreLeast ? kScoreLeast : (rows > kScoreMost ? kScoreMost : rows);
+  int64_t tokens = (rows + p.G - 1) / p.G;
+  if (tokens > p.Nq) tokens = p.Nq;
+  const dim3 grid(static_cast<unsigned>(cols * ((p.Nq + tokens - 1) / tokens)), p.Hk, p.B);
+  const int n = static_cast<int>(tokens), bytes = ScoreSmem<D>::kBytes;
+  switch (p.G) {
+    case 1: return launch_tiles(scores_tiles<D, 1>, grid, bytes, s, p, n);
+    case 2: return launch_tiles(scores_tiles<D, 2>, grid, bytes, s, p, n);
+    case 4: return launch_tiles(scores_tiles<D, 4>, grid, bytes, s, p, n);
+    case 8: return launch_tiles(scores_tiles<D, 8>, grid, bytes, s, p, n);
+    default: return launch_tiles(scores_tiles<D, 0>, grid, bytes, s, p, n);
+  }
+}
+
+template <int D>
+cudaError_t weights_tiles_dim(const LongParams& p, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((p.max_len + 127) / 128), p.Hk, p.B);
+  return launch_tiles(weights_tiles<D>, grid, WeightSmem<D>::kBytes, s, p);
+}
+
+}  // namespace dev
+
+cudaError_t launch_scores_tiles(const LongParams& p, int d, cudaStream_t s) {
+  switch (d) {
+    case 32: return dev::scores_tiles_dim<32>(p, s);
+    case 64: return dev::scores_tiles_dim<64>(p, s);
+    case 128: return dev::scores_tiles_dim<128>(p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t launch_weights_tiles(const LongParams& p, int d, cudaStream_t s) {
+  switch (d) {
+    case 32: return dev::weights_tiles_dim<32>(p, s);
+    case 64: return dev::weights_tiles_dim<64>(p, s);
+    case 128: return dev::weights_tiles_dim<128>(p, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+cudaError_t long_take_status(uint32_t word[4]) {
+  cudaError_t e = cudaMemcpyFromSymbol(word, dev::g_long_status, 4 * sizeof(uint32_t), 0, cudaMemcpyDeviceToHost);
+  if (e != cudaSuccess || word[0] == 0) return e;
+  const uint32_t zero[4] = {0, 0, 0, 0};
+  return cudaMemcpyToSymbol(dev::g_long_status, zero, sizeof(zero), 0, cudaMemcpyHostToDevice);
+}
+
+}  // namespace attn
