@@ -39,7 +39,7 @@ int check_sizes(const attn_long_params* p, bool queries, bool heads) {
 int fill(const attn_long_params* p, LongParams* r, bool queries, bool heads, bool table) {
   int rc = check_sizes(p, queries, heads);
   if (rc != ATTN_OK) return rc;
-  std::memset(r, 0, sizeof(*r));
+  std::memset(static_cast<void*>(r), 0, sizeof(*r));
   if ((rc = log2_page(p->page_size, &r->page_shift)) != ATTN_OK) return rc;
   if (table && p->n_pages < 1) return fail_with(ATTN_ERR_INVALID_ARG, "n_pages must be >= 1");
   if (p->kv_lens == nullptr || (table && p->block_table == nullptr))
@@ -75,6 +75,7 @@ int fill(const attn_long_params* p, LongParams* r, bool queries, bool heads, boo
   r->Hk = p->Hk;
   r->Nq = p->Nq;
   r->G = heads && queries ? p->Hq / p->Hk : 1;
+  r->by_g = attn::FastDiv(static_cast<uint32_t>(r->G));
   r->n_pages = p->n_pages;
   r->max_len = static_cast<int>(max_len);
   r->n = p->n;
@@ -239,7 +240,8 @@ int attn_kv_weights(const attn_long_params* p) {
   r.c_hi = static_cast<float>(c);
   if (static_cast<double>(r.c_hi) >= c) r.c_hi = std::nextafter(r.c_hi, 0.f);
   r.c_lo = static_cast<float>(c - static_cast<double>(r.c_hi));
-  if (!std::isfinite(r.c_hi) || !(r.c_lo > 0.f)) return fail_with(ATTN_ERR_INVALID_ARG, "scale is out of range");
+  if (!(p->scale >= 0x1p-64f && p->scale <= 0x1p64f) || !(r.c_lo > 0.f))
+    return fail_with(ATTN_ERR_INVALID_ARG, "scale must be 2^-64 to 2^64");
   if ((rc = this_gpu()) != ATTN_OK) return rc;
   return done(attn::launch_weights(r, p->d, stream_of(p->stream)), "received weights launch");
 }

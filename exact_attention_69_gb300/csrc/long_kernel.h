@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "paged_kernel.h"
+
 namespace attn {
 
 struct LongParams {
@@ -34,6 +36,7 @@ struct LongParams {
   int32_t* kept;                // [B, Hk, n]
   int32_t* new_lens;            // [B]
   int B, Hq, Hk, Nq, G;
+  FastDiv by_g;
   int n_pages, page_shift;
   int max_len;                  // table_width * page size
   int n, first, last;           // selected pages or kept slots, those always taken at either end

@@ -74,6 +74,12 @@ __device__ __forceinline__ void issue_tile(uint32_t d_tmem, uint32_t a, uint32_t
   }
 }
 
+// D += the product of 16 further channels in operands of 64-byte rows.
+__device__ __forceinline__ void issue_more(uint32_t d_tmem, uint32_t a, uint32_t b) {
+  constexpr uint32_t kIdesc = make_idesc(128, kTileRows, false);
+  mma_ss(d_tmem, smem_desc(a, 16, 8 * 64, 4u), smem_desc(b, 16, 8 * 64, 4u), kIdesc, 1u);
+}
+
 // What both kernels set up: barriers and TMEM.
 struct Tiles2 {
   uint32_t bar[2];
@@ -144,15 +150,16 @@ __global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_consta
 
   // query rows of a tile: pieces of 16 bytes, D / 8 threads a row
   uint4 q[kLoads];
+  const int piece = static_cast<int>(threadIdx.x) % kPieces, row = static_cast<int>(threadIdx.x) / kPieces;
+  constexpr int kStep = kTileThreads / kPieces;
+  const __nv_bfloat16* qbase = static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb +
+                               static_cast<int64_t>(hk) * heads * p.q_sh + tok0 * p.q_sn + piece * 8;
   const auto load = [&](int t) {
 #pragma unroll
     for (int e = 0; e < kLoads; ++e) {
-      const int x = e * kTileThreads + static_cast<int>(threadIdx.x), r = t * kTileRows + x / kPieces, c = x % kPieces;
-      const int n = r / heads, g = r - n * heads;
-      q[e] = make_uint4(0, 0, 0, 0);
-      if (r < rows)
-        q[e] = ldev::ld16(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb +
-                          (static_cast<int64_t>(hk) * heads + g) * p.q_sh + (tok0 + n) * p.q_sn + c * 8);
+      const int r = t * kTileRows + e * kStep + row;
+      const int n = G > 0 ? r / heads : p.by_g.div(r), g = r - n * heads;
+      q[e] = r < rows ? ldev::ld16(qbase + g * p.q_sh + n * p.q_sn) : make_uint4(0, 0, 0, 0);
     }
   };
   if (tiles > 0) {
@@ -170,6 +177,8 @@ __global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_consta
 
   float best = -INFINITY;
   int tok = 0, g = 0;  // the token and head that the next column is
+  float* at = out;
+  const bool in = page < p.table_width;
   const auto reduce = [&](int t) {
     uint32_t v[2][32];
     tmem_ld32(tl.d(t) + ((threadIdx.x >> 5) << 21), v[0]);
@@ -184,13 +193,14 @@ __global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_consta
         last = ++g == heads;
       }
       if (last) {
-        if (tok < live - tok0 && page < p.table_width) {
+        if (in && tok < live - tok0) {
           const bool sees = page < long_pages(p, long_seen(p, lens, tok0 + tok));
-          out[static_cast<int64_t>(tok) * p.table_width] = sees ? best * p.scale : -INFINITY;
+          *at = sees ? best * p.scale : -INFINITY;
         }
         best = -INFINITY;
         g = 0;
         ++tok;
+        at += p.table_width;
       }
     }
   };
@@ -201,7 +211,7 @@ __global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_consta
     if (t > 0) ok = tl.wait(t - 1);  // its operand may be replaced
 #pragma unroll
     for (int e = 0; e < kLoads; ++e) {
-      const int x = e * kTileThreads + static_cast<int>(threadIdx.x), r = x / kPieces, c = x % kPieces;
+      const int r = e * kStep + row;
       const __nv_bfloat162 zero(__ushort_as_bfloat16(0), __ushort_as_bfloat16(0));
       uint4 neg, pos;
 #pragma unroll
@@ -210,10 +220,10 @@ __global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_consta
         reinterpret_cast<__nv_bfloat162*>(&neg)[i] = __hmin2_nan(y, zero);
         reinterpret_cast<__nv_bfloat162*>(&pos)[i] = __hmax2_nan(y, zero);
       }
-      *reinterpret_cast<uint4*>(smem + S::kA + operand_at<S::kK>(r, c, kTileRows)) = neg;
-      *reinterpret_cast<uint4*>(smem + S::kA + operand_at<S::kK>(r, c + kPieces, kTileRows)) = pos;
+      *reinterpret_cast<uint4*>(smem + S::kA + operand_at<S::kK>(r, piece, kTileRows)) = neg;
+      *reinterpret_cast<uint4*>(smem + S::kA + operand_at<S::kK>(r, piece + kPieces, kTileRows)) = pos;
     }
-    if (t == 0) ldev::copy_wait();
+    if (t == 0) ldev::copy_wait<0>();
     fence_async_smem();
     tc_fence_before();
     if (__syncthreads_or(!ok)) break;
@@ -239,29 +249,35 @@ __global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_consta
 
 // ------------------------------------------------------------------ weights
 
+// The rows' lse takes part in the product: keys get four further channels of one, query
+// row r those of -lse[r] / scale in four parts (three of 8 bits each that hold its fp32
+// value, and what that leaves), so a tile's accumulator is q . k - lse / scale, formed in
+// fp32 like the sum itself, and a weight is one product and one exp2 of it. The extra 16
+// channels lie in operands of 32 (64-byte rows), half of which nothing reads.
 template <int D>
 struct WeightSmem {
-  static constexpr int kA = 128 * D * 2, kB = kTileRows * D * 2;
-  static constexpr int kBytes = kA + 2 * kB + 1024;
+  static constexpr int kA = 128 * D * 2, kB = kTileRows * D * 2, kStages = 3;
+  static constexpr int kAX = 128 * 64, kBX = kTileRows * 64;
+  static constexpr int kOffB = kA, kOffAX = kOffB + kStages * kB, kOffBX = kOffAX + kAX;
+  static constexpr int kBytes = kOffBX + kStages * kBX + 1024;
 };
 
-// The numbers of a tile's rows: -lse * log2(e) in two parts, slots that the row sees.
+// Slots that a tile's rows see.
 struct alignas(16) RowNumbers {  // (read 16 bytes at a time)
-  float hi[kTileRows], lo[kTileRows];
   int sees[kTileRows];
-  int least[2];  // of the first and second half of sees
+  int least[4];  // of the first and second half
 };
 
 template <int D>
 __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_constant__ LongParams p) {
   using S = WeightSmem<D>;
-  constexpr int kPieces = D / 8;
+  constexpr int kPieces = D / 8, kStep = kTileThreads / kPieces;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2];
   __shared__ uint32_t slot;
-  __shared__ __align__(16) RowNumbers numbers[3];
+  __shared__ RowNumbers numbers[4];
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
-  const uint32_t a_at = smem_u32(smem), b_at = a_at + S::kA;
+  const uint32_t base = smem_u32(smem);
   Tiles2 tl;
   tl.begin(bars, &slot);
   ldev::grid_dep_launch();
@@ -273,59 +289,60 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
   const int page_mask = (1 << p.page_shift) - 1;
   const int rows = key0 < lens.len ? lens.ql * p.G : 0, tiles = (rows + kTileRows - 1) / kTileRows;
   const float* lse = p.lse + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * p.Nq;
+  const int piece = static_cast<int>(threadIdx.x) % kPieces, row = static_cast<int>(threadIdx.x) / kPieces;
+  const __nv_bfloat16* qbase =
+      static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb + static_cast<int64_t>(hk) * p.G * p.q_sh + piece * 8;
 
+  // a tile's query rows, two tiles before they are used
   const auto fetch = [&](int t) {
-    const int base = t * kTileRows;
 #pragma unroll
-    for (int x0 = 0; x0 < kTileRows * kPieces; x0 += kTileThreads) {
-      const int x = x0 + static_cast<int>(threadIdx.x), r = x / kPieces, c = x % kPieces;
-      const int n = (base + r) / p.G, g = base + r - n * p.G;
-      if (base + r < rows)
-        ldev::copy16(b_at + (t & 1) * S::kB + operand_at<D>(r, c, kTileRows),
-                     static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb + (static_cast<int64_t>(hk) * p.G + g) * p.q_sh +
-                         n * p.q_sn + c * 8,
-                     16);
+    for (int r0 = 0; r0 < kTileRows; r0 += kStep) {
+      const int r = t * kTileRows + r0 + row, n = p.by_g.div(r), g = r - n * p.G;
+      if (r < rows)
+        ldev::copy16(base + S::kOffB + (t % S::kStages) * S::kB + operand_at<D>(r0 + row, piece, kTileRows),
+                     qbase + g * p.q_sh + n * p.q_sn, 16);
     }
     ldev::copy_commit();
-    if (threadIdx.x < kTileRows) {
-      RowNumbers& to = numbers[t % 3];
-      const int r = threadIdx.x;
-      float hi = 0.f, lo = 0.f;
-      int most = 0;
-      if (base + r < rows) {
-        const int n = (base + r) / p.G, g = base + r - n * p.G;
-        const float x = lse[static_cast<int64_t>(g) * p.Nq + n];
-        hi = -x * 1.4426950408889634f;
-        lo = fabsf(x) == INFINITY ? 0.f : fmaf(-x, 1.4426950408889634f, -hi) - x * 1.925963033e-8f;
-        most = x == -INFINITY ? 0 : long_seen(p, lens, n);
-      }
-      to.hi[r] = hi;
-      to.lo[r] = lo;
-      to.sees[r] = most;
-      const int least = __reduce_min_sync(0xffffffffu, most);
-      if ((r & 31) == 0) to.least[r >> 5] = least;
+  };
+  // the lse of a tile's rows: read one tile earlier still, put in place with the rows
+  const auto read = [&](int t) {
+    const int r = t * kTileRows + static_cast<int>(threadIdx.x), n = p.by_g.div(r), g = r - n * p.G;
+    return threadIdx.x < kTileRows && r < rows ? lse[static_cast<int64_t>(g) * p.Nq + n] : -INFINITY;
+  };
+  const auto place = [&](int t, float z) {
+    if (threadIdx.x >= kTileRows) return;
+    const int r = t * kTileRows + static_cast<int>(threadIdx.x);
+    const bool none = fabsf(z) == INFINITY;  // -inf: the row saw nothing; +inf: weights of zero
+    const float x = none ? 0.f : -z * p.c_hi;  // (c_hi + c_lo: 1 / scale)
+    float x1 = 0.f, x2 = 0.f, left = 0.f;
+    if (fabsf(x) < 1e38f) {  // (else, or NaN, the first part says it all)
+      x1 = x - __bfloat162float(__float2bfloat16_rn(x));
+      x2 = x1 - __bfloat162float(__float2bfloat16_rn(x1));
+      left = fmaf(-z, p.c_hi, -x) - z * p.c_lo;
     }
+    const uint2 v = make_uint2(ldev::pack_bf16(x, x1), ldev::pack_bf16(x2, left));
+    *reinterpret_cast<uint2*>(smem + S::kOffBX + (t % S::kStages) * S::kBX + operand_at<32>(threadIdx.x, 0, kTileRows)) = v;
+    const int sees = none ? 0 : long_seen(p, lens, p.by_g.div(r));
+    numbers[t % 4].sees[threadIdx.x] = r < rows ? sees : 0;
+    const int least = __reduce_min_sync(0xffffffffu, r < rows ? sees : 0);
+    if ((threadIdx.x & 31) == 0) numbers[t % 4].least[threadIdx.x >> 5] = least;
   };
   ldev::F2 sum = ldev::pair(0.f, 0.f);
-  const ldev::F2 c_hi = ldev::pair(p.c_hi, p.c_hi), c_lo = ldev::pair(p.c_lo, p.c_lo);
+  const ldev::F2 c = ldev::pair(p.scale, p.scale);  // (scale * log2(e))
   const auto reduce = [&](int t) {
-    const RowNumbers& now = numbers[t % 3];
+    const RowNumbers& now = numbers[t % 4];
     const bool whole = key0 + 128 <= min(now.least[0], now.least[1]);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       uint32_t v[32];
       tmem_ld32(tl.d(t) + ((threadIdx.x >> 5) << 21) + half * 32, v);
 #pragma unroll
-      for (int c = 0; c < 32; c += 4) {
-        const float4 hi = *reinterpret_cast<const float4*>(now.hi + half * 32 + c);
-        const float4 lo = *reinterpret_cast<const float4*>(now.lo + half * 32 + c);
-        const ldev::F2 y0 = ldev::pair(__uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-        const ldev::F2 y1 = ldev::pair(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3]));
-        const float2 a0 = ldev::split(ldev::add2(ldev::fma2(y0, c_hi, ldev::pair(hi.x, hi.y)), ldev::fma2(y0, c_lo, ldev::pair(lo.x, lo.y))));
-        const float2 a1 = ldev::split(ldev::add2(ldev::fma2(y1, c_hi, ldev::pair(hi.z, hi.w)), ldev::fma2(y1, c_lo, ldev::pair(lo.z, lo.w))));
+      for (int x = 0; x < 32; x += 4) {
+        const float2 a0 = ldev::split(ldev::mul2(ldev::pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), c));
+        const float2 a1 = ldev::split(ldev::mul2(ldev::pair(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), c));
         float w[4] = {ex2(a0.x), ex2(a0.y), ex2(a1.x), ex2(a1.y)};
         if (!whole) {
-          const int4 most = *reinterpret_cast<const int4*>(now.sees + half * 32 + c);
+          const int4 most = *reinterpret_cast<const int4*>(now.sees + half * 32 + x);
           if (key >= most.x) w[0] = 0.f;
           if (key >= most.y) w[1] = 0.f;
           if (key >= most.z) w[2] = 0.f;
@@ -336,35 +353,57 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
     }
   };
 
+  float z = 0.f;
   if (tiles > 0) {
+    z = read(0);
+    const float z1 = read(1);
     for (int x = threadIdx.x; x < 128 * kPieces; x += kTileThreads) {
-      const int r = x / kPieces, c = x % kPieces, at = key0 + r;
+      const int r = x / kPieces, at = key0 + r;
       const int id = at < lens.len ? p.table[b * p.table_sb + (at >> p.page_shift)] : -1;
       const bool real = id >= 0 && id < p.n_pages;
-      ldev::copy16(a_at + operand_at<D>(r, c, 128),
+      ldev::copy16(base + operand_at<D>(r, piece, 128),
                    static_cast<const __nv_bfloat16*>(p.kc) + (real ? id * p.kc_sp : 0) + hk * p.kc_sh +
-                       (at & page_mask) * p.kc_st + c * 8,
+                       (at & page_mask) * p.kc_st + piece * 8,
                    real ? 16 : 0);
     }
     fetch(0);
+    fetch(1);
+    // the further channels: ones for the keys, zeros behind the four of the rows
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(smem + S::kOffAX + operand_at<32>(threadIdx.x, 0, 128)) = make_uint4(0x3F803F80u, 0x3F803F80u, 0, 0);
+    *reinterpret_cast<uint4*>(smem + S::kOffAX + operand_at<32>(threadIdx.x, 1, 128)) = zero;
+    for (int x = threadIdx.x; x < S::kStages * kTileRows; x += kTileThreads) {
+      *reinterpret_cast<uint4*>(smem + S::kOffBX + (x / kTileRows) * S::kBX + operand_at<32>(x % kTileRows, 0, kTileRows)) = zero;
+      *reinterpret_cast<uint4*>(smem + S::kOffBX + (x / kTileRows) * S::kBX + operand_at<32>(x % kTileRows, 1, kTileRows)) = zero;
+    }
+    __syncthreads();
+    place(0, z);
+    place(1, z1);
+    z = read(2);
   }
   bool ok = true;
   int t = 0;
   for (; t < tiles; ++t) {
-    ldev::copy_wait();
+    ldev::copy_wait<1>();  // tile t's; t + 1's may still come
     fence_async_smem();
     tc_fence_before();
     if (__syncthreads_or(!ok)) break;
     if (threadIdx.x < 32) {
       tc_fence_after();
-      issue_tile<D>(tl.d(t), a_at, b_at + (t & 1) * S::kB);
+      issue_tile<D>(tl.d(t), base, base + S::kOffB + (t % S::kStages) * S::kB);
+      issue_more(tl.d(t), base + S::kOffAX, base + S::kOffBX + (t % S::kStages) * S::kBX);
       mma_commit(tl.bar[t & 1]);
     }
-    if (t > 0) ok = tl.wait(t - 1);
+    if (t > 0) ok = tl.wait(t - 1);  // its operands may be replaced
     tc_fence_after();
-    if (t + 1 < tiles) fetch(t + 1);
+    fetch(t + 2);  // (nothing behind the last one: an empty group)
+    if (t + 2 < tiles) {
+      place(t + 2, z);
+      z = read(t + 3);
+    }
     if (t > 0 && ok) reduce(t - 1);
   }
+  ldev::copy_wait<0>();
   if (t > 0 && t == tiles) {
     ok = tl.wait(t - 1) && ok;
     tc_fence_after();
@@ -374,9 +413,9 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
     const int id = p.table[b * p.table_sb + (key >> p.page_shift)];
     if (id >= 0 && id < p.n_pages) {
       const int64_t at = ((static_cast<int64_t>(id) * p.Hk + hk) << p.page_shift) + (key & page_mask);
-      const float2 z = ldev::split(sum);
+      const float2 w = ldev::split(sum);
       const bool old = p.decay != 0.f && !(p.causal && key >= lens.len - lens.ql);
-      p.weights_out[at] = old ? fmaf(p.decay, p.weights[at], z.x + z.y) : z.x + z.y;
+      p.weights_out[at] = old ? fmaf(p.decay, p.weights[at], w.x + w.y) : w.x + w.y;
     }
   }
   tl.end();
@@ -418,7 +457,12 @@ cudaError_t scores_tiles_dim(const LongParams& p, cudaStream_t s) {
 template <int D>
 cudaError_t weights_tiles_dim(const LongParams& p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>((p.max_len + 127) / 128), p.Hk, p.B);
-  return launch_tiles(weights_tiles<D>, grid, WeightSmem<D>::kBytes, s, p);
+  LongParams r = p;
+  const double scale = p.scale, inv = 1.0 / scale;
+  r.c_hi = static_cast<float>(inv);
+  r.c_lo = static_cast<float>(inv - static_cast<double>(r.c_hi));
+  r.scale = static_cast<float>(scale * 1.4426950408889634074);
+  return launch_tiles(weights_tiles<D>, grid, WeightSmem<D>::kBytes, s, r);
 }
 
 }  // namespace dev
