@@ -80,6 +80,31 @@ __device__ __forceinline__ void issue_more(uint32_t d_tmem, uint32_t a, uint32_t
   mma_ss(d_tmem, smem_desc(a, 16, 8 * 64, 4u), smem_desc(b, 16, 8 * 64, 4u), kIdesc, 1u);
 }
 
+// Where a thread's piece of a query row is, row by row of a stride: r = n * heads + g
+// without a division each.
+struct RowWalk {
+  const __nv_bfloat16* at;
+  int64_t step, wrap;  // elements that a stride adds; what it adds more if g passes the heads
+  int g, dg, heads;
+  __device__ __forceinline__ RowWalk(const __nv_bfloat16* base, int r, int stride, int heads_, FastDiv by_g, int64_t sh, int64_t sn)
+      : heads(heads_) {
+    const int n = by_g.div(r), dn = by_g.div(stride);
+    g = r - n * heads;
+    dg = stride - dn * heads;
+    at = base + n * sn + g * sh;
+    step = dn * sn + dg * sh;
+    wrap = sn - heads * sh;
+  }
+  __device__ __forceinline__ void next() {
+    at += step;
+    g += dg;
+    if (g >= heads) {
+      g -= heads;
+      at += wrap;
+    }
+  }
+};
+
 // What both kernels set up: barriers and TMEM.
 struct Tiles2 {
   uint32_t bar[2];
@@ -152,18 +177,20 @@ __global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_consta
   uint4 q[kLoads];
   const int piece = static_cast<int>(threadIdx.x) % kPieces, row = static_cast<int>(threadIdx.x) / kPieces;
   constexpr int kStep = kTileThreads / kPieces;
-  const __nv_bfloat16* qbase = static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb +
-                               static_cast<int64_t>(hk) * heads * p.q_sh + tok0 * p.q_sn + piece * 8;
-  const auto load = [&](int t) {
+  RowWalk walk(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb + static_cast<int64_t>(hk) * heads * p.q_sh +
+                   tok0 * p.q_sn + piece * 8,
+               row, kStep, heads, p.by_g, p.q_sh, p.q_sn);
+  int next = row;  // the row that the walk is at
+  const auto load = [&]() {
 #pragma unroll
     for (int e = 0; e < kLoads; ++e) {
-      const int r = t * kTileRows + e * kStep + row;
-      const int n = G > 0 ? r / heads : p.by_g.div(r), g = r - n * heads;
-      q[e] = r < rows ? ldev::ld16(qbase + g * p.q_sh + n * p.q_sn) : make_uint4(0, 0, 0, 0);
+      q[e] = next < rows ? ldev::ld16(walk.at) : make_uint4(0, 0, 0, 0);
+      walk.next();
+      next += kStep;
     }
   };
   if (tiles > 0) {
-    load(0);
+    load();
     for (int x = threadIdx.x; x < 128 * 2 * kPieces; x += kTileThreads) {
       const int r = x / (2 * kPieces), c = x % (2 * kPieces);
       const int id = page0 + r < pages ? p.table[b * p.table_sb + page0 + r] : -1;
@@ -233,7 +260,7 @@ __global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_consta
       mma_commit(tl.bar[t & 1]);
     }
     tc_fence_after();
-    if (t + 1 < tiles) load(t + 1);
+    if (t + 1 < tiles) load();
     if (t > 0) reduce(t - 1);
   }
   if (t > 0 && t == tiles) {
@@ -290,17 +317,20 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
   const int rows = key0 < lens.len ? lens.ql * p.G : 0, tiles = (rows + kTileRows - 1) / kTileRows;
   const float* lse = p.lse + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * p.Nq;
   const int piece = static_cast<int>(threadIdx.x) % kPieces, row = static_cast<int>(threadIdx.x) / kPieces;
-  const __nv_bfloat16* qbase =
-      static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb + static_cast<int64_t>(hk) * p.G * p.q_sh + piece * 8;
+  RowWalk walk(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb + static_cast<int64_t>(hk) * p.G * p.q_sh + piece * 8,
+               row, kStep, p.G, p.by_g, p.q_sh, p.q_sn);
+  int next = row;  // the row that the walk is at
+  const uint32_t to = operand_at<D>(row, piece, kTileRows);
 
   // a tile's query rows, two tiles before they are used
-  const auto fetch = [&](int t) {
+  const auto fetch = [&](int stage) {
+    static_assert(kStep % 8 == 0, "the swizzle of a thread's rows is the same");
+    const uint32_t dst = base + S::kOffB + stage * S::kB + to;
 #pragma unroll
     for (int r0 = 0; r0 < kTileRows; r0 += kStep) {
-      const int r = t * kTileRows + r0 + row, n = p.by_g.div(r), g = r - n * p.G;
-      if (r < rows)
-        ldev::copy16(base + S::kOffB + (t % S::kStages) * S::kB + operand_at<D>(r0 + row, piece, kTileRows),
-                     qbase + g * p.q_sh + n * p.q_sn, 16);
+      if (next < rows) ldev::copy16(dst + r0 * (D >= 64 ? 128 : 64), walk.at, 16);
+      walk.next();
+      next += kStep;
     }
     ldev::copy_commit();
   };
@@ -309,7 +339,7 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
     const int r = t * kTileRows + static_cast<int>(threadIdx.x), n = p.by_g.div(r), g = r - n * p.G;
     return threadIdx.x < kTileRows && r < rows ? lse[static_cast<int64_t>(g) * p.Nq + n] : -INFINITY;
   };
-  const auto place = [&](int t, float z) {
+  const auto place = [&](int t, int stage, float z) {
     if (threadIdx.x >= kTileRows) return;
     const int r = t * kTileRows + static_cast<int>(threadIdx.x);
     const bool none = fabsf(z) == INFINITY;  // -inf: the row saw nothing; +inf: weights of zero
@@ -321,7 +351,7 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
       left = fmaf(-z, p.c_hi, -x) - z * p.c_lo;
     }
     const uint2 v = make_uint2(ldev::pack_bf16(x, x1), ldev::pack_bf16(x2, left));
-    *reinterpret_cast<uint2*>(smem + S::kOffBX + (t % S::kStages) * S::kBX + operand_at<32>(threadIdx.x, 0, kTileRows)) = v;
+    *reinterpret_cast<uint2*>(smem + S::kOffBX + stage * S::kBX + operand_at<32>(threadIdx.x, 0, kTileRows)) = v;
     const int sees = none ? 0 : long_seen(p, lens, p.by_g.div(r));
     numbers[t % 4].sees[threadIdx.x] = r < rows ? sees : 0;
     const int least = __reduce_min_sync(0xffffffffu, r < rows ? sees : 0);
@@ -367,7 +397,7 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
                    real ? 16 : 0);
     }
     fetch(0);
-    fetch(1);
+    fetch(1);  // (nothing behind the last row: an empty group)
     // the further channels: ones for the keys, zeros behind the four of the rows
     const uint4 zero = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4*>(smem + S::kOffAX + operand_at<32>(threadIdx.x, 0, 128)) = make_uint4(0x3F803F80u, 0x3F803F80u, 0, 0);
@@ -377,12 +407,12 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
       *reinterpret_cast<uint4*>(smem + S::kOffBX + (x / kTileRows) * S::kBX + operand_at<32>(x % kTileRows, 1, kTileRows)) = zero;
     }
     __syncthreads();
-    place(0, z);
-    place(1, z1);
+    place(0, 0, z);
+    place(1, 1, z1);
     z = read(2);
   }
   bool ok = true;
-  int t = 0;
+  int t = 0, stage = 0;  // (stage: t modulo kStages)
   for (; t < tiles; ++t) {
     ldev::copy_wait<1>();  // tile t's; t + 1's may still come
     fence_async_smem();
@@ -390,18 +420,20 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
     if (__syncthreads_or(!ok)) break;
     if (threadIdx.x < 32) {
       tc_fence_after();
-      issue_tile<D>(tl.d(t), base, base + S::kOffB + (t % S::kStages) * S::kB);
-      issue_more(tl.d(t), base + S::kOffAX, base + S::kOffBX + (t % S::kStages) * S::kBX);
+      issue_tile<D>(tl.d(t), base, base + S::kOffB + stage * S::kB);
+      issue_more(tl.d(t), base + S::kOffAX, base + S::kOffBX + stage * S::kBX);
       mma_commit(tl.bar[t & 1]);
     }
     if (t > 0) ok = tl.wait(t - 1);  // its operands may be replaced
     tc_fence_after();
-    fetch(t + 2);  // (nothing behind the last one: an empty group)
+    const int before = stage == 0 ? S::kStages - 1 : stage - 1;  // of tiles t - 1 and t + 2
+    fetch(before);
     if (t + 2 < tiles) {
-      place(t + 2, z);
+      place(t + 2, before, z);
       z = read(t + 3);
     }
     if (t > 0 && ok) reduce(t - 1);
+    stage = stage + 1 == S::kStages ? 0 : stage + 1;
   }
   ldev::copy_wait<0>();
   if (t > 0 && t == tiles) {
@@ -432,17 +464,18 @@ cudaError_t launch_tiles(void (*kern)(Args...), dim3 grid, int bytes, cudaStream
   return ldev::launch(kern, grid, kTileThreads, static_cast<size_t>(bytes), s, 1, args...);
 }
 
-// Tokens of a CTA: rows that are worth loading the pages' bounds for, few enough to give
-// every SM work.
-constexpr int kScoreMost = 2048, kScoreLeast = 256, kScoreCtas = 4 * 152;
+// Tokens of a CTA: what gives kScoreCtas CTAs at most (two fit on a SM with d = 128), but
+// kScoreLeast rows, which are worth loading the pages' bounds for.
+constexpr int kScoreLeast = 256, kScoreCtas = 2 * 152;
 
 template <int D>
 cudaError_t scores_tiles_dim(const LongParams& p, cudaStream_t s) {
   const int64_t cols = (p.table_width + 127) / 128;
-  int64_t rows = cols * p.B * p.Hk * p.Nq * p.G / kScoreCtas;
-  rows = rows < kScoreLeast ? kScoreLeast : (rows > kScoreMost ? kScoreMost : rows);
-  int64_t tokens = (rows + p.G - 1) / p.G;
-  if (tokens > p.Nq) tokens = p.Nq;
+  int64_t runs = kScoreCtas / (cols * p.B * p.Hk);
+  const int64_t most = (static_cast<int64_t>(p.Nq) * p.G + kScoreLeast - 1) / kScoreLeast;
+  if (runs > most) runs = most;
+  if (runs < 1) runs = 1;
+  const int64_t tokens = (p.Nq + runs - 1) / runs;
   const dim3 grid(static_cast<unsigned>(cols * ((p.Nq + tokens - 1) / tokens)), p.Hk, p.B);
   const int n = static_cast<int>(tokens), bytes = ScoreSmem<D>::kBytes;
   switch (p.G) {
