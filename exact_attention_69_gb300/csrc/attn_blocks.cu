@@ -25,7 +25,7 @@ namespace {
 using namespace ldev;
 
 constexpr int kWindow = 1024;  // pages that the bits cover at a time
-constexpr int kThreads = 32 * kBlocksWarps;
+constexpr int kListThreads = kWindow / 8;  // threads that list them, a byte of the bits each
 constexpr float kSlack = 8.f;
 
 // Parts of a row: maxima (log2 units) and sums first, then the weighted values in order.
@@ -81,13 +81,13 @@ struct Entry {
 
 template <int D, int NT>
 struct Shared {
-  static constexpr int kRows = 8 * NT;
+  static constexpr int kRows = 8 * NT, kBlocksWarps = blocks_warps(NT);
   struct Lists {
     uint32_t bits[kRows][kWindow / 32];
     Entry entry[kWindow];
     uint16_t who[kWindow];
     int32_t table[kWindow];
-    uint32_t sums[kBlocksWarps];
+    uint32_t sums[kListThreads / 32];
   };
   struct Join {
     float o[kBlocksWarps][kRows][D];  // (the first also takes the joined part)
@@ -101,8 +101,8 @@ struct Shared {
 };
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) blocks_kernel(const __grid_constant__ LongParams p) {
-  constexpr int kRows = 8 * NT, kC = D / 32, kM = D / 16;
+__global__ void __launch_bounds__(32 * blocks_warps(NT), 2) blocks_kernel(const __grid_constant__ LongParams p) {
+  constexpr int kRows = 8 * NT, kC = D / 32, kM = D / 16, kBlocksWarps = blocks_warps(NT), kThreads = 32 * kBlocksWarps;
   constexpr int kVec = D == 32 ? 4 : 8;           // neighbouring channels that a lane takes of V
   constexpr int kVC = D == 128 ? 2 : 1;           // such runs
   extern __shared__ __align__(16) unsigned char smem[];
@@ -172,24 +172,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) blocks_kernel(const
     }
     __syncthreads();
     // the pages that have a bit, in order: thread x has 8 of them
-    constexpr int kPer = kWindow / kThreads;
-    static_assert(kPer == 8, "a byte of the bits a thread");
-    uint32_t mine = 0;
+    uint32_t mine = 0, at = 0;
     const int word = threadIdx.x / 4, sft = (threadIdx.x % 4) * 8;
-    for (int t = 0; t < toks; ++t) mine |= sh.l.bits[t][word];
-    mine = (mine >> sft) & 255u;
-    uint32_t at = __popc(mine);
+    if (threadIdx.x < kListThreads) {
+      for (int t = 0; t < toks; ++t) mine |= sh.l.bits[t][word];
+      mine = (mine >> sft) & 255u;
+      at = __popc(mine);
 #pragma unroll
-    for (int s = 1; s < 32; s *= 2) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, at, s);
-      if (lane >= s) at += y;
+      for (int s = 1; s < 32; s *= 2) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, at, s);
+        if (lane >= s) at += y;
+      }
+      if (lane == 31) sh.l.sums[warp] = at;
     }
-    if (lane == 31) sh.l.sums[warp] = at;
     __syncthreads();
     int count = 0;
     at -= __popc(mine);
 #pragma unroll
-    for (int s = 0; s < kBlocksWarps; ++s) {
+    for (int s = 0; s < kListThreads / 32; ++s) {
       if (s < warp) at += sh.l.sums[s];
       count += sh.l.sums[s];
     }
@@ -384,7 +384,7 @@ cudaError_t blocks_dim(const LongParams& p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(tiles * p.splits), p.Hk, p.B);
   constexpr size_t kSmem = sizeof(Shared<D, NT>);
   static_assert(kSmem <= 48 * 1024, "no opt-in needed");
-  return launch(blocks_kernel<D, NT>, grid, kThreads, kSmem, s, p.splits, p);
+  return launch(blocks_kernel<D, NT>, grid, 32 * blocks_warps(NT), kSmem, s, p.splits, p);
 }
 
 }  // namespace

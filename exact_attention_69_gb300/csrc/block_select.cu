@@ -78,8 +78,12 @@ __device__ __forceinline__ void pick(Team<T>& team, At at, int lo, int hi, int k
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int x = first + 32 * e;
-    key[e] = 0u;  // (no value has this key)
-    if (x >= lo && x < hi) key[e] = key_of(at(x));
+    key[e] = __float_as_uint(at(min(max(x, lo), hi - 1)));  // (unconditional: all loads at once)
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const int x = first + 32 * e;
+    key[e] = x >= lo && x < hi ? key_of(__uint_as_float(key[e])) : 0u;  // (no value has the key 0)
   }
 #pragma unroll
   for (int e = 0; e < E; ++e)

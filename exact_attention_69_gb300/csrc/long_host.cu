@@ -136,19 +136,15 @@ int check_taken(const attn_long_params* p, const char* what) {
   return ATTN_OK;
 }
 
-// attn_blocks: CTAs that share a tile, a power of two. Enough for kBlocksCtas a SM, each
-// warp with kBlocksUnits groups of 16 keys or more.
-constexpr int kBlocksCtas = 3, kBlocksUnits = 2;
-
+// attn_blocks: CTAs that share a tile, a power of two: until there are 1.5 CTAs a SM, while
+// every warp has a group of 16 keys.
 int blocks_splits(const attn_long_params* p, int sms) {
   const int64_t rows = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk);
-  const int tr = attn::blocks_tile_rows(rows);
+  const int tr = attn::blocks_tile_rows(rows), warps = attn::blocks_warps(tr / 8);
   const int64_t all = (rows + tr - 1) / tr * p->B * p->Hk;
   const int64_t units = static_cast<int64_t>(p->n < p->table_width ? p->n : p->table_width) * (p->page_size / 16);
   int s = 1;
-  while (s < attn::kBlocksMaxSplits && all * s < static_cast<int64_t>(sms) * kBlocksCtas &&
-         2 * s * attn::kBlocksWarps * kBlocksUnits <= units)
-    s *= 2;
+  while (s < attn::kBlocksMaxSplits && 2 * all * s < 3 * static_cast<int64_t>(sms) && 2 * s * warps <= units) s *= 2;
   return s;
 }
 

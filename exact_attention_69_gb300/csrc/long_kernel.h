@@ -82,7 +82,8 @@ cudaError_t long_take_status(uint32_t word[4]);
 
 // attn_blocks: rows of a tile (a group of 8 columns of the products, or two).
 __host__ __device__ constexpr int blocks_tile_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
-constexpr int kBlocksWarps = 4;       // warps of a CTA, each with keys of its own
+// Warps of a CTA, each with keys of its own: two CTAs share a SM's registers.
+__host__ __device__ constexpr int blocks_warps(int groups) { return groups == 1 ? 6 : 4; }
 constexpr int kBlocksMaxSplits = 8;   // CTAs of a cluster on any GPU
 
 }  // namespace attn

@@ -147,12 +147,13 @@ struct ScoreSmem {
 // B holds min(q, 0) in its first D channels and max(q, 0) in the others. G: query heads of a
 // key head (0: any number).
 template <int D, int G>
-__global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_constant__ LongParams p, int tokens) {
+__global__ void __launch_bounds__(kTileThreads, 2) scores_tiles(const __grid_constant__ LongParams p, int tokens) {
   using S = ScoreSmem<D>;
   constexpr int kPieces = D / 8, kLoads = kTileRows * kPieces / kTileThreads;
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2];
   __shared__ uint32_t slot;
+  __shared__ int ids[128];  // the pages
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t a_at = smem_u32(smem), b_at = a_at + S::kA;
   Tiles2 tl;
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_consta
   const int rows = some ? (live - tok0) * heads : 0, tiles = (rows + kTileRows - 1) / kTileRows;
 
   // query rows of a tile: pieces of 16 bytes, D / 8 threads a row
-  uint4 q[kLoads];
+  uint4 q[kLoads], ahead[kLoads];  // of the next tile, and of the one behind it
   const int piece = static_cast<int>(threadIdx.x) % kPieces, row = static_cast<int>(threadIdx.x) / kPieces;
   constexpr int kStep = kTileThreads / kPieces;
   RowWalk walk(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb + static_cast<int64_t>(hk) * heads * p.q_sh +
@@ -184,16 +185,21 @@ __global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_consta
   const auto load = [&]() {
 #pragma unroll
     for (int e = 0; e < kLoads; ++e) {
-      q[e] = next < rows ? ldev::ld16(walk.at) : make_uint4(0, 0, 0, 0);
+      q[e] = ahead[e];
+      ahead[e] = next < rows ? ldev::ld16(walk.at) : make_uint4(0, 0, 0, 0);
       walk.next();
       next += kStep;
     }
   };
   if (tiles > 0) {
+    int mine = page < pages ? p.table[b * p.table_sb + page] : -1;
     load();
+    load();
+    ids[threadIdx.x] = mine;
+    __syncthreads();
+#pragma unroll 4
     for (int x = threadIdx.x; x < 128 * 2 * kPieces; x += kTileThreads) {
-      const int r = x / (2 * kPieces), c = x % (2 * kPieces);
-      const int id = page0 + r < pages ? p.table[b * p.table_sb + page0 + r] : -1;
+      const int r = x / (2 * kPieces), c = x % (2 * kPieces), id = ids[r];
       const bool real = id >= 0 && id < p.n_pages;
       ldev::copy16(a_at + operand_at<S::kK>(r, c, 128),
                    static_cast<const __nv_bfloat16*>(p.bounds) + ((real ? static_cast<int64_t>(id) : 0) * p.Hk + hk) * 2 * D + c * 8,
@@ -260,7 +266,7 @@ __global__ void __launch_bounds__(kTileThreads) scores_tiles(const __grid_consta
       mma_commit(tl.bar[t & 1]);
     }
     tc_fence_after();
-    if (t + 1 < tiles) load();
+    load();
     if (t > 0) reduce(t - 1);
   }
   if (t > 0 && t == tiles) {
@@ -303,6 +309,7 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
   __shared__ uint64_t bars[2];
   __shared__ uint32_t slot;
   __shared__ RowNumbers numbers[4];
+  __shared__ int ids[128];  // the keys' pages
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem);
   Tiles2 tl;
@@ -385,11 +392,14 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
 
   float z = 0.f;
   if (tiles > 0) {
+    const int mine = key < lens.len ? p.table[b * p.table_sb + (key >> p.page_shift)] : -1;
     z = read(0);
     const float z1 = read(1);
+    ids[threadIdx.x] = mine;
+    __syncthreads();
+#pragma unroll 4
     for (int x = threadIdx.x; x < 128 * kPieces; x += kTileThreads) {
-      const int r = x / kPieces, at = key0 + r;
-      const int id = at < lens.len ? p.table[b * p.table_sb + (at >> p.page_shift)] : -1;
+      const int r = x / kPieces, at = key0 + r, id = ids[r];
       const bool real = id >= 0 && id < p.n_pages;
       ldev::copy16(base + operand_at<D>(r, piece, 128),
                    static_cast<const __nv_bfloat16*>(p.kc) + (real ? id * p.kc_sp : 0) + hk * p.kc_sh +
