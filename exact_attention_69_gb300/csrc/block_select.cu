@@ -5,10 +5,11 @@
 // taken (the first ones and the last ones), ties to the lowest index, listed in
 // ascending order. Values become unsigned keys of the same order (NaN above
 // everything, -0 equal to +0). A team of threads holds a row's keys in registers, each
-// warp a run of consecutive ones, and finds bit by bit from the top the largest T that
-// at least k keys reach, or earlier one that exactly k reach. Ballots then place the
-// keys above T and the first of those equal to it. No atomics on the way, so the same
-// row always gives the same answer.
+// warp a run of consecutive ones, and finds the k-th greatest key digit by digit, from the
+// highest bit in which keys differ: a count of each digit among the keys that agree so
+// far, in shared memory (whole numbers: the order of the additions does not matter), until
+// the keys of a digit are wanted all. Ballots then place the keys above it and the
+// first of those equal to it.
 #include "long_dev.cuh"
 #include "long_kernel.h"
 
@@ -24,36 +25,35 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 }
 
 // A team of T threads: one warp, or a block.
+constexpr int kBins = 256;
 template <int T>
 struct Team {
   static_assert(T == 32 || (T % 32 == 0 && T <= 1024), "team");
-  int rank;
-  uint32_t* words;  // shared, two times T / 32
-  int turn = 0;
-  __device__ __forceinline__ Team(uint32_t* s) : rank(threadIdx.x % T), words(s) {}
+  struct Shared {
+    __align__(16) uint32_t bins[2][kBins];
+    uint32_t words[2][T / 32];
+  };
+  int rank, turn = 0, pass = 0;
+  Shared& sh;
+  __device__ __forceinline__ Team(Shared& s) : rank(threadIdx.x % T), sh(s) {}
   __device__ __forceinline__ int lane() const { return rank % 32; }
   __device__ __forceinline__ int warp() const { return rank / 32; }
-
+  __device__ __forceinline__ void barrier() {
+    if constexpr (T == 32)
+      __syncwarp();
+    else
+      __syncthreads();
+  }
   // A value of every warp, in lane w that of warp w (others 0).
   __device__ __forceinline__ uint32_t gather(uint32_t x) {
-    uint32_t* s = words + (turn ^= T / 32);  // (one barrier a call: the other half may still be read)
+    uint32_t* s = sh.words[turn ^= 1];  // (one barrier a call: the other half may still be read)
     if (lane() == 0) s[warp()] = x;
     __syncthreads();
     return lane() < T / 32 ? s[lane()] : 0u;
   }
-  __device__ __forceinline__ uint32_t sum(uint32_t x) {
-    x = __reduce_add_sync(0xffffffffu, x);
-    return T == 32 ? x : __reduce_add_sync(0xffffffffu, gather(x));
-  }
-  // Bits in which the threads' values differ.
-  __device__ __forceinline__ uint32_t differ(uint32_t ones, uint32_t zeros) {
-    ones = __reduce_or_sync(0xffffffffu, ones);
-    zeros = __reduce_or_sync(0xffffffffu, zeros);
-    if constexpr (T > 32) {
-      ones = __reduce_or_sync(0xffffffffu, gather(ones));
-      zeros = __reduce_or_sync(0xffffffffu, gather(zeros));
-    }
-    return ones & zeros;
+  __device__ __forceinline__ uint32_t any_of(uint32_t x) {
+    x = __reduce_or_sync(0xffffffffu, x);
+    return T == 32 ? x : __reduce_or_sync(0xffffffffu, gather(x));
   }
   // Of a count that is the same in all lanes of a warp: that of the warps before; `all`
   // gets the sum.
@@ -66,7 +66,48 @@ struct Team {
     *all = __reduce_add_sync(0xffffffffu, w);
     return __reduce_add_sync(0xffffffffu, lane() < warp() ? w : 0u);
   }
+  // Counts of digits, in the two sets in turn: those of the pass before may still be read.
+  __device__ __forceinline__ uint32_t* clear() {
+    uint32_t* h = sh.bins[pass ^= 1];
+    for (int x = rank; x < kBins; x += T) h[x] = 0;
+    barrier();
+    return h;
+  }
+  // The digit that holds the `left`-th key from the top; `left` becomes its rank among
+  // the digit's keys, `count` their number.
+  __device__ __forceinline__ uint32_t digit(const uint32_t* h, uint32_t& left, uint32_t& count) {
+    barrier();
+    uint32_t v[8], s = 0;  // from the greatest digit down
+    const uint4 a = reinterpret_cast<const uint4*>(h)[63 - 2 * lane()], b = reinterpret_cast<const uint4*>(h)[62 - 2 * lane()];
+    v[0] = a.w, v[1] = a.z, v[2] = a.y, v[3] = a.x, v[4] = b.w, v[5] = b.z, v[6] = b.y, v[7] = b.x;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) s += v[x];
+    uint32_t up = s;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, up, o);
+      if (lane() >= o) up += y;
+    }
+    const int at = __ffs(__ballot_sync(0xffffffffu, up >= left)) - 1;
+    uint32_t rest = left - (up - s), d = 0, c = 0;  // (what matters in lane `at`)
+    bool found = false;
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      if (!found && rest <= v[x]) {
+        found = true;
+        d = 255u - 8u * lane() - x;
+        c = v[x];
+      }
+      if (!found) rest -= v[x];
+    }
+    left = __shfl_sync(0xffffffffu, rest, at);
+    count = __shfl_sync(0xffffffffu, c, at);
+    return __shfl_sync(0xffffffffu, d, at);
+  }
 };
+
+// Whether the bits of x from `bits` up are zero.
+__device__ __forceinline__ bool agrees(uint32_t x, int bits) { return bits == 32 || (x >> bits) == 0; }
 
 // The k greatest of the values at [lo, hi), 1 <= k < hi - lo, hi <= T * E, ascending to
 // out. Warp w has the values 32 E w ..; value e of lane x is number 32 e + x of them.
@@ -83,45 +124,40 @@ __device__ __forceinline__ void pick(Team<T>& team, At at, int lo, int hi, int k
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     const int x = first + 32 * e;
-    key[e] = x >= lo && x < hi ? key_of(__uint_as_float(key[e])) : 0u;  // (no value has the key 0)
+    const bool in = x >= lo && x < hi;
+    key[e] = in ? key_of(__uint_as_float(key[e])) : 0u;  // (no value has the key 0)
+    ones |= key[e];
+    zeros |= in ? ~key[e] : 0u;
   }
-#pragma unroll
-  for (int e = 0; e < E; ++e)
-    if (key[e] != 0u) {
-      ones |= key[e];
-      zeros |= ~key[e];
-    }
-  const uint32_t open = team.differ(ones, zeros);
-  // bits that all keys have above the highest one in which they differ
-  const uint32_t top = open == 0u ? 0u : 0x80000000u >> __clz(open);
-  uint32_t t = T == 32 ? __reduce_or_sync(0xffffffffu, ones) : 0u;
-  if constexpr (T > 32) t = __reduce_or_sync(0xffffffffu, team.gather(__reduce_or_sync(0xffffffffu, ones)));
-  t &= open == 0u ? 0xffffffffu : ~((top << 1) - 1u);
+  ones = team.any_of(ones);
+  const uint32_t open = ones & team.any_of(zeros);
+  int bits = 32 - __clz(open);  // low bits that are not known yet; the keys agree above them
+  uint32_t t = bits == 32 ? 0u : (ones >> bits) << bits, left = static_cast<uint32_t>(k);
   bool ties = true;  // more keys than wanted may be equal to t
-  for (uint32_t bit = top; bit != 0; bit >>= 1) {
-    uint32_t c = 0;
+  while (bits > 0) {
+    const int shift = max(bits - 8, 0);
+    uint32_t* h = team.clear();
 #pragma unroll
-    for (int e = 0; e < E; ++e) c += key[e] >= (t | bit);
-    c = team.sum(c);
-    if (c >= static_cast<uint32_t>(k)) t |= bit;
-    if (c == static_cast<uint32_t>(k)) {
+    for (int e = 0; e < E; ++e)
+      if (key[e] != 0u && agrees(key[e] ^ t, bits)) atomicAdd(h + ((key[e] >> shift) & ((1u << (bits - shift)) - 1u)), 1u);
+    uint32_t count;
+    t |= team.digit(h, left, count) << shift;
+    bits = shift;
+    if (count == left) {
       ties = false;
       break;
     }
   }
   uint32_t above = 0, equal = 0, all;
-  if (!ties) t -= 1;  // (t has a bit set: it is some key's prefix above lower ones)
+  if (!ties) t -= 1;  // all keys from t up (t is not 0: some key lies below it)
 #pragma unroll
   for (int e = 0; e < E; ++e) {
     above += key[e] > t;
     equal += key[e] == t;
   }
-  above = __reduce_add_sync(0xffffffffu, above);
-  uint32_t a = team.before(above, &all), q = 0, want = 0;
-  if (ties) {
-    want = static_cast<uint32_t>(k) - all;  // of those equal to t, the first
-    q = team.before(__reduce_add_sync(0xffffffffu, equal), &all);
-  }
+  uint32_t a = team.before(__reduce_add_sync(0xffffffffu, above), &all), q = 0;
+  const uint32_t want = ties ? left : 0u;  // of those equal to t, the first
+  if (ties) q = team.before(__reduce_add_sync(0xffffffffu, equal), &all);
   const uint32_t mine = (1u << team.lane()) - 1u;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
@@ -136,26 +172,18 @@ __device__ __forceinline__ void pick(Team<T>& team, At at, int lo, int hi, int k
   }
 }
 
-// The same for rows of any length: the row is read again for every digit of 8 bits and
-// for the placing.
+// The same for rows of any length: the row is read again for every digit and for the
+// placing.
 template <int T, typename At>
-__device__ __forceinline__ void pick_long(Team<T>& team, uint32_t* hist, At at, int lo, int hi, int k, int32_t* out) {
-  uint32_t t = 0;
-  int left = k;  // of the keys that agree with t so far, how many are wanted
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    __syncthreads();
-    for (int x = team.rank; x < 256; x += T) hist[x] = 0;
-    __syncthreads();
+__device__ __forceinline__ void pick_long(Team<T>& team, At at, int lo, int hi, int k, int32_t* out) {
+  uint32_t t = 0, left = static_cast<uint32_t>(k), count;
+  for (int bits = 32; bits > 0; bits -= 8) {
+    uint32_t* h = team.clear();
     for (int x = lo + team.rank; x < hi; x += T) {
       const uint32_t key = key_of(at(x));
-      if (shift == 24 || (key >> (shift + 8)) == (t >> (shift + 8))) atomicAdd(hist + ((key >> shift) & 255u), 1u);
+      if (agrees(key ^ t, bits)) atomicAdd(h + ((key >> (bits - 8)) & 255u), 1u);
     }
-    __syncthreads();
-    int digit = 255;
-    uint32_t c = 0;
-    while (digit > 0 && c + hist[digit] < static_cast<uint32_t>(left)) c += hist[digit--];
-    left -= static_cast<int>(c);
-    t |= static_cast<uint32_t>(digit) << shift;
+    t |= team.digit(h, left, count) << (bits - 8);
   }
   uint32_t done = 0, tied = 0;
   const uint32_t mine = (1u << team.lane()) - 1u;
@@ -167,7 +195,7 @@ __device__ __forceinline__ void pick_long(Team<T>& team, uint32_t* hist, At at, 
     const uint32_t same = __ballot_sync(0xffffffffu, eq);
     const uint32_t q = tied + team.before(__popc(same), &all) + __popc(same & mine);
     tied += all;
-    const bool take = key > t || (eq && q < static_cast<uint32_t>(left));
+    const bool take = key > t || (eq && q < left);
     const uint32_t took = __ballot_sync(0xffffffffu, take);
     const uint32_t a = done + team.before(__popc(took), &all) + __popc(took & mine);
     done += all;
@@ -178,7 +206,7 @@ __device__ __forceinline__ void pick_long(Team<T>& team, uint32_t* hist, At at, 
 // A row of `n` values, `take` to be taken, the first `first` and last `last` among them
 // for sure; -1 behind them in out[0, width).
 template <int T, int E, bool LONG, typename At>
-__device__ __forceinline__ void choose(Team<T>& team, uint32_t* hist, At at, int n, int take, int first, int last,
+__device__ __forceinline__ void choose(Team<T>& team, At at, int n, int take, int first, int last,
                                        int width, int32_t* out) {
   if (n <= take) {
     for (int x = team.rank; x < width; x += T) out[x] = x < n ? x : -1;
@@ -190,7 +218,7 @@ __device__ __forceinline__ void choose(Team<T>& team, uint32_t* hist, At at, int
   for (int x = take + team.rank; x < width; x += T) out[x] = -1;
   if (k <= 0) return;
   if constexpr (LONG)
-    pick_long<T>(team, hist, at, first, n - last, k, out + first);
+    pick_long<T>(team, at, first, n - last, k, out + first);
   else
     pick<T, E>(team, at, first, n - last, k, out + first);
 }
@@ -199,8 +227,7 @@ __device__ __forceinline__ void choose(Team<T>& team, uint32_t* hist, At at, int
 
 template <int T, int E, bool LONG>
 __global__ void __launch_bounds__(T < 128 ? 128 : T) select_kernel(const __grid_constant__ LongParams p) {
-  __shared__ uint32_t words[T > 32 ? 2 * (T / 32) : 1];
-  __shared__ uint32_t hist[LONG ? 256 : 1];
+  __shared__ typename Team<T>::Shared shared[T == 32 ? 4 : 1];
   grid_dep_wait();
   grid_dep_launch();
   const int64_t row = T == 32 ? static_cast<int64_t>(blockIdx.x) * 4 + threadIdx.x / 32 : blockIdx.x;
@@ -208,16 +235,15 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) select_kernel(const __grid_
   const int i = static_cast<int>(row % p.Nq), b = static_cast<int>(row / (static_cast<int64_t>(p.Nq) * p.Hk));
   const int n = min(long_pages(p, long_seen(p, long_lens(p, b), i)), p.table_width);
   const float* s = p.scores + row * p.table_width;
-  Team<T> team(words);
-  choose<T, E, LONG>(team, hist, [&](int x) { return s[x]; }, n, p.n, p.first, p.last, p.n, p.blocks + row * p.n);
+  Team<T> team(shared[T == 32 ? threadIdx.x / 32 : 0]);
+  choose<T, E, LONG>(team, [&](int x) { return s[x]; }, n, p.n, p.first, p.last, p.n, p.blocks + row * p.n);
 }
 
 // ------------------------------------------------------------------ tokens of a cache
 
 template <int T, int E, bool LONG>
 __global__ void __launch_bounds__(T) keep_kernel(const __grid_constant__ LongParams p) {
-  __shared__ uint32_t words[2 * (T / 32)];
-  __shared__ uint32_t hist[LONG ? 256 : 1];
+  __shared__ typename Team<T>::Shared shared;
   grid_dep_wait();
   grid_dep_launch();
   const int hk = blockIdx.x % p.Hk, b = blockIdx.x / p.Hk;
@@ -225,12 +251,12 @@ __global__ void __launch_bounds__(T) keep_kernel(const __grid_constant__ LongPar
   if (hk == 0 && threadIdx.x == 0) p.new_lens[b] = min(n, p.n);
   const int32_t* table = p.table + b * p.table_sb;
   const int mask = (1 << p.page_shift) - 1;
-  Team<T> team(words);
+  Team<T> team(shared);
   const auto at = [&](int x) {
     const int id = table[x >> p.page_shift];
     return id >= 0 && id < p.n_pages ? p.weights[((static_cast<int64_t>(id) * p.Hk + hk) << p.page_shift) + (x & mask)] : 0.f;
   };
-  choose<T, E, LONG>(team, hist, at, n, p.n, p.first, p.last, p.n, p.kept + (static_cast<int64_t>(b) * p.Hk + hk) * p.n);
+  choose<T, E, LONG>(team, at, n, p.n, p.first, p.last, p.n, p.kept + (static_cast<int64_t>(b) * p.Hk + hk) * p.n);
 }
 
 // Moves the kept tokens. Token x of the list goes to place x, which is no later than
@@ -324,7 +350,9 @@ cudaError_t launch_select(const LongParams& p, cudaStream_t s) {
 cudaError_t launch_evict(const LongParams& p, int d, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(p.B) * static_cast<unsigned>(p.Hk));
   cudaError_t e;
-  if (p.max_len <= 4096)
+  if (p.max_len <= 2048)
+    e = launch(keep_kernel<256, 8, false>, grid, 256, 0, s, 1, p);
+  else if (p.max_len <= 4096)
     e = launch(keep_kernel<1024, 4, false>, grid, 1024, 0, s, 1, p);
   else if (p.max_len <= 16384)
     e = launch(keep_kernel<1024, 16, false>, grid, 1024, 0, s, 1, p);

@@ -211,29 +211,42 @@ __global__ void __launch_bounds__(kTileThreads, 2) scores_tiles(const __grid_con
   float best = -INFINITY;
   int tok = 0, g = 0;  // the token and head that the next column is
   float* at = out;
+  // token n of the run (below live) sees max(first + n * by, 0) slots
+  const int first = p.causal ? lens.len - lens.ql + tok0 + 1 : lens.len, by = p.causal ? 1 : 0;
+  const auto sees = [&](int n) { return long_pages(p, max(first + n * by, 0)); };
   const bool in = page < p.table_width;
   const auto reduce = [&](int t) {
     uint32_t v[2][32];
     tmem_ld32(tl.d(t) + ((threadIdx.x >> 5) << 21), v[0]);
     tmem_ld32(tl.d(t) + ((threadIdx.x >> 5) << 21) + 32, v[1]);
+    if constexpr (G > 0) {  // (G divides the tile)
+      constexpr int kToks = kTileRows / G;
+      const bool whole = page0 + 128 <= sees(tok) && tok + kToks <= live - tok0;  // every page, for every token
 #pragma unroll
-    for (int c = 0; c < kTileRows; ++c) {
-      best = max_nan(best, __uint_as_float(v[c >> 5][c & 31]));
-      bool last;
-      if constexpr (G > 0) {
-        last = (c + 1) % G == 0;  // (G divides the tile)
-      } else {
-        last = ++g == heads;
-      }
-      if (last) {
-        if (in && tok < live - tok0) {
-          const bool sees = page < long_pages(p, long_seen(p, lens, tok0 + tok));
-          *at = sees ? best * p.scale : -INFINITY;
+      for (int n = 0; n < kToks; ++n) {
+        float z = __uint_as_float(v[n * G >> 5][(n * G) & 31]);
+#pragma unroll
+        for (int c = n * G + 1; c < (n + 1) * G; ++c) z = max_nan(z, __uint_as_float(v[c >> 5][c & 31]));
+        z *= p.scale;
+        if (whole) {
+          *at = z;
+        } else if (in && tok + n < live - tok0) {
+          *at = page < sees(tok + n) ? z : -INFINITY;
         }
-        best = -INFINITY;
-        g = 0;
-        ++tok;
         at += p.table_width;
+      }
+      tok += kToks;
+    } else {
+#pragma unroll
+      for (int c = 0; c < kTileRows; ++c) {
+        best = max_nan(best, __uint_as_float(v[c >> 5][c & 31]));
+        if (++g == heads) {
+          if (in && tok < live - tok0) *at = page < sees(tok) ? best * p.scale : -INFINITY;
+          best = -INFINITY;
+          g = 0;
+          ++tok;
+          at += p.table_width;
+        }
       }
     }
   };
@@ -476,7 +489,7 @@ cudaError_t launch_tiles(void (*kern)(Args...), dim3 grid, int bytes, cudaStream
 
 // Tokens of a CTA: what gives kScoreCtas CTAs at most (two fit on a SM with d = 128), but
 // kScoreLeast rows, which are worth loading the pages' bounds for.
-constexpr int kScoreLeast = 256, kScoreCtas = 2 * 152;
+constexpr int kScoreLeast = 256, kScoreCtas = 4 * 152;
 
 template <int D>
 cudaError_t scores_tiles_dim(const LongParams& p, cudaStream_t s) {
