@@ -106,25 +106,27 @@ struct Team {
   }
 };
 
-// Whether the bits of x from `bits` up are zero.
-__device__ __forceinline__ bool agrees(uint32_t x, int bits) { return bits == 32 || (x >> bits) == 0; }
-
 // The k greatest of the values at [lo, hi), 1 <= k < hi - lo, hi <= T * E, ascending to
-// out. Warp w has the values 32 E w ..; value e of lane x is number 32 e + x of them.
-template <int T, int E, typename At>
+// out. Warp w has the values 32 E w ..; lane x has runs of V neighbouring ones, run e
+// beginning at number 32 V e + V x of them. at(x, v): values x .. x + V - 1 (x a multiple
+// of V below hi; what lies behind hi may be anything).
+template <int T, int E, int V, typename At>
 __device__ __forceinline__ void pick(Team<T>& team, At at, int lo, int hi, int k, int32_t* out) {
+  static_assert(E % V == 0, "whole runs");
   uint32_t key[E];
-  const int first = team.warp() * 32 * E + team.lane();
+  const int first = team.warp() * 32 * E + team.lane() * V;
+  const auto place = [&](int e) { return first + e / V * (32 * V) + e % V; };
   uint32_t ones = 0, zeros = 0;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const int x = first + 32 * e;
-    key[e] = __float_as_uint(at(min(max(x, lo), hi - 1)));  // (unconditional: all loads at once)
+  for (int e = 0; e < E; e += V) {  // (unconditional: all loads at once)
+    float v[V];
+    at(min(place(e), (hi - 1) / V * V), v);
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[e + i] = __float_as_uint(v[i]);
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    const int x = first + 32 * e;
-    const bool in = x >= lo && x < hi;
+    const bool in = place(e) >= lo && place(e) < hi;
     key[e] = in ? key_of(__uint_as_float(key[e])) : 0u;  // (no value has the key 0)
     ones |= key[e];
     zeros |= in ? ~key[e] : 0u;
@@ -133,42 +135,72 @@ __device__ __forceinline__ void pick(Team<T>& team, At at, int lo, int hi, int k
   const uint32_t open = ones & team.any_of(zeros);
   int bits = 32 - __clz(open);  // low bits that are not known yet; the keys agree above them
   uint32_t t = bits == 32 ? 0u : (ones >> bits) << bits, left = static_cast<uint32_t>(k);
-  bool ties = true;  // more keys than wanted may be equal to t
+  bool ties = true, all_agree = true;  // ties: more keys than wanted may be equal to t
   while (bits > 0) {
     const int shift = max(bits - 8, 0);
+    const uint32_t mask = (1u << (bits - shift)) - 1u;
     uint32_t* h = team.clear();
+    if (all_agree) {
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if (key[e] != 0u && agrees(key[e] ^ t, bits)) atomicAdd(h + ((key[e] >> shift) & ((1u << (bits - shift)) - 1u)), 1u);
+      for (int e = 0; e < E; ++e)
+        if (key[e] != 0u) atomicAdd(h + ((key[e] >> shift) & mask), 1u);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (((key[e] ^ t) >> bits) == 0u) atomicAdd(h + ((key[e] >> shift) & mask), 1u);  // (bits < 32; t > 0: not key 0)
+    }
     uint32_t count;
     t |= team.digit(h, left, count) << shift;
     bits = shift;
+    all_agree = false;
     if (count == left) {
       ties = false;
       break;
     }
   }
-  uint32_t above = 0, equal = 0, all;
   if (!ties) t -= 1;  // all keys from t up (t is not 0: some key lies below it)
+  uint32_t above = 0, equal = 0, all;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    above += key[e] > t;
-    equal += key[e] == t;
-  }
-  uint32_t a = team.before(__reduce_add_sync(0xffffffffu, above), &all), q = 0;
-  const uint32_t want = ties ? left : 0u;  // of those equal to t, the first
-  if (ties) q = team.before(__reduce_add_sync(0xffffffffu, equal), &all);
+  for (int e = 0; e < E; ++e) above += key[e] > t;
+  uint32_t a = team.before(__reduce_add_sync(0xffffffffu, above), &all);
   const uint32_t mine = (1u << team.lane()) - 1u;
+  if (!ties) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const uint32_t up = __ballot_sync(0xffffffffu, key[e] > t);
-    uint32_t eq = 0;
-    if (ties) eq = __ballot_sync(0xffffffffu, key[e] == t);
-    const uint32_t qe = q + __popc(eq & mine);
-    const bool take = key[e] > t || (ties && key[e] == t && qe < want);
-    if (take) out[a + __popc(up & mine) + min(qe, want)] = first + 32 * e;
-    a += __popc(up);
-    q += __popc(eq);
+    for (int e = 0; e < E; e += V) {
+      uint32_t up[V], n = a;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        up[i] = __ballot_sync(0xffffffffu, key[e + i] > t);
+        n += __popc(up[i] & mine);
+        a += __popc(up[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (key[e + i] > t) out[n++] = place(e + i);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < E; ++e) equal += key[e] == t;
+  uint32_t q = team.before(__reduce_add_sync(0xffffffffu, equal), &all);
+#pragma unroll
+  for (int e = 0; e < E; e += V) {
+    uint32_t n = a, m = q;  // of those above t, and equal to it, before this lane's run
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const uint32_t up = __ballot_sync(0xffffffffu, key[e + i] > t), eq = __ballot_sync(0xffffffffu, key[e + i] == t);
+      n += __popc(up & mine);
+      a += __popc(up);
+      m += __popc(eq & mine);
+      q += __popc(eq);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const bool eq = key[e + i] == t;
+      if (key[e + i] > t || (eq && m < left)) out[n + min(m, left)] = place(e + i);  // (left: of the equal ones, the first)
+      n += key[e + i] > t;
+      m += eq;
+    }
   }
 }
 
@@ -181,7 +213,7 @@ __device__ __forceinline__ void pick_long(Team<T>& team, At at, int lo, int hi, 
     uint32_t* h = team.clear();
     for (int x = lo + team.rank; x < hi; x += T) {
       const uint32_t key = key_of(at(x));
-      if (agrees(key ^ t, bits)) atomicAdd(h + ((key >> (bits - 8)) & 255u), 1u);
+      if (bits == 32 || ((key ^ t) >> bits) == 0u) atomicAdd(h + ((key >> (bits - 8)) & 255u), 1u);
     }
     t |= team.digit(h, left, count) << (bits - 8);
   }
@@ -205,9 +237,8 @@ __device__ __forceinline__ void pick_long(Team<T>& team, At at, int lo, int hi, 
 
 // A row of `n` values, `take` to be taken, the first `first` and last `last` among them
 // for sure; -1 behind them in out[0, width).
-template <int T, int E, bool LONG, typename At>
-__device__ __forceinline__ void choose(Team<T>& team, At at, int n, int take, int first, int last,
-                                       int width, int32_t* out) {
+template <int T, int E, int V, bool LONG, typename At>
+__device__ __forceinline__ void choose(Team<T>& team, At at, int n, int take, int first, int last, int width, int32_t* out) {
   if (n <= take) {
     for (int x = team.rank; x < width; x += T) out[x] = x < n ? x : -1;
     return;
@@ -218,9 +249,16 @@ __device__ __forceinline__ void choose(Team<T>& team, At at, int n, int take, in
   for (int x = take + team.rank; x < width; x += T) out[x] = -1;
   if (k <= 0) return;
   if constexpr (LONG)
-    pick_long<T>(team, at, first, n - last, k, out + first);
+    pick_long<T>(
+        team,
+        [&](int x) {
+          float v[1];
+          at(x, v);
+          return v[0];
+        },
+        first, n - last, k, out + first);
   else
-    pick<T, E>(team, at, first, n - last, k, out + first);
+    pick<T, E, V>(team, at, first, n - last, k, out + first);
 }
 
 // ------------------------------------------------------------------ pages of a query
@@ -236,7 +274,7 @@ __global__ void __launch_bounds__(T < 128 ? 128 : T) select_kernel(const __grid_
   const int n = min(long_pages(p, long_seen(p, long_lens(p, b), i)), p.table_width);
   const float* s = p.scores + row * p.table_width;
   Team<T> team(shared[T == 32 ? threadIdx.x / 32 : 0]);
-  choose<T, E, LONG>(team, [&](int x) { return s[x]; }, n, p.n, p.first, p.last, p.n, p.blocks + row * p.n);
+  choose<T, E, 1, LONG>(team, [&](int x, float(&v)[1]) { v[0] = s[x]; }, n, p.n, p.first, p.last, p.n, p.blocks + row * p.n);
 }
 
 // ------------------------------------------------------------------ tokens of a cache
@@ -252,11 +290,22 @@ __global__ void __launch_bounds__(T) keep_kernel(const __grid_constant__ LongPar
   const int32_t* table = p.table + b * p.table_sb;
   const int mask = (1 << p.page_shift) - 1;
   Team<T> team(shared);
-  const auto at = [&](int x) {
+  // (a page's weights are contiguous, and aligned to 16 bytes)
+  constexpr int V = LONG ? 1 : 4;
+  const auto at = [&](int x, float(&v)[V]) {
     const int id = table[x >> p.page_shift];
-    return id >= 0 && id < p.n_pages ? p.weights[((static_cast<int64_t>(id) * p.Hk + hk) << p.page_shift) + (x & mask)] : 0.f;
+    const bool real = id >= 0 && id < p.n_pages;
+    const float* w = p.weights + ((static_cast<int64_t>(real ? id : 0) * p.Hk + hk) << p.page_shift) + (x & mask);
+    if constexpr (V == 4) {
+      const float4 y = *reinterpret_cast<const float4*>(w);
+      v[0] = y.x, v[1] = y.y, v[2] = y.z, v[3] = y.w;
+    } else {
+      v[0] = *w;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = real ? v[i] : 0.f;
   };
-  choose<T, E, LONG>(team, at, n, p.n, p.first, p.last, p.n, p.kept + (static_cast<int64_t>(b) * p.Hk + hk) * p.n);
+  choose<T, E, V, LONG>(team, at, n, p.n, p.first, p.last, p.n, p.kept + (static_cast<int64_t>(b) * p.Hk + hk) * p.n);
 }
 
 // Moves the kept tokens. Token x of the list goes to place x, which is no later than

@@ -250,6 +250,7 @@ int attn_kv_evict(const attn_long_params* p) {
       (rc = check_taken(p, "tokens to keep")) != ATTN_OK || (rc = need(p->weights, "weights")) != ATTN_OK ||
       (rc = need(p->kept, "kept")) != ATTN_OK || (rc = need(p->new_lens, "new_lens")) != ATTN_OK)
     return rc;
+  if (!aligned(p->weights, 16)) return fail_with(ATTN_ERR_MISALIGNED, "weights must be 16-byte aligned");
   if (p->new_lens == p->kv_lens) return fail_with(ATTN_ERR_INVALID_ARG, "new_lens must not be kv_lens");
   if (static_cast<int64_t>(p->B) * p->Hk >= kMaxCount || static_cast<int64_t>(p->n) >= kMaxCount)
     return fail_with(ATTN_ERR_INVALID_ARG, "too many rows, or n too large");

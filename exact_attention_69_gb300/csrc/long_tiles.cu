@@ -74,11 +74,13 @@ __device__ __forceinline__ void issue_tile(uint32_t d_tmem, uint32_t a, uint32_t
   }
 }
 
-// D += the product of 16 further channels in operands of 64-byte rows.
+// D += the product of 16 further channels. Their operands are not swizzled: groups of 8
+// rows, 128 bytes (8 rows of 16) for the first 8 channels, then 128 for the others.
 __device__ __forceinline__ void issue_more(uint32_t d_tmem, uint32_t a, uint32_t b) {
   constexpr uint32_t kIdesc = make_idesc(128, kTileRows, false);
-  mma_ss(d_tmem, smem_desc(a, 16, 8 * 64, 4u), smem_desc(b, 16, 8 * 64, 4u), kIdesc, 1u);
+  mma_ss(d_tmem, smem_desc(a, 128, 256, 0u), smem_desc(b, 128, 256, 0u), kIdesc, 1u);
 }
+__device__ __forceinline__ uint32_t more_at(int r, int half) { return (r >> 3) * 256 + half * 128 + (r & 7) * 16; }
 
 // Where a thread's piece of a query row is, row by row of a stride: r = n * heads + g
 // without a division each.
@@ -298,12 +300,12 @@ __global__ void __launch_bounds__(kTileThreads, 2) scores_tiles(const __grid_con
 // The rows' lse takes part in the product: keys get four further channels of one, query
 // row r those of -lse[r] / scale in four parts (three of 8 bits each that hold its fp32
 // value, and what that leaves), so a tile's accumulator is q . k - lse / scale, formed in
-// fp32 like the sum itself, and a weight is one product and one exp2 of it. The extra 16
-// channels lie in operands of 32 (64-byte rows), half of which nothing reads.
+// fp32 like the sum itself, and a weight is one product and one exp2 of it. The further 16
+// channels lie in operands of their own, unswizzled (8 rows of 16 bytes after one another).
 template <int D>
 struct WeightSmem {
-  static constexpr int kA = 128 * D * 2, kB = kTileRows * D * 2, kStages = 3;
-  static constexpr int kAX = 128 * 64, kBX = kTileRows * 64;
+  static constexpr int kA = 128 * D * 2, kB = kTileRows * D * 2, kStages = D == 128 ? 2 : 3;
+  static constexpr int kAX = 128 * 32, kBX = kTileRows * 32;
   static constexpr int kOffB = kA, kOffAX = kOffB + kStages * kB, kOffBX = kOffAX + kAX;
   static constexpr int kBytes = kOffBX + kStages * kBX + 1024;
 };
@@ -318,6 +320,7 @@ template <int D>
 __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_constant__ LongParams p) {
   using S = WeightSmem<D>;
   constexpr int kPieces = D / 8, kStep = kTileThreads / kPieces;
+  constexpr int kAhead = S::kStages - 1;  // tiles that rows are fetched ahead
   extern __shared__ uint8_t raw[];
   __shared__ uint64_t bars[2];
   __shared__ uint32_t slot;
@@ -342,7 +345,7 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
   int next = row;  // the row that the walk is at
   const uint32_t to = operand_at<D>(row, piece, kTileRows);
 
-  // a tile's query rows, two tiles before they are used
+  // a tile's query rows, kAhead tiles before they are used
   const auto fetch = [&](int stage) {
     static_assert(kStep % 8 == 0, "the swizzle of a thread's rows is the same");
     const uint32_t dst = base + S::kOffB + stage * S::kB + to;
@@ -371,7 +374,7 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
       left = fmaf(-z, p.c_hi, -x) - z * p.c_lo;
     }
     const uint2 v = make_uint2(ldev::pack_bf16(x, x1), ldev::pack_bf16(x2, left));
-    *reinterpret_cast<uint2*>(smem + S::kOffBX + stage * S::kBX + operand_at<32>(threadIdx.x, 0, kTileRows)) = v;
+    *reinterpret_cast<uint2*>(smem + S::kOffBX + stage * S::kBX + more_at(threadIdx.x, 0)) = v;
     const int sees = none ? 0 : long_seen(p, lens, p.by_g.div(r));
     numbers[t % 4].sees[threadIdx.x] = r < rows ? sees : 0;
     const int least = __reduce_min_sync(0xffffffffu, r < rows ? sees : 0);
@@ -407,7 +410,7 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
   if (tiles > 0) {
     const int mine = key < lens.len ? p.table[b * p.table_sb + (key >> p.page_shift)] : -1;
     z = read(0);
-    const float z1 = read(1);
+    const float z1 = kAhead > 1 ? read(1) : 0.f;
     ids[threadIdx.x] = mine;
     __syncthreads();
 #pragma unroll 4
@@ -420,24 +423,22 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
                    real ? 16 : 0);
     }
     fetch(0);
-    fetch(1);  // (nothing behind the last row: an empty group)
+    if constexpr (kAhead > 1) fetch(1);  // (nothing behind the last row: an empty group)
     // the further channels: ones for the keys, zeros behind the four of the rows
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(smem + S::kOffAX + operand_at<32>(threadIdx.x, 0, 128)) = make_uint4(0x3F803F80u, 0x3F803F80u, 0, 0);
-    *reinterpret_cast<uint4*>(smem + S::kOffAX + operand_at<32>(threadIdx.x, 1, 128)) = zero;
-    for (int x = threadIdx.x; x < S::kStages * kTileRows; x += kTileThreads) {
-      *reinterpret_cast<uint4*>(smem + S::kOffBX + (x / kTileRows) * S::kBX + operand_at<32>(x % kTileRows, 0, kTileRows)) = zero;
-      *reinterpret_cast<uint4*>(smem + S::kOffBX + (x / kTileRows) * S::kBX + operand_at<32>(x % kTileRows, 1, kTileRows)) = zero;
-    }
+    *reinterpret_cast<uint4*>(smem + S::kOffAX + more_at(threadIdx.x, 0)) = make_uint4(0x3F803F80u, 0x3F803F80u, 0, 0);
+    *reinterpret_cast<uint4*>(smem + S::kOffAX + more_at(threadIdx.x, 1)) = zero;
+    for (int x = threadIdx.x; x < S::kStages * S::kBX / 16; x += kTileThreads)
+      *reinterpret_cast<uint4*>(smem + S::kOffBX + x * 16) = zero;
     __syncthreads();
     place(0, 0, z);
-    place(1, 1, z1);
-    z = read(2);
+    if constexpr (kAhead > 1) place(1, 1, z1);
+    z = read(kAhead);
   }
   bool ok = true;
   int t = 0, stage = 0;  // (stage: t modulo kStages)
   for (; t < tiles; ++t) {
-    ldev::copy_wait<1>();  // tile t's; t + 1's may still come
+    ldev::copy_wait<kAhead - 1>();  // tile t's; the next one's may still come
     fence_async_smem();
     tc_fence_before();
     if (__syncthreads_or(!ok)) break;
@@ -449,11 +450,11 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
     }
     if (t > 0) ok = tl.wait(t - 1);  // its operands may be replaced
     tc_fence_after();
-    const int before = stage == 0 ? S::kStages - 1 : stage - 1;  // of tiles t - 1 and t + 2
+    const int before = stage == 0 ? S::kStages - 1 : stage - 1;  // of tiles t - 1 and t + kAhead
     fetch(before);
-    if (t + 2 < tiles) {
-      place(t + 2, before, z);
-      z = read(t + 3);
+    if (t + kAhead < tiles) {
+      place(t + kAhead, before, z);
+      z = read(t + kAhead + 1);
     }
     if (t > 0 && ok) reduce(t - 1);
     stage = stage + 1 == S::kStages ? 0 : stage + 1;
