@@ -75,5 +75,26 @@ inline int log2_page(int page_size, int* shift) {
   return ATTN_OK;
 }
 
+// A cache's tensor map: boxes of `rows` slots, or a page if that is less.
+inline int encode_pages(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, int d, int page_size,
+                 int heads, int pages, int rows, const int64_t st[3], const char* name) {
+  const int cols = d >= 64 ? 64 : 32;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
+                              static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(pages)};
+  // a dimension of size 1 may have any stride that the map accepts
+  auto bytes = [&](int64_t s) { return static_cast<cuuint64_t>(s > 0 ? s : d) * 2; };
+  const cuuint64_t strides[3] = {bytes(st[2]), bytes(st[1]), bytes(st[0])};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(cols),
+                             static_cast<cuuint32_t>(page_size < rows ? page_size : rows), 1, 1};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, ones,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            d >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail_with(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", name, static_cast<int>(r));
+  return ATTN_OK;
+}
+
 }  // namespace host
 }  // namespace attn

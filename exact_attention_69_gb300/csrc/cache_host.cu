@@ -195,26 +195,6 @@ void plan_paged(const attn_paged_params* p, int sms, PagedPlan* pl) {
   }
 }
 
-int encode_pages(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const void* base, int d, int page_size,
-                 int heads, int pages, const int64_t st[3], const char* name) {
-  const int cols = d >= 64 ? 64 : 32;
-  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page_size),
-                              static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(pages)};
-  // a dimension of size 1 may have any stride that the map accepts
-  auto bytes = [&](int64_t s) { return static_cast<cuuint64_t>(s > 0 ? s : d) * 2; };
-  const cuuint64_t strides[3] = {bytes(st[2]), bytes(st[1]), bytes(st[0])};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(cols),
-                             static_cast<cuuint32_t>(page_size < attn::kBN ? page_size : attn::kBN), 1, 1};
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
-  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box, ones,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            d >= 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  if (r != CUDA_SUCCESS)
-    return fail_with(ATTN_ERR_CUDA, "cuTensorMapEncodeTiled(%s) failed with CUresult %d", name, static_cast<int>(r));
-  return ATTN_OK;
-}
-
 int encode_queries(PFN_cuTensorMapEncodeTiled_v12000 encode, CUtensorMap* m, const attn_paged_params* p,
                    const attn::RopeTensor& q, int G, bool sequences) {
   const cuuint64_t dims[4] = {static_cast<cuuint64_t>(p->d), static_cast<cuuint64_t>(p->Hq),
@@ -440,8 +420,8 @@ int attn_paged(const attn_paged_params* p) {
                      static_cast<unsigned long long>(p->workspace ? p->workspace_bytes : 0),
                      static_cast<long long>(pl.bytes()));
   const int64_t ks[3] = {kc.sb, kc.sh, kc.sn}, vs[3] = {vc.sb, vc.sh, vc.sn};
-  if ((rc = encode_pages(encode, &k.tm_k, p->k_cache, p->d, p->page_size, p->Hk, p->n_pages, ks, "k_cache")) != ATTN_OK ||
-      (rc = encode_pages(encode, &k.tm_v, p->v_cache, p->d, p->page_size, p->Hk, p->n_pages, vs, "v_cache")) != ATTN_OK)
+  if ((rc = encode_pages(encode, &k.tm_k, p->k_cache, p->d, p->page_size, p->Hk, p->n_pages, attn::kBN, ks, "k_cache")) != ATTN_OK ||
+      (rc = encode_pages(encode, &k.tm_v, p->v_cache, p->d, p->page_size, p->Hk, p->n_pages, attn::kBN, vs, "v_cache")) != ATTN_OK)
     return rc;
   // Query tiles as boxes of a tensor map: 128 / G queries of a sequence, or all
   // queries of several sequences (batched prefix tasks). Boxes against rows

@@ -10,6 +10,11 @@
 #include "cache_checks.h"
 #include "long_kernel.h"
 
+#ifndef FULL_TILES
+#define FULL_TILES 1
+#define FULL_ROWS 64
+#endif
+
 namespace {
 
 using namespace attn::host;
@@ -148,6 +153,12 @@ int blocks_splits(const attn_long_params* p, int sms) {
   return s;
 }
 
+// attn_blocks: whether to take tiles of 128 rows.
+bool blocks_full_tiles(const attn_long_params* p, int sms) {
+  const int64_t rows = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk);
+  return rows >= FULL_ROWS && (rows + 127) / 128 * p->B * p->Hk >= FULL_TILES;
+}
+
 int this_gpu() {
   int dev = 0, sms = 0;
   const int rc = this_device(&dev, &sms);
@@ -204,7 +215,7 @@ int attn_blocks(const attn_long_params* p) {
   LongParams r;
   RopeTensor o;
   int rc = fill(p, &r, true, true, true);
-  if (rc != ATTN_OK || (rc = fill_queries(p, &r)) != ATTN_OK || (rc = fill_cache(p, &r, true, true, kRead)) != ATTN_OK ||
+  if (rc != ATTN_OK || (rc = fill_queries(p, &r)) != ATTN_OK || (rc = fill_cache(p, &r, true, true, kMapped)) != ATTN_OK ||
       (rc = check_scale(p, &r)) != ATTN_OK || (rc = need(p->blocks, "blocks")) != ATTN_OK ||
       (rc = tensor(p->o, p->o_stride, p->B, p->Hq, p->Nq, p->d, kWritten, "o", &o)) != ATTN_OK)
     return rc;
@@ -216,6 +227,17 @@ int attn_blocks(const attn_long_params* p) {
   r.o_sb = o.sb;
   r.o_sh = o.sh;
   r.o_sn = o.sn;
+  if (blocks_full_tiles(p, sms)) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+    CUtensorMap tm_k, tm_v;
+    const int64_t ks[3] = {r.kc_sp, r.kc_sh, r.kc_st}, vs[3] = {r.vc_sp, r.vc_sh, r.vc_st};
+    if ((rc = tensor_map_encoder(&encode)) != ATTN_OK ||
+        (rc = encode_pages(encode, &tm_k, r.kc, p->d, p->page_size, p->Hk, p->n_pages, attn::kBlocksBox, ks, "k_cache")) != ATTN_OK ||
+        (rc = encode_pages(encode, &tm_v, r.vc, p->d, p->page_size, p->Hk, p->n_pages, attn::kBlocksBox, vs, "v_cache")) != ATTN_OK)
+      return rc;
+    long_used(dev);
+    return done(attn::launch_blocks_tiles(r, tm_k, tm_v, p->d, stream_of(p->stream)), "attention over selected pages launch");
+  }
   r.splits = blocks_splits(p, sms);
   return done(attn::launch_blocks(r, p->d, stream_of(p->stream)), "attention over selected pages launch");
 }

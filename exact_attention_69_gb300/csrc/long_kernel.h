@@ -3,6 +3,7 @@
 // attention over selected pages (attn_blocks.cu), received weights (kv_weights.cu).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -77,7 +78,10 @@ cudaError_t launch_weights(const LongParams& p, int d, cudaStream_t s);
 // The same for many query rows (long_tiles.cu).
 cudaError_t launch_scores_tiles(const LongParams& p, int d, cudaStream_t s);
 cudaError_t launch_weights_tiles(const LongParams& p, int d, cudaStream_t s);
-// Reads and clears the current device's status word of these two.
+// Maps of the caches: boxes of min(page size, kBlocksBox) slots.
+cudaError_t launch_blocks_tiles(const LongParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int d, cudaStream_t s);
+constexpr int kBlocksBox = 64;
+// Reads and clears the current device's status word of these.
 cudaError_t long_take_status(uint32_t word[4]);
 
 // attn_blocks: rows of a tile (a group of 8 columns of the products, or two).

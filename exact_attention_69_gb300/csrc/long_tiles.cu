@@ -523,6 +523,24 @@ cudaError_t weights_tiles_dim(const LongParams& p, cudaStream_t s) {
 }
 
 }  // namespace dev
+}  // namespace attn
+
+#include "blocks_tiles.cuh"
+
+namespace attn {
+
+cudaError_t launch_blocks_tiles(const LongParams& p, const CUtensorMap& tm_k, const CUtensorMap& tm_v, int d, cudaStream_t s) {
+  dev::BlocksTiles a;
+  a.p = p;
+  a.tm_k = tm_k;
+  a.tm_v = tm_v;
+  switch (d) {
+    case 32: return dev::blocks_tiles_dim<32>(a, s);
+    case 64: return dev::blocks_tiles_dim<64>(a, s);
+    case 128: return dev::blocks_tiles_dim<128>(a, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
 
 cudaError_t launch_scores_tiles(const LongParams& p, int d, cudaStream_t s) {
   switch (d) {
