@@ -4,10 +4,10 @@
 // A CTA has 128 rows of one sequence and key head (rows r = n * G + g) and goes over the
 // pages that any of its queries selected, 64 keys at a time; two CTAs share a SM, so one's
 // products run while the other's softmax does.
-//   warps 0-3  softmax, one thread a row (a TMEM lane): whether its query selected the page
-//              is a bit in shared memory; rows that did not put zeros into P. Where no row
+//   warps 0-3  softmax, one thread a row (a TMEM lane). Whether the row's query selected the
+//              stage's page is a bit; rows that did not put zeros into P, and where no row
 //              of a warp did, nothing is computed.
-//   warp 4     loader: TMA of the pages' keys and values into two-stage rings
+//   warp 4, 6  loaders of keys and of values: TMA of the pages into two-stage rings
 //   warp 5     products: S = Q K^T, one stage ahead of O += P V (P as bf16 in TMEM over S)
 // Neighbouring queries select much the same pages, so a page is read once for (128 / G)
 // queries, and its products serve most rows. What pages those are is worked out by all
@@ -20,7 +20,8 @@
 namespace attn {
 namespace dev {
 
-constexpr int kBlocksThreads = 192, kBlocksKeys = 64, kTileWindow = 512;
+constexpr int kBlocksThreads = 224, kBlocksKeys = 64, kTileWindow = 256;
+constexpr int kWarpK = 4, kWarpMma = 5, kWarpV = 6;
 constexpr float kBlocksSlack = 8.f;
 constexpr uint32_t kBlocksCols = 256;  // TMEM: S_0 [0, 64), S_1 [64, 128) (P over their first 32), O from 128
 
@@ -40,10 +41,12 @@ struct BlocksSmem {
   static constexpr uint32_t kLayout = D >= 64 ? 2u : 4u;
 };
 
+constexpr int kWindowWords = kTileWindow / 32;
 struct BlocksLists {
-  uint32_t bits[128][kTileWindow / 32];  // of each query of the tile
-  uint32_t any[kTileWindow / 32];
-  uint16_t page[kTileWindow];            // the pages that have a bit, from the window's first
+  uint32_t bits[128][kWindowWords];  // of each query of the tile: pages of the window that it selected,
+  uint32_t took[128][kWindowWords];  // and, of the pages listed, which those are
+  uint32_t any[kWindowWords];
+  uint16_t page[kTileWindow];        // the pages that have a bit, from the window's first
   int32_t id[kTileWindow];
   uint64_t bars[13];
   uint32_t tmem;
@@ -78,80 +81,247 @@ __device__ __forceinline__ bool blocks_wait(uint32_t bar, uint32_t parity, const
   return ctl_wait(bar, parity, c, tile, kRoleTiles, honour);
 }
 
-template <int D>
+// Keys (VALUES: values) of a window's stages. One warp each: a stage's keys are done with
+// earlier than its values, and the next ones need not wait for these.
+template <int D, bool VALUES>
 __device__ __forceinline__ bool blocks_load(const BlocksTiles& a, const BlocksLists& l, uint32_t base, const BlocksBars& bars,
                                             const Stages& st, int hk, int n, int& gs, const Ctl& ctl) {
   using S = BlocksSmem<D>;
   const uint64_t pol = l2_policy_evict_last();
   for (int s = 0; s < n; ++s, ++gs) {
     const int slot = gs & 1, at = st.slot(s);
-    const uint32_t phase = ((gs >> 1) & 1) ^ 1u;
+    if (!blocks_wait(VALUES ? bars.v_empty(slot) : bars.k_empty(slot), ((gs >> 1) & 1) ^ 1u, ctl, gs)) return false;
+    const uint32_t full = VALUES ? bars.v_full(slot) : bars.k_full(slot);
+    mbar_expect_tx(full, S::kKV);
+    for (int i = 0; i < (1 << st.sub); ++i) {
+      const int e = st.entry(s, i);
+      const int id = e < l.count ? l.id[e] : -1;  // (a page that the cache has not reads as zeros)
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      if (!blocks_wait(v ? bars.v_empty(slot) : bars.k_empty(slot), phase, ctl, gs)) return false;
-      const uint32_t full = v ? bars.v_full(slot) : bars.k_full(slot);
-      mbar_expect_tx(full, S::kKV);
-      for (int i = 0; i < (1 << st.sub); ++i) {
-        const int e = st.entry(s, i);
-        const int id = e < l.count ? l.id[e] : -1;  // (a page that the cache has not reads as zeros)
-#pragma unroll
-        for (int c = 0; c < S::kChunks; ++c)
-          tma_load_4d_hint(base + (v ? S::kOffV : S::kOffK) + slot * S::kKV + c * S::kChunk + i * st.keys() * S::kRow,
-                           v ? &a.tm_v : &a.tm_k, full, c * 64, at, hk, id, pol);
-      }
+      for (int c = 0; c < S::kChunks; ++c)
+        tma_load_4d_hint(base + (VALUES ? S::kOffV : S::kOffK) + slot * S::kKV + c * S::kChunk + i * st.keys() * S::kRow,
+                         VALUES ? &a.tm_v : &a.tm_k, full, c * 64, at, hk, id, pol);
     }
   }
   return true;
 }
 
-// O += P V of stage x (the window's number xs).
+// What the warp that issues the products keeps from stage to stage.
 template <int D>
-__device__ __forceinline__ bool blocks_pv(const BlocksLists& l, uint8_t* smem, uint32_t base, const BlocksBars& bars,
-                                          const Stages& st, uint32_t tmem, int len, int w0, int xs, int x, const Ctl& ctl) {
+struct BlocksMma {
   using S = BlocksSmem<D>;
-  const int slot = x & 1;
-  const uint32_t parity = (x >> 1) & 1;
-  if (!blocks_wait(bars.v_full(slot), parity, ctl, x)) return false;
-  // values behind the sequence's end may be anything: 0 * NaN must not reach the sum
+  uint64_t q, k, v;  // descriptors of Q and of stage 0 of K and V
+  uint32_t tmem;
+  static constexpr uint64_t kStep = S::kKV >> 4;
+  __device__ __forceinline__ BlocksMma(uint32_t base, uint32_t tmem_)
+      : q(smem_desc(base, 16, 8 * S::kRow, S::kLayout)),
+        k(smem_desc(base + S::kOffK, 16, 8 * S::kRow, S::kLayout)),
+        v(smem_desc(base + S::kOffV, S::kChunk, 8 * S::kRow, S::kLayout)),
+        tmem(tmem_) {}
+  __device__ __forceinline__ void scores(int slot) const {
+    constexpr uint32_t kIdesc = make_idesc(128, kBlocksKeys, false);
+    const uint64_t ks = k + slot * kStep;
+    if constexpr (D == 32) {
+      mma_ss2<2>(tmem + slot * 64, q, ks, kIdesc, 0u);
+    } else {
+      mma_ss4<2, 4, 6>(tmem + slot * 64, q, ks, kIdesc, 0u);
+      if constexpr (D == 128)
+        mma_ss4<2, 4, 6>(tmem + slot * 64, q + (128 * S::kRow >> 4), ks + (S::kChunk >> 4), kIdesc, 1u);
+    }
+  }
+  __device__ __forceinline__ void values(int slot, bool more) const {
+    constexpr uint32_t kIdesc = make_idesc(128, D, true);
+    mma_ts4<S::kRow, 2 * S::kRow, 3 * S::kRow>(tmem + 128, tmem + slot * 64, v + slot * kStep, kIdesc, more);
+  }
+};
+
+// Zeroes the values of stage s that lie behind the sequence's end, where a page may hold
+// anything: 0 * NaN must not reach the sum.
+template <int D>
+__device__ __noinline__ void blocks_clear(const BlocksLists& l, uint8_t* values, int page_shift, int len, int w0, int s) {
+  using S = BlocksSmem<D>;
+  const Stages st(page_shift);
   for (int i = 0; i < (1 << st.sub); ++i) {
-    const int e = st.entry(xs, i);
+    const int e = st.entry(s, i);
     if (e >= l.count) break;
-    const int live = len - ((w0 + l.page[e]) << st.page_shift) - st.slot(xs);
-    if (live >= st.keys()) continue;
-    const int first = i * st.keys() + max(live, 0), rows = (i + 1) * st.keys() - first;
+    const int live = len - ((w0 + l.page[e]) << st.page_shift) - st.slot(s);
+    const int first = i * st.keys() + min(max(live, 0), st.keys()), rows = (i + 1) * st.keys() - first;
     for (int y = threadIdx.x & 31; y < rows * (D / 8); y += 32) {
       const int r = first + y / (D / 8), c = y % (D / 8);
-      *reinterpret_cast<uint4*>(smem + S::kOffV + slot * S::kKV + (c / (S::kRow / 16)) * S::kChunk + r * S::kRow +
-                                (c % (S::kRow / 16)) * 16) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(values + (c / (S::kRow / 16)) * S::kChunk + r * S::kRow + (c % (S::kRow / 16)) * 16) =
+          make_uint4(0, 0, 0, 0);
     }
-    fence_async_smem();
-    __syncwarp();
   }
-  if (!blocks_wait(bars.p_full(slot), parity, ctl, x)) return false;
-  tc_fence_after();
-  constexpr uint32_t kIdesc = make_idesc(128, D, true);
-  const uint64_t dv = smem_desc(base + S::kOffV + slot * S::kKV, S::kChunk, 8 * S::kRow, S::kLayout);
-  mma_ts4<S::kRow, 2 * S::kRow, 3 * S::kRow>(tmem + 128, tmem + slot * 64, dv, kIdesc, x > 0);
-  mma_commit(bars.o_done());
-  mma_commit(bars.v_empty(slot));
+  fence_async_smem();
+  __syncwarp();
+}
+
+// The products of a window's stages: S of one, then O += P V of the one before.
+template <int D>
+__device__ __forceinline__ bool blocks_mma(const BlocksMma<D>& mm, const BlocksLists& l, uint8_t* smem, const BlocksBars& bars,
+                                           const Stages& st, int len, int w0, int n, int& gs, const Ctl& ctl) {
+  using S = BlocksSmem<D>;
+  // only the last page listed can hold slots behind the sequence's end
+  const int last = l.count - 1, dead = ((w0 + l.page[last] + 1) << st.page_shift) > len ? (last << st.cut) >> st.sub : n;
+  for (int s = 0; s <= n; ++s) {
+    if (s < n) {
+      const int slot = gs & 1;
+      if (!blocks_wait(bars.k_full(slot), (gs >> 1) & 1, ctl, gs)) return false;
+      tc_fence_after();
+      // (S goes where stage gs - 2 had its P: that product was issued before, and read it)
+      mm.scores(slot);
+      mma_commit(bars.s_full(slot));
+      mma_commit(bars.k_empty(slot));
+      ++gs;
+    }
+    if (s > 0) {
+      const int x = gs - 1 - (s < n), slot = x & 1;
+      const uint32_t parity = (x >> 1) & 1;
+      if (!blocks_wait(bars.v_full(slot), parity, ctl, x)) return false;
+      if (s - 1 >= dead) blocks_clear<D>(l, smem + S::kOffV + slot * S::kKV, st.page_shift, len, w0, s - 1);
+      if (!blocks_wait(bars.p_full(slot), parity, ctl, x)) return false;
+      tc_fence_after();
+      mm.values(slot, x > 0);
+      mma_commit(bars.o_done());
+      mma_commit(bars.v_empty(slot));
+    }
+  }
   return true;
 }
 
+// Columns [0, 32) and [32, 64) from an address on, one wait for both.
+__device__ __forceinline__ void tmem_ld32x2(uint32_t ta, uint32_t (&a)[32], uint32_t (&b)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, "
+      "%46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%65];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]), "=r"(a[6]), "=r"(a[7]), "=r"(a[8]),
+        "=r"(a[9]), "=r"(a[10]), "=r"(a[11]), "=r"(a[12]), "=r"(a[13]), "=r"(a[14]), "=r"(a[15]), "=r"(a[16]),
+        "=r"(a[17]), "=r"(a[18]), "=r"(a[19]), "=r"(a[20]), "=r"(a[21]), "=r"(a[22]), "=r"(a[23]), "=r"(a[24]),
+        "=r"(a[25]), "=r"(a[26]), "=r"(a[27]), "=r"(a[28]), "=r"(a[29]), "=r"(a[30]), "=r"(a[31]), "=r"(b[0]),
+        "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]), "=r"(b[6]), "=r"(b[7]), "=r"(b[8]), "=r"(b[9]),
+        "=r"(b[10]), "=r"(b[11]), "=r"(b[12]), "=r"(b[13]), "=r"(b[14]), "=r"(b[15]), "=r"(b[16]), "=r"(b[17]),
+        "=r"(b[18]), "=r"(b[19]), "=r"(b[20]), "=r"(b[21]), "=r"(b[22]), "=r"(b[23]), "=r"(b[24]), "=r"(b[25]),
+        "=r"(b[26]), "=r"(b[27]), "=r"(b[28]), "=r"(b[29]), "=r"(b[30]), "=r"(b[31])
+      : "r"(ta), "r"(ta + 32u)
+      : "memory");
+}
+
+// What a softmax thread keeps of its row.
+struct BlocksRow {
+  uint32_t tl;      // TMEM address of its lane
+  int tok, seen;    // its query in the tile, and slots that it sees
+  float c;          // scale * log2(e)
+  float m, sum;     // running maximum and sum
+  uint32_t word;    // of the 32 pages listed from a multiple of 32 on, which the query selected
+};
+
+// How many of 16 columns, from slot `pos` of the sequence on, the row sees.
+__device__ __forceinline__ uint32_t blocks_limit(int seen, int pos) { return static_cast<uint32_t>(min(max(seen - pos, 0), 16)); }
+
+// The row of O times f.
 template <int D>
-__device__ __forceinline__ bool blocks_mma(const BlocksLists& l, uint8_t* smem, uint32_t base, const BlocksBars& bars,
-                                           const Stages& st, uint32_t tmem, int len, int w0, int n, int& gs, const Ctl& ctl) {
-  using S = BlocksSmem<D>;
-  for (int s = 0; s < n; ++s, ++gs) {
-    const int slot = gs & 1;
-    if (!blocks_wait(bars.k_full(slot), (gs >> 1) & 1, ctl, gs)) return false;
-    tc_fence_after();
-    // (S goes where stage gs - 2 had its P: that product was issued before, and read it)
-    issue_tile<D>(tmem + slot * 64, base, base + S::kOffK + slot * S::kKV);
-    mma_commit(bars.s_full(slot));
-    mma_commit(bars.k_empty(slot));
-    if (s > 0 && !blocks_pv<D>(l, smem, base, bars, st, tmem, len, w0, s - 1, gs - 1, ctl)) return false;
+__device__ __noinline__ void blocks_rescale(uint32_t to, float f) {
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t o[32];
+    tmem_ld32(to + c, o);
+#pragma unroll
+    for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
+    tmem_st32(to + c, o);
   }
-  return blocks_pv<D>(l, smem, base, bars, st, tmem, len, w0, n - 1, gs - 1, ctl);
+  tmem_wait_st();
+}
+
+// One stage of a row's softmax: S to P, the running maximum and sum.
+template <int D>
+__device__ __forceinline__ bool blocks_softmax(const BlocksLists& l, const BlocksBars& bars, const Stages& st, int w0, int s, int gs,
+                                               BlocksRow& r, const Ctl& ctl) {
+  const int slot = gs & 1;
+  const uint32_t ts = r.tl + slot * 64;
+  // of each 16 columns, how many the row sees: keys of pages that its query selected
+  uint32_t lim[4] = {0u, 0u, 0u, 0u};
+  if (st.sub == 0) {  // one page
+    const int e = s >> st.cut;
+    if ((e & 31) == 0) r.word = l.took[r.tok][e >> 5];
+    if ((r.word >> (e & 31)) & 1u) {
+      const int pos = ((w0 + l.page[e]) << st.page_shift) + st.slot(s);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) lim[g] = blocks_limit(r.seen, pos + 16 * g);
+    }
+  } else {  // two or four (their bits lie in one word)
+    const int e0 = s << st.sub, left = l.count - e0;
+    const uint32_t took = l.took[r.tok][e0 >> 5] >> (e0 & 31);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int i = g >> (2 - st.sub);
+      if (i < left && ((took >> i) & 1u) != 0u)
+        lim[g] = blocks_limit(r.seen, ((w0 + l.page[e0 + i]) << st.page_shift) + g * 16 - i * st.keys());
+    }
+  }
+  const uint32_t some = lim[0] | lim[1] | lim[2] | lim[3];
+  if (!blocks_wait(bars.s_full(slot), (gs >> 1) & 1, ctl, gs)) return false;
+  tc_fence_after();
+  uint32_t w[32];
+  if (__any_sync(0xffffffffu, some != 0u)) {
+    uint32_t v[2][32];
+    tmem_ld32x2(ts, v[0], v[1]);
+    if (__any_sync(0xffffffffu, (some & 15u) != 0u)) {  // (else each 16 are seen whole, or not at all)
+#pragma unroll
+      for (int x = 0; x < 64; ++x)
+        if ((x & 15) >= lim[x >> 4]) v[x >> 5][x & 31] = 0xFF800000u;
+    }
+    const auto at = [&](int x) { return __uint_as_float(v[x >> 5][x & 31]); };
+    float top = -INFINITY;
+#pragma unroll
+    for (int g = 0; g < 64; g += 16) {
+      float z = fmaxf(at(g), at(g + 15)), y = fmax3(at(g + 1), at(g + 2), at(g + 3));
+#pragma unroll
+      for (int x = g + 4; x < g + 15; x += 4) {
+        z = fmax3(z, at(x), at(x + 1));
+        y = fmax3(y, at(x + 2), x + 3 < g + 15 ? at(x + 3) : y);
+      }
+      if (lim[g >> 4] != 0u) top = fmaxf(top, fmaxf(z, y));
+    }
+    top *= r.c;
+    if (__any_sync(0xffffffffu, top > r.m + kBlocksSlack)) {
+      const float next = fmaxf(r.m, ceilf(top));
+      const float f = r.m == next ? 1.f : ex2(r.m - next);  // (m -inf: 0)
+      r.m = next;
+      r.sum *= f;
+      if (gs > 0) {
+        if (!blocks_wait(bars.o_done(), (gs - 1) & 1, ctl, gs)) return false;
+        tc_fence_after();
+        blocks_rescale<D>(r.tl + 128, f);
+      }
+    }
+    const float neg = r.m == -INFINITY ? 0.f : -r.m;
+    const ldev::F2 c2 = ldev::pair(r.c, r.c), neg2 = ldev::pair(neg, neg);
+#pragma unroll
+    for (int g = 0; g < 64; g += 16) {
+      const bool sees = lim[g >> 4] != 0u;
+      ldev::F2 part = ldev::pair(0.f, 0.f);
+#pragma unroll
+      for (int x = g; x < g + 16; x += 2) {
+        const float2 y = ldev::split(ldev::fma2(ldev::pair(at(x), at(x + 1)), c2, neg2));
+        const float e0 = ex2(y.x), e1 = ex2(y.y);  // (a score of +inf: inf - inf, NaN)
+        part = ldev::add2(part, ldev::pair(e0, e1));
+        w[x / 2] = sees ? pack_bf16(e0, e1) : 0u;
+      }
+      const float2 y = ldev::split(part);
+      r.sum += sees ? y.x + y.y : 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int x = 0; x < 32; ++x) w[x] = 0u;
+  }
+  tmem_st32(ts, w);
+  tmem_wait_st();
+  tc_fence_before();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(bars.p_full(slot));
+  return true;
 }
 
 template <int D>
@@ -179,7 +349,7 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
     prefetch_tmap(&a.tm_k);
     prefetch_tmap(&a.tm_v);
   }
-  if (warp == 5) {
+  if (warp == kWarpMma) {
     tmem_alloc(smem_u32(&l.tmem), kBlocksCols);
     tmem_relinquish();
   }
@@ -209,17 +379,22 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
                  r < rn ? 16 : 0);
   }
   ldev::copy_commit();
-  const int row = static_cast<int>(threadIdx.x), n_mine = p.by_g.div(r0 + min(row, rn - 1)), tok = n_mine - tok0;
-  const int seen = row < rn ? long_seen(p, lens, n_mine) : 0;
-  float m = -INFINITY, sum = 0.f;
-  const uint32_t lanes = static_cast<uint32_t>(warp) << 21;
+  const int row = static_cast<int>(threadIdx.x) & 127, n_mine = p.by_g.div(r0 + min(row, rn - 1));
+  BlocksRow r;
+  r.tl = tmem + (static_cast<uint32_t>(warp) << 21);
+  r.tok = n_mine - tok0;
+  r.seen = row < rn ? long_seen(p, lens, n_mine) : 0;
+  r.c = p.c_hi;
+  r.m = -INFINITY;
+  r.sum = 0.f;
+  r.word = 0;
   int gs = 0;  // stages so far
   bool ok = true;
 
   for (int w0 = 0; w0 < pages; w0 += kTileWindow) {
     __syncthreads();  // the lists of the window before are done with
-    for (int x = threadIdx.x; x < toks * (kTileWindow / 32); x += kBlocksThreads) (&l.bits[0][0])[x] = 0u;
-    if (threadIdx.x < kTileWindow / 32) l.any[threadIdx.x] = 0u;
+    for (int x = threadIdx.x; x < toks * kWindowWords; x += kBlocksThreads) (&l.bits[0][0])[x] = (&l.took[0][0])[x] = 0u;
+    if (threadIdx.x < kWindowWords) l.any[threadIdx.x] = 0u;
     __syncthreads();
     for (int x = threadIdx.x; x < toks * p.n; x += kBlocksThreads) {
       const int t = x / p.n, page = lists[x] - w0;
@@ -232,9 +407,9 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
     ldev::copy_wait<0>();
     fence_async_smem();
     __syncthreads();
-    if (warp == 0) {  // a lane has 16 pages
-      static_assert(kTileWindow == 32 * 16, "half a word of the bits a lane");
-      uint32_t mine = (l.any[lane >> 1] >> ((lane & 1) * 16)) & 0xFFFFu, at = __popc(mine);
+    if (warp == 0) {  // a lane has 8 pages
+      static_assert(kTileWindow == 32 * 8, "a byte of the bits a lane");
+      uint32_t mine = (l.any[lane >> 2] >> ((lane & 3) * 8)) & 0xFFu, at = __popc(mine);
 #pragma unroll
       for (int s = 1; s < 32; s *= 2) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, at, s);
@@ -242,147 +417,74 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
       }
       if (lane == 31) l.count = static_cast<int>(at);
       at -= __popc(mine);
-      for (; mine != 0u; mine &= mine - 1, ++at) l.page[at] = static_cast<uint16_t>(lane * 16 + __ffs(mine) - 1);
+      for (; mine != 0u; mine &= mine - 1, ++at) l.page[at] = static_cast<uint16_t>(lane * 8 + __ffs(mine) - 1);
     }
     __syncthreads();
-    for (int x = threadIdx.x; x < l.count; x += kBlocksThreads) l.id[x] = p.table[b * p.table_sb + w0 + l.page[x]];
+    const int count = l.count;
+    for (int x = threadIdx.x; x < count; x += kBlocksThreads) l.id[x] = p.table[b * p.table_sb + w0 + l.page[x]];
+    // a query's bits in the order of the list: eight pages a thread at a time
+    const int eights = (count + 7) >> 3;
+    for (int x = threadIdx.x; x < toks * eights; x += kBlocksThreads) {
+      const int t = x / eights, e0 = (x - t * eights) * 8;
+      uint32_t z = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int page = l.page[e0 + e];  // (behind the list: any page of the window, or a value left there)
+        if (e0 + e < count) z |= ((l.bits[t][page >> 5] >> (page & 31)) & 1u) << e;
+      }
+      reinterpret_cast<uint8_t*>(l.took[t])[e0 >> 3] = static_cast<uint8_t>(z);
+    }
     __syncthreads();
-    const int n = st.count(l.count);
+    const int n = st.count(count);
     if (n > 0) {
-      if (warp == 4) {
-        ok = blocks_load<D>(a, l, base, bars, st, hk, n, gs, ctl);
-      } else if (warp == 5) {
-        ok = blocks_mma<D>(l, smem, base, bars, st, tmem, lens.len, w0, n, gs, ctl);
+      if (warp == kWarpK) {
+        ok = blocks_load<D, false>(a, l, base, bars, st, hk, n, gs, ctl);
+      } else if (warp == kWarpV) {
+        ok = blocks_load<D, true>(a, l, base, bars, st, hk, n, gs, ctl);
+      } else if (warp == kWarpMma) {
+        ok = blocks_mma<D>(BlocksMma<D>(base, tmem), l, smem, bars, st, lens.len, w0, n, gs, ctl);
       } else {
-        for (int s = 0; s < n; ++s, ++gs) {
-          const int slot = gs & 1;
-          // of each 16 columns, how many the row sees: keys of pages that its query selected
-          int lim[4];
-          bool some = false, even = true;
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int i = g >> (2 - st.sub), e = st.entry(s, i);  // (sub 0: all of the one page; 1: two; 2: four)
-            lim[g] = 0;
-            if (e < l.count) {
-              const int page = l.page[e];
-              const int pos = ((w0 + page) << st.page_shift) + st.slot(s) + (g * 16 - i * st.keys());
-              if ((l.bits[tok][page >> 5] >> (page & 31)) & 1u) lim[g] = min(max(seen - pos, 0), 16);
-            }
-            some |= lim[g] > 0;
-            even &= lim[g] == 0 || lim[g] == 16;
-          }
-          ok = blocks_wait(bars.s_full(slot), (gs >> 1) & 1, ctl, gs);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t ts = tmem + lanes + slot * 64;
-          uint32_t w[32];
-          if (!__any_sync(0xffffffffu, some)) {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) w[x] = 0u;
-          } else {
-            uint32_t v[2][32];
-            tmem_ld32(ts, v[0]);
-            tmem_ld32(ts + 32, v[1]);
-            const auto at = [&](int c) -> uint32_t& { return v[c >> 5][c & 31]; };
-            if (!__all_sync(0xffffffffu, even)) {
-#pragma unroll
-              for (int c = 0; c < 64; ++c)
-                if ((c & 15) >= lim[c >> 4]) at(c) = 0xFF800000u;
-            }
-            float top = -INFINITY;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              float z = __uint_as_float(at(16 * g));
-#pragma unroll
-              for (int c = 1; c < 15; c += 2) z = fmax3(z, __uint_as_float(at(16 * g + c)), __uint_as_float(at(16 * g + c + 1)));
-              z = fmaxf(z, __uint_as_float(at(16 * g + 15)));
-              top = fmaxf(top, lim[g] > 0 ? z : -INFINITY);
-            }
-            top *= p.c_hi;
-            if (__any_sync(0xffffffffu, top > m + kBlocksSlack)) {
-              const float next = fmaxf(m, ceilf(top));
-              const float f = m == next ? 1.f : ex2(m - next);  // (m -inf: 0)
-              m = next;
-              sum *= f;
-              if (gs > 0) {
-                ok = blocks_wait(bars.o_done(), (gs - 1) & 1, ctl, gs);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll 1
-                for (int c = 0; c < D; c += 32) {
-                  uint32_t o[32];
-                  tmem_ld32(tmem + lanes + 128 + c, o);
-#pragma unroll
-                  for (int x = 0; x < 32; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-                  tmem_st32(tmem + lanes + 128 + c, o);
-                }
-                tmem_wait_st();
-              }
-            }
-            const float neg = m == -INFINITY ? 0.f : -m;
-            const ldev::F2 c2 = ldev::pair(p.c_hi, p.c_hi), neg2 = ldev::pair(neg, neg);
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              ldev::F2 part = ldev::pair(0.f, 0.f);
-#pragma unroll
-              for (int c = 16 * g; c < 16 * g + 16; c += 2) {
-                const float2 x = ldev::split(ldev::fma2(ldev::pair(__uint_as_float(at(c)), __uint_as_float(at(c + 1))), c2, neg2));
-                const float e0 = ex2(x.x), e1 = ex2(x.y);  // (a score of +inf: inf - inf, NaN)
-                part = ldev::add2(part, ldev::pair(e0, e1));
-                w[c / 2] = lim[g] > 0 ? pack_bf16(e0, e1) : 0u;
-              }
-              const float2 y = ldev::split(part);
-              sum += lim[g] > 0 ? y.x + y.y : 0.f;
-            }
-          }
-          tmem_st32(ts, w);
-          tmem_wait_st();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bars.p_full(slot));
-        }
+        for (int s = 0; s < n && ok; ++s, ++gs) ok = blocks_softmax<D>(l, bars, st, w0, s, gs, r, ctl);
       }
     }
     if (__syncthreads_or(!ok)) break;
   }
 
-  if (ok && gs > 0 && warp < 4) {
-    ok = blocks_wait(bars.o_done(), (gs - 1) & 1, ctl, gs);
-    tc_fence_after();
-  }
   if (warp < 4) {
+    if (ok && gs > 0) {
+      ok = blocks_wait(bars.o_done(), (gs - 1) & 1, ctl, gs);
+      tc_fence_after();
+    }
     const int g = r0 + row - n_mine * G, h = hk * G + g;
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float inv = r.sum == 0.f ? 0.f : 1.f / r.sum;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + b * p.o_sb + h * p.o_sh + n_mine * p.o_sn;
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       uint32_t o[32];
-      if (gs > 0) tmem_ld32(tmem + lanes + 128 + c, o);
+      if (gs > 0) tmem_ld32(r.tl + 128 + c, o);
       if (row < rn) {
 #pragma unroll
         for (int x = 0; x < 32; x += 8) {
           uint32_t y[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i)
-            y[i] = sum == 0.f ? 0u : pack_bf16(__uint_as_float(o[x + 2 * i]) * inv, __uint_as_float(o[x + 2 * i + 1]) * inv);
+            y[i] = r.sum == 0.f ? 0u : pack_bf16(__uint_as_float(o[x + 2 * i]) * inv, __uint_as_float(o[x + 2 * i + 1]) * inv);
           *reinterpret_cast<uint4*>(out + c + x) = make_uint4(y[0], y[1], y[2], y[3]);
         }
       }
     }
     if (row < rn && p.lse != nullptr)
-      p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Nq + n_mine] = CUDART_LN2_F * (m + log2f(sum));
+      p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Nq + n_mine] = CUDART_LN2_F * (r.m + log2f(r.sum));
   }
-  if (l.abort != 0u && warp == 4) {
+  if (l.abort != 0u && (warp == kWarpK || warp == kWarpV)) {
     // copies in flight land in this CTA's shared memory: wait (bounded) for the last ones
-    for (int x = max(gs - 1, 0); x <= gs; ++x) {
-      blocks_wait(bars.k_full(x & 1), (x >> 1) & 1, ctl, x, false);
-      blocks_wait(bars.v_full(x & 1), (x >> 1) & 1, ctl, x, false);
-    }
+    for (int x = max(gs - 2, 0); x < gs; ++x)
+      blocks_wait(warp == kWarpV ? bars.v_full(x & 1) : bars.k_full(x & 1), (x >> 1) & 1, ctl, x, false);
   }
   ldev::copy_wait<0>();  // (no page, no wait so far)
   tc_fence_before();
   __syncthreads();
-  if (warp == 5) tmem_dealloc(tmem, kBlocksCols);
+  if (warp == kWarpMma) tmem_dealloc(tmem, kBlocksCols);
 }
 
 template <int D>

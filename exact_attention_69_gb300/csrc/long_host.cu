@@ -10,11 +10,6 @@
 #include "cache_checks.h"
 #include "long_kernel.h"
 
-#ifndef FULL_TILES
-#define FULL_TILES 1
-#define FULL_ROWS 64
-#endif
-
 namespace {
 
 using namespace attn::host;
@@ -153,10 +148,26 @@ int blocks_splits(const attn_long_params* p, int sms) {
   return s;
 }
 
-// attn_blocks: whether to take tiles of 128 rows.
+// attn_blocks: whether to take tiles of 128 rows. Such a tile reads a page once for up to
+// 128 rows, but goes over its pages one after the other; groups of 16 rows are eight times
+// as many tasks. So: 64 rows of a sequence and key head, and 48 a SM in all. Measured (us;
+// 32 of 256 pages of 64 a query, d = 128, G = 4 unless said; queries that select much the
+// same pages, and pages at random), tiles of 128 and of 16 rows:
+//   8 sequences x 8 key heads, 8 queries (14 rows a SM)   38 / 122   35 /  81
+//                              16        (27)             45 / 166   58 / 141
+//                              32        (54)             57 / 185  102 / 247
+//                             128        (216)            67 / 211  328 / 793
+//   1 x 8, 64 queries (14 rows a SM)                      47 / 157   30 /  66
+//         128         (27)                                48 / 162   50 / 119
+//         512         (108)                               55 / 196  180 / 433
+//   1 x 1, G = 8, 512 queries (27)                        40 / 140   45 /  68
+//   16 x 4, G = 7, 16 queries, d = 32 (47)                24 /  81   20 /  44
+//   4 x 4, G = 1, 512 queries, d = 64, 64 pages of 16 (54)  55 / 118   48 / 173
+constexpr int kFullTileRows = 64, kFullRowsPerSm = 48;
+
 bool blocks_full_tiles(const attn_long_params* p, int sms) {
   const int64_t rows = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk);
-  return rows >= FULL_ROWS && (rows + 127) / 128 * p->B * p->Hk >= FULL_TILES;
+  return rows >= kFullTileRows && rows * p->B * p->Hk >= static_cast<int64_t>(kFullRowsPerSm) * sms;
 }
 
 int this_gpu() {
