@@ -175,7 +175,8 @@ class AttnLongParams(ctypes.Structure):
         + [(n, ctypes.c_int) for n in ("n", "first", "last", "n_new")]
         + [("scale", ctypes.c_float), ("decay", ctypes.c_float), ("mask_kind", ctypes.c_int)]
         + [(n, ctypes.c_int64 * 3) for n in ("q_stride", "o_stride", "k_cache_stride", "v_cache_stride")]
-        + [("stream", ctypes.c_void_p)])
+        + [("stream", ctypes.c_void_p), ("full_tiles", ctypes.c_int), ("timeout_ns", ctypes.c_uint64),
+           ("inject", ctypes.c_int)])
 
 
 LONG_CALLS = ("attn_kv_bounds", "attn_block_scores", "attn_block_select", "attn_blocks", "attn_kv_weights",

@@ -222,7 +222,7 @@ cudaError_t launch_bounds(const LongParams& p, int d, cudaStream_t s) {
 }
 
 cudaError_t launch_scores(const LongParams& p, int d, cudaStream_t s) {
-  if (static_cast<int64_t>(p.Nq) * padded_heads(p.G) > kFewRows) return launch_scores_tiles(p, d, s);
+  if (p.full_tiles == 1 || static_cast<int64_t>(p.Nq) * padded_heads(p.G) > kFewRows) return launch_scores_tiles(p, d, s);
   switch (d) {
     case 32: return scores_dim<32>(p, s);
     case 64: return scores_dim<64>(p, s);

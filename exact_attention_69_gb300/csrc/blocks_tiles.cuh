@@ -92,6 +92,7 @@ __device__ __forceinline__ bool blocks_load(const BlocksTiles& a, const BlocksLi
     const int slot = gs & 1, at = st.slot(s);
     if (!blocks_wait(VALUES ? bars.v_empty(slot) : bars.k_empty(slot), ((gs >> 1) & 1) ^ 1u, ctl, gs)) return false;
     const uint32_t full = VALUES ? bars.v_full(slot) : bars.k_full(slot);
+    if (!VALUES && gs == 0 && a.p.inject == 1) continue;
     mbar_expect_tx(full, S::kKV);
     for (int i = 0; i < (1 << st.sub); ++i) {
       const int e = st.entry(s, i);
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = l.tmem;
-  const Ctl ctl{&l.abort, g_long_status, 2000000000ull};
+  const Ctl ctl{&l.abort, g_long_status, p.timeout_ns};
   ldev::grid_dep_launch();
   ldev::grid_dep_wait();
 
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
   }
   if (l.abort != 0u && (warp == kWarpK || warp == kWarpV)) {
     // copies in flight land in this CTA's shared memory: wait (bounded) for the last ones
-    for (int x = max(gs - 2, 0); x < gs; ++x)
+    for (int x = max(gs - 2, p.inject); x < gs; ++x)  // (what inject withheld never comes)
       blocks_wait(warp == kWarpV ? bars.v_full(x & 1) : bars.k_full(x & 1), (x >> 1) & 1, ctl, x, false);
   }
   ldev::copy_wait<0>();  // (no page, no wait so far)

@@ -146,7 +146,7 @@ cudaError_t weights_dim(const LongParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_weights(const LongParams& p, int d, cudaStream_t s) {
-  if (static_cast<int64_t>(p.Nq) * p.G > kFewRows) return launch_weights_tiles(p, d, s);
+  if (p.full_tiles == 1 || static_cast<int64_t>(p.Nq) * p.G > kFewRows) return launch_weights_tiles(p, d, s);
   switch (d) {
     case 32: return weights_dim<32>(p, s);
     case 64: return weights_dim<64>(p, s);

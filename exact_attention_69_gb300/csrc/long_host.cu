@@ -83,6 +83,11 @@ int fill(const attn_long_params* p, LongParams* r, bool queries, bool heads, boo
   r->last = p->last;
   r->n_new = p->n_new;
   r->decay = p->decay;
+  if (p->full_tiles < 0 || p->full_tiles > 2 || p->inject < 0 || p->inject > 1)
+    return fail_with(ATTN_ERR_INVALID_ARG, "full_tiles must be 0 to 2, inject 0 or 1");
+  r->full_tiles = p->full_tiles;
+  r->timeout_ns = p->timeout_ns ? p->timeout_ns : kTimeoutNs;
+  r->inject = p->inject;
   return ATTN_OK;
 }
 
@@ -166,6 +171,7 @@ int blocks_splits(const attn_long_params* p, int sms) {
 constexpr int kFullTileRows = 64, kFullRowsPerSm = 48;
 
 bool blocks_full_tiles(const attn_long_params* p, int sms) {
+  if (p->full_tiles != 0) return p->full_tiles == 1;
   const int64_t rows = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk);
   return rows >= kFullTileRows && rows * p->B * p->Hk >= static_cast<int64_t>(kFullRowsPerSm) * sms;
 }

@@ -46,6 +46,9 @@ struct LongParams {
   float scale;                  // of the scores
   float c_hi, c_lo;             // scale * log2(e), the fp32 value and what it leaves
   float decay;
+  int full_tiles;               // 0: by the rule, 1: tiles of 128 rows, 2: the form for few rows
+  uint64_t timeout_ns;          // tiles of 128 rows: bound on every wait
+  int inject;                   // 1: withhold something once (tests the bounded wait)
   int splits;                   // CTAs (a cluster) that share a row tile's pages
 };
 

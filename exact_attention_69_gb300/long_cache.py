@@ -82,11 +82,25 @@ def _queries(p, q, device, mask, scale):
     p.scale = float(1.0 / math.sqrt(p.d) if scale is None else scale)
 
 
+_calls: dict = {}
+
+
 def _call(name, p, handle):
     p.stream = handle
-    code = getattr(_lib.load(), name)(ctypes.byref(p))
+    f = _calls.get(name)
+    if f is None:
+        f = _calls[name] = getattr(_lib.load(), name)
+    code = f(ctypes.byref(p))
     if code:
         _lib.check(code, name.replace("attn_kv", "kv").replace("attn_block_", "block_"))
+
+
+def _form(p, full_tiles, timeout_ns, inject):
+    """The fields of the calls that have a form with tiles of 128 rows."""
+    if timeout_ns < 0:
+        raise ValueError("timeout_ns must be >= 0")
+    p.full_tiles = 0 if full_tiles is None else 1 if full_tiles else 2
+    p.timeout_ns, p.inject = _fits("timeout_ns", timeout_ns, 64), _fits("inject", inject)
 
 
 def _cuda(t, name):
@@ -132,8 +146,10 @@ def kv_bounds(k_cache: torch.Tensor, bounds: torch.Tensor, block_table: torch.Te
     _on(k_cache.device, stream, (k_cache, bounds, block_table, kv_lens), run)
 
 
-def _plan_scores(q, bounds, block_table, kv_lens, page_size, q_lens, scale, mask, out):
+def _plan_scores(q, bounds, block_table, kv_lens, page_size, q_lens, scale, mask, out, full_tiles, timeout_ns, inject):
     p = _lib.AttnLongParams()
+    _fits("page_size", page_size)
+    _form(p, full_tiles or None, timeout_ns, inject)
     device = _cuda(bounds, "bounds")
     if bounds.dim() != 4:
         raise ValueError("bounds must be [n_pages, Hk, 2, d]")
@@ -149,20 +165,24 @@ def _plan_scores(q, bounds, block_table, kv_lens, page_size, q_lens, scale, mask
 
 def block_scores(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor, *,
                  page_size: int, q_lens: torch.Tensor | None = None, scale: float | None = None,
-                 mask: str = "causal_br", out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+                 mask: str = "causal_br", out: torch.Tensor | None = None, full_tiles: bool | None = None,
+                 timeout_ns: int = 0, inject: int = 0, stream=None) -> torch.Tensor:
     """How large a score each page's keys can have with each query, from kv_bounds.
 
     Returns fp32 [B, Hk, Nq, width of the table]: the largest over the query heads of a
     key head of scale * sum_c (min(q_c, 0) lower_c + max(q_c, 0) upper_c), -inf for pages
-    of which the query sees nothing. scale None: 1 / sqrt(d).
+    of which the query sees nothing. scale None: 1 / sqrt(d). full_tiles, timeout_ns and
+    inject: as attn_blocks has them.
     """
-    page_size = _fits("page_size", int(page_size))
+    page_size, timeout_ns, inject = int(page_size), int(timeout_ns), int(inject)
     scale = None if scale is None else float(scale)
+    full_tiles = None if full_tiles is None else bool(full_tiles)
     key = ("scores", _sig(q), _sig(bounds), _sig(block_table), _sig(kv_lens), page_size, _sig(q_lens), scale, mask,
-           _sig(out))
+           _sig(out), full_tiles, timeout_ns, inject)
     plan = _plans.get(key)
     if plan is None:
-        plan = _remember(key, _plan_scores(q, bounds, block_table, kv_lens, page_size, q_lens, scale, mask, out))
+        plan = _remember(key, _plan_scores(q, bounds, block_table, kv_lens, page_size, q_lens, scale, mask, out, full_tiles,
+                                           timeout_ns, inject))
     p = _lib.AttnLongParams.from_buffer_copy(plan[0])
     p.q, p.bounds, p.block_table, p.kv_lens = (t.data_ptr() for t in (q, bounds, block_table, kv_lens))
     p.q_lens = _ptr(q_lens)
@@ -180,6 +200,10 @@ def block_scores(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
 
 def _plan_select(scores, kv_lens, n, page_size, q_lens, first, last, mask, out):
     p = _lib.AttnLongParams()
+    for name, x in (("n", n), ("page_size", page_size), ("first", first), ("last", last)):
+        _fits(name, x)
+    if n < 1 or first < 0 or last < 0 or first + last > n:
+        raise ValueError("n must be >= 1, first and last >= 0 and no more than n together")
     device = _cuda(scores, "scores")
     if scores.dim() != 4:
         raise ValueError("scores must be [B, Hk, Nq, pages]")
@@ -204,10 +228,7 @@ def block_select(scores: torch.Tensor, kv_lens: torch.Tensor, n: int, *, page_si
     all; every one if it sees no more. Ties go to the lowest page, NaN counts as the
     greatest score.
     """
-    n, page_size, first, last = (_fits(a, int(x)) for a, x in (("n", n), ("page_size", page_size), ("first", first),
-                                                             ("last", last)))
-    if n < 1 or first < 0 or last < 0 or first + last > n:
-        raise ValueError("n must be >= 1, first and last >= 0 and no more than n together")
+    n, page_size, first, last = int(n), int(page_size), int(first), int(last)
     key = ("select", _sig(scores), _sig(kv_lens), n, page_size, _sig(q_lens), first, last, mask, _sig(out))
     plan = _plans.get(key)
     if plan is None:
@@ -226,8 +247,10 @@ def block_select(scores: torch.Tensor, kv_lens: torch.Tensor, n: int, *, page_si
     return _on(scores.device, stream, (scores, kv_lens, q_lens, out), run)
 
 
-def _plan_blocks(q, k_cache, v_cache, block_table, kv_lens, blocks, q_lens, scale, mask, out, lse):
+def _plan_blocks(q, k_cache, v_cache, block_table, kv_lens, blocks, q_lens, scale, mask, out, lse, full_tiles,
+                 timeout_ns, inject):
     p = _lib.AttnLongParams()
+    _form(p, full_tiles, timeout_ns, inject)
     _pages(p, "k_cache", k_cache)
     p.k_cache_stride[:] = _heads("k_cache", k_cache)
     p.v_cache_stride[:] = _heads("v_cache", v_cache, k_cache.shape)
@@ -249,7 +272,8 @@ def _plan_blocks(q, k_cache, v_cache, block_table, kv_lens, blocks, q_lens, scal
 def attn_blocks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
                 kv_lens: torch.Tensor, blocks: torch.Tensor, *, q_lens: torch.Tensor | None = None,
                 scale: float | None = None, mask: str = "causal_br", out: torch.Tensor | None = None,
-                lse: torch.Tensor | None = None, return_lse: bool = True, stream=None):
+                lse: torch.Tensor | None = None, return_lse: bool = True, full_tiles: bool | None = None,
+                timeout_ns: int = 0, inject: int = 0, stream=None):
     """Attention of each query over the pages that it selected.
 
     As attn_paged over the whole cache, but query i of a key head's query heads sees only
@@ -257,17 +281,20 @@ def attn_blocks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     sequence's row in the block table, in any order; a page named twice counts once,
     negative entries and pages of which the query sees nothing not at all). A row without
     a slot gives 0 and an LSE of -inf. Values of slots that only some queries of a
-    sequence read must be finite.
+    sequence read must be finite. full_tiles: None for the library's choice by sizes, True
+    for tiles of 128 rows, False for the form for few rows; timeout_ns: bound on every wait
+    on the device (0: two seconds; device_status says if one ran out); inject: test hook.
 
     Returns (o, lse) or o; no gradient goes through it.
     """
-    scale = None if scale is None else float(scale)
+    scale, timeout_ns, inject = None if scale is None else float(scale), int(timeout_ns), int(inject)
+    full_tiles = None if full_tiles is None else bool(full_tiles)
     key = ("blocks", _sig(q), _sig(k_cache), _sig(v_cache), _sig(block_table), _sig(kv_lens), _sig(blocks),
-           _sig(q_lens), scale, mask, _sig(out), _sig(lse))
+           _sig(q_lens), scale, mask, _sig(out), _sig(lse), full_tiles, timeout_ns, inject)
     plan = _plans.get(key)
     if plan is None:
         plan = _remember(key, _plan_blocks(q, k_cache, v_cache, block_table, kv_lens, blocks, q_lens, scale, mask, out,
-                                           lse))
+                                           lse, full_tiles, timeout_ns, inject))
     device = q.device
     p = _lib.AttnLongParams.from_buffer_copy(plan)
     p.q, p.k_cache, p.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
@@ -288,8 +315,12 @@ def attn_blocks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     return _on(device, stream, (q, k_cache, v_cache, block_table, kv_lens, blocks, q_lens, out, lse), run)
 
 
-def _plan_weights(q, k_cache, block_table, kv_lens, lse, weights, q_lens, scale, mask, decay, out):
+def _plan_weights(q, k_cache, block_table, kv_lens, lse, weights, q_lens, scale, mask, decay, out, full_tiles, timeout_ns,
+                  inject):
     p = _lib.AttnLongParams()
+    if not (math.isfinite(decay) and decay >= 0):
+        raise ValueError("decay must be finite and >= 0")
+    _form(p, full_tiles or None, timeout_ns, inject)
     _pages(p, "k_cache", k_cache)
     p.k_cache_stride[:] = _heads("k_cache", k_cache)
     device = k_cache.device
@@ -306,7 +337,7 @@ def _plan_weights(q, k_cache, block_table, kv_lens, lse, weights, q_lens, scale,
 def kv_weights(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor, kv_lens: torch.Tensor,
                lse: torch.Tensor, weights: torch.Tensor, *, q_lens: torch.Tensor | None = None, decay: float = 1.0,
                scale: float | None = None, mask: str = "causal_br", out: torch.Tensor | None = None,
-               stream=None) -> None:
+               full_tiles: bool | None = None, timeout_ns: int = 0, inject: int = 0, stream=None) -> None:
     """Adds the attention that cached tokens received from these queries to their weights.
 
     weights [n_pages, Hk, page_size] fp32, in place (or into `out`, for the slots that the
@@ -315,17 +346,17 @@ def kv_weights(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor
     attn_paged (a shared prefix counted in) or attn_blocks returned for the same queries.
     With 'causal_br' the queries' own slots are new and start from zero, whatever a
     recycled page held; with decay 0 all slots do. Sums are fp32 in a fixed order.
+    full_tiles, timeout_ns and inject: as attn_blocks has them.
     """
-    decay = float(decay)
-    if not (math.isfinite(decay) and decay >= 0):
-        raise ValueError("decay must be finite and >= 0")
+    decay, timeout_ns, inject = float(decay), int(timeout_ns), int(inject)
     scale = None if scale is None else float(scale)
+    full_tiles = None if full_tiles is None else bool(full_tiles)
     key = ("weights", _sig(q), _sig(k_cache), _sig(block_table), _sig(kv_lens), _sig(lse), _sig(weights), _sig(q_lens),
-           scale, mask, decay, _sig(out))
+           scale, mask, decay, _sig(out), full_tiles, timeout_ns, inject)
     plan = _plans.get(key)
     if plan is None:
         plan = _remember(key, _plan_weights(q, k_cache, block_table, kv_lens, lse, weights, q_lens, scale, mask, decay,
-                                            out))
+                                            out, full_tiles, timeout_ns, inject))
     p = _lib.AttnLongParams.from_buffer_copy(plan)
     p.q, p.k_cache, p.block_table, p.kv_lens = (t.data_ptr() for t in (q, k_cache, block_table, kv_lens))
     p.lse, p.weights, p.q_lens = lse.data_ptr(), weights.data_ptr(), _ptr(q_lens)
@@ -341,6 +372,10 @@ def kv_weights(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor
 
 def _plan_evict(k_cache, v_cache, weights, block_table, kv_lens, budget, first, last, dst_table):
     p = _lib.AttnLongParams()
+    for name, x in (("budget", budget), ("first", first), ("last", last)):
+        _fits(name, x)
+    if budget < 1 or first < 0 or last < 0 or first + last > budget:
+        raise ValueError("budget must be >= 1, first and last >= 0 and no more than budget together")
     _pages(p, "k_cache", k_cache)
     p.k_cache_stride[:] = _heads("k_cache", k_cache)
     p.v_cache_stride[:] = _heads("v_cache", v_cache, k_cache.shape)
@@ -369,9 +404,7 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor
     heads keep different tokens: give kv_append the tokens' true positions from then on,
     and find the pages' bounds again (kv_bounds) where they are used.
     """
-    budget, first, last = (_fits(a, int(x)) for a, x in (("budget", budget), ("first", first), ("last", last)))
-    if budget < 1 or first < 0 or last < 0 or first + last > budget:
-        raise ValueError("budget must be >= 1, first and last >= 0 and no more than budget together")
+    budget, first, last = int(budget), int(first), int(last)
     key = ("evict", _sig(k_cache), _sig(v_cache), _sig(weights), _sig(block_table), _sig(kv_lens), budget, first, last,
            _sig(dst_table))
     plan = _plans.get(key)

@@ -539,6 +539,11 @@ typedef struct attn_long_params {
   int64_t q_stride[3], o_stride[3];             /* elements, (b, h, n); zero = contiguous */
   int64_t k_cache_stride[3], v_cache_stride[3]; /* pages, heads, slots; zero = contiguous */
   void* stream;
+  int full_tiles;             /* attn_blocks, attn_block_scores, attn_kv_weights: 0 = the library's rule,
+                               * 1 = tiles of 128 rows, 2 = the form for few rows (attn_blocks only);
+                               * other values than 0 are for tests */
+  uint64_t timeout_ns;        /* bound on every device-side wait of these; 0 = 2 seconds */
+  int inject;                 /* test hook, as attn_params_ex.inject (tiles of 128 rows) */
 } attn_long_params;
 
 void attn_long_params_init(attn_long_params* p);

@@ -32,6 +32,17 @@ def ints(x):
     return torch.tensor(x, dtype=torch.int32)
 
 
+def done(E):
+    """Nothing that a device wait ran out for."""
+    torch.cuda.synchronize()
+    code, detail = E.device_status()
+    assert code == 0, detail
+
+
+# by the library's rule, and with tiles of 128 rows whatever the sizes
+FORMS = pytest.mark.parametrize("full", [None, True], ids=["rule", "full"])
+
+
 class Problem:
     """Inputs on the CPU: shuffled pages, NaN in every slot that no sequence holds, unused
     table entries that name no page."""
@@ -79,29 +90,32 @@ class Problem:
 
     def check_blocks(self, E, lists, mask="causal_br", **kw):
         o, lse = self.run_blocks(E, lists, mask, **kw)
+        done(E)
         ro, bo, rl, bl = O.blocks(self.q, self.k0(), self.v.nan_to_num(0.0), self.table, self.lens, lists, self.q_lens,
                                   self.scale, mask)
         check("o", o, ro, bo)
         check("lse", lse, rl, bl)
 
-    def check_scores(self, E, mask="causal_br"):
+    def check_scores(self, E, mask="causal_br", **kw):
         bnd = torch.zeros(self.n_pages, self.Hk, 2, self.d, dtype=torch.bfloat16)
         got = bnd.cuda()
         E.kv_bounds(self.k.cuda(), got, self.table.cuda(), self.lens.cuda())
         want = O.bounds(self.k, bnd, self.table, self.lens, None)
         assert torch.equal(got.cpu(), want)
         s = E.block_scores(self.q.cuda(), got, self.table.cuda(), self.lens.cuda(), page_size=self.page,
-                           q_lens=None if self.q_lens is None else self.q_lens.cuda(), mask=mask)
+                           q_lens=None if self.q_lens is None else self.q_lens.cuda(), mask=mask, **kw)
+        done(E)
         check("scores", s, *O.scores(self.q, want, self.table, self.lens, self.q_lens, self.page, self.scale, mask))
         return s
 
-    def check_weights(self, E, mask="causal_br", decay=1.0, lse=None):
+    def check_weights(self, E, mask="causal_br", decay=1.0, lse=None, **kw):
         if lse is None:
             k, g = self.k0(), torch.Generator().manual_seed(9)
             lse = 2 + torch.rand(self.q.shape[:3], generator=g)
         got = self.w.cuda()
         E.kv_weights(self.q.cuda(), self.k.cuda(), self.table.cuda(), self.lens.cuda(), lse.cuda(), got,
-                     q_lens=None if self.q_lens is None else self.q_lens.cuda(), mask=mask, decay=decay)
+                     q_lens=None if self.q_lens is None else self.q_lens.cuda(), mask=mask, decay=decay, **kw)
+        done(E)
         ref, err = O.weights(self.q, self.k0(), self.table, self.lens, lse, self.w, self.q_lens, self.scale, mask, decay)
         nan = ref.isnan()
         assert torch.equal(got.cpu().isnan(), nan)
@@ -129,28 +143,31 @@ CASES = [
 ]
 
 
+@FORMS
 @pytest.mark.parametrize("mask", ["causal_br", "none"])
 @pytest.mark.parametrize("case", CASES, ids=str)
-def test_scores(E, case, mask):
+def test_scores(E, case, mask, full):
     Hq, Hk, d, Nq, lens, page, q_lens = case
-    Problem(Hq, Hk, d, Nq, lens, page, q_lens, seed=100).check_scores(E, mask)
+    Problem(Hq, Hk, d, Nq, lens, page, q_lens, seed=100).check_scores(E, mask, full_tiles=full)
 
 
+@FORMS
 @pytest.mark.parametrize("mask", ["causal_br", "none"])
 @pytest.mark.parametrize("n", [1, 5, 40])
 @pytest.mark.parametrize("case", CASES, ids=str)
-def test_blocks(E, case, n, mask):
+def test_blocks(E, case, n, mask, full):
     Hq, Hk, d, Nq, lens, page, q_lens = case
     p = Problem(Hq, Hk, d, Nq, lens, page, q_lens, seed=200)
-    p.check_blocks(E, p.lists(n, seed=n), mask)
+    p.check_blocks(E, p.lists(n, seed=n), mask, full_tiles=full)
 
 
+@FORMS
 @pytest.mark.parametrize("mask", ["causal_br", "none"])
 @pytest.mark.parametrize("decay", [0.0, 1.0, 0.5])
 @pytest.mark.parametrize("case", CASES, ids=str)
-def test_weights(E, case, decay, mask):
+def test_weights(E, case, decay, mask, full):
     Hq, Hk, d, Nq, lens, page, q_lens = case
-    Problem(Hq, Hk, d, Nq, lens, page, q_lens, seed=300).check_weights(E, mask, decay)
+    Problem(Hq, Hk, d, Nq, lens, page, q_lens, seed=300).check_weights(E, mask, decay, full_tiles=full)
 
 
 @pytest.mark.parametrize("n_new", [0, 1, 2, 16, 17, 33, 1000])
@@ -179,16 +196,24 @@ def test_bounds_of_nan_and_infinities(E):
     assert took.tolist() == [[[[1, 2]]]]
 
 
+@FORMS
 @pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 8, 11, 16, 24, 70])
-def test_scores_of_head_groups(E, G):
-    Problem(2 * G, 2, 32, 9, [100, 300], 16, seed=420 + G).check_scores(E)
+def test_scores_of_head_groups(E, G, full):
+    Problem(2 * G, 2, 32, 9, [100, 300], 16, seed=420 + G).check_scores(E, full_tiles=full)
 
 
-def test_scores_of_negative_queries(E):
+def test_scores_of_many_pages_and_tokens(E):
+    """Several tiles of pages and several runs of tokens."""
+    Problem(4, 1, 64, 200, [16 * 300, 16 * 140], 16, [200, 77], seed=430).check_scores(E)
+    Problem(6, 2, 128, 90, [16 * 200 + 5], 16, seed=431).check_scores(E, "none")
+
+
+@FORMS
+def test_scores_of_negative_queries(E, full):
     """Every head of a group scores below zero: padding must not win."""
     p = Problem(3, 1, 64, 2, [200], 16, seed=440)
     p.q, p.k = -p.q.abs() - 1, p.k.abs() + 1
-    s = p.check_scores(E)
+    s = p.check_scores(E, full_tiles=full)
     assert bool((s[s > -math.inf] < 0).all())
 
 
@@ -237,28 +262,46 @@ def test_blocks_equal_paged_where_every_page_is_selected(E):
         assert float((o.float() - o2.float()).abs().max()) < 0.05
 
 
-def test_blocks_of_wide_tables(E):
+@FORMS
+def test_blocks_of_wide_tables(E, full):
     """More pages than the bits in shared memory cover at a time."""
     p = Problem(4, 2, 32, 1, [16 * 2500 + 3, 40], 16, seed=520)
-    p.check_blocks(E, p.lists(64, seed=1))
+    p.check_blocks(E, p.lists(64, seed=1), full_tiles=full)
     p = Problem(2, 1, 32, 6, [16 * 3300, 100], 16, seed=521)
-    p.check_blocks(E, p.lists(30, seed=2))
+    p.check_blocks(E, p.lists(30, seed=2), full_tiles=full)
 
 
-def test_blocks_of_rising_maxima(E):
+@pytest.mark.parametrize("Hq,Hk,d,Nq,lens,page,q_lens,n", [
+    # enough rows for tiles of 128 by the rule: one query after another, heads that do not
+    # divide a tile, pages smaller and larger than a stage, ragged counts, a short sequence
+    (8, 2, 128, 1000, [1100], 64, None, 6),
+    (3, 1, 64, 1300, [1300, 1500], 16, [1300, 1290], 9),
+    (12, 4, 32, 700, [4000], 32, None, 5),
+    (16, 1, 64, 500, [900], 128, [471], 4),
+    (2, 2, 128, 1900, [1900, 2000], 256, [0, 1900], 3),
+    (5, 1, 32, 1500, [3], 16, None, 2),
+], ids=str)
+def test_blocks_of_many_rows(E, Hq, Hk, d, Nq, lens, page, q_lens, n):
+    p = Problem(Hq, Hk, d, Nq, lens, page, q_lens, seed=525)
+    p.check_blocks(E, p.lists(n, seed=4))
+
+
+@FORMS
+def test_blocks_of_rising_maxima(E, full):
     """Scores that grow from page to page by far more than the running maximum's slack."""
     p = Problem(4, 1, 64, 1, [900], 16, seed=530)
     ramp = torch.linspace(0.1, 14.0, 57)
     for j, pg in enumerate(p.table[0].tolist()):
         p.k[pg] *= ramp[j]
-    p.check_blocks(E, p.lists(57, seed=3))
+    p.check_blocks(E, p.lists(57, seed=3), full_tiles=full)
     # the other way round: the last page, partly unused, is then read whole
     p.k, p.v, p.table = p.k0(), p.v.nan_to_num(0.0), p.table.flip(1)
     p.lens = ints([56 * 16])
-    p.check_blocks(E, torch.arange(57, dtype=torch.int32).expand(1, 1, 1, 57).contiguous())
+    p.check_blocks(E, torch.arange(57, dtype=torch.int32).expand(1, 1, 1, 57).contiguous(), full_tiles=full)
 
 
-def test_blocks_with_scores_that_are_not_finite(E):
+@FORMS
+def test_blocks_with_scores_that_are_not_finite(E, full):
     """A key of NaN or a score of +inf gives NaN where it is read, nothing where it is not;
     a row of scores -inf is a row without a key."""
     p = Problem(2, 1, 64, 1, [64], 16, seed=540)
@@ -266,7 +309,7 @@ def test_blocks_with_scores_that_are_not_finite(E):
     ids = p.table[0].tolist()
     p.k[ids[0], :, 2], p.k[ids[1], :, 5], p.k[ids[2], :] = float("nan"), float("inf"), -float("inf")
     for entry, want in ((0, "nan"), (1, "nan"), (2, "none"), (3, "fine")):
-        o, lse = p.run_blocks(E, ints([[[[entry, -1]]]]))
+        o, lse = p.run_blocks(E, ints([[[[entry, -1]]]]), full_tiles=full)
         if want == "nan":
             assert bool(o.isnan().all()) and bool(lse.isnan().all())
         elif want == "none":
@@ -275,35 +318,40 @@ def test_blocks_with_scores_that_are_not_finite(E):
             assert bool(torch.isfinite(o).all()) and bool(torch.isfinite(lse).all())
 
 
-def test_weights_of_rows_without_a_sum(E):
+@FORMS
+def test_weights_of_rows_without_a_sum(E, full):
     """Rows whose lse is -inf count nothing, NaN reaches only the slots that such a row sees."""
     p = Problem(2, 2, 64, 3, [50, 40], 16, seed=550)
     lse = torch.full((2, 2, 3), 2.5)
-    lse[0, 0], lse[1, 1, 1] = -math.inf, -math.inf
-    p.check_weights(E, lse=lse)
+    lse[0, 0], lse[1, 1, 1], lse[1, 0, 2] = -math.inf, -math.inf, math.inf
+    p.check_weights(E, lse=lse, full_tiles=full)
     lse[0, 1, 0] = float("nan")
     w = p.w.cuda()
-    E.kv_weights(p.q.cuda(), p.k.cuda(), p.table.cuda(), p.lens.cuda(), lse.cuda(), w)
+    E.kv_weights(p.q.cuda(), p.k.cuda(), p.table.cuda(), p.lens.cuda(), lse.cuda(), w, full_tiles=full)
     got = O.rows(w.cpu(), p.table[0], 50)
     assert bool(got[1, :48].isnan().all()) and not bool(got[1, 48:].isnan().any()) and not bool(got[0].isnan().any())
 
 
-def test_weights_of_keys_that_are_infinite(E):
+@FORMS
+def test_weights_of_keys_that_are_infinite(E, full):
     p = Problem(1, 1, 32, 1, [40], 16, seed=560)
     p.q = p.q.abs() + 1
     p.k[int(p.table[0, 0]), 0, 3] = -float("inf")
     w = p.w.cuda()
-    E.kv_weights(p.q.cuda(), p.k.cuda(), p.table.cuda(), p.lens.cuda(), torch.full((1, 1, 1), 3.0).cuda(), w, decay=0.0)
+    E.kv_weights(p.q.cuda(), p.k.cuda(), p.table.cuda(), p.lens.cuda(), torch.full((1, 1, 1), 3.0).cuda(), w, decay=0.0,
+                 full_tiles=full)
     assert float(w[int(p.table[0, 0]), 0, 3]) == 0.0 and bool(torch.isfinite(O.rows(w.cpu(), p.table[0], 40)).all())
 
 
-def test_weights_sum_to_the_number_of_rows(E):
+@FORMS
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_weights_sum_to_the_number_of_rows(E, d, full):
     """With the lse that the attention returned, each row hands out one in all."""
-    p = Problem(6, 2, 64, 20, [20, 300, 77], 32, [20, 13, 1], seed=570)
+    p = Problem(6, 2, d, 20, [20, 300, 77], 32, [20, 13, 1], seed=570)
     args = p.k.cuda(), p.v.cuda(), p.table.cuda(), p.lens.cuda()
     _, lse = E.attn_paged(p.q.cuda(), *args, q_lens=p.q_lens.cuda())
     w = p.w.cuda()
-    E.kv_weights(p.q.cuda(), args[0], args[2], args[3], lse, w, q_lens=p.q_lens.cuda(), decay=0.0)
+    E.kv_weights(p.q.cuda(), args[0], args[2], args[3], lse, w, q_lens=p.q_lens.cuda(), decay=0.0, full_tiles=full)
     for b in range(3):
         got = O.rows(w.cpu(), p.table[b], int(p.lens[b])).sum(1)
         assert torch.allclose(got, torch.full((2,), 3.0 * int(p.q_lens[b])).double(), rtol=2.0 ** -14)
@@ -368,22 +416,42 @@ def test_evict_where_the_table_names_no_page(E):
     evicted(E, p, 50, 2, 5, dst)
 
 
-def test_lengths_beyond_the_table_are_cut(E):
+@FORMS
+def test_lengths_beyond_the_table_are_cut(E, full):
     p = Problem(2, 1, 32, 1, [48, 20], 16, seed=640)
     p.lens = ints([1 << 30, -5])
-    p.check_scores(E)
-    p.check_blocks(E, p.lists(6))
-    p.check_weights(E)
+    p.check_scores(E, full_tiles=full)
+    p.check_blocks(E, p.lists(6), full_tiles=full)
+    p.check_weights(E, full_tiles=full)
     evicted(E, p, 20, 1, 1)
 
 
-def test_pages_that_the_cache_has_not(E):
+@FORMS
+def test_pages_that_the_cache_has_not(E, full):
     """Entries that name no page read as zeros: scores and values 0, nothing outside."""
     p = Problem(2, 1, 64, 1, [64], 16, seed=650)
     p.table[0, 1], p.table[0, 3] = p.n_pages, -1
-    p.check_scores(E)
-    p.check_blocks(E, ints([[[[0, 1, 2, 3]]]]))
-    p.check_weights(E)
+    p.check_scores(E, full_tiles=full)
+    p.check_blocks(E, ints([[[[0, 1, 2, 3]]]]), full_tiles=full)
+    p.check_weights(E, full_tiles=full)
+
+
+def test_timeouts_are_reported(E):
+    """Something withheld in the forms with tiles of 128 rows: the bounded wait runs out, the
+    status says so, and the next call is right."""
+    p = Problem(4, 1, 64, 40, [700], 16, seed=655)
+    lists, how = p.lists(5), dict(timeout_ns=20_000_000, inject=1, full_tiles=True)
+    b = torch.zeros(p.n_pages, 1, 2, 64, dtype=torch.bfloat16, device="cuda")
+    args = p.table.cuda(), p.lens.cuda()
+    for call in (lambda: p.run_blocks(E, lists, **how), lambda: E.block_scores(p.q.cuda(), b, *args, page_size=16, **how),
+                 lambda: E.kv_weights(p.q.cuda(), p.k.cuda(), *args, torch.zeros(1, 4, 40).cuda(), p.w.cuda(), **how)):
+        call()
+        torch.cuda.synchronize()
+        code, detail = E.device_status()
+        assert code == 5 and detail[0] == 5
+        p.check_blocks(E, lists, full_tiles=True)
+        p.check_scores(E, full_tiles=True)
+        p.check_weights(E, full_tiles=True)
 
 
 def test_layouts(E):
@@ -404,6 +472,8 @@ def test_layouts(E):
     assert all(torch.equal(a, b) for a, b in zip(got, want))
     lse = torch.full((2, 6, 4), 3.0, device="cuda")
     w1, w2 = p.w.cuda(), p.w.cuda()
+    assert torch.equal(E.attn_blocks(qh, kn, vn, wide[:, :table.shape[1]], lens, lists, full_tiles=True)[0],
+                       p.run_blocks(E, lists, full_tiles=True)[0])
     E.kv_weights(q, p.k.cuda(), table, lens, lse, w1)
     E.kv_weights(qh, kn, wide[:, :table.shape[1]], lens, lse, w2)
     assert torch.equal(w1.nan_to_num(0.0), w2.nan_to_num(0.0))
@@ -421,12 +491,12 @@ def test_layouts(E):
     assert torch.equal(kn.nan_to_num(0.0), k1.nan_to_num(0.0)) and torch.equal(vn.nan_to_num(0.0), v1.nan_to_num(0.0))
 
 
-def step(E, p, bnd, w, n=4, stream=None, **bufs):
+def step(E, p, bnd, w, n=4, stream=None, full=None, **bufs):
     """One decoding step of every operator, into given buffers."""
-    kw = dict(stream=stream)
-    E.kv_bounds(bufs["k"], bnd, bufs["table"], bufs["lens"], n_new=p.Nq, **kw)
+    kw = dict(stream=stream, full_tiles=full)
+    E.kv_bounds(bufs["k"], bnd, bufs["table"], bufs["lens"], n_new=p.Nq, stream=stream)
     s = E.block_scores(bufs["q"], bnd, bufs["table"], bufs["lens"], page_size=p.page, **kw)
-    lists = E.block_select(s, bufs["lens"], n, page_size=p.page, **kw)
+    lists = E.block_select(s, bufs["lens"], n, page_size=p.page, stream=stream)
     o, lse = E.attn_blocks(bufs["q"], bufs["k"], bufs["v"], bufs["table"], bufs["lens"], lists, **kw)
     E.kv_weights(bufs["q"], bufs["k"], bufs["table"], bufs["lens"], lse, w, **kw)
     return s, lists, o, lse
@@ -438,31 +508,33 @@ def buffers(p):
             dict(q=p.q.cuda(), k=p.k.cuda(), v=p.v.cuda(), table=p.table.cuda(), lens=p.lens.cuda()))
 
 
-def test_same_bits_twice_and_two_streams(E):
+@FORMS
+def test_same_bits_twice_and_two_streams(E, full):
     """No atomics that change results: equal bits, also for two calls at once."""
     ps = [Problem(8, 2, 128, 1, [100, 700, 33], 16, seed=700), Problem(4, 4, 64, 3, [10, 900], 64, seed=701)]
     want = []
     for p in ps:
         bnd, w, bufs = buffers(p)
-        want.append((*step(E, p, bnd, w, **bufs), w))
+        want.append((*step(E, p, bnd, w, full=full, **bufs), w))
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream(), torch.cuda.Stream()]
     for _ in range(4):
         state = [buffers(p) for p in ps]
         torch.cuda.synchronize()
-        got = [(*step(E, p, bnd, w, stream=st, **bufs), w) for p, st, (bnd, w, bufs) in zip(ps, streams, state)]
+        got = [(*step(E, p, bnd, w, stream=st, full=full, **bufs), w) for p, st, (bnd, w, bufs) in zip(ps, streams, state)]
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(x.nan_to_num(0.0) if x.is_floating_point() else x,
                                    y.nan_to_num(0.0) if y.is_floating_point() else y) for x, y in zip(a, b))
 
 
-def test_graph_follows_the_lengths(E):
+@FORMS
+def test_graph_follows_the_lengths(E, full):
     p = Problem(4, 2, 64, 1, [300, 300, 300], 32, seed=800)
     bnd, w, bufs = buffers(p)
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
-        s, lists, o, lse = step(E, p, bnd, w, **bufs)
+        s, lists, o, lse = step(E, p, bnd, w, full=full, **bufs)
         new, kept = E.kv_evict(bufs["k"].clone(), bufs["v"].clone(), w.clone(), bufs["table"], bufs["lens"], 100, last=10)
     for now in ([300, 300, 300], [1, 128, 257], [0, 0, 5]):
         bufs["lens"].copy_(ints(now))
@@ -538,8 +610,9 @@ def test_offsets_beyond_32_bits(E):
     assert torch.equal(vc[ids].cpu().nan_to_num(0.0), rv.nan_to_num(0.0))
 
 
+@FORMS
 @pytest.mark.parametrize("seed", range(16))
-def test_random_problems(E, seed):
+def test_random_problems(E, seed, full):
     r = random.Random(seed)
     Hk, G, d = r.choice([1, 2, 3]), r.choice([1, 2, 3, 4, 5, 8, 16, 20]), r.choice([32, 64, 128])
     Nq = r.choice([1, 1, 2, r.randint(3, 20), r.randint(60, 140)])
@@ -550,13 +623,13 @@ def test_random_problems(E, seed):
             for b in range(B)]
     p = Problem(Hk * G, Hk, d, Nq, lens, page, q_lens, seed=2000 + 10 * seed, width=r.choice([None, 40]))
     mask = r.choice(["none", "causal_br"])
-    s = p.check_scores(E, mask)
+    s = p.check_scores(E, mask, full_tiles=full)
     n = r.randint(3, 20)
     lists = E.block_select(s, p.lens.cuda(), n, page_size=page, q_lens=None if q_lens is None else p.q_lens.cuda(), mask=mask)
     assert torch.equal(lists.cpu(), O.select(s.cpu(), p.lens, p.q_lens, n, page, 1, 2, mask))
-    p.check_blocks(E, lists.cpu(), mask)
-    p.check_blocks(E, p.lists(n, seed=seed), mask)
-    p.check_weights(E, mask, r.choice([0.0, 1.0, 0.75]))
+    p.check_blocks(E, lists.cpu(), mask, full_tiles=full)
+    p.check_blocks(E, p.lists(n, seed=seed), mask, full_tiles=full)
+    p.check_weights(E, mask, r.choice([0.0, 1.0, 0.75]), full_tiles=full)
     budget = r.randint(1, 400)
     evicted(E, p, budget, r.randint(0, budget // 3), r.randint(0, budget // 3))
 
@@ -583,7 +656,7 @@ def test_refusals(E):
                       dict(page_size=8), dict(n=1 << 40), dict(kv_lens=b["lens"][:1]), dict(mask="wrap")],
         attn_blocks=[dict(blocks=lists.long()), dict(blocks=lists[..., :0]), dict(blocks=lists[:, :1]), dict(scale=-1.0),
                      dict(v_cache=b["v"][:, :1]), dict(lse=lse.double()), dict(out=b["q"][:1]), dict(q=b["q"].cpu()),
-                     dict(q=b["q"][..., :32])],
+                     dict(q=b["q"][..., :32]), dict(inject=2), dict(timeout_ns=-1), dict(timeout_ns=1 << 64)],
         kv_weights=[dict(decay=-0.5), dict(decay=float("inf")), dict(weights=w.double()), dict(lse=lse[:1]), dict(out=w[:1]),
                     dict(weights=w.transpose(0, 1)), dict(lse=lse.cpu()), dict(scale=1e-44)],
         kv_evict=[dict(budget=0), dict(first=5, last=4), dict(weights=w[:1]), dict(dst_table=b["table"].long()),

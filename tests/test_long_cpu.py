@@ -36,7 +36,7 @@ def block(name):
 
 
 COMMON = [(dict(B=0), INV), (dict(Hk=0), INV), (dict(B=70000), INV), (dict(page_size=8), INV), (dict(page_size=48), INV),
-          (dict(kv_lens=None), INV), (dict(kv_lens=A + 2), MIS), (dict(table_width=0), INV),
+          (dict(full_tiles=3), INV), (dict(inject=2), INV), (dict(kv_lens=None), INV), (dict(kv_lens=A + 2), MIS), (dict(table_width=0), INV),
           (dict(table_width=1 << 27, table_stride=1 << 27), INV)]
 TABLE = [(dict(block_table=None), INV), (dict(block_table=A + 1), MIS), (dict(table_stride=3), INV), (dict(n_pages=0), INV)]
 HEADS = [(dict(d=48), UNS), (dict(d=256), UNS)]
@@ -56,9 +56,9 @@ BAD = dict(
         (dict(n=1 << 29), INV), (dict(lse=A + 2), MIS)],
     attn_kv_weights=COMMON + TABLE + HEADS + QUERIES + Q + KEYS + [(dict(lse=None), INV), (dict(weights=None), INV),
                                                                    (dict(weights_out=None), INV), (dict(decay=-1.0), INV), (dict(decay=math.nan), INV),
-                                                                   (dict(weights=A + 2), MIS), (dict(scale=1e-44), INV)],
+                                                                   (dict(weights=A + 2), MIS), (dict(scale=1e-44), INV), (dict(scale=2.0 ** -65), INV), (dict(scale=2.0 ** 65), INV)],
     attn_kv_evict=COMMON + TABLE + HEADS + KEYS + VALUES + TAKEN + [
-        (dict(weights=None), INV), (dict(kept=None), INV), (dict(new_lens=None), INV), (dict(new_lens=2 * A), INV),
+        (dict(weights=None), INV), (dict(weights=A + 8), MIS), (dict(kept=None), INV), (dict(new_lens=None), INV), (dict(new_lens=2 * A), INV),
         (dict(k_cache_stride=(1024, 1024, 64)), INV), (dict(v_cache_stride=(64, 1024, 64)), INV), (dict(dst_table=A), INV),
         (dict(dst_table=A, dst_width=2, dst_stride=1), INV), (dict(dst_table=A + 2, dst_width=2, dst_stride=2), MIS),
         (dict(dst_table=A, dst_width=1, dst_stride=1, n=20), INV)],
