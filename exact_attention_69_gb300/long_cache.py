@@ -35,6 +35,9 @@ import torch
 from . import _lib
 from .cache import _PAGED_MASKS, _fits, _heads, _int32, _on, _plans, _ptr, _remember, _same_device, _sig, _wrote
 
+_Params, _byref, _empty = _lib.AttnLongParams, ctypes.byref, torch.empty
+_device_now, _stream_now = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
 
 def _plain(name, t, dtype, device, shape):
     """Checks a contiguous tensor of the library's own layout."""
@@ -85,14 +88,17 @@ def _queries(p, q, device, mask, scale):
 _calls: dict = {}
 
 
-def _call(name, p, handle):
-    p.stream = handle
+def _call(name, p):
     f = _calls.get(name)
     if f is None:
         f = _calls[name] = getattr(_lib.load(), name)
-    code = f(ctypes.byref(p))
+    code = f(_byref(p))
     if code:
         _lib.check(code, name.replace("attn_kv", "kv").replace("attn_block_", "block_"))
+
+
+# A call on the current stream of the current device, the usual one, goes straight to
+# its _run_ function; others go there through _on.
 
 
 def _form(p, full_tiles, timeout_ns, inject):
@@ -110,7 +116,7 @@ def _cuda(t, name):
 
 
 def _plan_bounds(k_cache, bounds, block_table, kv_lens):
-    p = _lib.AttnLongParams()
+    p = _Params()
     _pages(p, "k_cache", k_cache)
     p.k_cache_stride[:] = _heads("k_cache", k_cache)
     device = k_cache.device
@@ -135,19 +141,23 @@ def kv_bounds(k_cache: torch.Tensor, bounds: torch.Tensor, block_table: torch.Te
     plan = _plans.get(key)
     if plan is None:
         plan = _remember(key, _plan_bounds(k_cache, bounds, block_table, kv_lens))
-    p = _lib.AttnLongParams.from_buffer_copy(plan)
-    p.k_cache, p.bounds, p.block_table, p.kv_lens = (t.data_ptr() for t in (k_cache, bounds, block_table, kv_lens))
+    p = _Params.from_buffer_copy(plan)
+    p.k_cache, p.bounds, p.block_table, p.kv_lens = k_cache.data_ptr(), bounds.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr()
     p.n_new = n_new
+    device = k_cache.device
+    if stream is None and _device_now() == device.index:
+        return _run_bounds(_stream_now(device.index), p, bounds)
+    _on(device, stream, (k_cache, bounds, block_table, kv_lens), lambda handle: _run_bounds(handle, p, bounds))
 
-    def run(handle):
-        _call("attn_kv_bounds", p, handle)
-        _wrote((bounds,))
 
-    _on(k_cache.device, stream, (k_cache, bounds, block_table, kv_lens), run)
+def _run_bounds(handle, p, bounds):
+    p.stream = handle
+    _call("attn_kv_bounds", p)
+    _wrote((bounds,))
 
 
 def _plan_scores(q, bounds, block_table, kv_lens, page_size, q_lens, scale, mask, out, full_tiles, timeout_ns, inject):
-    p = _lib.AttnLongParams()
+    p = _Params()
     _fits("page_size", page_size)
     _form(p, full_tiles or None, timeout_ns, inject)
     device = _cuda(bounds, "bounds")
@@ -183,23 +193,27 @@ def block_scores(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
     if plan is None:
         plan = _remember(key, _plan_scores(q, bounds, block_table, kv_lens, page_size, q_lens, scale, mask, out, full_tiles,
                                            timeout_ns, inject))
-    p = _lib.AttnLongParams.from_buffer_copy(plan[0])
-    p.q, p.bounds, p.block_table, p.kv_lens = (t.data_ptr() for t in (q, bounds, block_table, kv_lens))
+    p = _Params.from_buffer_copy(plan[0])
+    p.q, p.bounds, p.block_table, p.kv_lens = q.data_ptr(), bounds.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr()
     p.q_lens = _ptr(q_lens)
+    device = q.device
+    if stream is None and _device_now() == device.index:
+        return _run_scores(_stream_now(device.index), p, plan[1], device, out)
+    return _on(device, stream, (q, bounds, block_table, kv_lens, q_lens, out),
+               lambda handle: _run_scores(handle, p, plan[1], device, out))
 
-    def run(handle):
-        s = torch.empty(plan[1], dtype=torch.float32, device=q.device) if out is None else out
-        p.scores = s.data_ptr()
-        _call("attn_block_scores", p, handle)
-        if out is not None:
-            _wrote((out,))
-        return s
 
-    return _on(q.device, stream, (q, bounds, block_table, kv_lens, q_lens, out), run)
+def _run_scores(handle, p, shape, device, out):
+    s = _empty(shape, dtype=torch.float32, device=device) if out is None else out
+    p.scores, p.stream = s.data_ptr(), handle
+    _call("attn_block_scores", p)
+    if out is not None:
+        _wrote((out,))
+    return s
 
 
 def _plan_select(scores, kv_lens, n, page_size, q_lens, first, last, mask, out):
-    p = _lib.AttnLongParams()
+    p = _Params()
     for name, x in (("n", n), ("page_size", page_size), ("first", first), ("last", last)):
         _fits(name, x)
     if n < 1 or first < 0 or last < 0 or first + last > n:
@@ -233,23 +247,26 @@ def block_select(scores: torch.Tensor, kv_lens: torch.Tensor, n: int, *, page_si
     plan = _plans.get(key)
     if plan is None:
         plan = _remember(key, _plan_select(scores, kv_lens, n, page_size, q_lens, first, last, mask, out))
-    p = _lib.AttnLongParams.from_buffer_copy(plan[0])
+    p = _Params.from_buffer_copy(plan[0])
     p.scores, p.kv_lens, p.q_lens = scores.data_ptr(), kv_lens.data_ptr(), _ptr(q_lens)
+    device = scores.device
+    if stream is None and _device_now() == device.index:
+        return _run_select(_stream_now(device.index), p, plan[1], device, out)
+    return _on(device, stream, (scores, kv_lens, q_lens, out), lambda handle: _run_select(handle, p, plan[1], device, out))
 
-    def run(handle):
-        blocks = torch.empty(plan[1], dtype=torch.int32, device=scores.device) if out is None else out
-        p.blocks = blocks.data_ptr()
-        _call("attn_block_select", p, handle)
-        if out is not None:
-            _wrote((out,))
-        return blocks
 
-    return _on(scores.device, stream, (scores, kv_lens, q_lens, out), run)
+def _run_select(handle, p, shape, device, out):
+    blocks = _empty(shape, dtype=torch.int32, device=device) if out is None else out
+    p.blocks, p.stream = blocks.data_ptr(), handle
+    _call("attn_block_select", p)
+    if out is not None:
+        _wrote((out,))
+    return blocks
 
 
 def _plan_blocks(q, k_cache, v_cache, block_table, kv_lens, blocks, q_lens, scale, mask, out, lse, full_tiles,
                  timeout_ns, inject):
-    p = _lib.AttnLongParams()
+    p = _Params()
     _form(p, full_tiles, timeout_ns, inject)
     _pages(p, "k_cache", k_cache)
     p.k_cache_stride[:] = _heads("k_cache", k_cache)
@@ -295,29 +312,29 @@ def attn_blocks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, b
     if plan is None:
         plan = _remember(key, _plan_blocks(q, k_cache, v_cache, block_table, kv_lens, blocks, q_lens, scale, mask, out,
                                            lse, full_tiles, timeout_ns, inject))
+    p = _Params.from_buffer_copy(plan)
+    p.q, p.k_cache, p.v_cache, p.block_table = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr()
+    p.kv_lens, p.q_lens, p.blocks = kv_lens.data_ptr(), _ptr(q_lens), blocks.data_ptr()
     device = q.device
-    p = _lib.AttnLongParams.from_buffer_copy(plan)
-    p.q, p.k_cache, p.v_cache = q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
-    p.block_table, p.kv_lens, p.q_lens, p.blocks = block_table.data_ptr(), kv_lens.data_ptr(), _ptr(q_lens), blocks.data_ptr()
+    if stream is None and _device_now() == device.index:
+        return _run_blocks(_stream_now(device.index), p, q.shape, device, out, lse, return_lse)
+    return _on(device, stream, (q, k_cache, v_cache, block_table, kv_lens, blocks, q_lens, out, lse),
+               lambda handle: _run_blocks(handle, p, q.shape, device, out, lse, return_lse))
 
-    def run(handle):
-        o = torch.empty(q.shape, dtype=torch.bfloat16, device=device) if out is None else out
-        p.o = o.data_ptr()
-        z = lse
-        if z is None and return_lse:
-            z = torch.empty(q.shape[:3], dtype=torch.float32, device=device)
-        p.lse = _ptr(z)
-        _call("attn_blocks", p, handle)
-        if out is not None or lse is not None:
-            _wrote([t for t in (out, lse) if t is not None])
-        return (o, z) if return_lse else o
 
-    return _on(device, stream, (q, k_cache, v_cache, block_table, kv_lens, blocks, q_lens, out, lse), run)
+def _run_blocks(handle, p, shape, device, out, lse, return_lse):
+    o = _empty(shape, dtype=torch.bfloat16, device=device) if out is None else out
+    z = _empty(shape[:3], dtype=torch.float32, device=device) if lse is None and return_lse else lse
+    p.o, p.lse, p.stream = o.data_ptr(), _ptr(z), handle
+    _call("attn_blocks", p)
+    if out is not None or lse is not None:
+        _wrote([t for t in (out, lse) if t is not None])
+    return (o, z) if return_lse else o
 
 
 def _plan_weights(q, k_cache, block_table, kv_lens, lse, weights, q_lens, scale, mask, decay, out, full_tiles, timeout_ns,
                   inject):
-    p = _lib.AttnLongParams()
+    p = _Params()
     if not (math.isfinite(decay) and decay >= 0):
         raise ValueError("decay must be finite and >= 0")
     _form(p, full_tiles or None, timeout_ns, inject)
@@ -357,21 +374,25 @@ def kv_weights(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor
     if plan is None:
         plan = _remember(key, _plan_weights(q, k_cache, block_table, kv_lens, lse, weights, q_lens, scale, mask, decay,
                                             out, full_tiles, timeout_ns, inject))
-    p = _lib.AttnLongParams.from_buffer_copy(plan)
-    p.q, p.k_cache, p.block_table, p.kv_lens = (t.data_ptr() for t in (q, k_cache, block_table, kv_lens))
+    p = _Params.from_buffer_copy(plan)
+    p.q, p.k_cache, p.block_table, p.kv_lens = q.data_ptr(), k_cache.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr()
     p.lse, p.weights, p.q_lens = lse.data_ptr(), weights.data_ptr(), _ptr(q_lens)
     to = weights if out is None else out
     p.weights_out = to.data_ptr()
+    device = q.device
+    if stream is None and _device_now() == device.index:
+        return _run_weights(_stream_now(device.index), p, to)
+    _on(device, stream, (q, k_cache, block_table, kv_lens, lse, weights, q_lens, out), lambda handle: _run_weights(handle, p, to))
 
-    def run(handle):
-        _call("attn_kv_weights", p, handle)
-        _wrote((to,))
 
-    _on(q.device, stream, (q, k_cache, block_table, kv_lens, lse, weights, q_lens, out), run)
+def _run_weights(handle, p, to):
+    p.stream = handle
+    _call("attn_kv_weights", p)
+    _wrote((to,))
 
 
 def _plan_evict(k_cache, v_cache, weights, block_table, kv_lens, budget, first, last, dst_table):
-    p = _lib.AttnLongParams()
+    p = _Params()
     for name, x in (("budget", budget), ("first", first), ("last", last)):
         _fits(name, x)
     if budget < 1 or first < 0 or last < 0 or first + last > budget:
@@ -411,17 +432,20 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor
     if plan is None:
         plan = _remember(key, _plan_evict(k_cache, v_cache, weights, block_table, kv_lens, budget, first, last,
                                           dst_table))
-    device = k_cache.device
-    p = _lib.AttnLongParams.from_buffer_copy(plan[0])
+    p = _Params.from_buffer_copy(plan[0])
     p.k_cache, p.v_cache, p.weights = k_cache.data_ptr(), v_cache.data_ptr(), weights.data_ptr()
     p.block_table, p.kv_lens, p.dst_table = block_table.data_ptr(), kv_lens.data_ptr(), _ptr(dst_table)
+    device = k_cache.device
+    if stream is None and _device_now() == device.index:
+        return _run_evict(_stream_now(device.index), p, plan, device, k_cache, v_cache, weights)
+    return _on(device, stream, (k_cache, v_cache, weights, block_table, kv_lens, dst_table),
+               lambda handle: _run_evict(handle, p, plan, device, k_cache, v_cache, weights))
 
-    def run(handle):
-        lens = torch.empty(plan[1], dtype=torch.int32, device=device)
-        kept = torch.empty(plan[1], plan[2], budget, dtype=torch.int32, device=device)
-        p.new_lens, p.kept = lens.data_ptr(), kept.data_ptr()
-        _call("attn_kv_evict", p, handle)
-        _wrote((k_cache, v_cache, weights))
-        return lens, kept
 
-    return _on(device, stream, (k_cache, v_cache, weights, block_table, kv_lens, dst_table), run)
+def _run_evict(handle, p, plan, device, k_cache, v_cache, weights):
+    lens = _empty(plan[1], dtype=torch.int32, device=device)
+    kept = _empty((plan[1], plan[2], p.n), dtype=torch.int32, device=device)
+    p.new_lens, p.kept, p.stream = lens.data_ptr(), kept.data_ptr(), handle
+    _call("attn_kv_evict", p)
+    _wrote((k_cache, v_cache, weights))
+    return lens, kept
