@@ -7,9 +7,10 @@
 // memory as the A operand, query rows stream by as B, 64 at a time, and a thread owns one
 // page or key (a TMEM lane) and walks along the rows (columns) with its running maximum or
 // sum in a register: no shuffles, no padding of heads, neighbouring lanes write
-// neighbouring places. A CTA is four warps; several share an SM. While the tensor core
-// works on tile t, the warps reduce tile t - 1 and the rows of tile t + 1 are on their
-// way.
+// neighbouring places. A CTA is eight warps, two threads a lane, each with half of a
+// tile's columns; several share an SM. While the tensor core works on tile t, the warps
+// reduce tile t - 1 and the rows of tile t + 1 are on their way. (One thread a lane: 512
+// tokens' scores 26.5 us, 333 rows' weights 38.9.)
 //
 // Every wait is bounded: when one runs out the CTA notes it in the status word, leaves its
 // loop, waits (bounded) for its products in flight, frees TMEM and returns.
@@ -24,7 +25,7 @@ namespace dev {
 
 __device__ uint32_t g_long_status[4];
 
-constexpr int kTileThreads = 128, kTileRows = 64;  // threads: one for each of 128 pages or keys
+constexpr int kTileThreads = 256, kTileRows = 64;  // threads: two for each of 128 pages or keys
 constexpr uint32_t kTileCols = 2 * kTileRows;      // TMEM columns: two accumulators
 constexpr uint32_t kRoleTiles = 4;
 
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) scores_tiles(const __grid_con
   const int tok0 = static_cast<int>(blockIdx.x % runs) * tokens, page0 = static_cast<int>(blockIdx.x / runs) * 128;
   const LongLens lens = long_lens(p, b);
   const int toks = min(tokens, p.Nq - tok0);
-  const int page = page0 + static_cast<int>(threadIdx.x);
+  const int half = static_cast<int>(threadIdx.x) >> 7, page = page0 + (static_cast<int>(threadIdx.x) & 127);
   float* out = p.scores + ((static_cast<int64_t>(b) * p.Hk + hk) * p.Nq + tok0) * p.table_width + page;
   // pages of which no query of the run sees anything need no product
   const int live = min(tok0 + toks, lens.ql);
@@ -204,10 +205,10 @@ __global__ void __launch_bounds__(kTileThreads, 2) scores_tiles(const __grid_con
     }
   };
   if (tiles > 0) {
-    int mine = page < pages ? p.table[b * p.table_sb + page] : -1;
+    const int mine = half == 0 && page < pages ? p.table[b * p.table_sb + page] : -1;
     load();
     load();
-    ids[threadIdx.x] = mine;
+    if (half == 0) ids[threadIdx.x] = mine;
     __syncthreads();
 #pragma unroll 4
     for (int x = threadIdx.x; x < 128 * 2 * kPieces; x += kTileThreads) {
@@ -220,25 +221,26 @@ __global__ void __launch_bounds__(kTileThreads, 2) scores_tiles(const __grid_con
     ldev::copy_commit();
   }
 
+  // (heads that do not divide half a tile: the first of a lane's threads takes all columns)
+  constexpr int kHalfToks = G > 0 ? kTileRows / 2 / (G > 0 ? G : 1) : 0;
   float best = -INFINITY;
-  int tok = 0, g = 0;  // the token and head that the next column is
-  float* at = out;
+  int tok = half * kHalfToks, g = 0;  // the token and head that the next column is
+  float* at = out + static_cast<int64_t>(tok) * p.table_width;
+  const uint32_t lanes = ((threadIdx.x >> 5) & 3u) << 21;
   // token n of the run (below live) sees max(first + n * by, 0) slots
   const int first = p.causal ? lens.len - lens.ql + tok0 + 1 : lens.len, by = p.causal ? 1 : 0;
   const auto sees = [&](int n) { return long_pages(p, max(first + n * by, 0)); };
   const bool in = page < p.table_width;
   const auto reduce = [&](int t) {
-    uint32_t v[2][32];
-    tmem_ld32(tl.d(t) + ((threadIdx.x >> 5) << 21), v[0]);
-    tmem_ld32(tl.d(t) + ((threadIdx.x >> 5) << 21) + 32, v[1]);
-    if constexpr (G > 0) {  // (G divides the tile)
-      constexpr int kToks = kTileRows / G;
-      const bool whole = page0 + 128 <= sees(tok) && tok + kToks <= live - tok0;  // every page, for every token
+    uint32_t v[32];
+    if constexpr (G > 0) {
+      tmem_ld32(tl.d(t) + lanes + half * 32, v);
+      const bool whole = page0 + 128 <= sees(tok) && tok + kHalfToks <= live - tok0;  // every page, for every token
 #pragma unroll
-      for (int n = 0; n < kToks; ++n) {
-        float z = __uint_as_float(v[n * G >> 5][(n * G) & 31]);
+      for (int n = 0; n < kHalfToks; ++n) {
+        float z = __uint_as_float(v[n * G]);
 #pragma unroll
-        for (int c = n * G + 1; c < (n + 1) * G; ++c) z = max_nan(z, __uint_as_float(v[c >> 5][c & 31]));
+        for (int c = n * G + 1; c < (n + 1) * G; ++c) z = max_nan(z, __uint_as_float(v[c]));
         z *= p.scale;
         if (whole) {
           *at = z;
@@ -247,17 +249,23 @@ __global__ void __launch_bounds__(kTileThreads, 2) scores_tiles(const __grid_con
         }
         at += p.table_width;
       }
-      tok += kToks;
+      tok += 2 * kHalfToks;
+      at += static_cast<int64_t>(kHalfToks) * p.table_width;
     } else {
+      if (half != 0) return;
+#pragma unroll 1
+      for (int h = 0; h < kTileRows; h += 32) {
+        tmem_ld32(tl.d(t) + lanes + h, v);
 #pragma unroll
-      for (int c = 0; c < kTileRows; ++c) {
-        best = max_nan(best, __uint_as_float(v[c >> 5][c & 31]));
-        if (++g == heads) {
-          if (in && tok < live - tok0) *at = page < sees(tok) ? best * p.scale : -INFINITY;
-          best = -INFINITY;
-          g = 0;
-          ++tok;
-          at += p.table_width;
+        for (int c = 0; c < 32; ++c) {
+          best = max_nan(best, __uint_as_float(v[c]));
+          if (++g == heads) {
+            if (in && tok < live - tok0) *at = page < sees(tok) ? best * p.scale : -INFINITY;
+            best = -INFINITY;
+            g = 0;
+            ++tok;
+            at += p.table_width;
+          }
         }
       }
     }
@@ -300,7 +308,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) scores_tiles(const __grid_con
     if (ok) reduce(t - 1);
   }
   // what no query sees
-  for (int n = some ? max(live - tok0, 0) : 0; n < toks; ++n)
+  for (int n = (some ? max(live - tok0, 0) : 0) + half; n < toks; n += 2)
     if (page < p.table_width) out[static_cast<int64_t>(n) * p.table_width] = -INFINITY;
   tl.end();
 }
@@ -335,7 +343,8 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
   __shared__ uint64_t bars[2];
   __shared__ uint32_t slot;
   __shared__ RowNumbers numbers[4];
-  __shared__ int ids[128];  // the keys' pages
+  __shared__ int ids[128];     // the keys' pages
+  __shared__ float sums[128];  // of the second of a key's threads
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem);
   Tiles2 tl(p);
@@ -345,7 +354,8 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
 
   const int b = blockIdx.z, hk = blockIdx.y;
   const LongLens lens = long_lens(p, b);
-  const int key0 = static_cast<int>(blockIdx.x) * 128, key = key0 + static_cast<int>(threadIdx.x);
+  const int half = static_cast<int>(threadIdx.x) >> 7, unit = static_cast<int>(threadIdx.x) & 127;
+  const int key0 = static_cast<int>(blockIdx.x) * 128, key = key0 + unit;
   const int page_mask = (1 << p.page_shift) - 1;
   const int rows = key0 < lens.len ? lens.ql * p.G : 0, tiles = (rows + kTileRows - 1) / kTileRows;
   const float* lse = p.lse + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * p.Nq;
@@ -394,34 +404,31 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
   const ldev::F2 c = ldev::pair(p.scale, p.scale);  // (scale * log2(e))
   const auto reduce = [&](int t) {
     const RowNumbers& now = numbers[t % 4];
-    const bool whole = key0 + 128 <= min(now.least[0], now.least[1]);
+    const bool whole = key0 + 128 <= now.least[half];
+    uint32_t v[32];
+    tmem_ld32(tl.d(t) + (((threadIdx.x >> 5) & 3u) << 21) + half * 32, v);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      uint32_t v[32];
-      tmem_ld32(tl.d(t) + ((threadIdx.x >> 5) << 21) + half * 32, v);
-#pragma unroll
-      for (int x = 0; x < 32; x += 4) {
-        const float2 a0 = ldev::split(ldev::mul2(ldev::pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), c));
-        const float2 a1 = ldev::split(ldev::mul2(ldev::pair(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), c));
-        float w[4] = {ex2(a0.x), ex2(a0.y), ex2(a1.x), ex2(a1.y)};
-        if (!whole) {
-          const int4 most = *reinterpret_cast<const int4*>(now.sees + half * 32 + x);
-          if (key >= most.x) w[0] = 0.f;
-          if (key >= most.y) w[1] = 0.f;
-          if (key >= most.z) w[2] = 0.f;
-          if (key >= most.w) w[3] = 0.f;
-        }
-        sum = ldev::add2(sum, ldev::add2(ldev::pair(w[0], w[1]), ldev::pair(w[2], w[3])));
+    for (int x = 0; x < 32; x += 4) {
+      const float2 a0 = ldev::split(ldev::mul2(ldev::pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), c));
+      const float2 a1 = ldev::split(ldev::mul2(ldev::pair(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), c));
+      float w[4] = {ex2(a0.x), ex2(a0.y), ex2(a1.x), ex2(a1.y)};
+      if (!whole) {
+        const int4 most = *reinterpret_cast<const int4*>(now.sees + half * 32 + x);
+        if (key >= most.x) w[0] = 0.f;
+        if (key >= most.y) w[1] = 0.f;
+        if (key >= most.z) w[2] = 0.f;
+        if (key >= most.w) w[3] = 0.f;
       }
+      sum = ldev::add2(sum, ldev::add2(ldev::pair(w[0], w[1]), ldev::pair(w[2], w[3])));
     }
   };
 
   float z = 0.f;
   if (tiles > 0) {
-    const int mine = key < lens.len ? p.table[b * p.table_sb + (key >> p.page_shift)] : -1;
+    const int mine = half == 0 && key < lens.len ? p.table[b * p.table_sb + (key >> p.page_shift)] : -1;
     z = read(0);
     const float z1 = kAhead > 1 ? read(1) : 0.f;
-    ids[threadIdx.x] = mine;
+    if (half == 0) ids[unit] = mine;
     __syncthreads();
 #pragma unroll 4
     for (int x = threadIdx.x; x < 128 * kPieces; x += kTileThreads) {
@@ -436,8 +443,8 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
     if constexpr (kAhead > 1) fetch(1);  // (nothing behind the last row: an empty group)
     // the further channels: ones for the keys, zeros behind the four of the rows
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(smem + S::kOffAX + more_at(threadIdx.x, 0)) = make_uint4(0x3F803F80u, 0x3F803F80u, 0, 0);
-    *reinterpret_cast<uint4*>(smem + S::kOffAX + more_at(threadIdx.x, 1)) = zero;
+    *reinterpret_cast<uint4*>(smem + S::kOffAX + more_at(unit, half)) =
+        half == 0 ? make_uint4(0x3F803F80u, 0x3F803F80u, 0, 0) : zero;
     for (int x = threadIdx.x; x < S::kStages * S::kBX / 16; x += kTileThreads)
       *reinterpret_cast<uint4*>(smem + S::kOffBX + x * 16) = zero;
     __syncthreads();
@@ -475,13 +482,16 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
     tc_fence_after();
     if (ok) reduce(t - 1);
   }
-  if (key < lens.len && ok) {
+  const float2 both = ldev::split(sum);
+  if (half != 0) sums[unit] = both.x + both.y;
+  __syncthreads();
+  if (half == 0 && key < lens.len && ok) {
     const int id = p.table[b * p.table_sb + (key >> p.page_shift)];
     if (id >= 0 && id < p.n_pages) {
       const int64_t at = ((static_cast<int64_t>(id) * p.Hk + hk) << p.page_shift) + (key & page_mask);
-      const float2 w = ldev::split(sum);
+      const float w = both.x + both.y + sums[unit];
       const bool old = p.decay != 0.f && !(p.causal && key >= lens.len - lens.ql);
-      p.weights_out[at] = old ? fmaf(p.decay, p.weights[at], w.x + w.y) : w.x + w.y;
+      p.weights_out[at] = old ? fmaf(p.decay, p.weights[at], w) : w;
     }
   }
   tl.end();
