@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_const
     fence_async_smem();
     tc_fence_before();
     if (__syncthreads_or(!ok)) break;
-    if (threadIdx.x < 32) {
+    if (threadIdx.x >= kTileThreads - 32) {  // (not a warp that has `place` to do)
       tc_fence_after();
       issue_tile<D>(tl.d(t), base, base + S::kOffB + stage * S::kB);
       issue_more(tl.d(t), base + S::kOffAX, base + S::kOffBX + stage * S::kBX);
