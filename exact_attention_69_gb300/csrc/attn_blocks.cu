@@ -12,6 +12,12 @@
 // are joined in shared memory, and those of the CTAs that share a tile, which are a
 // cluster, through each other's shared memory: one launch, no workspace, a fixed order.
 //
+// One or two tokens are bound by memory: 32 sequences x 8 key heads x 32 pages of 64, d = 128
+// (269 MB) take 45.3 us, 5.9 TB/s. (In four warps a CTA and up to three CTAs a SM 53 us, with
+// two CTAs a tile 64: a CTA's start, some 3 us of lists and first loads, weighs more.)
+// Few pages are a chain of latencies: 5.6 us for 16 pages of 16 slots (6.6 with the list of
+// one query made into bits first; 6.9 and 15.1 where 32 pages lie among 4096).
+//
 // The running maximum is a whole number (log2 units) and moves only when a score
 // passes it by more than 8: weights stay below 2^8 and rescaling is exact. Weights go into
 // the second product as two bf16 parts, 16 bits of each: memory sets the pace, so the second
@@ -91,6 +97,7 @@ struct Shared {
     uint16_t who[kWindow];
     int32_t table[kWindow];
     uint32_t sums[kListThreads / 32];
+    int next;
   };
   struct Join {
     float o[kBlocksWarps][kRows][D];  // (the first also takes the joined part)
@@ -162,25 +169,54 @@ __global__ void __launch_bounds__(32 * blocks_warps(NT), 2) blocks_kernel(const 
   const int shift = p.page_shift - 4;             // groups of 16 keys a page
   const int workers = kBlocksWarps * p.splits, me = split * kBlocksWarps + warp;
 
-  for (int w0 = 0; w0 < (lens.ql > tok0 ? pages : 0); w0 += kWindow) {
+  const int total = lens.ql > tok0 ? pages : 0;
+  // One query's short list is taken as it is, longer ones and several window by window. (In tiles
+  // of 16 rows all: the branch took 0.4 us of 8.5 from calls of several queries there.)
+  const bool direct = NT == 1 && toks == 1 && p.n <= kListThreads;
+  const int head = static_cast<int>(threadIdx.x) < toks * p.n ? lists[threadIdx.x] : -1;  // this thread's first entry
+  int next = total;  // first page of the next window that has a bit
+  for (int w0 = 0; w0 < total; w0 = next) {
     __syncthreads();
-    for (int x = threadIdx.x; x < kRows * (kWindow / 32); x += kThreads) (&sh.l.bits[0][0])[x] = 0u;
-    for (int x = threadIdx.x; x < min(kWindow, pages - w0); x += kThreads)
-      sh.l.table[x] = p.table[b * p.table_sb + w0 + x];
-    __syncthreads();
-    for (int x = threadIdx.x; x < toks * p.n; x += kThreads) {
-      const int t = x / p.n, blk = lists[x] - w0;
-      const int most = min(long_pages(p, long_seen(p, lens, tok0 + t)) - w0, kWindow);
-      if (blk >= 0 && blk < most) atomicOr(&sh.l.bits[t][blk >> 5], 1u << (blk & 31));
+    uint32_t mine = 0, at = 0;  // pages that this thread lists: bits from `from` on
+    int from = 0, id = -1;
+    if (direct) {
+      const int x = threadIdx.x;
+      int page = head;
+      if (page >= total) page = -1;
+      if (x < kListThreads) sh.l.table[x] = page;
+      if (page >= 0) id = p.table[b * p.table_sb + page];
+      __syncthreads();
+      bool take = page >= 0;  // (named before: counted once)
+      for (int e = 0; e < p.n; ++e) take &= e >= x || sh.l.table[e] != page;
+      mine = take ? 1u : 0u;
+      from = page;
+    } else {
+      for (int x = threadIdx.x; x < kRows * (kWindow / 32); x += kThreads) (&sh.l.bits[0][0])[x] = 0u;
+      if (threadIdx.x == 0) sh.l.next = total;
+      for (int x = threadIdx.x; x < min(kWindow, pages - w0); x += kThreads)
+        sh.l.table[x] = p.table[b * p.table_sb + w0 + x];
+      __syncthreads();
+      for (int x = threadIdx.x; x < toks * p.n; x += kThreads) {
+        const int t = x / p.n, page = x == static_cast<int>(threadIdx.x) ? head : lists[x];
+        if (page < w0 || page >= long_pages(p, long_seen(p, lens, tok0 + t))) continue;
+        if (page < w0 + kWindow)
+          atomicOr(&sh.l.bits[t][(page - w0) >> 5], 1u << ((page - w0) & 31));
+        else
+          atomicMin(&sh.l.next, page);
+      }
+      __syncthreads();
+      next = sh.l.next & ~31;  // (a multiple of 32, as all windows' first pages; total: the loop ends)
+      if (sh.l.next == total) next = total;
+      if (threadIdx.x < kListThreads) {  // 8 pages a thread
+        from = threadIdx.x * 8;
+        for (int t = 0; t < toks; ++t) mine |= sh.l.bits[t][from >> 5];
+        mine = (mine >> (from & 31)) & 255u;
+      }
     }
-    __syncthreads();
-    // the pages that have a bit, in order: thread x has 8 of them
-    uint32_t mine = 0, at = 0;
-    const int word = threadIdx.x / 4, sft = (threadIdx.x % 4) * 8;
+    // the pages that have a bit, in order
+    const uint32_t n_mine = __popc(mine);
     if (threadIdx.x < kListThreads) {
-      for (int t = 0; t < toks; ++t) mine |= sh.l.bits[t][word];
-      mine = (mine >> sft) & 255u;
-      at = __popc(mine);
+      at = n_mine;
 #pragma unroll
       for (int s = 1; s < 32; s *= 2) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, at, s);
@@ -190,20 +226,25 @@ __global__ void __launch_bounds__(32 * blocks_warps(NT), 2) blocks_kernel(const 
     }
     __syncthreads();
     int count = 0;
-    at -= __popc(mine);
+    at -= n_mine;
 #pragma unroll
     for (int s = 0; s < kListThreads / 32; ++s) {
       if (s < warp) at += sh.l.sums[s];
       count += sh.l.sums[s];
     }
-    while (mine != 0u) {
-      const int k = __ffs(mine) - 1, blk = word * 32 + sft + k;
-      mine &= mine - 1;
-      uint32_t who = 0;
-      for (int t = 0; t < toks; ++t) who |= ((sh.l.bits[t][word] >> (sft + k)) & 1u) << t;
-      sh.l.entry[at] = Entry{w0 + blk, sh.l.table[blk]};
-      sh.l.who[at] = static_cast<uint16_t>(who);
-      ++at;
+    if (direct) {
+      if (mine != 0u) {
+        sh.l.entry[at] = Entry{from, id};
+        sh.l.who[at] = 1;
+      }
+    } else {
+      for (; mine != 0u; mine &= mine - 1, ++at) {
+        const int page = from + __ffs(mine) - 1;
+        uint32_t who = 0;
+        for (int t = 0; t < toks; ++t) who |= ((sh.l.bits[t][page >> 5] >> (page & 31)) & 1u) << t;
+        sh.l.entry[at] = Entry{w0 + page, sh.l.table[page]};
+        sh.l.who[at] = static_cast<uint16_t>(who);
+      }
     }
     __syncthreads();
 

@@ -11,16 +11,27 @@
 //   warp 5     products: S = Q K^T, one stage ahead of O += P V (P as bf16 in TMEM over S)
 // Neighbouring queries select much the same pages, so a page is read once for (128 / G)
 // queries, and its products serve most rows. What pages those are is worked out by all
-// warps for kTileWindow pages of the sequence at a time.
+// warps for a window of the sequence at a time.
+//
+// What bounds it is a stage's chain: S, softmax, P V, some 1200 cycles for a CTA alone, 1800
+// for two of them on a SM; 512 queries x 32 heads of two sequences, 32 pages of 64 each,
+// d = 128: 59 us (tiles of 16 rows with the matrix instruction of single warps: 124). What
+// made it shorter: which pages a row selected as a register word in the list's order rather
+// than three dependent reads of shared memory a stage (600 cycles), S read once, loaders of
+// keys and values apart.
 //
 // The running maximum is a whole number (log2 units) and moves only when a score passes it
-// by more than 8, so O in TMEM is seldom rescaled, and exactly.
+// by more than 8, so O in TMEM is seldom rescaled, and exactly. P is rounded to bf16 once
+// (the tensor core's input type; the sum takes the unrounded values): against 64 bits O is off
+// by 0.0023 of its norm, the rounding of the output alone is 0.0017. A second part of P, as the
+// form for few rows has it, would lengthen the stage's chain.
 #pragma once
 
 namespace attn {
 namespace dev {
 
-constexpr int kBlocksThreads = 224, kBlocksKeys = 64, kTileWindow = 256;
+constexpr int kBlocksThreads = 224, kBlocksKeys = 64;
+constexpr int kWindowMost = 1024, kWindowBits = 256 * 128;  // pages of a window: 256, for fewer queries more
 constexpr int kWarpK = 4, kWarpMma = 5, kWarpV = 6;
 constexpr float kBlocksSlack = 8.f;
 constexpr uint32_t kBlocksCols = 256;  // TMEM: S_0 [0, 64), S_1 [64, 128) (P over their first 32), O from 128
@@ -41,17 +52,17 @@ struct BlocksSmem {
   static constexpr uint32_t kLayout = D >= 64 ? 2u : 4u;
 };
 
-constexpr int kWindowWords = kTileWindow / 32;
 struct BlocksLists {
-  uint32_t bits[128][kWindowWords];  // of each query of the tile: pages of the window that it selected,
-  uint32_t took[128][kWindowWords];  // and, of the pages listed, which those are
-  uint32_t any[kWindowWords];
-  uint16_t page[kTileWindow];        // the pages that have a bit, from the window's first
-  int32_t id[kTileWindow];
+  uint32_t bits[kWindowBits / 32];  // of each query of the tile: pages of the window that it selected,
+  uint32_t took[kWindowBits / 32];  // and, of the pages listed, which those are
+  uint32_t any[kWindowMost / 32];
+  uint16_t page[kWindowMost];       // the pages that have a bit, from the window's first
+  int32_t id[kWindowMost];
   uint64_t bars[13];
   uint32_t tmem;
   uint32_t abort;
   int count;
+  int next;  // the first page behind the window that a query selected
 };
 
 struct BlocksBars {
@@ -212,7 +223,8 @@ __device__ __forceinline__ void tmem_ld32x2(uint32_t ta, uint32_t (&a)[32], uint
 // What a softmax thread keeps of its row.
 struct BlocksRow {
   uint32_t tl;      // TMEM address of its lane
-  int tok, seen;    // its query in the tile, and slots that it sees
+  const uint32_t* took;  // of its query, in shared memory
+  int seen;         // slots that it sees
   float c;          // scale * log2(e)
   float m, sum;     // running maximum and sum
   uint32_t word;    // of the 32 pages listed from a multiple of 32 on, which the query selected
@@ -245,7 +257,7 @@ __device__ __forceinline__ bool blocks_softmax(const BlocksLists& l, const Block
   uint32_t lim[4] = {0u, 0u, 0u, 0u};
   if (st.sub == 0) {  // one page
     const int e = s >> st.cut;
-    if ((e & 31) == 0) r.word = l.took[r.tok][e >> 5];
+    if ((e & 31) == 0) r.word = r.took[e >> 5];
     if ((r.word >> (e & 31)) & 1u) {
       const int pos = ((w0 + l.page[e]) << st.page_shift) + st.slot(s);
 #pragma unroll
@@ -253,7 +265,7 @@ __device__ __forceinline__ bool blocks_softmax(const BlocksLists& l, const Block
     }
   } else {  // two or four (their bits lie in one word)
     const int e0 = s << st.sub, left = l.count - e0;
-    const uint32_t took = l.took[r.tok][e0 >> 5] >> (e0 & 31);
+    const uint32_t took = r.took[e0 >> 5] >> (e0 & 31);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int i = g >> (2 - st.sub);
@@ -325,7 +337,13 @@ __device__ __forceinline__ bool blocks_softmax(const BlocksLists& l, const Block
   return true;
 }
 
-template <int D>
+// Wide: windows of up to 1024 pages, for tables of more than 256: each window is three
+// barriers, a pass over the lists and a pipeline that starts anew. (512 queries x 32 heads,
+// d = 128, 65536 tokens, 32 pages of much the same ones a query: 64 us and not 72 with pages of
+// 64, 36 and not 76 with 16; 32768 tokens, 8 heads, d = 64: 34 and 33, with 16 pages of 64 at
+// random 318 and 305. Tables of up to 256 pages: 59.3 with the width known to the compiler,
+// 61.2 without.)
+template <int D, bool Wide>
 __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_constant__ BlocksTiles a) {
   using S = BlocksSmem<D>;
   const LongParams& p = a.p;
@@ -383,7 +401,6 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
   const int row = static_cast<int>(threadIdx.x) & 127, n_mine = p.by_g.div(r0 + min(row, rn - 1));
   BlocksRow r;
   r.tl = tmem + (static_cast<uint32_t>(warp) << 21);
-  r.tok = n_mine - tok0;
   r.seen = row < rn ? long_seen(p, lens, n_mine) : 0;
   r.c = p.c_hi;
   r.m = -INFINITY;
@@ -392,25 +409,43 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
   int gs = 0;  // stages so far
   bool ok = true;
 
-  for (int w0 = 0; w0 < pages; w0 += kTileWindow) {
+  // a window: 256 pages, or as many as the bits hold for so many queries
+  const int words = Wide ? (toks <= 32 ? 32 : toks <= 64 ? 16 : 8) : 8, window = words * 32;
+  r.took = l.took + (n_mine - tok0) * words;
+  for (int w0 = 0, next; w0 < pages; w0 = next) {
     __syncthreads();  // the lists of the window before are done with
-    for (int x = threadIdx.x; x < toks * kWindowWords; x += kBlocksThreads) (&l.bits[0][0])[x] = (&l.took[0][0])[x] = 0u;
-    if (threadIdx.x < kWindowWords) l.any[threadIdx.x] = 0u;
+    for (int x = threadIdx.x; x < toks * words; x += kBlocksThreads) l.bits[x] = l.took[x] = 0u;
+    if (static_cast<int>(threadIdx.x) < words) l.any[threadIdx.x] = 0u;
+    if (threadIdx.x == 0) l.next = pages;
     __syncthreads();
-    for (int x = threadIdx.x; x < toks * p.n; x += kBlocksThreads) {
-      const int t = x / p.n, page = lists[x] - w0;
-      const int most = min(long_pages(p, long_seen(p, lens, tok0 + t)) - w0, kTileWindow);
-      if (page >= 0 && page < most) {
-        atomicOr(&l.bits[t][page >> 5], 1u << (page & 31));
-        atomicOr(&l.any[page >> 5], 1u << (page & 31));
+    constexpr int kBatch = 5;  // entries on their way to a thread at once
+    for (int x0 = threadIdx.x; x0 < toks * p.n; x0 += kBatch * kBlocksThreads) {
+      int page[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int x = x0 + i * kBlocksThreads;
+        page[i] = x < toks * p.n ? lists[x] : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        if (page[i] < w0) continue;
+        const int t = (x0 + i * kBlocksThreads) / p.n, at = page[i] - w0;
+        if (page[i] >= long_pages(p, long_seen(p, lens, tok0 + t))) continue;
+        if (at >= window) {
+          atomicMin(&l.next, page[i]);
+          continue;
+        }
+        atomicOr(&l.bits[t * words + (at >> 5)], 1u << (at & 31));
+        atomicOr(&l.any[at >> 5], 1u << (at & 31));
       }
     }
     ldev::copy_wait<0>();
     fence_async_smem();
     __syncthreads();
-    if (warp == 0) {  // a lane has 8 pages
-      static_assert(kTileWindow == 32 * 8, "a byte of the bits a lane");
-      uint32_t mine = (l.any[lane >> 2] >> ((lane & 3) * 8)) & 0xFFu, at = __popc(mine);
+    next = l.next == pages ? pages : l.next & ~31;  // (all windows begin at a multiple of 32)
+    if (warp == 0) {  // a lane has a word of the pages, or part of one
+      const int per = words, first = lane * per;
+      uint32_t mine = (l.any[first >> 5] >> (first & 31)) & (per == 32 ? 0xFFFFFFFFu : (1u << per) - 1u), at = __popc(mine);
 #pragma unroll
       for (int s = 1; s < 32; s *= 2) {
         const uint32_t y = __shfl_up_sync(0xffffffffu, at, s);
@@ -418,7 +453,7 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
       }
       if (lane == 31) l.count = static_cast<int>(at);
       at -= __popc(mine);
-      for (; mine != 0u; mine &= mine - 1, ++at) l.page[at] = static_cast<uint16_t>(lane * 8 + __ffs(mine) - 1);
+      for (; mine != 0u; mine &= mine - 1, ++at) l.page[at] = static_cast<uint16_t>(first + __ffs(mine) - 1);
     }
     __syncthreads();
     const int count = l.count;
@@ -430,10 +465,10 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
       uint32_t z = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int page = l.page[e0 + e];  // (behind the list: any page of the window, or a value left there)
-        if (e0 + e < count) z |= ((l.bits[t][page >> 5] >> (page & 31)) & 1u) << e;
+        const int page = l.page[e0 + e];  // (behind the list: a value left there)
+        if (e0 + e < count) z |= ((l.bits[t * words + (page >> 5)] >> (page & 31)) & 1u) << e;
       }
-      reinterpret_cast<uint8_t*>(l.took[t])[e0 >> 3] = static_cast<uint8_t>(z);
+      reinterpret_cast<uint8_t*>(l.took + t * words)[e0 >> 3] = static_cast<uint8_t>(z);
     }
     __syncthreads();
     const int n = st.count(count);
@@ -488,13 +523,13 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
   if (warp == kWarpMma) tmem_dealloc(tmem, kBlocksCols);
 }
 
-template <int D>
+template <int D, bool Wide>
 cudaError_t blocks_tiles_dim(const BlocksTiles& a, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(a.p.Nq) * a.p.G;
   const cudaError_t e =
-      cudaFuncSetAttribute(blocks_tiles<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, BlocksSmem<D>::kBytes);
+      cudaFuncSetAttribute(blocks_tiles<D, Wide>, cudaFuncAttributeMaxDynamicSharedMemorySize, BlocksSmem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  return ldev::launch(blocks_tiles<D>, dim3(static_cast<unsigned>((rows + 127) / 128), a.p.Hk, a.p.B), kBlocksThreads,
+  return ldev::launch(blocks_tiles<D, Wide>, dim3(static_cast<unsigned>((rows + 127) / 128), a.p.Hk, a.p.B), kBlocksThreads,
                       static_cast<size_t>(BlocksSmem<D>::kBytes), s, 1, a);
 }
 

@@ -12,6 +12,12 @@
 // reduce tile t - 1 and the rows of tile t + 1 are on their way. (One thread a lane: 512
 // tokens' scores 26.5 us, 333 rows' weights 38.9.)
 //
+// What bounds them is instructions: of some 200 that a warp issues for 64 rows of weights
+// only 64 are the exponentials and sums of its 32 columns; the others bring rows, place
+// their lse, wait. 333 rows x 15 heads of d = 64 over 23204 tokens: 34.5 us, 0.27 PFLOP/s (exp2
+// alone would take 9); 512 tokens x 32 heads of d = 128 over the bounds of 1128 pages: 24 us,
+// 25 MB of scores written among it.
+//
 // Every wait is bounded: when one runs out the CTA notes it in the status word, leaves its
 // loop, waits (bounded) for its products in flight, frees TMEM and returns.
 #include <math_constants.h>
@@ -554,10 +560,11 @@ cudaError_t launch_blocks_tiles(const LongParams& p, const CUtensorMap& tm_k, co
   a.p = p;
   a.tm_k = tm_k;
   a.tm_v = tm_v;
+  const bool wide = p.table_width > 256;
   switch (d) {
-    case 32: return dev::blocks_tiles_dim<32>(a, s);
-    case 64: return dev::blocks_tiles_dim<64>(a, s);
-    case 128: return dev::blocks_tiles_dim<128>(a, s);
+    case 32: return wide ? dev::blocks_tiles_dim<32, true>(a, s) : dev::blocks_tiles_dim<32, false>(a, s);
+    case 64: return wide ? dev::blocks_tiles_dim<64, true>(a, s) : dev::blocks_tiles_dim<64, false>(a, s);
+    case 128: return wide ? dev::blocks_tiles_dim<128, true>(a, s) : dev::blocks_tiles_dim<128, false>(a, s);
     default: return cudaErrorInvalidValue;
   }
 }

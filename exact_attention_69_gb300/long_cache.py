@@ -16,7 +16,7 @@ in the block table; a prefix that sequences share is pages that several rows nam
 
 A decoding step over a long cache:
 
-    kv_append(...)                                        # the new token
+    q = kv_append(...)                                    # the new token
     kv_bounds(k_cache, bounds, table, lens, n_new=1)      # its page's bounds
     scores = block_scores(q, bounds, table, lens, page_size=page)
     pages = block_select(scores, lens, 32, page_size=page)
@@ -133,6 +133,7 @@ def kv_bounds(k_cache: torch.Tensor, bounds: torch.Tensor, block_table: torch.Te
     channel over the page's slots below the sequence's end. Pages that hold one of the
     newest `n_new` tokens of each sequence (kv_lens [B] counts them in) are looked at,
     each whole; None: every page that holds a token. Exact; NaN keys give NaN bounds.
+    Sequences may share pages that are full in each.
     """
     if n_new is not None and int(n_new) < 0:
         raise ValueError("n_new must be >= 0")

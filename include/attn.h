@@ -500,7 +500,8 @@ int64_t attn_paged_workspace_bytes(const attn_paged_params* p);
  * ATTN_MASK_NONE all of them. Lengths, tables and lists are read on the device when the
  * kernels run; lengths are clamped, a table entry that is not a page of the cache reads
  * as zeros and is never written. Pages that a call writes must not be shared between
- * sequences. Slots behind a sequence's end may hold anything.
+ * sequences (bounds may be, where the page is full in each). Slots behind a sequence's
+ * end may hold anything.
  *
  * One parameter block serves the six calls; each names the fields that it reads, and
  * takes the sizes (B, Hk, d, n_pages, page_size, table_width) with the table always.

@@ -271,6 +271,43 @@ def test_blocks_of_wide_tables(E, full):
     p.check_blocks(E, p.lists(30, seed=2), full_tiles=full)
 
 
+@FORMS
+@pytest.mark.parametrize("n", [1, 2, 31, 40, 127, 128, 129, 200])
+@pytest.mark.parametrize("Hq,Hk,d,lens,page", [
+    (4, 2, 64, [16 * 90 + 5, 1, 0, 300], 16),
+    (3, 1, 128, [64 * 150 + 63], 64),
+    (10, 1, 32, [32 * 20, 32 * 64 + 1], 32),
+], ids=str)
+def test_blocks_of_one_query(E, Hq, Hk, d, lens, page, n, full):
+    """Lists shorter and longer than what a block takes at once, many entries twice or more."""
+    p = Problem(Hq, Hk, d, 1, lens, page, seed=540 + n)
+    p.check_blocks(E, p.lists(n, seed=n), full_tiles=full)
+
+
+@FORMS
+@pytest.mark.parametrize("Hq,Hk,d,Nq,lens,page,n", [
+    (4, 1, 32, 20, [16 * 2600 + 9, 16 * 1025], 16, 5),    # 20 queries a tile
+    (2, 1, 64, 70, [16 * 1100 + 1, 16 * 511 + 3], 16, 4),  # up to 64
+    (1, 1, 32, 150, [16 * 800 + 2, 16 * 257], 16, 3),     # up to 128
+], ids=str)
+@pytest.mark.parametrize("spread", ["anywhere", "ends", "edges", "last", "none"])
+def test_blocks_far_apart(E, Hq, Hk, d, Nq, lens, page, n, spread, full):
+    """Pages at random, at the two ends, next to multiples of 256, the last alone, none."""
+    p = Problem(Hq, Hk, d, Nq, lens, page, seed=545)
+    W = p.table.shape[1]
+    lists = p.lists(n, seed=7)
+    last = ((p.lens - 1) // page)[:, None, None, None].expand_as(lists)
+    if spread == "ends":
+        lists = torch.where(lists % 2 == 0, lists % 5, last - lists % 5)
+    elif spread == "edges":
+        lists = lists // 256 * 256 + lists % 3 - 1
+    elif spread == "last":
+        lists = last.clone()
+    elif spread == "none":
+        lists = torch.where(lists % 2 == 0, -1, W + 5)
+    p.check_blocks(E, lists.int().contiguous(), full_tiles=full)
+
+
 @pytest.mark.parametrize("Hq,Hk,d,Nq,lens,page,q_lens,n", [
     # enough rows for tiles of 128 by the rule: one query after another, heads that do not
     # divide a tile, pages smaller and larger than a stage, ragged counts, a short sequence
