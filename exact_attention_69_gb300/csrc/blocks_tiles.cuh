@@ -11,14 +11,16 @@
 //   warp 5     products: S = Q K^T, one stage ahead of O += P V (P as bf16 in TMEM over S)
 // Neighbouring queries select much the same pages, so a page is read once for (128 / G)
 // queries, and its products serve most rows. What pages those are is worked out by all
-// warps for a window of the sequence at a time.
+// warps for a window of the sequence at a time. Where tiles are few, the CTAs of a cluster share
+// a window's stages and join through each other's shared memory: one launch, a fixed order.
 //
 // What bounds it is a stage's chain: S, softmax, P V, some 1200 cycles for a CTA alone, 1800
-// for two of them on a SM; 512 queries x 32 heads of two sequences, 32 pages of 64 each,
-// d = 128: 59 us (tiles of 16 rows with the matrix instruction of single warps: 124). What
-// made it shorter: which pages a row selected as a register word in the list's order rather
-// than three dependent reads of shared memory a stage (600 cycles), S read once, loaders of
-// keys and values apart.
+// for two of them on a SM, and around it the lists and the join; 512 queries x 32 heads of two
+// sequences, half of them padding, 32 pages of 64 each, d = 128: 44 us (59 by one CTA a tile: 16
+// stages on average, but 68 for the longest; 124 by tiles of 16 rows). What made it shorter:
+// which pages a row selected as a register word in the list's order rather than three
+// dependent reads of shared memory a stage (600 cycles), S read once, loaders of keys and
+// values apart.
 //
 // The running maximum is a whole number (log2 units) and moves only when a score passes it
 // by more than 8, so O in TMEM is seldom rescaled, and exactly. P is rounded to bf16 once
@@ -50,6 +52,7 @@ struct BlocksSmem {
   static constexpr int kOffK = kQ, kOffV = kOffK + 2 * kKV;
   static constexpr int kBytes = kOffV + 2 * kKV + 1024;
   static constexpr uint32_t kLayout = D >= 64 ? 2u : 4u;
+  static_assert(4 * kKV == 128 * D * 4, "a part of O takes the place of K and V");
 };
 
 struct BlocksLists {
@@ -92,14 +95,14 @@ __device__ __forceinline__ bool blocks_wait(uint32_t bar, uint32_t parity, const
   return ctl_wait(bar, parity, c, tile, kRoleTiles, honour);
 }
 
-// Keys (VALUES: values) of a window's stages. One warp each: a stage's keys are done with
+// Keys (VALUES: values) of stages [first, end) of a window. One warp each: a stage's keys are done with
 // earlier than its values, and the next ones need not wait for these.
 template <int D, bool VALUES>
 __device__ __forceinline__ bool blocks_load(const BlocksTiles& a, const BlocksLists& l, uint32_t base, const BlocksBars& bars,
-                                            const Stages& st, int hk, int n, int& gs, const Ctl& ctl) {
+                                            const Stages& st, int hk, int first, int end, int& gs, const Ctl& ctl) {
   using S = BlocksSmem<D>;
   const uint64_t pol = l2_policy_evict_last();
-  for (int s = 0; s < n; ++s, ++gs) {
+  for (int s = first; s < end; ++s, ++gs) {
     const int slot = gs & 1, at = st.slot(s);
     if (!blocks_wait(VALUES ? bars.v_empty(slot) : bars.k_empty(slot), ((gs >> 1) & 1) ^ 1u, ctl, gs)) return false;
     const uint32_t full = VALUES ? bars.v_full(slot) : bars.k_full(slot);
@@ -167,15 +170,16 @@ __device__ __noinline__ void blocks_clear(const BlocksLists& l, uint8_t* values,
   __syncwarp();
 }
 
-// The products of a window's stages: S of one, then O += P V of the one before.
+// The products of stages [first, end): S of one, then O += P V of the one before.
 template <int D>
 __device__ __forceinline__ bool blocks_mma(const BlocksMma<D>& mm, const BlocksLists& l, uint8_t* smem, const BlocksBars& bars,
-                                           const Stages& st, int len, int w0, int n, int& gs, const Ctl& ctl) {
+                                           const Stages& st, int len, int w0, int first, int end, int& gs,
+                                           const Ctl& ctl) {
   using S = BlocksSmem<D>;
   // only the last page listed can hold slots behind the sequence's end
-  const int last = l.count - 1, dead = ((w0 + l.page[last] + 1) << st.page_shift) > len ? (last << st.cut) >> st.sub : n;
-  for (int s = 0; s <= n; ++s) {
-    if (s < n) {
+  const int last = l.count - 1, dead = ((w0 + l.page[last] + 1) << st.page_shift) > len ? (last << st.cut) >> st.sub : end;
+  for (int s = first; s <= end; ++s) {
+    if (s < end) {
       const int slot = gs & 1;
       if (!blocks_wait(bars.k_full(slot), (gs >> 1) & 1, ctl, gs)) return false;
       tc_fence_after();
@@ -185,8 +189,8 @@ __device__ __forceinline__ bool blocks_mma(const BlocksMma<D>& mm, const BlocksL
       mma_commit(bars.k_empty(slot));
       ++gs;
     }
-    if (s > 0) {
-      const int x = gs - 1 - (s < n), slot = x & 1;
+    if (s > first) {
+      const int x = gs - 1 - (s < end), slot = x & 1;
       const uint32_t parity = (x >> 1) & 1;
       if (!blocks_wait(bars.v_full(slot), parity, ctl, x)) return false;
       if (s - 1 >= dead) blocks_clear<D>(l, smem + S::kOffV + slot * S::kKV, st.page_shift, len, w0, s - 1);
@@ -337,6 +341,62 @@ __device__ __forceinline__ bool blocks_softmax(const BlocksLists& l, const Block
   return true;
 }
 
+// A row's part of O, its maximum and sum, to shared memory: 4 channels of all rows after 4
+// channels of all rows, in the place of the keys and values, which are done with.
+template <int D>
+__device__ __forceinline__ void blocks_part(uint8_t* part, float2* ml, const BlocksRow& r, int row, bool some) {
+  ml[row] = make_float2(r.m, r.sum);
+  if (!some) return;  // (nothing reads O of a sum of 0)
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t o[32];
+    tmem_ld32(r.tl + 128 + c, o);
+#pragma unroll
+    for (int x = 0; x < 32; x += 4)
+      reinterpret_cast<uint4*>(part)[(c + x) / 4 * 128 + row] = make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+  }
+}
+
+// The cluster's parts of a row joined, in the order of its CTAs: this CTA's share of the
+// channels (8 at least), the first also the LSE.
+template <int D>
+__device__ __forceinline__ void blocks_join(uint32_t part, uint32_t ml, int splits, int split, int row, __nv_bfloat16* out,
+                                            float* lse) {
+  float f[kBlocksMaxSplits], top = -INFINITY, sum = 0.f;
+  bool some[kBlocksMaxSplits];
+#pragma unroll
+  for (int i = 0; i < kBlocksMaxSplits; ++i)
+    if (i < splits) {
+      const float2 y = ldev::peer_f2(ml + row * 8, i);
+      f[i] = y.x;
+      some[i] = y.y != 0.f;
+      top = fmaxf(top, y.x);
+    }
+#pragma unroll
+  for (int i = 0; i < kBlocksMaxSplits; ++i)
+    if (i < splits) {
+      f[i] = some[i] ? ex2(f[i] - (top == -INFINITY ? 0.f : top)) : 0.f;
+      sum += some[i] ? f[i] * ldev::peer_f2(ml + row * 8, i).y : 0.f;
+    }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  if (split == 0 && lse != nullptr) *lse = CUDART_LN2_F * (top + log2f(sum));
+  if (out == nullptr) return;
+  const int per = D / splits;
+#pragma unroll 1
+  for (int c = split * per; c < (split + 1) * per; c += 8) {
+    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < kBlocksMaxSplits; ++i)
+      if (i < splits && some[i]) {
+        const float4 x = ldev::peer_f4(part + (c / 4 * 128 + row) * 16, i), y = ldev::peer_f4(part + (c / 4 * 128 + 128 + row) * 16, i);
+        acc[0] += f[i] * x.x, acc[1] += f[i] * x.y, acc[2] += f[i] * x.z, acc[3] += f[i] * x.w;
+        acc[4] += f[i] * y.x, acc[5] += f[i] * y.y, acc[6] += f[i] * y.z, acc[7] += f[i] * y.w;
+      }
+    *reinterpret_cast<uint4*>(out + c) = make_uint4(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv),
+                                                    pack_bf16(acc[4] * inv, acc[5] * inv), pack_bf16(acc[6] * inv, acc[7] * inv));
+  }
+}
+
 // Wide: windows of up to 1024 pages, for tables of more than 256: each window is three
 // barriers, a pass over the lists and a pipeline that starts anew. (512 queries x 32 heads,
 // d = 128, 65536 tokens, 32 pages of much the same ones a query: 64 us and not 72 with pages of
@@ -381,7 +441,8 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
   ldev::grid_dep_wait();
 
   const int b = blockIdx.z, hk = blockIdx.y, G = p.G;
-  const int all = p.Nq * G, r0 = static_cast<int>(blockIdx.x) * 128, rn = min(all - r0, 128);
+  const int split = static_cast<int>(blockIdx.x) % p.splits;
+  const int all = p.Nq * G, r0 = static_cast<int>(blockIdx.x) / p.splits * 128, rn = min(all - r0, 128);
   const int tok0 = p.by_g.div(r0), toks = p.by_g.div(r0 + rn - 1) - tok0 + 1;
   const LongLens lens = long_lens(p, b);
   const int live = min(tok0 + toks, lens.ql);  // queries of the tile that are real: [tok0, live)
@@ -471,16 +532,17 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
       reinterpret_cast<uint8_t*>(l.took + t * words)[e0 >> 3] = static_cast<uint8_t>(z);
     }
     __syncthreads();
-    const int n = st.count(count);
-    if (n > 0) {
+    const int n = st.count(count), first = n * split / p.splits, end = n * (split + 1) / p.splits;
+    if (first < end) {
       if (warp == kWarpK) {
-        ok = blocks_load<D, false>(a, l, base, bars, st, hk, n, gs, ctl);
+        ok = blocks_load<D, false>(a, l, base, bars, st, hk, first, end, gs, ctl);
       } else if (warp == kWarpV) {
-        ok = blocks_load<D, true>(a, l, base, bars, st, hk, n, gs, ctl);
+        ok = blocks_load<D, true>(a, l, base, bars, st, hk, first, end, gs, ctl);
       } else if (warp == kWarpMma) {
-        ok = blocks_mma<D>(BlocksMma<D>(base, tmem), l, smem, bars, st, lens.len, w0, n, gs, ctl);
+        ok = blocks_mma<D>(BlocksMma<D>(base, tmem), l, smem, bars, st, lens.len, w0, first, end, gs, ctl);
       } else {
-        for (int s = 0; s < n && ok; ++s, ++gs) ok = blocks_softmax<D>(l, bars, st, w0, s, gs, r, ctl);
+        r.word = r.took[st.entry(first, 0) >> 5];
+        for (int s = first; s < end && ok; ++s, ++gs) ok = blocks_softmax<D>(l, bars, st, w0, s, gs, r, ctl);
       }
     }
     if (__syncthreads_or(!ok)) break;
@@ -492,34 +554,45 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
       tc_fence_after();
     }
     const int g = r0 + row - n_mine * G, h = hk * G + g;
-    const float inv = r.sum == 0.f ? 0.f : 1.f / r.sum;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + b * p.o_sb + h * p.o_sh + n_mine * p.o_sn;
+    float* lse = p.lse == nullptr || row >= rn ? nullptr : p.lse + (static_cast<int64_t>(b) * p.Hq + h) * p.Nq + n_mine;
+    if (p.splits == 1) {
+      const float inv = r.sum == 0.f ? 0.f : 1.f / r.sum;
 #pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-      uint32_t o[32];
-      if (gs > 0) tmem_ld32(r.tl + 128 + c, o);
-      if (row < rn) {
+      for (int c = 0; c < D; c += 32) {
+        uint32_t o[32];
+        if (gs > 0) tmem_ld32(r.tl + 128 + c, o);
+        if (row < rn) {
 #pragma unroll
-        for (int x = 0; x < 32; x += 8) {
-          uint32_t y[4];
+          for (int x = 0; x < 32; x += 8) {
+            uint32_t y[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            y[i] = r.sum == 0.f ? 0u : pack_bf16(__uint_as_float(o[x + 2 * i]) * inv, __uint_as_float(o[x + 2 * i + 1]) * inv);
-          *reinterpret_cast<uint4*>(out + c + x) = make_uint4(y[0], y[1], y[2], y[3]);
+            for (int i = 0; i < 4; ++i)
+              y[i] = r.sum == 0.f ? 0u : pack_bf16(__uint_as_float(o[x + 2 * i]) * inv, __uint_as_float(o[x + 2 * i + 1]) * inv);
+            *reinterpret_cast<uint4*>(out + c + x) = make_uint4(y[0], y[1], y[2], y[3]);
+          }
         }
       }
+      if (lse != nullptr) *lse = CUDART_LN2_F * (r.m + log2f(r.sum));
+    } else {
+      blocks_part<D>(smem + S::kOffK, reinterpret_cast<float2*>(l.bits), r, row, gs > 0);
+      ldev::cluster_sync();
+      blocks_join<D>(base + S::kOffK, smem_u32(l.bits), p.splits, split, row, row < rn ? out : nullptr, lse);
     }
-    if (row < rn && p.lse != nullptr)
-      p.lse[(static_cast<int64_t>(b) * p.Hq + h) * p.Nq + n_mine] = CUDART_LN2_F * (r.m + log2f(r.sum));
+  } else if (p.splits > 1) {
+    ldev::cluster_sync();
   }
   if (l.abort != 0u && (warp == kWarpK || warp == kWarpV)) {
     // copies in flight land in this CTA's shared memory: wait (bounded) for the last ones
-    for (int x = max(gs - 2, p.inject); x < gs; ++x)  // (what inject withheld never comes)
+    for (int x = max(gs - 2, warp == kWarpK ? p.inject : 0); x < gs; ++x)  // (the keys that inject withheld never come)
       blocks_wait(warp == kWarpV ? bars.v_full(x & 1) : bars.k_full(x & 1), (x >> 1) & 1, ctl, x, false);
   }
   ldev::copy_wait<0>();  // (no page, no wait so far)
   tc_fence_before();
-  __syncthreads();
+  if (p.splits > 1)
+    ldev::cluster_sync();  // (no CTA leaves while another reads its part)
+  else
+    __syncthreads();
   if (warp == kWarpMma) tmem_dealloc(tmem, kBlocksCols);
 }
 
@@ -529,8 +602,8 @@ cudaError_t blocks_tiles_dim(const BlocksTiles& a, cudaStream_t s) {
   const cudaError_t e =
       cudaFuncSetAttribute(blocks_tiles<D, Wide>, cudaFuncAttributeMaxDynamicSharedMemorySize, BlocksSmem<D>::kBytes);
   if (e != cudaSuccess) return e;
-  return ldev::launch(blocks_tiles<D, Wide>, dim3(static_cast<unsigned>((rows + 127) / 128), a.p.Hk, a.p.B), kBlocksThreads,
-                      static_cast<size_t>(BlocksSmem<D>::kBytes), s, 1, a);
+  return ldev::launch(blocks_tiles<D, Wide>, dim3(static_cast<unsigned>((rows + 127) / 128 * a.p.splits), a.p.Hk, a.p.B),
+                      kBlocksThreads, static_cast<size_t>(BlocksSmem<D>::kBytes), s, a.p.splits, a);
 }
 
 }  // namespace dev

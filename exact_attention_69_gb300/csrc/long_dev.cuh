@@ -109,6 +109,31 @@ __host__ __device__ constexpr int row_bytes() {
   return D == 32 ? 64 : 2 * D + 64;
 }
 
+// All threads of the cluster; what they wrote before is seen by its other CTAs.
+__device__ __forceinline__ void cluster_sync() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The same shared address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer(uint32_t addr, int rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ float2 peer_f2(uint32_t addr, int rank) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(peer(addr, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 peer_f4(uint32_t addr, int rank) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(peer(addr, rank))
+               : "memory");
+  return v;
+}
+
 template <typename... Args, typename... Given>
 cudaError_t launch(void (*kern)(Args...), dim3 grid, int threads, size_t smem, cudaStream_t s, int cluster,
                    const Given&... args) {

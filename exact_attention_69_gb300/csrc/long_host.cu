@@ -153,27 +153,49 @@ int blocks_splits(const attn_long_params* p, int sms) {
   return s;
 }
 
-// attn_blocks: whether to take tiles of 128 rows. Such a tile reads a page once for up to
-// 128 rows, but goes over its pages one after the other; groups of 16 rows are eight times
-// as many tasks. So: 64 rows of a sequence and key head, and 48 a SM in all. Measured (us;
-// 32 of 256 pages of 64 a query, d = 128, G = 4 unless said; queries that select much the
+// attn_blocks, tiles of 128 rows: CTAs that share a tile's stages of 64 keys, each with two of
+// them or more and 8 channels of O to join: as many as two CTAs a SM have room for. Work for
+// twice as many only makes two rounds, each with a start and a join (us; 64 tiles, by 4 and 8
+// CTAs a tile: 34 / 50; 128 tiles, 2 and 4: 40 / 52; 256, 1 and 2: 68 / 80). With q_lens, though,
+// a batch is padded, and half of the tiles are taken to have nothing (2 sequences x 512 queries
+// x 8 heads of G = 4, 256 tiles, half of the queries padding: 59 by one CTA, 44 by two, 55 by four).
+int blocks_tile_splits(const attn_long_params* p, int sms) {
+  const int64_t rows = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk);
+  const int64_t tiles = (rows + 127) / 128 * p->B * p->Hk >> (p->q_lens != nullptr);
+  const int64_t stages = (static_cast<int64_t>(p->n < p->table_width ? p->n : p->table_width) * p->page_size + 63) / 64;
+  int s = 1;
+  while (s < attn::kBlocksMaxSplits && 8 * s < p->d && tiles * s <= sms && 4 * s <= stages) s *= 2;
+  return s;
+}
+
+// attn_blocks: whether to take tiles of 128 rows. They read a page once for up to 128 rows and
+// multiply on full tiles, but take longer to begin and to join. So: where there are 16 rows
+// of a sequence and key head, and 12288 pairs of a row and a selected slot a SM in all. Measured
+// (us; d = 128, pages of 64, G = 4, 32 pages a query unless said; queries that select much the
 // same pages, and pages at random), tiles of 128 and of 16 rows:
-//   8 sequences x 8 key heads, 8 queries (14 rows a SM)   38 / 122   35 /  81
-//                              16        (27)             45 / 166   58 / 141
-//                              32        (54)             57 / 185  102 / 247
-//                             128        (216)            67 / 211  328 / 793
-//   1 x 8, 64 queries (14 rows a SM)                      47 / 157   30 /  66
-//         128         (27)                                48 / 162   50 / 119
-//         512         (108)                               55 / 196  180 / 433
-//   1 x 1, G = 8, 512 queries (27)                        40 / 140   45 /  68
-//   16 x 4, G = 7, 16 queries, d = 32 (47)                24 /  81   20 /  44
-//   4 x 4, G = 1, 512 queries, d = 64, 64 pages of 16 (54)  55 / 118   48 / 173
-constexpr int kFullTileRows = 64, kFullRowsPerSm = 48;
+//   32 sequences x 8 key heads, 2 queries (8 rows each)   53 /  76   52 /  76
+//                               4                         57 / 113   70 / 145
+//                               8                         61 / 143  116 / 252
+//   32 x 8, G = 16, 1 query                               48         56
+//   8 x 8,  4 queries (13800 pairs a SM)                  19 /  38   24 /  44
+//         128                                             68 / 216  352 / 843
+//   4 x 8,  4 queries (6900)                              15 /  21   17 /  26
+//   1 x 8, 16 queries (6900)                              16 /  32   15 /  26
+//          32 (13800)                                     18 /  36   21 /  41
+//         512                                             40 / 118  190 / 458
+//   4 x 2, G = 16, 8 queries, pages of 32, d = 64 (6900)  12 /  17   10 /  10
+//   4 x 4, 32 queries, 64 pages of 16, d = 64 (13800)     17 /  31   16 /  29
+//         128                                             20 /  45   41 /  90
+//   4 x 4, G = 1, 128 queries, 64 pages of 16, d = 64     36 /  54   19 /  56
+//   16 x 2, 32 queries, 16 pages of 16, d = 32 (6900)     12 /  29   10 /  17
+constexpr int kFullTileRows = 16, kFullPairsPerSm = 12288;
 
 bool blocks_full_tiles(const attn_long_params* p, int sms) {
   if (p->full_tiles != 0) return p->full_tiles == 1;
   const int64_t rows = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk);
-  return rows >= kFullTileRows && rows * p->B * p->Hk >= static_cast<int64_t>(kFullRowsPerSm) * sms;
+  const int64_t slots = static_cast<int64_t>(p->n < p->table_width ? p->n : p->table_width) * p->page_size;
+  return rows >= kFullTileRows &&
+         static_cast<double>(rows * p->B * p->Hk) * static_cast<double>(slots) >= static_cast<double>(kFullPairsPerSm) * sms;
 }
 
 int this_gpu() {
@@ -252,6 +274,7 @@ int attn_blocks(const attn_long_params* p) {
         (rc = encode_pages(encode, &tm_k, r.kc, p->d, p->page_size, p->Hk, p->n_pages, attn::kBlocksBox, ks, "k_cache")) != ATTN_OK ||
         (rc = encode_pages(encode, &tm_v, r.vc, p->d, p->page_size, p->Hk, p->n_pages, attn::kBlocksBox, vs, "v_cache")) != ATTN_OK)
       return rc;
+    r.splits = blocks_tile_splits(p, sms);
     long_used(dev);
     return done(attn::launch_blocks_tiles(r, tm_k, tm_v, p->d, stream_of(p->stream)), "attention over selected pages launch");
   }

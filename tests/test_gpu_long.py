@@ -308,6 +308,62 @@ def test_blocks_far_apart(E, Hq, Hk, d, Nq, lens, page, n, spread, full):
     p.check_blocks(E, lists.int().contiguous(), full_tiles=full)
 
 
+# full tiles whose stages two, four or eight blocks share: 2, 4, 8 of lists of 8, 16 and 32
+# stages (d = 32: four at most), windows of fewer stages than blocks, ragged counts, rows
+# that select nothing, heads that do not divide a tile
+@pytest.mark.parametrize("Hq,Hk,d,Nq,lens,page,q_lens,n", [
+    (4, 2, 64, 3, [2000, 1, 0], 64, None, 8),
+    (3, 1, 128, 50, [3000, 50], 64, [50, 17], 17),
+    (8, 1, 128, 20, [64 * 70 + 1], 64, [13], 40),
+    (2, 2, 32, 70, [900, 2000], 32, [70, 1], 70),
+    (5, 1, 64, 33, [16 * 600 + 1, 16 * 70], 16, None, 130),
+    (2, 1, 64, 130, [256 * 9 + 200], 256, None, 9),
+    (6, 2, 128, 1, [512 * 6 + 5, 100], 512, None, 5),
+    (7, 1, 32, 9, [16 * 2000 + 7], 16, None, 70),
+], ids=str)
+@pytest.mark.parametrize("mask", ["causal_br", "none"])
+def test_blocks_shared_by_a_cluster(E, Hq, Hk, d, Nq, lens, page, q_lens, n, mask):
+    p = Problem(Hq, Hk, d, Nq, lens, page, q_lens, seed=550)
+    lists = p.lists(n, seed=5)
+    lists[:, :, ::7] = -1
+    p.check_blocks(E, lists, mask, full_tiles=True)
+    same = p.run_blocks(E, lists, mask, full_tiles=True)
+    again = p.run_blocks(E, lists, mask, full_tiles=True)
+    assert all(torch.equal(x, y) for x, y in zip(same, again))
+    # one page a query: most blocks of a cluster have nothing
+    lists[..., 1:] = -1
+    p.check_blocks(E, lists, mask, full_tiles=True)
+
+
+def test_blocks_of_a_cluster_with_scores_that_are_not_finite(E):
+    """A NaN or +inf score reaches its row from whichever block met it; rows of other queries,
+    whose pages it is not on, keep their values."""
+    p = Problem(2, 1, 64, 4, [64 * 32], 64, seed=555)
+    want = torch.arange(32, dtype=torch.int32).expand(1, 1, 4, 32).contiguous()
+    for bad in (float("nan"), float("inf")):
+        for page in (0, 13, 31):
+            k = p.k.clone()
+            k[p.table[0, page], 0, 5] = bad if bad != bad else torch.sign(p.q[0, 0, 3].float()).bfloat16() * bad
+            lists = want.clone()
+            lists[0, 0, :3, page] = -1  # (queries 0 to 2 did not select it)
+            o, lse = E.attn_blocks(p.q.cuda(), k.cuda(), p.v.cuda(), p.table.cuda(), p.lens.cuda(), lists.cuda(),
+                                   mask="none", full_tiles=True)
+            done(E)
+            assert bool(o[0, 0, 3].isnan().all()) and bool(lse[0, 0, 3].isnan())
+            ro, bo, rl, bl = O.blocks(p.q, p.k0(), p.v.nan_to_num(0.0), p.table, p.lens, lists, None, p.scale, "none")
+            check("o", o[:, :, :3], ro[:, :, :3], bo[:, :, :3])
+            check("lse", lse[:, :, :3], rl[:, :, :3], bl[:, :, :3])
+
+
+def test_timeouts_of_a_cluster_are_reported(E):
+    p = Problem(4, 1, 64, 40, [64 * 40], 64, seed=556)
+    lists = p.lists(32)
+    p.run_blocks(E, lists, full_tiles=True, timeout_ns=20_000_000, inject=1)
+    torch.cuda.synchronize()
+    assert E.device_status()[0] != 0
+    p.check_blocks(E, lists, full_tiles=True)
+
+
 @pytest.mark.parametrize("Hq,Hk,d,Nq,lens,page,q_lens,n", [
     # enough rows for tiles of 128 by the rule: one query after another, heads that do not
     # divide a tile, pages smaller and larger than a stage, ragged counts, a short sequence
