@@ -7,16 +7,18 @@
 // memory as the A operand, query rows stream by as B, 64 at a time, and a thread owns one
 // page or key (a TMEM lane) and walks along the rows (columns) with its running maximum or
 // sum in a register: no shuffles, no padding of heads, neighbouring lanes write
-// neighbouring places. A CTA is eight warps, two threads a lane, each with half of a
-// tile's columns; several share an SM. While the tensor core works on tile t, the warps
-// reduce tile t - 1 and the rows of tile t + 1 are on their way. (One thread a lane: 512
-// tokens' scores 26.5 us, 333 rows' weights 38.9.)
+// neighbouring places. Eight warps reduce, two threads a lane, each with half of a tile's
+// columns (one: 512 tokens' scores 26.5 us, not 24); several CTAs share an SM. While the tensor
+// core works on tile t, they reduce tile t - 1 and the rows of tile t + 1 are on their way: for
+// scores, where rows are split by sign, brought by the same warps, a block barrier a tile;
+// for weights by warps of their own and barriers in shared memory, so that the chains of
+// bringing rows, of placing their lse and of the products run next to the sums (333 rows' weights
+// 27 us and not 34.5; with one warp that places lse and issues products 32: its chain a
+// tile, some 2500 cycles, was longer than the sums').
 //
-// What bounds them is instructions: of some 200 that a warp issues for 64 rows of weights
-// only 64 are the exponentials and sums of its 32 columns; the others bring rows, place
-// their lse, wait. 333 rows x 15 heads of d = 64 over 23204 tokens: 34.5 us, 0.27 PFLOP/s (exp2
-// alone would take 9); 512 tokens x 32 heads of d = 128 over the bounds of 1128 pages: 24 us,
-// 25 MB of scores written among it.
+// What bounds them is instructions and those chains. 333 rows x 15 heads of d = 64 over 23204
+// tokens: 27 us, 0.35 PFLOP/s (exp2 alone would take 8); 512 tokens x 32 heads of d = 128 over the
+// bounds of 1128 pages: 24 us, 25 MB of scores written among it.
 //
 // Every wait is bounded: when one runs out the CTA notes it in the status word, leaves its
 // loop, waits (bounded) for its products in flight, frees TMEM and returns.
@@ -340,178 +342,225 @@ struct alignas(16) RowNumbers {  // (read 16 bytes at a time)
   int least[4];  // of the first and second half
 };
 
+// Warps 0-7 reduce: two threads a key, each with half of a tile's columns. Warp 8 + s brings
+// the query rows and lse of stage s, and the last warp issues the products: nothing but
+// barriers of its own rows and accumulators makes a warp wait. (A stage has one warp: a
+// parity tells a phase from the next, not from the one after it.)
+constexpr int kWeightWarps = 8;
 template <int D>
-__global__ void __launch_bounds__(kTileThreads) weights_tiles(const __grid_constant__ LongParams p) {
+constexpr int kWeightThreads = 32 * (kWeightWarps + WeightSmem<D>::kStages + 1);
+
+template <int D>
+__global__ void __launch_bounds__(kWeightThreads<D>, 3) weights_tiles(const __grid_constant__ LongParams p) {
   using S = WeightSmem<D>;
-  constexpr int kPieces = D / 8, kStep = kTileThreads / kPieces;
-  constexpr int kAhead = S::kStages - 1;  // tiles that rows are fetched ahead
+  constexpr int kPieces = D / 8, kStages = S::kStages, kRow = D >= 64 ? 128 : 64;
+  // a tile's numbers are placed at most kStages + 2 tiles ahead of those that are being read
+  constexpr int kNumbers = kStages + 3;
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bars[2];
-  __shared__ uint32_t slot;
-  __shared__ RowNumbers numbers[4];
-  __shared__ int ids[128];     // the keys' pages
-  __shared__ float sums[128];  // of the second of a key's threads
+  __shared__ uint64_t bars[2 * kStages + 4];
+  __shared__ uint32_t slot, abort;
+  __shared__ RowNumbers numbers[kNumbers];
+  __shared__ int ids[128];  // the keys' pages; then the sums of the second of a key's threads
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
   const uint32_t base = smem_u32(smem);
-  Tiles2 tl(p);
-  tl.begin(bars, &slot);
+  const int warp = static_cast<int>(threadIdx.x) >> 5, lane = static_cast<int>(threadIdx.x) & 31;
+  const uint32_t bar0 = smem_u32(bars);
+  const auto full = [&](int s) { return bar0 + 8 * s; };                       // a stage's rows and lse
+  const auto empty = [&](int s) { return bar0 + 8 * (kStages + s); };          // its product is done
+  const auto d_full = [&](int t) { return bar0 + 8 * (2 * kStages + (t & 1)); };
+  const auto d_empty = [&](int t) { return bar0 + 8 * (2 * kStages + 2 + (t & 1)); };
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(d_full(s), 2);  // (the product, and the warp that knows of its rows' numbers)
+      mbar_init(d_empty(s), kWeightWarps);
+    }
+    abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(&slot), kTileCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = slot;
+  const Ctl ctl{&abort, g_long_status, p.timeout_ns};
   ldev::grid_dep_launch();
   ldev::grid_dep_wait();
 
   const int b = blockIdx.z, hk = blockIdx.y;
   const LongLens lens = long_lens(p, b);
-  const int half = static_cast<int>(threadIdx.x) >> 7, unit = static_cast<int>(threadIdx.x) & 127;
+  const int half = warp >> 2, unit = static_cast<int>(threadIdx.x) & 127;
   const int key0 = static_cast<int>(blockIdx.x) * 128, key = key0 + unit;
   const int page_mask = (1 << p.page_shift) - 1;
   const int rows = key0 < lens.len ? lens.ql * p.G : 0, tiles = (rows + kTileRows - 1) / kTileRows;
-  const float* lse = p.lse + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * p.Nq;
-  const int piece = static_cast<int>(threadIdx.x) % kPieces, row = static_cast<int>(threadIdx.x) / kPieces;
-  RowWalk walk(static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb + static_cast<int64_t>(hk) * p.G * p.q_sh + piece * 8,
-               row, kStep, p.G, p.by_g, p.q_sh, p.q_sn);
-  int next = row;  // the row that the walk is at
-  const uint32_t to = operand_at<D>(row, piece, kTileRows);
+  const auto wait = [&](uint32_t bar, uint32_t parity, int t) { return ctl_wait(bar, parity, ctl, t, kRoleTiles); };
 
-  // a tile's query rows, kAhead tiles before they are used
-  const auto fetch = [&](int stage) {
-    static_assert(kStep % 8 == 0, "the swizzle of a thread's rows is the same");
-    const uint32_t dst = base + S::kOffB + stage * S::kB + to;
+  // a tile's query rows and their lse, by one warp
+  constexpr int kStep = 32 / kPieces;  // rows between a lane's pieces
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + b * p.q_sb + static_cast<int64_t>(hk) * p.G * p.q_sh +
+                           lane % kPieces * 8;
+  const float* lse = p.lse + (static_cast<int64_t>(b) * p.Hq + hk * p.G) * p.Nq;
+  const auto bring = [&](int t, int s) {
+    float z[2];
+    int sees[2];
 #pragma unroll
-    for (int r0 = 0; r0 < kTileRows; r0 += kStep) {
-      if (next < rows) ldev::copy16(dst + r0 * (D >= 64 ? 128 : 64), walk.at, 16);
+    for (int i = 0; i < 2; ++i) {
+      const int r = t * kTileRows + i * 32 + lane, n = p.by_g.div(r), g = r - n * p.G;
+      z[i] = r < rows ? lse[static_cast<int64_t>(g) * p.Nq + n] : -INFINITY;
+      sees[i] = r < rows ? long_seen(p, lens, n) : 0;
+    }
+    const int row = lane / kPieces;
+    RowWalk walk(q, t * kTileRows + row, kStep, p.G, p.by_g, p.q_sh, p.q_sn);
+    const uint32_t dst = base + S::kOffB + s * S::kB, to = operand_at<D>(row, lane % kPieces, kTileRows);
+    const int left = rows - t * kTileRows - row;  // rows from this lane's first on
+#pragma unroll
+    for (int x = 0; x < kTileRows; x += kStep) {
+      if (x < left) ldev::copy16(dst + (to ^ ((x & 7u) << 4)) + x * kRow, walk.at, 16);
       walk.next();
-      next += kStep;
     }
     ldev::copy_commit();
-  };
-  // the lse of a tile's rows: read one tile earlier still, put in place with the rows
-  const auto read = [&](int t) {
-    const int r = t * kTileRows + static_cast<int>(threadIdx.x), n = p.by_g.div(r), g = r - n * p.G;
-    return threadIdx.x < kTileRows && r < rows ? lse[static_cast<int64_t>(g) * p.Nq + n] : -INFINITY;
-  };
-  const auto place = [&](int t, int stage, float z) {
-    if (threadIdx.x >= kTileRows) return;
-    const int r = t * kTileRows + static_cast<int>(threadIdx.x);
-    const bool none = fabsf(z) == INFINITY;  // -inf: the row saw nothing; +inf: weights of zero
-    const float x = none ? 0.f : -z * p.c_hi;  // (c_hi + c_lo: 1 / scale)
-    float x1 = 0.f, x2 = 0.f, left = 0.f;
-    if (fabsf(x) < 1e38f) {  // (else, or NaN, the first part says it all)
-      x1 = x - __bfloat162float(__float2bfloat16_rn(x));
-      x2 = x1 - __bfloat162float(__float2bfloat16_rn(x1));
-      left = fmaf(-z, p.c_hi, -x) - z * p.c_lo;
-    }
-    const uint2 v = make_uint2(ldev::pack_bf16(x, x1), ldev::pack_bf16(x2, left));
-    *reinterpret_cast<uint2*>(smem + S::kOffBX + stage * S::kBX + more_at(threadIdx.x, 0)) = v;
-    const int sees = none ? 0 : long_seen(p, lens, p.by_g.div(r));
-    numbers[t % 4].sees[threadIdx.x] = r < rows ? sees : 0;
-    const int least = __reduce_min_sync(0xffffffffu, r < rows ? sees : 0);
-    if ((threadIdx.x & 31) == 0) numbers[t % 4].least[threadIdx.x >> 5] = least;
-  };
-  ldev::F2 sum = ldev::pair(0.f, 0.f);
-  const ldev::F2 c = ldev::pair(p.scale, p.scale);  // (scale * log2(e))
-  const auto reduce = [&](int t) {
-    const RowNumbers& now = numbers[t % 4];
-    const bool whole = key0 + 128 <= now.least[half];
-    uint32_t v[32];
-    tmem_ld32(tl.d(t) + (((threadIdx.x >> 5) & 3u) << 21) + half * 32, v);
+    RowNumbers& now = numbers[t % kNumbers];
 #pragma unroll
-    for (int x = 0; x < 32; x += 4) {
-      const float2 a0 = ldev::split(ldev::mul2(ldev::pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), c));
-      const float2 a1 = ldev::split(ldev::mul2(ldev::pair(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), c));
-      float w[4] = {ex2(a0.x), ex2(a0.y), ex2(a1.x), ex2(a1.y)};
-      if (!whole) {
-        const int4 most = *reinterpret_cast<const int4*>(now.sees + half * 32 + x);
-        if (key >= most.x) w[0] = 0.f;
-        if (key >= most.y) w[1] = 0.f;
-        if (key >= most.z) w[2] = 0.f;
-        if (key >= most.w) w[3] = 0.f;
+    for (int i = 0; i < 2; ++i) {
+      const bool none = fabsf(z[i]) == INFINITY;  // -inf: the row saw nothing; +inf: weights of zero
+      const float x = none ? 0.f : -z[i] * p.c_hi;  // (c_hi + c_lo: 1 / scale)
+      float x1 = 0.f, x2 = 0.f, left = 0.f;
+      if (fabsf(x) < 1e38f) {  // (else, or NaN, the first part says it all)
+        x1 = x - __bfloat162float(__float2bfloat16_rn(x));
+        x2 = x1 - __bfloat162float(__float2bfloat16_rn(x1));
+        left = fmaf(-z[i], p.c_hi, -x) - z[i] * p.c_lo;
       }
-      sum = ldev::add2(sum, ldev::add2(ldev::pair(w[0], w[1]), ldev::pair(w[2], w[3])));
+      *reinterpret_cast<uint2*>(smem + S::kOffBX + s * S::kBX + more_at(i * 32 + lane, 0)) =
+          make_uint2(ldev::pack_bf16(x, x1), ldev::pack_bf16(x2, left));
+      if (none) sees[i] = 0;
+      now.sees[i * 32 + lane] = sees[i];
+      const int least = __reduce_min_sync(0xffffffffu, sees[i]);
+      if (lane == 0) now.least[i] = least;
     }
+    ldev::copy_wait<0>();
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full(s));
   };
 
-  float z = 0.f;
+  ldev::F2 sum = ldev::pair(0.f, 0.f);
   if (tiles > 0) {
-    const int mine = half == 0 && key < lens.len ? p.table[b * p.table_sb + (key >> p.page_shift)] : -1;
-    z = read(0);
-    const float z1 = kAhead > 1 ? read(1) : 0.f;
-    if (half == 0) ids[unit] = mine;
+    if (threadIdx.x < 128) ids[unit] = key < lens.len ? p.table[b * p.table_sb + (key >> p.page_shift)] : -1;
     __syncthreads();
 #pragma unroll 4
-    for (int x = threadIdx.x; x < 128 * kPieces; x += kTileThreads) {
-      const int r = x / kPieces, at = key0 + r, id = ids[r];
+    for (int x = threadIdx.x; x < 128 * kPieces; x += kWeightThreads<D>) {
+      const int r = x / kPieces, c = x % kPieces, at = key0 + r, id = ids[r];
       const bool real = id >= 0 && id < p.n_pages;
-      ldev::copy16(base + operand_at<D>(r, piece, 128),
+      ldev::copy16(base + operand_at<D>(r, c, 128),
                    static_cast<const __nv_bfloat16*>(p.kc) + (real ? id * p.kc_sp : 0) + hk * p.kc_sh +
-                       (at & page_mask) * p.kc_st + piece * 8,
+                       (at & page_mask) * p.kc_st + c * 8,
                    real ? 16 : 0);
     }
-    fetch(0);
-    if constexpr (kAhead > 1) fetch(1);  // (nothing behind the last row: an empty group)
     // the further channels: ones for the keys, zeros behind the four of the rows
     const uint4 zero = make_uint4(0, 0, 0, 0);
-    *reinterpret_cast<uint4*>(smem + S::kOffAX + more_at(unit, half)) =
-        half == 0 ? make_uint4(0x3F803F80u, 0x3F803F80u, 0, 0) : zero;
-    for (int x = threadIdx.x; x < S::kStages * S::kBX / 16; x += kTileThreads)
+    if (warp < kWeightWarps)
+      *reinterpret_cast<uint4*>(smem + S::kOffAX + more_at(unit, half)) =
+          half == 0 ? make_uint4(0x3F803F80u, 0x3F803F80u, 0, 0) : zero;
+    for (int x = threadIdx.x; x < kStages * S::kBX / 16; x += kWeightThreads<D>)
       *reinterpret_cast<uint4*>(smem + S::kOffBX + x * 16) = zero;
-    __syncthreads();
-    place(0, 0, z);
-    if constexpr (kAhead > 1) place(1, 1, z1);
-    z = read(kAhead);
-  }
-  bool ok = true;
-  int t = 0, stage = 0;  // (stage: t modulo kStages)
-  for (; t < tiles; ++t) {
-    ldev::copy_wait<kAhead - 1>();  // tile t's; the next one's may still come
+    ldev::copy_wait<0>();
     fence_async_smem();
-    tc_fence_before();
-    if (__syncthreads_or(!ok)) break;
-    if (threadIdx.x >= kTileThreads - 32) {  // (not a warp that has `place` to do)
-      tc_fence_after();
-      issue_tile<D>(tl.d(t), base, base + S::kOffB + stage * S::kB);
-      issue_more(tl.d(t), base + S::kOffAX, base + S::kOffBX + stage * S::kBX);
-      tl.commit(t);
+    __syncthreads();
+
+    if (warp < kWeightWarps) {
+      const ldev::F2 c = ldev::pair(p.scale, p.scale);  // (scale * log2(e))
+      const uint32_t lanes = (static_cast<uint32_t>(warp) & 3u) << 21;
+      for (int t = 0; t < tiles; ++t) {
+        if (!wait(d_full(t), (t >> 1) & 1, t)) break;
+        tc_fence_after();
+        uint32_t v[32];
+        tmem_ld32(tmem + (t & 1) * kTileRows + lanes + half * 32, v);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_empty(t));
+        const RowNumbers& now = numbers[t % kNumbers];
+        const auto weights = [&](int x, float(&w)[4]) {
+          const float2 a0 = ldev::split(ldev::mul2(ldev::pair(__uint_as_float(v[x]), __uint_as_float(v[x + 1])), c));
+          const float2 a1 = ldev::split(ldev::mul2(ldev::pair(__uint_as_float(v[x + 2]), __uint_as_float(v[x + 3])), c));
+          w[0] = ex2(a0.x), w[1] = ex2(a0.y), w[2] = ex2(a1.x), w[3] = ex2(a1.y);
+        };
+        const auto add = [&](const float(&w)[4]) {
+          sum = ldev::add2(sum, ldev::add2(ldev::pair(w[0], w[1]), ldev::pair(w[2], w[3])));
+        };
+        if (key0 + 128 <= now.least[half]) {  // all keys are seen by all of these rows
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            float w[4];
+            weights(x, w);
+            add(w);
+          }
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            float w[4];
+            weights(x, w);
+            const int4 most = *reinterpret_cast<const int4*>(now.sees + half * 32 + x);
+            w[0] = key < most.x ? w[0] : 0.f;
+            w[1] = key < most.y ? w[1] : 0.f;
+            w[2] = key < most.z ? w[2] : 0.f;
+            w[3] = key < most.w ? w[3] : 0.f;
+            add(w);
+          }
+        }
+      }
+    } else if (warp < kWeightWarps + kStages) {
+      const int s = warp - kWeightWarps;
+      for (int t = s; t < tiles; t += kStages) {
+        if (!wait(empty(s), ((t / kStages) & 1) ^ 1, t)) break;
+        bring(t, s);
+      }
+    } else {
+      for (int t = 0; t < tiles; ++t) {
+        const int s = t % kStages;
+        if (!wait(full(s), (t / kStages) & 1, t) || !wait(d_empty(t), ((t >> 1) & 1) ^ 1, t)) break;
+        tc_fence_after();
+        const uint32_t d = tmem + (t & 1) * kTileRows;
+        issue_tile<D>(d, base, base + S::kOffB + s * S::kB);
+        issue_more(d, base + S::kOffAX, base + S::kOffBX + s * S::kBX);
+        mma_commit(empty(s));
+        if (p.inject != 1 || t != 0) mma_commit(d_full(t));
+        if (lane == 0) mbar_arrive(d_full(t));
+        __syncwarp();
+      }
     }
-    if (t > 0) ok = tl.wait(t - 1);  // its operands may be replaced
-    tc_fence_after();
-    const int before = stage == 0 ? S::kStages - 1 : stage - 1;  // of tiles t - 1 and t + kAhead
-    fetch(before);
-    if (t + kAhead < tiles) {
-      place(t + kAhead, before, z);
-      z = read(t + kAhead + 1);
-    }
-    if (t > 0 && ok) reduce(t - 1);
-    stage = stage + 1 == S::kStages ? 0 : stage + 1;
-  }
-  ldev::copy_wait<0>();
-  if (t > 0 && t == tiles) {
-    ok = tl.wait(t - 1) && ok;
-    tc_fence_after();
-    if (ok) reduce(t - 1);
   }
   const float2 both = ldev::split(sum);
-  if (half != 0) sums[unit] = both.x + both.y;
+  if (half == 1) ids[unit] = __float_as_int(both.x + both.y);
   __syncthreads();
-  if (half == 0 && key < lens.len && ok) {
+  if (half == 0 && key < lens.len && abort == 0) {
     const int id = p.table[b * p.table_sb + (key >> p.page_shift)];
     if (id >= 0 && id < p.n_pages) {
       const int64_t at = ((static_cast<int64_t>(id) * p.Hk + hk) << p.page_shift) + (key & page_mask);
-      const float w = both.x + both.y + sums[unit];
+      const float w = both.x + both.y + __int_as_float(ids[unit]);
       const bool old = p.decay != 0.f && !(p.causal && key >= lens.len - lens.ql);
       p.weights_out[at] = old ? fmaf(p.decay, p.weights[at], w) : w;
     }
   }
-  tl.end();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, kTileCols);
 }
 
 // ------------------------------------------------------------------ launches
 
 template <typename... Args, typename... Given>
-cudaError_t launch_tiles(void (*kern)(Args...), dim3 grid, int bytes, cudaStream_t s, const Given&... args) {
+cudaError_t launch_tiles(void (*kern)(Args...), dim3 grid, int threads, int bytes, cudaStream_t s, const Given&... args) {
   if (bytes > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
   }
-  return ldev::launch(kern, grid, kTileThreads, static_cast<size_t>(bytes), s, 1, args...);
+  return ldev::launch(kern, grid, threads, static_cast<size_t>(bytes), s, 1, args...);
 }
 
 // Tokens of a CTA: what gives kScoreCtas CTAs at most (two fit on a SM with d = 128), but
@@ -529,11 +578,11 @@ cudaError_t scores_tiles_dim(const LongParams& p, cudaStream_t s) {
   const dim3 grid(static_cast<unsigned>(cols * ((p.Nq + tokens - 1) / tokens)), p.Hk, p.B);
   const int n = static_cast<int>(tokens), bytes = ScoreSmem<D>::kBytes;
   switch (p.G) {
-    case 1: return launch_tiles(scores_tiles<D, 1>, grid, bytes, s, p, n);
-    case 2: return launch_tiles(scores_tiles<D, 2>, grid, bytes, s, p, n);
-    case 4: return launch_tiles(scores_tiles<D, 4>, grid, bytes, s, p, n);
-    case 8: return launch_tiles(scores_tiles<D, 8>, grid, bytes, s, p, n);
-    default: return launch_tiles(scores_tiles<D, 0>, grid, bytes, s, p, n);
+    case 1: return launch_tiles(scores_tiles<D, 1>, grid, kTileThreads, bytes, s, p, n);
+    case 2: return launch_tiles(scores_tiles<D, 2>, grid, kTileThreads, bytes, s, p, n);
+    case 4: return launch_tiles(scores_tiles<D, 4>, grid, kTileThreads, bytes, s, p, n);
+    case 8: return launch_tiles(scores_tiles<D, 8>, grid, kTileThreads, bytes, s, p, n);
+    default: return launch_tiles(scores_tiles<D, 0>, grid, kTileThreads, bytes, s, p, n);
   }
 }
 
@@ -545,7 +594,7 @@ cudaError_t weights_tiles_dim(const LongParams& p, cudaStream_t s) {
   r.c_hi = static_cast<float>(inv);
   r.c_lo = static_cast<float>(inv - static_cast<double>(r.c_hi));
   r.scale = static_cast<float>(scale * 1.4426950408889634074);
-  return launch_tiles(weights_tiles<D>, grid, WeightSmem<D>::kBytes, s, r);
+  return launch_tiles(weights_tiles<D>, grid, kWeightThreads<D>, WeightSmem<D>::kBytes, s, r);
 }
 
 }  // namespace dev

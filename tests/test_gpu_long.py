@@ -425,6 +425,13 @@ def test_weights_of_rows_without_a_sum(E, full):
     assert bool(got[1, :48].isnan().all()) and not bool(got[1, 48:].isnan().any()) and not bool(got[0].isnan().any())
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("Hq,Hk,Nq", [(3, 1, 700), (16, 2, 130), (1, 1, 1)])
+def test_weights_of_many_tiles_of_rows(E, d, Hq, Hk, Nq):
+    """Dozens of tiles of 64 rows go through the few stages of shared memory."""
+    Problem(Hq, Hk, d, Nq, [Nq + 150, Nq], 16, [Nq, max(1, Nq - 60)], seed=640).check_weights(E, full_tiles=True)
+
+
 @FORMS
 def test_weights_of_keys_that_are_infinite(E, full):
     p = Problem(1, 1, 32, 1, [40], 16, seed=560)
