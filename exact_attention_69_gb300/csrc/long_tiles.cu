@@ -521,7 +521,8 @@ __global__ void __launch_bounds__(kWeightThreads<D>, 3) weights_tiles(const __gr
         bring(t, s);
       }
     } else {
-      for (int t = 0; t < tiles; ++t) {
+      int t = 0;
+      for (; t < tiles; ++t) {
         const int s = t % kStages;
         if (!wait(full(s), (t / kStages) & 1, t) || !wait(d_empty(t), ((t >> 1) & 1) ^ 1, t)) break;
         tc_fence_after();
@@ -533,6 +534,9 @@ __global__ void __launch_bounds__(kWeightThreads<D>, 3) weights_tiles(const __gr
         if (lane == 0) mbar_arrive(d_full(t));
         __syncwarp();
       }
+      // a product in flight reads this CTA's shared memory and writes its TMEM: wait (bounded) for the last
+      if (t < tiles && t > 0)
+        ctl_wait(empty((t - 1) % kStages), ((t - 1) / kStages) & 1, ctl, t, kRoleTiles, false);
     }
   }
   const float2 both = ldev::split(sum);
