@@ -399,10 +399,9 @@ __device__ __forceinline__ void blocks_join(uint32_t part, uint32_t ml, int spli
 
 // Wide: windows of up to 1024 pages, for tables of more than 256: each window is three
 // barriers, a pass over the lists and a pipeline that starts anew. (512 queries x 32 heads,
-// d = 128, 65536 tokens, 32 pages of much the same ones a query: 64 us and not 72 with pages of
-// 64, 36 and not 76 with 16; 32768 tokens, 8 heads, d = 64: 34 and 33, with 16 pages of 64 at
-// random 318 and 305. Tables of up to 256 pages: 59.3 with the width known to the compiler,
-// 61.2 without.)
+// d = 128, 65536 tokens, 32 pages of much the same ones a query: 43 us and not 53 with pages of
+// 64, 34 and not 79 with 16; 32768 tokens, 8 heads, d = 64, 16 pages of 64: 22 both ways. Tables of
+// up to 256 pages, one CTA a tile: 59.3 with the width known to the compiler, 61.2 without.)
 template <int D, bool Wide>
 __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_constant__ BlocksTiles a) {
   using S = BlocksSmem<D>;
