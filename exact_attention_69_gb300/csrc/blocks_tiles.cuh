@@ -22,6 +22,10 @@
 // dependent reads of shared memory a stage (600 cycles), S read once, loaders of keys and
 // values apart.
 //
+// CTAs of a cluster wait for each other with their TMEM allocated. Registers let no more than
+// two CTAs of these kernels into a SM, 512 columns in all, so none of them waits for TMEM that
+// another cluster holds; other kernels that hold some wait for no other CTA.
+//
 // The running maximum is a whole number (log2 units) and moves only when a score passes it
 // by more than 8, so O in TMEM is seldom rescaled, and exactly. P is rounded to bf16 once
 // (the tensor core's input type; the sum takes the unrounded values): against 64 bits O is off

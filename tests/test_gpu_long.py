@@ -355,6 +355,25 @@ def test_blocks_of_a_cluster_with_scores_that_are_not_finite(E):
             check("lse", lse[:, :, :3], rl[:, :, :3], bl[:, :, :3])
 
 
+def test_clusters_of_calls_at_once(E):
+    """Calls on several streams, also captured and replayed, whose blocks share tiles: the same bits."""
+    ps = [Problem(4, 2, d, 90, [64 * 30, 64 * 12 + 5, 700], 64, seed=557 + d) for d in (32, 64, 128)]
+    args = [tuple(x.cuda() for x in (p.q, p.k, p.v, p.table, p.lens, p.lists(24))) for p in ps]
+    want = [E.attn_blocks(*a, full_tiles=True) for a in args]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = [E.attn_blocks(*a, full_tiles=True) for a in args for _ in range(2)]
+    for _ in range(5):
+        got = [[E.attn_blocks(*a, full_tiles=True, stream=s) for _ in range(3)] for a, s in zip(args, streams)]
+        g.replay()
+        torch.cuda.synchronize()
+        for x, y in [(x, w) for w, runs in zip(want, got) for x in runs] + list(zip(held, [w for w in want for _ in range(2)])):
+            assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+    done(E)
+
+
 def test_timeouts_of_a_cluster_are_reported(E):
     p = Problem(4, 1, 64, 40, [64 * 40], 64, seed=556)
     lists = p.lists(32)
