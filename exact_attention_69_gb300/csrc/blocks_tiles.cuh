@@ -40,6 +40,7 @@ constexpr int kBlocksThreads = 224, kBlocksKeys = 64;
 constexpr int kWindowMost = 1024, kWindowBits = 256 * 128;  // pages of a window: 256, for fewer queries more
 constexpr int kWarpK = 4, kWarpMma = 5, kWarpV = 6;
 constexpr float kBlocksSlack = 8.f;
+constexpr uint64_t kLateNs = 20000;  // inject -1
 constexpr uint32_t kBlocksCols = 256;  // TMEM: S_0 [0, 64), S_1 [64, 128) (P over their first 32), O from 128
 
 struct BlocksTiles {
@@ -65,7 +66,7 @@ struct BlocksLists {
   uint32_t any[kWindowMost / 32];
   uint16_t page[kWindowMost];       // the pages that have a bit, from the window's first
   int32_t id[kWindowMost];
-  uint64_t bars[13];
+  uint64_t bars[14];
   uint32_t tmem;
   uint32_t abort;
   int count;
@@ -80,7 +81,10 @@ struct BlocksBars {
   __device__ uint32_t v_empty(int s) const { return base + 48 + 8 * s; }
   __device__ uint32_t s_full(int s) const { return base + 64 + 8 * s; }
   __device__ uint32_t p_full(int s) const { return base + 80 + 8 * s; }
-  __device__ uint32_t o_done() const { return base + 96; }
+  // (two, for the stages in turn: S of a stage goes ahead of the product of the stage before, so a
+  // row that is through with its last stage waits for the last product but one as well, and a
+  // parity tells a phase from the next one, not from the one after it)
+  __device__ uint32_t o_done(int s) const { return base + 96 + 8 * s; }
 };
 
 // Stages of a window's list, and what a stage has: pages of 64 slots or more are cut
@@ -111,6 +115,10 @@ __device__ __forceinline__ bool blocks_load(const BlocksTiles& a, const BlocksLi
     if (!blocks_wait(VALUES ? bars.v_empty(slot) : bars.k_empty(slot), ((gs >> 1) & 1) ^ 1u, ctl, gs)) return false;
     const uint32_t full = VALUES ? bars.v_full(slot) : bars.k_full(slot);
     if (!VALUES && gs == 0 && a.p.inject == 1) continue;
+    if (VALUES && a.p.inject == -1) {  // (long after the stage's softmax is through)
+      for (const uint64_t t0 = global_ns(); global_ns() - t0 < kLateNs;) {
+      }
+    }
     mbar_expect_tx(full, S::kKV);
     for (int i = 0; i < (1 << st.sub); ++i) {
       const int e = st.entry(s, i);
@@ -201,7 +209,7 @@ __device__ __forceinline__ bool blocks_mma(const BlocksMma<D>& mm, const BlocksL
       if (!blocks_wait(bars.p_full(slot), parity, ctl, x)) return false;
       tc_fence_after();
       mm.values(slot, x > 0);
-      mma_commit(bars.o_done());
+      mma_commit(bars.o_done(slot));
       mma_commit(bars.v_empty(slot));
     }
   }
@@ -312,7 +320,7 @@ __device__ __forceinline__ bool blocks_softmax(const BlocksLists& l, const Block
       r.m = next;
       r.sum *= f;
       if (gs > 0) {
-        if (!blocks_wait(bars.o_done(), (gs - 1) & 1, ctl, gs)) return false;
+        if (!blocks_wait(bars.o_done(slot ^ 1), ((gs - 1) >> 1) & 1, ctl, gs)) return false;
         tc_fence_after();
         blocks_rescale<D>(r.tl + 128, f);
       }
@@ -424,8 +432,8 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
       mbar_init(bars.v_empty(s), 1);
       mbar_init(bars.s_full(s), 1);
       mbar_init(bars.p_full(s), 4);
+      mbar_init(bars.o_done(s), 1);
     }
-    mbar_init(bars.o_done(), 1);
     l.abort = 0;
     fence_barrier_init();
     prefetch_tmap(&a.tm_k);
@@ -553,7 +561,7 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
 
   if (warp < 4) {
     if (ok && gs > 0) {
-      ok = blocks_wait(bars.o_done(), (gs - 1) & 1, ctl, gs);
+      ok = blocks_wait(bars.o_done((gs - 1) & 1), ((gs - 1) >> 1) & 1, ctl, gs);
       tc_fence_after();
     }
     const int g = r0 + row - n_mine * G, h = hk * G + g;
@@ -587,7 +595,7 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
   }
   if (l.abort != 0u && (warp == kWarpK || warp == kWarpV)) {
     // copies in flight land in this CTA's shared memory: wait (bounded) for the last ones
-    for (int x = max(gs - 2, warp == kWarpK ? p.inject : 0); x < gs; ++x)  // (the keys that inject withheld never come)
+    for (int x = max(gs - 2, warp == kWarpK && p.inject == 1 ? 1 : 0); x < gs; ++x)  // (the keys that inject withheld never come)
       blocks_wait(warp == kWarpV ? bars.v_full(x & 1) : bars.k_full(x & 1), (x >> 1) & 1, ctl, x, false);
   }
   ldev::copy_wait<0>();  // (no page, no wait so far)

@@ -83,8 +83,8 @@ int fill(const attn_long_params* p, LongParams* r, bool queries, bool heads, boo
   r->last = p->last;
   r->n_new = p->n_new;
   r->decay = p->decay;
-  if (p->full_tiles < 0 || p->full_tiles > 2 || p->inject < 0 || p->inject > 1)
-    return fail_with(ATTN_ERR_INVALID_ARG, "full_tiles must be 0 to 2, inject 0 or 1");
+  if (p->full_tiles < 0 || p->full_tiles > 2 || p->inject < -1 || p->inject > 1)
+    return fail_with(ATTN_ERR_INVALID_ARG, "full_tiles must be 0 to 2, inject -1 to 1");
   r->full_tiles = p->full_tiles;
   r->timeout_ns = p->timeout_ns ? p->timeout_ns : kTimeoutNs;
   r->inject = p->inject;

@@ -48,7 +48,7 @@ struct LongParams {
   float decay;
   int full_tiles;               // 0: by the rule, 1: tiles of 128 rows, 2: the form for few rows
   uint64_t timeout_ns;          // tiles of 128 rows: bound on every wait
-  int inject;                   // 1: withhold something once (tests the bounded wait)
+  int inject;                   // 1: withhold something once (tests the bounded wait); -1: attn_blocks, values come late
   int splits;                   // CTAs (a cluster) that share a row tile's pages
 };
 

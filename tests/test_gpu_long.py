@@ -383,6 +383,19 @@ def test_timeouts_of_a_cluster_are_reported(E):
     p.check_blocks(E, lists, full_tiles=True)
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("pages", [1, 2, 3, 4, 7])
+def test_blocks_whose_values_come_late(E, d, pages):
+    """S = Q K^T runs a stage ahead of O += P V: a row that is through with its last stage's
+    softmax waits for that stage's O although the one before is not done either."""
+    p = Problem(8, 2, d, 40, [64 * pages, 64 * 20], 64, seed=560 + pages)
+    lists = torch.arange(pages, dtype=torch.int32).expand(2, 2, 40, pages).contiguous()
+    for mask in ("none", "causal_br"):
+        p.check_blocks(E, lists, mask, full_tiles=True, inject=-1)
+        late, on_time = p.run_blocks(E, lists, mask, full_tiles=True, inject=-1), p.run_blocks(E, lists, mask, full_tiles=True)
+        assert all(torch.equal(x, y) for x, y in zip(late, on_time))
+
+
 @pytest.mark.parametrize("Hq,Hk,d,Nq,lens,page,q_lens,n", [
     # enough rows for tiles of 128 by the rule: one query after another, heads that do not
     # divide a tile, pages smaller and larger than a stage, ragged counts, a short sequence
