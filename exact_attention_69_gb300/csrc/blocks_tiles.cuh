@@ -40,7 +40,7 @@ constexpr int kBlocksThreads = 224, kBlocksKeys = 64;
 constexpr int kWindowMost = 1024, kWindowBits = 256 * 128;  // pages of a window: 256, for fewer queries more
 constexpr int kWarpK = 4, kWarpMma = 5, kWarpV = 6;
 constexpr float kBlocksSlack = 8.f;
-constexpr uint64_t kLateNs = 20000;  // inject -1
+constexpr uint64_t kLateNs = 2000000;  // inject -1 (more than a few polls of a wait, which park for 0.2 ms at most)
 constexpr uint32_t kBlocksCols = 256;  // TMEM: S_0 [0, 64), S_1 [64, 128) (P over their first 32), O from 128
 
 struct BlocksTiles {
@@ -66,7 +66,7 @@ struct BlocksLists {
   uint32_t any[kWindowMost / 32];
   uint16_t page[kWindowMost];       // the pages that have a bit, from the window's first
   int32_t id[kWindowMost];
-  uint64_t bars[14];
+  uint64_t bars[15];
   uint32_t tmem;
   uint32_t abort;
   int count;
@@ -85,6 +85,7 @@ struct BlocksBars {
   // row that is through with its last stage waits for the last product but one as well, and a
   // parity tells a phase from the next one, not from the one after it)
   __device__ uint32_t o_done(int s) const { return base + 96 + 8 * s; }
+  __device__ uint32_t done() const { return base + 112; }  // every product
 };
 
 // Stages of a window's list, and what a stage has: pages of 64 slots or more are cut
@@ -434,6 +435,7 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
       mbar_init(bars.p_full(s), 4);
       mbar_init(bars.o_done(s), 1);
     }
+    mbar_init(bars.done(), 1);
     l.abort = 0;
     fence_barrier_init();
     prefetch_tmap(&a.tm_k);
@@ -447,7 +449,7 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = l.tmem;
-  const Ctl ctl{&l.abort, g_long_status, p.timeout_ns};
+  const Ctl ctl{&l.abort, g_long_status, p.timeout_ns}, drain{&l.abort, g_long_status, kDrainNs};
   ldev::grid_dep_launch();
   ldev::grid_dep_wait();
 
@@ -559,6 +561,10 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
     if (__syncthreads_or(!ok)) break;
   }
 
+  if (warp == kWarpMma) {  // products in flight read this CTA's shared memory and write its TMEM: wait (bounded) for all
+    mma_commit(bars.done());
+    blocks_wait(bars.done(), 0, drain, gs, false);
+  }
   if (warp < 4) {
     if (ok && gs > 0) {
       ok = blocks_wait(bars.o_done((gs - 1) & 1), ((gs - 1) >> 1) & 1, ctl, gs);
@@ -596,7 +602,7 @@ __global__ void __launch_bounds__(kBlocksThreads, 2) blocks_tiles(const __grid_c
   if (l.abort != 0u && (warp == kWarpK || warp == kWarpV)) {
     // copies in flight land in this CTA's shared memory: wait (bounded) for the last ones
     for (int x = max(gs - 2, warp == kWarpK && p.inject == 1 ? 1 : 0); x < gs; ++x)  // (the keys that inject withheld never come)
-      blocks_wait(warp == kWarpV ? bars.v_full(x & 1) : bars.k_full(x & 1), (x >> 1) & 1, ctl, x, false);
+      blocks_wait(warp == kWarpV ? bars.v_full(x & 1) : bars.k_full(x & 1), (x >> 1) & 1, drain, x, false);
   }
   ldev::copy_wait<0>();  // (no page, no wait so far)
   tc_fence_before();

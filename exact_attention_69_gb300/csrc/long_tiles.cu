@@ -36,6 +36,9 @@ __device__ uint32_t g_long_status[4];
 constexpr int kTileThreads = 256, kTileRows = 64;  // threads: two for each of 128 pages or keys
 constexpr uint32_t kTileCols = 2 * kTileRows;      // TMEM columns: two accumulators
 constexpr uint32_t kRoleTiles = 4;
+// Bound on the wait for copies and products in flight after a wait has run out: theirs, not the
+// caller's, which may be shorter than they take.
+constexpr uint64_t kDrainNs = 2000000000;
 
 // True once phase `parity` of `bar` is complete; false after the time limit.
 __device__ __noinline__ bool tile_wait_slow(uint32_t bar, uint32_t parity, int tile, uint64_t timeout_ns) {

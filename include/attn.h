@@ -545,7 +545,7 @@ typedef struct attn_long_params {
                                * other values than 0 are for tests */
   uint64_t timeout_ns;        /* bound on every device-side wait of these; 0 = 2 seconds */
   int inject;                 /* test hook, as attn_params_ex.inject (tiles of 128 rows); -1: attn_blocks,
-                               * every load of values begins 20 us late */
+                               * every load of values begins 2 ms late */
 } attn_long_params;
 
 void attn_long_params_init(attn_long_params* p);

@@ -384,6 +384,21 @@ def test_timeouts_of_a_cluster_are_reported(E):
 
 
 @pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("lens", [[64 * 40], [64 * 6]], ids=["cluster", "few stages"])
+def test_blocks_that_give_up_with_copies_on_their_way(E, d, lens):
+    """The shortest limit, and values that come after it: a block gives up between a stage's S
+    and its O, waits for what is in flight, reports it and leaves nothing behind for the next call."""
+    p = Problem(4, 1, d, 40, lens, 64, seed=558)
+    lists = p.lists(24, seed=6)
+    for _ in range(2):
+        p.run_blocks(E, lists, full_tiles=True, timeout_ns=1, inject=-1)
+        torch.cuda.synchronize()
+        code, detail = E.device_status()
+        assert code == 5 and detail[0] == 5
+        p.check_blocks(E, lists, full_tiles=True)
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("pages", [1, 2, 3, 4, 7])
 def test_blocks_whose_values_come_late(E, d, pages):
     """S = Q K^T runs a stage ahead of O += P V: a row that is through with its last stage's
