@@ -123,24 +123,23 @@ struct RowWalk {
   }
 };
 
-// What both kernels set up: barriers and TMEM.
+// What the scores' kernel sets up: barriers and TMEM.
 struct Tiles2 {
-  uint32_t bar[2];
+  uint32_t bars;  // of the two accumulators; of all products
   uint32_t tmem;
   uint64_t timeout_ns;
   int inject;
   __device__ __forceinline__ Tiles2(const LongParams& p) : timeout_ns(p.timeout_ns), inject(p.inject) {}
+  __device__ __forceinline__ uint32_t bar(int i) const { return bars + 8 * i; }
   __device__ __forceinline__ void commit(int t) const {
-    if (inject != 1 || t != 0) mma_commit(bar[t & 1]);
+    if (inject != 1 || t != 0) mma_commit(bar(t & 1));
   }
   __device__ __forceinline__ uint32_t d(int t) const { return tmem + (t & 1) * kTileRows; }
-  __device__ __forceinline__ bool wait(int t) const { return tile_wait(bar[t & 1], (t >> 1) & 1, t, timeout_ns); }
-  __device__ __forceinline__ void begin(uint64_t* bars, uint32_t* slot) {
-    bar[0] = smem_u32(bars);
-    bar[1] = bar[0] + 8;
+  __device__ __forceinline__ bool wait(int t) const { return tile_wait(bar(t & 1), (t >> 1) & 1, t, timeout_ns); }
+  __device__ __forceinline__ void begin(uint64_t* words, uint32_t* slot) {
+    bars = smem_u32(words);
     if (threadIdx.x == 0) {
-      mbar_init(bar[0], 1);
-      mbar_init(bar[1], 1);
+      for (int i = 0; i < 3; ++i) mbar_init(bar(i), 1);
       fence_barrier_init();
     }
     if (threadIdx.x < 32) {
@@ -151,6 +150,13 @@ struct Tiles2 {
     __syncthreads();
     tc_fence_after();
     tmem = *slot;
+  }
+  // The block has given up: the warp that issued its products waits (bounded) for those in flight.
+  __device__ __forceinline__ void drain(int t) const {
+    if (threadIdx.x >= 32) return;
+    mma_commit(bar(2));
+    tile_wait(bar(2), 0, t, kDrainNs);
+    __syncwarp();
   }
   __device__ __forceinline__ void end() const {
     tc_fence_before();
@@ -175,7 +181,7 @@ __global__ void __launch_bounds__(kTileThreads, 2) scores_tiles(const __grid_con
   using S = ScoreSmem<D>;
   constexpr int kPieces = D / 8, kLoads = kTileRows * kPieces / kTileThreads;
   extern __shared__ uint8_t raw[];
-  __shared__ uint64_t bars[2];
+  __shared__ uint64_t bars[3];
   __shared__ uint32_t slot;
   __shared__ int ids[128];  // the pages
   uint8_t* smem = raw + ((1024u - (smem_u32(raw) & 1023u)) & 1023u);
@@ -313,11 +319,14 @@ __global__ void __launch_bounds__(kTileThreads, 2) scores_tiles(const __grid_con
     load();
     if (t > 0) reduce(t - 1);
   }
-  if (t > 0 && t == tiles) {
+  bool gave_up = t < tiles;  // (the same in all threads)
+  if (t > 0 && !gave_up) {
     ok = tl.wait(t - 1);
     tc_fence_after();
-    if (ok) reduce(t - 1);
+    gave_up = __syncthreads_or(!ok);
+    if (!gave_up) reduce(t - 1);
   }
+  if (gave_up) tl.drain(t);
   // what no query sees
   for (int n = (some ? max(live - tok0, 0) : 0) + half; n < toks; n += 2)
     if (page < p.table_width) out[static_cast<int64_t>(n) * p.table_width] = -INFINITY;

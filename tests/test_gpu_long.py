@@ -601,6 +601,19 @@ def test_timeouts_are_reported(E):
         p.check_weights(E, full_tiles=True)
 
 
+@pytest.mark.parametrize("Nq", [10, 40])
+def test_scores_that_give_up(E, Nq):
+    """The wait that runs out is the only one (40 rows, one tile), or one between tiles."""
+    p = Problem(4, 2, 64, Nq, [700, 90], 16, seed=656)
+    b = torch.zeros(p.n_pages, 2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for _ in range(2):
+        E.block_scores(p.q.cuda(), b, p.table.cuda(), p.lens.cuda(), page_size=16, full_tiles=True, timeout_ns=1, inject=1)
+        torch.cuda.synchronize()
+        code, detail = E.device_status()
+        assert code == 5 and detail[0] == 5
+        p.check_scores(E, full_tiles=True)
+
+
 def test_layouts(E):
     """Heads-last queries and outputs, [page, slot, head, d] caches, K and V in one tensor, a
     wider table."""
