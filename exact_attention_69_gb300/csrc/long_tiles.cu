@@ -401,7 +401,7 @@ __global__ void __launch_bounds__(kWeightThreads<D>, 3) weights_tiles(const __gr
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = slot;
-  const Ctl ctl{&abort, g_long_status, p.timeout_ns};
+  const Ctl ctl{&abort, g_long_status, p.timeout_ns}, drain{&abort, g_long_status, kDrainNs};
   ldev::grid_dep_launch();
   ldev::grid_dep_wait();
 
@@ -546,9 +546,9 @@ __global__ void __launch_bounds__(kWeightThreads<D>, 3) weights_tiles(const __gr
         if (lane == 0) mbar_arrive(d_full(t));
         __syncwarp();
       }
-      // a product in flight reads this CTA's shared memory and writes its TMEM: wait (bounded) for the last
-      if (t < tiles && t > 0)
-        ctl_wait(empty((t - 1) % kStages), ((t - 1) / kStages) & 1, ctl, t, kRoleTiles, false);
+      // a product in flight reads this CTA's shared memory and writes its TMEM: wait (bounded) for the
+      // last one, also where all were issued and only a warp that reduces has given up
+      if (t > 0) ctl_wait(empty((t - 1) % kStages), ((t - 1) / kStages) & 1, drain, t, kRoleTiles, false);
     }
   }
   const float2 both = ldev::split(sum);

@@ -614,6 +614,22 @@ def test_scores_that_give_up(E, Nq):
         p.check_scores(E, full_tiles=True)
 
 
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("Nq", [10, 40, 200])
+def test_weights_that_give_up(E, Nq, d):
+    """All products issued (one tile, two), or some: whichever warp's wait runs out, the block
+    waits for its products, writes no weight and leaves nothing behind for the next call."""
+    p = Problem(4, 2, d, Nq, [700, 290], 16, seed=657)
+    for _ in range(2):
+        w = torch.zeros(p.n_pages, 2, 16, device="cuda")
+        E.kv_weights(p.q.cuda(), p.k.cuda(), p.table.cuda(), p.lens.cuda(), torch.zeros(2, 4, Nq).cuda(), w, decay=0.0,
+                     full_tiles=True, timeout_ns=1, inject=1)
+        torch.cuda.synchronize()
+        code, detail = E.device_status()
+        assert code == 5 and detail[0] == 5 and not bool(w.any())
+        p.check_weights(E, full_tiles=True)
+
+
 def test_layouts(E):
     """Heads-last queries and outputs, [page, slot, head, d] caches, K and V in one tensor, a
     wider table."""
