@@ -10,6 +10,8 @@
 // Few rows are bound by memory: keys once, weights once each way. 32 sequences of 256 to
 // 4224 tokens, 8 key heads, d = 128, pages of 64 (115 MB) take 21.7 us, 5.3 TB/s. (One
 // group of 16 keys a warp, nothing on its way meanwhile: 31.6 us.)
+#include <cfloat>
+
 #include "long_dev.cuh"
 #include "long_kernel.h"
 
@@ -19,6 +21,8 @@ namespace {
 using namespace ldev;
 
 constexpr int kWeightWarps = 4, kFewRows = 32;
+// log2(e), and what its fp32 value leaves of it
+constexpr float kLog2e = 1.4426950408889634f, kLog2eLeft = static_cast<float>(1.4426950408889634074 - kLog2e);
 
 // Few rows (up to 32, all in shared memory): the keys stream by. A warp takes every
 // fourth group of 16 keys of its block's `units` groups a warp, the next group's keys and
@@ -80,9 +84,13 @@ __global__ void __launch_bounds__(32 * kWeightWarps) weights_kernel(const __grid
     if (r < rows) {
       const int n = p.by_g.div(r), g = r - n * p.G;
       const float x = p.lse[(static_cast<int64_t>(b) * p.Hq + hk * p.G + g) * p.Nq + n];
-      zh = -x * 1.4426950408889634f;
-      // (what the product left, and x times log2(e) less its fp32 value)
-      zl = fabsf(x) == INFINITY ? 0.f : fmaf(-x, 1.4426950408889634f, -zh) - x * 1.925963033e-8f;
+      zh = -x * kLog2e;
+      // (what the product left, and x times log2(e) less its fp32 value; none of an infinity)
+      if (fabsf(x) >= 1e38f) {
+        if (fabsf(x) < INFINITY) zh = copysignf(FLT_MAX, -x);  // (finite, as the lse is)
+      } else {
+        zl = fmaf(-x, kLog2e, -zh) - x * kLog2eLeft;
+      }
       most = x == -INFINITY ? 0 : long_seen(p, lens, n);
     }
     hi[r] = zh;

@@ -359,6 +359,7 @@ struct alignas(16) RowNumbers {  // (read 16 bytes at a time)
 // barriers of its own rows and accumulators makes a warp wait. (A stage has one warp: a
 // parity tells a phase from the next, not from the one after it.)
 constexpr int kWeightWarps = 8;
+constexpr float kBf16Most = 0x1.FEp127f;
 template <int D>
 constexpr int kWeightThreads = 32 * (kWeightWarps + WeightSmem<D>::kStages + 1);
 
@@ -440,9 +441,10 @@ __global__ void __launch_bounds__(kWeightThreads<D>, 3) weights_tiles(const __gr
     RowNumbers& now = numbers[t % kNumbers];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const bool none = fabsf(z[i]) == INFINITY;  // -inf: the row saw nothing; +inf: weights of zero
-      const float x = none ? 0.f : -z[i] * p.c_hi;  // (c_hi + c_lo: 1 / scale)
+      const bool none = z[i] == -INFINITY;          // the row saw nothing
+      float x = none ? 0.f : -z[i] * p.c_hi;        // (c_hi + c_lo: 1 / scale)
       float x1 = 0.f, x2 = 0.f, left = 0.f;
+      if (fabsf(x) >= 1e38f && fabsf(z[i]) < INFINITY) x = copysignf(kBf16Most, x);  // (finite, as its lse is)
       if (fabsf(x) < 1e38f) {  // (else, or NaN, the first part says it all)
         x1 = x - __bfloat162float(__float2bfloat16_rn(x));
         x2 = x1 - __bfloat162float(__float2bfloat16_rn(x1));

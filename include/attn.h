@@ -592,10 +592,11 @@ int attn_blocks(const attn_long_params* p);
 /*
  * attn_kv_weights: weights_out[slot] = decay * weights[slot] + sum over the queries that
  * see the slot and the query heads of its key head of exp(scale q . k - lse), lse being
- * what the attention of the same queries returned (rows of -inf count nothing). With
- * ATTN_MASK_CAUSAL_BR the queries' own slots, the last q_lens[b], are new in this call
- * and start from zero; with decay 0 all do, and weights is not read. Sums are fp32 in a
- * fixed order. Slots that no sequence holds stay as they are. scale is 2^-64 to 2^64.
+ * what the attention of the same queries returned (rows of -inf count nothing; a product
+ * and an lse that are both +inf give NaN). With ATTN_MASK_CAUSAL_BR the queries' own
+ * slots, the last q_lens[b], are new in this call and start from zero; with decay 0 all
+ * do, and weights is not read. Sums are fp32 in a fixed order. Slots that no sequence
+ * holds stay as they are. scale is 2^-64 to 2^64.
  * Reads q, k_cache, kv_lens, q_lens, lse, weights (NULL if decay is 0); writes weights_out.
  */
 int attn_kv_weights(const attn_long_params* p);

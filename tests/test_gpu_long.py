@@ -472,6 +472,28 @@ def test_weights_of_rows_without_a_sum(E, full):
     assert bool(got[1, :48].isnan().all()) and not bool(got[1, 48:].isnan().any()) and not bool(got[0].isnan().any())
 
 
+@FORMS
+def test_weights_of_infinite_products_and_lse(E, full):
+    """exp(s - lse) with an infinity on either side, or on both: 0, infinity, NaN in every form."""
+    p = Problem(4, 1, 32, 1, [40], 16, seed=561)
+    p.q = p.q.abs() + 1
+    page = int(p.table[0, 0])
+    p.k[page, 0, 3], p.k[page, 0, 4] = float("inf"), -float("inf")
+    inf = math.inf
+    most = torch.finfo(torch.float32).max
+    for row, want3, want4 in ((inf, "nan", 0.0), (-inf, 0.0, 0.0), (3.0, inf, 0.0), (1e38, inf, 0.0), (-1e38, inf, 0.0),
+                              (most, inf, 0.0), (-most, inf, 0.0)):
+        lse = torch.full((1, 4, 1), -inf)
+        lse[0, 1] = row
+        w = p.w.cuda()
+        E.kv_weights(p.q.cuda(), p.k.cuda(), p.table.cuda(), p.lens.cuda(), lse.cuda(), w, decay=0.0, full_tiles=full)
+        got = O.rows(w.cpu(), p.table[0], 40)[0]
+        for at, want in ((3, want3), (4, want4)):
+            assert bool(got[at].isnan()) if want == "nan" else float(got[at]) == want, (row, at, float(got[at]))
+        rest = got[[0, 1, 2, 5, 39]]
+        assert bool((rest == (inf if -inf < row < 0 else 0.0)).all()) if row != 3.0 else bool(torch.isfinite(rest).all())
+
+
 @pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("Hq,Hk,Nq", [(3, 1, 700), (16, 2, 130), (1, 1, 1)])
 def test_weights_of_many_tiles_of_rows(E, d, Hq, Hk, Nq):
