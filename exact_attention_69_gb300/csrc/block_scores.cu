@@ -76,13 +76,7 @@ __global__ void __launch_bounds__(kBoundsThreads) bounds_kernel(const __grid_con
 
 // ------------------------------------------------------------------ scores
 
-constexpr int kScoreWarps = 4, kScorePages = 16 * kScoreWarps, kFewRows = 32;
-
-// Query heads of a key head, padded so that groups of 8 columns hold whole tokens or a
-// token whole groups: 1, 2, 4 or a multiple of 8.
-__host__ __device__ constexpr int padded_heads(int g) {
-  return g <= 2 ? g : (g <= 4 ? 4 : (g + 7) / 8 * 8);
-}
+constexpr int kScoreWarps = 4, kScorePages = 16 * kScoreWarps;
 
 // Few rows (up to 32, all in shared memory): a warp takes the bounds of 16 pages into
 // registers and goes over the rows 8 at a time. Columns of a product are rows n * Gp + g
@@ -227,7 +221,7 @@ cudaError_t launch_bounds(const LongParams& p, int d, cudaStream_t s) {
 }
 
 cudaError_t launch_scores(const LongParams& p, int d, cudaStream_t s) {
-  if (p.full_tiles == 1 || static_cast<int64_t>(p.Nq) * padded_heads(p.G) > kFewRows) return launch_scores_tiles(p, d, s);
+  if (p.full_tiles == 1 || !scores_few_rows(p)) return launch_scores_tiles(p, d, s);
   switch (d) {
     case 32: return scores_dim<32>(p, s);
     case 64: return scores_dim<64>(p, s);

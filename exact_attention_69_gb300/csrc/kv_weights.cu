@@ -20,7 +20,7 @@ namespace {
 
 using namespace ldev;
 
-constexpr int kWeightWarps = 4, kFewRows = 32;
+constexpr int kWeightWarps = 4;
 // log2(e), and what its fp32 value leaves of it
 constexpr float kLog2e = 1.4426950408889634f, kLog2eLeft = static_cast<float>(1.4426950408889634074 - kLog2e);
 
@@ -158,7 +158,7 @@ cudaError_t weights_dim(const LongParams& p, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_weights(const LongParams& p, int d, cudaStream_t s) {
-  if (p.full_tiles == 1 || static_cast<int64_t>(p.Nq) * p.G > kFewRows) return launch_weights_tiles(p, d, s);
+  if (p.full_tiles == 1 || !weights_few_rows(p)) return launch_weights_tiles(p, d, s);
   switch (d) {
     case 32: return weights_dim<32>(p, s);
     case 64: return weights_dim<64>(p, s);

@@ -205,6 +205,13 @@ int this_gpu() {
   return rc;
 }
 
+// The scores' and weights' form for few rows, where it is asked for by name.
+int check_few(const attn_long_params* p, bool fits) {
+  if (p->full_tiles == 2 && !fits)
+    return fail_with(ATTN_ERR_INVALID_ARG, "full_tiles 2: the form for few rows holds %d rows of a key head", attn::kFewRows);
+  return ATTN_OK;
+}
+
 int done(cudaError_t e, const char* what) { return e == cudaSuccess ? ATTN_OK : cuda_error(e, what); }
 
 }  // namespace
@@ -232,7 +239,8 @@ int attn_block_scores(const attn_long_params* p) {
   LongParams r;
   int rc = fill(p, &r, true, true, true);
   if (rc != ATTN_OK || (rc = fill_queries(p, &r)) != ATTN_OK || (rc = check_scale(p, &r)) != ATTN_OK ||
-      (rc = need(p->bounds, "bounds")) != ATTN_OK || (rc = need(p->scores, "scores")) != ATTN_OK)
+      (rc = need(p->bounds, "bounds")) != ATTN_OK || (rc = need(p->scores, "scores")) != ATTN_OK ||
+      (rc = check_few(p, attn::scores_few_rows(r))) != ATTN_OK)
     return rc;
   if (!aligned(p->bounds, 16)) return fail_with(ATTN_ERR_MISALIGNED, "bounds must be 16-byte aligned");
   if ((rc = this_gpu()) != ATTN_OK) return rc;
@@ -288,7 +296,7 @@ int attn_kv_weights(const attn_long_params* p) {
   int rc = fill(p, &r, true, true, true);
   if (rc != ATTN_OK || (rc = fill_queries(p, &r)) != ATTN_OK || (rc = fill_cache(p, &r, true, false, kRead)) != ATTN_OK ||
       (rc = check_scale(p, &r)) != ATTN_OK || (rc = need(p->lse, "lse")) != ATTN_OK ||
-      (rc = need(p->weights_out, "weights_out")) != ATTN_OK)
+      (rc = need(p->weights_out, "weights_out")) != ATTN_OK || (rc = check_few(p, attn::weights_few_rows(r))) != ATTN_OK)
     return rc;
   if (!std::isfinite(p->decay) || p->decay < 0.f) return fail_with(ATTN_ERR_INVALID_ARG, "decay must be finite and >= 0");
   if (p->decay != 0.f && (rc = need(p->weights, "weights")) != ATTN_OK) return rc;

@@ -93,4 +93,12 @@ __host__ __device__ constexpr int blocks_tile_rows(int64_t rows) { return rows <
 __host__ __device__ constexpr int blocks_warps(int groups) { return groups == 1 ? 6 : 4; }
 constexpr int kBlocksMaxSplits = 8;   // CTAs of a cluster on any GPU
 
+// Rows of a sequence and key head that the scores' and weights' forms for few rows hold.
+constexpr int kFewRows = 32;
+// Query heads of a key head as the scores' form for few rows pads them, so that groups of 8
+// columns hold whole tokens or a token whole groups: 1, 2, 4 or a multiple of 8.
+__host__ __device__ constexpr int padded_heads(int g) { return g <= 2 ? g : (g <= 4 ? 4 : (g + 7) / 8 * 8); }
+inline bool scores_few_rows(const LongParams& p) { return static_cast<int64_t>(p.Nq) * padded_heads(p.G) <= kFewRows; }
+inline bool weights_few_rows(const LongParams& p) { return static_cast<int64_t>(p.Nq) * p.G <= kFewRows; }
+
 }  // namespace attn

@@ -160,7 +160,7 @@ def _run_bounds(handle, p, bounds):
 def _plan_scores(q, bounds, block_table, kv_lens, page_size, q_lens, scale, mask, out, full_tiles, timeout_ns, inject):
     p = _Params()
     _fits("page_size", page_size)
-    _form(p, full_tiles or None, timeout_ns, inject)
+    _form(p, full_tiles, timeout_ns, inject)
     device = _cuda(bounds, "bounds")
     if bounds.dim() != 4:
         raise ValueError("bounds must be [n_pages, Hk, 2, d]")
@@ -183,7 +183,9 @@ def block_scores(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tenso
     Returns fp32 [B, Hk, Nq, width of the table]: the largest over the query heads of a
     key head of scale * sum_c (min(q_c, 0) lower_c + max(q_c, 0) upper_c), -inf for pages
     of which the query sees nothing. scale None: 1 / sqrt(d). full_tiles, timeout_ns and
-    inject: as attn_blocks has them.
+    inject: as attn_blocks has them, but the form for few rows holds 32 (Nq times the
+    query heads of a key head, those rounded up to 4 or a multiple of 8): False with more
+    is refused.
     """
     page_size, timeout_ns, inject = int(page_size), int(timeout_ns), int(inject)
     scale = None if scale is None else float(scale)
@@ -338,7 +340,7 @@ def _plan_weights(q, k_cache, block_table, kv_lens, lse, weights, q_lens, scale,
     p = _Params()
     if not (math.isfinite(decay) and decay >= 0):
         raise ValueError("decay must be finite and >= 0")
-    _form(p, full_tiles or None, timeout_ns, inject)
+    _form(p, full_tiles, timeout_ns, inject)
     _pages(p, "k_cache", k_cache)
     p.k_cache_stride[:] = _heads("k_cache", k_cache)
     device = k_cache.device
@@ -364,7 +366,8 @@ def kv_weights(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor
     attn_paged (a shared prefix counted in) or attn_blocks returned for the same queries.
     With 'causal_br' the queries' own slots are new and start from zero, whatever a
     recycled page held; with decay 0 all slots do. Sums are fp32 in a fixed order.
-    full_tiles, timeout_ns and inject: as attn_blocks has them.
+    full_tiles, timeout_ns and inject: as attn_blocks has them, but the form for few rows
+    holds 32 (Nq times the query heads of a key head): False with more is refused.
     """
     decay, timeout_ns, inject = float(decay), int(timeout_ns), int(inject)
     scale = None if scale is None else float(scale)

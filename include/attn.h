@@ -541,8 +541,9 @@ typedef struct attn_long_params {
   int64_t k_cache_stride[3], v_cache_stride[3]; /* pages, heads, slots; zero = contiguous */
   void* stream;
   int full_tiles;             /* attn_blocks, attn_block_scores, attn_kv_weights: 0 = the library's rule,
-                               * 1 = tiles of 128 rows, 2 = the form for few rows (attn_blocks only);
-                               * other values than 0 are for tests */
+                               * 1 = tiles of 128, 2 = the form for few rows (scores and weights: up to
+                               * 32 rows of a sequence and key head, Nq times the query heads, which
+                               * scores round up to 4 or a multiple of 8; refused above) */
   uint64_t timeout_ns;        /* bound on every device-side wait of these; 0 = 2 seconds */
   int inject;                 /* test hook, as attn_params_ex.inject (tiles of 128 rows); -1: attn_blocks,
                                * every load of values begins 2 ms late */

@@ -426,6 +426,28 @@ def test_blocks_of_many_rows(E, Hq, Hk, d, Nq, lens, page, q_lens, n):
     p.check_blocks(E, p.lists(n, seed=4))
 
 
+@pytest.mark.parametrize("Hq,Hk,d,Nq,lens,page,q_lens,n", [
+    (8, 2, 128, 400, [1100], 64, None, 6),
+    (3, 1, 64, 300, [330, 1500], 16, [300, 290], 9),
+    (16, 1, 32, 100, [900], 128, [71], 4),
+], ids=str)
+def test_form_for_few_rows_where_the_rule_takes_tiles(E, Hq, Hk, d, Nq, lens, page, q_lens, n):
+    """full_tiles False: attention by tiles of 16 rows for any number of them; scores and weights
+    of so many are refused, and of few the rule's own bits."""
+    p = Problem(Hq, Hk, d, Nq, lens, page, q_lens, seed=526)
+    lists = p.lists(n, seed=4)
+    p.check_blocks(E, lists, full_tiles=False)
+    b, lse = torch.zeros(p.n_pages, Hk, 2, d, dtype=torch.bfloat16, device="cuda"), torch.zeros(p.q.shape[:3], device="cuda")
+    args = p.table.cuda(), p.lens.cuda()
+    with pytest.raises(E.AttnError, match="few rows"):
+        E.block_scores(p.q.cuda(), b, *args, page_size=page, full_tiles=False)
+    with pytest.raises(E.AttnError, match="few rows"):
+        E.kv_weights(p.q.cuda(), p.k.cuda(), *args, lse, p.w.cuda(), full_tiles=False)
+    few = Problem(Hq, Hk, d, 2, lens, page, seed=527)
+    assert torch.equal(few.check_scores(E, full_tiles=False), few.check_scores(E))
+    few.check_weights(E, full_tiles=False)
+
+
 @FORMS
 def test_blocks_of_rising_maxima(E, full):
     """Scores that grow from page to page by far more than the running maximum's slack."""

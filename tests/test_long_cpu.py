@@ -77,6 +77,19 @@ def test_refuses(lib, name, changes, code):
     assert lib.attn_last_error()
 
 
+@pytest.mark.parametrize("name,G,most", [("attn_block_scores", 1, 32), ("attn_block_scores", 3, 8), ("attn_block_scores", 9, 2),
+                                         ("attn_kv_weights", 1, 32), ("attn_kv_weights", 3, 10), ("attn_kv_weights", 9, 3)])
+def test_form_for_few_rows(lib, name, G, most):
+    """Asked for by name it is refused where it does not hold the rows; else the next check refuses."""
+    p = block(name)
+    p.Hq, p.full_tiles, p.bounds, p.decay = p.Hk * G, 2, A + 8, -1.0
+    p.q_stride[:] = (0, 0, 0)
+    for Nq, refused in ((most, False), (most + 1, True), (1 << 20, True)):
+        p.Nq = Nq
+        code, why = getattr(lib, name)(ctypes.byref(p)), lib.attn_last_error()
+        assert code != 0 and (b"few rows" in why if refused else b"aligned" in why or b"decay" in why), (Nq, code, why)
+
+
 def test_null_blocks(lib):
     for name in _lib.LONG_CALLS:
         assert getattr(lib, name)(None) == INV
