@@ -12,7 +12,9 @@ whose last dimension is contiguous; a cache [n_pages, Hk, page_size, d] bf16; ta
 lengths and lists int32 on the device. The queries of sequence b are the last q_lens[b]
 (None: Nq) of its kv_lens[b] tokens; mask 'causal_br': query i sees slots up to i +
 kv_lens[b] - q_lens[b]; 'none': all of them. Page x of a sequence is entry x of its row
-in the block table; a prefix that sequences share is pages that several rows name.
+in the block table; a prefix that sequences share is pages that several rows name, for
+the calls that read them: pages that kv_weights or kv_evict writes must be one
+sequence's only (what to do with a shared prefix is said there).
 
 A decoding step over a long cache:
 
@@ -366,6 +368,10 @@ def kv_weights(q: torch.Tensor, k_cache: torch.Tensor, block_table: torch.Tensor
     attn_paged (a shared prefix counted in) or attn_blocks returned for the same queries.
     With 'causal_br' the queries' own slots are new and start from zero, whatever a
     recycled page held; with decay 0 all slots do. Sums are fp32 in a fixed order.
+    No page may be in two rows of the table: each sequence reads, adds to and writes its
+    pages' weights, and one's sums would be lost. With a prefix that sequences share,
+    multiply `weights` by the decay, then call once for each sequence (its rows of q,
+    block_table, kv_lens, q_lens and lse), with decay 1, on one stream.
     full_tiles, timeout_ns and inject: as attn_blocks has them, but the form for few rows
     holds 32 (Nq times the query heads of a key head): False with more is refused.
     """
@@ -424,7 +430,9 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor
     (kv_weights) among the others, ties to the earliest, NaN as the greatest; every token
     if there are no more. Their keys, values and weights move, in their order, to the
     front of the sequence's pages, or to the pages of dst_table [B, width] (a copy; none
-    of them may be in block_table). Returns (new_lens [B], kept [B, Hk, budget]): the
+    of them may be in block_table). Pages that are written must be one sequence's only:
+    in place, no page may be in two rows of block_table; sequences that share a prefix
+    are cut into pages of dst_table, each of which is in it once. Returns (new_lens [B], kept [B, Hk, budget]): the
     lengths after it and the slots that the tokens came from, -1 behind the last. Key
     heads keep different tokens: give kv_append the tokens' true positions from then on,
     and find the pages' bounds again (kv_bounds) where they are used.

@@ -597,7 +597,9 @@ int attn_blocks(const attn_long_params* p);
  * and an lse that are both +inf give NaN). With ATTN_MASK_CAUSAL_BR the queries' own
  * slots, the last q_lens[b], are new in this call and start from zero; with decay 0 all
  * do, and weights is not read. Sums are fp32 in a fixed order. Slots that no sequence
- * holds stay as they are. scale is 2^-64 to 2^64.
+ * holds stay as they are. scale is 2^-64 to 2^64. No page may be in two rows of the
+ * table (one sequence's sums would be lost): for a shared prefix, one call for each
+ * sequence, weights multiplied by decay before them and decay 1 in them.
  * Reads q, k_cache, kv_lens, q_lens, lse, weights (NULL if decay is 0); writes weights_out.
  */
 int attn_kv_weights(const attn_long_params* p);
@@ -608,7 +610,8 @@ int attn_kv_weights(const attn_long_params* p);
  * earliest, NaN above everything; all if there are no more than n. Their keys, values
  * and weights move, in order, to the front of the sequence's pages, or to the pages of
  * dst_table[b] (which must not be pages of block_table; a destination that is not a
- * page, or lies behind dst_width, is left out). new_lens[b] = min(kv_lens[b], n), kept =
+ * page, or lies behind dst_width, is left out). In place no page may be in two rows of
+ * block_table; pages of dst_table must be in it once, its sources may be shared. new_lens[b] = min(kv_lens[b], n), kept =
  * the slots that they came from, -1 behind. Each key head keeps tokens of its own, so a
  * page's bounds have to be found again (attn_kv_bounds, n_new = -1).
  * Reads kv_lens; reads and writes k_cache, v_cache, weights; writes kept, new_lens.

@@ -627,6 +627,42 @@ def test_pages_that_the_cache_has_not(E, full):
     p.check_weights(E, full_tiles=full)
 
 
+def sharing(Hq, Hk, d, Nq, own, page, shared, seed, spare=1):
+    """Sequences whose first `shared` pages are the first one's; the others' stay unused."""
+    p = Problem(Hq, Hk, d, Nq, [shared * page + n for n in own], page, seed=seed, spare=spare)
+    p.table[1:, :shared] = p.table[:1, :shared]
+    return p
+
+
+@FORMS
+@pytest.mark.parametrize("Hq,Hk,d,Nq,page", [(4, 2, 64, 1, 16), (6, 2, 128, 7, 64), (2, 1, 32, 40, 32)], ids=str)
+def test_pages_that_sequences_share(E, Hq, Hk, d, Nq, page, full):
+    """A prefix's pages in every row of the table: bounds, scores, choice and attention."""
+    p = sharing(Hq, Hk, d, Nq, [Nq + 3, Nq + 100, Nq], page, 5, seed=653)
+    s = p.check_scores(E, full_tiles=full)
+    lists = E.block_select(s, p.lens.cuda(), 4, page_size=page)
+    assert torch.equal(lists.cpu(), O.select(s.cpu(), p.lens, None, 4, page, 1, 2, "causal_br"))
+    p.check_blocks(E, lists.cpu(), full_tiles=full)
+
+
+@FORMS
+def test_weights_and_eviction_with_a_shared_prefix(E, full):
+    """What their documentation says: a call for each sequence, and pages of its own for each."""
+    p = sharing(4, 2, 64, 3, [40, 9, 3], 16, 4, seed=654, spare=13)
+    lse = 2 + torch.rand(3, 4, 3, generator=torch.Generator().manual_seed(9))
+    w = p.w.cuda() * 0.5
+    ref, err = p.w.double() * 0.5, torch.zeros(p.w.shape, dtype=torch.float64)
+    for b in range(3):
+        one = slice(b, b + 1)
+        E.kv_weights(p.q[one].cuda(), p.k.cuda(), p.table[one].cuda(), p.lens[one].cuda(), lse[one].cuda(), w, full_tiles=full)
+        ref, e = O.weights(p.q[one], p.k0(), p.table[one], p.lens[one], lse[one], ref, None, p.scale, "causal_br", 1.0)
+        err += e
+    done(E)
+    check("weights", w.cpu().nan_to_num(0.0), ref.nan_to_num(0.0), err)
+    p.w = w.cpu()
+    evicted(E, p, 50, 3, 10, p.spare[:12].reshape(3, 4))
+
+
 def test_timeouts_are_reported(E):
     """Something withheld in the forms with tiles of 128 rows: the bounded wait runs out, the
     status says so, and the next call is right."""
