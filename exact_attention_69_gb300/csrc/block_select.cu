@@ -148,10 +148,14 @@ __device__ __forceinline__ void pick(Team<T>& team, At at, int lo, int hi, int k
 #pragma unroll
       for (int e = 0; e < E; ++e)
         if (key[e] != 0u) atomicAdd(h + ((key[e] >> shift) & mask), 1u);
-    } else {
+    } else {  // (bits < 32)
+      // While t is 0 (the k-th value is -inf, or next to the type's lowest) places outside [lo, hi), of key
+      // 0, are counted as well, in digit 0. That is below all that is wanted: this digit begins at bit 15 or
+      // 16 then, and the least key of a value is 0x007FFFFF, so values have 0x7F or more there; from the
+      // next pass on t is not 0.
 #pragma unroll
       for (int e = 0; e < E; ++e)
-        if (((key[e] ^ t) >> bits) == 0u) atomicAdd(h + ((key[e] >> shift) & mask), 1u);  // (bits < 32; t > 0: not key 0)
+        if (((key[e] ^ t) >> bits) == 0u) atomicAdd(h + ((key[e] >> shift) & mask), 1u);
     }
     uint32_t count;
     t |= team.digit(h, left, count) << shift;

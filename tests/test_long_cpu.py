@@ -124,6 +124,21 @@ def test_python_refuses(lib):
         E.kv_bounds(q, q, table, lens, n_new=-1)
 
 
+def test_keys_of_places_without_a_value():
+    """The choice by digits gives places without a value the key 0 and counts them as soon as the
+    wanted prefix is 0 after a first digit: none of a value's keys then shares their next digit."""
+    lowest = [-math.inf, -3.4028235e38, -3.0e38, -1.8e38, -1.7014118e38, -1.7e38, -8.5e37, -1.0, -1e-38, 0.0, 1.0]
+    u = torch.tensor(lowest).view(torch.int32).long() & 0xFFFFFFFF
+    keys = torch.where(u >> 31 == 1, ~u & 0xFFFFFFFF, u | 0x80000000).tolist()
+    assert keys[0] == 0x007FFFFF and keys == sorted(keys)
+    least = keys[0]
+    for bits in range(1, 33):                     # of the first pass: the highest in which keys differ
+        shift = max(bits - 8, 0)
+        if least >> shift == 0:                   # a prefix of 0 is possible
+            after = max(shift - 8, 0)
+            assert shift < 32 and all((k >> after) & ((1 << (shift - after)) - 1) > 0 for k in keys if k >> shift == 0)
+
+
 def test_take():
     nan = math.nan
     assert O.take([1, 5, 5, 2], 2, 0, 0) == [1, 2]
