@@ -30,7 +30,8 @@
 // by more than 8, so O in TMEM is seldom rescaled, and exactly. P is rounded to bf16 once
 // (the tensor core's input type; the sum takes the unrounded values): against 64 bits O is off
 // by 0.0023 of its norm, the rounding of the output alone is 0.0017. A second part of P, as the
-// form for few rows has it, would lengthen the stage's chain.
+// form for few rows has it (which a caller may ask for), takes the 0.0023 to 0.0017 and 43.5 us to
+// 50.6 (512 queries as above; 62 to 79 without padding): some 190 more instructions a stage and thread.
 #pragma once
 
 namespace attn {

@@ -586,6 +586,9 @@ int attn_block_select(const attn_long_params* p);
  * order. A row without a slot, or without a score above -inf, gives O = 0, LSE = -inf;
  * one with a score that is NaN or +inf NaN for both. Values (v_cache) of pages that only
  * some queries of a sequence read, and of slots that only some see, must be finite.
+ * Softmax weights enter the second product as bf16: in two parts in the form for few
+ * rows, in one in tiles of 128 rows (O off by 0.0017 and 0.0023 of its norm, of which its
+ * own rounding is 0.0017). full_tiles = 2 asks for the finer form at any size.
  * Reads q, k_cache, v_cache, kv_lens, q_lens, blocks; writes o and lse (or NULL).
  */
 int attn_blocks(const attn_long_params* p);

@@ -134,6 +134,17 @@ def blocks(q, k_cache, v_cache, table, lens, lists, q_lens, scale, mask):
     return o, ob, lse, lb
 
 
+def blocks_two_parts(q, k_cache, v_cache, table, lens, lists, q_lens, scale, mask, most):
+    """(o, bound) where P is held in two bf16 parts: the second is the first's rounding, rounded
+    itself, U of U p. What is left, with z = sum p |v|: U |o| of the output; U^2 z; the score's error
+    twice and exp2's, as above; products of up to `most` slots, added in fp32 with either
+    rounding, and 8 more steps for the join and the division: (most + 8) 2 T z."""
+    o, _, lse, lb = blocks(q, k_cache, v_cache, table, lens, lists, q_lens, scale, mask)
+    z = blocks(q, k_cache, v_cache.abs(), table, lens, lists, q_lens, scale, mask)[0]
+    err = torch.where(lse == -math.inf, 0.0, lb - 2.0 ** -20 * (1 + lse.abs()))[..., None]
+    return o, U * o.abs() + (U * U + 2 * err + 2.0 ** -21 + (most + 8) * 2 * T) * z
+
+
 def weights(q, k_cache, table, lens, lse, before, q_lens, scale, mask, decay, out=None):
     """(weights, bound); `before` and the result as [n_pages, Hk, page]."""
     B, Hq, Nq, d = q.shape

@@ -383,6 +383,24 @@ def test_timeouts_of_a_cluster_are_reported(E):
     p.check_blocks(E, lists, full_tiles=True)
 
 
+@pytest.mark.parametrize("Hq,Hk,d,Nq,lens,page,n", [
+    (4, 2, 64, 1, [40, 3], 16, 4),
+    (8, 2, 128, 20, [64 * 9 + 7, 30], 64, 3),
+    (3, 1, 32, 50, [700], 32, 6),
+    (2, 1, 64, 130, [64 * 40], 64, 33),
+    (4, 1, 128, 500, [800], 64, 9),
+], ids=str)
+def test_blocks_with_weights_in_two_parts(E, Hq, Hk, d, Nq, lens, page, n):
+    """What a caller who asks for the form for few rows gets at any size: the output's own
+    rounding is nearly all of the error."""
+    p = Problem(Hq, Hk, d, Nq, lens, page, seed=559)
+    lists = p.lists(n, seed=8)
+    o, _ = p.run_blocks(E, lists, full_tiles=False)
+    done(E)
+    check("o", o, *O.blocks_two_parts(p.q, p.k0(), p.v.nan_to_num(0.0), p.table, p.lens, lists, None, p.scale, "causal_br",
+                                      n * page))
+
+
 @pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("lens", [[64 * 40], [64 * 6]], ids=["cluster", "few stages"])
 def test_blocks_that_give_up_with_copies_on_their_way(E, d, lens):
