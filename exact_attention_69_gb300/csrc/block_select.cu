@@ -392,6 +392,9 @@ cudaError_t move_dim(const LongParams& p, cudaStream_t s) {
 
 }  // namespace
 
+// A warp takes a row of up to 1024 values, a block longer ones. Both for rows of 100, 500 and 1000 values (us):
+// 256 rows 3.7, 5.2, 7.7 by warps and 4.5, 4.5, 4.6 by blocks of 256; 2048 rows 4.4, 6.8, 11.1 and 13.6,
+// 14.3, 15.1; 8192 rows 8.6, 15.7, 27.4 and 45, 48, 50.
 cudaError_t launch_select(const LongParams& p, cudaStream_t s) {
   const int64_t rows = static_cast<int64_t>(p.B) * p.Hk * p.Nq;
   const dim3 warps(static_cast<unsigned>((rows + 3) / 4)), blocks(static_cast<unsigned>(rows));

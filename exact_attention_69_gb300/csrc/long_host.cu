@@ -159,6 +159,8 @@ int blocks_splits(const attn_long_params* p, int sms) {
 // CTAs a tile: 34 / 50; 128 tiles, 2 and 4: 40 / 52; 256, 1 and 2: 68 / 80). With q_lens, though,
 // a batch is padded, and half of the tiles are taken to have nothing (2 sequences x 512 queries
 // x 8 heads of G = 4, 256 tiles, half of the queries padding: 59 by one CTA, 44 by two, 55 by four).
+// Lengths are on the device, so this is a guess: q_lens of a batch without padding cost time (without
+// them and with them; 1 x 512 queries x 8 heads 40 / 52, 2 x 62 / 76, 4 x 118 / 118).
 int blocks_tile_splits(const attn_long_params* p, int sms) {
   const int64_t rows = static_cast<int64_t>(p->Nq) * (p->Hq / p->Hk);
   const int64_t tiles = (rows + 127) / 128 * p->B * p->Hk >> (p->q_lens != nullptr);
