@@ -435,10 +435,10 @@ def kv_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor
     front of the sequence's pages, or to the pages of dst_table [B, width] (a copy; none
     of them may be in block_table). Pages that are written must be one sequence's only:
     in place, no page may be in two rows of block_table; sequences that share a prefix
-    are cut into pages of dst_table, each of which is in it once. Returns (new_lens [B], kept [B, Hk, budget]): the
-    lengths after it and the slots that the tokens came from, -1 behind the last. Key
-    heads keep different tokens: give kv_append the tokens' true positions from then on,
-    and find the pages' bounds again (kv_bounds) where they are used.
+    are cut into pages of dst_table, each of which is in it once. Returns (new_lens [B],
+    kept [B, Hk, budget]): the lengths after it and the slots that the tokens came from,
+    -1 behind the last. Key heads keep different tokens: give kv_append the tokens' true
+    positions from then on, and find the pages' bounds again (kv_bounds) where they are used.
     """
     budget, first, last = int(budget), int(first), int(last)
     key = ("evict", _sig(k_cache), _sig(v_cache), _sig(weights), _sig(block_table), _sig(kv_lens), budget, first, last,

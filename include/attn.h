@@ -614,9 +614,10 @@ int attn_kv_weights(const attn_long_params* p);
  * and weights move, in order, to the front of the sequence's pages, or to the pages of
  * dst_table[b] (which must not be pages of block_table; a destination that is not a
  * page, or lies behind dst_width, is left out). In place no page may be in two rows of
- * block_table; pages of dst_table must be in it once, its sources may be shared. new_lens[b] = min(kv_lens[b], n), kept =
- * the slots that they came from, -1 behind. Each key head keeps tokens of its own, so a
- * page's bounds have to be found again (attn_kv_bounds, n_new = -1).
+ * block_table; pages of dst_table must be in it once, its sources may be shared.
+ * new_lens[b] = min(kv_lens[b], n), kept = the slots that they came from, -1 behind. Each
+ * key head keeps tokens of its own, so a page's bounds have to be found again
+ * (attn_kv_bounds, n_new = -1).
  * Reads kv_lens; reads and writes k_cache, v_cache, weights; writes kept, new_lens.
  */
 int attn_kv_evict(const attn_long_params* p);
