@@ -141,14 +141,14 @@ __global__ void __launch_bounds__(32 * kWeightWarps) weights_kernel(const __grid
   }
 }
 
-// Groups of 16 keys a warp: enough blocks for kWeightBlocks, groups enough to be worth a
+// Groups of 16 keys a warp: enough blocks for kWeightBlocks a SM, groups enough to be worth a
 // block's start.
-constexpr int kWeightBlocks = 8 * 152, kWeightUnits = 8;
+constexpr int kWeightBlocks = 8, kWeightUnits = 8;
 
 template <int D>
 cudaError_t weights_dim(const LongParams& p, cudaStream_t s) {
   const int64_t groups = p.max_len / 16;
-  int64_t units = groups * p.Hk * p.B / (static_cast<int64_t>(kWeightBlocks) * kWeightWarps);
+  int64_t units = groups * p.Hk * p.B / (static_cast<int64_t>(kWeightBlocks) * p.sms * kWeightWarps);
   units = units < 1 ? 1 : (units > kWeightUnits ? kWeightUnits : units);
   const int64_t keys = units * kWeightWarps * 16;
   const dim3 grid(static_cast<unsigned>((p.max_len + keys - 1) / keys), p.Hk, p.B);

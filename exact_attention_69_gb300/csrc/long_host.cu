@@ -200,9 +200,9 @@ bool blocks_full_tiles(const attn_long_params* p, int sms) {
          static_cast<double>(rows * p->B * p->Hk) * static_cast<double>(slots) >= static_cast<double>(kFullPairsPerSm) * sms;
 }
 
-int this_gpu() {
-  int dev = 0, sms = 0;
-  const int rc = this_device(&dev, &sms);
+int this_gpu(LongParams* r) {
+  int dev = 0;
+  const int rc = this_device(&dev, &r->sms);
   if (rc == ATTN_OK) long_used(dev);
   return rc;
 }
@@ -232,7 +232,7 @@ int attn_kv_bounds(const attn_long_params* p) {
     return rc;
   if (!aligned(p->bounds, 16)) return fail_with(ATTN_ERR_MISALIGNED, "bounds must be 16-byte aligned");
   if (p->n_new < -1) return fail_with(ATTN_ERR_INVALID_ARG, "n_new must be >= 0, or -1 for all tokens");
-  if ((rc = this_gpu()) != ATTN_OK) return rc;
+  if ((rc = this_gpu(&r)) != ATTN_OK) return rc;
   return done(attn::launch_bounds(r, p->d, stream_of(p->stream)), "page bounds launch");
 }
 
@@ -245,7 +245,7 @@ int attn_block_scores(const attn_long_params* p) {
       (rc = check_few(p, attn::scores_few_rows(r))) != ATTN_OK)
     return rc;
   if (!aligned(p->bounds, 16)) return fail_with(ATTN_ERR_MISALIGNED, "bounds must be 16-byte aligned");
-  if ((rc = this_gpu()) != ATTN_OK) return rc;
+  if ((rc = this_gpu(&r)) != ATTN_OK) return rc;
   return done(attn::launch_scores(r, p->d, stream_of(p->stream)), "page scores launch");
 }
 
@@ -254,7 +254,7 @@ int attn_block_select(const attn_long_params* p) {
   LongParams r;
   int rc = fill(p, &r, true, false, false);
   if (rc != ATTN_OK || (rc = check_taken(p, "pages of a list")) != ATTN_OK || (rc = need(p->scores, "scores")) != ATTN_OK ||
-      (rc = need(p->blocks, "blocks")) != ATTN_OK || (rc = this_gpu()) != ATTN_OK)
+      (rc = need(p->blocks, "blocks")) != ATTN_OK || (rc = this_gpu(&r)) != ATTN_OK)
     return rc;
   return done(attn::launch_select(r, stream_of(p->stream)), "page selection launch");
 }
@@ -310,7 +310,7 @@ int attn_kv_weights(const attn_long_params* p) {
   r.c_lo = static_cast<float>(c - static_cast<double>(r.c_hi));
   if (!(p->scale >= 0x1p-64f && p->scale <= 0x1p64f) || !(r.c_lo > 0.f))
     return fail_with(ATTN_ERR_INVALID_ARG, "scale must be 2^-64 to 2^64");
-  if ((rc = this_gpu()) != ATTN_OK) return rc;
+  if ((rc = this_gpu(&r)) != ATTN_OK) return rc;
   return done(attn::launch_weights(r, p->d, stream_of(p->stream)), "received weights launch");
 }
 
@@ -337,7 +337,7 @@ int attn_kv_evict(const attn_long_params* p) {
     r.dst_width = p->dst_width;
   }
   r.weights_out = p->weights;
-  if ((rc = this_gpu()) != ATTN_OK) return rc;
+  if ((rc = this_gpu(&r)) != ATTN_OK) return rc;
   return done(attn::launch_evict(r, p->d, stream_of(p->stream)), "eviction launch");
 }
 

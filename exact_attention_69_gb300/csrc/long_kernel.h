@@ -50,6 +50,7 @@ struct LongParams {
   uint64_t timeout_ns;          // tiles of 128 rows: bound on every wait
   int inject;                   // 1: withhold something once (tests the bounded wait); -1: attn_blocks, values come late
   int splits;                   // CTAs (a cluster) that share a row tile's pages
+  int sms;                      // the device's (scores and weights: how finely work is cut)
 };
 
 // Keys that query n of a sequence with `len` cached tokens and `ql` queries sees.

@@ -238,7 +238,8 @@ __global__ void __launch_bounds__(kTileThreads, 2) scores_tiles(const __grid_con
     ldev::copy_commit();
   }
 
-  // (heads that do not divide half a tile: the first of a lane's threads takes all columns)
+  // (other groups: the first of a lane's threads takes all columns; 2048 rows, 2 x 8 key heads of 512 pages,
+  // d = 128: 40 to 45 us for groups of 3, 5 and 7, 33 for 16 and 32, 19 to 21 for 4 and 8)
   constexpr int kHalfToks = G > 0 ? kTileRows / 2 / (G > 0 ? G : 1) : 0;
   float best = -INFINITY;
   int tok = half * kHalfToks, g = 0;  // the token and head that the next column is
@@ -581,14 +582,14 @@ cudaError_t launch_tiles(void (*kern)(Args...), dim3 grid, int threads, int byte
   return ldev::launch(kern, grid, threads, static_cast<size_t>(bytes), s, 1, args...);
 }
 
-// Tokens of a CTA: what gives kScoreCtas CTAs at most (two fit on a SM with d = 128), but
+// Tokens of a CTA: what gives kScoreCtas CTAs a SM at most (two fit there with d = 128), but
 // kScoreLeast rows, which are worth loading the pages' bounds for.
-constexpr int kScoreLeast = 256, kScoreCtas = 4 * 152;
+constexpr int kScoreLeast = 256, kScoreCtas = 4;
 
 template <int D>
 cudaError_t scores_tiles_dim(const LongParams& p, cudaStream_t s) {
   const int64_t cols = (p.table_width + 127) / 128;
-  int64_t runs = kScoreCtas / (cols * p.B * p.Hk);
+  int64_t runs = kScoreCtas * static_cast<int64_t>(p.sms) / (cols * p.B * p.Hk);
   const int64_t most = (static_cast<int64_t>(p.Nq) * p.G + kScoreLeast - 1) / kScoreLeast;
   if (runs > most) runs = most;
   if (runs < 1) runs = 1;
